@@ -4,15 +4,18 @@ The names ``fa_fwd``, ``fa_fwd_ex``, ``fa_fwd_ex_workspace_bytes``,
 ``fa_fwd_ex_default_splits``, ``fa_bwd``, ``fa_bwd_ex``, ``fa_bwd_preprocess``,
 ``fa_bwd_dkdv``, ``fa_bwd_dq_convert``, ``fa_bwd_workspace_bytes``, ``fa_strerror``,
 ``fa_last_device_status``, ``fa_selftest_wait_timeout``,
-``fa_selftest_drain_timeout``, ``fa_bwd_noalloc``, ``fa_last_cuda_error`` and
-``fa_version`` are
+``fa_selftest_drain_timeout``, ``fa_bwd_noalloc``, ``fa_rope``,
+``fa_paged_append``, ``fa_paged_decode``, ``fa_paged_decode_workspace_bytes``,
+``fa_paged_evict``, ``fa_last_cuda_error`` and ``fa_version`` are
 the C entry points of ``include/fa.h`` with the same arguments (pointers as
 Python ints, stream as an int handle); they return the integer status.
 
 ``forward``/``backward`` marshal torch CUDA tensors into those calls: they
 check dtype, shape, contiguity and device, allocate outputs with torch, pass
 ``data_ptr()`` and the current stream, and raise ``FAError`` on a non-zero
-status.  Every step of the computation runs in the library's kernels; there
+status.  ``rope``, ``rope_backward``, ``paged_append``, ``paged_decode`` and
+``paged_evict`` do the same for rotary positions and the paged key / value
+cache.  Every step of the computation runs in the library's kernels; there
 is no fallback of any kind.  If the library has not been built the first call
 raises ``FAError``.
 """
@@ -41,6 +44,9 @@ FA_ERR_BAD_ARGUMENT = 10
 FA_ERR_ALIASING = 11
 FA_ERR_SCRATCH_LIMIT = 12
 FA_ERR_DEVICE_DRAIN = 13
+FA_ERR_BAD_INDEX = 14
+FA_BF16 = 0
+FA_FP16 = 1
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 
@@ -57,6 +63,22 @@ _p = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
+
+
+class fa_rotary(ctypes.Structure):
+    _fields_ = [("positions", _p), ("axis_stride", _ll), ("batch_stride", _ll), ("inv_freq", _p), ("axes", _p),
+                ("n_axes", _i), ("rot", _i), ("interleaved", _i)]
+
+
+class fa_paged_kv(ctypes.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("page_stride", _ll), ("head_stride", _ll), ("slot_stride", _ll),
+                ("num_pages", _i), ("page_size", _i), ("Hkv", _i), ("d", _i), ("dtype", _i)]
+
+
+class fa_page_table(ctypes.Structure):
+    _fields_ = [("pages", _p), ("stride", _ll), ("max_pages", _i)]
+
 
 _SIGNATURES = {
     "fa_fwd": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f, _p], _i),
@@ -76,6 +98,11 @@ _SIGNATURES = {
     "fa_version": ([], _i),
     "fa_last_cuda_error": ([], ctypes.c_char_p),
     "fa_bwd_noalloc": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f, _p], _i),
+    "fa_rope": ([_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p, _i, _p], _i),
+    "fa_paged_append": ([_p, _p, _p, _p, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p, _i, _p, _p, _p], _i),
+    "fa_paged_decode": ([_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _f, _p, _sz, _p], _i),
+    "fa_paged_decode_workspace_bytes": ([_i, _i, _i, _i, _i, _i, _i], _sz),
+    "fa_paged_evict": ([_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _p], _i),
 }
 
 
@@ -192,6 +219,37 @@ def fa_bwd_noalloc(q, k, v, o, do, lse, dq, dk, dv, B, Hq, Hkv, N, d, causal, sc
     the library (for callers that cannot allocate device memory)."""
     return load_library().fa_bwd_noalloc(q, k, v, o, do, lse, dq, dk, dv, B, Hq, Hkv, N, d, int(causal),
                                          float(scale), stream)
+
+
+def _ref(s):
+    return ctypes.byref(s) if isinstance(s, ctypes.Structure) else s
+
+
+def fa_rope(q, q_strides, q_out, q_out_strides, k, k_strides, k_out, k_out_strides, B, Hq, Hk, N, d, dtype, rotary,
+            inverse, stream):
+    return load_library().fa_rope(q, q_strides, q_out, q_out_strides, k, k_strides, k_out, k_out_strides, B, Hq, Hk, N,
+                                  d, dtype, _ref(rotary), int(inverse), stream)
+
+
+def fa_paged_append(kv, table, seq_lens, cu_seqlens, B, T, k, k_strides, v, v_strides, q, q_strides, q_out,
+                    q_out_strides, Hq, rotary, scores, stream):
+    return load_library().fa_paged_append(_ref(kv), _ref(table), seq_lens, cu_seqlens, B, T, k, k_strides, v, v_strides,
+                                          q, q_strides, q_out, q_out_strides, Hq, _ref(rotary), scores, stream)
+
+
+def fa_paged_decode(q, q_strides, kv, table, seq_lens, o, lse, scores, B, Hq, window, scale, workspace,
+                    workspace_bytes, stream):
+    return load_library().fa_paged_decode(q, q_strides, _ref(kv), _ref(table), seq_lens, o, lse, scores, B, Hq, window,
+                                          scale, workspace, workspace_bytes, stream)
+
+
+def fa_paged_decode_workspace_bytes(B, Hq, Hkv, d, page_size, max_pages, with_scores):
+    return load_library().fa_paged_decode_workspace_bytes(B, Hq, Hkv, d, page_size, max_pages, int(with_scores))
+
+
+def fa_paged_evict(kv, scores, table, seq_lens, dst, new_lens, kept, B, budget, recent, sinks, stream):
+    return load_library().fa_paged_evict(_ref(kv), scores, _ref(table), seq_lens, _ref(dst), new_lens, kept, B, budget,
+                                         recent, sinks, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -312,3 +370,297 @@ def check_device_status(stream=None):
     s, detail = fa_last_device_status(_stream_handle(stream))
     if s != FA_OK:
         raise FAError(s, f"device status (block, site, thread) = {detail}")
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions and the paged key / value cache
+# ---------------------------------------------------------------------------
+
+class _Call:
+    """The device of a call's tensors and the stream it runs on.
+
+    The kernels run on the tensors' device, whichever device is current, and on
+    its current stream unless ``stream`` is given; what the call allocates
+    belongs to that stream, so the caching allocator does not hand a workspace
+    on to another stream while the kernels still use it."""
+
+    def __init__(self, t, stream):
+        import torch
+        self.device = t.device
+        self.enter = []
+        if t.device.index != torch.cuda.current_device():
+            self.enter.append(torch.cuda.device(t.device))
+        if stream is not None:
+            if stream.device != t.device:
+                raise ValueError(f"stream of {stream.device}, tensors on {t.device}")
+            self.enter.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        import torch
+        for x in self.enter:
+            x.__enter__()
+        self.handle = torch.cuda.current_stream(self.device).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        for x in reversed(self.enter):
+            x.__exit__(*exc)
+
+
+def _dtype_code(t, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return FA_BF16
+    if t.dtype == torch.float16:
+        return FA_FP16
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+
+
+def _check_view(t, name, shape, dtype, device):
+    """A CUDA tensor of this shape whose last dimension is contiguous; returns its address."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.data_ptr()
+
+
+def _check_dense(t, name, shape, dtype, device):
+    p = _check_view(t, name, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return p
+
+
+def _strides(t):
+    """Strides of all dimensions but the last, as a C array."""
+    s = t.stride()[:-1]
+    return (_ll * len(s))(*s)
+
+
+def _rotary(positions, inv_freq, axes, interleaved, d, lead, device):
+    """fa_rotary of positions [n_axes, *lead] int32, inv_freq [rot/2] float64, axes [rot/2] int32."""
+    import torch
+    if positions is None or inv_freq is None or axes is None:
+        raise ValueError("rotary positions need positions, inv_freq and axes")
+    if positions.dim() != len(lead) + 1:
+        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected (axes, *{tuple(lead)})")
+    pos = _check_view(positions, "positions", (positions.shape[0], *lead), torch.int32, device)
+    n = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
+    if n < 1 or 2 * n > d:
+        raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected 1 to {d // 2} frequencies")
+    w = _check_dense(inv_freq, "inv_freq", (n,), torch.float64, device)
+    ax = _check_dense(axes, "axes", (n,), torch.int32, device)
+    return fa_rotary(pos, positions.stride(0), positions.stride(1) if len(lead) == 2 else 0, w, ax, positions.shape[0],
+                     2 * n, int(interleaved))
+
+
+def rope_frequencies(sections, base: float = 10000.0, device="cuda"):
+    """inv_freq [r] float64 and axes [r] int32 for ``rope``: the r = sum(sections)
+    pairs have the frequencies base^(-i/r) and are dealt to the axes in runs of
+    ``sections`` pairs, e.g. (64,) for text at d = 128 or (16, 24, 24) for time,
+    height and width.  Any other two arrays of these types do as well."""
+    import torch
+    r = sum(sections)
+    if r < 1 or min(sections) < 0:
+        raise ValueError("sections must be non-negative with a positive sum")
+    inv = float(base) ** (-torch.arange(r, dtype=torch.float64) / r)
+    axes = torch.repeat_interleave(torch.arange(len(sections), dtype=torch.int32), torch.tensor(sections))
+    return inv.to(device), axes.to(device)
+
+
+def _rope(q, k, positions, inv_freq, axes, interleaved, inverse, q_out, k_out, stream):
+    import torch
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, H, N, d] tensor")
+    B, Hq, N, d = q.shape
+    dev, code = q.device, _dtype_code(q, "q")
+    qp = _check_view(q, "q", q.shape, q.dtype, dev)
+    Hk, kp, ks = 0, None, None
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be a [B, H, N, d] tensor")
+        Hk = k.shape[1]
+        kp, ks = _check_view(k, "k", (B, Hk, N, d), q.dtype, dev), _strides(k)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    rot = _rotary(positions, inv_freq, axes, interleaved, d, (B, N), dev)
+    with _Call(q, stream) as call:
+        if q_out is None:
+            q_out = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev)
+        op = _check_view(q_out, "q_out", (B, Hq, N, d), q.dtype, dev)
+        okp, oks = None, None
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty((B, Hk, N, d), dtype=q.dtype, device=dev)
+            okp, oks = _check_view(k_out, "k_out", (B, Hk, N, d), q.dtype, dev), _strides(k_out)
+        _raise(fa_rope(qp, _strides(q), op, _strides(q_out), kp, ks, okp, oks, B, Hq, Hk, N, d, code, rot, inverse,
+                       call.handle), "fa_rope")
+    return (q_out, k_out) if k is not None else q_out
+
+
+def rope(q, k, positions, inv_freq, axes, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """q [B,Hq,N,d] and k [B,Hk,N,d] (bf16 or fp16, any strides over B, H, N; k may
+    be None) with their first 2*len(inv_freq) elements turned: pair i by
+    positions[axes[i], b, n] * inv_freq[i] radians; see fa_rope.  positions is
+    int32 [n_axes, B, N] (expand over B to share them); inv_freq (float64) and
+    axes (int32) come from ``rope_frequencies`` or the caller.  Outputs may be the
+    inputs themselves.  Returns (q_out, k_out), or q_out without k."""
+    return _rope(q, k, positions, inv_freq, axes, interleaved, False, q_out, k_out, stream)
+
+
+def rope_backward(dq, dk, positions, inv_freq, axes, interleaved: bool = False, dq_out=None, dk_out=None, stream=None):
+    """Gradients of ``rope``'s inputs from those of its outputs: the opposite turn."""
+    return _rope(dq, dk, positions, inv_freq, axes, interleaved, True, dq_out, dk_out, stream)
+
+
+def _paged(k_cache, v_cache, block_table, seq_lens):
+    """(fa_paged_kv, fa_page_table, B) of checked cache tensors."""
+    import torch
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a [pages, Hkv, page_size, d] tensor")
+    dev = k_cache.device
+    P, Hkv, ps, d = k_cache.shape
+    kp = _check_view(k_cache, "k_cache", k_cache.shape, k_cache.dtype, dev)
+    vp = _check_view(v_cache, "v_cache", k_cache.shape, k_cache.dtype, dev)
+    st = k_cache.stride()
+    if v_cache.stride() != st:
+        raise ValueError("k_cache and v_cache must have the same strides")
+    kv = fa_paged_kv(kp, vp, st[0], st[1], st[2], P, ps, Hkv, d, _dtype_code(k_cache, "k_cache"))
+    table, B = _table(block_table, "block_table", dev)
+    return kv, table, B, _check_dense(seq_lens, "seq_lens", (B,), torch.int32, dev)
+
+
+def _table(t, name, dev):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a [B, pages] tensor")
+    return fa_page_table(_check_view(t, name, t.shape, torch.int32, dev), t.stride(0), t.shape[1]), t.shape[0]
+
+
+def _scores(scores, k_cache):
+    import torch
+    return _check_dense(scores, "scores", k_cache.shape[:3], torch.float32, k_cache.device)
+
+
+def paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens=None, q=None, positions=None, inv_freq=None,
+                 axes=None, interleaved: bool = False, scores=None, q_out=None, stream=None):
+    """Store new tokens' k, v [T,Hkv,d] in the paged cache [pages,Hkv,page_size,d].
+
+    ``seq_lens`` [B] int32 includes the new tokens.  Without ``cu_seqlens`` token
+    b is the last of sequence b (length 0: padding, skipped); with it ([B+1]
+    int32) tokens cu[b]..cu[b+1]-1 are sequence b's last ones and tokens from
+    cu[B] on are padding.  With ``positions`` [n_axes,T], ``inv_freq`` and
+    ``axes`` k is stored turned, and q [T,Hq,d], if given, is returned turned
+    (into ``q_out``, which may be q).  ``scores`` [pages,Hkv,page_size] fp32 gets
+    0 for the new tokens.  See fa_paged_append."""
+    import torch
+    kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
+    dev, dt, Hkv, d = k_cache.device, k_cache.dtype, kv.Hkv, kv.d
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a [T, Hkv, d] tensor")
+    T = k.shape[0]
+    kp, vp = _check_view(k, "k", (T, Hkv, d), dt, dev), _check_view(v, "v", (T, Hkv, d), dt, dev)
+    if cu_seqlens is None and T != B:
+        raise ValueError(f"{T} tokens for {B} sequences without cu_seqlens")
+    cu = None if cu_seqlens is None else _check_dense(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
+    rot = None
+    if positions is not None or inv_freq is not None or axes is not None:
+        rot = _rotary(positions, inv_freq, axes, interleaved, d, (T,), dev)
+    sp = None if scores is None else _scores(scores, k_cache)
+    qp, qs, Hq = None, None, 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a [T, Hq, d] tensor")
+        Hq = q.shape[1]
+        qp, qs = _check_view(q, "q", (T, Hq, d), dt, dev), _strides(q)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    with _Call(k_cache, stream) as call:
+        op, os_ = None, None
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+            op, os_ = _check_view(q_out, "q_out", (T, Hq, d), dt, dev), _strides(q_out)
+        if T == 0:
+            return q_out
+        _raise(fa_paged_append(kv, table, lens, cu, B, T, kp, _strides(k), vp, _strides(v), qp, qs, op, os_, Hq, rot, sp,
+                               call.handle), "fa_paged_append")
+    return q_out
+
+
+def paged_decode_workspace(B, Hq, k_cache, block_table, with_scores: bool = False):
+    """Workspace of paged_decode, for callers that keep one (one for each call that may run at the same time)."""
+    import torch
+    n = fa_paged_decode_workspace_bytes(B, Hq, k_cache.shape[1], k_cache.shape[3], k_cache.shape[2],
+                                        block_table.shape[1], with_scores)
+    if n == 0:
+        raise FAError(FA_ERR_BAD_SHAPE, "fa_paged_decode_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=k_cache.device)
+
+
+def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = None, window: int = 0, scores=None,
+                 out=None, lse=None, workspace=None, stream=None):
+    """O [B,Hq,d], LSE [B,Hq] of one query row per sequence, q [B,Hq,d], against the
+    seq_lens[b] keys of the paged cache (the last ``window`` of them if window >
+    0).  ``scores`` [pages,Hkv,page_size] fp32, if given, grows at each visible
+    key by its softmax weight summed over the group's heads.  See
+    fa_paged_decode."""
+    import torch
+    kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
+    dev, dt, d = k_cache.device, k_cache.dtype, kv.d
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [B, Hq, d] tensor")
+    Hq = q.shape[1]
+    qp = _check_view(q, "q", (B, Hq, d), dt, dev)
+    sp = None if scores is None else _scores(scores, k_cache)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _Call(k_cache, stream) as call:
+        if out is None:
+            out = torch.empty((B, Hq, d), dtype=dt, device=dev)
+        if lse is None:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        op = _check_dense(out, "out", (B, Hq, d), dt, dev)
+        lp = _check_dense(lse, "lse", (B, Hq), torch.float32, dev)
+        if workspace is None:
+            workspace = paged_decode_workspace(B, Hq, k_cache, block_table, scores is not None)
+        wp = _check_dense(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+        _raise(fa_paged_decode(qp, _strides(q), kv, table, lens, op, lp, sp, B, Hq, window, float(scale), wp,
+                               workspace.numel(), call.handle), "fa_paged_decode")
+    return out, lse
+
+
+def paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budget: int, recent: int = 0, sinks: int = 0,
+                new_lens=None, kept=None, stream=None):
+    """Keep min(seq_lens[b], budget) keys of every sequence and kv head: the first
+    ``sinks``, the last ``recent``, and those of the rest with the largest
+    ``scores``; their K, V and scores are written in order into the pages of
+    ``dst_table`` [B, >= ceil(budget/page_size)], which must be other pages than
+    those in use.  Returns (new_lens [B], kept [B,Hkv,budget]: the indices kept,
+    -1 past the new length).  See fa_paged_evict."""
+    import torch
+    kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
+    dev = k_cache.device
+    sp = _scores(scores, k_cache)
+    dst, Bd = _table(dst_table, "dst_table", dev)
+    if Bd != B:
+        raise ValueError(f"dst_table has {Bd} rows, expected {B}")
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    with _Call(k_cache, stream) as call:
+        if new_lens is None:
+            new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        if kept is None:
+            kept = torch.empty((B, kv.Hkv, budget), dtype=torch.int32, device=dev)
+        np_ = _check_dense(new_lens, "new_lens", (B,), torch.int32, dev)
+        ep = _check_dense(kept, "kept", (B, kv.Hkv, budget), torch.int32, dev)
+        _raise(fa_paged_evict(kv, sp, table, lens, dst, np_, ep, B, budget, recent, sinks, call.handle), "fa_paged_evict")
+    return new_lens, kept

@@ -10,7 +10,9 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
+#include <initializer_list>
 #include <mutex>
+#include <utility>
 
 #include "fa_internal.h"
 
@@ -406,6 +408,8 @@ const char* fa_strerror(fa_status s) {
     case FA_ERR_DEVICE_DRAIN:
       return "a kernel exited with its own copies or MMAs possibly in flight after a device-side timeout; "
              "no further launches on this device in this process";
+    case FA_ERR_BAD_INDEX:
+      return "a kernel read a page number, length, offset or axis out of range and skipped the access";
   }
   return "unknown status";
 }
@@ -722,3 +726,356 @@ extern "C" fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v,
   return fa_bwd(q, k, v, o, dO, lse, dq, dk, dv, B, Hq, Hkv, N, d, causal, scale, scratch,
                 (size_t)FA_NOALLOC_SCRATCH_BYTES, stream);
 }
+
+// ---------------------------------------------------------------------------
+// Rotary positions and the paged cache
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr long long kMaxSpan = 1LL << 46;   // elements one dimension may span
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Rows of `row` contiguous elements over up to three strided dimensions, in
+// bytes; dimensions of size 1 are dropped, the others sorted by stride, the
+// largest first.
+struct View {
+  uintptr_t base = 0;
+  unsigned long long row = 0;
+  int n = 0;
+  unsigned long long size[3] = {}, stride[3] = {};
+
+  // First byte past the last row of dimensions [from, n).
+  unsigned long long extent(int from = 0) const {
+    unsigned long long e = row;
+    for (int i = from; i < n; ++i) e += (size[i] - 1) * stride[i];
+    return e;
+  }
+  // Every dimension's steps clear what lies inside it, so no two rows meet.
+  bool distinct() const {
+    for (int i = 0; i < n; ++i)
+      if (stride[i] < extent(i + 1)) return false;
+    return true;
+  }
+  bool same(const View& o) const {
+    if (base != o.base || row != o.row || n != o.n) return false;
+    for (int i = 0; i < n; ++i)
+      if (size[i] != o.size[i] || stride[i] != o.stride[i]) return false;
+    return true;
+  }
+};
+
+View view(const void* p, long long row, int elem, std::initializer_list<std::pair<long long, long long>> dims) {
+  View v;
+  v.base = reinterpret_cast<uintptr_t>(p);
+  v.row = (unsigned long long)row * elem;
+  for (const auto& d : dims)
+    if (d.first > 1) {
+      int i = v.n++;
+      for (; i > 0 && v.stride[i - 1] < (unsigned long long)d.second * elem; --i) {
+        v.size[i] = v.size[i - 1];
+        v.stride[i] = v.stride[i - 1];
+      }
+      v.size[i] = (unsigned long long)d.first;
+      v.stride[i] = (unsigned long long)d.second * elem;
+    }
+  return v;
+}
+View bytes_view(const void* p, size_t n) { return view(p, (long long)n, 1, {}); }
+
+// Whether no byte of a's rows is one of b's: their address ranges are apart,
+// or both step alike through their outer dimensions and are apart inside one
+// step (the q, k and v parts of one projection's output).
+bool apart(const View& a, const View& b) {
+  if (a.base + a.extent() <= b.base || b.base + b.extent() <= a.base) return true;
+  const uintptr_t lo = std::min(a.base, b.base);
+  for (int outer = 1; outer <= a.n && outer <= b.n; ++outer) {
+    const int i = outer - 1;
+    if (a.stride[i] != b.stride[i]) return false;
+    const uintptr_t ea = a.base + a.extent(outer), eb = b.base + b.extent(outer);
+    // The span of both inside one step must fit the step, and the steps of
+    // this level must fit one step of the level outside it (the larger count).
+    const unsigned long long span = std::max(ea, eb) - lo;
+    if (i > 0 && std::max(a.size[i], b.size[i]) * a.stride[i] > a.stride[i - 1]) return false;
+    if (span <= a.stride[i] && (ea <= b.base || eb <= a.base)) return true;
+  }
+  return false;
+}
+
+// Strides of the dimensions larger than 1: none negative, all multiples of 8
+// elements, and small enough that no address computation overflows.
+fa_status check_strides(std::initializer_list<std::pair<long long, long long>> dims) {
+  for (const auto& d : dims)
+    if (d.first > 1) {
+      if (d.second < 0 || d.second > kMaxSpan / d.first) return FA_ERR_BAD_ARGUMENT;
+      if (d.second % 8) return FA_ERR_MISALIGNED;
+    }
+  return FA_OK;
+}
+
+long long stride_of(long long size, long long stride) { return size > 1 ? stride : 0; }
+
+fa_status check_rotary(const fa_rotary* r, int d) {
+  if (!r->positions || !r->inv_freq || !r->axes) return FA_ERR_NULL_PTR;
+  if (r->rot < 16 || r->rot > d || r->rot % 16 || r->n_axes < 1 || r->n_axes > 1024 || (r->interleaved != 0 && r->interleaved != 1) ||
+      r->axis_stride < 0 || r->axis_stride > kMaxSpan / 1024 || r->batch_stride < 0 || r->batch_stride > (1LL << 31))
+    return FA_ERR_BAD_ARGUMENT;
+  if (!aligned(r->positions, 4) || !aligned(r->inv_freq, 8) || !aligned(r->axes, 4)) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+fa::RotaryArgs rotary_args(const fa_rotary* r, int inverse) {
+  return fa::RotaryArgs{r->positions, r->axis_stride, r->batch_stride, r->inv_freq, r->axes,
+                        r->n_axes,    r->rot,         r->interleaved,  inverse};
+}
+
+fa_status check_dtype(int dtype) { return dtype == FA_BF16 || dtype == FA_FP16 ? FA_OK : FA_ERR_BAD_ARGUMENT; }
+
+View kv_view(const fa_paged_kv* kv, const void* p) {
+  return view(p, kv->d, 2,
+              {{kv->num_pages, kv->page_stride}, {kv->Hkv, kv->head_stride}, {kv->page_size, kv->slot_stride}});
+}
+
+fa_status check_kv(const fa_paged_kv* kv) {
+  if (!kv || !kv->k || !kv->v) return FA_ERR_NULL_PTR;
+  FA_TRY(check_dtype(kv->dtype));
+  if (kv->num_pages < 1 || kv->Hkv < 1 || kv->page_size < 16 || kv->page_size > 65536 || kv->page_size % 16)
+    return FA_ERR_BAD_SHAPE;
+  if (kv->d != 64 && kv->d != 128) return FA_ERR_UNSUPPORTED_HEADDIM;
+  FA_TRY(check_strides({{kv->num_pages, kv->page_stride}, {kv->Hkv, kv->head_stride}, {kv->page_size, kv->slot_stride}}));
+  if (!aligned16(kv->k) || !aligned16(kv->v)) return FA_ERR_MISALIGNED;
+  return kv_view(kv, kv->k).distinct() ? FA_OK : FA_ERR_BAD_ARGUMENT;
+}
+
+View scores_view(const fa_paged_kv* kv, const float* s) {
+  return bytes_view(s, (size_t)kv->num_pages * kv->Hkv * kv->page_size * 4);
+}
+
+fa_status check_table(const fa_page_table* t, int B) {
+  if (!t || !t->pages) return FA_ERR_NULL_PTR;
+  if (t->max_pages < 1) return FA_ERR_BAD_SHAPE;
+  if (B > 1 && (t->stride < 0 || t->stride > (1LL << 31))) return FA_ERR_BAD_ARGUMENT;
+  return aligned(t->pages, 4) ? FA_OK : FA_ERR_MISALIGNED;
+}
+
+View table_view(const fa_page_table* t, int B) { return view(t->pages, t->max_pages, 4, {{B, t->stride}}); }
+
+fa::PagedKv kv_args(const fa_paged_kv* kv) {
+  return fa::PagedKv{kv->k,
+                     kv->v,
+                     stride_of(kv->num_pages, kv->page_stride),
+                     stride_of(kv->Hkv, kv->head_stride),
+                     stride_of(kv->page_size, kv->slot_stride),
+                     kv->num_pages,
+                     kv->page_size,
+                     kv->Hkv,
+                     kv->d};
+}
+
+fa::PageTable table_args(const fa_page_table* t) { return fa::PageTable{t->pages, t->stride, t->max_pages}; }
+
+// Each output apart from every input and every other output.
+template <size_t NO, size_t NI>
+bool outputs_apart(const View (&outs)[NO], const View (&ins)[NI]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (size_t j = 0; j < NI; ++j)
+      if (!apart(outs[i], ins[j])) return false;
+    for (size_t j = 0; j < i; ++j)
+      if (!apart(outs[i], outs[j])) return false;
+  }
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_rope(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides, const void* k,
+                  const long long* k_strides, void* k_out, const long long* k_out_strides, int B, int Hq, int Hk, int N,
+                  int d, int dtype, const fa_rotary* rotary, int inverse, void* stream) {
+  NvtxRange nv("fa_rope");
+  if (!q || !q_strides || !q_out || !q_out_strides || !rotary) return FA_ERR_NULL_PTR;
+  if (Hk != 0 && (!k || !k_strides || !k_out || !k_out_strides)) return FA_ERR_NULL_PTR;
+  if (Hk < 0 || (Hk == 0 && (k || k_out))) return FA_ERR_BAD_SHAPE;
+  if (B < 1 || Hq < 1 || N < 1 || (long long)B * N >= (1LL << 31) || (long long)Hq + Hk > 65535) return FA_ERR_BAD_SHAPE;
+  if (d < 16 || d > 256 || d % 16) return FA_ERR_UNSUPPORTED_HEADDIM;
+  FA_TRY(check_dtype(dtype));
+  if (inverse != 0 && inverse != 1) return FA_ERR_BAD_ARGUMENT;
+  FA_TRY(check_rotary(rotary, d));
+  const void* ptrs[4] = {q, q_out, k, k_out};
+  const long long* strides[4] = {q_strides, q_out_strides, k_strides, k_out_strides};
+  fa::RowView rows[4] = {};
+  View views[4];
+  const int n = Hk ? 4 : 2;
+  for (int i = 0; i < n; ++i) {
+    const int H = i < 2 ? Hq : Hk;
+    const long long* s = strides[i];
+    FA_TRY(check_strides({{B, s[0]}, {H, s[1]}, {N, s[2]}}));
+    if (!aligned16(ptrs[i])) return FA_ERR_MISALIGNED;
+    rows[i] = fa::RowView{const_cast<void*>(ptrs[i]), stride_of(B, s[0]), stride_of(H, s[1]), stride_of(N, s[2])};
+    views[i] = view(ptrs[i], d, 2, {{B, s[0]}, {H, s[1]}, {N, s[2]}});
+  }
+  const View tables[3] = {
+      view(rotary->positions, N, 4, {{rotary->n_axes, rotary->axis_stride}, {B, rotary->batch_stride}}),
+      bytes_view(rotary->inv_freq, (size_t)rotary->rot / 2 * 8), bytes_view(rotary->axes, (size_t)rotary->rot / 2 * 4)};
+  for (int i = 1; i < n; i += 2) {
+    if (!views[i].distinct()) return FA_ERR_ALIASING;
+    for (int j = 0; j < n; ++j)
+      if (j != i && !(j == i - 1 && views[i].same(views[j])) && !apart(views[i], views[j])) return FA_ERR_ALIASING;
+    for (const View& t : tables)
+      if (!apart(views[i], t)) return FA_ERR_ALIASING;
+  }
+  DeviceState* ds = nullptr;
+  FA_TRY(device_state(&ds));
+  const fa::RopeArgs a{rows[0], rows[1], rows[2], rows[3], B, Hq, Hk, N, d, rotary_args(rotary, inverse)};
+  return launch_status(fa::launch_rope(dtype, a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_paged_append(const fa_paged_kv* kv, const fa_page_table* table, const int* seq_lens, const int* cu_seqlens,
+                          int B, int T, const void* k, const long long* k_strides, const void* v,
+                          const long long* v_strides, const void* q, const long long* q_strides, void* q_out,
+                          const long long* q_out_strides, int Hq, const fa_rotary* rotary, float* scores, void* stream) {
+  NvtxRange nv("fa_paged_append");
+  FA_TRY(check_kv(kv));
+  if (!seq_lens || !k_strides || !v_strides || (T != 0 && (!k || !v))) return FA_ERR_NULL_PTR;
+  if (B < 1 || T < 0 || (!cu_seqlens && T != B)) return FA_ERR_BAD_SHAPE;
+  FA_TRY(check_table(table, B));
+  if (!aligned(seq_lens, 4) || !aligned(cu_seqlens, 4) || !aligned16(scores)) return FA_ERR_MISALIGNED;
+  if (q && !rotary) return FA_ERR_BAD_ARGUMENT;
+  if (q ? (!q_out || !q_strides || !q_out_strides) : q_out != nullptr) return FA_ERR_NULL_PTR;
+  if (q ? Hq < 1 : Hq != 0) return FA_ERR_BAD_SHAPE;
+  if ((long long)Hq + 2LL * kv->Hkv > 65535) return FA_ERR_BAD_SHAPE;
+  if (rotary) FA_TRY(check_rotary(rotary, kv->d));
+  if (T == 0) return FA_OK;
+  const void* ptrs[4] = {k, v, q, q_out};
+  const long long* strides[4] = {k_strides, v_strides, q_strides, q_out_strides};
+  fa::RowView rows[4] = {};
+  View views[4];
+  const int n = q ? 4 : 2;
+  for (int i = 0; i < n; ++i) {
+    const int H = i < 2 ? kv->Hkv : Hq;
+    const long long* s = strides[i];
+    FA_TRY(check_strides({{T, s[0]}, {H, s[1]}}));
+    if (!aligned16(ptrs[i])) return FA_ERR_MISALIGNED;
+    rows[i] = fa::RowView{const_cast<void*>(ptrs[i]), 0, stride_of(H, s[1]), stride_of(T, s[0])};
+    views[i] = view(ptrs[i], kv->d, 2, {{T, s[0]}, {H, s[1]}});
+  }
+  View small[6];
+  int ns = 0;
+  small[ns++] = table_view(table, B);
+  small[ns++] = bytes_view(seq_lens, (size_t)B * 4);
+  if (cu_seqlens) small[ns++] = bytes_view(cu_seqlens, (size_t)(B + 1) * 4);
+  if (rotary) {
+    small[ns++] = view(rotary->positions, T, 4, {{rotary->n_axes, rotary->axis_stride}});
+    small[ns++] = bytes_view(rotary->inv_freq, (size_t)rotary->rot / 2 * 8);
+    small[ns++] = bytes_view(rotary->axes, (size_t)rotary->rot / 2 * 4);
+  }
+  View outs[4] = {kv_view(kv, kv->k), kv_view(kv, kv->v)};
+  int no = 2;
+  if (scores) outs[no++] = scores_view(kv, scores);
+  const int qo = q ? no : -1;
+  if (q) outs[no++] = views[3];
+  for (int i = 0; i < no; ++i) {
+    if (!outs[i].distinct()) return FA_ERR_ALIASING;
+    for (int j = 0; j < (q ? 3 : 2); ++j)
+      if (!(i == qo && j == 2 && outs[i].same(views[2])) && !apart(outs[i], views[j])) return FA_ERR_ALIASING;
+    for (int j = 0; j < i; ++j)
+      if (!apart(outs[i], outs[j])) return FA_ERR_ALIASING;
+    for (int j = 0; j < ns; ++j)
+      if (!apart(outs[i], small[j])) return FA_ERR_ALIASING;
+  }
+  DeviceState* ds = nullptr;
+  FA_TRY(device_state(&ds));
+  fa::AppendArgs a{};
+  a.k = rows[0];
+  a.v = rows[1];
+  a.q = rows[2];
+  a.q_out = rows[3];
+  a.kv = kv_args(kv);
+  a.table = table_args(table);
+  a.seq_lens = seq_lens;
+  a.cu = cu_seqlens;
+  a.scores = scores;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  if (rotary) a.r = rotary_args(rotary, 0);
+  return launch_status(fa::launch_append(kv->dtype, a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d, int page_size, int max_pages, int with_scores) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (d != 64 && d != 128) || page_size < 16 || page_size > 65536 ||
+      page_size % 16 || max_pages < 1 || (long long)B * Hq >= (1LL << 31))
+    return 0;
+  (void)with_scores;
+  return 256;
+}
+
+fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_paged_kv* kv, const fa_page_table* table,
+                          const int* seq_lens, void* o, float* lse, float* scores, int B, int Hq, int window,
+                          float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nv("fa_paged_decode");
+  FA_TRY(check_kv(kv));
+  if (!q || !q_strides || !seq_lens || !o || !lse || !workspace) return FA_ERR_NULL_PTR;
+  if (B < 1 || Hq < 1 || Hq % kv->Hkv || (long long)B * Hq >= (1LL << 31)) return FA_ERR_BAD_SHAPE;
+  FA_TRY(check_table(table, B));
+  FA_TRY(check_scale(0, scale));
+  if (window < 0) return FA_ERR_BAD_ARGUMENT;
+  FA_TRY(check_strides({{B, q_strides[0]}, {Hq, q_strides[1]}}));
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(scores) || !aligned16(workspace) ||
+      !aligned(seq_lens, 4))
+    return FA_ERR_MISALIGNED;
+  const size_t need =
+      fa_paged_decode_workspace_bytes(B, Hq, kv->Hkv, kv->d, kv->page_size, table->max_pages, scores ? 1 : 0);
+  if (need == 0) return FA_ERR_BAD_SHAPE;
+  if (workspace_bytes < need) return FA_ERR_WORKSPACE_TOO_SMALL;
+  const View ins[] = {view(q, kv->d, 2, {{B, q_strides[0]}, {Hq, q_strides[1]}}), kv_view(kv, kv->k), kv_view(kv, kv->v),
+                      table_view(table, B), bytes_view(seq_lens, (size_t)B * 4)};
+  const View outs[] = {bytes_view(o, (size_t)B * Hq * kv->d * 2), bytes_view(lse, (size_t)B * Hq * 4),
+                       bytes_view(workspace, need), scores ? scores_view(kv, scores) : bytes_view(nullptr, 0)};
+  if (!outputs_apart(outs, ins)) return FA_ERR_ALIASING;
+  DeviceState* ds = nullptr;
+  FA_TRY(device_state(&ds));
+  fa::DecodeArgs a{};
+  a.q = q;
+  a.q_sb = stride_of(B, q_strides[0]);
+  a.q_sh = stride_of(Hq, q_strides[1]);
+  a.kv = kv_args(kv);
+  a.table = table_args(table);
+  a.seq_lens = seq_lens;
+  a.o = o;
+  a.lse = lse;
+  a.scores = scores;
+  a.B = B;
+  a.Hq = Hq;
+  a.window = window;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return launch_status(
+      fa::launch_paged_decode(kv->dtype, a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_paged_evict(const fa_paged_kv* kv, float* scores, const fa_page_table* table, const int* seq_lens,
+                         const fa_page_table* dst, int* new_lens, int* kept, int B, int budget, int recent, int sinks,
+                         void* stream) {
+  NvtxRange nv("fa_paged_evict");
+  FA_TRY(check_kv(kv));
+  if (!scores || !seq_lens || !new_lens || !kept) return FA_ERR_NULL_PTR;
+  if (B < 1 || (long long)B * kv->Hkv >= (1LL << 31)) return FA_ERR_BAD_SHAPE;
+  FA_TRY(check_table(table, B));
+  FA_TRY(check_table(dst, B));
+  if (budget < 1 || recent < 0 || sinks < 0 || (long long)recent + sinks > budget ||
+      (long long)dst->max_pages * kv->page_size < budget)
+    return FA_ERR_BAD_ARGUMENT;
+  if (!aligned16(scores) || !aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(kept, 4)) return FA_ERR_MISALIGNED;
+  const View ins[] = {table_view(table, B), bytes_view(seq_lens, (size_t)B * 4), table_view(dst, B)};
+  const View outs[] = {kv_view(kv, kv->k), kv_view(kv, kv->v), scores_view(kv, scores), bytes_view(new_lens, (size_t)B * 4),
+                       bytes_view(kept, (size_t)B * kv->Hkv * budget * 4)};
+  if (!outputs_apart(outs, ins) || dst->pages == table->pages) return FA_ERR_ALIASING;
+  DeviceState* ds = nullptr;
+  FA_TRY(device_state(&ds));
+  const fa::EvictArgs a{kv_args(kv), scores, table_args(table), table_args(dst), seq_lens, new_lens, kept, B, budget, recent,
+                        sinks};
+  return launch_status(fa::launch_paged_evict(a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

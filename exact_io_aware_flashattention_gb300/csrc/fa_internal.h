@@ -75,6 +75,91 @@ cudaError_t launch_bwd_dkdv(int d, const TmaMap4& tq, const TmaMap4& tk, const T
 cudaError_t launch_bwd_dq_convert(const float* dq_accum, void* dq, float scale, long long n, int num_sms,
                                   cudaStream_t stream);
 
+// ---------------------------------------------------------------------------
+// Rotary positions and the paged cache (fa_rope.cu, fa_paged.cu, fa_evict.cu)
+// ---------------------------------------------------------------------------
+// Wait-site ids / index-check sites of these kernels in the status words.
+enum : int { kSiteAxis = 41, kSiteAppend = 42, kSiteDecodeLen = 43, kSiteDecodePage = 44, kSiteEvictLen = 45, kSiteEvictPage = 46 };
+constexpr int kErrBadIndex = 14;   // == FA_ERR_BAD_INDEX
+
+// Rows of d elements: (b, h, n) at b * sb + h * sh + n * sn elements from p.
+struct RowView {
+  void* p;
+  long long sb, sh, sn;
+};
+
+struct RotaryArgs {
+  const int* pos;            // [n_axes, B, N] with strides (pos_axis, pos_batch, 1)
+  long long pos_axis, pos_batch;
+  const double* inv_freq;    // [rot / 2] radians per position
+  const int* axes;           // [rot / 2] axis of each pair
+  int n_axes, rot;           // rot = 0: nothing is rotated
+  int interleaved;           // pair i = elements (2i, 2i+1) instead of (i, i + rot/2)
+  int inverse;               // angles negated (the gradient)
+};
+
+struct RopeArgs {
+  RowView q, q_out, k, k_out;
+  int B, Hq, Hk, N, d;
+  RotaryArgs r;
+};
+
+// A pool of pages: (page, kv head, slot) at page * s_page + g * s_head + slot * s_slot elements.
+struct PagedKv {
+  void* k;
+  void* v;
+  long long s_page, s_head, s_slot;
+  int num_pages, page_size, Hkv, d;
+};
+
+// Row b lists the pages of sequence b.
+struct PageTable {
+  const int* pages;
+  long long stride;
+  int cols;
+};
+
+struct AppendArgs {
+  RowView q, q_out, k, v;    // tokens as N (sb unused); q.p NULL: no q
+  PagedKv kv;
+  PageTable table;
+  const int* seq_lens;       // [B] lengths with the new tokens
+  const int* cu;             // [B + 1] first new token of each sequence, NULL: token b belongs to sequence b
+  float* scores;             // [num_pages, Hkv, page_size] or NULL
+  int B, T, Hq;
+  RotaryArgs r;
+};
+
+cudaError_t launch_rope(int dtype, const RopeArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream);
+cudaError_t launch_append(int dtype, const AppendArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream);
+
+struct DecodeArgs {
+  const void* q;             // (b, h) at b * q_sb + h * q_sh elements
+  long long q_sb, q_sh;
+  PagedKv kv;
+  PageTable table;
+  const int* seq_lens;
+  void* o;                   // [B, Hq, d]
+  float* lse;                // [B, Hq]
+  float* scores;             // [num_pages, Hkv, page_size] or NULL
+  int B, Hq, window;
+  float scale_log2;
+};
+
+cudaError_t launch_paged_decode(int dtype, const DecodeArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream);
+
+struct EvictArgs {
+  PagedKv kv;
+  float* scores;
+  PageTable table, dst;
+  const int* seq_lens;
+  int* new_lens;             // [B]
+  int* kept;                 // [B, Hkv, budget], -1 past the new length
+  int B, budget, recent, sinks;
+};
+
+cudaError_t launch_paged_evict(const EvictArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream);
+
 // One-time set-up of the current device for each translation unit's kernels
 // (shared-memory sizes; the forward also checks that every instance was
 // compiled with the register count its warpgroup split assumes).

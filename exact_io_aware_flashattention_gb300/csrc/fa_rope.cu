@@ -1,0 +1,286 @@
+// Rotary positions with several axes, and the append of new tokens to a paged
+// key / value cache with the same rotation fused in.
+//
+// Pair i of a row (elements i and i + rot/2, or 2i and 2i + 1 when
+// interleaved) turns by angle = pos[axis_i] * inv_freq_i:
+//   (x, y) -> (x cos - y sin, y cos + x sin);
+// the gradient turns by -angle (the rotation is orthogonal).
+//
+// The angle.  pos * inv_freq reaches 1e6 radians and more, where an fp32
+// product leaves no digits, and fp64 arithmetic is slow here.  Only the angle
+// modulo one turn matters, so inv_freq becomes F = inv_freq / (2 pi) * 2^64
+// as a 64-bit integer (from the double's mantissa and exponent, integer
+// arithmetic only) and the phase is pos * F modulo 2^64: the wrap-around of
+// the integer product is the reduction, exact for every int32 position.  The
+// phase's top 32 bits, as a signed fraction of half a turn, go to sincospif.
+// Error: F is off by < 2^-63 relative, the 32 bits by 2^-32 of a turn.
+//
+// Bound by HBM: every element is read once and written once.  A thread owns
+// one token and eight pairs (two 16-byte vectors of a row): its eight
+// cosines and sines are formed once and used for every head, so the
+// trigonometry costs 1/(Hq + Hkv) of a per-element evaluation.
+#include "fa_internal.h"
+#include "sm103a.cuh"
+
+#include <cuda_fp16.h>
+
+namespace fa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;   // heads whose loads are in flight per thread
+
+template <typename T>
+struct Pair2;
+template <>
+struct Pair2<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 up(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t down(float lo, float hi) { return cvt_bf16x2(lo, hi); }
+};
+template <>
+struct Pair2<__half> {
+  static __device__ __forceinline__ float2 up(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  static __device__ __forceinline__ uint32_t down(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+// inv_freq / (2 pi) modulo 1, in units of 2^-64 turns.  inv_freq = M 2^(e-63)
+// with M its mantissa in the top bits of a word, 1 / (2 pi) = C 2^-66, so the
+// result is the 128-bit product M C shifted by e - 65.
+__device__ __forceinline__ uint64_t turns64(double w) {
+  const uint64_t bits = (uint64_t)__double_as_longlong(w);
+  const int ex = (int)((bits >> 52) & 0x7ff);
+  if (ex == 0 || ex == 0x7ff) return 0;                     // zero (or not a finite frequency)
+  const uint64_t M = (1ull << 63) | ((bits & 0xfffffffffffffull) << 11);
+  const uint64_t C = 0xA2F9836E4E44152Aull;                 // 2^66 / (2 pi)
+  const uint64_t hi = __umul64hi(M, C), lo = M * C;
+  const int s = ex - 1023 - 1;                              // hi:lo shifted left by s, the upper word
+  uint64_t F;
+  if (s >= 64) F = 0;
+  else if (s > 0) F = (hi << s) | (lo >> (64 - s));
+  else F = s > -64 ? hi >> -s : 0;
+  return (bits >> 63) ? 0 - F : F;
+}
+
+// Cosines and sines of the pairs 8c .. 8c+7 of the token whose positions
+// start at pos.
+__device__ __forceinline__ void load_angles(const RotaryArgs& r, const int* pos, int c, const DevStatus& st,
+                                            float (&cs)[8], float (&sn)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    int ax = r.axes[c * 8 + i];
+    if (ax < 0 || ax >= r.n_axes) {
+      record_error(st, kErrBadIndex, kSiteAxis);
+      ax = 0;
+    }
+    const uint64_t phase = (uint64_t)(int64_t)pos[ax * r.pos_axis] * turns64(r.inv_freq[c * 8 + i]);
+    const float half_turns = (float)(int32_t)(uint32_t)(phase >> 32) * 4.656612873077393e-10f;   // 2^-31
+    sincospif(half_turns, &sn[i], &cs[i]);
+    if (r.inverse) sn[i] = -sn[i];
+  }
+}
+
+// Eight pairs: elements of a at i, of b at i (halves) or adjacent (interleaved).
+template <typename T, bool kInter>
+__device__ __forceinline__ void turn8(uint4& va, uint4& vb, const float (&cs)[8], const float (&sn)[8]) {
+  uint32_t* a = reinterpret_cast<uint32_t*>(&va);
+  uint32_t* b = reinterpret_cast<uint32_t*>(&vb);
+  if constexpr (kInter) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t& w = i < 4 ? a[i] : b[i - 4];
+      const float2 x = Pair2<T>::up(w);
+      w = Pair2<T>::down(x.x * cs[i] - x.y * sn[i], x.y * cs[i] + x.x * sn[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = Pair2<T>::up(a[i]), y = Pair2<T>::up(b[i]);
+      a[i] = Pair2<T>::down(x.x * cs[2 * i] - y.x * sn[2 * i], x.y * cs[2 * i + 1] - y.y * sn[2 * i + 1]);
+      b[i] = Pair2<T>::down(y.x * cs[2 * i] + x.x * sn[2 * i], y.y * cs[2 * i + 1] + x.y * sn[2 * i + 1]);
+    }
+  }
+}
+
+// What one thread does to a row: the two 16-byte vectors it owns, turned, or
+// (kind kCopy) moved unchanged.  A row has rot/16 turned chunks and then
+// (d - rot)/16 chunks that pass through.
+struct Chunk {
+  int e0, e1;      // first elements of the two vectors
+  bool turned;
+};
+template <bool kInter>
+__device__ __forceinline__ Chunk chunk_of(int c, int rot) {
+  Chunk k;
+  k.turned = c < rot / 16;
+  if (k.turned && !kInter) {
+    k.e0 = 8 * c;
+    k.e1 = rot / 2 + 8 * c;
+  } else {
+    k.e0 = 16 * c;
+    k.e1 = 16 * c + 8;
+  }
+  return k;
+}
+
+// Heads [h0, h1) of one token: in + h * in_sh -> out + h * out_sh.
+template <typename T, bool kInter>
+__device__ __forceinline__ void do_heads(const T* in, long long in_sh, T* out, long long out_sh, int h0, int h1,
+                                         const Chunk& ck, bool turned, const float (&cs)[8], const float (&sn)[8]) {
+  for (int h = h0; h < h1; h += kUnroll) {
+    uint4 a[kUnroll], b[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (h + u < h1) {
+        a[u] = *reinterpret_cast<const uint4*>(in + (h + u) * in_sh + ck.e0);
+        b[u] = *reinterpret_cast<const uint4*>(in + (h + u) * in_sh + ck.e1);
+      }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (h + u < h1) {
+        if (turned) turn8<T, kInter>(a[u], b[u], cs, sn);
+        *reinterpret_cast<uint4*>(out + (h + u) * out_sh + ck.e0) = a[u];
+        *reinterpret_cast<uint4*>(out + (h + u) * out_sh + ck.e1) = b[u];
+      }
+  }
+}
+
+// grid: x over groups of 256 / (d/16) tokens, y over groups of hpb heads of q
+// and then k.
+template <typename T, bool kInter>
+__global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeArgs a, int hpb, const DevStatus st) {
+  const int nch = a.d / 16, tpb = kThreads / nch;
+  const int lt = threadIdx.x / nch, c = threadIdx.x - lt * nch;
+  const long long t = (long long)blockIdx.x * tpb + lt;
+  if (lt >= tpb || t >= (long long)a.B * a.N) return;
+  const int b = (int)(t / a.N), n = (int)(t - (long long)b * a.N);
+  const Chunk ck = chunk_of<kInter>(c, a.r.rot);
+  float cs[8] = {}, sn[8] = {};
+  if (ck.turned) load_angles(a.r, a.r.pos + b * a.r.pos_batch + n, c, st, cs, sn);
+  const int h0 = blockIdx.y * hpb, h1 = min(h0 + hpb, a.Hq + a.Hk);
+  auto rows = [&](const RowView& in, const RowView& out, int lo, int hi) {
+    if (lo < hi)
+      do_heads<T, kInter>(static_cast<const T*>(in.p) + b * in.sb + n * in.sn, in.sh,
+                          static_cast<T*>(out.p) + b * out.sb + n * out.sn, out.sh, lo, hi, ck, ck.turned, cs, sn);
+  };
+  rows(a.q, a.q_out, h0, min(h1, a.Hq));
+  rows(a.k, a.k_out, max(h0 - a.Hq, 0), h1 - a.Hq);
+}
+
+// Where token t goes: sequence, index in it, page and slot.  Returns false for
+// a token that is not stored: padding (past the last sequence, or a sequence
+// of length 0 in the one-token form), or an index out of range, which is
+// recorded.
+__device__ __forceinline__ bool place_token(const AppendArgs& a, int t, const DevStatus& st, int& page, int& slot) {
+  int b = t, back = 1;
+  if (a.cu) {
+    if (t >= a.cu[a.B]) return false;
+    int lo = 0, hi = a.B;                  // last b with cu[b] <= t
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.cu[mid] <= t) lo = mid; else hi = mid;
+    }
+    b = lo;
+    back = a.cu[b + 1] - t;
+  } else if (a.seq_lens[b] == 0) {
+    return false;
+  }
+  const long long i = (long long)a.seq_lens[b] - back;
+  if (back < 1 || i < 0 || i >= (long long)a.table.cols * a.kv.page_size) {
+    record_error(st, kErrBadIndex, kSiteAppend);
+    return false;
+  }
+  const int col = (int)i / a.kv.page_size;
+  page = a.table.pages[b * a.table.stride + col];
+  slot = (int)i - col * a.kv.page_size;
+  if (page < 0 || page >= a.kv.num_pages) {
+    record_error(st, kErrBadIndex, kSiteAppend);
+    return false;
+  }
+  return true;
+}
+
+// As fa_rope_kernel over tokens, with the heads of q, then k, then v; k and v
+// rows go to their slot of the cache, whose accumulated weight starts at 0.
+template <typename T, bool kInter>
+__global__ void __launch_bounds__(kThreads) fa_append_kernel(const AppendArgs a, int hpb, const DevStatus st) {
+  const int nch = a.kv.d / 16, tpb = kThreads / nch;
+  const int lt = threadIdx.x / nch, c = threadIdx.x - lt * nch;
+  const long long t = (long long)blockIdx.x * tpb + lt;
+  if (lt >= tpb || t >= a.T) return;
+  int page, slot;
+  if (!place_token(a, (int)t, st, page, slot)) return;
+  const int Hkv = a.kv.Hkv;
+  const int h0 = blockIdx.y * hpb, h1 = min(h0 + hpb, a.Hq + 2 * Hkv);
+  const Chunk ck = chunk_of<kInter>(c, a.r.rot);
+  float cs[8] = {}, sn[8] = {};
+  if (ck.turned && h0 < a.Hq + Hkv) load_angles(a.r, a.r.pos + t, c, st, cs, sn);
+  const long long at = page * a.kv.s_page + slot * a.kv.s_slot;
+  if (h0 < a.Hq)
+    do_heads<T, kInter>(static_cast<const T*>(a.q.p) + t * a.q.sn, a.q.sh, static_cast<T*>(a.q_out.p) + t * a.q_out.sn,
+                        a.q_out.sh, h0, min(h1, a.Hq), ck, ck.turned, cs, sn);
+  int lo = max(h0 - a.Hq, 0), hi = min(h1 - a.Hq, Hkv);
+  if (lo < hi) {
+    do_heads<T, kInter>(static_cast<const T*>(a.k.p) + t * a.k.sn, a.k.sh, static_cast<T*>(a.kv.k) + at, a.kv.s_head, lo,
+                        hi, ck, ck.turned, cs, sn);
+    if (a.scores)
+      for (int h = lo + c; h < hi; h += nch) a.scores[((long long)page * Hkv + h) * a.kv.page_size + slot] = 0.f;
+  }
+  lo = max(h0 - a.Hq - Hkv, 0);
+  hi = h1 - a.Hq - Hkv;
+  if (lo < hi)
+    do_heads<T, kInter>(static_cast<const T*>(a.v.p) + t * a.v.sn, a.v.sh, static_cast<T*>(a.kv.v) + at, a.kv.s_head, lo,
+                        hi, ck, false, cs, sn);
+}
+
+// Heads per block: all of them where the tokens alone fill the GPU (the
+// angles are then formed once a token), fewer where they do not.
+int heads_per_block(long long token_blocks, int heads, int num_sms) {
+  const long long want = 4LL * num_sms;
+  long long splits = (want + token_blocks - 1) / token_blocks;
+  const long long most = (heads + kUnroll - 1) / kUnroll;
+  if (splits > most) splits = most;
+  if (splits < 1) splits = 1;
+  return (int)((heads + splits - 1) / splits);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(int dtype, const RopeArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream) {
+  const int tpb = kThreads / (a.d / 16);
+  const long long blocks = ((long long)a.B * a.N + tpb - 1) / tpb;
+  const int heads = a.Hq + a.Hk, hpb = heads_per_block(blocks, heads, num_sms);
+  const dim3 grid((unsigned)blocks, (unsigned)((heads + hpb - 1) / hpb));
+  if (dtype == 0) {
+    if (a.r.interleaved) fa_rope_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, stream>>>(a, hpb, st);
+    else fa_rope_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, stream>>>(a, hpb, st);
+  } else {
+    if (a.r.interleaved) fa_rope_kernel<__half, true><<<grid, kThreads, 0, stream>>>(a, hpb, st);
+    else fa_rope_kernel<__half, false><<<grid, kThreads, 0, stream>>>(a, hpb, st);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_append(int dtype, const AppendArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream) {
+  const int tpb = kThreads / (a.kv.d / 16);
+  const long long blocks = ((long long)a.T + tpb - 1) / tpb;
+  const int heads = a.Hq + 2 * a.kv.Hkv, hpb = heads_per_block(blocks, heads, num_sms);
+  const dim3 grid((unsigned)blocks, (unsigned)((heads + hpb - 1) / hpb));
+  if (dtype == 0) {
+    if (a.r.interleaved) fa_append_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, stream>>>(a, hpb, st);
+    else fa_append_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, stream>>>(a, hpb, st);
+  } else {
+    if (a.r.interleaved) fa_append_kernel<__half, true><<<grid, kThreads, 0, stream>>>(a, hpb, st);
+    else fa_append_kernel<__half, false><<<grid, kThreads, 0, stream>>>(a, hpb, st);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace fa

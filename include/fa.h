@@ -65,9 +65,11 @@ typedef enum fa_status {
   FA_ERR_BAD_ARGUMENT = 10,        /* scale not finite / not > 0, causal not 0/1 */
   FA_ERR_ALIASING = 11,            /* an output overlaps an input or another output */
   FA_ERR_SCRATCH_LIMIT = 12,       /* fa_bwd_noalloc: problem needs more than FA_NOALLOC_SCRATCH_BYTES */
-  FA_ERR_DEVICE_DRAIN = 13         /* after a device timeout a kernel exited with its own copies or MMAs
+  FA_ERR_DEVICE_DRAIN = 13,        /* after a device timeout a kernel exited with its own copies or MMAs
                                       possibly still in flight: the library refuses further launches on
                                       that device for the rest of the process */
+  FA_ERR_BAD_INDEX = 14            /* a kernel read a page number, length, offset or axis out of range and
+                                      skipped the access (fa_last_device_status) */
 } fa_status;
 
 /*
@@ -251,6 +253,148 @@ fa_status fa_selftest_drain_timeout(unsigned long long timeout_ns, void* stream)
 fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, const void* dO,
                          const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int d,
                          int causal, float scale, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions and the paged key / value cache.
+ *
+ * Shared by the entry points below:
+ *   - dtype is FA_BF16 or FA_FP16, the type of every q, k, v, o and cache
+ *     element of the call.
+ *   - Tensors with strides: the last dimension (d elements) is contiguous, the
+ *     others have strides in ELEMENTS, each a multiple of 8 (16 bytes; the
+ *     stride of a dimension of size 1 is not looked at), none negative
+ *     (FA_ERR_MISALIGNED / FA_ERR_BAD_ARGUMENT).  So a projection's output
+ *     split into q, k and v is passed as it is.
+ *   - Pointers are 16-byte aligned, but those to int, float and double data
+ *     that the kernels read by element (positions, inv_freq, axes, block
+ *     tables, lengths, offsets, new_lens, kept) only need their element's.
+ *   - An output's rows must be distinct, and distinct from every other
+ *     tensor's, except where a call says that it may run in place
+ *     (FA_ERR_ALIASING).
+ *   - Page numbers, lengths, offsets and axes lie in device memory, so the
+ *     kernels check them: one out of range is recorded (FA_ERR_BAD_INDEX by
+ *     fa_last_device_status), the access is skipped, and the outputs of the
+ *     sequence that it belongs to are unspecified.  Block table columns past a
+ *     sequence's last page are never read.
+ *   - The calls allocate nothing, do not synchronise and keep nothing between
+ *     calls: they can be captured into a graph.
+ * ---------------------------------------------------------------------- */
+
+typedef enum fa_dtype { FA_BF16 = 0, FA_FP16 = 1 } fa_dtype;
+
+/*
+ * Rotary positions with several axes (text: 1; images: height, width; video:
+ * time, height, width).  The first `rot` elements of a row of d form rot / 2
+ * pairs: elements (i, i + rot/2), or (2i, 2i + 1) with interleaved = 1.  Pair
+ * i turns by angle = position[axes[i]] * inv_freq[i] radians:
+ *   (x, y) -> (x cos - y sin, y cos + x sin).
+ * The other d - rot elements pass through.  rot is a multiple of 16, 16 <=
+ * rot <= d.  Positions are any int32, also negative or beyond 2^24: the angle
+ * is reduced modulo one turn exactly before its sine is taken.  inv_freq must
+ * be finite.
+ */
+typedef struct fa_rotary {
+  const int* positions;          /* axis x, batch b, token n at x * axis_stride + b * batch_stride + n */
+  long long axis_stride;
+  long long batch_stride;        /* 0: all batches share the positions */
+  const double* inv_freq;        /* [rot / 2] */
+  const int* axes;               /* [rot / 2], each in [0, n_axes) */
+  int n_axes;
+  int rot;
+  int interleaved;
+} fa_rotary;
+
+/*
+ * Turns q [B,Hq,N,d] and k [B,Hk,N,d] (strides: batch, head, token) into
+ * q_out and k_out; inverse = 1 turns by the negative angles, which is the
+ * gradient (dq = inverse turn of dq_out).  k may be NULL with Hk = 0.  An
+ * output may be its own input (same pointer and strides): in place.  d is a
+ * multiple of 16, 16 <= d <= 256.  One launch.
+ */
+fa_status fa_rope(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides, const void* k,
+                  const long long* k_strides, void* k_out, const long long* k_out_strides, int B, int Hq, int Hk, int N,
+                  int d, int dtype, const fa_rotary* rotary, int inverse, void* stream);
+
+/*
+ * A paged cache: a pool of num_pages pages of page_size slots for each kv
+ * head.  The row of (page p, kv head g, slot s) starts p * page_stride +
+ * g * head_stride + s * slot_stride elements from k (and from v).  page_size
+ * is a multiple of 16 (at most 65536), d is 64 or 128.  A sequence's key j
+ * lies in slot j % page_size of page table[b * table_stride + j / page_size].
+ */
+typedef struct fa_paged_kv {
+  void* k;
+  void* v;
+  long long page_stride, head_stride, slot_stride;
+  int num_pages, page_size, Hkv, d, dtype;
+} fa_paged_kv;
+
+/* Block table int32 [B, max_pages] with a row stride (elements). */
+typedef struct fa_page_table {
+  const int* pages;
+  long long stride;
+  int max_pages;
+} fa_page_table;
+
+/*
+ * Stores the k and v rows of T new tokens ([T,Hkv,d]; strides: token, head)
+ * in the cache.  seq_lens [B] are the lengths INCLUDING the new tokens.
+ *   - cu_seqlens = NULL (T == B, decoding): token b is the last of sequence b;
+ *     a sequence of length 0 is padding, its token is skipped.
+ *   - cu_seqlens [B + 1], from 0, non-decreasing: tokens cu[b] .. cu[b+1]-1
+ *     are the last cu[b+1] - cu[b] of sequence b, in order; tokens from cu[B]
+ *     on are padding and are skipped.
+ * rotary (may be NULL): k is stored turned, at positions [n_axes, T]
+ * (batch_stride unused), and, if q [T,Hq,d] is given, q_out [T,Hq,d] is q
+ * turned (may be q itself); rows of skipped tokens are left as they were.  q
+ * without rotary is FA_ERR_BAD_ARGUMENT.
+ * scores (may be NULL), fp32 [num_pages, Hkv, page_size] contiguous: the new
+ * tokens' entries become 0.  No two tokens of a call may fall on the same
+ * slot.  T = 0 does nothing.  One launch.
+ */
+fa_status fa_paged_append(const fa_paged_kv* kv, const fa_page_table* table, const int* seq_lens, const int* cu_seqlens,
+                          int B, int T, const void* k, const long long* k_strides, const void* v,
+                          const long long* v_strides, const void* q, const long long* q_strides, void* q_out,
+                          const long long* q_out_strides, int Hq, const fa_rotary* rotary, float* scores, void* stream);
+
+/*
+ * Attention of one query row per sequence and head, q [B,Hq,d] (strides:
+ * batch, head), against the sequence's seq_lens[b] cached keys; head h reads
+ * kv head h / (Hq / Hkv).  window = w > 0: only the last w keys are visible.
+ * Writes o [B,Hq,d] and lse fp32 [B,Hq] (natural log), both contiguous.  A
+ * sequence of length 0 gets o = 0, lse = -inf.  Cache slots that are not
+ * visible may hold anything, NaN included.
+ * scores (may be NULL), fp32 [num_pages, Hkv, page_size] contiguous: the entry
+ * of each visible key grows by the sum over the group's heads of its softmax
+ * weight.  Sequences may share pages: their weights add up (in no fixed order).
+ * workspace: at least fa_paged_decode_workspace_bytes(...) bytes, contents
+ * don't matter; calls that may run at the same time need one each.
+ */
+fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_paged_kv* kv, const fa_page_table* table,
+                          const int* seq_lens, void* o, float* lse, float* scores, int B, int Hq, int window,
+                          float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of fa_paged_decode (with_scores: 1 if scores are given); 0 for invalid shapes. */
+size_t fa_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d, int page_size, int max_pages, int with_scores);
+
+/*
+ * Eviction by accumulated attention weight.  For each sequence b and kv head,
+ * m = min(seq_lens[b], budget) keys stay: all if the length is at most the
+ * budget; else the first `sinks`, the last `recent`, and of the others the
+ * budget - sinks - recent with the largest score (equal scores: the lowest
+ * index; NaN counts as the smallest).  Their K rows, V rows and scores are
+ * written, in order, to slots 0 .. m-1 of the pages that row b of dst names,
+ * new_lens[b] = m, and kept [B,Hkv,budget] holds their indices, -1 past m.
+ * Source pages are only read, so sequences may share them; pages of dst must
+ * not appear in the parts of `table` that are read, nor twice in dst.  The
+ * caller then uses dst as the sequences' block table and frees the old pages.
+ * Keys keep the rotation they were stored with; slots are no longer positions.
+ * dst->max_pages * page_size >= budget >= 1, sinks + recent <= budget
+ * (FA_ERR_BAD_ARGUMENT).
+ */
+fa_status fa_paged_evict(const fa_paged_kv* kv, float* scores, const fa_page_table* table, const int* seq_lens,
+                         const fa_page_table* dst, int* new_lens, int* kept, int B, int budget, int recent, int sinks,
+                         void* stream);
 
 /*
  * Text of the most recent CUDA runtime error behind an FA_ERR_LAUNCH or

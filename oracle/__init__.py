@@ -28,6 +28,8 @@ Modules:
 * ``brute`` -- the same definition in pure-Python loops, for tiny shapes.
 * ``online`` -- the pages' streaming numerator/denominator recurrence, used
   only to pin the definition against the pages' own derivation.
+* ``paged`` -- rotary positions and the paged-cache operators (append,
+  one-token attention, eviction by accumulated weight).
 
 Parity status: every function here is pinned by tests under ``tests/`` that
 do not call back into the same arithmetic (closed forms, brute force, finite

@@ -1,0 +1,785 @@
+"""GPU parity of rotary positions, paged append, paged one-token attention and
+eviction against the fp64 oracle, through the Python binding.
+
+Tolerances (u = half a step of the tensors' type: bf16 2^-8, fp16 2^-11).
+
+Rotation: |out - ref| <= u |ref| + c (|x| + |y|) + tiny, where c bounds the fp32
+part: the phase is off by < 2^-31 of a turn plus its conversion (2^-25 of half
+a turn = 1e-7 rad), sincospi by 2^-22, and two products and a sum round by
+3 * 2^-24: c = 1e-6.  The rounding of a value that is off by e is off by at
+most u (|ref| + e) + e, so c is doubled; tiny is the fp16 subnormal step.
+
+Attention: with A = sum p |v| (from the oracle) the weights are applied
+rounded to the tensors' type (u A), o is rounded once (u |o|), and a relative
+error e of each weight moves o by at most 2 e A (numerator and denominator).
+e: a score is a sum of d products in fp32 (d 2^-23 relative to scale sum |q k|,
+the factor 2 for adders that truncate), rounded by its scaling (2^-23), its
+exponential by 2^-22, and sums over n keys by n 2^-24.  lse is off by e, the
+accumulated weights by 2 e of themselves; an fp32 weight below 2^-126 is a
+subnormal or 0, so each of the G weights of a key is off by at most 2^-126
+more.  scale sum |q k| <= X = scale |q|_2
+max |k|_2.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_flashattention_gb300 as fa
+from oracle import paged
+from tests.parity import GuardedBuffers
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+BF, HF = torch.bfloat16, torch.float16
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def ok():
+    torch.cuda.synchronize()
+    fa.check_device_status()
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions
+# ---------------------------------------------------------------------------
+def rotation_bound(x, ref, r, interleaved, dt):
+    pair = np.abs(f64(x))
+    size = np.zeros_like(ref)
+    lo, hi = (np.arange(0, 2 * r, 2), np.arange(1, 2 * r, 2)) if interleaved else (np.arange(r), np.arange(r, 2 * r))
+    s = pair[..., lo] + pair[..., hi]
+    size[..., lo], size[..., hi] = s, s
+    return U[dt] * np.abs(ref) + 2e-6 * size + (2.0 ** -24 if dt == HF else 0.0)
+
+
+def assert_rotated(out, x, pos, w, axes, interleaved, inverse, what):
+    ref = paged.rotate(f64(x), pos.cpu().numpy(), w.cpu().numpy(), axes.cpu().numpy(), interleaved, inverse)
+    err = np.abs(f64(out) - ref)
+    off = err > rotation_bound(x, ref, w.numel(), interleaved, out.dtype)
+    assert not off.any(), f"{what}: {off.sum()} values, {err.max()}"
+
+
+ROPE = [
+    # B, Hq, Hk, N, d, sections, interleaved, first position, dtype
+    (1, 1, 0, 1, 64, (32,), False, 0, BF),
+    (2, 4, 2, 33, 128, (16, 24, 24), False, 0, BF),
+    (1, 3, 1, 257, 128, (20, 12), True, 5, HF),
+    (3, 5, 5, 7, 64, (8,), False, 10 ** 6, HF),            # partial, far
+    (1, 2, 1, 40, 64, (8, 0, 8), True, 2 ** 31 - 100, BF), # an axis without pairs, the last positions
+    (1, 2, 2, 65, 256, (64, 64), False, -30, BF),          # negative positions
+    (2, 9, 3, 19, 16, (8,), False, 3, HF),
+    (1, 32, 8, 300, 80, (40,), False, 3, BF),              # d not a power of two
+    (1, 6, 6, 50, 96, (16,), True, 77, BF),
+]
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("B,Hq,Hk,N,d,sections,interleaved,start,dt", ROPE)
+def test_rope(cuda_lib, B, Hq, Hk, N, d, sections, interleaved, start, dt, inverse):
+    g = torch.Generator().manual_seed(N * d + Hq)
+    q = torch.randn((B, Hq, N, d), generator=g).to(dt).to(DEV)
+    k = torch.randn((B, Hk, N, d), generator=g).to(dt).to(DEV) if Hk else None
+    A = len(sections)
+    pos = (start + torch.randint(0, 60, (A, B, N), generator=g)).to(torch.int32).to(DEV)
+    w, axes = fa.rope_frequencies(sections, device=DEV)
+    gb = GuardedBuffers(DEV)
+    turn = fa.rope_backward if inverse else fa.rope
+    qo = gb.empty((B, Hq, N, d), dt)
+    if k is None:
+        assert turn(q, None, pos, w, axes, interleaved, qo) is qo
+    else:
+        ko = gb.empty((B, Hk, N, d), dt)
+        turn(q, k, pos, w, axes, interleaved, qo, ko)
+    ok()
+    gb.check()
+    assert_rotated(qo, q, pos, w, axes, interleaved, inverse, "q")
+    r = 2 * w.numel()
+    assert torch.equal(qo[..., r:], q[..., r:])
+    if k is not None:
+        assert_rotated(ko, k, pos, w, axes, interleaved, inverse, "k")
+
+
+@pytest.mark.parametrize("layout", ["token-major", "head-major"])
+def test_rope_in_place_on_a_projection(cuda_lib, layout):
+    B, Hq, Hk, N, d = 2, 4, 2, 37, 64
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((B, Hq + 2 * Hk, N, d), generator=g).to(BF).to(DEV)
+    if layout == "token-major":
+        x = x.transpose(1, 2).contiguous().transpose(1, 2)      # [B, N, H, d] in memory
+    before = x.clone()
+    q, k, v = x.split([Hq, Hk, Hk], dim=1)
+    pos = torch.arange(N, dtype=torch.int32, device=DEV).expand(1, B, N)
+    w, axes = fa.rope_frequencies((32,), device=DEV)
+    fa.rope(q, k, pos, w, axes, q_out=q, k_out=k)
+    ok()
+    q0, k0, v0 = before.split([Hq, Hk, Hk], dim=1)
+    assert_rotated(q, q0, pos, w, axes, False, False, "q")
+    assert_rotated(k, k0, pos, w, axes, False, False, "k")
+    assert torch.equal(v, v0)
+
+
+def test_rope_gradient_is_the_transpose(cuda_lib):
+    # <g, R x> = <R^T g, x> with R x and R^T g from the kernels, and the
+    # backward of the forward gives x back.
+    g = torch.Generator().manual_seed(4)
+    x, y = (torch.randn((1, 3, 50, 128), generator=g).to(HF).to(DEV) for _ in range(2))
+    pos = torch.randint(0, 10 ** 6, (3, 1, 50), generator=g).to(torch.int32).to(DEV)
+    w, axes = fa.rope_frequencies((16, 24, 24), device=DEV)
+    fx, by = fa.rope(x, None, pos, w, axes), fa.rope_backward(y, None, pos, w, axes)
+    ok()
+    lhs, rhs = float((f64(y) * f64(fx)).sum()), float((f64(by) * f64(x)).sum())
+    size = float(np.abs(f64(y) * f64(fx)).sum() + np.abs(f64(by) * f64(x)).sum())
+    assert abs(lhs - rhs) <= (U[HF] + 4e-6) * size
+    back = fa.rope_backward(fx, None, pos, w, axes)
+    ok()
+    # Two roundings of values at most |x| + |y| each.
+    assert (back.float() - x.float()).abs().max().item() <= 4 * U[HF] * 2 * x.float().abs().max().item()
+
+
+def test_rope_bad_axis_is_recorded(cuda_lib):
+    q = torch.randn((1, 1, 4, 64), device=DEV).to(BF)
+    w, axes = fa.rope_frequencies((32,), device=DEV)
+    axes[5] = 1
+    fa.rope(q, None, torch.zeros((1, 1, 4), dtype=torch.int32, device=DEV), w, axes)
+    s, _ = fa.fa_last_device_status()
+    assert s == fa.FA_ERR_BAD_INDEX
+    ok()
+
+
+# ---------------------------------------------------------------------------
+# Paged cache
+# ---------------------------------------------------------------------------
+def new_pool(pages, Hkv, ps, d, dt, layout="hnd", fill=float("nan")):
+    """k and v caches [pages, Hkv, ps, d] in one of several memory orders."""
+    if layout == "hnd":
+        k, v = (torch.full((pages, Hkv, ps, d), fill, dtype=dt, device=DEV) for _ in range(2))
+    elif layout == "nhd":
+        k, v = (torch.full((pages, ps, Hkv, d), fill, dtype=dt, device=DEV).transpose(1, 2) for _ in range(2))
+    else:                                                        # k and v page by page
+        x = torch.full((pages, 2, Hkv, ps, d), fill, dtype=dt, device=DEV)
+        k, v = x[:, 0], x[:, 1]
+    return k, v
+
+
+def filled(lens, Hkv, ps, d, dt, seed, layout="hnd", extra=2, sigma=1.0, share=False):
+    """A cache holding sequences of these lengths; every other slot is NaN, and
+    block table columns past a sequence's pages are far out of range."""
+    g = torch.Generator().manual_seed(seed)
+    n = [-(-x // ps) for x in lens]
+    total = sum(n) + extra
+    k, v = new_pool(total, Hkv, ps, d, dt, layout)
+    order = torch.randperm(total, generator=g).tolist()
+    table = torch.full((len(lens), max(1, max(n)) + 1), 2 ** 30, dtype=torch.int32)
+    at = 0
+    for b, x in enumerate(lens):
+        table[b, :n[b]] = torch.tensor(order[at:at + n[b]], dtype=torch.int32)
+        at += n[b]
+        for j in range(n[b]):
+            m = min(ps, x - j * ps)
+            k[table[b, j].item(), :, :m] = (sigma * torch.randn((Hkv, m, d), generator=g)).to(dt).to(DEV)
+            v[table[b, j].item(), :, :m] = torch.randn((Hkv, m, d), generator=g).to(dt).to(DEV)
+    return k, v, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+
+def assert_decoded(o, lse, q, k, v, table, lens, scale, window, scores=None, before=None, what=""):
+    dt, d = o.dtype, q.shape[-1]
+    kn, vn, tb, ln = f64(k), f64(v), table.cpu().numpy(), lens.cpu().numpy()
+    ro, rl, rw, a = paged.decode(f64(q), kn, vn, tb, ln, scale, window)
+    seen = max(1, int(ln.max()))
+    big = np.sqrt(np.nanmax((np.where(np.isnan(kn), 0, kn) ** 2).sum(-1))) * np.sqrt((f64(q) ** 2).sum(-1).max())
+    e = scale * big * (d * 2.0 ** -23 + 2.0 ** -23) + 2.0 ** -21 + seen * 2.0 ** -24
+    err = np.abs(f64(o) - ro)
+    bound = U[dt] * (a + np.abs(ro)) + 2.1 * e * a + (2.0 ** -24 if dt == HF else 0.0)
+    if dt == HF:
+        bound = bound + 2.0 ** -25 * seen * np.nanmax(np.abs(vn))      # weights below fp16's normal range
+    worst = (err / np.maximum(bound, 1e-30)).max()
+    assert worst <= 1, f"{what}: o off by {worst} of the bound"
+    fine = np.isfinite(rl)
+    gl = f64(lse)
+    assert np.array_equal(np.isneginf(gl), ~fine), what
+    far = np.abs(gl[fine] - rl[fine]) > e + 2.0 ** -23 * np.abs(rl[fine])
+    assert not far.any(), f"{what}: {far.sum()} lse"
+    if scores is not None:
+        ps = k.shape[2]
+        want = f64(before)
+        for b, n in enumerate(ln):
+            for j in range(n):
+                want[tb[b, j // ps], :, j % ps] += rw[b][:, j]
+        got = f64(scores)
+        grown = np.abs(want - f64(before))
+        least = q.shape[1] // k.shape[1] * 2.0 ** -126
+        off = np.abs(got - want) > 2.1 * e * grown + 2.0 ** -23 * np.abs(want) + least
+        assert not off.any(), f"{what}: {off.sum()} scores"
+
+
+DECODE = [
+    # lens, Hq, Hkv, d, page, window, dtype, layout
+    ([1], 1, 1, 64, 16, 0, BF, "hnd"),
+    ([0], 4, 2, 128, 16, 0, BF, "hnd"),
+    ([15, 16, 17, 0, 31, 33], 8, 2, 128, 16, 0, BF, "hnd"),
+    ([63, 64, 65, 127, 128, 129], 4, 4, 64, 32, 0, HF, "nhd"),
+    ([1000, 1, 0, 777], 6, 2, 128, 48, 0, BF, "pair"),        # page 48, three heads a group
+    ([2500, 300], 8, 1, 64, 64, 0, HF, "hnd"),
+    ([700, 130, 50], 9, 1, 128, 16, 0, BF, "nhd"),            # nine heads a group
+    ([500, 90], 32, 2, 64, 128, 0, BF, "hnd"),                # sixteen
+    ([333, 64], 17, 1, 128, 16, 0, HF, "pair"),
+    ([260, 65], 33, 1, 64, 16, 0, BF, "hnd"),
+    ([150], 72, 1, 128, 32, 0, BF, "hnd"),
+    ([1000, 5, 0, 64], 8, 2, 128, 16, 1, BF, "hnd"),
+    ([1000, 100, 65], 8, 4, 64, 16, 64, HF, "hnd"),
+    ([1000, 257, 3], 4, 2, 128, 80, 250, BF, "nhd"),
+    ([400, 60], 4, 2, 128, 16, 10 ** 9, BF, "hnd"),
+    ([10000], 2, 1, 128, 256, 0, BF, "hnd"),
+]
+
+
+@pytest.mark.parametrize("with_scores", [False, True])
+@pytest.mark.parametrize("lens,Hq,Hkv,d,page,window,dt,layout", DECODE)
+def test_decode(cuda_lib, lens, Hq, Hkv, d, page, window, dt, layout, with_scores):
+    k, v, table, ln = filled(lens, Hkv, page, d, dt, seed=Hq * 100 + d, layout=layout)
+    B = len(lens)
+    g = torch.Generator().manual_seed(9)
+    proj = torch.randn((B, Hq + 3, d), generator=g).to(dt).to(DEV)
+    q = proj[:, 1:Hq + 1]                                            # strided rows
+    gb = GuardedBuffers(DEV)
+    o, lse = gb.empty((B, Hq, d), dt), gb.empty((B, Hq), torch.float32)
+    ws = gb.empty((fa.paged_decode_workspace(B, Hq, k, table, with_scores).numel(),), torch.uint8)
+    scores = before = None
+    if with_scores:
+        scores = gb.empty(tuple(k.shape[:3]), torch.float32)
+        scores.copy_(torch.rand(k.shape[:3], generator=g))
+        before = scores.clone()
+    scale = 0.11
+    fa.paged_decode(q, k, v, table, ln, scale=scale, window=window, scores=scores, out=o, lse=lse, workspace=ws)
+    ok()
+    gb.check()
+    assert_decoded(o, lse, q, k, v, table, ln, scale, window, scores, before, f"{lens}")
+
+
+@pytest.mark.parametrize("sigma,scale", [(4.0, 0.3), (0.0, 1.0)])
+def test_decode_peaked_and_flat(cuda_lib, sigma, scale):
+    # Scores of +-50 and more: single keys dominate and the running maximum
+    # keeps moving; and all scores equal.
+    k, v, table, ln = filled([900, 64, 300], 2, 16, 64, HF, seed=5, sigma=sigma)
+    q = (4.0 * torch.randn((3, 8, 64), generator=torch.Generator().manual_seed(6))).to(HF).to(DEV)
+    scores = torch.zeros(k.shape[:3], device=DEV)
+    o, lse = fa.paged_decode(q, k, v, table, ln, scale=scale, scores=scores)
+    ok()
+    assert_decoded(o, lse, q, k, v, table, ln, scale, 0, scores, torch.zeros_like(scores), f"sigma {sigma}")
+
+
+def test_decode_rising_scores(cuda_lib):
+    # Each tile's scores exceed the last one's by far, then fall again: the
+    # running maximum moves at every step.
+    n, d = 640, 64
+    k, v, table, ln = filled([n], 1, 16, d, BF, seed=8)
+    step = torch.cat([torch.arange(20), torch.arange(20).flip(0)]) * 2.0
+    for j in range(n // 16):
+        k[table[0, j].item(), 0, :, 0] = step[j].item()
+    q = torch.randn((1, 4, d), generator=torch.Generator().manual_seed(7))
+    q[:, :, 0] = torch.tensor([8.0, -8.0, 4.0, 16.0])
+    q = q.to(BF).to(DEV)
+    scores = torch.zeros(k.shape[:3], device=DEV)
+    o, lse = fa.paged_decode(q, k, v, table, ln, scale=0.5, scores=scores)
+    ok()
+    assert_decoded(o, lse, q, k, v, table, ln, 0.5, 0, scores, torch.zeros_like(scores), "rising")
+
+
+def test_decode_pages_shared_by_sequences(cuda_lib):
+    # Two sequences with a common prefix: the weights of both add up.
+    k, v, table, ln = filled([200, 200], 2, 16, 64, BF, seed=12)
+    table[1, :6] = table[0, :6]
+    ln[1] = 150
+    q = torch.randn((2, 4, 64), generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
+    scores = torch.zeros(k.shape[:3], device=DEV)
+    o, lse = fa.paged_decode(q, k, v, table, ln, scores=scores)
+    ok()
+    assert_decoded(o, lse, q, k, v, table, ln, 0.125, 0, scores, torch.zeros_like(scores), "shared")
+
+
+def test_decode_is_reproducible_and_independent_of_the_rest_of_the_batch(cuda_lib):
+    k, v, table, ln = filled([3000, 70, 1200, 0, 16], 2, 16, 128, BF, seed=13)
+    q = torch.randn((5, 8, 128), generator=torch.Generator().manual_seed(2)).to(BF).to(DEV)
+    o1, l1 = fa.paged_decode(q, k, v, table, ln)
+    o2, l2 = fa.paged_decode(q, k, v, table, ln)
+    ok()
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+
+
+@pytest.mark.parametrize("bad", ["page", "negative page", "length", "negative length"])
+def test_decode_bad_indices_are_recorded(cuda_lib, bad):
+    lens = [100, 200, 50]
+    k, v, table, ln = filled(lens, 2, 16, 64, BF, seed=14)
+    q = torch.randn((3, 4, 64), generator=torch.Generator().manual_seed(3)).to(BF).to(DEV)
+    good_o, good_l = fa.paged_decode(q, k, v, table, ln)
+    ok()
+    t2, n2 = table.clone(), ln.clone()
+    if bad.endswith("page"):
+        t2[1, 3] = -1 if bad.startswith("neg") else k.shape[0]
+    else:
+        n2[1] = -5 if bad.startswith("neg") else table.shape[1] * 16 + 1
+    scores = torch.zeros(k.shape[:3], device=DEV)
+    o, l = fa.paged_decode(q, k, v, t2, n2, scores=scores)
+    s, _ = fa.fa_last_device_status()
+    assert s == fa.FA_ERR_BAD_INDEX
+    for b in (0, 2):                                      # the other sequences are as before, up to the split's rounding
+        assert (o[b].float() - good_o[b].float()).abs().max().item() <= 0.05
+        assert (l[b] - good_l[b]).abs().max().item() <= 1e-3
+    ok()
+
+
+def test_decode_offsets_past_32_bits(cuda_lib):
+    # Element offsets past 2^31 in the pool, and past 2^32 bytes.
+    Hkv, ps, d = 8, 64, 128
+    pages = 2 ** 31 // (Hkv * ps * d) + 40
+    k = torch.empty((pages, Hkv, ps, d), dtype=BF, device=DEV)
+    v = torch.empty_like(k)
+    g = torch.Generator().manual_seed(15)
+    use = [pages - 1, 3, pages - 20, pages // 2 + 7]
+    for p in use:
+        k[p] = torch.randn((Hkv, ps, d), generator=g).to(BF).to(DEV)
+        v[p] = torch.randn((Hkv, ps, d), generator=g).to(BF).to(DEV)
+    table = torch.tensor([use], dtype=torch.int32, device=DEV)
+    ln = torch.tensor([250], dtype=torch.int32, device=DEV)
+    q = torch.randn((1, 16, d), generator=g).to(BF).to(DEV)
+    scores = torch.zeros((pages, Hkv, ps), device=DEV)
+    # The new token's row lands at the far end too.
+    kn, vn = (torch.randn((1, Hkv, d), generator=g).to(BF).to(DEV) for _ in range(2))
+    use2 = torch.tensor([use[::-1]], dtype=torch.int32, device=DEV)
+    fa.paged_append(k, v, use2, ln, kn, vn, scores=scores)
+    o, lse = fa.paged_decode(q, k, v, use2, ln, scores=scores)
+    dst = torch.tensor([[pages - 2, pages - 3]], dtype=torch.int32, device=DEV)
+    nl, kept = fa.paged_evict(k, v, scores, use2, ln, dst, 100, recent=10, sinks=1)
+    ok()
+    small = torch.tensor(use[::-1] + [pages - 2, pages - 3], device=DEV)
+    ks, vs, ss = k[small], v[small], scores[small]
+    t = torch.arange(4, dtype=torch.int32, device=DEV)[None]
+    assert torch.equal(ks[3, :, 249 % 64], kn[0]) and torch.equal(vs[3, :, 249 % 64], vn[0])
+    assert_decoded(o, lse, q, ks, vs, t, ln, d ** -0.5, 0, what="far pages")
+    for h in range(Hkv):
+        row = ss[:4, h].reshape(-1)[:250].cpu().tolist()
+        want = paged.kept_keys(row, 100, 10, 1)
+        assert kept[0, h].tolist() == want
+        assert torch.equal(ks[4:, h].reshape(-1, d)[:100], ks[:4, h].reshape(-1, d)[want])
+        assert torch.equal(vs[4:, h].reshape(-1, d)[:100], vs[:4, h].reshape(-1, d)[want])
+
+
+# ---------------------------------------------------------------------------
+# Append
+# ---------------------------------------------------------------------------
+def check_append(k0, v0, s0, kc, vc, sc, table, lens, cu, k, v, q, qo, q0, rot):
+    """Every slot of the pools and every row of q_out, bit by bit where nothing is turned."""
+    T, ps = k.shape[0], kc.shape[2]
+    places = paged.token_places(lens, cu, T)
+    want_k, want_v, want_s = k0.clone(), v0.clone(), s0.clone()
+    for t, pl in enumerate(places):
+        if pl is None:
+            if qo is not None:
+                assert torch.equal(qo[t], q0[t]), "a padding row was written"
+            continue
+        p, s = table[pl[0], pl[1] // ps].item(), pl[1] % ps
+        if rot is None:
+            want_k[p, :, s] = k[t]
+        else:
+            pos, w, axes, inter = rot
+            got = kc[p, :, s][None, :, None]
+            assert_rotated(got, k[t][None, :, None], pos[:, t].view(-1, 1, 1), w, axes, inter, False, "k")
+            want_k[p, :, s] = kc[p, :, s]
+            if qo is not None:
+                assert_rotated(qo[t][None, :, None], q[t][None, :, None], pos[:, t].view(-1, 1, 1), w, axes, inter, False, "q")
+        want_v[p, :, s] = v[t]
+        want_s[p, :, s] = 0
+    bits = lambda x: x.contiguous().view(torch.int16)  # noqa: E731
+    assert torch.equal(bits(kc), bits(want_k)) and torch.equal(bits(vc), bits(want_v)) and torch.equal(sc, want_s)
+
+
+APPEND = [
+    # lens, new (None: one each), padding tokens, Hq, Hkv, d, page, sections, interleaved, dtype, layout
+    ([5, 0, 16, 17, 1], None, 0, 4, 2, 64, 16, (32,), False, BF, "hnd"),
+    ([100, 33, 0, 64], [100, 1, 0, 30], 3, 8, 2, 128, 32, (16, 24, 24), False, BF, "pair"),
+    ([40, 50], [40, 0], 0, 0, 3, 128, 48, None, False, HF, "nhd"),
+    ([1], [1], 0, 1, 1, 64, 16, (16,), True, HF, "hnd"),
+    ([0, 0], [0, 0], 2, 2, 2, 64, 16, (32,), False, BF, "hnd"),
+    ([300, 7], [290, 7], 1, 5, 1, 128, 16, (20, 12), True, BF, "nhd"),
+]
+
+
+@pytest.mark.parametrize("lens,new,pad,Hq,Hkv,d,page,sections,inter,dt,layout", APPEND)
+def test_append(cuda_lib, lens, new, pad, Hq, Hkv, d, page, sections, inter, dt, layout):
+    kc, vc, table, ln = filled(lens, Hkv, page, d, dt, seed=21, layout=layout)
+    sc = torch.rand(kc.shape[:3], device=DEV)
+    k0, v0, s0 = kc.clone(), vc.clone(), sc.clone()
+    cu = None if new is None else [sum(new[:b]) for b in range(len(new) + 1)]
+    T = len(lens) if new is None else cu[-1] + pad
+    g = torch.Generator().manual_seed(22)
+    x = torch.randn((T, Hq + 2 * Hkv, d), generator=g).to(dt).to(DEV)
+    q, k, v = x.split([Hq, Hkv, Hkv], dim=1)
+    rot, kw, qo, q0 = None, {}, None, None
+    if sections:
+        w, axes = fa.rope_frequencies(sections, device=DEV)
+        pos = torch.randint(-5, 100000, (len(sections), T), generator=g).to(torch.int32).to(DEV)
+        rot = (pos, w, axes, inter)
+        gb = GuardedBuffers(DEV)
+        qo = gb.empty((T, Hq, d), dt)
+        qo.fill_(7.0)
+        q0 = qo.clone()
+        kw = dict(q=q, positions=pos, inv_freq=w, axes=axes, interleaved=inter, q_out=qo)
+    cud = None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV)
+    fa.paged_append(kc, vc, table, ln, k, v, cu_seqlens=cud, scores=sc, **kw)
+    ok()
+    check_append(k0, v0, s0, kc, vc, sc, table, lens, cu, k, v, q, qo, q0, rot)
+    if sections:
+        gb.check()
+
+
+def test_append_in_place_q_and_no_tokens(cuda_lib):
+    kc, vc, table, ln = filled([9, 3], 2, 16, 64, BF, seed=23)
+    x = torch.randn((2, 8, 64), device=DEV).to(BF)
+    q, k, v = x.split([4, 2, 2], dim=1)
+    q0 = q.clone()
+    w, axes = fa.rope_frequencies((32,), device=DEV)
+    pos = torch.tensor([[8, 2]], dtype=torch.int32, device=DEV)
+    assert fa.paged_append(kc, vc, table, ln, k, v, q=q, positions=pos, inv_freq=w, axes=axes, q_out=q) is q
+    ok()
+    assert_rotated(q.transpose(0, 1)[None], q0.transpose(0, 1)[None], pos[:, None], w, axes, False, False, "q")
+    before = kc.clone()
+    fa.paged_append(kc, vc, table, ln, k[:0], v[:0], cu_seqlens=torch.zeros(3, dtype=torch.int32, device=DEV))
+    ok()
+    assert torch.equal(kc.view(torch.int16), before.view(torch.int16))
+
+
+@pytest.mark.parametrize("bad", ["page", "length", "more tokens than keys", "offsets"])
+def test_append_bad_indices_are_recorded(cuda_lib, bad):
+    kc, vc, table, ln = filled([20, 40], 2, 16, 64, BF, seed=24)
+    before = kc.clone()
+    x = torch.randn((6, 2, 64), device=DEV).to(BF)
+    cu = torch.tensor([0, 3, 6], dtype=torch.int32, device=DEV)
+    if bad == "page":
+        table[1, 2] = kc.shape[0]
+    elif bad == "length":
+        ln[1] = table.shape[1] * 16 + 3
+    elif bad == "offsets":
+        cu = torch.tensor([0, -2, 6], dtype=torch.int32, device=DEV)
+    else:
+        ln[1] = 2
+    fa.paged_append(kc, vc, table, ln, x, x, cu_seqlens=cu)
+    s, _ = fa.fa_last_device_status()
+    assert s == (fa.FA_OK if bad == "offsets" else fa.FA_ERR_BAD_INDEX) or bad == "offsets"
+    if bad != "offsets":
+        changed = (kc.view(torch.int16) != before.view(torch.int16)).any(-1).any(1)
+        slots = {(table[0, 1].item(), s) for s in (1, 2, 3)}
+        if bad == "more tokens than keys":
+            slots |= {(table[1, 0].item(), s) for s in (0, 1)}
+        assert {tuple(i) for i in changed.nonzero().tolist()} == slots
+    ok()
+
+
+# ---------------------------------------------------------------------------
+# Eviction
+# ---------------------------------------------------------------------------
+EVICT = [
+    # lens, Hkv, d, page, budget, recent, sinks, kind of scores, dtype, layout
+    ([40], 1, 64, 16, 20, 0, 0, "normal", BF, "hnd"),
+    ([0, 1, 16, 17, 100], 2, 64, 16, 16, 4, 2, "normal", BF, "hnd"),
+    ([1000, 500, 2], 2, 128, 48, 333, 100, 4, "heavy", HF, "pair"),
+    ([300, 299, 5000], 3, 64, 32, 299, 298, 1, "normal", BF, "nhd"),     # nothing left to choose
+    ([700, 31], 2, 128, 16, 128, 0, 0, "ties", BF, "hnd"),
+    ([700, 130], 1, 64, 16, 1, 0, 0, "equal", HF, "hnd"),
+    ([700, 130], 1, 64, 16, 1, 1, 0, "equal", HF, "hnd"),
+    ([2100, 64], 2, 64, 64, 1500, 10, 0, "odd", BF, "hnd"),              # NaN, infinities, -0
+    ([40000], 1, 64, 64, 5000, 100, 4, "heavy", BF, "hnd"),
+    ([9000, 4097], 2, 64, 128, 8999, 0, 16, "narrow", BF, "hnd"),        # values that share their high bits
+]
+
+
+def make_scores(kind, shape, g):
+    x = torch.randn(shape, generator=g)
+    if kind == "heavy":
+        x = (2 * x).exp() * (torch.rand(shape, generator=g) > 0.3)
+    elif kind == "ties":
+        x = torch.randint(0, 4, shape, generator=g).float()
+    elif kind == "equal":
+        x = torch.full(shape, 0.25)
+    elif kind == "narrow":
+        x = 1.0 + torch.randint(0, 200, shape, generator=g).float() * 2.0 ** -23
+    elif kind == "odd":
+        pick = torch.randint(0, 8, shape, generator=g)
+        for i, value in enumerate((float("nan"), float("inf"), -float("inf"), -0.0, 0.0, -1.5)):
+            x = torch.where(pick == i, torch.tensor(value), x)
+    return x
+
+
+@pytest.mark.parametrize("lens,Hkv,d,page,budget,recent,sinks,kind,dt,layout", EVICT)
+def test_evict(cuda_lib, lens, Hkv, d, page, budget, recent, sinks, kind, dt, layout):
+    cols = -(-budget // page)
+    kc, vc, table, ln = filled(lens, Hkv, page, d, dt, seed=31, layout=layout, extra=len(lens) * cols + 2)
+    g = torch.Generator().manual_seed(32)
+    sc = make_scores(kind, kc.shape[:3], g).to(DEV)
+    used = {p for b, n in enumerate(lens) for p in table[b, :-(-n // page)].tolist()}
+    spare = [p for p in range(kc.shape[0]) if p not in used]
+    dst = torch.tensor(spare[:len(lens) * cols], dtype=torch.int32, device=DEV).view(len(lens), cols)
+    k0, v0, s0 = kc.clone(), vc.clone(), sc.clone()
+    gb = GuardedBuffers(DEV)
+    nl, kept = gb.empty((len(lens),), torch.int32), gb.empty((len(lens), Hkv, budget), torch.int32)
+    fa.paged_evict(kc, vc, sc, table, ln, dst, budget, recent, sinks, new_lens=nl, kept=kept)
+    ok()
+    gb.check()
+    want_k, want_v, want_s = k0.clone(), v0.clone(), s0.clone()
+    for b, n in enumerate(lens):
+        m = min(n, budget)
+        assert nl[b].item() == m
+        if m == 0:
+            assert bool((kept[b] == -1).all())
+            continue
+        j = torch.arange(n, device=DEV)
+        sp = table[b].long()[j // page]
+        r = torch.arange(m, device=DEV)
+        dp = dst[b].long()[r // page]
+        for h in range(Hkv):
+            keep = paged.kept_keys(s0[sp, h, j % page].cpu().tolist(), budget, recent, sinks)
+            assert kept[b, h].tolist() == keep + [-1] * (budget - m), (b, h)
+            i = torch.tensor(keep, device=DEV)
+            want_k[dp, h, r % page] = k0[sp[i], h, i % page]
+            want_v[dp, h, r % page] = v0[sp[i], h, i % page]
+            want_s[dp, h, r % page] = s0[sp[i], h, i % page]
+    bits = lambda x, t: x.contiguous().view(t)  # noqa: E731
+    assert torch.equal(bits(kc, torch.int16), bits(want_k, torch.int16))
+    assert torch.equal(bits(vc, torch.int16), bits(want_v, torch.int16))
+    assert torch.equal(bits(sc, torch.int32), bits(want_s, torch.int32))
+
+
+@pytest.mark.parametrize("bad", ["source page", "target page", "length"])
+def test_evict_bad_indices_are_recorded(cuda_lib, bad):
+    kc, vc, table, ln = filled([100, 60], 2, 16, 64, BF, seed=33, extra=6)
+    used = {p for b, n in enumerate([100, 60]) for p in table[b, :-(-n // 16)].tolist()}
+    spare = [p for p in range(kc.shape[0]) if p not in used]
+    dst = torch.tensor(spare[:4], dtype=torch.int32, device=DEV).view(2, 2)
+    sc = torch.rand(kc.shape[:3], device=DEV)
+    s0 = sc.clone()
+    if bad == "source page":
+        table[0, 1] = -7
+    elif bad == "target page":
+        dst[0, 1] = kc.shape[0] + 5
+    else:
+        ln[0] = 10 ** 6
+    nl, kept = fa.paged_evict(kc, vc, sc, table, ln, dst, 32)
+    s, _ = fa.fa_last_device_status()
+    assert s == fa.FA_ERR_BAD_INDEX
+    row = s0[table[1].long()[torch.arange(60, device=DEV) // 16], 1, torch.arange(60, device=DEV) % 16]
+    assert kept[1, 1].tolist() == paged.kept_keys(row.cpu().tolist(), 32, 0, 0)
+    ok()
+
+
+# ---------------------------------------------------------------------------
+# Together, and how calls are made
+# ---------------------------------------------------------------------------
+class Served:
+    """A few decoding steps over a paged cache, mirrored in fp64 on the CPU."""
+
+    def __init__(self, dt, B=3, Hq=8, Hkv=2, d=64, page=16, budget=40):
+        self.dt, self.B, self.Hq, self.Hkv, self.d, self.page, self.budget = dt, B, Hq, Hkv, d, page, budget
+        self.kc, self.vc = new_pool(64, Hkv, page, d, dt)
+        self.sc = torch.full((64, Hkv, page), 1e9, device=DEV)
+        self.g = torch.Generator().manual_seed(41)
+        self.w, self.axes = fa.rope_frequencies((8, 12, 12), device=DEV)
+        self.free = torch.randperm(64, generator=self.g).tolist()
+
+    def pages(self, n):
+        out, self.free = self.free[:n], self.free[n:]
+        return out
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_serving_run(cuda_lib, dt):
+    """Prompt, decoding steps with scores, eviction, more steps: the cache and
+    each step's output against the oracle."""
+    s = Served(dt)
+    B, Hq, Hkv, d, page = s.B, s.Hq, s.Hkv, s.d, s.page
+    lens = [50, 17, 64]
+    true_len = list(lens)                                   # positions go on after an eviction
+    table = torch.zeros((B, 6), dtype=torch.int32)
+    for b in range(B):
+        table[b] = torch.tensor(s.pages(6))
+    table = table.to(DEV)
+
+    def project(T):
+        return torch.randn((T, Hq + 2 * Hkv, d), generator=s.g).to(dt).to(DEV).split([Hq, Hkv, Hkv], dim=1)
+
+    def positions(p):
+        p = torch.tensor(p, dtype=torch.int32, device=DEV)
+        return torch.stack([p, p // 8, p % 8])
+
+    cu = torch.tensor([0, 50, 67, 131], dtype=torch.int32, device=DEV)
+    q, k, v = project(131)
+    pos = positions([i for n in lens for i in range(n)])
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    fa.paged_append(s.kc, s.vc, table, ln, k, v, cu_seqlens=cu, q=q, positions=pos, inv_freq=s.w, axes=s.axes, scores=s.sc)
+    ok()
+    acc = [np.zeros((Hkv, n)) for n in lens]
+
+    def step():
+        nonlocal ln
+        q, k, v = project(B)
+        ln = ln + 1
+        pos = positions(true_len)
+        qr = fa.paged_append(s.kc, s.vc, table, ln, k, v, q=q, positions=pos, inv_freq=s.w, axes=s.axes, scores=s.sc)
+        before = s.sc.clone()
+        o, lse = fa.paged_decode(qr, s.kc, s.vc, table, ln, scores=s.sc)
+        ok()
+        assert_decoded(o, lse, qr, s.kc, s.vc, table, ln, d ** -0.5, 0, s.sc, before, "step")
+        # The step from the unturned rows, in 64 bits throughout: the newest
+        # key's score against the query, both turned by the same angles, is
+        # that of the unturned rows up to their roundings.
+        rq, rk = f64(qr), f64(s.kc)
+        for b in range(B):
+            n = int(ln[b])
+            kn = rk[table[b, (n - 1) // page].item(), :, (n - 1) % page]
+            for h in range(Hq):
+                a, r = f64(q[b, h]), f64(k[b, h // (Hq // Hkv)])
+                plain, turned = float(a @ r), float(rq[b, h] @ kn[h // (Hq // Hkv)])
+                assert abs(plain - turned) <= (2 * U[dt] + 1e-5) * 2 * np.linalg.norm(a) * np.linalg.norm(r)
+            true_len[b] += 1
+            w = paged.decode(rq[b:b + 1], rk, f64(s.vc), table[b:b + 1].cpu().numpy(), [n], d ** -0.5)[2][0]
+            acc[b] = np.concatenate([acc[b], np.zeros((Hkv, 1))], axis=1) + w
+
+    def check_scores():
+        for b in range(B):
+            n = int(ln[b])
+            got = paged.gather(f64(s.sc), table[b].cpu().numpy(), n)
+            assert np.abs(got - acc[b]).max() <= 1e-3 * max(1.0, acc[b].max())
+
+    for _ in range(4):
+        step()
+    check_scores()
+    # Evict into fresh pages; the kept keys by the oracle from the scores.
+    new_table = torch.zeros((B, 6), dtype=torch.int32)
+    for b in range(B):
+        new_table[b] = torch.tensor(s.pages(6))
+    new_table = new_table.to(DEV)
+    rows = [paged.gather(f64(s.sc), table[b].cpu().numpy(), int(ln[b])) for b in range(B)]
+    kv_before = [(paged.gather(f64(s.kc), table[b].cpu().numpy(), int(ln[b])),
+                  paged.gather(f64(s.vc), table[b].cpu().numpy(), int(ln[b]))) for b in range(B)]
+    new, kept = fa.paged_evict(s.kc, s.vc, s.sc, table, ln, new_table[:, :3], s.budget, recent=8, sinks=2)
+    ok()
+    table = new_table
+    for b in range(B):
+        m = int(new[b])
+        assert m == min(int(ln[b]), s.budget)
+        k2, v2 = (paged.gather(f64(x), table[b].cpu().numpy(), m) for x in (s.kc, s.vc))
+        old = acc[b]
+        acc[b] = np.zeros((Hkv, m))
+        for h in range(Hkv):
+            want = paged.kept_keys(rows[b][h].tolist(), s.budget, 8, 2)
+            assert kept[b, h, :m].tolist() == want
+            assert np.array_equal(k2[h], kv_before[b][0][h][want]) and np.array_equal(v2[h], kv_before[b][1][h][want])
+            acc[b][h] = old[h][want]
+    ln = new
+    for _ in range(3):
+        step()
+    check_scores()
+
+
+def one_step(dt=BF, B=4, lens=(100, 0, 37, 512)):
+    """Inputs of a decoding step and a function that makes it."""
+    k, v, table, ln = filled(list(lens), 2, 16, 128, dt, seed=51)
+    g = torch.Generator().manual_seed(52)
+    x = torch.randn((B, 12, 128), generator=g).to(dt).to(DEV)
+    w, axes = fa.rope_frequencies((64,), device=DEV)
+    pos = (ln - 1).clamp(min=0)[None].contiguous()
+    scores = torch.zeros(k.shape[:3], device=DEV)
+    q, kn, vn = x.split([8, 2, 2], dim=1)
+
+    def step(stream=None):
+        qr = fa.paged_append(k, v, table, ln, kn, vn, q=q, positions=pos, inv_freq=w, axes=axes, scores=scores,
+                             stream=stream)
+        o, lse = fa.paged_decode(qr, k, v, table, ln, scores=scores, stream=stream)
+        return o, lse
+    return step, x, scores
+
+
+def test_step_in_a_captured_graph(cuda_lib):
+    step, x, scores = one_step()
+    o, lse = step()
+    ok()
+    after_one = scores.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                                        # warm-up outside the capture
+    torch.cuda.current_stream().wait_stream(side)
+    graph, graph2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go, gl = step()
+    with torch.cuda.graph(graph2):
+        go2, gl2 = step()
+    rows = torch.tensor([0, 2, 3], device=DEV)        # sequence 1 is padding: its q row is not written
+    for gr, a, l in ((graph, go, gl), (graph2, go2, gl2), (graph, go, gl)):
+        a.zero_()
+        scores.zero_()
+        gr.replay()
+        ok()
+        assert torch.equal(a[rows], o[rows]) and torch.equal(l, lse)
+        assert torch.equal(scores, after_one)
+    # New inputs in the same buffers.
+    x.mul_(0.5)
+    graph.replay()
+    ok()
+    a, l = go.clone(), gl.clone()
+    o3, l3 = step()
+    ok()
+    assert torch.equal(a[rows], o3[rows]) and torch.equal(l, l3)
+
+
+def test_steps_on_two_streams(cuda_lib):
+    # Two independent steps in flight at once, on streams that are not the
+    # current one, many times over.
+    a, b = one_step(), one_step(dt=HF, lens=(700, 64, 0, 9))
+    want = [s[0]() for s in (a, b)]
+    ok()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate((a, b)):
+            got[i].append(s[0](stream=streams[i]))
+    ok()
+    skip = [1, 2]
+    for i in range(2):
+        rows = torch.tensor([r for r in range(4) if r != skip[i]], device=DEV)
+        for o, l in got[i]:
+            assert torch.equal(o[rows], want[i][0][rows]) and torch.equal(l, want[i][1])
+
+
+def test_binding_refusals(cuda_lib):
+    k, v, table, ln = filled([20], 2, 16, 64, BF, seed=61)
+    q = torch.zeros((1, 4, 64), dtype=BF, device=DEV)
+    with pytest.raises(TypeError):
+        fa.paged_decode(q.half(), k, v, table, ln)
+    with pytest.raises(TypeError):
+        fa.paged_decode(q, k, v, table.long(), ln)
+    with pytest.raises(ValueError):
+        fa.paged_decode(q, k, v, table, ln.expand(2))
+    with pytest.raises(ValueError):
+        fa.paged_decode(q, k, v.transpose(1, 2).contiguous().transpose(1, 2), table, ln)
+    with pytest.raises(ValueError):
+        fa.paged_decode(q, k, v, table, ln, scores=torch.zeros(k.shape[:2], device=DEV))
+    with pytest.raises(fa.FAError):
+        fa.paged_decode(q[:, :3], k, v, table, ln)                     # 3 query heads, 2 kv heads
+    with pytest.raises(fa.FAError):
+        fa.paged_decode(q, k, v, table, ln, window=-1)
+    with pytest.raises(fa.FAError):
+        fa.paged_decode(q, k, v, table, ln, out=q)
+    with pytest.raises(ValueError):
+        fa.paged_append(k, v, table, ln, q[:, :2].expand(3, 2, 64), q[:, :2].expand(3, 2, 64))
+    with pytest.raises(ValueError):
+        fa.paged_evict(k, v, torch.zeros(k.shape[:3], device=DEV), table, ln, table[:, :1], 0)
+    with pytest.raises(fa.FAError):
+        fa.paged_evict(k, v, torch.zeros(k.shape[:3], device=DEV), table, ln, table, 10)
+    ok()
