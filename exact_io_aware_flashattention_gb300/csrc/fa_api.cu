@@ -874,6 +874,39 @@ fa::PagedKv kv_args(const fa_paged_kv* kv) {
 
 fa::PageTable table_args(const fa_page_table* t) { return fa::PageTable{t->pages, t->stride, t->max_pages}; }
 
+// K or V pool as {d, page_size, Hkv, num_pages} with a 16-slot box.  The
+// stride of a dimension of size 1 is never stepped: any valid value does.
+fa_status tmap_pool(fa::TmaMap4* m, const fa_paged_kv* kv, const void* base) {
+  auto bytes = [&](long long size, long long stride) { return (cuuint64_t)(size > 1 ? stride : kv->d) * 2; };
+  cuuint64_t dims[4] = {(cuuint64_t)kv->d, (cuuint64_t)kv->page_size, (cuuint64_t)kv->Hkv, (cuuint64_t)kv->num_pages};
+  cuuint64_t strides[3] = {bytes(kv->page_size, kv->slot_stride), bytes(kv->Hkv, kv->head_stride),
+                           bytes(kv->num_pages, kv->page_stride)};
+  cuuint32_t box[4] = {64, 16, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(&m->m, kv->dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                              4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_LAUNCH;
+}
+
+// Decode workspace: tiles before each sequence, the parts of cut units with
+// their (max, sum), and, with scores, the LSE and every key's scores.
+struct DecodeWs {
+  size_t prefix, part, ml, lse2, stash, total;
+};
+DecodeWs decode_ws(int B, int Hq, int d, int page_size, int max_pages, bool with_scores) {
+  DecodeWs w{};
+  const size_t slots = (size_t)fa::kDecodeMaxParts * 2 * 16;
+  w.prefix = 0;
+  w.part = align256((size_t)(B + 1) * 8);
+  w.ml = w.part + slots * d * 4;
+  w.lse2 = w.ml + slots * 8;
+  w.stash = w.lse2 + (with_scores ? align256((size_t)B * Hq * 4) : 0);
+  w.total = w.stash + (with_scores ? align256((size_t)B * Hq * page_size * max_pages * 4) : 0);
+  return w;
+}
+
 // Each output apart from every input and every other output.
 template <size_t NO, size_t NI>
 bool outputs_apart(const View (&outs)[NO], const View (&ins)[NI]) {
@@ -1007,8 +1040,7 @@ size_t fa_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d, int page_s
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (d != 64 && d != 128) || page_size < 16 || page_size > 65536 ||
       page_size % 16 || max_pages < 1 || (long long)B * Hq >= (1LL << 31))
     return 0;
-  (void)with_scores;
-  return 256;
+  return decode_ws(B, Hq, d, page_size, max_pages, with_scores != 0).total;
 }
 
 fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_paged_kv* kv, const fa_page_table* table,
@@ -1050,8 +1082,25 @@ fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_pa
   a.Hq = Hq;
   a.window = window;
   a.scale_log2 = scale * 1.4426950408889634f;
-  return launch_status(
-      fa::launch_paged_decode(kv->dtype, a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
+  const int G = Hq / kv->Hkv;
+  a.unit_heads = G <= 8 ? 8 : 16;
+  const DecodeWs w = decode_ws(B, Hq, kv->d, kv->page_size, table->max_pages, scores != nullptr);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.prefix = reinterpret_cast<long long*>(ws + w.prefix);
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.lse2 = scores ? reinterpret_cast<float*>(ws + w.lse2) : nullptr;
+  a.stash = scores ? reinterpret_cast<float*>(ws + w.stash) : nullptr;
+  a.stash_keys = (long long)kv->page_size * table->max_pages;
+  // Two CTAs per SM, but no more than there can be tiles.
+  const long long columns = (long long)kv->Hkv * ((G + a.unit_heads - 1) / a.unit_heads);
+  const long long tiles = (long long)B * columns * ((a.stash_keys + 63) / 64);
+  const int parts = (int)std::min<long long>(tiles, std::min(2 * ds->num_sms, fa::kDecodeMaxParts));
+  fa::TmaMap4 tk, tv;
+  FA_TRY(tmap_pool(&tk, kv, kv->k));
+  FA_TRY(tmap_pool(&tv, kv, kv->v));
+  return launch_status(fa::launch_paged_decode(kv->dtype, tk, tv, a, dev_status(ds), parts, ds->num_sms,
+                                               static_cast<cudaStream_t>(stream)));
 }
 
 fa_status fa_paged_evict(const fa_paged_kv* kv, float* scores, const fa_page_table* table, const int* seq_lens,

@@ -144,9 +144,21 @@ struct DecodeArgs {
   float* scores;             // [num_pages, Hkv, page_size] or NULL
   int B, Hq, window;
   float scale_log2;
+  int unit_heads;            // query heads of a kv group that share a unit: 8 or 16
+  // Workspace
+  long long* prefix;         // [B + 1] 64-key tiles of the sequences before b
+  float* part;               // [kDecodeMaxParts][2][16][d] unnormalised O of units cut over CTAs
+  float2* part_ml;           // [kDecodeMaxParts][2][16] their maximum (log2 units) and sum
+  float* lse2;               // [B, Hq] log-sum-exp in log2 units (with scores)
+  float* stash;              // [B, Hkv, stash_keys, G] scores in log2 units (with scores)
+  long long stash_keys;
 };
 
-cudaError_t launch_paged_decode(int dtype, const DecodeArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream);
+constexpr int kDecodeMaxParts = 320;   // CTAs of the decode kernel at most
+
+// `tk`, `tv` view the pools as {d, page_size, Hkv, num_pages}; `parts` CTAs.
+cudaError_t launch_paged_decode(int dtype, const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs& a, const DevStatus& st,
+                                int parts, int num_sms, cudaStream_t stream);
 
 struct EvictArgs {
   PagedKv kv;
@@ -166,11 +178,13 @@ cudaError_t launch_paged_evict(const EvictArgs& a, const DevStatus& st, int num_
 cudaError_t configure_fwd_kernels();
 cudaError_t configure_bwd_kernels();
 cudaError_t configure_dq_kernels();
+cudaError_t configure_paged_kernels();
 
 inline cudaError_t configure_kernels() {
   cudaError_t e = configure_fwd_kernels();
   if (e == cudaSuccess) e = configure_bwd_kernels();
   if (e == cudaSuccess) e = configure_dq_kernels();
+  if (e == cudaSuccess) e = configure_paged_kernels();
   return e;
 }
 
