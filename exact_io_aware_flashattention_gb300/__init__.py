@@ -22,9 +22,11 @@ raises ``FAError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
+import struct
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "_lib", "libfa_gb300.so")
@@ -240,7 +242,7 @@ def fa_paged_append(kv, table, seq_lens, cu_seqlens, B, T, k, k_strides, v, v_st
 def fa_paged_decode(q, q_strides, kv, table, seq_lens, o, lse, scores, B, Hq, window, scale, workspace,
                     workspace_bytes, stream):
     return load_library().fa_paged_decode(q, q_strides, _ref(kv), _ref(table), seq_lens, o, lse, scores, B, Hq, window,
-                                          scale, workspace, workspace_bytes, stream)
+                                          float(scale), workspace, workspace_bytes, stream)
 
 
 def fa_paged_decode_workspace_bytes(B, Hq, Hkv, d, page_size, max_pages, with_scores):
@@ -374,92 +376,98 @@ def check_device_status(stream=None):
 
 # ---------------------------------------------------------------------------
 # Rotary positions and the paged key / value cache
+#
+# A decoding step makes these calls for every layer on tensors of a few KB, so
+# their time is the binding's: the checks of a valid argument are one
+# expression (the message is found out afterwards), structs and stride arrays
+# are packed bytes, and the stream comes as a raw handle.
 # ---------------------------------------------------------------------------
 
-class _Call:
-    """The device of a call's tensors and the stream it runs on.
-
-    The kernels run on the tensors' device, whichever device is current, and on
-    its current stream unless ``stream`` is given; what the call allocates
-    belongs to that stream, so the caching allocator does not hand a workspace
-    on to another stream while the kernels still use it."""
-
-    def __init__(self, t, stream):
-        import torch
-        self.device = t.device
-        self.enter = []
-        if t.device.index != torch.cuda.current_device():
-            self.enter.append(torch.cuda.device(t.device))
-        if stream is not None:
-            if stream.device != t.device:
-                raise ValueError(f"stream of {stream.device}, tensors on {t.device}")
-            self.enter.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        import torch
-        for x in self.enter:
-            x.__enter__()
-        self.handle = torch.cuda.current_stream(self.device).cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        for x in reversed(self.enter):
-            x.__exit__(*exc)
+_pack_rotary = struct.Struct("@PqqPPiii4x").pack          # fa_rotary
+_pack_kv = struct.Struct("@PPqqqiiiii4x").pack            # fa_paged_kv
+_pack_table = struct.Struct("@Pqi4x").pack                # fa_page_table
+_pack2 = struct.Struct("@qq").pack
+_pack3 = struct.Struct("@qqq").pack
 
 
-def _dtype_code(t, name):
-    import torch
-    if t.dtype == torch.bfloat16:
-        return FA_BF16
-    if t.dtype == torch.float16:
-        return FA_FP16
-    raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
-
-
-def _check_view(t, name, shape, dtype, device):
-    """A CUDA tensor of this shape whose last dimension is contiguous; returns its address."""
+def _check_view(t, name, shape, dtype, dev):
+    """Address of a tensor of this shape on CUDA device ``dev``, contiguous in its last dimension."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.stride()[-1] == 1:
+            return t.data_ptr()
+    except (AttributeError, IndexError):
+        pass
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.dim() and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     return t.data_ptr()
 
 
-def _check_dense(t, name, shape, dtype, device):
-    p = _check_view(t, name, shape, dtype, device)
+def _check_dense(t, name, shape, dtype, dev):
+    p = _check_view(t, name, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return p
 
 
-def _strides(t):
-    """Strides of all dimensions but the last, as a C array."""
-    s = t.stride()[:-1]
-    return (_ll * len(s))(*s)
+def _first(t, name, dims, what):
+    """(shape, CUDA device index, dtype code) of a call's first tensor."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be a {what} tensor, got shape {tuple(t.shape)}")
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        code = FA_BF16
+    elif dt is torch.float16:
+        code = FA_FP16
+    else:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {dt}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    return t.shape, t.get_device(), code
 
 
-def _rotary(positions, inv_freq, axes, interleaved, d, lead, device):
+def _on(dev, stream, call):
+    """``call(raw stream handle)`` with device ``dev`` current, on its current
+    stream or on ``stream``.  What the call allocates belongs to that stream, so
+    that the caching allocator does not hand a workspace on to another stream
+    while the kernels still use it."""
+    import torch
+    if stream is None and dev == torch._C._cuda_getDevice():
+        return call(torch._C._cuda_getCurrentRawStream(dev))
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device}, tensors on cuda:{dev}")
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call(torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _rotary(positions, inv_freq, axes, interleaved, d, lead, dev):
     """fa_rotary of positions [n_axes, *lead] int32, inv_freq [rot/2] float64, axes [rot/2] int32."""
     import torch
-    if positions is None or inv_freq is None or axes is None:
-        raise ValueError("rotary positions need positions, inv_freq and axes")
-    if positions.dim() != len(lead) + 1:
-        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected (axes, *{tuple(lead)})")
-    pos = _check_view(positions, "positions", (positions.shape[0], *lead), torch.int32, device)
-    n = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
+    if not all(isinstance(t, torch.Tensor) for t in (positions, inv_freq, axes)):
+        raise ValueError("rotary positions need positions, inv_freq and axes as tensors")
+    n_axes = positions.shape[0] if positions.dim() else 0
+    pos = _check_view(positions, "positions", (n_axes, *lead), torch.int32, dev)
+    n = inv_freq.numel()
     if n < 1 or 2 * n > d:
-        raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected 1 to {d // 2} frequencies")
-    w = _check_dense(inv_freq, "inv_freq", (n,), torch.float64, device)
-    ax = _check_dense(axes, "axes", (n,), torch.int32, device)
-    return fa_rotary(pos, positions.stride(0), positions.stride(1) if len(lead) == 2 else 0, w, ax, positions.shape[0],
-                     2 * n, int(interleaved))
+        raise ValueError(f"inv_freq has {n} frequencies, expected 1 to {d // 2}")
+    w = _check_dense(inv_freq, "inv_freq", (n,), torch.float64, dev)
+    ax = _check_dense(axes, "axes", (n,), torch.int32, dev)
+    st = positions.stride()
+    return _pack_rotary(pos, st[0], st[1] if len(lead) == 2 else 0, w, ax, n_axes, 2 * n, 1 if interleaved else 0)
 
 
 def rope_frequencies(sections, base: float = 10000.0, device="cuda"):
@@ -478,32 +486,34 @@ def rope_frequencies(sections, base: float = 10000.0, device="cuda"):
 
 def _rope(q, k, positions, inv_freq, axes, interleaved, inverse, q_out, k_out, stream):
     import torch
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a [B, H, N, d] tensor")
-    B, Hq, N, d = q.shape
-    dev, code = q.device, _dtype_code(q, "q")
-    qp = _check_view(q, "q", q.shape, q.dtype, dev)
+    (B, Hq, N, d), dev, code = _first(q, "q", 4, "[B, Hq, N, d]")
+    dt = q.dtype
+    qp = _check_view(q, "q", q.shape, dt, dev)
     Hk, kp, ks = 0, None, None
     if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != 4:
-            raise ValueError("k must be a [B, H, N, d] tensor")
-        Hk = k.shape[1]
-        kp, ks = _check_view(k, "k", (B, Hk, N, d), q.dtype, dev), _strides(k)
+        Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+        kp = _check_view(k, "k", (B, Hk, N, d), dt, dev)
+        ks = _pack3(*k.stride()[:3])
     elif k_out is not None:
         raise ValueError("k_out without k")
     rot = _rotary(positions, inv_freq, axes, interleaved, d, (B, N), dev)
-    with _Call(q, stream) as call:
-        if q_out is None:
-            q_out = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev)
-        op = _check_view(q_out, "q_out", (B, Hq, N, d), q.dtype, dev)
+
+    def call(handle):
+        qo, ko = q_out, k_out
+        if qo is None:
+            qo = torch.empty((B, Hq, N, d), dtype=dt, device=q.device)
+        op = _check_view(qo, "q_out", (B, Hq, N, d), dt, dev)
         okp, oks = None, None
         if k is not None:
-            if k_out is None:
-                k_out = torch.empty((B, Hk, N, d), dtype=q.dtype, device=dev)
-            okp, oks = _check_view(k_out, "k_out", (B, Hk, N, d), q.dtype, dev), _strides(k_out)
-        _raise(fa_rope(qp, _strides(q), op, _strides(q_out), kp, ks, okp, oks, B, Hq, Hk, N, d, code, rot, inverse,
-                       call.handle), "fa_rope")
-    return (q_out, k_out) if k is not None else q_out
+            if ko is None:
+                ko = torch.empty((B, Hk, N, d), dtype=dt, device=q.device)
+            okp, oks = _check_view(ko, "k_out", (B, Hk, N, d), dt, dev), _pack3(*ko.stride()[:3])
+        status = fa_rope(qp, _pack3(*q.stride()[:3]), op, _pack3(*qo.stride()[:3]), kp, ks, okp, oks, B, Hq, Hk, N, d, code,
+                         rot, inverse, handle)
+        if status:
+            _raise(status, "fa_rope")
+        return qo if k is None else (qo, ko)
+    return _on(dev, stream, call)
 
 
 def rope(q, k, positions, inv_freq, axes, interleaved: bool = False, q_out=None, k_out=None, stream=None):
@@ -513,41 +523,34 @@ def rope(q, k, positions, inv_freq, axes, interleaved: bool = False, q_out=None,
     int32 [n_axes, B, N] (expand over B to share them); inv_freq (float64) and
     axes (int32) come from ``rope_frequencies`` or the caller.  Outputs may be the
     inputs themselves.  Returns (q_out, k_out), or q_out without k."""
-    return _rope(q, k, positions, inv_freq, axes, interleaved, False, q_out, k_out, stream)
+    return _rope(q, k, positions, inv_freq, axes, interleaved, 0, q_out, k_out, stream)
 
 
 def rope_backward(dq, dk, positions, inv_freq, axes, interleaved: bool = False, dq_out=None, dk_out=None, stream=None):
     """Gradients of ``rope``'s inputs from those of its outputs: the opposite turn."""
-    return _rope(dq, dk, positions, inv_freq, axes, interleaved, True, dq_out, dk_out, stream)
+    return _rope(dq, dk, positions, inv_freq, axes, interleaved, 1, dq_out, dk_out, stream)
 
 
 def _paged(k_cache, v_cache, block_table, seq_lens):
-    """(fa_paged_kv, fa_page_table, B) of checked cache tensors."""
+    """Checked cache tensors: (shape, device index, dtype, fa_paged_kv, fa_page_table, B, seq_lens address)."""
     import torch
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        raise ValueError("k_cache must be a [pages, Hkv, page_size, d] tensor")
-    dev = k_cache.device
-    P, Hkv, ps, d = k_cache.shape
-    kp = _check_view(k_cache, "k_cache", k_cache.shape, k_cache.dtype, dev)
-    vp = _check_view(v_cache, "v_cache", k_cache.shape, k_cache.dtype, dev)
+    shape, dev, code = _first(k_cache, "k_cache", 4, "[pages, Hkv, page_size, d]")
+    dt = k_cache.dtype
+    kp = _check_view(k_cache, "k_cache", shape, dt, dev)
+    vp = _check_view(v_cache, "v_cache", shape, dt, dev)
     st = k_cache.stride()
     if v_cache.stride() != st:
         raise ValueError("k_cache and v_cache must have the same strides")
-    kv = fa_paged_kv(kp, vp, st[0], st[1], st[2], P, ps, Hkv, d, _dtype_code(k_cache, "k_cache"))
+    P, Hkv, ps, d = shape
     table, B = _table(block_table, "block_table", dev)
-    return kv, table, B, _check_dense(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    return (shape, dev, dt, _pack_kv(kp, vp, st[0], st[1], st[2], P, ps, Hkv, d, code), table, B,
+            _check_dense(seq_lens, "seq_lens", (B,), torch.int32, dev))
 
 
 def _table(t, name, dev):
     import torch
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name} must be a [B, pages] tensor")
-    return fa_page_table(_check_view(t, name, t.shape, torch.int32, dev), t.stride(0), t.shape[1]), t.shape[0]
-
-
-def _scores(scores, k_cache):
-    import torch
-    return _check_dense(scores, "scores", k_cache.shape[:3], torch.float32, k_cache.device)
+    shape = t.shape if isinstance(t, torch.Tensor) and t.dim() == 2 else ("B", "pages")
+    return _pack_table(_check_view(t, name, shape, torch.int32, dev), t.stride()[0], shape[1]), shape[0]
 
 
 def paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens=None, q=None, positions=None, inv_freq=None,
@@ -559,48 +562,56 @@ def paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens=None,
     int32) tokens cu[b]..cu[b+1]-1 are sequence b's last ones and tokens from
     cu[B] on are padding.  With ``positions`` [n_axes,T], ``inv_freq`` and
     ``axes`` k is stored turned, and q [T,Hq,d], if given, is returned turned
-    (into ``q_out``, which may be q).  ``scores`` [pages,Hkv,page_size] fp32 gets
-    0 for the new tokens.  See fa_paged_append."""
+    (into ``q_out``, which may be q); rows of padding tokens are not written.
+    ``scores`` [pages,Hkv,page_size] fp32 gets 0 for the new tokens.  See
+    fa_paged_append."""
     import torch
-    kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
-    dev, dt, Hkv, d = k_cache.device, k_cache.dtype, kv.Hkv, kv.d
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("k must be a [T, Hkv, d] tensor")
-    T = k.shape[0]
-    kp, vp = _check_view(k, "k", (T, Hkv, d), dt, dev), _check_view(v, "v", (T, Hkv, d), dt, dev)
-    if cu_seqlens is None and T != B:
-        raise ValueError(f"{T} tokens for {B} sequences without cu_seqlens")
-    cu = None if cu_seqlens is None else _check_dense(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
+    (_, Hkv, _, d), dev, dt, kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
+    T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+    kp = _check_view(k, "k", (T, Hkv, d), dt, dev)
+    vp = _check_view(v, "v", (T, Hkv, d), dt, dev)
+    if cu_seqlens is None:
+        cu = None
+        if T != B:
+            raise ValueError(f"{T} tokens for {B} sequences without cu_seqlens")
+    else:
+        cu = _check_dense(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
     rot = None
     if positions is not None or inv_freq is not None or axes is not None:
         rot = _rotary(positions, inv_freq, axes, interleaved, d, (T,), dev)
-    sp = None if scores is None else _scores(scores, k_cache)
+    sp = None if scores is None else _check_dense(scores, "scores", k_cache.shape[:3], torch.float32, dev)
     qp, qs, Hq = None, None, 0
     if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
-            raise ValueError("q must be a [T, Hq, d] tensor")
-        Hq = q.shape[1]
-        qp, qs = _check_view(q, "q", (T, Hq, d), dt, dev), _strides(q)
+        Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+        qp = _check_view(q, "q", (T, Hq, d), dt, dev)
+        qs = _pack2(*q.stride()[:2])
     elif q_out is not None:
         raise ValueError("q_out without q")
-    with _Call(k_cache, stream) as call:
-        op, os_ = None, None
+
+    def call(handle):
+        qo, op, os_ = q_out, None, None
         if q is not None:
-            if q_out is None:
-                q_out = torch.empty((T, Hq, d), dtype=dt, device=dev)
-            op, os_ = _check_view(q_out, "q_out", (T, Hq, d), dt, dev), _strides(q_out)
-        if T == 0:
-            return q_out
-        _raise(fa_paged_append(kv, table, lens, cu, B, T, kp, _strides(k), vp, _strides(v), qp, qs, op, os_, Hq, rot, sp,
-                               call.handle), "fa_paged_append")
-    return q_out
+            if qo is None:
+                qo = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+            op, os_ = _check_view(qo, "q_out", (T, Hq, d), dt, dev), _pack2(*qo.stride()[:2])
+        if T:
+            status = fa_paged_append(kv, table, lens, cu, B, T, kp, _pack2(*k.stride()[:2]), vp, _pack2(*v.stride()[:2]), qp,
+                                     qs, op, os_, Hq, rot, sp, handle)
+            if status:
+                _raise(status, "fa_paged_append")
+        return qo
+    return _on(dev, stream, call)
+
+
+# A size is a pure function of the shapes; a decoding loop asks for the same one every step.
+_decode_ws_bytes = functools.lru_cache(maxsize=256)(
+    lambda *shape: fa_paged_decode_workspace_bytes(*shape))
 
 
 def paged_decode_workspace(B, Hq, k_cache, block_table, with_scores: bool = False):
     """Workspace of paged_decode, for callers that keep one (one for each call that may run at the same time)."""
     import torch
-    n = fa_paged_decode_workspace_bytes(B, Hq, k_cache.shape[1], k_cache.shape[3], k_cache.shape[2],
-                                        block_table.shape[1], with_scores)
+    n = _decode_ws_bytes(B, Hq, k_cache.shape[1], k_cache.shape[3], k_cache.shape[2], block_table.shape[1], bool(with_scores))
     if n == 0:
         raise FAError(FA_ERR_BAD_SHAPE, "fa_paged_decode_workspace_bytes")
     return torch.empty(n, dtype=torch.uint8, device=k_cache.device)
@@ -614,28 +625,30 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float | None
     key by its softmax weight summed over the group's heads.  See
     fa_paged_decode."""
     import torch
-    kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
-    dev, dt, d = k_cache.device, k_cache.dtype, kv.d
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [B, Hq, d] tensor")
-    Hq = q.shape[1]
+    (_, _, _, d), dev, dt, kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
+    Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
     qp = _check_view(q, "q", (B, Hq, d), dt, dev)
-    sp = None if scores is None else _scores(scores, k_cache)
+    sp = None if scores is None else _check_dense(scores, "scores", k_cache.shape[:3], torch.float32, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _Call(k_cache, stream) as call:
-        if out is None:
-            out = torch.empty((B, Hq, d), dtype=dt, device=dev)
-        if lse is None:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-        op = _check_dense(out, "out", (B, Hq, d), dt, dev)
-        lp = _check_dense(lse, "lse", (B, Hq), torch.float32, dev)
-        if workspace is None:
-            workspace = paged_decode_workspace(B, Hq, k_cache, block_table, scores is not None)
-        wp = _check_dense(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
-        _raise(fa_paged_decode(qp, _strides(q), kv, table, lens, op, lp, sp, B, Hq, window, float(scale), wp,
-                               workspace.numel(), call.handle), "fa_paged_decode")
-    return out, lse
+
+    def call(handle):
+        o, l, ws = out, lse, workspace
+        if o is None:
+            o = torch.empty((B, Hq, d), dtype=dt, device=k_cache.device)
+        if l is None:
+            l = torch.empty((B, Hq), dtype=torch.float32, device=k_cache.device)
+        if ws is None:
+            ws = paged_decode_workspace(B, Hq, k_cache, block_table, scores is not None)
+        op = _check_dense(o, "out", (B, Hq, d), dt, dev)
+        lp = _check_dense(l, "lse", (B, Hq), torch.float32, dev)
+        n = ws.numel()
+        status = fa_paged_decode(qp, _pack2(*q.stride()[:2]), kv, table, lens, op, lp, sp, B, Hq, window, scale,
+                                 _check_dense(ws, "workspace", (n,), torch.uint8, dev), n, handle)
+        if status:
+            _raise(status, "fa_paged_decode")
+        return o, l
+    return _on(dev, stream, call)
 
 
 def paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budget: int, recent: int = 0, sinks: int = 0,
@@ -647,20 +660,24 @@ def paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budg
     those in use.  Returns (new_lens [B], kept [B,Hkv,budget]: the indices kept,
     -1 past the new length).  See fa_paged_evict."""
     import torch
-    kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
-    dev = k_cache.device
-    sp = _scores(scores, k_cache)
-    dst, Bd = _table(dst_table, "dst_table", dev)
-    if Bd != B:
-        raise ValueError(f"dst_table has {Bd} rows, expected {B}")
+    (_, Hkv, _, _), dev, _, kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
+    sp = _check_dense(scores, "scores", k_cache.shape[:3], torch.float32, dev)
+    dst, rows = _table(dst_table, "dst_table", dev)
+    if rows != B:
+        raise ValueError(f"dst_table has {rows} rows, expected {B}")
     if budget < 1:
         raise ValueError("budget must be at least 1")
-    with _Call(k_cache, stream) as call:
-        if new_lens is None:
-            new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
-        if kept is None:
-            kept = torch.empty((B, kv.Hkv, budget), dtype=torch.int32, device=dev)
-        np_ = _check_dense(new_lens, "new_lens", (B,), torch.int32, dev)
-        ep = _check_dense(kept, "kept", (B, kv.Hkv, budget), torch.int32, dev)
-        _raise(fa_paged_evict(kv, sp, table, lens, dst, np_, ep, B, budget, recent, sinks, call.handle), "fa_paged_evict")
-    return new_lens, kept
+
+    def call(handle):
+        n, idx = new_lens, kept
+        if n is None:
+            n = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
+        if idx is None:
+            idx = torch.empty((B, Hkv, budget), dtype=torch.int32, device=k_cache.device)
+        np_ = _check_dense(n, "new_lens", (B,), torch.int32, dev)
+        ip = _check_dense(idx, "kept", (B, Hkv, budget), torch.int32, dev)
+        status = fa_paged_evict(kv, sp, table, lens, dst, np_, ip, B, budget, recent, sinks, handle)
+        if status:
+            _raise(status, "fa_paged_evict")
+        return n, idx
+    return _on(dev, stream, call)

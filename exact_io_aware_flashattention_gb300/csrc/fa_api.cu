@@ -1109,7 +1109,10 @@ fa_status fa_paged_evict(const fa_paged_kv* kv, float* scores, const fa_page_tab
   NvtxRange nv("fa_paged_evict");
   FA_TRY(check_kv(kv));
   if (!scores || !seq_lens || !new_lens || !kept) return FA_ERR_NULL_PTR;
-  if (B < 1 || (long long)B * kv->Hkv >= (1LL << 31)) return FA_ERR_BAD_SHAPE;
+  // Grids: up to 8 CTAs, and a block per 64 kept keys, for each (sequence, kv head).
+  if (B < 1 || (long long)B * kv->Hkv >= (1LL << 27) ||
+      (long long)B * kv->Hkv * (((long long)budget + 63) / 64) >= (1LL << 31))
+    return FA_ERR_BAD_SHAPE;
   FA_TRY(check_table(table, B));
   FA_TRY(check_table(dst, B));
   if (budget < 1 || recent < 0 || sinks < 0 || (long long)recent + sinks > budget ||

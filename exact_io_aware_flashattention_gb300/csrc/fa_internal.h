@@ -179,12 +179,14 @@ cudaError_t configure_fwd_kernels();
 cudaError_t configure_bwd_kernels();
 cudaError_t configure_dq_kernels();
 cudaError_t configure_paged_kernels();
+cudaError_t configure_evict_kernels();
 
 inline cudaError_t configure_kernels() {
   cudaError_t e = configure_fwd_kernels();
   if (e == cudaSuccess) e = configure_bwd_kernels();
   if (e == cudaSuccess) e = configure_dq_kernels();
   if (e == cudaSuccess) e = configure_paged_kernels();
+  if (e == cudaSuccess) e = configure_evict_kernels();
   return e;
 }
 
