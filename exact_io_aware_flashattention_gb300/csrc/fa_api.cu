@@ -1125,8 +1125,18 @@ fa_status fa_paged_evict(const fa_paged_kv* kv, float* scores, const fa_page_tab
   if (!outputs_apart(outs, ins) || dst->pages == table->pages) return FA_ERR_ALIASING;
   DeviceState* ds = nullptr;
   FA_TRY(device_state(&ds));
-  const fa::EvictArgs a{kv_args(kv), scores, table_args(table), table_args(dst), seq_lens, new_lens, kept, B, budget, recent,
-                        sinks};
+  fa::EvictArgs a{};
+  a.kv = kv_args(kv);
+  a.scores = scores;
+  a.table = table_args(table);
+  a.dst = table_args(dst);
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.kept = kept;
+  a.B = B;
+  a.budget = budget;
+  a.recent = recent;
+  a.sinks = sinks;
   return launch_status(fa::launch_paged_evict(a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -14,16 +14,19 @@
 //
 // fa_evict_select_kernel.  One cluster of 1, 2, 4 or 8 CTAs per (b, g), each
 // with an equal run of the keys, held in shared memory as order-preserving
-// integers.  The need-th largest is found 11, 11 and 10 bits at a time: every
-// CTA counts its keys that match the digits found so far into a histogram,
-// reads the others' histograms through distributed shared memory, and all
-// reach the same digit; three passes over shared memory replace a sort.  It
-// stops early when the digit's bin is wanted whole.  The kept indices then go
-// out in order by one block scan and the counts of the CTAs before.
+// integers (protected ones as the largest).  The need-th largest of the others
+// is found 11, 11 and 10 bits at a time: every CTA counts its keys that match
+// the digits found so far into a histogram, reads the others' histograms
+// through distributed shared memory, and all reach the same digit; three
+// passes over shared memory replace a sort.  It stops early when the digit's
+// bin is wanted whole.  The kept indices then go out in order: each warp
+// counts its run of keys by votes, sums the counts of the warps and CTAs before,
+// and writes.
 //
-// fa_evict_copy_kernel.  A warp takes 32 (or 8) consecutive kept keys: each
-// lane looks one up (index, source page, target page) and moves its score,
-// then the rows go 16 bytes a lane, eight loads in flight.
+// fa_evict_copy_kernel.  A warp takes 8 consecutive kept keys: eight lanes look
+// one up each (index, source page, target page) and move its score, then the
+// rows go 16 bytes a lane, all loads in flight before the first store.  (16 or
+// 32 keys a warp, in rounds of 8 or 4, fill the last wave worse: 2-5 % slower.)
 #include "fa_internal.h"
 #include "sm103a.cuh"
 
@@ -31,11 +34,12 @@ namespace fa {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;                 // of the selection
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxCached = 49 * kThreads;     // keys in shared memory: 196 KB with the histograms
+constexpr int kMaxCached = 49 * 1024;         // keys in shared memory: 196 KB with the histograms
+constexpr uint32_t kProtected = 0xffffffffu;  // above every score's key
 
 // Order-preserving map of scores to unsigned: larger score, larger key;
 // -0 counts as +0 and NaN as the smallest.
@@ -45,8 +49,11 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 __device__ __forceinline__ int ld_cluster(const int* p, int rank) {
   uint32_t a;
@@ -55,44 +62,51 @@ __device__ __forceinline__ int ld_cluster(const int* p, int rank) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ int2 ld_cluster2(const int* p, int rank) {
+  uint32_t a;
+  int2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// j / page_size by a multiplication: page_size = 16 q, and with s = ceil(log2 q),
+// page_mul = ceil(2^(27+s) / q) the product n page_mul / 2^(27+s) exceeds n / q
+// by less than n 2^-(27+s) < 1/q for n = j / 16 < 2^27.
+__device__ __forceinline__ int page_of(int j, const EvictArgs& a) {
+  return (int)(((uint64_t)((uint32_t)j >> 4) * a.page_mul) >> a.page_shift);
+}
+
 struct Select {
   int hist[3][kBins];
-  int warp_sums[kWarps];
-  int counts[2];          // this CTA's keys: above the threshold or protected, equal to it
+  int coarse[3][kBins / 32];          // sums of 32 bins
+  int above[kWarps], equal[kWarps];   // each warp's keys above the threshold, and equal to it
+  int2 counts;                        // the CTA's
   int bin, left, whole;
 };
 
-// Inclusive sum over the block; total to every thread.
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive sum over the warp.
+__device__ __forceinline__ int warp_scan(int x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += y;
   }
-  __syncthreads();                    // the last scan's sums have been read
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int s = warp_sums[lane];
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, s, d);
-    if (lane >= d) s += y;
-  }
-  total = __shfl_sync(0xffffffffu, s, 31);
-  const int before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
-  return x + (warp > 0 ? before : 0);
+  return x;
 }
 
-__global__ void __launch_bounds__(kThreads) fa_evict_select_kernel(const EvictArgs a, int cluster, int cap, const DevStatus st) {
+__global__ void __launch_bounds__(kThreads, 2)
+    fa_evict_select_kernel(const EvictArgs a, int cluster, int cap, const DevStatus st) {
   extern __shared__ __align__(16) uint8_t smem[];
   Select& sh = *reinterpret_cast<Select*>(smem);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + sizeof(Select));     // [cap]
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + (sizeof(Select) + 15) / 16 * 16);     // [cap]
   launch_dependents();
   const int unit = blockIdx.x / cluster, rank = blockIdx.x - unit * cluster;
   const int b = unit / a.kv.Hkv, g = unit - b * a.kv.Hkv;
-  const int ps = a.kv.page_size, tid = threadIdx.x;
+  const int ps = a.kv.page_size, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int len = a.seq_lens[b];
   if (len < 0 || len > (long long)a.table.cols * ps) {
     if (tid == 0) record_error(st, kErrBadIndex, kSiteEvictLen);
@@ -106,62 +120,139 @@ __global__ void __launch_bounds__(kThreads) fa_evict_select_kernel(const EvictAr
     for (int i = rank * kThreads + tid; i < m; i += cluster * kThreads) kept[i] = i;
     return;                            // the whole cluster does
   }
-  // Candidates are [lo, hi); the others are protected.
-  const int lo = a.sinks, hi = len - a.recent;
+  const int lo = a.sinks, hi = len - a.recent;     // keys outside [lo, hi) are protected
   int need = m - a.sinks - a.recent;
-  const int run = (len + cluster - 1) / cluster, j0 = min(len, rank * run), j1 = min(len, j0 + run);
+  // The CTA's run of keys: a multiple of 4, so that four consecutive keys, one
+  // 16-byte load, lie in one page (page sizes are multiples of 16).
+  const int run = ((len + cluster - 1) / cluster + 3) & ~3;
+  const int j0 = (int)min((long long)len, (long long)rank * run), n_run = min(len - j0, run);
   const bool cached = run <= cap;
   const int* pages = a.table.pages + b * a.table.stride;
-  auto key_at = [&](int j) -> uint32_t {
-    const int c = j / ps, p = pages[c];
-    if (p < 0 || p >= a.kv.num_pages) {
-      record_error(st, kErrBadIndex, kSiteEvictPage);
-      return 0u;
-    }
-    return score_key(a.scores[((long long)p * a.kv.Hkv + g) * ps + (j - c * ps)]);
-  };
-  // Keys [from, from + n) of the run into shared memory.
+  const float* pool = a.scores + (long long)g * ps;
+  const long long page_scores = (long long)a.kv.Hkv * ps;
+  // Keys [from, from + n) into shared memory, in fours; past the sequence's
+  // end 0, the smallest: equal keys go by index, so those never come before a
+  // key of the sequence.  n rounded up to 128 is filled.
   auto load = [&](int from, int n) {
-#pragma unroll 4
-    for (int i = tid; i < n; i += kThreads) keys[i] = key_at(from + i);
+    constexpr int kBatch = 4;          // page numbers, then scores, in flight per thread
+    const int quads = (n + 127) / 128 * 32;
+    for (int i0 = tid; i0 < quads; i0 += kBatch * kThreads) {
+      int p[kBatch], slot[kBatch];
+      float4 x[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int j = from + 4 * (i0 + u * kThreads);
+        const bool in = j < from + n;
+        const int c = in ? page_of(j, a) : 0;
+        p[u] = in ? pages[c] : 0;
+        slot[u] = in ? j - c * ps : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const bool ok = p[u] >= 0 && p[u] < a.kv.num_pages;
+        if (!ok) record_error(st, kErrBadIndex, kSiteEvictPage);
+        p[u] = ok ? p[u] : 0;          // any page: what such a sequence keeps is unspecified
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) x[u] = *reinterpret_cast<const float4*>(pool + p[u] * page_scores + slot[u]);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * kThreads, j = from + 4 * i;
+        if (i >= quads) break;
+        uint4 k = make_uint4(score_key(x[u].x), score_key(x[u].y), score_key(x[u].z), score_key(x[u].w));
+        if (j < lo || j + 4 > hi) {
+          uint32_t* y = &k.x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + e < lo || j + e >= hi) y[e] = j + e < len ? kProtected : 0u;
+        }
+        reinterpret_cast<uint4*>(keys)[i] = k;
+      }
+    }
+  };
+  // body(from, n) over the run in pieces that fit shared memory.
+  auto pieces = [&](auto body) {
+    for (int from = j0; from < j0 + n_run; from += cap) {
+      const int n = min(cap, j0 + n_run - from);
+      if (!cached) {
+        __syncthreads();
+        load(from, n);
+        __syncthreads();
+      }
+      body(from, n);
+    }
   };
   for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
-  if (cached) load(j0, j1 - j0);
+  if (cached) load(j0, n_run);
   __syncthreads();
 
-  uint32_t prefix = 0, mask = 0;
+  // Without a choice only the protected keys are above the threshold.
+  uint32_t prefix = need > 0 ? 0u : kProtected - 1, mask = need > 0 ? 0u : kProtected;
   if (need > 0)
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       int* hist = sh.hist[pass];
-      for (int i = tid; i < j1 - j0; i += kThreads) {
-        const int j = j0 + i;
-        if (j < lo || j >= hi) continue;
-        const uint32_t k = cached ? keys[i] : key_at(j);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+      pieces([&](int, int n) {
+        const int quads = (n + 3) / 4;
+#pragma unroll 2
+        for (int i = tid; i < quads; i += kThreads) {
+          const uint4 k = reinterpret_cast<const uint4*>(keys)[i];
+          auto count = [&](uint32_t x) {
+            if ((x & mask) == prefix && x != kProtected) atomicAdd(&hist[(x >> shift) & ((1u << bits) - 1)], 1);
+          };
+          count(k.x);
+          count(k.y);
+          count(k.z);
+          count(k.w);
+        }
+      });
+      __syncthreads();
+      // Sums of 32 bins, so that the others need to read 64 of them and then
+      // 32 bins, not all 2048.
+      for (int c = warp; c < kBins / 32; c += kWarps) {
+        const int sum = __reduce_add_sync(0xffffffffu, hist[c * 32 + lane]);
+        if (lane == 0) sh.coarse[pass][c] = sum;
       }
       if (cluster > 1) cluster_sync(); else __syncthreads();
-      // Two bins a thread, the largest first: where the running count reaches
-      // `need` is the digit.
-      const int top = kBins - 1 - 2 * tid;
-      int n0 = 0, n1 = 0;
-      if (cluster == 1) {
-        n0 = hist[top];
-        n1 = hist[top - 1];
-      } else {
-        for (int r = 0; r < cluster; ++r) {
-          n0 += ld_cluster(&hist[top], r);
-          n1 += ld_cluster(&hist[top - 1], r);
+      if (warp == 0) {
+        // Largest first: lane l has coarse bins 63 - 2l and 62 - 2l, then bin
+        // 31 - l of the coarse bin in which the running count reaches `need`.
+        int n0 = 0, n1 = 0;
+        if (cluster == 1) {
+          n0 = sh.coarse[pass][63 - 2 * lane];
+          n1 = sh.coarse[pass][62 - 2 * lane];
+        } else {
+          int2 v[kMaxCluster];         // all loads in flight before the first is used
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) v[r] = ld_cluster2(&sh.coarse[pass][62 - 2 * lane], r < cluster ? r : rank);
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) {
+            n0 += r < cluster ? v[r].y : 0;
+            n1 += r < cluster ? v[r].x : 0;
+          }
         }
-      }
-      int total;
-      const int upto = block_scan(n0 + n1, sh.warp_sums, total);
-      const int before = upto - n0 - n1;
-      if (before < need && upto >= need) {
-        const bool first = before + n0 >= need;
-        sh.bin = first ? top : top - 1;
-        sh.left = need - before - (first ? 0 : n0);
-        sh.whole = sh.left == (first ? n0 : n1);
+        int before = warp_scan(n0 + n1) - n0 - n1;
+        const bool here0 = before < need && before + n0 >= need;
+        const bool here1 = before + n0 < need && before + n0 + n1 >= need;
+        const int src = __ffs(__ballot_sync(0xffffffffu, here0 || here1)) - 1;
+        const int coarse = __shfl_sync(0xffffffffu, here0 ? 63 - 2 * lane : 62 - 2 * lane, src);
+        const int rest = need - __shfl_sync(0xffffffffu, here0 ? before : before + n0, src);
+        int c = 0;
+        if (cluster == 1) {
+          c = hist[coarse * 32 + 31 - lane];
+        } else {
+          int v[kMaxCluster];
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) v[r] = ld_cluster(&hist[coarse * 32 + 31 - lane], r < cluster ? r : rank);
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) c += r < cluster ? v[r] : 0;
+        }
+        before = warp_scan(c) - c;
+        if (before < rest && before + c >= rest) {
+          sh.bin = coarse * 32 + 31 - lane;
+          sh.left = rest - before;
+          sh.whole = rest - before == c;
+        }
       }
       __syncthreads();
       prefix |= (uint32_t)sh.bin << shift;
@@ -169,79 +260,125 @@ __global__ void __launch_bounds__(kThreads) fa_evict_select_kernel(const EvictAr
       need = sh.left;
       if (sh.whole) break;             // every key with these digits stays
     }
-  // A key stays if it is protected, its digits are above the threshold's, or
-  // they are equal and it is among the first `need` such keys.
-  auto classify = [&](int j, uint32_t k, int& keep, int& eq) {
-    const bool safe = j < lo || j >= hi;
-    keep = safe || (mask != 0 && (k & mask) > prefix);
-    eq = !safe && mask != 0 && (k & mask) == prefix;
+  // A key stays if its digits are above the threshold's, or equal and it is
+  // among the first `need` such keys.  Each warp takes a run of a piece, 128
+  // keys at a time, four consecutive ones a lane.
+  const uint32_t below = (1u << lane) - 1;
+  int above_before = 0, equal_before = 0;          // of the CTAs before, then of the pieces before
+  // Keys above and equal to the threshold in the warp's run of a piece, then
+  // per warp in shared memory.
+  auto warp_run = [&](int n, int& i0, int& i1) {
+    const int per = ((n + kWarps - 1) / kWarps + 127) & ~127;
+    i0 = min(n, warp * per);
+    i1 = min(n, i0 + per);
   };
-  int keep_before = 0, eq_before = 0;
-  if (cluster > 1) {
-    int keep = 0, eq = 0;
-    for (int i = tid; i < j1 - j0; i += kThreads) {
-      int x, y;
-      classify(j0 + i, cached ? keys[i] : key_at(j0 + i), x, y);
-      keep += x;
-      eq += y;
+  auto count_run = [&](int n, int& above, int& equal) {
+    int i0, i1;
+    warp_run(n, i0, i1);
+    for (int i = i0 + 4 * lane; i < i1; i += 128) {
+      const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+      above += ((k.x & mask) > prefix) + ((k.y & mask) > prefix) + ((k.z & mask) > prefix) + ((k.w & mask) > prefix);
+      equal += ((k.x & mask) == prefix) + ((k.y & mask) == prefix) + ((k.z & mask) == prefix) + ((k.w & mask) == prefix);
     }
-    int total_keep, total_eq;
-    block_scan(keep, sh.warp_sums, total_keep);
-    block_scan(eq, sh.warp_sums, total_eq);
-    if (tid == 0) {
-      sh.counts[0] = total_keep;
-      sh.counts[1] = total_eq;
+  };
+  auto publish = [&](int above, int equal) {
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    __syncthreads();                   // the counts before have been read
+    if (lane == 0) {
+      sh.above[warp] = above;
+      sh.equal[warp] = equal;
+    }
+    __syncthreads();
+  };
+  int above = 0, equal = 0;
+  if (cached) {
+    count_run(n_run, above, equal);
+    publish(above, equal);
+  }
+  if (cluster > 1) {
+    if (!cached) {
+      pieces([&](int, int n) { count_run(n, above, equal); });
+      publish(above, equal);
+    }
+    if (warp == 0) {
+      const int x = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.above[lane] : 0);
+      const int y = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.equal[lane] : 0);
+      if (lane == 0) sh.counts = make_int2(x, y);
     }
     cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      keep_before += ld_cluster(&sh.counts[0], r);
-      eq_before += ld_cluster(&sh.counts[1], r);
-    }
-    cluster_sync();                    // nobody exits while its counts are read
+    const int2 c = lane < rank ? ld_cluster2(&sh.counts.x, lane) : make_int2(0, 0);
+    above_before = __reduce_add_sync(0xffffffffu, c.x);
+    equal_before = __reduce_add_sync(0xffffffffu, c.y);
+    cluster_arrive();
   }
-  // Each thread takes an odd number of consecutive keys (an odd stride between
-  // threads meets every bank once).
-  int out = keep_before + min(eq_before, need), seen = eq_before;
-  for (int from = j0; from < j1; from += cap) {
-    const int n = min(cap, j1 - from);
+  pieces([&](int from, int n) {
     if (!cached) {
-      __syncthreads();
-      load(from, n);
-      __syncthreads();
+      above = equal = 0;
+      count_run(n, above, equal);
+      publish(above, equal);
     }
-    const int per = ((n + kThreads - 1) / kThreads) | 1;
-    const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
-    int keep = 0, eq = 0;
-    for (int i = i0; i < i1; ++i) {
-      int x, y;
-      classify(from + i, keys[i], x, y);
-      keep += x;
-      eq += y;
+    const int aw = lane < kWarps ? sh.above[lane] : 0, ew = lane < kWarps ? sh.equal[lane] : 0;
+    const int a0 = above_before + __reduce_add_sync(0xffffffffu, lane < warp ? aw : 0);
+    int e0 = equal_before + __reduce_add_sync(0xffffffffu, lane < warp ? ew : 0);
+    above_before += __reduce_add_sync(0xffffffffu, aw);
+    equal_before += __reduce_add_sync(0xffffffffu, ew);
+    int i0, i1;
+    warp_run(n, i0, i1);
+    int* out = kept + a0 + min(e0, need);
+    // Keys past the piece's end, up to a whole 128, are 0 or the next keys of
+    // the run: neither counts.
+    for (int i = i0; i < i1; i += 128) {
+      const int at = i + 4 * lane;
+      const uint4 q = *reinterpret_cast<const uint4*>(keys + at);
+      const uint32_t k[4] = {q.x & mask, q.y & mask, q.z & mask, q.w & mask};
+      bool keep[4], eq[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        keep[e] = k[e] > prefix && at + e < i1;
+        eq[e] = k[e] == prefix && at + e < i1;
+      }
+      const int mine = eq[0] + eq[1] + eq[2] + eq[3];
+      if (__any_sync(0xffffffffu, mine)) {
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += y;
+        }
+        int r = e0 + upto - mine;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (eq[e]) keep[e] = r++ < need;
+        e0 += __shfl_sync(0xffffffffu, upto, 31);
+      }
+      int pos = 0, total = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t v = __ballot_sync(0xffffffffu, keep[e]);
+        pos += __popc(v & below);
+        total += __popc(v);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (keep[e]) out[pos++] = from + at + e;
+      out += total;
     }
-    int total_eq, total;
-    int rank_eq = block_scan(eq, sh.warp_sums, total_eq) - eq + seen;
-    const int mine = keep + max(0, min(eq, need - rank_eq));
-    int at = block_scan(mine, sh.warp_sums, total) - mine + out;
-    for (int i = i0; i < i1; ++i) {
-      int x, y;
-      classify(from + i, keys[i], x, y);
-      if (y) x = rank_eq++ < need;
-      if (x) kept[at++] = from + i;
-    }
-    seen += total_eq;
-    out += total;
-  }
+  });
+  if (cluster > 1) cluster_wait();     // nobody exits while its counts are read
 }
 
-// kRows kept keys a warp, kUnroll rows' loads in flight.
-template <int D, int kRows>
-__global__ void __launch_bounds__(256) fa_evict_copy_kernel(const EvictArgs a, int blocks_per_unit, const DevStatus st) {
+constexpr int kRows = 8;   // kept keys a warp
+constexpr int kCopyThreads = 128;
+constexpr int kBlockRows = kRows * kCopyThreads / 32;
+
+template <int D>
+__global__ void __launch_bounds__(kCopyThreads, 8)
+    fa_evict_copy_kernel(const EvictArgs a, int blocks_per_unit, const DevStatus st) {
   constexpr int kVec = D / 8, kSide = 32 / (2 * kVec);   // 16-byte vectors a row; rows a warp moves at once, K and V
-  constexpr int kUnroll = 8;
-  static_assert(kRows % (kSide * kUnroll) == 0 || kRows == kSide * 4 || kRows == kSide * 8, "whole rounds");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int unit = blockIdx.x / blocks_per_unit, b = unit / a.kv.Hkv, g = unit - b * a.kv.Hkv, ps = a.kv.page_size;
-  const int r0 = ((blockIdx.x - unit * blocks_per_unit) * 8 + warp) * kRows;
+  const int r0 = (blockIdx.x - unit * blocks_per_unit) * kBlockRows + warp * kRows;
   wait_for_previous();
   const int m = a.new_lens[b];
   if (r0 >= m) return;
@@ -249,7 +386,7 @@ __global__ void __launch_bounds__(256) fa_evict_copy_kernel(const EvictArgs a, i
   long long from = -1, to = -1;
   if (lane < n) {
     const int i = r0 + lane, j = a.kept[(long long)unit * a.budget + i];
-    const int cj = j / ps, ci = i / ps;
+    const int cj = page_of(j, a), ci = page_of(i, a);
     const int p = a.table.pages[b * a.table.stride + cj], q = a.dst.pages[b * a.dst.stride + ci];
     if (p >= 0 && p < a.kv.num_pages && q >= 0 && q < a.kv.num_pages) {
       from = p * a.kv.s_page + g * a.kv.s_head + (long long)(j - cj * ps) * a.kv.s_slot;
@@ -263,19 +400,16 @@ __global__ void __launch_bounds__(256) fa_evict_copy_kernel(const EvictArgs a, i
   const int side = lane / (2 * kVec), v = lane % kVec;
   const bool is_v = (lane / kVec) & 1;
   uint16_t* pool = static_cast<uint16_t*>(is_v ? a.kv.v : a.kv.k) + v * 8;
-  constexpr int kStep = kSide * kUnroll < kRows ? kSide * kUnroll : kRows;
-  for (int r = 0; r < n; r += kStep) {
-    uint4 x[kStep / kSide];
+  uint4 x[kRows / kSide];
 #pragma unroll
-    for (int u = 0; u < kStep / kSide; ++u) {
-      const long long f = __shfl_sync(0xffffffffu, from, r + u * kSide + side);
-      if (f >= 0) x[u] = *reinterpret_cast<const uint4*>(pool + f);
-    }
+  for (int u = 0; u < kRows / kSide; ++u) {
+    const long long f = __shfl_sync(0xffffffffu, from, u * kSide + side);
+    if (f >= 0) x[u] = *reinterpret_cast<const uint4*>(pool + f);
+  }
 #pragma unroll
-    for (int u = 0; u < kStep / kSide; ++u) {
-      const long long t = __shfl_sync(0xffffffffu, to, r + u * kSide + side);
-      if (t >= 0) *reinterpret_cast<uint4*>(pool + t) = x[u];
-    }
+  for (int u = 0; u < kRows / kSide; ++u) {
+    const long long t = __shfl_sync(0xffffffffu, to, u * kSide + side);
+    if (t >= 0) *reinterpret_cast<uint4*>(pool + t) = x[u];
   }
 }
 
@@ -305,32 +439,33 @@ cudaError_t launch(void (*k)(P...), dim3 grid, int block, size_t smem, int clust
 
 }  // namespace
 
+constexpr size_t kSelectBytes = (sizeof(Select) + 15) / 16 * 16;
+
 cudaError_t configure_evict_kernels() {
   return cudaFuncSetAttribute(fa_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)(sizeof(Select) + kMaxCached * 4));
+                              (int)(kSelectBytes + kMaxCached * 4));
 }
 
-cudaError_t launch_paged_evict(const EvictArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream) {
+cudaError_t launch_paged_evict(EvictArgs a, const DevStatus& st, int num_sms, cudaStream_t stream) {
+  const int q = a.kv.page_size / 16;
+  a.page_shift = 27;
+  while ((1 << (a.page_shift - 27)) < q) ++a.page_shift;
+  a.page_mul = (unsigned)(((1ull << a.page_shift) + q - 1) / q);
   const long long most = (long long)a.table.cols * a.kv.page_size;     // keys a sequence can have
   const int units = a.B * a.kv.Hkv;
-  // More CTAs a unit while there are idle SMs and each still has 4 keys a thread.
+  // More CTAs a unit while there are SMs for them and each still has 4 keys a
+  // thread (two CTAs an SM: 45.4 instead of 43.1 us for 128 units of 8192 keys).
   int cluster = 1;
   while (cluster < kMaxCluster && (long long)units * cluster * 2 <= num_sms && most > 4LL * kThreads * cluster) cluster *= 2;
   const long long run = (most + cluster - 1) / cluster;
-  const int cap = (int)(run < kMaxCached ? (run + kThreads - 1) / kThreads * kThreads : kMaxCached);
-  cudaError_t e = launch(fa_evict_select_kernel, dim3((unsigned)units * cluster), kThreads, sizeof(Select) + (size_t)cap * 4,
+  const int cap = (int)(run + 4 < kMaxCached ? (run + 4 + 127) / 128 * 128 : kMaxCached);
+  cudaError_t e = launch(fa_evict_select_kernel, dim3((unsigned)units * cluster), kThreads, kSelectBytes + (size_t)cap * 4,
                          cluster, false, stream, a, cluster, cap, st);
   if (e != cudaSuccess) return e;
-  // 32 rows a warp where that still gives every SM its fill of warps, else 8.
-  const bool wide = (long long)units * a.budget >= 32LL * 32 * num_sms;
-  const int rows = (wide ? 32 : 8) * 8;
-  const int per_unit = (a.budget + rows - 1) / rows;
+  const int per_unit = (a.budget + kBlockRows - 1) / kBlockRows;
   const dim3 grid((unsigned)((long long)units * per_unit));
-  if (a.kv.d == 64)
-    return wide ? launch(fa_evict_copy_kernel<64, 32>, grid, 256, 0, 1, true, stream, a, per_unit, st)
-                : launch(fa_evict_copy_kernel<64, 8>, grid, 256, 0, 1, true, stream, a, per_unit, st);
-  return wide ? launch(fa_evict_copy_kernel<128, 32>, grid, 256, 0, 1, true, stream, a, per_unit, st)
-              : launch(fa_evict_copy_kernel<128, 8>, grid, 256, 0, 1, true, stream, a, per_unit, st);
+  return a.kv.d == 64 ? launch(fa_evict_copy_kernel<64>, grid, kCopyThreads, 0, 1, true, stream, a, per_unit, st)
+                      : launch(fa_evict_copy_kernel<128>, grid, kCopyThreads, 0, 1, true, stream, a, per_unit, st);
 }
 
 }  // namespace fa

@@ -168,9 +168,11 @@ struct EvictArgs {
   int* new_lens;             // [B]
   int* kept;                 // [B, Hkv, budget], -1 past the new length
   int B, budget, recent, sinks;
+  unsigned page_mul;         // division by page_size (set by the launcher)
+  int page_shift;
 };
 
-cudaError_t launch_paged_evict(const EvictArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_evict(EvictArgs a, const DevStatus& st, int num_sms, cudaStream_t stream);
 
 // One-time set-up of the current device for each translation unit's kernels
 // (shared-memory sizes; the forward also checks that every instance was

@@ -495,6 +495,11 @@ EVICT = [
     ([2100, 64], 2, 64, 64, 1500, 10, 0, "odd", BF, "hnd"),              # NaN, infinities, -0
     ([40000], 1, 64, 64, 5000, 100, 4, "heavy", BF, "hnd"),
     ([9000, 4097], 2, 64, 128, 8999, 0, 16, "narrow", BF, "hnd"),        # values that share their high bits
+    # More keys than shared memory holds: in one block (too many units for a
+    # cluster each), and over a whole cluster.
+    ([60000] + [40] * 79, 1, 64, 2048, 1000, 10, 4, "heavy", BF, "hnd"),
+    ([450001], 1, 64, 4096, 60000, 5, 0, "heavy", BF, "hnd"),
+    ([450001], 1, 64, 4096, 300000, 1000, 7, "ties", BF, "hnd"),
 ]
 
 
