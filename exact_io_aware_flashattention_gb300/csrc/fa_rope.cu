@@ -28,7 +28,7 @@ namespace fa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kUnroll = 4;   // heads whose loads are in flight per thread
 
 template <typename T>
@@ -139,15 +139,15 @@ __device__ __forceinline__ void do_heads(const T* in, long long in_sh, T* out, l
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
       if (h + u < h1) {
-        a[u] = *reinterpret_cast<const uint4*>(in + (h + u) * in_sh + ck.e0);
-        b[u] = *reinterpret_cast<const uint4*>(in + (h + u) * in_sh + ck.e1);
+        a[u] = __ldcs(reinterpret_cast<const uint4*>(in + (h + u) * in_sh + ck.e0));
+        b[u] = __ldcs(reinterpret_cast<const uint4*>(in + (h + u) * in_sh + ck.e1));
       }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
       if (h + u < h1) {
         if (turned) turn8<T, kInter>(a[u], b[u], cs, sn);
-        *reinterpret_cast<uint4*>(out + (h + u) * out_sh + ck.e0) = a[u];
-        *reinterpret_cast<uint4*>(out + (h + u) * out_sh + ck.e1) = b[u];
+        __stcs(reinterpret_cast<uint4*>(out + (h + u) * out_sh + ck.e0), a[u]);
+        __stcs(reinterpret_cast<uint4*>(out + (h + u) * out_sh + ck.e1), b[u]);
       }
   }
 }
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) fa_append_kernel(const AppendArgs a,
 // Heads per block: all of them where the tokens alone fill the GPU (the
 // angles are then formed once a token), fewer where they do not.
 int heads_per_block(long long token_blocks, int heads, int num_sms) {
-  const long long want = 4LL * num_sms;
+  const long long want = 8LL * num_sms;
   long long splits = (want + token_blocks - 1) / token_blocks;
   const long long most = (heads + kUnroll - 1) / kUnroll;
   if (splits > most) splits = most;
