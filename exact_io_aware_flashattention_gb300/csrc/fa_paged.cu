@@ -15,8 +15,8 @@
 // evenly and one long sequence is spread over all of them.  A part starts and
 // ends anywhere: a unit that lies in one CTA is finished there, a unit cut
 // over several leaves one unnormalised (O, max, sum) per CTA in the workspace
-// (at most two a CTA: its first and its last unit), which fa_paged_join_kernel
-// joins in a fixed order.
+// (at most two a CTA: its first and its last unit), which
+// fa_paged_finish_kernel joins in a fixed order.
 //   Warp 4 is the producer: it looks the pages of eight tiles up at once and
 // copies 16-key slices (a page is a multiple of 16, so a slice lies in one
 // page) into a ring of tiles with TMA, 128-byte swizzled.  Warps 0-3 each own
@@ -528,45 +528,52 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Joins the parts of units that were cut, in order, relative to the largest
-// maximum: O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  One block per
-// (sequence, head), its warps taking every fourth part.  Sequences without
-// visible keys get O = 0, LSE = -inf.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) fa_paged_join_kernel(const DecodeArgs a, int parts) {
-  constexpr int E = D / 32;
-  __shared__ float sm[4], sl[4], so[4][D];
-  launch_dependents();
-  wait_for_previous();
-  const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = blockIdx.x;
+// The parts [i0, i1] over which head h of (b, g) is cut, and its index in them.
+struct Cut {
+  int i0, i1, hh;
+  // Where part i left the head: its last unit if it is the unit's first part.
+  __device__ __forceinline__ long long at(int i) const { return ((long long)i * 2 + (i == i0 ? 1 : 0)) * 16 + hh; }
+};
+__device__ __forceinline__ Cut cut_of(const DecodeArgs& a, int g, int h, long long before, long long n, long long all,
+                                      int parts) {
   const int G = a.Hq / a.kv.Hkv, per = a.unit_heads, chunks = (G + per - 1) / per, cols = a.kv.Hkv * chunks;
-  const long long before = a.prefix[b], n = a.prefix[b + 1] - before;
+  const int hc = h / per;
+  const long long total = all * cols, t0 = before * cols + (g * chunks + hc) * n;
+  parts = (int)min(total, (long long)parts);
+  return Cut{part_of(t0, total, parts), part_of(t0 + n - 1, total, parts), h - hc * per};
+}
+
+// What is left after the tiles, in one launch (each half needs only the decode
+// kernel): block r < B * Hq joins row r, the other blocks add the weights.
+//
+// Join: the parts of a unit that was cut, in order, relative to the largest
+// maximum: O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i; warps take every
+// fourth part.  Sequences without visible keys get O = 0, LSE = -inf.
+template <typename T, int D>
+__device__ __forceinline__ void join_row(const DecodeArgs& a, int parts) {
+  constexpr int E = D / 32;
+  __shared__ float sl[4], so[4][D];
+  const long long row = blockIdx.x;
+  const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq, G = a.Hq / a.kv.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long before = a.prefix[b], n = a.prefix[b + 1] - before, all = a.prefix[a.B];
   if (n == 0) {
     for (int e = threadIdx.x; e < D; e += 128) static_cast<T*>(a.o)[row * D + e] = (T)0.f;
-    if (threadIdx.x == 0) {
-      a.lse[row] = -INFINITY;
-      if (a.lse2) a.lse2[row] = -INFINITY;
-    }
+    if (threadIdx.x == 0) a.lse[row] = -INFINITY;
     return;
   }
-  const int g = h / G, hc = (h - g * G) / per, hh = (h - g * G) % per;
-  const long long total = a.prefix[a.B] * cols, t0 = before * cols + (g * chunks + hc) * n;
-  parts = (int)min(total, (long long)parts);
-  const int i0 = part_of(t0, total, parts), i1 = part_of(t0 + n - 1, total, parts);
-  if (i0 == i1) return;
-  auto at = [&](int i) { return ((long long)i * 2 + (i == i0 ? 1 : 0)) * 16 + hh; };
+  const Cut c = cut_of(a, hq / G, hq % G, before, n, all, parts);
+  if (c.i0 == c.i1) return;
   float m = -INFINITY;
-  for (int i = i0 + lane; i <= i1; i += 32) m = fmaxf(m, a.part_ml[at(i)].x);
+  for (int i = c.i0 + lane; i <= c.i1; i += 32) m = fmaxf(m, a.part_ml[c.at(i)].x);
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   const float mu = m == -INFINITY ? 0.f : m;
   float l = 0.f, o[E] = {};
 #pragma unroll 4
-  for (int i = i0 + warp; i <= i1; i += 4) {
-    const float2 y = a.part_ml[at(i)];
+  for (int i = c.i0 + warp; i <= c.i1; i += 4) {
+    const float2 y = a.part_ml[c.at(i)];
     const float f = ex2(y.x - mu);
-    const float* x = a.part + at(i) * D + lane * E;
+    const float* x = a.part + c.at(i) * D + lane * E;
     l += f * y.y;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[e], o[e]);
@@ -579,57 +586,115 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const DecodeArgs a, 
   const float inv = 1.f / l;
   for (int e = threadIdx.x; e < D; e += 128)
     static_cast<T*>(a.o)[row * D + e] = (T)(((so[0][e] + so[1][e]) + (so[2][e] + so[3][e])) * inv);
-  if (threadIdx.x == 0) {
-    const float lse2 = m + log2f(l);
-    a.lse[row] = lse2 * 0.69314718055994530942f;
-    if (a.lse2) a.lse2[row] = lse2;
-  }
+  if (threadIdx.x == 0) a.lse[row] = (m + log2f(l)) * 0.69314718055994530942f;
 }
 
-// Adds each visible key's weight, summed over the group's heads from the
-// stashed scores (log2 units), to its accumulated weight.  Warps take tiles of
-// the line without head chunks (a kv head's keys once), 2 keys a lane.  A
-// reduction at L2 rather than a load and a store, so that sequences sharing a
-// page both count.
-__global__ void __launch_bounds__(256) fa_paged_weights_kernel(const DecodeArgs a) {
-  wait_for_previous();
-  const int warps = gridDim.x * 8, warp = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+// Log-sum-exp (log2 units) of head h of (b, g): the decode kernel's if the
+// unit was whole, else from its parts.
+__device__ __forceinline__ float head_lse2(const DecodeArgs& a, int b, int g, int h, long long before, long long n,
+                                           long long all, int parts) {
+  const Cut c = cut_of(a, g, h, before, n, all, parts);
+  if (c.i0 == c.i1) return a.lse2[(long long)b * a.Hq + g * (a.Hq / a.kv.Hkv) + h];
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int i = c.i0; i <= c.i1; ++i) m = fmaxf(m, a.part_ml[c.at(i)].x);
+  const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+  for (int i = c.i0; i <= c.i1; ++i) {
+    const float2 y = a.part_ml[c.at(i)];
+    l = fmaf(ex2(y.x - mu), y.y, l);
+  }
+  return m + log2f(l);
+}
+
+// Weights: adds each visible key's weight, summed over the group's heads from
+// the stashed scores (log2 units), to its accumulated weight.  Warps take
+// equal runs of the line of tiles (a kv head's keys once, whatever its head
+// chunks), two keys a lane.  A reduction at L2 rather than a load and a store,
+// so that sequences sharing a page both count.
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, int parts) {
+  const int lane = threadIdx.x & 31;
+  const int first = a.B * a.Hq, warp = (blockIdx.x - first) * 4 + (threadIdx.x >> 5), warps = (gridDim.x - first) * 4;
   const int Hkv = a.kv.Hkv, G = a.Hq / Hkv;
-  const long long total = a.prefix[a.B] * Hkv;
+  const long long all = a.prefix[a.B], total = all * Hkv;
   long long t = total * warp / warps;
   const long long end = total * (warp + 1) / warps;
   if (t >= end) return;
-  int lo = 0, hi = a.B;                            // last b with prefix[b] * Hkv <= t
+  // Last sequence with prefix * Hkv <= t, 32 samples a round.
+  int lo = 0, hi = a.B;
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.prefix[mid] * Hkv <= t) lo = mid; else hi = mid;
+    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+    const int k = __popc(__ballot_sync(0xffffffffu, at < hi && a.prefix[at] * Hkv <= t));
+    lo += k * step;
+    hi = min(hi, lo + step);
   }
   int b = lo;
   Span s = span_of(a, b);
-  int g = (int)((t - a.prefix[b] * Hkv) / s.n), tile = (int)(t - a.prefix[b] * Hkv - (long long)g * s.n);
+  long long before = a.prefix[b];
+  int g = (int)((t - before * Hkv) / s.n), tile = (int)(t - before * Hkv - (long long)g * s.n);
+  bool fresh = true;
+  float lse2 = 0.f;
   for (; t < end; ++t) {
-    const float* lse2 = a.lse2 + (long long)b * a.Hq + g * G;
+    // Lane h holds the LSE of head h (of the 32 heads at hand, for larger groups).
+    float w[2] = {0.f, 0.f};
+    int page[2] = {-1, -1};
+    long long slot[2] = {0, 0};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int key = (s.tile0 + tile) * kTileKeys + u * 32 + lane;
       if (key >= s.first && key < s.len) {
-        const float* x = a.stash + (((long long)b * Hkv + g) * a.stash_keys + key) * G;
-        float w = 0.f;
-        for (int h = 0; h < G; ++h) w += ex2(x[h] - lse2[h]);
-        const int c = key / a.kv.page_size, page = a.table.pages[b * a.table.stride + c];
-        if (page >= 0 && page < a.kv.num_pages)
-          atomicAdd(&a.scores[((long long)page * Hkv + g) * a.kv.page_size + key - c * a.kv.page_size], w);
+        const int c = key / a.kv.page_size;
+        page[u] = a.table.pages[b * a.table.stride + c];
+        slot[u] = key - c * a.kv.page_size;
       }
     }
-    if (++tile == s.n) {
+    for (int h0 = 0; h0 < G; h0 += 32) {
+      if (fresh || G > 32) lse2 = h0 + lane < G ? head_lse2(a, b, g, h0 + lane, before, s.n, all, parts) : 0.f;
+      const int nh = min(32, G - h0);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int key = (s.tile0 + tile) * kTileKeys + u * 32 + lane;
+        const bool in = key >= s.first && key < s.len;
+        const float* x = a.stash + (((long long)b * Hkv + g) * a.stash_keys + key) * G + h0;
+        if (G % 4 == 0) {
+          for (int h = 0; h < nh; h += 4) {
+            const float l0 = __shfl_sync(0xffffffffu, lse2, h), l1 = __shfl_sync(0xffffffffu, lse2, h + 1);
+            const float l2 = __shfl_sync(0xffffffffu, lse2, h + 2), l3 = __shfl_sync(0xffffffffu, lse2, h + 3);
+            if (in) {
+              const float4 y = *reinterpret_cast<const float4*>(x + h);
+              w[u] += (ex2(y.x - l0) + ex2(y.y - l1)) + (ex2(y.z - l2) + ex2(y.w - l3));
+            }
+          }
+        } else {
+          for (int h = 0; h < nh; ++h) {
+            const float l = __shfl_sync(0xffffffffu, lse2, h);
+            if (in) w[u] += ex2(x[h] - l);
+          }
+        }
+      }
+    }
+    fresh = false;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (page[u] >= 0 && page[u] < a.kv.num_pages)
+        atomicAdd(&a.scores[((long long)page[u] * Hkv + g) * a.kv.page_size + slot[u]], w[u]);
+    if (++tile == s.n && t + 1 < end) {
       tile = 0;
+      fresh = true;
       if (++g == Hkv) {
         g = 0;
-        if (t + 1 < end)
-          do s = span_of(a, ++b); while (s.n == 0 && b + 1 < a.B);
+        do s = span_of(a, ++b); while (s.n == 0 && b + 1 < a.B);
+        before = a.prefix[b];
       }
     }
   }
+}
+
+template <typename T, int D, bool kScores>
+__global__ void __launch_bounds__(128) fa_paged_finish_kernel(const DecodeArgs a, int parts) {
+  wait_for_previous();
+  if (!kScores || blockIdx.x < a.B * a.Hq) join_row<T, D>(a, parts);
+  else add_weights(a, parts);
 }
 
 // A launch whose blocks may start before the kernel in front of it is done
@@ -654,9 +719,13 @@ cudaError_t launch_decode(const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs
   if (a.unit_heads == 8) fa_paged_decode_kernel<T, D, 1><<<parts, kThreads, Cfg<D>::kBytes, stream>>>(tk, tv, a, st);
   else fa_paged_decode_kernel<T, D, 2><<<parts, kThreads, Cfg<D>::kBytes, stream>>>(tk, tv, a, st);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_after(fa_paged_join_kernel<T, D>, a.B * a.Hq, 128, stream, a, parts);
-  if (e == cudaSuccess && a.scores) e = launch_after(fa_paged_weights_kernel, num_sms * 4, 256, stream, a);
-  return e;
+  if (e != cudaSuccess) return e;
+  const long long rows = (long long)a.B * a.Hq;
+  if (!a.scores) return launch_after(fa_paged_finish_kernel<T, D, false>, (unsigned)rows, 128, stream, a, parts);
+  // For the weights 16 tiles a block, up to 4 blocks an SM.
+  const long long tiles = (a.stash_keys + kTileKeys - 1) / kTileKeys * a.B * a.kv.Hkv;
+  const long long blocks = (tiles + 15) / 16 < 4LL * num_sms ? (tiles + 15) / 16 : 4LL * num_sms;
+  return launch_after(fa_paged_finish_kernel<T, D, true>, (unsigned)(rows + blocks), 128, stream, a, parts);
 }
 
 template <typename T, int D>
