@@ -1094,7 +1094,8 @@ fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_pa
   a.stash_keys = (long long)kv->page_size * table->max_pages;
   // Two CTAs per SM, but no more than there can be tiles.
   const long long columns = (long long)kv->Hkv * ((G + a.unit_heads - 1) / a.unit_heads);
-  const long long tiles = (long long)B * columns * ((a.stash_keys + 63) / 64);
+  const int keys = fa::decode_tile_keys(kv->d);
+  const long long tiles = (long long)B * columns * ((a.stash_keys + keys - 1) / keys);
   const int parts = (int)std::min<long long>(tiles, std::min(2 * ds->num_sms, fa::kDecodeMaxParts));
   fa::TmaMap4 tk, tv;
   FA_TRY(tmap_pool(&tk, kv, kv->k));

@@ -146,7 +146,7 @@ struct DecodeArgs {
   float scale_log2;
   int unit_heads;            // query heads of a kv group that share a unit: 8 or 16
   // Workspace
-  long long* prefix;         // [B + 1] 64-key tiles of the sequences before b
+  long long* prefix;         // [B + 1] tiles of the sequences before b (decode_tile_keys keys each)
   float* part;               // [kDecodeMaxParts][2][16][d] unnormalised O of units cut over CTAs
   float2* part_ml;           // [kDecodeMaxParts][2][16] their maximum (log2 units) and sum
   float* lse2;               // [B, Hq] log-sum-exp in log2 units (with scores)
@@ -155,6 +155,7 @@ struct DecodeArgs {
 };
 
 constexpr int kDecodeMaxParts = 320;   // CTAs of the decode kernel at most
+constexpr int decode_tile_keys(int d) { return d == 64 ? 128 : 64; }
 
 // `tk`, `tv` view the pools as {d, page_size, Hkv, num_pages}; `parts` CTAs.
 cudaError_t launch_paged_decode(int dtype, const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs& a, const DevStatus& st,

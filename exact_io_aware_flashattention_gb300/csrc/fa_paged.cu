@@ -10,18 +10,19 @@
 // head, 4 d bytes per key against 4 G d operations (G = Hq / Hkv heads).
 //
 // fa_paged_decode_kernel.  The keys of all (sequence, kv head, chunk of up to
-// 16 query heads) units, in tiles of 64, form one line that is cut into equal
-// parts, one per CTA (two CTAs per SM), so batches of any lengths load the SMs
-// evenly and one long sequence is spread over all of them.  A part starts and
-// ends anywhere: a unit that lies in one CTA is finished there, a unit cut
-// over several leaves one unnormalised (O, max, sum) per CTA in the workspace
-// (at most two a CTA: its first and its last unit), which
-// fa_paged_finish_kernel joins in a fixed order.
-//   Warp 4 is the producer: it looks the pages of eight tiles up at once and
+// 16 query heads) units, in tiles of 64 (d = 128) or 128 (d = 64), form one
+// line that is cut into equal parts, one per CTA (two CTAs per SM), so batches
+// of any lengths load the SMs evenly and one long sequence is spread over all
+// of them.  A part starts and ends anywhere: a unit that lies in one CTA is
+// finished there, a unit cut over several leaves one unnormalised (O, max,
+// sum) per CTA in the workspace (at most two a CTA: its first and its last
+// unit), which fa_paged_finish_kernel joins in a fixed order.
+//   Warp 4 is the producer: it looks the pages of several tiles up at once and
 // copies 16-key slices (a page is a multiple of 16, so a slice lies in one
-// page) into a ring of tiles with TMA, 128-byte swizzled.  Warps 0-3 each own
-// one slice of every tile and run their own online softmax over it, so they
-// meet only at a unit's end.
+// page) into a ring of three 32 KB tiles with TMA, 128-byte swizzled.  Warps
+// 0-3 each own every fourth slice and run their own online softmax over it, so
+// they meet only at a unit's end; the next unit's query rows are loaded while
+// the current one is worked on.
 //   Matrix products by mma.sync (m16n8k16): S^T = K Q^T takes 16 keys as rows
 // and 8 heads as columns, and O^T += V^T P^T takes 16 elements of d as rows,
 // so groups of up to 8 heads waste nothing on padding to 16 rows, and a
@@ -41,15 +42,17 @@ namespace {
 
 constexpr int kConsumers = 4;                      // warps, one 16-key slice of a tile each
 constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kTileKeys = 16 * kConsumers;
-
 // Wait-site ids.
 enum : int { kSiteFull = 47, kSiteEmpty = 48, kDrainFull = 49 };
 
 template <int D>
 struct Cfg {
-  static constexpr int kStages = D == 128 ? 3 : 6;             // 96 KB of tiles in flight per CTA
-  static constexpr uint32_t kHalf = kTileKeys * D * 2u;        // K or V of a tile: [D/64][64 keys][128 bytes]
+  static constexpr int kSl = 128 / D;                          // slices of a tile per warp
+  static constexpr int kSlices = kSl * kConsumers;
+  static constexpr int kKeys = 16 * kSlices;                   // keys of a tile
+  static constexpr int kStages = 3;                            // 96 KB of tiles in flight per CTA
+  static constexpr uint32_t kHalf = kKeys * D * 2u;            // K or V of a tile: [D/64][keys][128 bytes]
+  static constexpr uint32_t kAtom = kKeys * 128u;
   static constexpr uint32_t kStage = 2u * kHalf;
   static constexpr uint32_t kBuf = kStages * kStage;           // [4 warps][8 heads][D] fp32, one head group
   static constexpr uint32_t kMl = kBuf + kConsumers * 8u * D * 4u;   // [4 warps][16 heads] (max, sum)
@@ -58,8 +61,8 @@ struct Cfg {
 };
 
 struct Bars {
-  uint64_t full[6], empty[6];
-  uint32_t mask[6];          // slices of the stage's tile that were loaded
+  uint64_t full[3], empty[3];
+  uint32_t mask[3];          // slices of the stage's tile that were loaded
   int abort;
   int scan[kThreads / 32];
   int b0;                    // first sequence of this CTA's part
@@ -121,17 +124,18 @@ __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;"
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Visible keys [first, len) of a sequence, as 64-key tiles [tile0, tile0 + n).
+// Visible keys [first, len) of a sequence, as tiles [tile0, tile0 + n) of kKeys.
 struct Span {
   int len, first, tile0, n;
 };
+template <int kKeys>
 __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b) {
   Span s;
   s.len = a.seq_lens[b];
   if (s.len < 0 || s.len > (long long)a.table.cols * a.kv.page_size) s.len = -1;   // recorded by the caller
   s.first = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
-  s.tile0 = s.first / kTileKeys;
-  s.n = s.len > 0 ? (s.len - 1) / kTileKeys - s.tile0 + 1 : 0;
+  s.tile0 = s.first / kKeys;
+  s.n = s.len > 0 ? (s.len - 1) / kKeys - s.tile0 + 1 : 0;
   return s;
 }
 
@@ -143,13 +147,13 @@ __device__ __forceinline__ int part_of(long long tile, long long total, int part
 }
 
 // A CTA's way through its part: unit (b, column), tile within the unit.
+template <int kKeys>
 struct Walk {
   int b, col, tile;
   Span s;
   long long left;      // tiles of the part from here on
-  __device__ __forceinline__ void next(const DecodeArgs& a, int cols) {
-    --left;
-    if (++tile < s.n || left == 0) return;
+  // On to the unit after this one.
+  __device__ __forceinline__ void next_unit(const DecodeArgs& a, int cols) {
     tile = 0;
     if (++col < cols) return;
     col = 0;
@@ -158,16 +162,52 @@ struct Walk {
         left = 0;
         return;
       }
-      s = span_of(a, b);
+      s = span_of<kKeys>(a, b);
     } while (s.n == 0);
   }
+  __device__ __forceinline__ void next(const DecodeArgs& a, int cols) {
+    --left;
+    if (++tile == s.n && left > 0) next_unit(a, cols);
+  }
 };
+
+// Query rows of unit (b, col) as the B operands of S^T = K Q^T: column = head
+// lane / 4, rows = two elements of d at 2 (lane % 4), and eight further on.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int col, int chunks, uint32_t (&q)[NT][D / 16][2]) {
+  const int lane = threadIdx.x & 31, G = a.Hq / a.kv.Hkv;
+  const int g = col / chunks, h0 = g * G + (col - g * chunks) * 8 * NT + (lane >> 2), h1 = (g + 1) * G;
+  const T* p = static_cast<const T*>(a.q) + b * a.q_sb + (lane & 3) * 2;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const bool in = h0 + n * 8 < h1;
+    const T* x = p + (in ? h0 + n * 8 : h1 - 1) * a.q_sh;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) q[n][k][e] = in ? *reinterpret_cast<const uint32_t*>(x + k * 16 + e * 8) : 0u;
+  }
+}
+
+// Sequences without visible keys: O = 0, LSE = -inf.  One warp of each CTA
+// takes every gridDim.x-th sequence.
+template <typename T, int D>
+__device__ __forceinline__ void fill_empty(const DecodeArgs& a) {
+  const int lane = threadIdx.x & 31;
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (span_of<Cfg<D>::kKeys>(a, b).n > 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + (long long)b * a.Hq * D);
+    for (int i = lane; i < a.Hq * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < a.Hq; i += 32) a.lse[(long long)b * a.Hq + i] = -INFINITY;
+  }
+}
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
     fa_paged_decode_kernel(const __grid_constant__ TmaMap4 tmK, const __grid_constant__ TmaMap4 tmV, const DecodeArgs a,
                            const DevStatus st) {
   using C = Cfg<D>;
+  constexpr int kSl = C::kSl;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kBar);
   volatile int* abort_flag = &bars->abort;
@@ -200,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int b = base + threadIdx.x;
       Span s{};
       if (b < a.B) {
-        s = span_of(a, b);
+        s = span_of<C::kKeys>(a, b);
         if (s.len < 0 && round == 0 && blockIdx.x == 0) record_error(st, kErrBadIndex, kSiteDecodeLen);
       }
       int x = s.n;
@@ -231,12 +271,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   __syncthreads();
   const int parts = (int)min(total, (long long)gridDim.x);
-  if ((int)blockIdx.x >= parts) return;
+  if ((int)blockIdx.x >= parts) {
+    if (warp == kConsumers) fill_empty<T, D>(a);
+    return;
+  }
   const long long t0 = part_start(total, blockIdx.x, parts), t1 = part_start(total, blockIdx.x + 1, parts);
-  Walk w;
+  Walk<C::kKeys> w;
   w.left = t1 - t0;
   w.b = bars->b0;
-  w.s = span_of(a, w.b);
+  w.s = span_of<C::kKeys>(a, w.b);
   {
     const long long in = t0 - bars->before;
     w.col = (int)(in / w.s.n);
@@ -245,23 +288,37 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer
-    // Lane l looks up slice l % 4 of tile l / 4 of the next eight tiles of the
-    // unit; lanes 0-15 issue one copy each: slice, K or V, 64-column block.
-    constexpr int kAtoms = D / 64;
-    int it = 0;
-    bool good = true;
-    while (good && w.left > 0) {
-      const int have = (int)min((long long)min(w.s.n - w.tile, 8), w.left);
-      const int key0 = (w.s.tile0 + w.tile + (lane >> 2)) * kTileKeys + (lane & 3) * 16;
-      int page = -1, slot = 0;
-      if ((lane >> 2) < have && key0 < w.s.len && key0 + 16 > w.s.first) {
+    // Lane l looks up slice l % kSlices of tile l / kSlices of the unit's next
+    // tiles; lanes 0-15 issue one copy each: slice, K or V, 64-column block.
+    constexpr int kAhead = 32 / C::kSlices;
+    static_assert(C::kSlices * 2 * (D / 64) == 16, "copies of a tile");
+    // The lookup of the next run of tiles is issued before the copies of this
+    // one, and not repeated for the next kv head of a sequence that fits one.
+    const int my_slice = lane % C::kSlices, my_tile = lane / C::kSlices;
+    auto look_up = [&](const Walk<C::kKeys>& x, int& page, int& slot) {
+      const int have = (int)min((long long)min(x.s.n - x.tile, kAhead), x.left);
+      const int key0 = (x.s.tile0 + x.tile + my_tile) * C::kKeys + my_slice * 16;
+      page = 0;
+      slot = -1;                       // not visible: not copied
+      if (my_tile < have && key0 < x.s.len && key0 + 16 > x.s.first) {
         const int c = key0 / a.kv.page_size;
         slot = key0 - c * a.kv.page_size;
-        page = a.table.pages[w.b * a.table.stride + c];
-        if (page < 0 || page >= a.kv.num_pages) {
-          record_error(st, kErrBadIndex, kSiteDecodePage);
-          page = -1;
-        }
+        page = a.table.pages[x.b * a.table.stride + c];
+      }
+      return have;
+    };
+    int it = 0, page, slot, have = look_up(w, page, slot);
+    bool good = true;
+    while (good && w.left > 0) {
+      Walk<C::kKeys> x = w;
+      x.left -= have;
+      x.tile += have;
+      if (x.tile == x.s.n && x.left > 0) x.next_unit(a, cols);
+      int page_next = page, slot_next = slot, have_next = have;
+      if (x.left > 0 && !(x.b == w.b && x.tile == w.tile && x.left >= have)) have_next = look_up(x, page_next, slot_next);
+      if (slot >= 0 && (page < 0 || page >= a.kv.num_pages)) {
+        record_error(st, kErrBadIndex, kSiteDecodePage);
+        slot = -1;
       }
       const int g = w.col / chunks;
       for (int i = 0; i < have; ++i, ++it) {
@@ -270,22 +327,26 @@ __global__ void __launch_bounds__(kThreads, 2)
           good = false;
           break;
         }
-        const int p = __shfl_sync(0xffffffffu, page, i * 4 + (lane & 3));
-        const int sl = __shfl_sync(0xffffffffu, slot, i * 4 + (lane & 3));
-        const uint32_t mask = __ballot_sync(0xffffffffu, p >= 0) & 15u;
+        const int p = __shfl_sync(0xffffffffu, page, i * C::kSlices + my_slice);
+        const int sl = __shfl_sync(0xffffffffu, slot, i * C::kSlices + my_slice);
+        const uint32_t mask = __ballot_sync(0xffffffffu, sl >= 0) & ((1u << C::kSlices) - 1);
         if (lane == 0) {
           bars->mask[s] = mask;
           mbar_arrive_expect_tx(&bars->full[s], __popc(mask) * 2u * 16u * D * 2u);
         }
         __syncwarp();
-        if (lane < 8 * kAtoms && p >= 0) {
-          const int kv = (lane >> 2) & 1, atom = lane >> 3;
-          tma_load_4d(smem + s * C::kStage + kv * C::kHalf + atom * (kTileKeys * 128u) + (lane & 3) * 2048u, kv ? &tmV : &tmK,
+        if (lane < 16 && sl >= 0) {
+          const int kv = my_tile & 1, atom = my_tile >> 1;
+          tma_load_4d(smem + s * C::kStage + kv * C::kHalf + atom * C::kAtom + my_slice * 2048u, kv ? &tmV : &tmK,
                       &bars->full[s], atom * 64, sl, g, p);
         }
-        w.next(a, cols);
       }
+      w = x;
+      page = page_next;
+      slot = slot_next;
+      have = have_next;
     }
+    fill_empty<T, D>(a);
     // Every copy issued must have landed before the CTA may exit.
     if (lane == 0)
       for (int s = 0; s < C::kStages && s < it; ++s) {
@@ -307,70 +368,108 @@ __global__ void __launch_bounds__(kThreads, 2)
   float2* ml = reinterpret_cast<float2*>(smem + C::kMl);
   const float sl2 = a.scale_log2;
 
-  uint32_t q[NT][D / 16][2];
+  uint32_t q[NT][D / 16][2], q_next[NT][D / 16][2];
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
   bool dead = false, fresh = true;
-  long long unit_pos = w.tile;                    // tile of the unit at which this CTA entered it
+  int unit_pos = w.tile;                          // tile of the unit at which this CTA entered it
+  // (Where the registers for a second set of query rows are lacking they are
+  // loaded when their unit comes up.)
+  constexpr bool kAheadQ = NT * D <= 128;
+  if constexpr (kAheadQ) load_q<T, D, NT>(a, w.b, w.col, chunks, q_next);
+  int g = 0, h0 = 0, h1 = 0;                      // kv head, query heads [h0, h1) of the unit
+  float* stash = nullptr;                         // this lane's first score of key 0 of the unit
   for (int it = 0; w.left > 0; ++it) {
-    const int g = w.col / chunks, h0 = g * G + (w.col - g * chunks) * 8 * NT, h1 = (g + 1) * G;
     if (fresh) {
       fresh = false;
       unit_pos = w.tile;
-      const T* qp = static_cast<const T*>(a.q) + w.b * a.q_sb;
+      g = w.col / chunks;
+      h0 = g * G + (w.col - g * chunks) * 8 * NT;
+      h1 = (g + 1) * G;
+      if (a.stash) stash = a.stash + ((long long)w.b * a.kv.Hkv + g) * a.stash_keys * G + h0 - g * G + qc * 2;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int h = h0 + n * 8 + qr;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const T* x = qp + h * a.q_sh + k * 16 + qc * 2;
-          q[n][k][0] = h < h1 ? *reinterpret_cast<const uint32_t*>(x) : 0u;
-          q[n][k][1] = h < h1 ? *reinterpret_cast<const uint32_t*>(x + 8) : 0u;
-        }
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
+          if constexpr (kAheadQ) {
+            q[n][k][0] = q_next[n][k][0];
+            q[n][k][1] = q_next[n][k][1];
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
+        }
         m[n][0] = m[n][1] = -INFINITY;
         l[n][0] = l[n][1] = 0.f;
+      }
+      if constexpr (!kAheadQ) {
+        load_q<T, D, NT>(a, w.b, w.col, chunks, q);
+      } else if (w.left > w.s.n - w.tile) {
+        Walk<C::kKeys> x = w;
+        x.next_unit(a, cols);
+        if (x.left > 0) load_q<T, D, NT>(a, x.b, x.col, chunks, q_next);
       }
     }
     const int s = it % C::kStages;
     // After a wait that gave up the warp goes on through its part without
     // touching the tiles, so that the warps still meet at each unit's end.
     if (!dead && !mbar_wait_warp(&bars->full[s], (it / C::kStages) & 1, st, abort_flag, kSiteFull)) dead = true;
-    if (!dead && (bars->mask[s] >> warp & 1)) {
-      const int key0 = (w.s.tile0 + w.tile) * kTileKeys + warp * 16;
-      // Keys [lo, hi) of the slice are visible.
-      const int lo = w.s.first - key0, hi = w.s.len - key0;
-      const bool edge = lo > 0 || hi < 16;
-      float c[NT][2][4] = {};
+    // The warp's slices are warp, warp + 4, ...
+    const uint32_t loaded = dead ? 0u : bars->mask[s] >> warp;
+    constexpr uint32_t kMine = kSl == 1 ? 1u : 0x11u;
+    if (loaded & kMine) {
+      const int key0 = (w.s.tile0 + w.tile) * C::kKeys + warp * 16;
+      // Keys [lo, hi) of slice u are visible; of one that was not loaded none.
+      int lo[kSl], hi[kSl];
+      bool edge = false;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        uint32_t x[4];
-        ldsm4(x, kbase + s * C::kStage + (k >> 2) * (kTileKeys * 128u) + ((((k & 3) * 2 + khalf) ^ (krow & 7)) << 4));
-#pragma unroll
-        for (int n = 0; n < NT; ++n) Mma<T>::mma(c[n][k & 1], x, q[n][k][0], q[n][k][1]);
+      for (int u = 0; u < kSl; ++u) {
+        lo[u] = w.s.first - key0 - u * 64;
+        hi[u] = loaded >> (4 * u) & 1 ? w.s.len - key0 - u * 64 : 0;
+        edge |= lo[u] > 0 || hi[u] < 16;
       }
-      const bool in0 = qr >= lo && qr < hi, in1 = qr + 8 >= lo && qr + 8 < hi;
-      uint32_t pb[NT][2];
+      float c[kSl][NT][2][4] = {};
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int u = 0; u < kSl; ++u) {
+          uint32_t x[4];
+          ldsm4(x, kbase + s * C::kStage + (k >> 2) * C::kAtom + u * 64 * 128u + ((((k & 3) * 2 + khalf) ^ (krow & 7)) << 4));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) Mma<T>::mma(c[u][n][k & 1], x, q[n][k][0], q[n][k][1]);
+        }
+      bool in0[kSl], in1[kSl];
+#pragma unroll
+      for (int u = 0; u < kSl; ++u) {
+        in0[u] = qr >= lo[u] && qr < hi[u];
+        in1[u] = qr + 8 >= lo[u] && qr + 8 < hi[u];
+      }
+      uint32_t pb[kSl][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float x[4];
+        float x[kSl][4], mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = (c[n][0][e] + c[n][1][e]) * sl2;
-        if (a.stash) {
-          const int h = h0 - g * G + n * 8 + qc * 2;
-          float* z = a.stash + (((long long)w.b * a.kv.Hkv + g) * a.stash_keys + key0 + qr) * G + h;
-          if (in0 && h < G) z[0] = x[0];
-          if (in0 && h + 1 < G) z[1] = x[1];
-          if (in1 && h < G) z[8LL * G] = x[2];
-          if (in1 && h + 1 < G) z[8LL * G + 1] = x[3];
+        for (int u = 0; u < kSl; ++u) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][e] = (c[u][n][0][e] + c[u][n][1][e]) * sl2;
+          if (a.stash) {
+            const int h = h0 + n * 8 + qc * 2;
+            float* z = stash + (long long)(key0 + u * 64 + qr) * G + n * 8;
+            if (G % 2 == 0) {
+              if (in0[u] && h < h1) *reinterpret_cast<float2*>(z) = make_float2(x[u][0], x[u][1]);
+              if (in1[u] && h < h1) *reinterpret_cast<float2*>(z + 8 * G) = make_float2(x[u][2], x[u][3]);
+            } else {
+              if (in0[u] && h < h1) z[0] = x[u][0];
+              if (in0[u] && h + 1 < h1) z[1] = x[u][1];
+              if (in1[u] && h < h1) z[8 * G] = x[u][2];
+              if (in1[u] && h + 1 < h1) z[8 * G + 1] = x[u][3];
+            }
+          }
+          if (edge) {
+            if (!in0[u]) x[u][0] = x[u][1] = -INFINITY;
+            if (!in1[u]) x[u][2] = x[u][3] = -INFINITY;
+          }
+          mx0 = fmaxf(mx0, fmaxf(x[u][0], x[u][2]));
+          mx1 = fmaxf(mx1, fmaxf(x[u][1], x[u][3]));
         }
-        if (edge) {
-          if (!in0) x[0] = x[1] = -INFINITY;
-          if (!in1) x[2] = x[3] = -INFINITY;
-        }
-        float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
@@ -395,36 +494,45 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0], u1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-        x[0] = ex2(x[0] - u0);
-        x[1] = ex2(x[1] - u1);
-        x[2] = ex2(x[2] - u0);
-        x[3] = ex2(x[3] - u1);
-        l[n][0] += x[0] + x[2];
-        l[n][1] += x[1] + x[3];
-        pb[n][0] = transpose8(Mma<T>::pack(x[0], x[1]));
-        pb[n][1] = transpose8(Mma<T>::pack(x[2], x[3]));
+#pragma unroll
+        for (int u = 0; u < kSl; ++u) {
+          x[u][0] = ex2(x[u][0] - u0);
+          x[u][1] = ex2(x[u][1] - u1);
+          x[u][2] = ex2(x[u][2] - u0);
+          x[u][3] = ex2(x[u][3] - u1);
+          l[n][0] += x[u][0] + x[u][2];
+          l[n][1] += x[u][1] + x[u][3];
+          pb[u][n][0] = transpose8(Mma<T>::pack(x[u][0], x[u][1]));
+          pb[u][n][1] = transpose8(Mma<T>::pack(x[u][2], x[u][3]));
+        }
       }
       // V rows that are not visible may hold anything, NaN included: a weight
       // of 0 does not silence them, so their operand entries become 0.
-      const int k0 = qc * 2;
-      uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;
+      uint32_t z0[kSl], z1[kSl];
       if (edge) {
-        z0 = (k0 >= lo && k0 < hi ? 0xffffu : 0u) | (k0 + 1 >= lo && k0 + 1 < hi ? 0xffff0000u : 0u);
-        z1 = (k0 + 8 >= lo && k0 + 8 < hi ? 0xffffu : 0u) | (k0 + 9 >= lo && k0 + 9 < hi ? 0xffff0000u : 0u);
-      }
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        uint32_t x[4];
-        ldsm4_trans(x, vbase + s * C::kStage + (k >> 2) * (kTileKeys * 128u) + ((((k & 3) * 2 + vhalf) ^ (vrow & 7)) << 4));
-        if (edge) {
-          x[0] &= z0;
-          x[1] &= z0;
-          x[2] &= z1;
-          x[3] &= z1;
+        for (int u = 0; u < kSl; ++u) {
+          const int k0 = qc * 2;
+          z0[u] = (k0 >= lo[u] && k0 < hi[u] ? 0xffffu : 0u) | (k0 + 1 >= lo[u] && k0 + 1 < hi[u] ? 0xffff0000u : 0u);
+          z1[u] = (k0 + 8 >= lo[u] && k0 + 8 < hi[u] ? 0xffffu : 0u) | (k0 + 9 >= lo[u] && k0 + 9 < hi[u] ? 0xffff0000u : 0u);
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) Mma<T>::mma(o[n][k], x, pb[n][0], pb[n][1]);
       }
+#pragma unroll
+      for (int u = 0; u < kSl; ++u)
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t x[4];
+          ldsm4_trans(x, vbase + s * C::kStage + (k >> 2) * C::kAtom + u * 64 * 128u +
+                             ((((k & 3) * 2 + vhalf) ^ (vrow & 7)) << 4));
+          if (edge) {
+            x[0] &= z0[u];
+            x[1] &= z0[u];
+            x[2] &= z1[u];
+            x[3] &= z1[u];
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) Mma<T>::mma(o[n][k], x, pb[u][n][0], pb[u][n][1]);
+        }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->empty[s]);
@@ -528,80 +636,116 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// The parts [i0, i1] over which head h of (b, g) is cut, and its index in them.
-struct Cut {
-  int i0, i1, hh;
-  // Where part i left the head: its last unit if it is the unit's first part.
-  __device__ __forceinline__ long long at(int i) const { return ((long long)i * 2 + (i == i0 ? 1 : 0)) * 16 + hh; }
-};
-__device__ __forceinline__ Cut cut_of(const DecodeArgs& a, int g, int h, long long before, long long n, long long all,
-                                      int parts) {
-  const int G = a.Hq / a.kv.Hkv, per = a.unit_heads, chunks = (G + per - 1) / per, cols = a.kv.Hkv * chunks;
-  const int hc = h / per;
-  const long long total = all * cols, t0 = before * cols + (g * chunks + hc) * n;
-  parts = (int)min(total, (long long)parts);
-  return Cut{part_of(t0, total, parts), part_of(t0 + n - 1, total, parts), h - hc * per};
+// Last sequence b with prefix[b] * cols <= t, 32 samples a round (a whole warp).
+__device__ __forceinline__ int find_sequence(const DecodeArgs& a, int cols, long long t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+    const int k = __popc(__ballot_sync(0xffffffffu, at < hi && a.prefix[at] * cols <= t));
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// Where part i left head hh of a unit whose first part is i0: in the part's
+// last unit if that is where the unit starts, else in its first.
+__device__ __forceinline__ long long left_at(int i, int i0, int hh) {
+  return ((long long)i * 2 + (i == i0 ? 1 : 0)) * 16 + hh;
 }
 
 // What is left after the tiles, in one launch (each half needs only the decode
-// kernel): block r < B * Hq joins row r, the other blocks add the weights.
+// kernel): the first blocks join the units that were cut, the others add the
+// weights.
 //
-// Join: the parts of a unit that was cut, in order, relative to the largest
-// maximum: O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i; warps take every
-// fourth part.  Sequences without visible keys get O = 0, LSE = -inf.
+// Join.  Only the boundaries between two parts cut units, whatever the batch:
+// unit_heads / 4 blocks for each boundary.  The blocks of a unit's boundaries
+// share its heads: a block per head, its four warps taking every fourth part,
+// or, where there are fewer blocks than heads, a warp per head.
+//   O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, m = max_i m_i.
 template <typename T, int D>
-__device__ __forceinline__ void join_row(const DecodeArgs& a, int parts) {
+__device__ __forceinline__ void join(const DecodeArgs& a, int parts) {
   constexpr int E = D / 32;
   __shared__ float sl[4], so[4][D];
-  const long long row = blockIdx.x;
-  const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq, G = a.Hq / a.kv.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long before = a.prefix[b], n = a.prefix[b + 1] - before, all = a.prefix[a.B];
-  if (n == 0) {
-    for (int e = threadIdx.x; e < D; e += 128) static_cast<T*>(a.o)[row * D + e] = (T)0.f;
-    if (threadIdx.x == 0) a.lse[row] = -INFINITY;
-    return;
-  }
-  const Cut c = cut_of(a, hq / G, hq % G, before, n, all, parts);
-  if (c.i0 == c.i1) return;
+  const int G = a.Hq / a.kv.Hkv, per = a.unit_heads, chunks = (G + per - 1) / per, cols = a.kv.Hkv * chunks;
+  const int Y = per / 4, i = 1 + blockIdx.x / Y;
+  const long long total = a.prefix[a.B] * cols;
+  parts = (int)min(total, (long long)parts);
+  if (i >= parts) return;
+  const long long t = part_start(total, i, parts);
+  const int b = find_sequence(a, cols, t);
+  const long long before = a.prefix[b], n = a.prefix[b + 1] - before, in = t - before * cols;
+  const int col = (int)(in / n);
+  if (in == col * n) return;           // the boundary lies between two units
+  const long long u0 = before * cols + col * n;
+  const int i0 = part_of(u0, total, parts), i1 = part_of(u0 + n - 1, total, parts);
+  const int g = col / chunks, hc = col - g * chunks, heads = min(per, G - hc * per);
+  const int blocks = (i1 - i0) * Y, z = (i - i0 - 1) * Y + blockIdx.x % Y;
+  const bool alone = blocks < heads;   // a warp does a head alone
+  const int hh = alone ? z * 4 + warp : z, step = alone ? 1 : 4, from = i0 + (alone ? 0 : warp);
+  if (hh >= heads) return;             // alone: the warp; else the block
   float m = -INFINITY;
-  for (int i = c.i0 + lane; i <= c.i1; i += 32) m = fmaxf(m, a.part_ml[c.at(i)].x);
+  for (int x = i0 + lane; x <= i1; x += 32) m = fmaxf(m, a.part_ml[left_at(x, i0, hh)].x);
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   const float mu = m == -INFINITY ? 0.f : m;
   float l = 0.f, o[E] = {};
 #pragma unroll 4
-  for (int i = c.i0 + warp; i <= c.i1; i += 4) {
-    const float2 y = a.part_ml[c.at(i)];
+  for (int x = from; x <= i1; x += step) {
+    const long long at = left_at(x, i0, hh);
+    const float2 y = a.part_ml[at];
     const float f = ex2(y.x - mu);
-    const float* x = a.part + c.at(i) * D + lane * E;
-    l += f * y.y;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[e], o[e]);
+    const float* p = a.part + at * D + lane * E;
+    l = fmaf(f, y.y, l);
+    if constexpr (E == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      o[0] = fmaf(f, v.x, o[0]);
+      o[1] = fmaf(f, v.y, o[1]);
+      o[2] = fmaf(f, v.z, o[2]);
+      o[3] = fmaf(f, v.w, o[3]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(p);
+      o[0] = fmaf(f, v.x, o[0]);
+      o[1] = fmaf(f, v.y, o[1]);
+    }
   }
+  if (!alone) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-  if (lane == 0) sl[warp] = l;
-  __syncthreads();
-  l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+    if (lane == 0) sl[warp] = l;
+    __syncthreads();
+    if (warp > 0) return;
+    l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      o[e] = (so[0][lane * E + e] + so[1][lane * E + e]) + (so[2][lane * E + e] + so[3][lane * E + e]);
+  }
+  const long long row = (long long)b * a.Hq + g * G + hc * per + hh;
   const float inv = 1.f / l;
-  for (int e = threadIdx.x; e < D; e += 128)
-    static_cast<T*>(a.o)[row * D + e] = (T)(((so[0][e] + so[1][e]) + (so[2][e] + so[3][e])) * inv);
-  if (threadIdx.x == 0) a.lse[row] = (m + log2f(l)) * 0.69314718055994530942f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + row * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = Mma<T>::pack(o[e] * inv, o[e + 1] * inv);
+  if (lane == 0) a.lse[row] = (m + log2f(l)) * 0.69314718055994530942f;
 }
 
 // Log-sum-exp (log2 units) of head h of (b, g): the decode kernel's if the
 // unit was whole, else from its parts.
 __device__ __forceinline__ float head_lse2(const DecodeArgs& a, int b, int g, int h, long long before, long long n,
                                            long long all, int parts) {
-  const Cut c = cut_of(a, g, h, before, n, all, parts);
-  if (c.i0 == c.i1) return a.lse2[(long long)b * a.Hq + g * (a.Hq / a.kv.Hkv) + h];
+  const int G = a.Hq / a.kv.Hkv, per = a.unit_heads, chunks = (G + per - 1) / per, cols = a.kv.Hkv * chunks;
+  const int hc = h / per, hh = h - hc * per;
+  const long long total = all * cols, u0 = before * cols + (g * chunks + hc) * n;
+  parts = (int)min(total, (long long)parts);
+  const int i0 = part_of(u0, total, parts), i1 = part_of(u0 + n - 1, total, parts);
+  if (i0 == i1) return a.lse2[(long long)b * a.Hq + g * G + h];
   float m = -INFINITY, l = 0.f;
 #pragma unroll 4
-  for (int i = c.i0; i <= c.i1; ++i) m = fmaxf(m, a.part_ml[c.at(i)].x);
+  for (int i = i0; i <= i1; ++i) m = fmaxf(m, a.part_ml[left_at(i, i0, hh)].x);
   const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll 4
-  for (int i = c.i0; i <= c.i1; ++i) {
-    const float2 y = a.part_ml[c.at(i)];
+  for (int i = i0; i <= i1; ++i) {
+    const float2 y = a.part_ml[left_at(i, i0, hh)];
     l = fmaf(ex2(y.x - mu), y.y, l);
   }
   return m + log2f(l);
@@ -610,38 +754,34 @@ __device__ __forceinline__ float head_lse2(const DecodeArgs& a, int b, int g, in
 // Weights: adds each visible key's weight, summed over the group's heads from
 // the stashed scores (log2 units), to its accumulated weight.  Warps take
 // equal runs of the line of tiles (a kv head's keys once, whatever its head
-// chunks), two keys a lane.  A reduction at L2 rather than a load and a store,
+// chunks).  A reduction at L2 rather than a load and a store,
 // so that sequences sharing a page both count.
-__device__ __forceinline__ void add_weights(const DecodeArgs& a, int parts) {
+template <int kKeys>
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, int first, int parts) {
+  constexpr int kLane = kKeys / 32;    // keys a lane
   const int lane = threadIdx.x & 31;
-  const int first = a.B * a.Hq, warp = (blockIdx.x - first) * 4 + (threadIdx.x >> 5), warps = (gridDim.x - first) * 4;
+  const int warp = (blockIdx.x - first) * 4 + (threadIdx.x >> 5), warps = (gridDim.x - first) * 4;
   const int Hkv = a.kv.Hkv, G = a.Hq / Hkv;
   const long long all = a.prefix[a.B], total = all * Hkv;
   long long t = total * warp / warps;
   const long long end = total * (warp + 1) / warps;
   if (t >= end) return;
-  // Last sequence with prefix * Hkv <= t, 32 samples a round.
-  int lo = 0, hi = a.B;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-    const int k = __popc(__ballot_sync(0xffffffffu, at < hi && a.prefix[at] * Hkv <= t));
-    lo += k * step;
-    hi = min(hi, lo + step);
-  }
-  int b = lo;
-  Span s = span_of(a, b);
+  int b = find_sequence(a, Hkv, t);
+  Span s = span_of<kKeys>(a, b);
   long long before = a.prefix[b];
   int g = (int)((t - before * Hkv) / s.n), tile = (int)(t - before * Hkv - (long long)g * s.n);
   bool fresh = true;
   float lse2 = 0.f;
   for (; t < end; ++t) {
     // Lane h holds the LSE of head h (of the 32 heads at hand, for larger groups).
-    float w[2] = {0.f, 0.f};
-    int page[2] = {-1, -1};
-    long long slot[2] = {0, 0};
+    float w[kLane] = {};
+    int page[kLane];
+    int slot[kLane];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int key = (s.tile0 + tile) * kTileKeys + u * 32 + lane;
+    for (int u = 0; u < kLane; ++u) {
+      const int key = (s.tile0 + tile) * kKeys + u * 32 + lane;
+      page[u] = -1;
+      slot[u] = 0;
       if (key >= s.first && key < s.len) {
         const int c = key / a.kv.page_size;
         page[u] = a.table.pages[b * a.table.stride + c];
@@ -652,8 +792,8 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int parts) {
       if (fresh || G > 32) lse2 = h0 + lane < G ? head_lse2(a, b, g, h0 + lane, before, s.n, all, parts) : 0.f;
       const int nh = min(32, G - h0);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int key = (s.tile0 + tile) * kTileKeys + u * 32 + lane;
+      for (int u = 0; u < kLane; ++u) {
+        const int key = (s.tile0 + tile) * kKeys + u * 32 + lane;
         const bool in = key >= s.first && key < s.len;
         const float* x = a.stash + (((long long)b * Hkv + g) * a.stash_keys + key) * G + h0;
         if (G % 4 == 0) {
@@ -675,7 +815,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int parts) {
     }
     fresh = false;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kLane; ++u)
       if (page[u] >= 0 && page[u] < a.kv.num_pages)
         atomicAdd(&a.scores[((long long)page[u] * Hkv + g) * a.kv.page_size + slot[u]], w[u]);
     if (++tile == s.n && t + 1 < end) {
@@ -683,7 +823,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int parts) {
       fresh = true;
       if (++g == Hkv) {
         g = 0;
-        do s = span_of(a, ++b); while (s.n == 0 && b + 1 < a.B);
+        do s = span_of<kKeys>(a, ++b); while (s.n == 0 && b + 1 < a.B);
         before = a.prefix[b];
       }
     }
@@ -691,10 +831,10 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int parts) {
 }
 
 template <typename T, int D, bool kScores>
-__global__ void __launch_bounds__(128) fa_paged_finish_kernel(const DecodeArgs a, int parts) {
+__global__ void __launch_bounds__(128) fa_paged_finish_kernel(const DecodeArgs a, int joins, int parts) {
   wait_for_previous();
-  if (!kScores || blockIdx.x < a.B * a.Hq) join_row<T, D>(a, parts);
-  else add_weights(a, parts);
+  if (!kScores || blockIdx.x < joins) join<T, D>(a, parts);
+  else add_weights<Cfg<D>::kKeys>(a, joins, parts);
 }
 
 // A launch whose blocks may start before the kernel in front of it is done
@@ -720,17 +860,20 @@ cudaError_t launch_decode(const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs
   else fa_paged_decode_kernel<T, D, 2><<<parts, kThreads, Cfg<D>::kBytes, stream>>>(tk, tv, a, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)a.B * a.Hq;
-  if (!a.scores) return launch_after(fa_paged_finish_kernel<T, D, false>, (unsigned)rows, 128, stream, a, parts);
-  // For the weights 16 tiles a block, up to 4 blocks an SM.
-  const long long tiles = (a.stash_keys + kTileKeys - 1) / kTileKeys * a.B * a.kv.Hkv;
-  const long long blocks = (tiles + 15) / 16 < 4LL * num_sms ? (tiles + 15) / 16 : 4LL * num_sms;
-  return launch_after(fa_paged_finish_kernel<T, D, true>, (unsigned)(rows + blocks), 128, stream, a, parts);
+  const int joins = (parts - 1) * (a.unit_heads / 4);
+  if (!a.scores)
+    return joins == 0 ? cudaSuccess
+                      : launch_after(fa_paged_finish_kernel<T, D, false>, joins, 128, stream, a, joins, parts);
+  // For the weights 1024 keys a block, up to 4 blocks an SM.
+  const long long blocks = (a.stash_keys * a.B * a.kv.Hkv + 1023) / 1024, most = 4LL * num_sms;
+  return launch_after(fa_paged_finish_kernel<T, D, true>, (unsigned)(joins + (blocks < most ? blocks : most)), 128, stream,
+                      a, joins, parts);
 }
 
 template <typename T, int D>
 cudaError_t configure_decode() {
   static_assert(Cfg<D>::kBytes <= 115712, "two CTAs per SM");
+  static_assert(Cfg<D>::kKeys == decode_tile_keys(D), "tile");
   cudaError_t e = cudaFuncSetAttribute(fa_paged_decode_kernel<T, D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D>::kBytes);
   if (e == cudaSuccess)
