@@ -890,16 +890,16 @@ fa_status tmap_pool(fa::TmaMap4* m, const fa_paged_kv* kv, const void* base) {
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_LAUNCH;
 }
 
-// Decode workspace: tiles before each sequence, the parts of cut units with
-// their (max, sum), and, with scores, the LSE and every key's scores.
+// Decode workspace: the CTAs' parts, what they left of cut units with its
+// (max, sum), and, with scores, the LSE and every key's scores.
 struct DecodeWs {
-  size_t prefix, part, ml, lse2, stash, total;
+  size_t parts, part, ml, lse2, stash, total;
 };
 DecodeWs decode_ws(int B, int Hq, int d, int page_size, int max_pages, bool with_scores) {
   DecodeWs w{};
   const size_t slots = (size_t)fa::kDecodeMaxParts * 2 * 16;
-  w.prefix = 0;
-  w.part = align256((size_t)(B + 1) * 8);
+  w.parts = 0;
+  w.part = align256((size_t)fa::kDecodeMaxParts * sizeof(fa::DecodePart));
   w.ml = w.part + slots * d * 4;
   w.lse2 = w.ml + slots * 8;
   w.stash = w.lse2 + (with_scores ? align256((size_t)B * Hq * 4) : 0);
@@ -1086,7 +1086,7 @@ fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_pa
   a.unit_heads = G <= 8 ? 8 : 16;
   const DecodeWs w = decode_ws(B, Hq, kv->d, kv->page_size, table->max_pages, scores != nullptr);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.prefix = reinterpret_cast<long long*>(ws + w.prefix);
+  a.parts = reinterpret_cast<fa::DecodePart*>(ws + w.parts);
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.lse2 = scores ? reinterpret_cast<float*>(ws + w.lse2) : nullptr;
@@ -1100,7 +1100,7 @@ fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_pa
   fa::TmaMap4 tk, tv;
   FA_TRY(tmap_pool(&tk, kv, kv->k));
   FA_TRY(tmap_pool(&tv, kv, kv->v));
-  return launch_status(fa::launch_paged_decode(kv->dtype, tk, tv, a, dev_status(ds), parts, ds->num_sms,
+  return launch_status(fa::launch_paged_decode(kv->dtype, tk, tv, a, dev_status(ds), parts,
                                                static_cast<cudaStream_t>(stream)));
 }
 

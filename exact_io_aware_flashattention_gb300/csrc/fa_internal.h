@@ -133,6 +133,13 @@ struct AppendArgs {
 cudaError_t launch_rope(int dtype, const RopeArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream);
 cudaError_t launch_append(int dtype, const AppendArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream);
 
+// What a CTA of the decode kernel worked on: `left` tiles (decode_tile_keys
+// keys each) from `tile` of unit (b, col) on.  The first unit is spread over
+// the CTAs i0 .. i1, the last one (if it is another) over this one .. last_i1.
+struct DecodePart {
+  int b, col, tile, left, i0, i1, last_i1, pad;
+};
+
 struct DecodeArgs {
   const void* q;             // (b, h) at b * q_sb + h * q_sh elements
   long long q_sb, q_sh;
@@ -146,7 +153,7 @@ struct DecodeArgs {
   float scale_log2;
   int unit_heads;            // query heads of a kv group that share a unit: 8 or 16
   // Workspace
-  long long* prefix;         // [B + 1] tiles of the sequences before b (decode_tile_keys keys each)
+  DecodePart* parts;         // [kDecodeMaxParts]
   float* part;               // [kDecodeMaxParts][2][16][d] unnormalised O of units cut over CTAs
   float2* part_ml;           // [kDecodeMaxParts][2][16] their maximum (log2 units) and sum
   float* lse2;               // [B, Hq] log-sum-exp in log2 units (with scores)
@@ -159,7 +166,7 @@ constexpr int decode_tile_keys(int d) { return d == 64 ? 128 : 64; }
 
 // `tk`, `tv` view the pools as {d, page_size, Hkv, num_pages}; `parts` CTAs.
 cudaError_t launch_paged_decode(int dtype, const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs& a, const DevStatus& st,
-                                int parts, int num_sms, cudaStream_t stream);
+                                int parts, cudaStream_t stream);
 
 struct EvictArgs {
   PagedKv kv;

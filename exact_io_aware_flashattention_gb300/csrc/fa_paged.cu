@@ -129,14 +129,18 @@ struct Span {
   int len, first, tile0, n;
 };
 template <int kKeys>
-__device__ __forceinline__ Span span_of(const DecodeArgs& a, int b) {
+__device__ __forceinline__ Span span_of_len(const DecodeArgs& a, int len) {
   Span s;
-  s.len = a.seq_lens[b];
+  s.len = len;
   if (s.len < 0 || s.len > (long long)a.table.cols * a.kv.page_size) s.len = -1;   // recorded by the caller
   s.first = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
   s.tile0 = s.first / kKeys;
   s.n = s.len > 0 ? (s.len - 1) / kKeys - s.tile0 + 1 : 0;
   return s;
+}
+template <int kKeys>
+__device__ __forceinline__ Span span_of(const DecodeArgs& a, int b) {
+  return span_of_len<kKeys>(a, a.seq_lens[b]);
 }
 
 // The line of `total` tiles is cut into min(total, CTAs) parts: none is empty.
@@ -213,6 +217,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int* abort_flag = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
+  // On its way while the barriers are set up.
+  const int first_len = (int)threadIdx.x < a.B ? a.seq_lens[threadIdx.x] : 0;
   if ((smem_u32(smem) & 1023u) != 0) {
     if (threadIdx.x == 0) record_error(st, kErrDeviceTimeout, 0);
     return;
@@ -229,8 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   const int G = a.Hq / a.kv.Hkv, chunks = (G + 8 * NT - 1) / (8 * NT), cols = a.kv.Hkv * chunks;
 
-  // The line: tiles before each sequence (per column; CTA 0 keeps the list for
-  // the join), the total, and this CTA's first sequence.
+  // The line: its length, and this CTA's first sequence.
   long long total = 0;
   for (int round = 0; round < 2; ++round) {
     // Round 0 finds the total; round 1, for batches of more than one block's
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int b = base + threadIdx.x;
       Span s{};
       if (b < a.B) {
-        s = span_of<C::kKeys>(a, b);
+        s = span_of_len<C::kKeys>(a, base == 0 ? first_len : a.seq_lens[b]);
         if (s.len < 0 && round == 0 && blockIdx.x == 0) record_error(st, kErrBadIndex, kSiteDecodeLen);
       }
       int x = s.n;
@@ -256,7 +261,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (w < warp) pre += bars->scan[w];
         before += bars->scan[w];
       }
-      if (round == 0 && blockIdx.x == 0 && b < a.B) a.prefix[b] = pre;
       const bool last = base + kThreads >= a.B;
       if (round == 0 && last) total = before * cols;
       const int parts = (int)min(total, (long long)gridDim.x);
@@ -266,12 +270,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         bars->before = pre * cols;
       }
     }
-    if (round == 0 && blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.B] = before;
     if (a.B <= kThreads) break;
   }
   __syncthreads();
   const int parts = (int)min(total, (long long)gridDim.x);
   if ((int)blockIdx.x >= parts) {
+    if (threadIdx.x == 0) a.parts[blockIdx.x].left = 0;
     if (warp == kConsumers) fill_empty<T, D>(a);
     return;
   }
@@ -307,6 +311,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       return have;
     };
+    DecodePart part{};
+    part.b = w.b;
+    part.col = w.col;
+    part.tile = w.tile;
+    part.left = (int)w.left;
+    const int first_n = w.s.n;
     int it = 0, page, slot, have = look_up(w, page, slot);
     bool good = true;
     while (good && w.left > 0) {
@@ -345,6 +355,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       page = page_next;
       slot = slot_next;
       have = have_next;
+    }
+    if (lane == 0) {
+      DecodePart d = part;
+      const long long u0 = t0 - d.tile;
+      d.i0 = part_of(u0, total, parts);
+      d.i1 = part_of(u0 + first_n - 1, total, parts);
+      d.last_i1 = good && w.tile < w.s.n ? part_of(t1 - 1 + (w.s.n - w.tile), total, parts) : blockIdx.x;
+      a.parts[blockIdx.x] = d;
     }
     fill_empty<T, D>(a);
     // Every copy issued must have landed before the CTA may exit.
@@ -636,59 +654,35 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Last sequence b with prefix[b] * cols <= t, 32 samples a round (a whole warp).
-__device__ __forceinline__ int find_sequence(const DecodeArgs& a, int cols, long long t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = a.B;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-    const int k = __popc(__ballot_sync(0xffffffffu, at < hi && a.prefix[at] * cols <= t));
-    lo += k * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
 // Where part i left head hh of a unit whose first part is i0: in the part's
 // last unit if that is where the unit starts, else in its first.
 __device__ __forceinline__ long long left_at(int i, int i0, int hh) {
   return ((long long)i * 2 + (i == i0 ? 1 : 0)) * 16 + hh;
 }
 
-// What is left after the tiles, in one launch (each half needs only the decode
-// kernel): the first blocks join the units that were cut, the others add the
-// weights.
-//
-// Join.  Only the boundaries between two parts cut units, whatever the batch:
+// Joins the units that were cut:
+//   O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, m = max_i m_i.
+// Only the boundaries between two parts cut units, whatever the batch:
 // unit_heads / 4 blocks for each boundary.  The blocks of a unit's boundaries
 // share its heads: a block per head, its four warps taking every fourth part,
 // or, where there are fewer blocks than heads, a warp per head.
-//   O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, m = max_i m_i.
 template <typename T, int D>
-__device__ __forceinline__ void join(const DecodeArgs& a, int parts) {
+__device__ __forceinline__ void join(const DecodeArgs& a) {
   constexpr int E = D / 32;
   __shared__ float sl[4], so[4][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.Hq / a.kv.Hkv, per = a.unit_heads, chunks = (G + per - 1) / per, cols = a.kv.Hkv * chunks;
-  const int Y = per / 4, i = 1 + blockIdx.x / Y;
-  const long long total = a.prefix[a.B] * cols;
-  parts = (int)min(total, (long long)parts);
-  if (i >= parts) return;
-  const long long t = part_start(total, i, parts);
-  const int b = find_sequence(a, cols, t);
-  const long long before = a.prefix[b], n = a.prefix[b + 1] - before, in = t - before * cols;
-  const int col = (int)(in / n);
-  if (in == col * n) return;           // the boundary lies between two units
-  const long long u0 = before * cols + col * n;
-  const int i0 = part_of(u0, total, parts), i1 = part_of(u0 + n - 1, total, parts);
-  const int g = col / chunks, hc = col - g * chunks, heads = min(per, G - hc * per);
-  const int blocks = (i1 - i0) * Y, z = (i - i0 - 1) * Y + blockIdx.x % Y;
+  const int Y = a.unit_heads / 4, i = 1 + blockIdx.x / Y;
+  const DecodePart d = a.parts[i];
+  if (d.left == 0 || d.tile == 0) return;    // no such part, or it starts with a unit
+  const int G = a.Hq / a.kv.Hkv, per = a.unit_heads, chunks = (G + per - 1) / per;
+  const int g = d.col / chunks, hc = d.col - g * chunks, heads = min(per, G - hc * per);
+  const int i0 = d.i0, i1 = d.i1, blocks = (i1 - i0) * Y, z = (i - i0 - 1) * Y + blockIdx.x % Y;
   const bool alone = blocks < heads;   // a warp does a head alone
   const int hh = alone ? z * 4 + warp : z, step = alone ? 1 : 4, from = i0 + (alone ? 0 : warp);
   if (hh >= heads) return;             // alone: the warp; else the block
   float m = -INFINITY;
   for (int x = i0 + lane; x <= i1; x += 32) m = fmaxf(m, a.part_ml[left_at(x, i0, hh)].x);
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
   const float mu = m == -INFINITY ? 0.f : m;
   float l = 0.f, o[E] = {};
 #pragma unroll 4
@@ -721,94 +715,111 @@ __device__ __forceinline__ void join(const DecodeArgs& a, int parts) {
     for (int e = 0; e < E; ++e)
       o[e] = (so[0][lane * E + e] + so[1][lane * E + e]) + (so[2][lane * E + e] + so[3][lane * E + e]);
   }
-  const long long row = (long long)b * a.Hq + g * G + hc * per + hh;
+  const long long row = (long long)d.b * a.Hq + g * G + hc * per + hh;
   const float inv = 1.f / l;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + row * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = Mma<T>::pack(o[e] * inv, o[e + 1] * inv);
-  if (lane == 0) a.lse[row] = (m + log2f(l)) * 0.69314718055994530942f;
-}
-
-// Log-sum-exp (log2 units) of head h of (b, g): the decode kernel's if the
-// unit was whole, else from its parts.
-__device__ __forceinline__ float head_lse2(const DecodeArgs& a, int b, int g, int h, long long before, long long n,
-                                           long long all, int parts) {
-  const int G = a.Hq / a.kv.Hkv, per = a.unit_heads, chunks = (G + per - 1) / per, cols = a.kv.Hkv * chunks;
-  const int hc = h / per, hh = h - hc * per;
-  const long long total = all * cols, u0 = before * cols + (g * chunks + hc) * n;
-  parts = (int)min(total, (long long)parts);
-  const int i0 = part_of(u0, total, parts), i1 = part_of(u0 + n - 1, total, parts);
-  if (i0 == i1) return a.lse2[(long long)b * a.Hq + g * G + h];
-  float m = -INFINITY, l = 0.f;
-#pragma unroll 4
-  for (int i = i0; i <= i1; ++i) m = fmaxf(m, a.part_ml[left_at(i, i0, hh)].x);
-  const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-  for (int i = i0; i <= i1; ++i) {
-    const float2 y = a.part_ml[left_at(i, i0, hh)];
-    l = fmaf(ex2(y.x - mu), y.y, l);
+  if (lane == 0) {
+    const float lse2 = m + log2f(l);
+    a.lse[row] = lse2 * 0.69314718055994530942f;
+    if (a.lse2) a.lse2[row] = lse2;
   }
-  return m + log2f(l);
 }
 
-// Weights: adds each visible key's weight, summed over the group's heads from
-// the stashed scores (log2 units), to its accumulated weight.  Warps take
-// equal runs of the line of tiles (a kv head's keys once, whatever its head
-// chunks).  A reduction at L2 rather than a load and a store,
-// so that sequences sharing a page both count.
-template <int kKeys>
-__device__ __forceinline__ void add_weights(const DecodeArgs& a, int first, int parts) {
+// Adds each visible key's weight, summed over the group's heads from the
+// stashed scores (log2 units), to its accumulated weight.  kSplit blocks take
+// the tiles of a part in turn, a warp a tile.  With several head chunks to a
+// kv head its keys are taken once, with the first chunk's tiles.  A reduction
+// at L2 rather than a load and a store, so that sequences sharing a page both
+// count.
+// kJoined: every LSE is there; else those of cut units come from their parts.
+constexpr int kSplit = 2;
+template <int kKeys, bool kJoined>
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, int block) {
   constexpr int kLane = kKeys / 32;    // keys a lane
-  const int lane = threadIdx.x & 31;
-  const int warp = (blockIdx.x - first) * 4 + (threadIdx.x >> 5), warps = (gridDim.x - first) * 4;
-  const int Hkv = a.kv.Hkv, G = a.Hq / Hkv;
-  const long long all = a.prefix[a.B], total = all * Hkv;
-  long long t = total * warp / warps;
-  const long long end = total * (warp + 1) / warps;
-  if (t >= end) return;
-  int b = find_sequence(a, Hkv, t);
-  Span s = span_of<kKeys>(a, b);
-  long long before = a.prefix[b];
-  int g = (int)((t - before * Hkv) / s.n), tile = (int)(t - before * Hkv - (long long)g * s.n);
+  const int lane = threadIdx.x & 31, i = block / kSplit;
+  int skip = (block % kSplit) * 4 + (threadIdx.x >> 5);
+  const DecodePart d = a.parts[i];
+  if (d.left <= skip) return;
+  const int Hkv = a.kv.Hkv, G = a.Hq / Hkv, chunks = (G + a.unit_heads - 1) / a.unit_heads, cols = Hkv * chunks;
+  Walk<kKeys> w;
+  w.b = d.b;
+  w.col = d.col;
+  w.tile = d.tile;
+  w.left = d.left;
+  w.s = span_of<kKeys>(a, d.b);
+  int i0 = d.i0, i1 = d.i1;            // parts of the unit
   bool fresh = true;
   float lse2 = 0.f;
-  for (; t < end; ++t) {
-    // Lane h holds the LSE of head h (of the 32 heads at hand, for larger groups).
-    float w[kLane] = {};
-    int page[kLane];
-    int slot[kLane];
+  for (;;) {
+    // `skip` tiles on, unit by unit.
+    while (skip >= w.s.n - w.tile) {
+      const int n = w.s.n - w.tile;
+      if (w.left <= n) return;
+      skip -= n;
+      w.left -= n;
+      w.next_unit(a, cols);
+      if (w.left <= 0) return;
+      i0 = i;
+      i1 = w.s.n > w.left ? d.last_i1 : i;
+      fresh = true;
+    }
+    w.tile += skip;
+    w.left -= skip;
+    if (w.left <= 0) return;
+    skip = 4 * kSplit;
+    const int g = w.col / chunks;
+    if (w.col != g * chunks) continue;
+    float sum[kLane] = {};
+    int page[kLane], slot[kLane];
 #pragma unroll
     for (int u = 0; u < kLane; ++u) {
-      const int key = (s.tile0 + tile) * kKeys + u * 32 + lane;
+      const int key = (w.s.tile0 + w.tile) * kKeys + u * 32 + lane;
       page[u] = -1;
       slot[u] = 0;
-      if (key >= s.first && key < s.len) {
+      if (key >= w.s.first && key < w.s.len) {
         const int c = key / a.kv.page_size;
-        page[u] = a.table.pages[b * a.table.stride + c];
+        page[u] = a.table.pages[w.b * a.table.stride + c];
         slot[u] = key - c * a.kv.page_size;
       }
     }
     for (int h0 = 0; h0 < G; h0 += 32) {
-      if (fresh || G > 32) lse2 = h0 + lane < G ? head_lse2(a, b, g, h0 + lane, before, s.n, all, parts) : 0.f;
       const int nh = min(32, G - h0);
+      if (fresh || G > 32) {           // lane h holds the LSE of head h0 + h
+        if (lane < nh && (kJoined || i0 == i1)) {
+          lse2 = a.lse2[(long long)w.b * a.Hq + g * G + h0 + lane];
+        } else if (lane < nh) {
+          float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+          for (int x = i0; x <= i1; ++x) m = fmaxf(m, a.part_ml[left_at(x, i0, h0 + lane)].x);
+          const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+          for (int x = i0; x <= i1; ++x) {
+            const float2 y = a.part_ml[left_at(x, i0, h0 + lane)];
+            l = fmaf(ex2(y.x - mu), y.y, l);
+          }
+          lse2 = m + log2f(l);
+        }
+      }
 #pragma unroll
       for (int u = 0; u < kLane; ++u) {
-        const int key = (s.tile0 + tile) * kKeys + u * 32 + lane;
-        const bool in = key >= s.first && key < s.len;
-        const float* x = a.stash + (((long long)b * Hkv + g) * a.stash_keys + key) * G + h0;
+        const int key = (w.s.tile0 + w.tile) * kKeys + u * 32 + lane;
+        const bool in = key >= w.s.first && key < w.s.len;
+        const float* x = a.stash + (((long long)w.b * Hkv + g) * a.stash_keys + key) * G + h0;
         if (G % 4 == 0) {
           for (int h = 0; h < nh; h += 4) {
             const float l0 = __shfl_sync(0xffffffffu, lse2, h), l1 = __shfl_sync(0xffffffffu, lse2, h + 1);
             const float l2 = __shfl_sync(0xffffffffu, lse2, h + 2), l3 = __shfl_sync(0xffffffffu, lse2, h + 3);
             if (in) {
               const float4 y = *reinterpret_cast<const float4*>(x + h);
-              w[u] += (ex2(y.x - l0) + ex2(y.y - l1)) + (ex2(y.z - l2) + ex2(y.w - l3));
+              sum[u] += (ex2(y.x - l0) + ex2(y.y - l1)) + (ex2(y.z - l2) + ex2(y.w - l3));
             }
           }
         } else {
           for (int h = 0; h < nh; ++h) {
             const float l = __shfl_sync(0xffffffffu, lse2, h);
-            if (in) w[u] += ex2(x[h] - l);
+            if (in) sum[u] += ex2(x[h] - l);
           }
         }
       }
@@ -817,24 +828,26 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int first, int 
 #pragma unroll
     for (int u = 0; u < kLane; ++u)
       if (page[u] >= 0 && page[u] < a.kv.num_pages)
-        atomicAdd(&a.scores[((long long)page[u] * Hkv + g) * a.kv.page_size + slot[u]], w[u]);
-    if (++tile == s.n && t + 1 < end) {
-      tile = 0;
-      fresh = true;
-      if (++g == Hkv) {
-        g = 0;
-        do s = span_of<kKeys>(a, ++b); while (s.n == 0 && b + 1 < a.B);
-        before = a.prefix[b];
-      }
-    }
+        atomicAdd(&a.scores[((long long)page[u] * Hkv + g) * a.kv.page_size + slot[u]], sum[u]);
   }
 }
 
+// What is left after the tiles: the first blocks join, the others (with
+// scores) add the weights; neither half needs the other.
 template <typename T, int D, bool kScores>
-__global__ void __launch_bounds__(128) fa_paged_finish_kernel(const DecodeArgs a, int joins, int parts) {
+__global__ void __launch_bounds__(128) fa_paged_finish_kernel(const DecodeArgs a, int joins) {
+  launch_dependents();
   wait_for_previous();
-  if (!kScores || blockIdx.x < joins) join<T, D>(a, parts);
-  else add_weights<Cfg<D>::kKeys>(a, joins, parts);
+  if (!kScores || blockIdx.x < joins) join<T, D>(a);
+  else add_weights<Cfg<D>::kKeys, false>(a, blockIdx.x - joins);
+}
+
+// The weights after every join: where a kv head's units are several, a cut
+// one's parts are not known to the others.
+template <int kKeys>
+__global__ void __launch_bounds__(128) fa_paged_weights_kernel(const DecodeArgs a) {
+  wait_for_previous();
+  add_weights<kKeys, true>(a, blockIdx.x);
 }
 
 // A launch whose blocks may start before the kernel in front of it is done
@@ -855,19 +868,17 @@ cudaError_t launch_after(void (*k)(P...), dim3 grid, dim3 block, cudaStream_t st
 
 template <typename T, int D>
 cudaError_t launch_decode(const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs& a, const DevStatus& st, int parts,
-                          int num_sms, cudaStream_t stream) {
+                          cudaStream_t stream) {
   if (a.unit_heads == 8) fa_paged_decode_kernel<T, D, 1><<<parts, kThreads, Cfg<D>::kBytes, stream>>>(tk, tv, a, st);
   else fa_paged_decode_kernel<T, D, 2><<<parts, kThreads, Cfg<D>::kBytes, stream>>>(tk, tv, a, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int joins = (parts - 1) * (a.unit_heads / 4);
-  if (!a.scores)
-    return joins == 0 ? cudaSuccess
-                      : launch_after(fa_paged_finish_kernel<T, D, false>, joins, 128, stream, a, joins, parts);
-  // For the weights 1024 keys a block, up to 4 blocks an SM.
-  const long long blocks = (a.stash_keys * a.B * a.kv.Hkv + 1023) / 1024, most = 4LL * num_sms;
-  return launch_after(fa_paged_finish_kernel<T, D, true>, (unsigned)(joins + (blocks < most ? blocks : most)), 128, stream,
-                      a, joins, parts);
+  const int joins = (parts - 1) * (a.unit_heads / 4), adds = parts * kSplit;
+  if (a.scores && a.Hq / a.kv.Hkv <= a.unit_heads)
+    return launch_after(fa_paged_finish_kernel<T, D, true>, joins + adds, 128, stream, a, joins);
+  if (joins > 0) e = launch_after(fa_paged_finish_kernel<T, D, false>, joins, 128, stream, a, joins);
+  if (e == cudaSuccess && a.scores) e = launch_after(fa_paged_weights_kernel<Cfg<D>::kKeys>, adds, 128, stream, a);
+  return e;
 }
 
 template <typename T, int D>
@@ -892,12 +903,12 @@ cudaError_t configure_paged_kernels() {
 }
 
 cudaError_t launch_paged_decode(int dtype, const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs& a, const DevStatus& st,
-                                int parts, int num_sms, cudaStream_t stream) {
+                                int parts, cudaStream_t stream) {
   if (dtype == 0)
-    return a.kv.d == 64 ? launch_decode<__nv_bfloat16, 64>(tk, tv, a, st, parts, num_sms, stream)
-                        : launch_decode<__nv_bfloat16, 128>(tk, tv, a, st, parts, num_sms, stream);
-  return a.kv.d == 64 ? launch_decode<__half, 64>(tk, tv, a, st, parts, num_sms, stream)
-                      : launch_decode<__half, 128>(tk, tv, a, st, parts, num_sms, stream);
+    return a.kv.d == 64 ? launch_decode<__nv_bfloat16, 64>(tk, tv, a, st, parts, stream)
+                        : launch_decode<__nv_bfloat16, 128>(tk, tv, a, st, parts, stream);
+  return a.kv.d == 64 ? launch_decode<__half, 64>(tk, tv, a, st, parts, stream)
+                      : launch_decode<__half, 128>(tk, tv, a, st, parts, stream);
 }
 
 }  // namespace fa
