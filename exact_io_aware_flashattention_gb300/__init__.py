@@ -21,6 +21,7 @@ raises ``FAError``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -412,10 +413,14 @@ def _check_view(t, name, shape, dtype, dev):
 
 
 def _check_dense(t, name, shape, dtype, dev):
-    p = _check_view(t, name, shape, dtype, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return p
+    """Address of a contiguous tensor."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _check_view(t, name, shape, dtype, dev)
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _first(t, name, dims, what):
@@ -437,21 +442,26 @@ def _first(t, name, dims, what):
     return t.shape, t.get_device(), code
 
 
-def _on(dev, stream, call):
-    """``call(raw stream handle)`` with device ``dev`` current, on its current
-    stream or on ``stream``.  What the call allocates belongs to that stream, so
-    that the caching allocator does not hand a workspace on to another stream
-    while the kernels still use it."""
+def _raw_stream(dev, stream):
+    """Handle of device ``dev``'s current stream if that device is current and no
+    other stream is asked for, else None: the call is then made again inside
+    ``_on``, so that what it allocates belongs to the stream it runs on (the
+    caching allocator would else hand a workspace on to another stream while the
+    kernels still use it)."""
+    from torch import _C
+    if stream is None and dev == _C._cuda_getDevice():
+        return _C._cuda_getCurrentRawStream(dev)
+    return None
+
+
+@contextlib.contextmanager
+def _on(dev, stream):
+    """Device ``dev`` and ``stream`` (None: the device's current stream) made current."""
     import torch
-    if stream is None and dev == torch._C._cuda_getDevice():
-        return call(torch._C._cuda_getCurrentRawStream(dev))
     if stream is not None and stream.device.index != dev:
         raise ValueError(f"stream of {stream.device}, tensors on cuda:{dev}")
-    with torch.cuda.device(dev):
-        if stream is None:
-            return call(torch.cuda.current_stream(dev).cuda_stream)
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        yield
 
 
 def _rotary(positions, inv_freq, axes, interleaved, d, lead, dev):
@@ -497,23 +507,23 @@ def _rope(q, k, positions, inv_freq, axes, interleaved, inverse, q_out, k_out, s
     elif k_out is not None:
         raise ValueError("k_out without k")
     rot = _rotary(positions, inv_freq, axes, interleaved, d, (B, N), dev)
-
-    def call(handle):
-        qo, ko = q_out, k_out
-        if qo is None:
-            qo = torch.empty((B, Hq, N, d), dtype=dt, device=q.device)
-        op = _check_view(qo, "q_out", (B, Hq, N, d), dt, dev)
-        okp, oks = None, None
-        if k is not None:
-            if ko is None:
-                ko = torch.empty((B, Hk, N, d), dtype=dt, device=q.device)
-            okp, oks = _check_view(ko, "k_out", (B, Hk, N, d), dt, dev), _pack3(*ko.stride()[:3])
-        status = fa_rope(qp, _pack3(*q.stride()[:3]), op, _pack3(*qo.stride()[:3]), kp, ks, okp, oks, B, Hq, Hk, N, d, code,
-                         rot, inverse, handle)
-        if status:
-            _raise(status, "fa_rope")
-        return qo if k is None else (qo, ko)
-    return _on(dev, stream, call)
+    handle = _raw_stream(dev, stream)
+    if handle is None:
+        with _on(dev, stream):
+            return _rope(q, k, positions, inv_freq, axes, interleaved, inverse, q_out, k_out, None)
+    if q_out is None:
+        q_out = torch.empty((B, Hq, N, d), dtype=dt, device=q.device)
+    op = _check_view(q_out, "q_out", (B, Hq, N, d), dt, dev)
+    okp, oks = None, None
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty((B, Hk, N, d), dtype=dt, device=q.device)
+        okp, oks = _check_view(k_out, "k_out", (B, Hk, N, d), dt, dev), _pack3(*k_out.stride()[:3])
+    status = fa_rope(qp, _pack3(*q.stride()[:3]), op, _pack3(*q_out.stride()[:3]), kp, ks, okp, oks, B, Hq, Hk, N, d, code,
+                     rot, inverse, handle)
+    if status:
+        _raise(status, "fa_rope")
+    return q_out if k is None else (q_out, k_out)
 
 
 def rope(q, k, positions, inv_freq, axes, interleaved: bool = False, q_out=None, k_out=None, stream=None):
@@ -588,19 +598,22 @@ def paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens=None,
     elif q_out is not None:
         raise ValueError("q_out without q")
 
-    def call(handle):
-        qo, op, os_ = q_out, None, None
-        if q is not None:
-            if qo is None:
-                qo = torch.empty((T, Hq, d), dtype=dt, device=q.device)
-            op, os_ = _check_view(qo, "q_out", (T, Hq, d), dt, dev), _pack2(*qo.stride()[:2])
-        if T:
-            status = fa_paged_append(kv, table, lens, cu, B, T, kp, _pack2(*k.stride()[:2]), vp, _pack2(*v.stride()[:2]), qp,
-                                     qs, op, os_, Hq, rot, sp, handle)
-            if status:
-                _raise(status, "fa_paged_append")
-        return qo
-    return _on(dev, stream, call)
+    handle = _raw_stream(dev, stream)
+    if handle is None:
+        with _on(dev, stream):
+            return paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens, q, positions, inv_freq, axes,
+                                interleaved, scores, q_out)
+    op, os_ = None, None
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+        op, os_ = _check_view(q_out, "q_out", (T, Hq, d), dt, dev), _pack2(*q_out.stride()[:2])
+    if T:
+        status = fa_paged_append(kv, table, lens, cu, B, T, kp, _pack2(*k.stride()[:2]), vp, _pack2(*v.stride()[:2]), qp, qs,
+                                 op, os_, Hq, rot, sp, handle)
+        if status:
+            _raise(status, "fa_paged_append")
+    return q_out
 
 
 # A size is a pure function of the shapes; a decoding loop asks for the same one every step.
@@ -632,23 +645,23 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float | None
     if scale is None:
         scale = 1.0 / math.sqrt(d)
 
-    def call(handle):
-        o, l, ws = out, lse, workspace
-        if o is None:
-            o = torch.empty((B, Hq, d), dtype=dt, device=k_cache.device)
-        if l is None:
-            l = torch.empty((B, Hq), dtype=torch.float32, device=k_cache.device)
-        if ws is None:
-            ws = paged_decode_workspace(B, Hq, k_cache, block_table, scores is not None)
-        op = _check_dense(o, "out", (B, Hq, d), dt, dev)
-        lp = _check_dense(l, "lse", (B, Hq), torch.float32, dev)
-        n = ws.numel()
-        status = fa_paged_decode(qp, _pack2(*q.stride()[:2]), kv, table, lens, op, lp, sp, B, Hq, window, scale,
-                                 _check_dense(ws, "workspace", (n,), torch.uint8, dev), n, handle)
-        if status:
-            _raise(status, "fa_paged_decode")
-        return o, l
-    return _on(dev, stream, call)
+    handle = _raw_stream(dev, stream)
+    if handle is None:
+        with _on(dev, stream):
+            return paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, window, scores, out, lse, workspace)
+    if out is None:
+        out = torch.empty((B, Hq, d), dtype=dt, device=k_cache.device)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=k_cache.device)
+    if workspace is None:
+        workspace = paged_decode_workspace(B, Hq, k_cache, block_table, scores is not None)
+    n = workspace.numel()
+    status = fa_paged_decode(qp, _pack2(*q.stride()[:2]), kv, table, lens, _check_dense(out, "out", (B, Hq, d), dt, dev),
+                             _check_dense(lse, "lse", (B, Hq), torch.float32, dev), sp, B, Hq, window, scale,
+                             _check_dense(workspace, "workspace", (n,), torch.uint8, dev), n, handle)
+    if status:
+        _raise(status, "fa_paged_decode")
+    return out, lse
 
 
 def paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budget: int, recent: int = 0, sinks: int = 0,
@@ -668,16 +681,17 @@ def paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budg
     if budget < 1:
         raise ValueError("budget must be at least 1")
 
-    def call(handle):
-        n, idx = new_lens, kept
-        if n is None:
-            n = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
-        if idx is None:
-            idx = torch.empty((B, Hkv, budget), dtype=torch.int32, device=k_cache.device)
-        np_ = _check_dense(n, "new_lens", (B,), torch.int32, dev)
-        ip = _check_dense(idx, "kept", (B, Hkv, budget), torch.int32, dev)
-        status = fa_paged_evict(kv, sp, table, lens, dst, np_, ip, B, budget, recent, sinks, handle)
-        if status:
-            _raise(status, "fa_paged_evict")
-        return n, idx
-    return _on(dev, stream, call)
+    handle = _raw_stream(dev, stream)
+    if handle is None:
+        with _on(dev, stream):
+            return paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budget, recent, sinks, new_lens,
+                               kept)
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
+    if kept is None:
+        kept = torch.empty((B, Hkv, budget), dtype=torch.int32, device=k_cache.device)
+    status = fa_paged_evict(kv, sp, table, lens, dst, _check_dense(new_lens, "new_lens", (B,), torch.int32, dev),
+                            _check_dense(kept, "kept", (B, Hkv, budget), torch.int32, dev), B, budget, recent, sinks, handle)
+    if status:
+        _raise(status, "fa_paged_evict")
+    return new_lens, kept
