@@ -664,67 +664,121 @@ __device__ __forceinline__ long long left_at(int i, int i0, int hh) {
 //   O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, m = max_i m_i.
 // Only the boundaries between two parts cut units, whatever the batch:
 // unit_heads / 4 blocks for each boundary.  The blocks of a unit's boundaries
-// share its heads: a block per head, its four warps taking every fourth part,
-// or, where there are fewer blocks than heads, a warp per head.
+// share its heads: a warp per head where there are fewer blocks than heads
+// (units over few parts), else a block per head, or up to D / 32 blocks per
+// head, each with a slice of D.
+// Parts are taken 16 bytes of O a thread, as many at a time as the block has
+// threads for its slice; the order of the sums depends on the sizes alone.
+template <typename T, int D>
+__device__ __forceinline__ void write_row(const DecodeArgs& a, long long row, int d0, const float4& o, float m, float l) {
+  const float inv = 1.f / l;
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + row * D + d0) =
+      make_uint2(Mma<T>::pack(o.x * inv, o.y * inv), Mma<T>::pack(o.z * inv, o.w * inv));
+  if (d0 == 0) {
+    const float lse2 = m + log2f(l);
+    a.lse[row] = lse2 * 0.69314718055994530942f;
+    if (a.lse2) a.lse2[row] = lse2;
+  }
+}
+__device__ __forceinline__ void add_scaled(float4& o, float f, const float4& v) {
+  o.x = fmaf(f, v.x, o.x);
+  o.y = fmaf(f, v.y, o.y);
+  o.z = fmaf(f, v.z, o.z);
+  o.w = fmaf(f, v.w, o.w);
+}
 template <typename T, int D>
 __device__ __forceinline__ void join(const DecodeArgs& a) {
-  constexpr int E = D / 32;
-  __shared__ float sl[4], so[4][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float sf[kDecodeMaxParts], sm[4], sl[4];
+  __shared__ float4 so[128];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Y = a.unit_heads / 4, i = 1 + blockIdx.x / Y;
   const DecodePart d = a.parts[i];
   if (d.left == 0 || d.tile == 0) return;    // no such part, or it starts with a unit
   const int G = a.Hq / a.kv.Hkv, per = a.unit_heads, chunks = (G + per - 1) / per;
   const int g = d.col / chunks, hc = d.col - g * chunks, heads = min(per, G - hc * per);
-  const int i0 = d.i0, i1 = d.i1, blocks = (i1 - i0) * Y, z = (i - i0 - 1) * Y + blockIdx.x % Y;
-  const bool alone = blocks < heads;   // a warp does a head alone
-  const int hh = alone ? z * 4 + warp : z, step = alone ? 1 : 4, from = i0 + (alone ? 0 : warp);
-  if (hh >= heads) return;             // alone: the warp; else the block
-  float m = -INFINITY;
-  for (int x = i0 + lane; x <= i1; x += 32) m = fmaxf(m, a.part_ml[left_at(x, i0, hh)].x);
+  const int i0 = d.i0, n = d.i1 - i0 + 1, blocks = (n - 1) * Y, z = (i - i0 - 1) * Y + blockIdx.x % Y;
+  const long long row0 = (long long)d.b * a.Hq + g * G + hc * per;
+  if (blocks < heads) {
+    // A warp per head, D / 4 lanes: few parts.
+    const int hh = z * 4 + warp;
+    if (hh >= heads) return;
+    float m = -INFINITY, l = 0.f;
+    for (int x = lane; x < n; x += 32) m = fmaxf(m, a.part_ml[left_at(i0 + x, i0, hh)].x);
+    for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    const float mu = m == -INFINITY ? 0.f : m;
+    if (lane >= D / 4) return;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = 0; x < n; ++x) {
+      const long long at = left_at(i0 + x, i0, hh);
+      const float2 y = a.part_ml[at];
+      const float f = ex2(y.x - mu);
+      l = fmaf(f, y.y, l);
+      add_scaled(o, f, *reinterpret_cast<const float4*>(a.part + at * D + lane * 4));
+    }
+    write_row<T, D>(a, row0 + hh, lane * 4, o, m, l);
+    return;
+  }
+  int slices = D / 32;
+  while (slices > 1 && slices * heads > blocks) slices /= 2;
+  if (z >= heads * slices) return;
+  const int hh = z / slices, lanes = D / 4 / slices, groups = 128 / lanes;
+  const int d0 = (z - hh * slices) * (D / slices) + tid % lanes * 4, group = tid / lanes;
+  // Scale and sum of every part.
+  float2 y[(kDecodeMaxParts + 127) / 128];
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int u = 0; u < (kDecodeMaxParts + 127) / 128; ++u) {
+    const int x = u * 128 + tid;
+    y[u] = x < n ? a.part_ml[left_at(i0 + x, i0, hh)] : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, y[u].x);
+  }
   for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  if (lane == 0) sm[warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
   const float mu = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[E] = {};
+#pragma unroll
+  for (int u = 0; u < (kDecodeMaxParts + 127) / 128; ++u) {
+    const int x = u * 128 + tid;
+    const float f = ex2(y[u].x - mu);
+    if (x < n) sf[x] = f;
+    l = fmaf(f, y[u].y, l);
+  }
+  for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+  if (lane == 0) sl[warp] = l;
+  __syncthreads();
+  l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int x = group; x < n; x += groups)
+    add_scaled(o, sf[x], *reinterpret_cast<const float4*>(a.part + left_at(i0 + x, i0, hh) * D + d0));
+  so[tid] = o;
+  __syncthreads();
+  if (group > 0) return;
+  for (int k = 1; k < groups; ++k) add_scaled(o, 1.f, so[k * lanes + tid]);
+  write_row<T, D>(a, row0 + hh, d0, o, m, l);
+}
+
+// Log-sum-exp (log2 units) of head hh0 + lane < hh0 + n of a cut unit, from its
+// parts: as many parts at a time as the warp has lanes for n heads.
+__device__ __forceinline__ float parts_lse2(const DecodeArgs& a, int i0, int i1, int hh0, int n) {
+  const int lane = threadIdx.x & 31;
+  int w = 1;
+  while (w < n) w *= 2;
+  const int hh = hh0 + min(lane % w, n - 1), step = 32 / w, from = i0 + lane / w;
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int x = from; x <= i1; x += step) m = fmaxf(m, a.part_ml[left_at(x, i0, hh)].x);
+  for (int k = w; k < 32; k *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll 4
   for (int x = from; x <= i1; x += step) {
-    const long long at = left_at(x, i0, hh);
-    const float2 y = a.part_ml[at];
-    const float f = ex2(y.x - mu);
-    const float* p = a.part + at * D + lane * E;
-    l = fmaf(f, y.y, l);
-    if constexpr (E == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p);
-      o[0] = fmaf(f, v.x, o[0]);
-      o[1] = fmaf(f, v.y, o[1]);
-      o[2] = fmaf(f, v.z, o[2]);
-      o[3] = fmaf(f, v.w, o[3]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(p);
-      o[0] = fmaf(f, v.x, o[0]);
-      o[1] = fmaf(f, v.y, o[1]);
-    }
+    const float2 y = a.part_ml[left_at(x, i0, hh)];
+    l = fmaf(ex2(y.x - mu), y.y, l);
   }
-  if (!alone) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-    if (lane == 0) sl[warp] = l;
-    __syncthreads();
-    if (warp > 0) return;
-    l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = (so[0][lane * E + e] + so[1][lane * E + e]) + (so[2][lane * E + e] + so[3][lane * E + e]);
-  }
-  const long long row = (long long)d.b * a.Hq + g * G + hc * per + hh;
-  const float inv = 1.f / l;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + row * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = Mma<T>::pack(o[e] * inv, o[e + 1] * inv);
-  if (lane == 0) {
-    const float lse2 = m + log2f(l);
-    a.lse[row] = lse2 * 0.69314718055994530942f;
-    if (a.lse2) a.lse2[row] = lse2;
-  }
+  for (int k = w; k < 32; k *= 2) l += __shfl_xor_sync(0xffffffffu, l, k);
+  return m + log2f(l);
 }
 
 // Adds each visible key's weight, summed over the group's heads from the
@@ -734,7 +788,7 @@ __device__ __forceinline__ void join(const DecodeArgs& a) {
 // at L2 rather than a load and a store, so that sequences sharing a page both
 // count.
 // kJoined: every LSE is there; else those of cut units come from their parts.
-constexpr int kSplit = 2;
+constexpr int kSplit = 4;
 template <int kKeys, bool kJoined>
 __device__ __forceinline__ void add_weights(const DecodeArgs& a, int block) {
   constexpr int kLane = kKeys / 32;    // keys a lane
@@ -787,20 +841,9 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int block) {
     for (int h0 = 0; h0 < G; h0 += 32) {
       const int nh = min(32, G - h0);
       if (fresh || G > 32) {           // lane h holds the LSE of head h0 + h
-        if (lane < nh && (kJoined || i0 == i1)) {
-          lse2 = a.lse2[(long long)w.b * a.Hq + g * G + h0 + lane];
-        } else if (lane < nh) {
-          float m = -INFINITY, l = 0.f;
-#pragma unroll 4
-          for (int x = i0; x <= i1; ++x) m = fmaxf(m, a.part_ml[left_at(x, i0, h0 + lane)].x);
-          const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-          for (int x = i0; x <= i1; ++x) {
-            const float2 y = a.part_ml[left_at(x, i0, h0 + lane)];
-            l = fmaf(ex2(y.x - mu), y.y, l);
-          }
-          lse2 = m + log2f(l);
-        }
+        const bool known = kJoined || i0 == i1;
+        if (known && lane < nh) lse2 = a.lse2[(long long)w.b * a.Hq + g * G + h0 + lane];
+        if (!known) lse2 = parts_lse2(a, i0, i1, h0, nh);
       }
 #pragma unroll
       for (int u = 0; u < kLane; ++u) {
@@ -842,8 +885,9 @@ __global__ void __launch_bounds__(128) fa_paged_finish_kernel(const DecodeArgs a
   else add_weights<Cfg<D>::kKeys, false>(a, blockIdx.x - joins);
 }
 
-// The weights after every join: where a kv head's units are several, a cut
-// one's parts are not known to the others.
+// The weights after every join: where a kv head's units are several (a cut
+// one's parts are not known to the others), or cut so often that forming the
+// LSE from the parts in every warp costs more than waiting for the joins.
 template <int kKeys>
 __global__ void __launch_bounds__(128) fa_paged_weights_kernel(const DecodeArgs a) {
   wait_for_previous();
@@ -874,7 +918,9 @@ cudaError_t launch_decode(const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int joins = (parts - 1) * (a.unit_heads / 4), adds = parts * kSplit;
-  if (a.scores && a.Hq / a.kv.Hkv <= a.unit_heads)
+  // In one launch unless units are cut into more than about eight (2 sequences
+  // of 93735 keys, 152 parts each: 29.2 us in one, 27.2 us in two).
+  if (a.scores && a.Hq / a.kv.Hkv <= a.unit_heads && parts <= 8 * a.B * a.kv.Hkv)
     return launch_after(fa_paged_finish_kernel<T, D, true>, joins + adds, 128, stream, a, joins);
   if (joins > 0) e = launch_after(fa_paged_finish_kernel<T, D, false>, joins, 128, stream, a, joins);
   if (e == cudaSuccess && a.scores) e = launch_after(fa_paged_weights_kernel<Cfg<D>::kKeys>, adds, 128, stream, a);

@@ -12,8 +12,11 @@
 // as a 64-bit integer (from the double's mantissa and exponent, integer
 // arithmetic only) and the phase is pos * F modulo 2^64: the wrap-around of
 // the integer product is the reduction, exact for every int32 position.  The
-// phase's top 32 bits, as a signed fraction of half a turn, go to sincospif.
-// Error: F is off by < 2^-63 relative, the 32 bits by 2^-32 of a turn.
+// phase's top 32 bits, as a signed angle in [-pi, pi], go to __sinf and __cosf,
+// which are within 2^-21.4 and 2^-21.2 there; with the roundings of the angle
+// (3 2^-24 of it) a sine or cosine is off by less than 1e-6, 1/500 of the
+// rounding of an fp16 result.  A block turns the frequencies into F once, in
+// shared memory.
 //
 // Bound by HBM: every element is read once and written once.  A thread owns
 // one token and eight pairs (two 16-byte vectors of a row): its eight
@@ -69,21 +72,33 @@ __device__ __forceinline__ uint64_t turns64(double w) {
   return (bits >> 63) ? 0 - F : F;
 }
 
-// Cosines and sines of the pairs 8c .. 8c+7 of the token whose positions
-// start at pos.
-__device__ __forceinline__ void load_angles(const RotaryArgs& r, const int* pos, int c, const DevStatus& st,
-                                            float (&cs)[8], float (&sn)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    int ax = r.axes[c * 8 + i];
+// What a block keeps of the rotation: each pair's F and axis.
+struct Pairs {
+  uint64_t turns[128];
+  int axis[128];
+};
+__device__ __forceinline__ void load_pairs(const RotaryArgs& r, Pairs& p, const DevStatus& st) {
+  for (int i = threadIdx.x; i < r.rot / 2; i += kThreads) {
+    int ax = r.axes[i];
     if (ax < 0 || ax >= r.n_axes) {
       record_error(st, kErrBadIndex, kSiteAxis);
       ax = 0;
     }
-    const uint64_t phase = (uint64_t)(int64_t)pos[ax * r.pos_axis] * turns64(r.inv_freq[c * 8 + i]);
-    const float half_turns = (float)(int32_t)(uint32_t)(phase >> 32) * 4.656612873077393e-10f;   // 2^-31
-    sincospif(half_turns, &sn[i], &cs[i]);
-    if (r.inverse) sn[i] = -sn[i];
+    p.axis[i] = ax;
+    p.turns[i] = turns64(r.inv_freq[i]);
+  }
+}
+
+// Cosines and sines of the pairs 8c .. 8c+7 of the token whose positions
+// start at pos.
+__device__ __forceinline__ void load_angles(const RotaryArgs& r, const Pairs& p, const int* pos, int c, float (&cs)[8],
+                                            float (&sn)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t phase = (uint64_t)(int64_t)pos[p.axis[c * 8 + i] * r.pos_axis] * p.turns[c * 8 + i];
+    const float angle = (float)(int32_t)(uint32_t)(phase >> 32) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+    cs[i] = __cosf(angle);
+    sn[i] = __sinf(r.inverse ? -angle : angle);
   }
 }
 
@@ -156,6 +171,9 @@ __device__ __forceinline__ void do_heads(const T* in, long long in_sh, T* out, l
 // and then k.
 template <typename T, bool kInter>
 __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeArgs a, int hpb, const DevStatus st) {
+  __shared__ Pairs pairs;
+  load_pairs(a.r, pairs, st);
+  __syncthreads();
   const int nch = a.d / 16, tpb = kThreads / nch;
   const int lt = threadIdx.x / nch, c = threadIdx.x - lt * nch;
   const long long t = (long long)blockIdx.x * tpb + lt;
@@ -163,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeArgs a, int
   const int b = (int)(t / a.N), n = (int)(t - (long long)b * a.N);
   const Chunk ck = chunk_of<kInter>(c, a.r.rot);
   float cs[8] = {}, sn[8] = {};
-  if (ck.turned) load_angles(a.r, a.r.pos + b * a.r.pos_batch + n, c, st, cs, sn);
+  if (ck.turned) load_angles(a.r, pairs, a.r.pos + b * a.r.pos_batch + n, c, cs, sn);
   const int h0 = blockIdx.y * hpb, h1 = min(h0 + hpb, a.Hq + a.Hk);
   auto rows = [&](const RowView& in, const RowView& out, int lo, int hi) {
     if (lo < hi)
@@ -211,6 +229,9 @@ __device__ __forceinline__ bool place_token(const AppendArgs& a, int t, const De
 // rows go to their slot of the cache, whose accumulated weight starts at 0.
 template <typename T, bool kInter>
 __global__ void __launch_bounds__(kThreads) fa_append_kernel(const AppendArgs a, int hpb, const DevStatus st) {
+  __shared__ Pairs pairs;
+  load_pairs(a.r, pairs, st);
+  __syncthreads();
   const int nch = a.kv.d / 16, tpb = kThreads / nch;
   const int lt = threadIdx.x / nch, c = threadIdx.x - lt * nch;
   const long long t = (long long)blockIdx.x * tpb + lt;
@@ -221,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) fa_append_kernel(const AppendArgs a,
   const int h0 = blockIdx.y * hpb, h1 = min(h0 + hpb, a.Hq + 2 * Hkv);
   const Chunk ck = chunk_of<kInter>(c, a.r.rot);
   float cs[8] = {}, sn[8] = {};
-  if (ck.turned && h0 < a.Hq + Hkv) load_angles(a.r, a.r.pos + t, c, st, cs, sn);
+  if (ck.turned && h0 < a.Hq + Hkv) load_angles(a.r, pairs, a.r.pos + t, c, cs, sn);
   const long long at = page * a.kv.s_page + slot * a.kv.s_slot;
   if (h0 < a.Hq)
     do_heads<T, kInter>(static_cast<const T*>(a.q.p) + t * a.q.sn, a.q.sh, static_cast<T*>(a.q_out.p) + t * a.q_out.sn,

@@ -4,10 +4,11 @@ eviction against the fp64 oracle, through the Python binding.
 Tolerances (u = half a step of the tensors' type: bf16 2^-8, fp16 2^-11).
 
 Rotation: |out - ref| <= u |ref| + c (|x| + |y|) + tiny, where c bounds the fp32
-part: the phase is off by < 2^-31 of a turn plus its conversion (2^-25 of half
-a turn = 1e-7 rad), sincospi by 2^-22, and two products and a sum round by
-3 * 2^-24: c = 1e-6.  The rounding of a value that is off by e is off by at
-most u (|ref| + e) + e, so c is doubled; tiny is the fp16 subnormal step.
+part: the angle, at most pi, is rounded by its conversion, its scaling and the
+scale's constant (3 pi 2^-24 = 5.6e-7), its sine or cosine is off by 2^-21.2 =
+4.2e-7, and two products and a sum round by 3 2^-24 = 1.8e-7: 1.2e-6.  The
+rounding of a value that is off by e is off by at most u (|ref| + e) + e <
+u |ref| + 1.01 e, so c = 2e-6 holds; tiny is the fp16 subnormal step.
 
 Attention: with A = sum p |v| (from the oracle) the weights are applied
 rounded to the tensors' type (u A), o is rounded once (u |o|), and a relative
