@@ -242,8 +242,8 @@ def fa_paged_append(kv, table, seq_lens, cu_seqlens, B, T, k, k_strides, v, v_st
 
 def fa_paged_decode(q, q_strides, kv, table, seq_lens, o, lse, scores, B, Hq, window, scale, workspace,
                     workspace_bytes, stream):
-    return load_library().fa_paged_decode(q, q_strides, _ref(kv), _ref(table), seq_lens, o, lse, scores, B, Hq, window,
-                                          float(scale), workspace, workspace_bytes, stream)
+    return load_library().fa_paged_decode(q, q_strides, _ref(kv), _ref(table), seq_lens, o, lse, scores, B, Hq,
+                                          int(window), float(scale), workspace, workspace_bytes, stream)
 
 
 def fa_paged_decode_workspace_bytes(B, Hq, Hkv, d, page_size, max_pages, with_scores):
@@ -251,8 +251,8 @@ def fa_paged_decode_workspace_bytes(B, Hq, Hkv, d, page_size, max_pages, with_sc
 
 
 def fa_paged_evict(kv, scores, table, seq_lens, dst, new_lens, kept, B, budget, recent, sinks, stream):
-    return load_library().fa_paged_evict(_ref(kv), scores, _ref(table), seq_lens, _ref(dst), new_lens, kept, B, budget,
-                                         recent, sinks, stream)
+    return load_library().fa_paged_evict(_ref(kv), scores, _ref(table), seq_lens, _ref(dst), new_lens, kept, B,
+                                         int(budget), int(recent), int(sinks), stream)
 
 
 # ---------------------------------------------------------------------------
@@ -467,16 +467,15 @@ def _on(dev, stream):
 def _rotary(positions, inv_freq, axes, interleaved, d, lead, dev):
     """fa_rotary of positions [n_axes, *lead] int32, inv_freq [rot/2] float64, axes [rot/2] int32."""
     import torch
-    if not all(isinstance(t, torch.Tensor) for t in (positions, inv_freq, axes)):
-        raise ValueError("rotary positions need positions, inv_freq and axes as tensors")
-    n_axes = positions.shape[0] if positions.dim() else 0
+    try:
+        n_axes, n, st = positions.shape[0], inv_freq.shape[0], positions.stride()
+    except (AttributeError, IndexError):
+        raise ValueError("rotary positions need positions, inv_freq and axes as tensors") from None
     pos = _check_view(positions, "positions", (n_axes, *lead), torch.int32, dev)
-    n = inv_freq.numel()
     if n < 1 or 2 * n > d:
         raise ValueError(f"inv_freq has {n} frequencies, expected 1 to {d // 2}")
     w = _check_dense(inv_freq, "inv_freq", (n,), torch.float64, dev)
     ax = _check_dense(axes, "axes", (n,), torch.int32, dev)
-    st = positions.stride()
     return _pack_rotary(pos, st[0], st[1] if len(lead) == 2 else 0, w, ax, n_axes, 2 * n, 1 if interleaved else 0)
 
 
@@ -513,12 +512,17 @@ def _rope(q, k, positions, inv_freq, axes, interleaved, inverse, q_out, k_out, s
             return _rope(q, k, positions, inv_freq, axes, interleaved, inverse, q_out, k_out, None)
     if q_out is None:
         q_out = torch.empty((B, Hq, N, d), dtype=dt, device=q.device)
-    op = _check_view(q_out, "q_out", (B, Hq, N, d), dt, dev)
+        op = q_out.data_ptr()
+    else:
+        op = _check_view(q_out, "q_out", (B, Hq, N, d), dt, dev)
     okp, oks = None, None
     if k is not None:
         if k_out is None:
             k_out = torch.empty((B, Hk, N, d), dtype=dt, device=q.device)
-        okp, oks = _check_view(k_out, "k_out", (B, Hk, N, d), dt, dev), _pack3(*k_out.stride()[:3])
+            okp = k_out.data_ptr()
+        else:
+            okp = _check_view(k_out, "k_out", (B, Hk, N, d), dt, dev)
+        oks = _pack3(*k_out.stride()[:3])
     status = fa_rope(qp, _pack3(*q.stride()[:3]), op, _pack3(*q_out.stride()[:3]), kp, ks, okp, oks, B, Hq, Hk, N, d, code,
                      rot, inverse, handle)
     if status:
@@ -607,7 +611,10 @@ def paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens=None,
     if q is not None:
         if q_out is None:
             q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
-        op, os_ = _check_view(q_out, "q_out", (T, Hq, d), dt, dev), _pack2(*q_out.stride()[:2])
+            op = q_out.data_ptr()
+        else:
+            op = _check_view(q_out, "q_out", (T, Hq, d), dt, dev)
+        os_ = _pack2(*q_out.stride()[:2])
     if T:
         status = fa_paged_append(kv, table, lens, cu, B, T, kp, _pack2(*k.stride()[:2]), vp, _pack2(*v.stride()[:2]), qp, qs,
                                  op, os_, Hq, rot, sp, handle)
@@ -649,16 +656,24 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float | None
     if handle is None:
         with _on(dev, stream):
             return paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, window, scores, out, lse, workspace)
+    device = k_cache.device
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=dt, device=k_cache.device)
+        out = torch.empty((B, Hq, d), dtype=dt, device=device)
+        op = out.data_ptr()
+    else:
+        op = _check_dense(out, "out", (B, Hq, d), dt, dev)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=k_cache.device)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
+        lp = lse.data_ptr()
+    else:
+        lp = _check_dense(lse, "lse", (B, Hq), torch.float32, dev)
     if workspace is None:
         workspace = paged_decode_workspace(B, Hq, k_cache, block_table, scores is not None)
-    n = workspace.numel()
-    status = fa_paged_decode(qp, _pack2(*q.stride()[:2]), kv, table, lens, _check_dense(out, "out", (B, Hq, d), dt, dev),
-                             _check_dense(lse, "lse", (B, Hq), torch.float32, dev), sp, B, Hq, window, scale,
-                             _check_dense(workspace, "workspace", (n,), torch.uint8, dev), n, handle)
+        n, wp = workspace.numel(), workspace.data_ptr()
+    else:
+        n = workspace.numel()
+        wp = _check_dense(workspace, "workspace", (n,), torch.uint8, dev)
+    status = fa_paged_decode(qp, _pack2(*q.stride()[:2]), kv, table, lens, op, lp, sp, B, Hq, window, scale, wp, n, handle)
     if status:
         _raise(status, "fa_paged_decode")
     return out, lse
@@ -688,10 +703,15 @@ def paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budg
                                kept)
     if new_lens is None:
         new_lens = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
+        np_ = new_lens.data_ptr()
+    else:
+        np_ = _check_dense(new_lens, "new_lens", (B,), torch.int32, dev)
     if kept is None:
         kept = torch.empty((B, Hkv, budget), dtype=torch.int32, device=k_cache.device)
-    status = fa_paged_evict(kv, sp, table, lens, dst, _check_dense(new_lens, "new_lens", (B,), torch.int32, dev),
-                            _check_dense(kept, "kept", (B, Hkv, budget), torch.int32, dev), B, budget, recent, sinks, handle)
+        ip = kept.data_ptr()
+    else:
+        ip = _check_dense(kept, "kept", (B, Hkv, budget), torch.int32, dev)
+    status = fa_paged_evict(kv, sp, table, lens, dst, np_, ip, B, budget, recent, sinks, handle)
     if status:
         _raise(status, "fa_paged_evict")
     return new_lens, kept

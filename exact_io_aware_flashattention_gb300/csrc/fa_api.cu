@@ -851,9 +851,9 @@ View scores_view(const fa_paged_kv* kv, const float* s) {
   return bytes_view(s, (size_t)kv->num_pages * kv->Hkv * kv->page_size * 4);
 }
 
-fa_status check_table(const fa_page_table* t, int B) {
+fa_status check_table(const fa_page_table* t, int B, int page_size) {
   if (!t || !t->pages) return FA_ERR_NULL_PTR;
-  if (t->max_pages < 1) return FA_ERR_BAD_SHAPE;
+  if (t->max_pages < 1 || (long long)t->max_pages * page_size > (1LL << 30)) return FA_ERR_BAD_SHAPE;
   if (B > 1 && (t->stride < 0 || t->stride > (1LL << 31))) return FA_ERR_BAD_ARGUMENT;
   return aligned(t->pages, 4) ? FA_OK : FA_ERR_MISALIGNED;
 }
@@ -972,7 +972,7 @@ fa_status fa_paged_append(const fa_paged_kv* kv, const fa_page_table* table, con
   FA_TRY(check_kv(kv));
   if (!seq_lens || !k_strides || !v_strides || (T != 0 && (!k || !v))) return FA_ERR_NULL_PTR;
   if (B < 1 || T < 0 || (!cu_seqlens && T != B)) return FA_ERR_BAD_SHAPE;
-  FA_TRY(check_table(table, B));
+  FA_TRY(check_table(table, B, kv->page_size));
   if (!aligned(seq_lens, 4) || !aligned(cu_seqlens, 4) || !aligned16(scores)) return FA_ERR_MISALIGNED;
   if (q && !rotary) return FA_ERR_BAD_ARGUMENT;
   if (q ? (!q_out || !q_strides || !q_out_strides) : q_out != nullptr) return FA_ERR_NULL_PTR;
@@ -1038,7 +1038,8 @@ fa_status fa_paged_append(const fa_paged_kv* kv, const fa_page_table* table, con
 
 size_t fa_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d, int page_size, int max_pages, int with_scores) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (d != 64 && d != 128) || page_size < 16 || page_size > 65536 ||
-      page_size % 16 || max_pages < 1 || (long long)B * Hq >= (1LL << 31))
+      page_size % 16 || max_pages < 1 || (long long)max_pages * page_size > (1LL << 30) ||
+      (long long)B * Hq >= (1LL << 31))
     return 0;
   return decode_ws(B, Hq, d, page_size, max_pages, with_scores != 0).total;
 }
@@ -1050,7 +1051,7 @@ fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_pa
   FA_TRY(check_kv(kv));
   if (!q || !q_strides || !seq_lens || !o || !lse || !workspace) return FA_ERR_NULL_PTR;
   if (B < 1 || Hq < 1 || Hq % kv->Hkv || (long long)B * Hq >= (1LL << 31)) return FA_ERR_BAD_SHAPE;
-  FA_TRY(check_table(table, B));
+  FA_TRY(check_table(table, B, kv->page_size));
   FA_TRY(check_scale(0, scale));
   if (window < 0) return FA_ERR_BAD_ARGUMENT;
   FA_TRY(check_strides({{B, q_strides[0]}, {Hq, q_strides[1]}}));
@@ -1110,12 +1111,12 @@ fa_status fa_paged_evict(const fa_paged_kv* kv, float* scores, const fa_page_tab
   NvtxRange nv("fa_paged_evict");
   FA_TRY(check_kv(kv));
   if (!scores || !seq_lens || !new_lens || !kept) return FA_ERR_NULL_PTR;
-  // Grids: up to 8 CTAs, and a block per 64 kept keys, for each (sequence, kv head).
+  // Grids: up to 8 CTAs, and a block per 32 kept keys, for each (sequence, kv head).
   if (B < 1 || (long long)B * kv->Hkv >= (1LL << 27) ||
-      (long long)B * kv->Hkv * (((long long)budget + 63) / 64) >= (1LL << 31))
+      (long long)B * kv->Hkv * (((long long)budget + 31) / 32) >= (1LL << 31))
     return FA_ERR_BAD_SHAPE;
-  FA_TRY(check_table(table, B));
-  FA_TRY(check_table(dst, B));
+  FA_TRY(check_table(table, B, kv->page_size));
+  FA_TRY(check_table(dst, B, kv->page_size));
   if (budget < 1 || recent < 0 || sinks < 0 || (long long)recent + sinks > budget ||
       (long long)dst->max_pages * kv->page_size < budget)
     return FA_ERR_BAD_ARGUMENT;

@@ -442,8 +442,11 @@ cudaError_t launch(void (*k)(P...), dim3 grid, int block, size_t smem, int clust
 constexpr size_t kSelectBytes = (sizeof(Select) + 15) / 16 * 16;
 
 cudaError_t configure_evict_kernels() {
-  return cudaFuncSetAttribute(fa_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)(kSelectBytes + kMaxCached * 4));
+  cudaError_t e = cudaFuncSetAttribute(fa_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(kSelectBytes + kMaxCached * 4));
+  if (e == cudaSuccess) e = preload_kernel(fa_evict_copy_kernel<64>);
+  if (e == cudaSuccess) e = preload_kernel(fa_evict_copy_kernel<128>);
+  return e;
 }
 
 cudaError_t launch_paged_evict(EvictArgs a, const DevStatus& st, int num_sms, cudaStream_t stream) {

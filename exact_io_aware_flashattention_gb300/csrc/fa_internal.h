@@ -78,6 +78,14 @@ cudaError_t launch_bwd_dq_convert(const float* dq_accum, void* dq, float scale, 
 // ---------------------------------------------------------------------------
 // Rotary positions and the paged cache (fa_rope.cu, fa_paged.cu, fa_evict.cu)
 // ---------------------------------------------------------------------------
+// Loads a kernel ahead of its first launch, which may be inside a stream
+// capture, where loading is not safe.
+template <typename K>
+cudaError_t preload_kernel(K* k) {
+  cudaFuncAttributes attr;
+  return cudaFuncGetAttributes(&attr, k);
+}
+
 // Wait-site ids / index-check sites of these kernels in the status words.
 enum : int { kSiteAxis = 41, kSiteAppend = 42, kSiteDecodeLen = 43, kSiteDecodePage = 44, kSiteEvictLen = 45, kSiteEvictPage = 46 };
 constexpr int kErrBadIndex = 14;   // == FA_ERR_BAD_INDEX
@@ -190,6 +198,7 @@ cudaError_t configure_bwd_kernels();
 cudaError_t configure_dq_kernels();
 cudaError_t configure_paged_kernels();
 cudaError_t configure_evict_kernels();
+cudaError_t configure_rope_kernels();
 
 inline cudaError_t configure_kernels() {
   cudaError_t e = configure_fwd_kernels();
@@ -197,6 +206,7 @@ inline cudaError_t configure_kernels() {
   if (e == cudaSuccess) e = configure_dq_kernels();
   if (e == cudaSuccess) e = configure_paged_kernels();
   if (e == cudaSuccess) e = configure_evict_kernels();
+  if (e == cudaSuccess) e = configure_rope_kernels();
   return e;
 }
 

@@ -83,9 +83,15 @@ struct Mma<__nv_bfloat16> {
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return cvt_bf16x2(lo, hi); }
+  static constexpr float kShift = 0.f;
 };
 template <>
 struct Mma<__half> {
+  // Weights are formed as 2^(s - m + 12): relative to the largest they would
+  // vanish below 2^-25 in fp16, where many of them can still add up to
+  // something; so they do below 2^-37, and the largest is 4096.  Sums and O
+  // carry the factor alike.
+  static constexpr float kShift = 12.f;
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -493,9 +499,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
           mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
         }
-        // The maximum is the exact running one, so a row's largest weight is 1
-        // and rounding the weights to 16 bits for the product cannot touch it;
-        // the sums keep the unrounded weights.
+        // The maximum is the exact running one, so a row's largest weight is a
+        // power of two and rounding the weights to 16 bits for the product
+        // cannot touch it; the sums keep the unrounded weights.
         if (__any_sync(0xffffffffu, mx0 > m[n][0] || mx1 > m[n][1])) {
           const float n0 = fmaxf(m[n][0], mx0), n1 = fmaxf(m[n][1], mx1);
           const float f0 = n0 == -INFINITY ? 0.f : ex2(m[n][0] - n0), f1 = n1 == -INFINITY ? 0.f : ex2(m[n][1] - n1);
@@ -511,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             o[n][k][3] *= f1;
           }
         }
-        const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0], u1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+        const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - Mma<T>::kShift;
+        const float u1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - Mma<T>::kShift;
 #pragma unroll
         for (int u = 0; u < kSl; ++u) {
           x[u][0] = ex2(x[u][0] - u0);
@@ -633,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             if constexpr (D == 128) *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
             else *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
             if (e0 == 0) {
-              const float lse2 = M + log2f(L);
+              const float lse2 = M + (log2f(L) - Mma<T>::kShift);
               a.lse[(long long)w.b * a.Hq + h] = lse2 * 0.69314718055994530942f;
               if (a.lse2) a.lse2[(long long)w.b * a.Hq + h] = lse2;
             }
@@ -675,7 +682,7 @@ __device__ __forceinline__ void write_row(const DecodeArgs& a, long long row, in
   *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + row * D + d0) =
       make_uint2(Mma<T>::pack(o.x * inv, o.y * inv), Mma<T>::pack(o.z * inv, o.w * inv));
   if (d0 == 0) {
-    const float lse2 = m + log2f(l);
+    const float lse2 = m + (log2f(l) - Mma<T>::kShift);
     a.lse[row] = lse2 * 0.69314718055994530942f;
     if (a.lse2) a.lse2[row] = lse2;
   }
@@ -762,7 +769,7 @@ __device__ __forceinline__ void join(const DecodeArgs& a) {
 
 // Log-sum-exp (log2 units) of head hh0 + lane < hh0 + n of a cut unit, from its
 // parts: as many parts at a time as the warp has lanes for n heads.
-__device__ __forceinline__ float parts_lse2(const DecodeArgs& a, int i0, int i1, int hh0, int n) {
+__device__ __forceinline__ float parts_lse2(const DecodeArgs& a, int i0, int i1, int hh0, int n, float shift) {
   const int lane = threadIdx.x & 31;
   int w = 1;
   while (w < n) w *= 2;
@@ -778,7 +785,7 @@ __device__ __forceinline__ float parts_lse2(const DecodeArgs& a, int i0, int i1,
     l = fmaf(ex2(y.x - mu), y.y, l);
   }
   for (int k = w; k < 32; k *= 2) l += __shfl_xor_sync(0xffffffffu, l, k);
-  return m + log2f(l);
+  return m + (log2f(l) - shift);
 }
 
 // Adds each visible key's weight, summed over the group's heads from the
@@ -790,7 +797,7 @@ __device__ __forceinline__ float parts_lse2(const DecodeArgs& a, int i0, int i1,
 // kJoined: every LSE is there; else those of cut units come from their parts.
 constexpr int kSplit = 4;
 template <int kKeys, bool kJoined>
-__device__ __forceinline__ void add_weights(const DecodeArgs& a, int block) {
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, int block, float shift) {
   constexpr int kLane = kKeys / 32;    // keys a lane
   const int lane = threadIdx.x & 31, i = block / kSplit;
   int skip = (block % kSplit) * 4 + (threadIdx.x >> 5);
@@ -843,7 +850,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int block) {
       if (fresh || G > 32) {           // lane h holds the LSE of head h0 + h
         const bool known = kJoined || i0 == i1;
         if (known && lane < nh) lse2 = a.lse2[(long long)w.b * a.Hq + g * G + h0 + lane];
-        if (!known) lse2 = parts_lse2(a, i0, i1, h0, nh);
+        if (!known) lse2 = parts_lse2(a, i0, i1, h0, nh, shift);
       }
 #pragma unroll
       for (int u = 0; u < kLane; ++u) {
@@ -882,7 +889,7 @@ __global__ void __launch_bounds__(128) fa_paged_finish_kernel(const DecodeArgs a
   launch_dependents();
   wait_for_previous();
   if (!kScores || blockIdx.x < joins) join<T, D>(a);
-  else add_weights<Cfg<D>::kKeys, false>(a, blockIdx.x - joins);
+  else add_weights<Cfg<D>::kKeys, false>(a, blockIdx.x - joins, Mma<T>::kShift);
 }
 
 // The weights after every join: where a kv head's units are several (a cut
@@ -891,7 +898,7 @@ __global__ void __launch_bounds__(128) fa_paged_finish_kernel(const DecodeArgs a
 template <int kKeys>
 __global__ void __launch_bounds__(128) fa_paged_weights_kernel(const DecodeArgs a) {
   wait_for_previous();
-  add_weights<kKeys, true>(a, blockIdx.x);
+  add_weights<kKeys, true>(a, blockIdx.x, 0.f);
 }
 
 // A launch whose blocks may start before the kernel in front of it is done
@@ -920,7 +927,7 @@ cudaError_t launch_decode(const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs
   const int joins = (parts - 1) * (a.unit_heads / 4), adds = parts * kSplit;
   // In one launch unless units are cut into more than about eight (2 sequences
   // of 93735 keys, 152 parts each: 29.2 us in one, 27.2 us in two).
-  if (a.scores && a.Hq / a.kv.Hkv <= a.unit_heads && parts <= 8 * a.B * a.kv.Hkv)
+  if (a.scores && a.Hq / a.kv.Hkv <= a.unit_heads && parts <= 8LL * a.B * a.kv.Hkv)
     return launch_after(fa_paged_finish_kernel<T, D, true>, joins + adds, 128, stream, a, joins);
   if (joins > 0) e = launch_after(fa_paged_finish_kernel<T, D, false>, joins, 128, stream, a, joins);
   if (e == cudaSuccess && a.scores) e = launch_after(fa_paged_weights_kernel<Cfg<D>::kKeys>, adds, 128, stream, a);
@@ -935,6 +942,9 @@ cudaError_t configure_decode() {
                                        Cfg<D>::kBytes);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(fa_paged_decode_kernel<T, D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kBytes);
+  if (e == cudaSuccess) e = preload_kernel(fa_paged_finish_kernel<T, D, false>);
+  if (e == cudaSuccess) e = preload_kernel(fa_paged_finish_kernel<T, D, true>);
+  if (e == cudaSuccess) e = preload_kernel(fa_paged_weights_kernel<Cfg<D>::kKeys>);
   return e;
 }
 

@@ -274,6 +274,18 @@ int heads_per_block(long long token_blocks, int heads, int num_sms) {
 
 }  // namespace
 
+cudaError_t configure_rope_kernels() {
+  cudaError_t e = preload_kernel(fa_rope_kernel<__nv_bfloat16, false>);
+  if (e == cudaSuccess) e = preload_kernel(fa_rope_kernel<__nv_bfloat16, true>);
+  if (e == cudaSuccess) e = preload_kernel(fa_rope_kernel<__half, false>);
+  if (e == cudaSuccess) e = preload_kernel(fa_rope_kernel<__half, true>);
+  if (e == cudaSuccess) e = preload_kernel(fa_append_kernel<__nv_bfloat16, false>);
+  if (e == cudaSuccess) e = preload_kernel(fa_append_kernel<__nv_bfloat16, true>);
+  if (e == cudaSuccess) e = preload_kernel(fa_append_kernel<__half, false>);
+  if (e == cudaSuccess) e = preload_kernel(fa_append_kernel<__half, true>);
+  return e;
+}
+
 cudaError_t launch_rope(int dtype, const RopeArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream) {
   const int tpb = kThreads / (a.d / 16);
   const long long blocks = ((long long)a.B * a.N + tpb - 1) / tpb;

@@ -329,7 +329,10 @@ typedef struct fa_paged_kv {
   int num_pages, page_size, Hkv, d, dtype;
 } fa_paged_kv;
 
-/* Block table int32 [B, max_pages] with a row stride (elements). */
+/*
+ * Block table int32 [B, max_pages] with a row stride (elements); max_pages *
+ * page_size, the keys a sequence can have, is at most 2^30.
+ */
 typedef struct fa_page_table {
   const int* pages;
   long long stride;
@@ -367,8 +370,11 @@ fa_status fa_paged_append(const fa_paged_kv* kv, const fa_page_table* table, con
  * scores (may be NULL), fp32 [num_pages, Hkv, page_size] contiguous: the entry
  * of each visible key grows by the sum over the group's heads of its softmax
  * weight.  Sequences may share pages: their weights add up (in no fixed order).
- * workspace: at least fa_paged_decode_workspace_bytes(...) bytes, contents
- * don't matter; calls that may run at the same time need one each.
+ * workspace: at least fa_paged_decode_workspace_bytes(...) bytes (5.3 MB at
+ * d = 128; with scores 4 more for every query head and key that the block table
+ * has room for), contents don't matter; calls that may run at the same time
+ * need one each.  O, LSE and (but for shared pages) scores are bitwise
+ * reproducible.  Two or three launches.
  */
 fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_paged_kv* kv, const fa_page_table* table,
                           const int* seq_lens, void* o, float* lse, float* scores, int B, int Hq, int window,
@@ -390,7 +396,7 @@ size_t fa_paged_decode_workspace_bytes(int B, int Hq, int Hkv, int d, int page_s
  * caller then uses dst as the sequences' block table and frees the old pages.
  * Keys keep the rotation they were stored with; slots are no longer positions.
  * dst->max_pages * page_size >= budget >= 1, sinks + recent <= budget
- * (FA_ERR_BAD_ARGUMENT).
+ * (FA_ERR_BAD_ARGUMENT).  Two launches.
  */
 fa_status fa_paged_evict(const fa_paged_kv* kv, float* scores, const fa_page_table* table, const int* seq_lens,
                          const fa_page_table* dst, int* new_lens, int* kept, int B, int budget, int recent, int sinks,

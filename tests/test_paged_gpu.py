@@ -292,6 +292,30 @@ def test_decode_rising_scores(cuda_lib):
     assert_decoded(o, lse, q, k, v, table, ln, 0.5, 0, scores, torch.zeros_like(scores), "rising")
 
 
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("gap", [12.0, 17.5, 20.0])
+def test_decode_many_small_weights(cuda_lib, dt, gap):
+    # One key of score `gap` and value 1, all others of score 0 and value 3000:
+    # weights of e^-17.5 = 2^-25.2 are below what fp16 holds next to 1, and yet
+    # 4000 of them carry a quarter of the result.
+    n, d = 4000, 64
+    k, v, table, ln = filled([n], 1, 64, d, dt, seed=18)
+    k.zero_()
+    v.fill_(3000.0)
+    p, s = table[0, 20].item(), 7
+    k[p, 0, s, 0] = gap
+    v[p, 0, s] = 1.0
+    q = torch.zeros((1, 2, d), dtype=dt, device=DEV)
+    q[:, :, 0] = 1.0
+    o, lse = fa.paged_decode(q, k, v, table, ln, scale=1.0)
+    ok()
+    w = n * math.exp(-gap)
+    want = (1.0 + (w - math.exp(-gap)) * 3000.0) / (1.0 + w - math.exp(-gap))
+    # The weights' and the result's rounding, and fp32 sums of n terms.
+    assert (o.double() / want - 1).abs().max().item() <= 2.1 * U[dt] + n * 2.0 ** -23
+    assert abs(lse[0, 0].item() - math.log(math.exp(gap) + n - 1)) <= n * 2.0 ** -24 + 2.0 ** -20
+
+
 def test_decode_pages_shared_by_sequences(cuda_lib):
     # Two sequences with a common prefix: the weights of both add up.
     k, v, table, ln = filled([200, 200], 2, 16, 64, BF, seed=12)

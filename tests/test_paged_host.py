@@ -216,6 +216,7 @@ POOL_ERRORS = [
     (dict(kv=pool(v=A + 1024)), fa.FA_ERR_ALIASING),          # k's and v's pages overlap
     (dict(table=None), fa.FA_ERR_NULL_PTR),
     (dict(table=table(max_pages=0)), fa.FA_ERR_BAD_SHAPE),
+    (dict(table=table(max_pages=2 ** 26 + 1)), fa.FA_ERR_BAD_SHAPE),       # more than 2^30 keys a sequence
     (dict(table=table(pages=5 * A + 2)), fa.FA_ERR_MISALIGNED),
     (dict(table=table(pages=A)), fa.FA_ERR_ALIASING),
     (dict(seq_lens=None), fa.FA_ERR_NULL_PTR),
@@ -277,6 +278,7 @@ def test_decode_workspace(lib):
     assert 0 < f(2, 4, 2, 64, 16, 4, 0) <= f(2, 4, 2, 64, 16, 4, 1) <= WS
     assert f(2, 4, 3, 64, 16, 4, 0) == 0 and f(2, 4, 2, 96, 16, 4, 0) == 0 and f(0, 4, 2, 64, 16, 4, 0) == 0
     assert f(2, 4, 2, 64, 20, 4, 0) == 0 and f(2, 4, 2, 64, 16, 0, 0) == 0
+    assert f(1, 1, 1, 64, 16, 2 ** 26, 0) > 0 and f(1, 1, 1, 64, 16, 2 ** 26 + 1, 0) == 0
     valid(decode)
 
 
@@ -293,6 +295,7 @@ def evict(**kw):
     (dict(dst=None), fa.FA_ERR_NULL_PTR),
     (dict(budget=0), fa.FA_ERR_BAD_ARGUMENT),
     (dict(budget=65), fa.FA_ERR_BAD_ARGUMENT),                # more than dst's pages hold
+    (dict(dst=table(pages=5 * A + 4096, max_pages=2 ** 26 + 1)), fa.FA_ERR_BAD_SHAPE),
     (dict(recent=-1), fa.FA_ERR_BAD_ARGUMENT),
     (dict(recent=10, sinks=11), fa.FA_ERR_BAD_ARGUMENT),
     (dict(recent=2 ** 31 - 1, sinks=2 ** 31 - 1), fa.FA_ERR_BAD_ARGUMENT),
