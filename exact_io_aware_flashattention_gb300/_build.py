@@ -23,7 +23,7 @@ LIB_NAME = "libfa_gb300.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_rope.cu", "fa_paged.cu", "fa_evict.cu"]
-HEADERS = ["sm103a.cuh", "fa_internal.h"]
+HEADERS = ["sm103a.cuh", "fa_internal.h", "fa_paged.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

@@ -15,6 +15,7 @@
 #include <utility>
 
 #include "fa_internal.h"
+#include "fa_paged.h"
 
 namespace {
 
@@ -92,6 +93,7 @@ constexpr int kMaxDevices = 64;
 
 struct DeviceState {
   bool ready = false;
+  bool paged_ready = false;   // the paged-cache and rotary kernels too
   bool unusable = false;   // a kernel's drain gave up: no further launches on this device
   int num_sms = 0;
   int* status = nullptr;
@@ -907,6 +909,19 @@ DecodeWs decode_ws(int B, int Hq, int d, int page_size, int max_pages, bool with
   return w;
 }
 
+// device_state, with the kernels of this section set up (on their first use,
+// so that callers of the attention alone do not wait for it).
+fa_status paged_device_state(DeviceState** out) {
+  FA_TRY(device_state(out));
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!(*out)->paged_ready) {
+    const cudaError_t e = fa::configure_paged_kernels();
+    if (e != cudaSuccess) return launch_status(e);
+    (*out)->paged_ready = true;
+  }
+  return FA_OK;
+}
+
 // Each output apart from every input and every other output.
 template <size_t NO, size_t NI>
 bool outputs_apart(const View (&outs)[NO], const View (&ins)[NI]) {
@@ -959,7 +974,7 @@ fa_status fa_rope(const void* q, const long long* q_strides, void* q_out, const 
       if (!apart(views[i], t)) return FA_ERR_ALIASING;
   }
   DeviceState* ds = nullptr;
-  FA_TRY(device_state(&ds));
+  FA_TRY(paged_device_state(&ds));
   const fa::RopeArgs a{rows[0], rows[1], rows[2], rows[3], B, Hq, Hk, N, d, rotary_args(rotary, inverse)};
   return launch_status(fa::launch_rope(dtype, a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
 }
@@ -1018,7 +1033,7 @@ fa_status fa_paged_append(const fa_paged_kv* kv, const fa_page_table* table, con
       if (!apart(outs[i], small[j])) return FA_ERR_ALIASING;
   }
   DeviceState* ds = nullptr;
-  FA_TRY(device_state(&ds));
+  FA_TRY(paged_device_state(&ds));
   fa::AppendArgs a{};
   a.k = rows[0];
   a.v = rows[1];
@@ -1068,7 +1083,7 @@ fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_pa
                        bytes_view(workspace, need), scores ? scores_view(kv, scores) : bytes_view(nullptr, 0)};
   if (!outputs_apart(outs, ins)) return FA_ERR_ALIASING;
   DeviceState* ds = nullptr;
-  FA_TRY(device_state(&ds));
+  FA_TRY(paged_device_state(&ds));
   fa::DecodeArgs a{};
   a.q = q;
   a.q_sb = stride_of(B, q_strides[0]);
@@ -1126,7 +1141,7 @@ fa_status fa_paged_evict(const fa_paged_kv* kv, float* scores, const fa_page_tab
                        bytes_view(kept, (size_t)B * kv->Hkv * budget * 4)};
   if (!outputs_apart(outs, ins) || dst->pages == table->pages) return FA_ERR_ALIASING;
   DeviceState* ds = nullptr;
-  FA_TRY(device_state(&ds));
+  FA_TRY(paged_device_state(&ds));
   fa::EvictArgs a{};
   a.kv = kv_args(kv);
   a.scores = scores;

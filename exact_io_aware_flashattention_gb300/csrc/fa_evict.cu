@@ -27,7 +27,7 @@
 // one up each (index, source page, target page) and move its score, then the
 // rows go 16 bytes a lane, all loads in flight before the first store.  (16 or
 // 32 keys a warp, in rounds of 8 or 4, fill the last wave worse: 2-5 % slower.)
-#include "fa_internal.h"
+#include "fa_paged.h"
 #include "sm103a.cuh"
 
 namespace fa {

@@ -31,7 +31,7 @@
 // by one 8x8 transpose in registers.  At one query row per head the tensor
 // work is 1-2 % of what the copies take, so the tcgen05 path, whose 128-row
 // tiles would be filled 1/16 by a group of 8, has nothing to win here.
-#include "fa_internal.h"
+#include "fa_paged.h"
 #include "sm103a.cuh"
 
 #include <cuda_fp16.h>
@@ -950,7 +950,7 @@ cudaError_t configure_decode() {
 
 }  // namespace
 
-cudaError_t configure_paged_kernels() {
+cudaError_t configure_decode_kernels() {
   cudaError_t e = configure_decode<__nv_bfloat16, 64>();
   if (e == cudaSuccess) e = configure_decode<__nv_bfloat16, 128>();
   if (e == cudaSuccess) e = configure_decode<__half, 64>();

@@ -22,7 +22,7 @@
 // one token and eight pairs (two 16-byte vectors of a row): its eight
 // cosines and sines are formed once and used for every head, so the
 // trigonometry costs 1/(Hq + Hkv) of a per-element evaluation.
-#include "fa_internal.h"
+#include "fa_paged.h"
 #include "sm103a.cuh"
 
 #include <cuda_fp16.h>
