@@ -423,23 +423,36 @@ def _check_dense(t, name, shape, dtype, dev):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _first(t, name, dims, what):
-    """(shape, CUDA device index, dtype code) of a call's first tensor."""
+_torch = None           # the torch module, and its queries of the current device and stream,
+_current_device = None  # once the first call has imported it
+_current_stream = None
+
+
+def _load_torch():
+    global _torch, _current_device, _current_stream
     import torch
-    if not isinstance(t, torch.Tensor):
+    _torch, _current_device, _current_stream = torch, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _first(t, name, dims, what):
+    """(shape, CUDA device index, dtype code, dtype) of a call's first tensor."""
+    if _torch is None:
+        _load_torch()
+    if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must be a {what} tensor, got shape {tuple(t.shape)}")
-    dt = t.dtype
-    if dt is torch.bfloat16:
+    shape, dt = t.shape, t.dtype
+    if len(shape) != dims:
+        raise ValueError(f"{name} must be a {what} tensor, got shape {tuple(shape)}")
+    if dt is _torch.bfloat16:
         code = FA_BF16
-    elif dt is torch.float16:
+    elif dt is _torch.float16:
         code = FA_FP16
     else:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {dt}")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
-    return t.shape, t.get_device(), code
+    return shape, dev, code, dt
 
 
 def _raw_stream(dev, stream):
@@ -448,10 +461,7 @@ def _raw_stream(dev, stream):
     ``_on``, so that what it allocates belongs to the stream it runs on (the
     caching allocator would else hand a workspace on to another stream while the
     kernels still use it)."""
-    from torch import _C
-    if stream is None and dev == _C._cuda_getDevice():
-        return _C._cuda_getCurrentRawStream(dev)
-    return None
+    return _current_stream(dev) if stream is None and dev == _current_device() else None
 
 
 @contextlib.contextmanager
@@ -466,16 +476,15 @@ def _on(dev, stream):
 
 def _rotary(positions, inv_freq, axes, interleaved, d, lead, dev):
     """fa_rotary of positions [n_axes, *lead] int32, inv_freq [rot/2] float64, axes [rot/2] int32."""
-    import torch
     try:
         n_axes, n, st = positions.shape[0], inv_freq.shape[0], positions.stride()
     except (AttributeError, IndexError):
         raise ValueError("rotary positions need positions, inv_freq and axes as tensors") from None
-    pos = _check_view(positions, "positions", (n_axes, *lead), torch.int32, dev)
+    pos = _check_view(positions, "positions", (n_axes, *lead), _torch.int32, dev)
     if n < 1 or 2 * n > d:
         raise ValueError(f"inv_freq has {n} frequencies, expected 1 to {d // 2}")
-    w = _check_dense(inv_freq, "inv_freq", (n,), torch.float64, dev)
-    ax = _check_dense(axes, "axes", (n,), torch.int32, dev)
+    w = _check_dense(inv_freq, "inv_freq", (n,), _torch.float64, dev)
+    ax = _check_dense(axes, "axes", (n,), _torch.int32, dev)
     return _pack_rotary(pos, st[0], st[1] if len(lead) == 2 else 0, w, ax, n_axes, 2 * n, 1 if interleaved else 0)
 
 
@@ -494,13 +503,11 @@ def rope_frequencies(sections, base: float = 10000.0, device="cuda"):
 
 
 def _rope(q, k, positions, inv_freq, axes, interleaved, inverse, q_out, k_out, stream):
-    import torch
-    (B, Hq, N, d), dev, code = _first(q, "q", 4, "[B, Hq, N, d]")
-    dt = q.dtype
+    (B, Hq, N, d), dev, code, dt = _first(q, "q", 4, "[B, Hq, N, d]")
     qp = _check_view(q, "q", q.shape, dt, dev)
     Hk, kp, ks = 0, None, None
     if k is not None:
-        Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+        Hk = k.shape[1] if isinstance(k, _torch.Tensor) and k.dim() == 4 else 0
         kp = _check_view(k, "k", (B, Hk, N, d), dt, dev)
         ks = _pack3(*k.stride()[:3])
     elif k_out is not None:
@@ -511,14 +518,14 @@ def _rope(q, k, positions, inv_freq, axes, interleaved, inverse, q_out, k_out, s
         with _on(dev, stream):
             return _rope(q, k, positions, inv_freq, axes, interleaved, inverse, q_out, k_out, None)
     if q_out is None:
-        q_out = torch.empty((B, Hq, N, d), dtype=dt, device=q.device)
+        q_out = _torch.empty((B, Hq, N, d), dtype=dt, device=q.device)
         op = q_out.data_ptr()
     else:
         op = _check_view(q_out, "q_out", (B, Hq, N, d), dt, dev)
     okp, oks = None, None
     if k is not None:
         if k_out is None:
-            k_out = torch.empty((B, Hk, N, d), dtype=dt, device=q.device)
+            k_out = _torch.empty((B, Hk, N, d), dtype=dt, device=q.device)
             okp = k_out.data_ptr()
         else:
             okp = _check_view(k_out, "k_out", (B, Hk, N, d), dt, dev)
@@ -547,9 +554,7 @@ def rope_backward(dq, dk, positions, inv_freq, axes, interleaved: bool = False, 
 
 def _paged(k_cache, v_cache, block_table, seq_lens):
     """Checked cache tensors: (shape, device index, dtype, fa_paged_kv, fa_page_table, B, seq_lens address)."""
-    import torch
-    shape, dev, code = _first(k_cache, "k_cache", 4, "[pages, Hkv, page_size, d]")
-    dt = k_cache.dtype
+    shape, dev, code, dt = _first(k_cache, "k_cache", 4, "[pages, Hkv, page_size, d]")
     kp = _check_view(k_cache, "k_cache", shape, dt, dev)
     vp = _check_view(v_cache, "v_cache", shape, dt, dev)
     st = k_cache.stride()
@@ -558,13 +563,12 @@ def _paged(k_cache, v_cache, block_table, seq_lens):
     P, Hkv, ps, d = shape
     table, B = _table(block_table, "block_table", dev)
     return (shape, dev, dt, _pack_kv(kp, vp, st[0], st[1], st[2], P, ps, Hkv, d, code), table, B,
-            _check_dense(seq_lens, "seq_lens", (B,), torch.int32, dev))
+            _check_dense(seq_lens, "seq_lens", (B,), _torch.int32, dev))
 
 
 def _table(t, name, dev):
-    import torch
-    shape = t.shape if isinstance(t, torch.Tensor) and t.dim() == 2 else ("B", "pages")
-    return _pack_table(_check_view(t, name, shape, torch.int32, dev), t.stride()[0], shape[1]), shape[0]
+    shape = t.shape if isinstance(t, _torch.Tensor) and t.dim() == 2 else ("B", "pages")
+    return _pack_table(_check_view(t, name, shape, _torch.int32, dev), t.stride()[0], shape[1]), shape[0]
 
 
 def paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens=None, q=None, positions=None, inv_freq=None,
@@ -579,9 +583,8 @@ def paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens=None,
     (into ``q_out``, which may be q); rows of padding tokens are not written.
     ``scores`` [pages,Hkv,page_size] fp32 gets 0 for the new tokens.  See
     fa_paged_append."""
-    import torch
     (_, Hkv, _, d), dev, dt, kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
-    T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+    T = k.shape[0] if isinstance(k, _torch.Tensor) and k.dim() == 3 else 0
     kp = _check_view(k, "k", (T, Hkv, d), dt, dev)
     vp = _check_view(v, "v", (T, Hkv, d), dt, dev)
     if cu_seqlens is None:
@@ -589,14 +592,14 @@ def paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens=None,
         if T != B:
             raise ValueError(f"{T} tokens for {B} sequences without cu_seqlens")
     else:
-        cu = _check_dense(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
+        cu = _check_dense(cu_seqlens, "cu_seqlens", (B + 1,), _torch.int32, dev)
     rot = None
     if positions is not None or inv_freq is not None or axes is not None:
         rot = _rotary(positions, inv_freq, axes, interleaved, d, (T,), dev)
-    sp = None if scores is None else _check_dense(scores, "scores", k_cache.shape[:3], torch.float32, dev)
+    sp = None if scores is None else _check_dense(scores, "scores", k_cache.shape[:3], _torch.float32, dev)
     qp, qs, Hq = None, None, 0
     if q is not None:
-        Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+        Hq = q.shape[1] if isinstance(q, _torch.Tensor) and q.dim() == 3 else 0
         qp = _check_view(q, "q", (T, Hq, d), dt, dev)
         qs = _pack2(*q.stride()[:2])
     elif q_out is not None:
@@ -610,7 +613,7 @@ def paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens=None,
     op, os_ = None, None
     if q is not None:
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+            q_out = _torch.empty((T, Hq, d), dtype=dt, device=q.device)
             op = q_out.data_ptr()
         else:
             op = _check_view(q_out, "q_out", (T, Hq, d), dt, dev)
@@ -644,11 +647,10 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float | None
     0).  ``scores`` [pages,Hkv,page_size] fp32, if given, grows at each visible
     key by its softmax weight summed over the group's heads.  See
     fa_paged_decode."""
-    import torch
     (_, _, _, d), dev, dt, kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
-    Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    Hq = q.shape[1] if isinstance(q, _torch.Tensor) and q.dim() == 3 else 0
     qp = _check_view(q, "q", (B, Hq, d), dt, dev)
-    sp = None if scores is None else _check_dense(scores, "scores", k_cache.shape[:3], torch.float32, dev)
+    sp = None if scores is None else _check_dense(scores, "scores", k_cache.shape[:3], _torch.float32, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
 
@@ -658,21 +660,21 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float | None
             return paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, window, scores, out, lse, workspace)
     device = k_cache.device
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=dt, device=device)
+        out = _torch.empty((B, Hq, d), dtype=dt, device=device)
         op = out.data_ptr()
     else:
         op = _check_dense(out, "out", (B, Hq, d), dt, dev)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
+        lse = _torch.empty((B, Hq), dtype=_torch.float32, device=device)
         lp = lse.data_ptr()
     else:
-        lp = _check_dense(lse, "lse", (B, Hq), torch.float32, dev)
+        lp = _check_dense(lse, "lse", (B, Hq), _torch.float32, dev)
     if workspace is None:
         workspace = paged_decode_workspace(B, Hq, k_cache, block_table, scores is not None)
         n, wp = workspace.numel(), workspace.data_ptr()
     else:
         n = workspace.numel()
-        wp = _check_dense(workspace, "workspace", (n,), torch.uint8, dev)
+        wp = _check_dense(workspace, "workspace", (n,), _torch.uint8, dev)
     status = fa_paged_decode(qp, _pack2(*q.stride()[:2]), kv, table, lens, op, lp, sp, B, Hq, window, scale, wp, n, handle)
     if status:
         _raise(status, "fa_paged_decode")
@@ -687,9 +689,8 @@ def paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budg
     ``dst_table`` [B, >= ceil(budget/page_size)], which must be other pages than
     those in use.  Returns (new_lens [B], kept [B,Hkv,budget]: the indices kept,
     -1 past the new length).  See fa_paged_evict."""
-    import torch
     (_, Hkv, _, _), dev, _, kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
-    sp = _check_dense(scores, "scores", k_cache.shape[:3], torch.float32, dev)
+    sp = _check_dense(scores, "scores", k_cache.shape[:3], _torch.float32, dev)
     dst, rows = _table(dst_table, "dst_table", dev)
     if rows != B:
         raise ValueError(f"dst_table has {rows} rows, expected {B}")
@@ -702,15 +703,15 @@ def paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budg
             return paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budget, recent, sinks, new_lens,
                                kept)
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
+        new_lens = _torch.empty((B,), dtype=_torch.int32, device=k_cache.device)
         np_ = new_lens.data_ptr()
     else:
-        np_ = _check_dense(new_lens, "new_lens", (B,), torch.int32, dev)
+        np_ = _check_dense(new_lens, "new_lens", (B,), _torch.int32, dev)
     if kept is None:
-        kept = torch.empty((B, Hkv, budget), dtype=torch.int32, device=k_cache.device)
+        kept = _torch.empty((B, Hkv, budget), dtype=_torch.int32, device=k_cache.device)
         ip = kept.data_ptr()
     else:
-        ip = _check_dense(kept, "kept", (B, Hkv, budget), torch.int32, dev)
+        ip = _check_dense(kept, "kept", (B, Hkv, budget), _torch.int32, dev)
     status = fa_paged_evict(kv, sp, table, lens, dst, np_, ip, B, budget, recent, sinks, handle)
     if status:
         _raise(status, "fa_paged_evict")

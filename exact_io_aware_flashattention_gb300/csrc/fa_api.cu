@@ -7,6 +7,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -93,7 +94,7 @@ constexpr int kMaxDevices = 64;
 
 struct DeviceState {
   bool ready = false;
-  bool paged_ready = false;   // the paged-cache and rotary kernels too
+  std::atomic<bool> paged_ready{false};   // the paged-cache and rotary kernels too
   bool unusable = false;   // a kernel's drain gave up: no further launches on this device
   int num_sms = 0;
   int* status = nullptr;
@@ -913,6 +914,7 @@ DecodeWs decode_ws(int B, int Hq, int d, int page_size, int max_pages, bool with
 // so that callers of the attention alone do not wait for it).
 fa_status paged_device_state(DeviceState** out) {
   FA_TRY(device_state(out));
+  if ((*out)->paged_ready) return FA_OK;
   std::lock_guard<std::mutex> lock(g_mu);
   if (!(*out)->paged_ready) {
     const cudaError_t e = fa::configure_paged_kernels();

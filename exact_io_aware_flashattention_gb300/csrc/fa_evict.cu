@@ -14,8 +14,8 @@
 //
 // fa_evict_select_kernel.  One cluster of 1, 2, 4 or 8 CTAs per (b, g), each
 // with an equal run of the keys, held in shared memory as order-preserving
-// integers (protected ones as the largest).  The need-th largest of the others
-// is found 11, 11 and 10 bits at a time: every CTA counts its keys that match
+// integers (protected ones as the largest).  The m-th largest is found 11, 11
+// and 10 bits at a time: every CTA counts its keys that match
 // the digits found so far into a histogram, reads the others' histograms
 // through distributed shared memory, and all reach the same digit; three
 // passes over shared memory replace a sort.  It stops early when the digit's
@@ -39,7 +39,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxCached = 49 * 1024;         // keys in shared memory: 196 KB with the histograms
-constexpr uint32_t kProtected = 0xffffffffu;  // above every score's key
+constexpr uint32_t kProtected = 0xffffffffu;  // above every score's key, so taken first
 
 // Order-preserving map of scores to unsigned: larger score, larger key;
 // -0 counts as +0 and NaN as the smallest.
@@ -69,6 +69,11 @@ __device__ __forceinline__ int2 ld_cluster2(const int* p, int rank) {
   asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
+// 16 bytes from global to shared memory, without a register in between.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -121,7 +126,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;                            // the whole cluster does
   }
   const int lo = a.sinks, hi = len - a.recent;     // keys outside [lo, hi) are protected
-  int need = m - a.sinks - a.recent;
   // The CTA's run of keys: a multiple of 4, so that four consecutive keys, one
   // 16-byte load, lie in one page (page sizes are multiples of 16).
   const int run = ((len + cluster - 1) / cluster + 3) & ~3;
@@ -130,44 +134,54 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int* pages = a.table.pages + b * a.table.stride;
   const float* pool = a.scores + (long long)g * ps;
   const long long page_scores = (long long)a.kv.Hkv * ps;
-  // Keys [from, from + n) into shared memory, in fours; past the sequence's
-  // end 0, the smallest: equal keys go by index, so those never come before a
-  // key of the sequence.  n rounded up to 128 is filled.
-  auto load = [&](int from, int n) {
-    constexpr int kBatch = 4;          // page numbers, then scores, in flight per thread
+  // Keys [from, from + n) into shared memory, in fours, and the first digits
+  // into `hist` if given.  Past the sequence's end 0, the smallest: equal keys
+  // go by index, so those never come before a key of the sequence.  n rounded
+  // up to 128 is filled.
+  auto load = [&](int from, int n, int* hist) {
+    constexpr int kBatch = 8;          // page numbers, then copies, in flight per thread
     const int quads = (n + 127) / 128 * 32;
+    uint4* quad = reinterpret_cast<uint4*>(keys);
     for (int i0 = tid; i0 < quads; i0 += kBatch * kThreads) {
-      int p[kBatch], slot[kBatch];
-      float4 x[kBatch];
+      int p[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int j = from + 4 * (i0 + u * kThreads);
-        const bool in = j < from + n;
-        const int c = in ? page_of(j, a) : 0;
-        p[u] = in ? pages[c] : 0;
-        slot[u] = in ? j - c * ps : 0;
+        p[u] = j < from + n ? pages[page_of(j, a)] : 0;
       }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const bool ok = p[u] >= 0 && p[u] < a.kv.num_pages;
-        if (!ok) record_error(st, kErrBadIndex, kSiteEvictPage);
-        p[u] = ok ? p[u] : 0;          // any page: what such a sequence keeps is unspecified
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) x[u] = *reinterpret_cast<const float4*>(pool + p[u] * page_scores + slot[u]);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int i = i0 + u * kThreads, j = from + 4 * i;
-        if (i >= quads) break;
-        uint4 k = make_uint4(score_key(x[u].x), score_key(x[u].y), score_key(x[u].z), score_key(x[u].w));
+        if (j >= from + n) break;
+        if (p[u] < 0 || p[u] >= a.kv.num_pages) {
+          record_error(st, kErrBadIndex, kSiteEvictPage);
+          p[u] = 0;                    // any page: what such a sequence keeps is unspecified
+        }
+        copy16_async(quad + i, pool + p[u] * page_scores + (j - page_of(j, a) * ps));
+      }
+    }
+    wait_copies();
+    // Each thread turns the scores it copied into keys.
+    for (int i = tid; i < quads; i += kThreads) {
+      const int j = from + 4 * i;
+      uint4 k = make_uint4(0, 0, 0, 0);
+      if (j < from + n) {
+        const float4 x = reinterpret_cast<const float4*>(quad)[i];
+        k = make_uint4(score_key(x.x), score_key(x.y), score_key(x.z), score_key(x.w));
         if (j < lo || j + 4 > hi) {
           uint32_t* y = &k.x;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (j + e < lo || j + e >= hi) y[e] = j + e < len ? kProtected : 0u;
         }
-        reinterpret_cast<uint4*>(keys)[i] = k;
+        if (hist) {
+          atomicAdd(&hist[k.x >> 21], 1);
+          atomicAdd(&hist[k.y >> 21], 1);
+          atomicAdd(&hist[k.z >> 21], 1);
+          atomicAdd(&hist[k.w >> 21], 1);
+        }
       }
+      quad[i] = k;
     }
   };
   // body(from, n) over the run in pieces that fit shared memory.
@@ -176,90 +190,98 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int n = min(cap, j0 + n_run - from);
       if (!cached) {
         __syncthreads();
-        load(from, n);
+        load(from, n, nullptr);
         __syncthreads();
       }
       body(from, n);
     }
   };
   for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
-  if (cached) load(j0, n_run);
   __syncthreads();
 
-  // Without a choice only the protected keys are above the threshold.
-  uint32_t prefix = need > 0 ? 0u : kProtected - 1, mask = need > 0 ? 0u : kProtected;
-  if (need > 0)
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-      int* hist = sh.hist[pass];
+  // The m-th largest key, digit by digit.
+  uint32_t prefix = 0, mask = 0;
+  int need = m;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    int* hist = sh.hist[pass];
+    if (pass == 0) {
+      for (int from = j0; from < j0 + n_run; from += cap) {
+        if (from > j0) __syncthreads();
+        load(from, min(cap, j0 + n_run - from), hist);
+      }
+    } else {
       pieces([&](int, int n) {
         const int quads = (n + 3) / 4;
 #pragma unroll 2
         for (int i = tid; i < quads; i += kThreads) {
           const uint4 k = reinterpret_cast<const uint4*>(keys)[i];
-          auto count = [&](uint32_t x) {
-            if ((x & mask) == prefix && x != kProtected) atomicAdd(&hist[(x >> shift) & ((1u << bits) - 1)], 1);
-          };
-          count(k.x);
-          count(k.y);
-          count(k.z);
-          count(k.w);
-        }
-      });
-      __syncthreads();
-      // Sums of 32 bins, so that the others need to read 64 of them and then
-      // 32 bins, not all 2048.
-      for (int c = warp; c < kBins / 32; c += kWarps) {
-        const int sum = __reduce_add_sync(0xffffffffu, hist[c * 32 + lane]);
-        if (lane == 0) sh.coarse[pass][c] = sum;
-      }
-      if (cluster > 1) cluster_sync(); else __syncthreads();
-      if (warp == 0) {
-        // Largest first: lane l has coarse bins 63 - 2l and 62 - 2l, then bin
-        // 31 - l of the coarse bin in which the running count reaches `need`.
-        int n0 = 0, n1 = 0;
-        if (cluster == 1) {
-          n0 = sh.coarse[pass][63 - 2 * lane];
-          n1 = sh.coarse[pass][62 - 2 * lane];
-        } else {
-          int2 v[kMaxCluster];         // all loads in flight before the first is used
-#pragma unroll
-          for (int r = 0; r < kMaxCluster; ++r) v[r] = ld_cluster2(&sh.coarse[pass][62 - 2 * lane], r < cluster ? r : rank);
-#pragma unroll
-          for (int r = 0; r < kMaxCluster; ++r) {
-            n0 += r < cluster ? v[r].y : 0;
-            n1 += r < cluster ? v[r].x : 0;
+          const bool x = (k.x & mask) == prefix, y = (k.y & mask) == prefix;
+          const bool z = (k.z & mask) == prefix, w = (k.w & mask) == prefix;
+          if (x || y || z || w) {
+            const uint32_t digit = (1u << bits) - 1;
+            if (x) atomicAdd(&hist[(k.x >> shift) & digit], 1);
+            if (y) atomicAdd(&hist[(k.y >> shift) & digit], 1);
+            if (z) atomicAdd(&hist[(k.z >> shift) & digit], 1);
+            if (w) atomicAdd(&hist[(k.w >> shift) & digit], 1);
           }
         }
-        int before = warp_scan(n0 + n1) - n0 - n1;
-        const bool here0 = before < need && before + n0 >= need;
-        const bool here1 = before + n0 < need && before + n0 + n1 >= need;
-        const int src = __ffs(__ballot_sync(0xffffffffu, here0 || here1)) - 1;
-        const int coarse = __shfl_sync(0xffffffffu, here0 ? 63 - 2 * lane : 62 - 2 * lane, src);
-        const int rest = need - __shfl_sync(0xffffffffu, here0 ? before : before + n0, src);
-        int c = 0;
-        if (cluster == 1) {
-          c = hist[coarse * 32 + 31 - lane];
-        } else {
-          int v[kMaxCluster];
+      });
+    }
+    __syncthreads();
+    // Sums of 32 bins, so that the others need to read 64 of them and then 32
+    // bins, not all 2048.
+    for (int c = warp; c < kBins / 32; c += kWarps) {
+      const int sum = __reduce_add_sync(0xffffffffu, hist[c * 32 + lane]);
+      if (lane == 0) sh.coarse[pass][c] = sum;
+    }
+    if (cluster > 1) cluster_sync(); else __syncthreads();
+    if (warp == 0) {
+      // Largest first: lane l has coarse bins 63 - 2l and 62 - 2l, then bin
+      // 31 - l of the coarse bin in which the running count reaches `need`.
+      int n0 = 0, n1 = 0;
+      if (cluster == 1) {
+        n0 = sh.coarse[pass][63 - 2 * lane];
+        n1 = sh.coarse[pass][62 - 2 * lane];
+      } else {
+        int2 v[kMaxCluster];           // all loads in flight before the first is used
 #pragma unroll
-          for (int r = 0; r < kMaxCluster; ++r) v[r] = ld_cluster(&hist[coarse * 32 + 31 - lane], r < cluster ? r : rank);
+        for (int r = 0; r < kMaxCluster; ++r) v[r] = ld_cluster2(&sh.coarse[pass][62 - 2 * lane], r < cluster ? r : rank);
 #pragma unroll
-          for (int r = 0; r < kMaxCluster; ++r) c += r < cluster ? v[r] : 0;
-        }
-        before = warp_scan(c) - c;
-        if (before < rest && before + c >= rest) {
-          sh.bin = coarse * 32 + 31 - lane;
-          sh.left = rest - before;
-          sh.whole = rest - before == c;
+        for (int r = 0; r < kMaxCluster; ++r) {
+          n0 += r < cluster ? v[r].y : 0;
+          n1 += r < cluster ? v[r].x : 0;
         }
       }
-      __syncthreads();
-      prefix |= (uint32_t)sh.bin << shift;
-      mask |= ((1u << bits) - 1) << shift;
-      need = sh.left;
-      if (sh.whole) break;             // every key with these digits stays
+      int before = warp_scan(n0 + n1) - n0 - n1;
+      const bool here0 = before < need && before + n0 >= need;
+      const bool here1 = before + n0 < need && before + n0 + n1 >= need;
+      const int src = __ffs(__ballot_sync(0xffffffffu, here0 || here1)) - 1;
+      const int coarse = __shfl_sync(0xffffffffu, here0 ? 63 - 2 * lane : 62 - 2 * lane, src);
+      const int rest = need - __shfl_sync(0xffffffffu, here0 ? before : before + n0, src);
+      int c = 0;
+      if (cluster == 1) {
+        c = hist[coarse * 32 + 31 - lane];
+      } else {
+        int v[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) v[r] = ld_cluster(&hist[coarse * 32 + 31 - lane], r < cluster ? r : rank);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) c += r < cluster ? v[r] : 0;
+      }
+      before = warp_scan(c) - c;
+      if (before < rest && before + c >= rest) {
+        sh.bin = coarse * 32 + 31 - lane;
+        sh.left = rest - before;
+        sh.whole = rest - before == c;
+      }
     }
+    __syncthreads();
+    prefix |= (uint32_t)sh.bin << shift;
+    mask |= ((1u << bits) - 1) << shift;
+    need = sh.left;
+    if (sh.whole) break;               // every key with these digits stays
+  }
   // A key stays if its digits are above the threshold's, or equal and it is
   // among the first `need` such keys.  Each warp takes a run of a piece, 128
   // keys at a time, four consecutive ones a lane.
