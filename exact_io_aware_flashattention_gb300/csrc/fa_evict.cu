@@ -27,6 +27,13 @@
 // one up each (index, source page, target page) and move its score, then the
 // rows go 16 bytes a lane, all loads in flight before the first store.  (16 or
 // 32 keys a warp, in rounds of 8 or 4, fill the last wave worse: 2-5 % slower.)
+//
+// Measured: 2 sequences of 131072 keys, 8 heads, d = 128, to 32768: 104 us, of
+// which the selection 20 and the copy of 541 MB 82 (97 % of the 6.79 TB/s copy
+// rate); 16 sequences of 0 to 8192 keys to 2048: 43 us, the copy of 202 MB 32;
+// one of 1000 keys, 2 heads: 7.4 us.  The selection is bound by instructions
+// and latencies: of its 35 thousand cycles at 16384 keys a CTA the loads take
+// 7, the histograms 7, the exchanges over the cluster 10, the list 10.
 #include "fa_paged.h"
 #include "sm103a.cuh"
 

@@ -28,8 +28,8 @@ import pytest
 import torch
 
 import exact_io_aware_flashattention_gb300 as fa
-from oracle import paged
-from tests.parity import GuardedBuffers
+from oracle import paged, ref
+from tests.parity import GRAD_REL_L2, GuardedBuffers, rel_l2
 
 pytestmark = pytest.mark.gpu
 
@@ -141,6 +141,29 @@ def test_rope_gradient_is_the_transpose(cuda_lib):
     ok()
     # Two roundings of values at most |x| + |y| each.
     assert (back.float() - x.float()).abs().max().item() <= 4 * U[HF] * 2 * x.float().abs().max().item()
+
+
+@pytest.mark.parametrize("deterministic", [False, True])
+def test_rope_in_a_training_step(cuda_lib, deterministic):
+    # rope, attention, its backward, rope_backward: gradients of the unturned q
+    # and k against the oracle from the same turned tensors.
+    B, Hq, Hk, N, d = 1, 4, 2, 300, 64
+    g = torch.Generator().manual_seed(11)
+    q, k, v, do = (torch.randn((B, h, N, d), generator=g).to(BF).to(DEV) for h in (Hq, Hk, Hk, Hq))
+    pos = torch.stack([torch.arange(N) // 100, torch.arange(N) // 10 % 10, torch.arange(N) % 10]).to(torch.int32)
+    pos = pos[:, None].expand(3, B, N).to(DEV)
+    w, axes = fa.rope_frequencies((8, 12, 12), device=DEV)
+    qr, kr = fa.rope(q, k, pos, w, axes)
+    o, lse = fa.forward(qr, kr, v, causal=True)
+    dqr, dkr, dv = fa.backward(qr, kr, v, o, lse, do, causal=True, deterministic=deterministic)
+    dq, dk = fa.rope_backward(dqr, dkr, pos, w, axes)
+    ok()
+    rq, rk, rv = ref.attention_backward(f64(qr), f64(kr), f64(v), f64(do), True, d ** -0.5)
+    turn_back = lambda x: paged.rotate(x, pos.cpu().numpy(), w.cpu().numpy(), axes.cpu().numpy(), inverse=True)  # noqa: E731
+    # A rotation keeps norms, so the attention's tolerance carries over; the
+    # rotated gradients are rounded once more.
+    for got, want, name in ((dq, turn_back(rq), "dq"), (dk, turn_back(rk), "dk"), (dv, rv, "dv")):
+        assert rel_l2(f64(got), want) <= GRAD_REL_L2 + U[BF], name
 
 
 def test_rope_bad_axis_is_recorded(cuda_lib):
