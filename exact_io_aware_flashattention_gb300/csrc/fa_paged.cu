@@ -50,6 +50,7 @@ namespace {
 
 constexpr int kConsumers = 4;                      // warps, one 16-key slice of a tile each
 constexpr int kThreads = (kConsumers + 1) * 32;
+
 // Wait-site ids.
 enum : int { kSiteFull = 47, kSiteEmpty = 48, kDrainFull = 49 };
 
@@ -234,7 +235,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   // On its way while the barriers are set up.
   const int first_len = (int)threadIdx.x < a.B ? a.seq_lens[threadIdx.x] : 0;
   if ((smem_u32(smem) & 1023u) != 0) {
-    if (threadIdx.x == 0) record_error(st, kErrDeviceTimeout, 0);
+    if (threadIdx.x == 0) {
+      record_error(st, kErrDeviceTimeout, 0);
+      a.parts[blockIdx.x].left = 0;
+    }
     return;
   }
   if (threadIdx.x == 0) {

@@ -286,6 +286,34 @@ def test_decode(cuda_lib, lens, Hq, Hkv, d, page, window, dt, layout, with_score
     assert_decoded(o, lse, q, k, v, table, ln, scale, window, scores, before, f"{lens}")
 
 
+def spread(B, longest, seed):
+    """Lengths of a batch: some empty, some of one key, the rest anything."""
+    g = torch.Generator().manual_seed(seed)
+    return [[0, 1, int(x)][int(p)] if p < 2 else int(x)
+            for x, p in zip(torch.randint(1, longest + 1, (B,), generator=g), torch.randint(0, 12, (B,), generator=g))]
+
+
+@pytest.mark.parametrize("with_scores", [False, True])
+@pytest.mark.parametrize("B,longest,Hq,Hkv,d,page,window,dt", [
+    (40, 900, 8, 4, 128, 16, 0, BF),        # several tiles a CTA, units cut in two
+    (24, 900, 16, 8, 64, 32, 0, HF),
+    (30, 700, 16, 1, 128, 48, 0, BF),       # sixteen heads a group
+    (16, 900, 40, 2, 64, 16, 200, BF),      # two head chunks, a window
+    (161, 60, 2, 1, 64, 16, 0, BF),         # one sequence more than a block has threads
+    (700, 70, 2, 2, 64, 16, 0, HF),
+])
+def test_decode_batches(cuda_lib, B, longest, Hq, Hkv, d, page, window, dt, with_scores):
+    lens = spread(B, longest, seed=B)
+    k, v, table, ln = filled(lens, Hkv, page, d, dt, seed=B + 1)
+    g = torch.Generator().manual_seed(B + 2)
+    q = torch.randn((B, Hq, d), generator=g).to(dt).to(DEV)
+    scores = torch.rand(k.shape[:3], generator=g).to(DEV) if with_scores else None
+    before = scores.clone() if with_scores else None
+    o, lse = fa.paged_decode(q, k, v, table, ln, window=window, scores=scores)
+    ok()
+    assert_decoded(o, lse, q, k, v, table, ln, d ** -0.5, window, scores, before, f"batch of {B}")
+
+
 @pytest.mark.parametrize("sigma,scale", [(4.0, 0.3), (0.0, 1.0)])
 def test_decode_peaked_and_flat(cuda_lib, sigma, scale):
     # Scores of +-50 and more: single keys dominate and the running maximum
@@ -416,6 +444,36 @@ def test_decode_offsets_past_32_bits(cuda_lib):
         assert kept[0, h].tolist() == want
         assert torch.equal(ks[4:, h].reshape(-1, d)[:100], ks[:4, h].reshape(-1, d)[want])
         assert torch.equal(vs[4:, h].reshape(-1, d)[:100], vs[:4, h].reshape(-1, d)[want])
+
+
+def test_decode_workspace_past_32_bits(cuda_lib):
+    # Block tables with room for 2^20 keys a sequence: the stashed scores of the
+    # last sequences lie more than 2^32 elements into the workspace.
+    B, Hq, Hkv, d = 66, 64, 2, 64
+    k, v, table, ln = filled([20 + b % 7 for b in range(B)], Hkv, 16, d, BF, seed=16)
+    wide = torch.full((B, 2 ** 16), 2 ** 30, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    g = torch.Generator().manual_seed(17)
+    q = torch.randn((B, Hq, d), generator=g).to(BF).to(DEV)
+    scores = torch.zeros(k.shape[:3], device=DEV)
+    assert fa.fa_paged_decode_workspace_bytes(B, Hq, Hkv, d, 16, 2 ** 16, 1) > 2 ** 34
+    o, lse = fa.paged_decode(q, k, v, wide, ln, scores=scores)
+    ok()
+    assert_decoded(o, lse, q, k, v, table, ln, 0.125, 0, scores, torch.zeros_like(scores), "wide table")
+
+
+def test_rope_offsets_past_32_bits(cuda_lib):
+    N, d = 2 ** 24 + 40, 128                    # 2^31 elements and a few rows
+    x = torch.empty((1, 1, N, d), dtype=BF, device=DEV)
+    x[:, :, :64].normal_()
+    x[:, :, -64:].normal_()
+    head, tail = x[:, :, :64].clone(), x[:, :, -64:].clone()
+    pos = torch.arange(N, dtype=torch.int32, device=DEV).view(1, 1, N)
+    w, axes = fa.rope_frequencies((64,), device=DEV)
+    fa.rope(x, None, pos, w, axes, q_out=x)
+    ok()
+    assert_rotated(x[:, :, :64], head, pos[:, :, :64], w, axes, False, False, "first rows")
+    assert_rotated(x[:, :, -64:], tail, pos[:, :, -64:], w, axes, False, False, "last rows")
 
 
 # ---------------------------------------------------------------------------
@@ -787,6 +845,59 @@ def test_step_in_a_captured_graph(cuda_lib):
     o3, l3 = step()
     ok()
     assert torch.equal(a[rows], o3[rows]) and torch.equal(l, l3)
+
+
+def test_captured_decode_follows_lengths_and_tables(cuda_lib):
+    # A graph captured for one batch replays for others: lengths, pages and
+    # queries change in place, as a serving loop changes them.
+    k, v, table, ln = filled([300, 40, 0, 129], 2, 16, 64, BF, seed=71)
+    g = torch.Generator().manual_seed(72)
+    q = torch.randn((4, 8, 64), generator=g).to(BF).to(DEV)
+    scores = torch.zeros(k.shape[:3], device=DEV)
+    fa.paged_decode(q, k, v, table, ln, scores=scores)
+    ok()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = fa.paged_decode(q, k, v, table, ln, scores=scores)
+    tables = [table.clone(), table[[3, 0, 1, 2]].clone(), table[[1, 1, 0, 3]].clone()]
+    for t, n in zip(tables, ([300, 40, 0, 129], [100, 299, 33, 0], [7, 40, 16, 1])):
+        table.copy_(t)
+        ln.copy_(torch.tensor(n, dtype=torch.int32))
+        q.copy_(torch.randn((4, 8, 64), generator=g))
+        scores.zero_()
+        graph.replay()
+        ok()
+        assert_decoded(o, lse, q, k, v, table, ln, 0.125, 0, scores, torch.zeros_like(scores), f"{n}")
+
+
+def test_calls_from_two_threads(cuda_lib):
+    import threading
+    steps = [one_step(), one_step(dt=HF, lens=(700, 64, 0, 9))]
+    want = [s[0]() for s in steps]
+    ok()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            stream.wait_stream(torch.cuda.default_stream())
+            with torch.cuda.stream(stream):
+                got[i] = [steps[i][0]() for _ in range(30)]
+            stream.synchronize()
+        except Exception as e:          # reported by the test's thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    ok()
+    assert not errors, errors
+    for i, skip in enumerate((1, 2)):
+        rows = torch.tensor([r for r in range(4) if r != skip], device=DEV)
+        for o, l in got[i]:
+            assert torch.equal(o[rows], want[i][0][rows]) and torch.equal(l, want[i][1])
 
 
 def test_steps_on_two_streams(cuda_lib):
