@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     wait_copies();
+    if (hist) __syncthreads();         // the histogram is empty by now
     // Each thread turns the scores it copied into keys.
     for (int i = tid; i < quads; i += kThreads) {
       const int j = from + 4 * i;
@@ -204,7 +205,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   };
   for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
-  __syncthreads();
 
   // The m-th largest key, digit by digit.
   uint32_t prefix = 0, mask = 0;
@@ -213,10 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     int* hist = sh.hist[pass];
     if (pass == 0) {
-      for (int from = j0; from < j0 + n_run; from += cap) {
-        if (from > j0) __syncthreads();
-        load(from, min(cap, j0 + n_run - from), hist);
-      }
+      for (int from = j0; from < j0 + n_run; from += cap) load(from, min(cap, j0 + n_run - from), hist);
     } else {
       pieces([&](int, int n) {
         const int quads = (n + 3) / 4;
@@ -289,13 +286,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     need = sh.left;
     if (sh.whole) break;               // every key with these digits stays
   }
-  // A key stays if its digits are above the threshold's, or equal and it is
-  // among the first `need` such keys.  Each warp takes a run of a piece, 128
-  // keys at a time, four consecutive ones a lane.
-  const uint32_t below = (1u << lane) - 1;
+  // A key stays if its digits are above `bound`, or, where only some of the
+  // keys with the last digits found are wanted (ties), equal to it and among
+  // the first `need` such keys.  Each warp takes a run of a piece, 128 keys at a
+  // time, four consecutive ones a lane.  (Without ties the last digits are at
+  // least 1: all digits 0 would mean that every key stays.)
+  const bool ties = !sh.whole;
+  const uint32_t bound = ties ? prefix : prefix - 1, below = (1u << lane) - 1;
   int above_before = 0, equal_before = 0;          // of the CTAs before, then of the pieces before
-  // Keys above and equal to the threshold in the warp's run of a piece, then
-  // per warp in shared memory.
+  // Keys above and equal to the bound in the warp's run of a piece, then per
+  // warp in shared memory.
   auto warp_run = [&](int n, int& i0, int& i1) {
     const int per = ((n + kWarps - 1) / kWarps + 127) & ~127;
     i0 = min(n, warp * per);
@@ -306,8 +306,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     warp_run(n, i0, i1);
     for (int i = i0 + 4 * lane; i < i1; i += 128) {
       const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
-      above += ((k.x & mask) > prefix) + ((k.y & mask) > prefix) + ((k.z & mask) > prefix) + ((k.w & mask) > prefix);
-      equal += ((k.x & mask) == prefix) + ((k.y & mask) == prefix) + ((k.z & mask) == prefix) + ((k.w & mask) == prefix);
+      above += ((k.x & mask) > bound) + ((k.y & mask) > bound) + ((k.z & mask) > bound) + ((k.w & mask) > bound);
+      if (ties)
+        equal += ((k.x & mask) == bound) + ((k.y & mask) == bound) + ((k.z & mask) == bound) + ((k.w & mask) == bound);
     }
   };
   auto publish = [&](int above, int equal) {
@@ -354,33 +355,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     equal_before += __reduce_add_sync(0xffffffffu, ew);
     int i0, i1;
     warp_run(n, i0, i1);
-    int* out = kept + a0 + min(e0, need);
-    // Keys past the piece's end, up to a whole 128, are 0 or the next keys of
-    // the run: neither counts.
-    for (int i = i0; i < i1; i += 128) {
-      const int at = i + 4 * lane;
-      const uint4 q = *reinterpret_cast<const uint4*>(keys + at);
-      const uint32_t k[4] = {q.x & mask, q.y & mask, q.z & mask, q.w & mask};
-      bool keep[4], eq[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        keep[e] = k[e] > prefix && at + e < i1;
-        eq[e] = k[e] == prefix && at + e < i1;
-      }
-      const int mine = eq[0] + eq[1] + eq[2] + eq[3];
-      if (__any_sync(0xffffffffu, mine)) {
-        int upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, upto, d);
-          if (lane >= d) upto += y;
-        }
-        int r = e0 + upto - mine;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (eq[e]) keep[e] = r++ < need;
-        e0 += __shfl_sync(0xffffffffu, upto, 31);
-      }
+    // Writes the keys of the four flags a lane, in order, from `out` on.
+    auto put = [&](int* out, int at, const bool (&keep)[4]) {
       int pos = 0, total = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -391,7 +367,41 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (keep[e]) out[pos++] = from + at + e;
-      out += total;
+      return total;
+    };
+    if (!ties) {
+      // Past the piece's end, up to a whole 128, lie zeros, never above.
+      int* out = kept + a0;
+#pragma unroll 2
+      for (int i = i0; i < i1; i += 128) {
+        const int at = i + 4 * lane;
+        const uint4 q = *reinterpret_cast<const uint4*>(keys + at);
+        const bool keep[4] = {(q.x & mask) > bound, (q.y & mask) > bound, (q.z & mask) > bound, (q.w & mask) > bound};
+        out += put(out, at, keep);
+      }
+      return;
+    }
+    int* out = kept + a0 + min(e0, need);
+    for (int i = i0; i < i1; i += 128) {
+      const int at = i + 4 * lane;
+      const uint4 q = *reinterpret_cast<const uint4*>(keys + at);
+      const uint32_t k[4] = {q.x & mask, q.y & mask, q.z & mask, q.w & mask};
+      bool keep[4], eq[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        keep[e] = k[e] > bound && at + e < i1;
+        eq[e] = k[e] == bound && at + e < i1;
+      }
+      const int mine = eq[0] + eq[1] + eq[2] + eq[3];
+      if (__any_sync(0xffffffffu, mine)) {
+        const int upto = warp_scan(mine);
+        int r = e0 + upto - mine;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (eq[e]) keep[e] = r++ < need;
+        e0 += __shfl_sync(0xffffffffu, upto, 31);
+      }
+      out += put(out, at, keep);
     }
   });
   if (cluster > 1) cluster_wait();     // nobody exits while its counts are read
