@@ -688,6 +688,80 @@ def test_evict_bad_indices_are_recorded(cuda_lib, bad):
 
 
 # ---------------------------------------------------------------------------
+# Random sweep
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("seed", range(48))
+def test_random_cases(cuda_lib, seed):
+    """Append (ragged or one token), decode and evict on one random cache."""
+    r = np.random.default_rng(seed)
+    pick = lambda *x: x[r.integers(len(x))]  # noqa: E731
+    dt, d, layout = pick(BF, HF), pick(64, 128), pick("hnd", "nhd", "pair")
+    Hkv = int(r.integers(1, 5))
+    Hq = Hkv * int(pick(1, 2, 3, 4, 7, 8, 9, 16, 20))
+    page = int(pick(16, 32, 48, 64, 112, 256))
+    B = int(r.integers(1, 9))
+    lens = [int(x) for x in r.integers(0, pick(20, 200, 900) + 1, B)]
+    budget = int(r.integers(1, max(lens) + 2))
+    recent = int(r.integers(0, budget + 1))
+    sinks = int(r.integers(0, budget - recent + 1))
+    cols = -(-budget // page)
+    kc, vc, table, ln = filled(lens, Hkv, page, d, dt, seed=seed, layout=layout, extra=B * cols + 1,
+                               sigma=float(pick(0.5, 1.0, 2.0)))
+    g = torch.Generator().manual_seed(seed + 1000)
+    sc = torch.rand(kc.shape[:3], generator=g).to(DEV)
+    # Append: the newest tokens once more, with other values.
+    one = r.random() < 0.5
+    new = None if one else [int(r.integers(0, n + 1)) for n in lens]
+    cu = None if one else [sum(new[:b]) for b in range(B + 1)]
+    T = B if one else cu[-1] + int(r.integers(0, 3))
+    x = torch.randn((T, Hq + 2 * Hkv, d), generator=g).to(dt).to(DEV)
+    q, k, v = x.split([Hq, Hkv, Hkv], dim=1)
+    rot, kw, qo, q0 = None, {}, None, None
+    if r.random() < 0.7 and T:
+        n_axes = int(r.integers(1, 4))
+        pairs = 8 * int(r.integers(1, d // 16 + 1))
+        w = torch.from_numpy(1e4 ** -r.random(pairs)).to(DEV)
+        axes = torch.from_numpy(r.integers(0, n_axes, pairs).astype(np.int32)).to(DEV)
+        pos = torch.randint(-100, 10 ** 7, (n_axes, T), generator=g).to(torch.int32).to(DEV)
+        rot = (pos, w, axes, bool(r.random() < 0.5))
+        qo = torch.full((T, Hq, d), 7.0, dtype=dt, device=DEV)
+        q0 = qo.clone()
+        kw = dict(q=q, positions=pos, inv_freq=w, axes=axes, interleaved=rot[3], q_out=qo)
+    k0, v0, s0 = kc.clone(), vc.clone(), sc.clone()
+    cud = None if one else torch.tensor(cu, dtype=torch.int32, device=DEV)
+    fa.paged_append(kc, vc, table, ln, k, v, cu_seqlens=cud, scores=sc, **kw)
+    ok()
+    check_append(k0, v0, s0, kc, vc, sc, table, lens, cu, k, v, q, qo, q0, rot)
+    # Decode.
+    window = int(pick(0, 0, 1, 30, 300))
+    scale = float(pick(d ** -0.5, 0.03, 0.4))
+    qd = torch.randn((B, Hq, d), generator=g).to(dt).to(DEV)
+    before = sc.clone()
+    with_scores = r.random() < 0.6
+    o, lse = fa.paged_decode(qd, kc, vc, table, ln, scale=scale, window=window, scores=sc if with_scores else None)
+    ok()
+    assert_decoded(o, lse, qd, kc, vc, table, ln, scale, window, sc if with_scores else None, before, f"seed {seed}")
+    # Evict.
+    used = {p for b, n in enumerate(lens) for p in table[b, :-(-n // page)].tolist()}
+    spare = [p for p in range(kc.shape[0]) if p not in used]
+    dst = torch.tensor(spare[:B * cols], dtype=torch.int32, device=DEV).view(B, cols)
+    s0 = f64(sc)
+    rows = [(paged.gather(f64(kc), table[b].cpu().numpy(), n), paged.gather(f64(vc), table[b].cpu().numpy(), n),
+             paged.gather(s0, table[b].cpu().numpy(), n)) for b, n in enumerate(lens)]
+    nl, kept = fa.paged_evict(kc, vc, sc, table, ln, dst, budget, recent, sinks)
+    ok()
+    for b, n in enumerate(lens):
+        m = min(n, budget)
+        assert nl[b].item() == m
+        got = [paged.gather(f64(t), dst[b].cpu().numpy(), m) for t in (kc, vc, sc)]
+        for h in range(Hkv):
+            keep = paged.kept_keys(rows[b][2][h].tolist(), budget, recent, sinks)
+            assert kept[b, h].tolist() == keep + [-1] * (budget - m)
+            for t in range(3):
+                assert np.array_equal(got[t][h], rows[b][t][h][keep]), (seed, b, h, t)
+
+
+# ---------------------------------------------------------------------------
 # Together, and how calls are made
 # ---------------------------------------------------------------------------
 class Served:
