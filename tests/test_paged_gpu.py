@@ -944,6 +944,70 @@ def test_captured_decode_follows_lengths_and_tables(cuda_lib):
         assert_decoded(o, lse, q, k, v, table, ln, 0.125, 0, scores, torch.zeros_like(scores), f"{n}")
 
 
+def test_capture_with_a_forked_stream(cuda_lib):
+    # Two steps on two branches of one graph, other kernels before, between and after.
+    a, b = one_step(), one_step(dt=HF, lens=(700, 64, 0, 9))
+    want = [a[0](), b[0]()]
+    ok()
+    side = torch.cuda.Stream()
+    x = torch.zeros(1 << 20, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cur = torch.cuda.current_stream()
+        x.add_(1.0)
+        side.wait_stream(cur)
+        with torch.cuda.stream(side):
+            got_b = b[0]()
+            y = x * 2.0
+        got_a = a[0]()
+        x.mul_(1.0)
+        cur.wait_stream(side)
+        again = a[0]()
+        z = x + y
+    for n in range(1, 4):
+        for o, _ in (got_a, got_b, again):
+            o.zero_()
+        graph.replay()
+        ok()
+        assert z[0].item() == 3.0 * n
+        for (o, l), (wo, wl), skip in ((got_a, want[0], 1), (again, want[0], 1), (got_b, want[1], 2)):
+            rows = torch.tensor([r for r in range(4) if r != skip], device=DEV)
+            assert torch.equal(o[rows], wo[rows]) and torch.equal(l, wl)
+
+
+def test_calls_between_other_kernels_on_one_stream(cuda_lib):
+    # Inputs written right before a call and outputs overwritten right after it,
+    # with nothing that waits in between.
+    k, v, table, ln = filled([900, 5, 300, 64], 2, 16, 64, BF, seed=81)
+    g = torch.Generator().manual_seed(82)
+    qs = [torch.randn((4, 8, 64), generator=g).to(BF).to(DEV) for _ in range(6)]
+    want = [fa.paged_decode(q, k, v, table, ln)[0].clone() for q in qs]
+    w, axes = fa.rope_frequencies((32,), device=DEV)
+    pos = torch.arange(4, dtype=torch.int32, device=DEV).view(1, 1, 4)
+    turned = [fa.rope(q.transpose(0, 1)[None].contiguous(), None, pos, w, axes).clone() for q in qs]
+    ok()
+    buf, out, lse = torch.empty_like(qs[0]), torch.empty_like(qs[0]), torch.empty((4, 8), device=DEV)
+    ws = fa.paged_decode_workspace(4, 8, k, table)
+    rin, rout = torch.empty_like(turned[0]), torch.empty_like(turned[0])
+    got, got_turned = [], []
+    for _ in range(20):
+        got, got_turned = [], []
+        for q in qs:
+            buf.copy_(q)
+            fa.paged_decode(buf, k, v, table, ln, out=out, lse=lse, workspace=ws)
+            got.append(out.clone())
+            buf.fill_(float("nan"))
+            out.fill_(float("nan"))
+            rin.copy_(q.transpose(0, 1)[None])
+            fa.rope(rin, None, pos, w, axes, q_out=rout)
+            got_turned.append(rout.clone())
+            rin.fill_(float("nan"))
+            rout.fill_(float("nan"))
+        ok()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert all(torch.equal(x, y) for x, y in zip(got_turned, turned))
+
+
 def test_calls_from_two_threads(cuda_lib):
     import threading
     steps = [one_step(), one_step(dt=HF, lens=(700, 64, 0, 9))]
