@@ -379,10 +379,58 @@ def check_device_status(stream=None):
 # Rotary positions and the paged key / value cache
 #
 # A decoding step makes these calls for every layer on tensors of a few KB, so
-# their time is the binding's: the checks of a valid argument are one
-# expression (the message is found out afterwards), structs and stride arrays
-# are packed bytes, and the stream comes as a raw handle.
+# their time is the binding's.  The public functions first offer a call to the
+# native marshalling (csrc/fa_torch.cpp), which takes what is in order, on the
+# current device and stream; what it does not take, because something is wrong
+# or elsewhere, or because it has not been built, goes through the functions
+# below, which say what is wrong.  There the checks of a valid argument are one
+# expression, structs and stride arrays packed bytes, the stream a raw handle.
 # ---------------------------------------------------------------------------
+
+class _NotBuilt:
+    """Stands for the native marshalling where there is none: takes no call."""
+
+    @staticmethod
+    def _none(*args):
+        return None
+    rope = paged_append = paged_decode = paged_evict = _none
+
+
+_native = None
+
+
+def _load_native():
+    """The native marshalling, bound to the library's entry points."""
+    global _native
+    lib = load_library()
+    path = os.path.join(os.path.dirname(LIB_PATH), "fa_torch.so")
+    _native = _NotBuilt
+    if os.path.exists(path):
+        import importlib.util
+        import torch  # noqa: F401  (its libraries, which the module needs, are then loaded)
+        try:
+            spec = importlib.util.spec_from_file_location("fa_torch", path)
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+            m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.fa_rope, lib.fa_paged_append, lib.fa_paged_decode, lib.fa_paged_decode_workspace_bytes,
+                lib.fa_paged_evict)))
+            _native = m
+        except ImportError:          # built against another torch
+            pass
+    return _native
+
+
+def native_marshalling() -> bool:
+    """Whether calls are marshalled natively (see build's fa_torch.txt if not)."""
+    return (_native or _load_native()) is not _NotBuilt
+
+
+def _answer(r, what):
+    """The native marshalling's answer: outputs, or a status to raise."""
+    if type(r) is int:
+        _raise(r, what)
+    return r
 
 _pack_rotary = struct.Struct("@PqqPPiii4x").pack          # fa_rotary
 _pack_kv = struct.Struct("@PPqqqiiiii4x").pack            # fa_paged_kv
@@ -544,12 +592,20 @@ def rope(q, k, positions, inv_freq, axes, interleaved: bool = False, q_out=None,
     int32 [n_axes, B, N] (expand over B to share them); inv_freq (float64) and
     axes (int32) come from ``rope_frequencies`` or the caller.  Outputs may be the
     inputs themselves.  Returns (q_out, k_out), or q_out without k."""
-    return _rope(q, k, positions, inv_freq, axes, interleaved, 0, q_out, k_out, stream)
+    if stream is None:
+        r = (_native or _load_native()).rope(q, k, positions, inv_freq, axes, interleaved, False, q_out, k_out)
+        if r is not None:
+            return _answer(r, "fa_rope")
+    return _rope(q, k, positions, inv_freq, axes, interleaved, False, q_out, k_out, stream)
 
 
 def rope_backward(dq, dk, positions, inv_freq, axes, interleaved: bool = False, dq_out=None, dk_out=None, stream=None):
     """Gradients of ``rope``'s inputs from those of its outputs: the opposite turn."""
-    return _rope(dq, dk, positions, inv_freq, axes, interleaved, 1, dq_out, dk_out, stream)
+    if stream is None:
+        r = (_native or _load_native()).rope(dq, dk, positions, inv_freq, axes, interleaved, True, dq_out, dk_out)
+        if r is not None:
+            return _answer(r, "fa_rope")
+    return _rope(dq, dk, positions, inv_freq, axes, interleaved, True, dq_out, dk_out, stream)
 
 
 def _paged(k_cache, v_cache, block_table, seq_lens):
@@ -583,6 +639,17 @@ def paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens=None,
     (into ``q_out``, which may be q); rows of padding tokens are not written.
     ``scores`` [pages,Hkv,page_size] fp32 gets 0 for the new tokens.  See
     fa_paged_append."""
+    if stream is None:
+        r = (_native or _load_native()).paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens, q, positions,
+                                                     inv_freq, axes, interleaved, scores, q_out)
+        if r is not None:
+            return None if r is False else _answer(r, "fa_paged_append")
+    return _paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens, q, positions, inv_freq, axes,
+                         interleaved, scores, q_out, stream)
+
+
+def _paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens, q, positions, inv_freq, axes, interleaved,
+                  scores, q_out, stream):
     (_, Hkv, _, d), dev, dt, kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
     T = k.shape[0] if isinstance(k, _torch.Tensor) and k.dim() == 3 else 0
     kp = _check_view(k, "k", (T, Hkv, d), dt, dev)
@@ -608,8 +675,8 @@ def paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens=None,
     handle = _raw_stream(dev, stream)
     if handle is None:
         with _on(dev, stream):
-            return paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens, q, positions, inv_freq, axes,
-                                interleaved, scores, q_out)
+            return _paged_append(k_cache, v_cache, block_table, seq_lens, k, v, cu_seqlens, q, positions, inv_freq, axes,
+                                 interleaved, scores, q_out, None)
     op, os_ = None, None
     if q is not None:
         if q_out is None:
@@ -647,6 +714,15 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float | None
     0).  ``scores`` [pages,Hkv,page_size] fp32, if given, grows at each visible
     key by its softmax weight summed over the group's heads.  See
     fa_paged_decode."""
+    if stream is None:
+        r = (_native or _load_native()).paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, window, scores, out,
+                                                     lse, workspace)
+        if r is not None:
+            return _answer(r, "fa_paged_decode")
+    return _paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, window, scores, out, lse, workspace, stream)
+
+
+def _paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, window, scores, out, lse, workspace, stream):
     (_, _, _, d), dev, dt, kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
     Hq = q.shape[1] if isinstance(q, _torch.Tensor) and q.dim() == 3 else 0
     qp = _check_view(q, "q", (B, Hq, d), dt, dev)
@@ -657,7 +733,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float | None
     handle = _raw_stream(dev, stream)
     if handle is None:
         with _on(dev, stream):
-            return paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, window, scores, out, lse, workspace)
+            return _paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, window, scores, out, lse, workspace, None)
     device = k_cache.device
     if out is None:
         out = _torch.empty((B, Hq, d), dtype=dt, device=device)
@@ -689,6 +765,16 @@ def paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budg
     ``dst_table`` [B, >= ceil(budget/page_size)], which must be other pages than
     those in use.  Returns (new_lens [B], kept [B,Hkv,budget]: the indices kept,
     -1 past the new length).  See fa_paged_evict."""
+    if stream is None:
+        r = (_native or _load_native()).paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budget, recent,
+                                                    sinks, new_lens, kept)
+        if r is not None:
+            return _answer(r, "fa_paged_evict")
+    return _paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budget, recent, sinks, new_lens, kept,
+                        stream)
+
+
+def _paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budget, recent, sinks, new_lens, kept, stream):
     (_, Hkv, _, _), dev, _, kv, table, B, lens = _paged(k_cache, v_cache, block_table, seq_lens)
     sp = _check_dense(scores, "scores", k_cache.shape[:3], _torch.float32, dev)
     dst, rows = _table(dst_table, "dst_table", dev)
@@ -700,8 +786,8 @@ def paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budg
     handle = _raw_stream(dev, stream)
     if handle is None:
         with _on(dev, stream):
-            return paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budget, recent, sinks, new_lens,
-                               kept)
+            return _paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, budget, recent, sinks, new_lens,
+                                kept, None)
     if new_lens is None:
         new_lens = _torch.empty((B,), dtype=_torch.int32, device=k_cache.device)
         np_ = new_lens.data_ptr()

@@ -1,9 +1,14 @@
-"""Build libfa_gb300.so in-tree with nvcc for sm_103a (no cmake, no torch extension).
+"""Build libfa_gb300.so in-tree with nvcc for sm_103a (no cmake).
 
 The translation units are compiled in parallel, then linked into
 ``exact_io_aware_flashattention_gb300/_lib/libfa_gb300.so`` with the CUDA
 runtime linked statically.  ``ptxas -v`` output (registers, shared memory,
 spills) is kept next to the library as ``ptxas.txt``.
+
+``_lib/fa_torch.so``, the native marshalling of torch tensors, is host code
+compiled beside it against the installed torch; the library does not need it,
+and where it does not compile the binding marshals in Python.  What the
+compiler said is kept as ``fa_torch.txt``.
 """
 from __future__ import annotations
 
@@ -22,6 +27,10 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB_NAME = "libfa_gb300.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 
+TORCH_SOURCE = "fa_torch.cpp"
+TORCH_PATH = os.path.join(OUT_DIR, "fa_torch.so")
+TORCH_LOG = os.path.join(OUT_DIR, "fa_torch.txt")
+
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_rope.cu", "fa_paged.cu", "fa_evict.cu"]
 HEADERS = ["sm103a.cuh", "fa_internal.h", "fa_paged.h"]
 
@@ -38,13 +47,13 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
+    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + [TORCH_SOURCE]]
     files += [os.path.join(INCLUDE, "fa.h"), os.path.abspath(__file__)]
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(TORCH_LOG):
         return False
     t = os.path.getmtime(LIB_PATH)
     return all(os.path.getmtime(f) <= t for f in _inputs())
@@ -57,6 +66,32 @@ def _compile(src: str) -> tuple[str, str]:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
     return obj, r.stderr + r.stdout
+
+
+def _compile_torch() -> None:
+    """fa_torch.so, or the reason why not in fa_torch.txt."""
+    tmp = TORCH_PATH + ".tmp"
+    try:
+        import sysconfig
+
+        import torch
+        where = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(nvcc()))
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-isystem", os.path.join(where, "include"), "-isystem", sysconfig.get_paths()["include"],
+               "-isystem", os.path.join(cuda, "include"), "-I", INCLUDE, os.path.join(CSRC, TORCH_SOURCE), "-o", tmp,
+               "-L", os.path.join(where, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
+               "-lc10_cuda"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode == 0:
+            os.replace(tmp, TORCH_PATH)
+        elif os.path.exists(TORCH_PATH):
+            os.remove(TORCH_PATH)
+        said = f"{' '.join(cmd)}\nexit {r.returncode}\n{r.stdout}{r.stderr}"
+    except Exception as e:       # no torch, no compiler: Python marshals
+        said = f"{type(e).__name__}: {e}\n"
+    with open(TORCH_LOG, "w") as f:
+        f.write(said)
 
 
 # The forward kernel splits its launch allocation between warpgroups with
@@ -94,8 +129,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(OUT_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        native = ex.submit(_compile_torch)
         results = list(ex.map(_compile, SOURCES))
+        native.result()
     objs = [o for o, _ in results]
     with open(os.path.join(OUT_DIR, "ptxas.txt"), "w") as f:
         for (o, log), src in zip(results, SOURCES):

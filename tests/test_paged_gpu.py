@@ -1059,7 +1059,73 @@ def test_steps_on_two_streams(cuda_lib):
             assert torch.equal(o[rows], want[i][0][rows]) and torch.equal(l, want[i][1])
 
 
-def test_binding_refusals(cuda_lib):
+def test_native_marshalling_is_there(cuda_lib):
+    assert fa.native_marshalling(), "see _lib/fa_torch.txt"
+
+
+@pytest.fixture(params=["native", "python"])
+def marshalling(request, monkeypatch, cuda_lib):
+    if request.param == "native":
+        assert fa.native_marshalling()
+    else:
+        monkeypatch.setattr(fa, "_native", fa._NotBuilt)
+    return request.param
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_both_marshallings_make_the_same_calls(cuda_lib, monkeypatch, given):
+    """Every operator once through each, with and without the optional arguments."""
+    def calls():
+        g = torch.Generator().manual_seed(91)
+        kc, vc, table, ln = filled([50, 0, 33], 2, 16, 64, HF, seed=92, layout="pair", extra=9)
+        used = set(table[0, :4].tolist()) | set(table[2, :3].tolist())
+        spare = [p for p in range(kc.shape[0]) if p not in used]
+        x = torch.randn((3, 12, 64), generator=g).to(HF).to(DEV)
+        q, k, v = x.split([8, 2, 2], dim=1)
+        w, axes = fa.rope_frequencies((8, 8, 16), device=DEV)
+        pos = torch.randint(0, 99, (3, 3), generator=g).to(torch.int32).to(DEV)
+        sc = torch.rand(kc.shape[:3], generator=g).to(DEV)
+        cu = torch.tensor([0, 2, 2, 3], dtype=torch.int32, device=DEV)
+        new = lambda t: torch.full_like(t, 7.0) if given else None  # noqa: E731
+        out = [fa.paged_append(kc, vc, table, ln, k, v), sc]
+        out[0] is None or pytest.fail("q out of nothing")
+        q1 = torch.zeros((3, 8, 64), dtype=HF, device=DEV)
+        q1 = fa.paged_append(kc, vc, table, ln, k, v, cu, q, pos, w, axes, given, sc if given else None, q1)
+        o, lse = fa.paged_decode(q1, kc, vc, table, ln, 0.2 if given else None, 20 if given else 0, sc if given else None,
+                                 new(q1), torch.zeros((3, 8), device=DEV) if given else None,
+                                 fa.paged_decode_workspace(3, 8, kc, table, given) if given else None)
+        dst = torch.tensor(spare[:6], dtype=torch.int32, device=DEV).view(3, 2)
+        nl, kept = fa.paged_evict(kc, vc, sc, table, ln, dst, 20, 3, 1, torch.zeros(3, dtype=torch.int32, device=DEV) if given else None)
+        qb = torch.randn((2, 3, 9, 80), generator=g).to(BF).to(DEV).transpose(1, 2).contiguous().transpose(1, 2)
+        pb = torch.arange(9, dtype=torch.int32, device=DEV).expand(3, 2, 9)
+        r1 = fa.rope(qb, None, pb, w, axes, given, new(qb))
+        r2, r3 = fa.rope_backward(qb, qb[:, :1], pb, w, axes, given, new(qb), new(qb[:, :1]))
+        ok()
+        return [kc, vc, sc, q1, o, lse, nl, kept, r1, r2, r3]
+    assert fa.native_marshalling()
+    native = calls()
+    monkeypatch.setattr(fa, "_native", fa._NotBuilt)
+    python = calls()
+    for a, b in zip(native, python):
+        assert a.shape == b.shape and a.dtype == b.dtype
+        assert torch.equal(torch.nan_to_num(a.float(), nan=-3.0), torch.nan_to_num(b.float(), nan=-3.0))
+
+
+def test_a_failed_allocation_raises(cuda_lib):
+    # A block table whose workspace no device has room for.
+    k, v, table, ln = filled([20], 2, 16, 64, BF, seed=95)
+    q = torch.zeros((1, 512, 64), dtype=BF, device=DEV)
+    wide = table.new_zeros((1, 2 ** 26))
+    wide[:, :2] = table[:, :2]
+    scores = torch.zeros(k.shape[:3], device=DEV)
+    with pytest.raises(torch.OutOfMemoryError):
+        fa.paged_decode(q, k, v, wide, ln, scores=scores)          # 2 TB
+    o, _ = fa.paged_decode(q[:, :4], k, v, table, ln)
+    ok()
+    assert torch.isfinite(o).all()
+
+
+def test_binding_refusals(marshalling):
     k, v, table, ln = filled([20], 2, 16, 64, BF, seed=61)
     q = torch.zeros((1, 4, 64), dtype=BF, device=DEV)
     with pytest.raises(TypeError):
