@@ -81,9 +81,6 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // j / page_size by a multiplication: page_size = 16 q, and with s = ceil(log2 q),
 // page_mul = ceil(2^(27+s) / q) the product n page_mul / 2^(27+s) exceeds n / q
 // by less than n 2^-(27+s) < 1/q for n = j / 16 < 2^27.
@@ -116,6 +113,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   Select& sh = *reinterpret_cast<Select*>(smem);
   uint32_t* keys = reinterpret_cast<uint32_t*>(smem + (sizeof(Select) + 15) / 16 * 16);     // [cap]
   launch_dependents();
+  wait_for_previous();
   const int unit = blockIdx.x / cluster, rank = blockIdx.x - unit * cluster;
   const int b = unit / a.kv.Hkv, g = unit - b * a.kv.Hkv;
   const int ps = a.kv.page_size, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -415,6 +413,7 @@ template <int D>
 __global__ void __launch_bounds__(kCopyThreads, 8)
     fa_evict_copy_kernel(const EvictArgs a, int blocks_per_unit, const DevStatus st) {
   constexpr int kVec = D / 8, kSide = 32 / (2 * kVec);   // 16-byte vectors a row; rows a warp moves at once, K and V
+  launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int unit = blockIdx.x / blocks_per_unit, b = unit / a.kv.Hkv, g = unit - b * a.kv.Hkv, ps = a.kv.page_size;
   const int r0 = (blockIdx.x - unit * blocks_per_unit) * kBlockRows + warp * kRows;
@@ -452,30 +451,6 @@ __global__ void __launch_bounds__(kCopyThreads, 8)
   }
 }
 
-template <typename... P, typename... A>
-cudaError_t launch(void (*k)(P...), dim3 grid, int block, size_t smem, int cluster, bool after, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2] = {};
-  int n = 0;
-  if (cluster > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = cluster;
-    attr[n].val.clusterDim.y = 1;
-    attr[n++].val.clusterDim.z = 1;
-  }
-  if (after) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, k, args...);
-}
-
 }  // namespace
 
 constexpr size_t kSelectBytes = (sizeof(Select) + 15) / 16 * 16;
@@ -501,13 +476,13 @@ cudaError_t launch_paged_evict(EvictArgs a, const DevStatus& st, int num_sms, cu
   while (cluster < kMaxCluster && (long long)units * cluster * 2 <= num_sms && most > 4LL * kThreads * cluster) cluster *= 2;
   const long long run = (most + cluster - 1) / cluster;
   const int cap = (int)(run + 4 < kMaxCached ? (run + 4 + 127) / 128 * 128 : kMaxCached);
-  cudaError_t e = launch(fa_evict_select_kernel, dim3((unsigned)units * cluster), kThreads, kSelectBytes + (size_t)cap * 4,
-                         cluster, false, stream, a, cluster, cap, st);
+  const cudaError_t e = launch_after(fa_evict_select_kernel, dim3((unsigned)units * cluster), kThreads,
+                                     kSelectBytes + (size_t)cap * 4, cluster, stream, a, cluster, cap, st);
   if (e != cudaSuccess) return e;
   const int per_unit = (a.budget + kBlockRows - 1) / kBlockRows;
   const dim3 grid((unsigned)((long long)units * per_unit));
-  return a.kv.d == 64 ? launch(fa_evict_copy_kernel<64>, grid, kCopyThreads, 0, 1, true, stream, a, per_unit, st)
-                      : launch(fa_evict_copy_kernel<128>, grid, kCopyThreads, 0, 1, true, stream, a, per_unit, st);
+  return a.kv.d == 64 ? launch_after(fa_evict_copy_kernel<64>, grid, kCopyThreads, 0, 1, stream, a, per_unit, st)
+                      : launch_after(fa_evict_copy_kernel<128>, grid, kCopyThreads, 0, 1, stream, a, per_unit, st);
 }
 
 }  // namespace fa

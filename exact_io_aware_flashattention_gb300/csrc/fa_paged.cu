@@ -134,11 +134,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // Barrier among the consumer warps.
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory"); }
 
-// Programmatic dependent launch: let the next kernel of the stream start its
-// blocks / wait until everything of the kernel before is complete and visible.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Visible keys [first, len) of a sequence, as tiles [tile0, tile0 + n) of kKeys.
 struct Span {
   int len, first, tile0, n;
@@ -232,9 +227,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int* abort_flag = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
-  // On its way while the barriers are set up.
-  const int first_len = (int)threadIdx.x < a.B ? a.seq_lens[threadIdx.x] : 0;
   if ((smem_u32(smem) & 1023u) != 0) {
+    wait_for_previous();
     if (threadIdx.x == 0) {
       record_error(st, kErrDeviceTimeout, 0);
       a.parts[blockIdx.x].left = 0;
@@ -251,6 +245,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
+  wait_for_previous();
+  const int first_len = (int)threadIdx.x < a.B ? a.seq_lens[threadIdx.x] : 0;
   const int G = a.Hq / a.kv.Hkv, chunks = (G + 8 * NT - 1) / (8 * NT), cols = a.kv.Hkv * chunks;
 
   // The line: its length, and this CTA's first sequence.
@@ -909,40 +905,25 @@ __global__ void __launch_bounds__(128) fa_paged_finish_kernel(const DecodeArgs a
 // LSE from the parts in every warp costs more than waiting for the joins.
 template <int kKeys>
 __global__ void __launch_bounds__(128) fa_paged_weights_kernel(const DecodeArgs a) {
+  launch_dependents();
   wait_for_previous();
   add_weights<kKeys, true>(a, blockIdx.x, 0.f);
-}
-
-// A launch whose blocks may start before the kernel in front of it is done
-// (they wait for it themselves).
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*k)(P...), dim3 grid, dim3 block, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
 template <typename T, int D>
 cudaError_t launch_decode(const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs& a, const DevStatus& st, int parts,
                           cudaStream_t stream) {
-  if (a.unit_heads == 8) fa_paged_decode_kernel<T, D, 1><<<parts, kThreads, Cfg<D>::kBytes, stream>>>(tk, tv, a, st);
-  else fa_paged_decode_kernel<T, D, 2><<<parts, kThreads, Cfg<D>::kBytes, stream>>>(tk, tv, a, st);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e =
+      launch_after(a.unit_heads == 8 ? fa_paged_decode_kernel<T, D, 1> : fa_paged_decode_kernel<T, D, 2>, parts, kThreads,
+                   Cfg<D>::kBytes, 1, stream, tk, tv, a, st);
   if (e != cudaSuccess) return e;
   const int joins = (parts - 1) * (a.unit_heads / 4), adds = parts * kSplit;
   // In one launch unless units are cut into more than about eight (2 sequences
   // of 93735 keys, 152 parts each: 29.2 us in one, 27.2 us in two).
   if (a.scores && a.Hq / a.kv.Hkv <= a.unit_heads && parts <= 8LL * a.B * a.kv.Hkv)
-    return launch_after(fa_paged_finish_kernel<T, D, true>, joins + adds, 128, stream, a, joins);
-  if (joins > 0) e = launch_after(fa_paged_finish_kernel<T, D, false>, joins, 128, stream, a, joins);
-  if (e == cudaSuccess && a.scores) e = launch_after(fa_paged_weights_kernel<Cfg<D>::kKeys>, adds, 128, stream, a);
+    return launch_after(fa_paged_finish_kernel<T, D, true>, joins + adds, 128, 0, 1, stream, a, joins);
+  if (joins > 0) e = launch_after(fa_paged_finish_kernel<T, D, false>, joins, 128, 0, 1, stream, a, joins);
+  if (e == cudaSuccess && a.scores) e = launch_after(fa_paged_weights_kernel<Cfg<D>::kKeys>, adds, 128, 0, 1, stream, a);
   return e;
 }
 

@@ -180,6 +180,8 @@ __device__ __forceinline__ void do_heads(const T* in, long long in_sh, T* out, l
 template <typename T, bool kInter>
 __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeArgs a, int hpb, const DevStatus st) {
   __shared__ Pairs pairs;
+  launch_dependents();
+  wait_for_previous();
   load_pairs(a.r, pairs, st);
   __syncthreads();
   const int nch = a.d / 16, tpb = kThreads / nch;
@@ -238,6 +240,8 @@ __device__ __forceinline__ bool place_token(const AppendArgs& a, int t, const De
 template <typename T, bool kInter>
 __global__ void __launch_bounds__(kThreads) fa_append_kernel(const AppendArgs a, int hpb, const DevStatus st) {
   __shared__ Pairs pairs;
+  launch_dependents();
+  wait_for_previous();
   load_pairs(a.r, pairs, st);
   __syncthreads();
   const int nch = a.kv.d / 16, tpb = kThreads / nch;
@@ -269,14 +273,13 @@ __global__ void __launch_bounds__(kThreads) fa_append_kernel(const AppendArgs a,
                         hi, ck, false, cs, sn);
 }
 
-// Heads per block: as many as still leave 8 blocks of 128 threads an SM, so
-// that the angles are formed for many heads at once and the last wave is
-// short.  (4 an SM: the gradient above 59 instead of 54 us; 16: 134 MB in 22
-// instead of 20 us.  256 threads a block: 3-10 % slower on all.  Equal parts
-// of one line of (token, head) rows per resident block spilled and took up to
-// twice as long.)
+// Heads per block: as many as still leave 16 blocks of 128 threads an SM, so
+// that the angles are formed for several heads at once and the last wave is
+// short.  (8 an SM: the gradient above 54.5 instead of 52.6 us; 24: the prompt
+// 33.7 instead of 31.4.  Equal parts of one line of (token, head) rows per
+// resident block spilled and took up to twice as long.)
 int heads_per_block(long long token_blocks, int heads, int num_sms) {
-  const long long want = 8LL * num_sms;
+  const long long want = 16LL * num_sms;
   long long splits = (want + token_blocks - 1) / token_blocks;
   const long long most = (heads + kUnroll - 1) / kUnroll;
   if (splits > most) splits = most;
@@ -304,13 +307,11 @@ cudaError_t launch_rope(int dtype, const RopeArgs& a, const DevStatus& st, int n
   const int heads = a.Hq + a.Hk, hpb = heads_per_block(blocks, heads, num_sms);
   const dim3 grid((unsigned)blocks, (unsigned)((heads + hpb - 1) / hpb));
   if (dtype == 0) {
-    if (a.r.interleaved) fa_rope_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, stream>>>(a, hpb, st);
-    else fa_rope_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, stream>>>(a, hpb, st);
-  } else {
-    if (a.r.interleaved) fa_rope_kernel<__half, true><<<grid, kThreads, 0, stream>>>(a, hpb, st);
-    else fa_rope_kernel<__half, false><<<grid, kThreads, 0, stream>>>(a, hpb, st);
+    if (a.r.interleaved) return launch_after(fa_rope_kernel<__nv_bfloat16, true>, grid, kThreads, 0, 1, stream, a, hpb, st);
+    return launch_after(fa_rope_kernel<__nv_bfloat16, false>, grid, kThreads, 0, 1, stream, a, hpb, st);
   }
-  return cudaGetLastError();
+  if (a.r.interleaved) return launch_after(fa_rope_kernel<__half, true>, grid, kThreads, 0, 1, stream, a, hpb, st);
+  return launch_after(fa_rope_kernel<__half, false>, grid, kThreads, 0, 1, stream, a, hpb, st);
 }
 
 cudaError_t launch_append(int dtype, const AppendArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream) {
@@ -319,13 +320,11 @@ cudaError_t launch_append(int dtype, const AppendArgs& a, const DevStatus& st, i
   const int heads = a.Hq + 2 * a.kv.Hkv, hpb = heads_per_block(blocks, heads, num_sms);
   const dim3 grid((unsigned)blocks, (unsigned)((heads + hpb - 1) / hpb));
   if (dtype == 0) {
-    if (a.r.interleaved) fa_append_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, stream>>>(a, hpb, st);
-    else fa_append_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, stream>>>(a, hpb, st);
-  } else {
-    if (a.r.interleaved) fa_append_kernel<__half, true><<<grid, kThreads, 0, stream>>>(a, hpb, st);
-    else fa_append_kernel<__half, false><<<grid, kThreads, 0, stream>>>(a, hpb, st);
+    if (a.r.interleaved) return launch_after(fa_append_kernel<__nv_bfloat16, true>, grid, kThreads, 0, 1, stream, a, hpb, st);
+    return launch_after(fa_append_kernel<__nv_bfloat16, false>, grid, kThreads, 0, 1, stream, a, hpb, st);
   }
-  return cudaGetLastError();
+  if (a.r.interleaved) return launch_after(fa_append_kernel<__half, true>, grid, kThreads, 0, 1, stream, a, hpb, st);
+  return launch_after(fa_append_kernel<__half, false>, grid, kThreads, 0, 1, stream, a, hpb, st);
 }
 
 }  // namespace fa
