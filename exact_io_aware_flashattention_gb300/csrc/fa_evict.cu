@@ -15,25 +15,24 @@
 // fa_evict_select_kernel.  One cluster of 1, 2, 4 or 8 CTAs per (b, g), each
 // with an equal run of the keys, held in shared memory as order-preserving
 // integers (protected ones as the largest).  The m-th largest is found 11, 11
-// and 10 bits at a time: every CTA counts its keys that match
-// the digits found so far into a histogram, reads the others' histograms
-// through distributed shared memory, and all reach the same digit; three
+// and 10 bits at a time: every CTA counts its keys that match the digits found
+// so far into a histogram, reads the others' through distributed shared memory
+// (64 sums of 32 bins first, then 32 bins), and all reach the same digit; three
 // passes over shared memory replace a sort.  It stops early when the digit's
-// bin is wanted whole.  The kept indices then go out in order: each warp
-// counts its run of keys by votes, sums the counts of the warps and CTAs before,
-// and writes.
+// bin is wanted whole.  The kept indices then go out in order: each warp counts
+// its run of keys, sums the counts of the warps and CTAs before, and writes.
 //
 // fa_evict_copy_kernel.  A warp takes 8 consecutive kept keys: eight lanes look
 // one up each (index, source page, target page) and move its score, then the
 // rows go 16 bytes a lane, all loads in flight before the first store.  (16 or
 // 32 keys a warp, in rounds of 8 or 4, fill the last wave worse: 2-5 % slower.)
 //
-// Measured: 2 sequences of 131072 keys, 8 heads, d = 128, to 32768: 104 us, of
-// which the selection 20 and the copy of 541 MB 82 (97 % of the 6.79 TB/s copy
+// Measured: 2 sequences of 131072 keys, 8 heads, d = 128, to 32768: 103.5 us, of
+// which the selection 19 and the copy of 541 MB 82 (97 % of the 6.79 TB/s copy
 // rate); 16 sequences of 0 to 8192 keys to 2048: 43 us, the copy of 202 MB 32;
 // one of 1000 keys, 2 heads: 7.4 us.  The selection is bound by instructions
-// and latencies: of its 35 thousand cycles at 16384 keys a CTA the loads take
-// 7, the histograms 7, the exchanges over the cluster 10, the list 10.
+// and latencies: of its 33 thousand cycles at 16384 keys a CTA the loads take
+// 7, the histograms 7, the exchanges over the cluster 10, the list 9.
 #include "fa_paged.h"
 #include "sm103a.cuh"
 

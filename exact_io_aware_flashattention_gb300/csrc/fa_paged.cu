@@ -32,13 +32,14 @@
 // work is 1-2 % of what the copies take, so the tcgen05 path, whose 128-row
 // tiles would be filled 1/16 by a group of 8, has nothing to win here.
 //
-// Measured (cold caches; GB/s of the 6.79 TB/s copy rate), decode and finish
-// kernels together: 8 sequences of 32768 keys, 32 q and 8 kv heads, d = 128,
-// 1074 MB: 163 us, 97 %; 64 sequences of 0 to 8192 keys, 16 heads, d = 64, 1000
-// MB: 154 us, 96 %; 16 sequences of 0 to 8192, 236 MB: 45 us, and 51 us with
-// scores; one sequence of 1000 keys: 7.0 us.  About 5 us of every call are the
-// start (lengths, page numbers, first tiles) and the finish kernel.  From L2
-// alone the tiles run at 10-11 TB/s, so the SMs keep ahead of HBM.
+// Measured (calls in a row on three sets of tensors; of the 6.79 TB/s copy
+// rate), decode and finish kernels together: 8 sequences of 32768 keys, 32 q
+// and 8 kv heads, d = 128, 1074 MB: 164 us, 96 %; 64 sequences of 0 to 8192 keys,
+// 16 heads, d = 64, 1000 MB: 155 us, 95 %; 16 sequences of 0 to 8192, 236 MB: 45
+// us, and 51 us with scores; one sequence of 1000 keys: 6.9 us.  About 5 us of
+// every call are the start (lengths, page numbers, first tiles) and the finish
+// kernel.  From L2 alone the tiles run at 10-11 TB/s, so the SMs keep ahead of
+// HBM.
 #include "fa_paged.h"
 #include "sm103a.cuh"
 

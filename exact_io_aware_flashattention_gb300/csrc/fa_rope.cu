@@ -23,13 +23,13 @@
 // cosines and sines are formed once and used for all the heads of its block.
 // Loads and stores are marked as streaming: nothing is read twice.
 //
-// Measured (three sets of tensors in turn, so nothing comes from L2), of the
-// 6.79 TB/s copy rate: q and k of 4 x (16 + 16) heads x 2048 tokens, d = 128,
-// 134 MB: 20.1 us, 98 %; the gradient for 2 x (32 + 8) x 8192, 336 MB: 54 us,
-// 92 %; appending 7357 prompt tokens (32 q heads turned, 8 k and 8 v heads
-// stored), 181 MB: 31.6 us, 84 % (95 registers leave 20 warps an SM, and each
-// token first looks its slot up); one token for each of 64 sequences: 4.2 us,
-// of which the launch is most.
+// Measured (calls in a row on three sets of tensors), of the 6.79 TB/s copy
+// rate: q and k of 4 x (16 + 16) heads x 2048 tokens, d = 128, 134 MB: 23.5 us,
+// 84 %; the gradient for 2 x (32 + 8) x 8192, 336 MB: 52.7 us, 94 %; appending
+// 7357 prompt tokens (32 q heads turned, 8 k and 8 v heads stored), 181 MB:
+// 31.4 us, 85 % (95 registers leave 20 warps an SM, and each token first looks
+// its slot up); one token for each of 64 sequences: 3.8 us, of which the launch
+// is most.
 #include "fa_paged.h"
 #include "sm103a.cuh"
 
