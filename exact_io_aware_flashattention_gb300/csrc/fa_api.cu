@@ -760,12 +760,6 @@ struct View {
       if (stride[i] < extent(i + 1)) return false;
     return true;
   }
-  bool same(const View& o) const {
-    if (base != o.base || row != o.row || n != o.n) return false;
-    for (int i = 0; i < n; ++i)
-      if (size[i] != o.size[i] || stride[i] != o.stride[i]) return false;
-    return true;
-  }
 };
 
 View view(const void* p, long long row, int elem, std::initializer_list<std::pair<long long, long long>> dims) {
@@ -817,6 +811,12 @@ fa_status check_strides(std::initializer_list<std::pair<long long, long long>> d
 }
 
 long long stride_of(long long size, long long stride) { return size > 1 ? stride : 0; }
+
+// In place: every row is written where it is read.  (The same rows in another
+// order, as with two dimensions exchanged, would be read after they are lost.)
+bool in_place(const fa::RowView& out, const fa::RowView& in) {
+  return out.p == in.p && out.sb == in.sb && out.sh == in.sh && out.sn == in.sn;
+}
 
 fa_status check_rotary(const fa_rotary* r, int d) {
   if (!r->positions || !r->inv_freq || !r->axes) return FA_ERR_NULL_PTR;
@@ -971,7 +971,7 @@ fa_status fa_rope(const void* q, const long long* q_strides, void* q_out, const 
   for (int i = 1; i < n; i += 2) {
     if (!views[i].distinct()) return FA_ERR_ALIASING;
     for (int j = 0; j < n; ++j)
-      if (j != i && !(j == i - 1 && views[i].same(views[j])) && !apart(views[i], views[j])) return FA_ERR_ALIASING;
+      if (j != i && !(j == i - 1 && in_place(rows[i], rows[j])) && !apart(views[i], views[j])) return FA_ERR_ALIASING;
     for (const View& t : tables)
       if (!apart(views[i], t)) return FA_ERR_ALIASING;
   }
@@ -1028,7 +1028,7 @@ fa_status fa_paged_append(const fa_paged_kv* kv, const fa_page_table* table, con
   for (int i = 0; i < no; ++i) {
     if (!outs[i].distinct()) return FA_ERR_ALIASING;
     for (int j = 0; j < (q ? 3 : 2); ++j)
-      if (!(i == qo && j == 2 && outs[i].same(views[2])) && !apart(outs[i], views[j])) return FA_ERR_ALIASING;
+      if (!(i == qo && j == 2 && in_place(rows[3], rows[2])) && !apart(outs[i], views[j])) return FA_ERR_ALIASING;
     for (int j = 0; j < i; ++j)
       if (!apart(outs[i], outs[j])) return FA_ERR_ALIASING;
     for (int j = 0; j < ns; ++j)

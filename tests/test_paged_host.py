@@ -237,6 +237,18 @@ def test_append_refuses(lib, kw, status):
     assert append(**kw) == status
 
 
+def test_in_place_with_two_dimensions_exchanged_is_refused(lib):
+    # The rows are the same ones, but each is written where another is read:
+    # batch and head of q, head and token of k, token and head of appended q.
+    s = arr(8192, 4096, 64)
+    assert rope(q_out=A, q_out_strides=arr(4096, 8192, 64)) == fa.FA_ERR_ALIASING
+    assert rope(q_strides=s, q_out=A, q_out_strides=s, k=3 * A, k_strides=arr(1 << 20, 4096, 64), Hk=64, k_out=3 * A,
+                k_out_strides=arr(1 << 20, 64, 4096)) == fa.FA_ERR_ALIASING
+    assert append(Hq=2, q_strides=arr(512, 64), q_out_strides=arr(64, 512)) == fa.FA_ERR_ALIASING
+    # A stride that is never stepped does not matter.
+    valid(lambda: rope(B=1, q_out=A, q_out_strides=arr(64, 4096, 64)))
+
+
 def test_append_accepts_a_projection_and_an_interleaved_pool(lib):
     valid(append)
     assert append(T=0, cu_seqlens=9 * A) == fa.FA_OK
