@@ -217,7 +217,45 @@ __device__ __forceinline__ void fill_empty(const DecodeArgs& a) {
   }
 }
 
-template <typename T, int D, int NT>
+// A unit whose tiles a cluster shared: each CTA left its share's O [16][D] and
+// (max, sum) [16] in its shared memory.  The threads of all CTAs take two
+// elements of a head each.
+template <int D>
+constexpr uint32_t kClusterMl = 16u * D * 4u;
+template <typename T, int D>
+__device__ __forceinline__ void join_cluster(const DecodeArgs& a, const uint8_t* smem, const Walk<Cfg<D>::kKeys>& w, int rank,
+                                             int h0, int h1) {
+  for (int i = rank * kConsumers * 32 + threadIdx.x; i < (h1 - h0) * (D / 2); i += a.cluster * kConsumers * 32) {
+    const int hh = i / (D / 2), d = i % (D / 2) * 2;
+    float2 y[kMaxCluster], x[kMaxCluster];         // all loads in flight before the first is used
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      const int from = r < a.cluster ? r : rank;
+      y[r] = ld_cluster2(reinterpret_cast<const float2*>(smem + kClusterMl<D>) + hh, from);
+      x[r] = ld_cluster2(reinterpret_cast<const float2*>(smem + (hh * D + d) * 4), from);
+    }
+    float m = -INFINITY, l = 0.f;
+    float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) m = fmaxf(m, y[r].x);
+    const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < a.cluster) {
+        const float f = ex2(y[r].x - mu);
+        l = fmaf(f, y[r].y, l);
+        o.x = fmaf(f, x[r].x, o.x);
+        o.y = fmaf(f, x[r].y, o.y);
+      }
+    const long long row = (long long)w.b * a.Hq + h0 + hh;
+    const bool none = w.s.n == 0;                  // no visible keys
+    const float inv = none ? 0.f : 1.f / l;
+    *reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + row * D + d) = Mma<T>::pack(o.x * inv, o.y * inv);
+    if (d == 0) a.lse[row] = none ? -INFINITY : (m + (log2f(l) - Mma<T>::kShift)) * 0.69314718055994530942f;
+  }
+}
+
+template <typename T, int D, int NT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 2)
     fa_paged_decode_kernel(const __grid_constant__ TmaMap4 tmK, const __grid_constant__ TmaMap4 tmV, const DecodeArgs a,
                            const DevStatus st) {
@@ -232,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     wait_for_previous();
     if (threadIdx.x == 0) {
       record_error(st, kErrDeviceTimeout, 0);
-      a.parts[blockIdx.x].left = 0;
+      if (!kCluster) a.parts[blockIdx.x].left = 0;
     }
     return;
   }
@@ -247,62 +285,77 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&tmV);
   }
   wait_for_previous();
-  const int first_len = (int)threadIdx.x < a.B ? a.seq_lens[threadIdx.x] : 0;
   const int G = a.Hq / a.kv.Hkv, chunks = (G + 8 * NT - 1) / (8 * NT), cols = a.kv.Hkv * chunks;
-
-  // The line: its length, and this CTA's first sequence.
-  long long total = 0;
-  for (int round = 0; round < 2; ++round) {
-    // Round 0 finds the total; round 1, for batches of more than one block's
-    // worth, walks again to find the start (one block's worth is still there).
-    long long before = 0, t0 = 0;
-    for (int base = 0; base < a.B; base += kThreads) {
-      const int b = base + threadIdx.x;
-      Span s{};
-      if (b < a.B) {
-        s = span_of_len<C::kKeys>(a, base == 0 ? first_len : a.seq_lens[b]);
-        if (s.len < 0 && round == 0 && blockIdx.x == 0) record_error(st, kErrBadIndex, kSiteDecodeLen);
-      }
-      int x = s.n;
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) bars->scan[warp] = x;
-      __syncthreads();
-      long long pre = before + x - s.n;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) pre += bars->scan[w];
-        before += bars->scan[w];
-      }
-      const bool last = base + kThreads >= a.B;
-      if (round == 0 && last) total = before * cols;
-      const int parts = (int)min(total, (long long)gridDim.x);
-      if ((last || round == 1) && blockIdx.x < parts) t0 = part_start(total, blockIdx.x, parts);
-      if ((round == 1 || a.B <= kThreads) && s.n > 0 && pre * cols <= t0 && t0 < (pre + s.n) * cols) {
-        bars->b0 = b;
-        bars->before = pre * cols;
-      }
-    }
-    if (a.B <= kThreads) break;
-  }
-  __syncthreads();
-  const int parts = (int)min(total, (long long)gridDim.x);
-  if ((int)blockIdx.x >= parts) {
-    if (threadIdx.x == 0) a.parts[blockIdx.x].left = 0;
-    if (warp == kConsumers) fill_empty<T, D>(a);
-    return;
-  }
-  const long long t0 = part_start(total, blockIdx.x, parts), t1 = part_start(total, blockIdx.x + 1, parts);
   Walk<C::kKeys> w;
-  w.left = t1 - t0;
-  w.b = bars->b0;
-  w.s = span_of<C::kKeys>(a, w.b);
-  {
-    const long long in = t0 - bars->before;
-    w.col = (int)(in / w.s.n);
-    w.tile = (int)(in - (long long)w.col * w.s.n);
+  long long total = 0, t0 = 0, t1 = 0;            // the line's tiles, and this CTA's part of them
+  int parts = 0, rank = 0;
+  if constexpr (kCluster) {
+    // The cluster's unit, and this CTA's share of its tiles (perhaps none).
+    const int unit = blockIdx.x / a.cluster;
+    rank = blockIdx.x - unit * a.cluster;
+    w.b = unit / cols;
+    w.col = unit - w.b * cols;
+    w.s = span_of<C::kKeys>(a, w.b);
+    w.tile = w.s.n * rank / a.cluster;
+    w.left = w.s.n * (rank + 1) / a.cluster - w.tile;
+    if (w.s.len < 0 && w.col == 0 && rank == 0 && threadIdx.x == 0) record_error(st, kErrBadIndex, kSiteDecodeLen);
+    __syncthreads();
+  } else {
+    const int first_len = (int)threadIdx.x < a.B ? a.seq_lens[threadIdx.x] : 0;
+
+    // The line: its length, and this CTA's first sequence.
+    for (int round = 0; round < 2; ++round) {
+      // Round 0 finds the total; round 1, for batches of more than one block's
+      // worth, walks again to find the start (one block's worth is still there).
+      long long before = 0, t0 = 0;
+      for (int base = 0; base < a.B; base += kThreads) {
+        const int b = base + threadIdx.x;
+        Span s{};
+        if (b < a.B) {
+          s = span_of_len<C::kKeys>(a, base == 0 ? first_len : a.seq_lens[b]);
+          if (s.len < 0 && round == 0 && blockIdx.x == 0) record_error(st, kErrBadIndex, kSiteDecodeLen);
+        }
+        int x = s.n;
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, d);
+          if (lane >= d) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) bars->scan[warp] = x;
+        __syncthreads();
+        long long pre = before + x - s.n;
+        for (int w = 0; w < kThreads / 32; ++w) {
+          if (w < warp) pre += bars->scan[w];
+          before += bars->scan[w];
+        }
+        const bool last = base + kThreads >= a.B;
+        if (round == 0 && last) total = before * cols;
+        const int parts = (int)min(total, (long long)gridDim.x);
+        if ((last || round == 1) && blockIdx.x < parts) t0 = part_start(total, blockIdx.x, parts);
+        if ((round == 1 || a.B <= kThreads) && s.n > 0 && pre * cols <= t0 && t0 < (pre + s.n) * cols) {
+          bars->b0 = b;
+          bars->before = pre * cols;
+        }
+      }
+      if (a.B <= kThreads) break;
+    }
+    __syncthreads();
+    parts = (int)min(total, (long long)gridDim.x);
+    if ((int)blockIdx.x >= parts) {
+      if (threadIdx.x == 0) a.parts[blockIdx.x].left = 0;
+      if (warp == kConsumers) fill_empty<T, D>(a);
+      return;
+    }
+    t0 = part_start(total, blockIdx.x, parts);
+    t1 = part_start(total, blockIdx.x + 1, parts);
+    w.left = t1 - t0;
+    w.b = bars->b0;
+    w.s = span_of<C::kKeys>(a, w.b);
+    {
+      const long long in = t0 - bars->before;
+      w.col = (int)(in / w.s.n);
+      w.tile = (int)(in - (long long)w.col * w.s.n);
+    }
   }
 
   if (warp == kConsumers) {
@@ -371,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       slot = slot_next;
       have = have_next;
     }
-    if (lane == 0) {
+    if (!kCluster && lane == 0) {
       DecodePart d = part;
       const long long u0 = t0 - d.tile;
       d.i0 = part_of(u0, total, parts);
@@ -379,13 +432,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       d.last_i1 = good && w.tile < w.s.n ? part_of(t1 - 1 + (w.s.n - w.tile), total, parts) : blockIdx.x;
       a.parts[blockIdx.x] = d;
     }
-    fill_empty<T, D>(a);
+    if (!kCluster) fill_empty<T, D>(a);
     // Every copy issued must have landed before the CTA may exit.
     if (lane == 0)
       for (int s = 0; s < C::kStages && s < it; ++s) {
         const int last = it - 1 - ((it - 1 - s) % C::kStages);
         mbar_wait_drain(&bars->full[s], (last / C::kStages) & 1, st, kDrainFull);
       }
+    if (kCluster && a.cluster > 1) {
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
     return;
   }
 
@@ -411,7 +469,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if constexpr (kAheadQ) load_q<T, D, NT>(a, w.b, w.col, chunks, q_next);
   int g = 0, h0 = 0, h1 = 0;                      // kv head, query heads [h0, h1) of the unit
   float* stash = nullptr;                         // this lane's first score of key 0 of the unit
-  for (int it = 0; w.left > 0; ++it) {
+  for (int it = 0; w.left > 0 || (kCluster && it == 0); ++it) {
+    const bool some = !kCluster || w.left > 0;    // a CTA of a cluster may have no tile, and joins in all the same
     if (fresh) {
       fresh = false;
       unit_pos = w.tile;
@@ -444,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int s = it % C::kStages;
     // After a wait that gave up the warp goes on through its part without
     // touching the tiles, so that the warps still meet at each unit's end.
-    if (!dead && !mbar_wait_warp(&bars->full[s], (it / C::kStages) & 1, st, abort_flag, kSiteFull)) dead = true;
+    if (some && !dead && !mbar_wait_warp(&bars->full[s], (it / C::kStages) & 1, st, abort_flag, kSiteFull)) dead = true;
     // The warp's slices are warp, warp + 4, ...
-    const uint32_t loaded = dead ? 0u : bars->mask[s] >> warp;
+    const uint32_t loaded = dead || !some ? 0u : bars->mask[s] >> warp;
     constexpr uint32_t kMine = kSl == 1 ? 1u : 0x11u;
     if (loaded & kMine) {
       const int key0 = (w.s.tile0 + w.tile) * C::kKeys + warp * 16;
@@ -569,10 +628,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->empty[s]);
+    if (lane == 0 && some) mbar_arrive(&bars->empty[s]);
 
     const bool unit_ends = w.tile + 1 == w.s.n;
-    if (unit_ends || w.left == 1) {
+    if (unit_ends || w.left <= 1) {
       // ------------------------------------------------ the unit's end here
       const bool whole = unit_ends && unit_pos == 0;
 #pragma unroll
@@ -639,7 +698,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           r[e + 2] = y.z;
           r[e + 3] = y.w;
         }
-        if (h < h1) {
+        if constexpr (kCluster) {
+          // For the join; the tiles have been read.
+          float4* dst = reinterpret_cast<float4*>(smem + ((n * 8 + hh) * D + e0) * 4);
+#pragma unroll
+          for (int e = 0; e < D / 16; e += 4) dst[e / 4] = make_float4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+          if (e0 == 0) reinterpret_cast<float2*>(smem + kClusterMl<D>)[n * 8 + hh] = make_float2(M, L);
+        } else if (h < h1) {
           if (whole) {
             const float inv = 1.f / L;
             uint32_t y[D / 32];
@@ -667,6 +732,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       fresh = true;
     }
     w.next(a, cols);
+  }
+  if constexpr (kCluster) {
+    if (a.cluster > 1) cluster_sync();
+    else consumer_sync();
+    join_cluster<T, D>(a, smem, w, rank, h0, min(h1, h0 + 8 * NT));
+    __syncwarp();
+    if (a.cluster > 1) cluster_sync();             // nobody exits while its share is read
   }
 }
 
@@ -914,9 +986,12 @@ __global__ void __launch_bounds__(128) fa_paged_weights_kernel(const DecodeArgs 
 template <typename T, int D>
 cudaError_t launch_decode(const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs& a, const DevStatus& st, int parts,
                           cudaStream_t stream) {
+  if (a.cluster)
+    return launch_after(a.unit_heads == 8 ? fa_paged_decode_kernel<T, D, 1, true> : fa_paged_decode_kernel<T, D, 2, true>,
+                        parts, kThreads, Cfg<D>::kBytes, a.cluster, stream, tk, tv, a, st);
   cudaError_t e =
-      launch_after(a.unit_heads == 8 ? fa_paged_decode_kernel<T, D, 1> : fa_paged_decode_kernel<T, D, 2>, parts, kThreads,
-                   Cfg<D>::kBytes, 1, stream, tk, tv, a, st);
+      launch_after(a.unit_heads == 8 ? fa_paged_decode_kernel<T, D, 1, false> : fa_paged_decode_kernel<T, D, 2, false>, parts,
+                   kThreads, Cfg<D>::kBytes, 1, stream, tk, tv, a, st);
   if (e != cudaSuccess) return e;
   const int joins = (parts - 1) * (a.unit_heads / 4), adds = parts * kSplit;
   // In one launch unless units are cut into more than about eight (2 sequences
@@ -932,10 +1007,10 @@ template <typename T, int D>
 cudaError_t configure_decode() {
   static_assert(Cfg<D>::kBytes <= 115712, "two CTAs per SM");
   static_assert(Cfg<D>::kKeys == decode_tile_keys(D), "tile");
-  cudaError_t e = cudaFuncSetAttribute(fa_paged_decode_kernel<T, D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg<D>::kBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(fa_paged_decode_kernel<T, D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kBytes);
+  cudaError_t e = cudaSuccess;
+  for (auto k : {fa_paged_decode_kernel<T, D, 1, false>, fa_paged_decode_kernel<T, D, 2, false>,
+                 fa_paged_decode_kernel<T, D, 1, true>, fa_paged_decode_kernel<T, D, 2, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kBytes);
   if (e == cudaSuccess) e = preload_kernel(fa_paged_finish_kernel<T, D, false>);
   if (e == cudaSuccess) e = preload_kernel(fa_paged_finish_kernel<T, D, true>);
   if (e == cudaSuccess) e = preload_kernel(fa_paged_weights_kernel<Cfg<D>::kKeys>);

@@ -50,6 +50,33 @@ cudaError_t launch_after(void (*k)(P...), dim3 grid, int block, size_t smem, int
   cfg.attrs = attr;
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
+
+// Barrier of a cluster, and loads from the shared memory of one of its CTAs.
+constexpr int kMaxCluster = 8;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+__device__ __forceinline__ int ld_cluster(const int* p, int rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ int2 ld_cluster2(const int* p, int rank) {
+  uint32_t a;
+  int2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(const float2* p, int rank) {
+  const int2 v = ld_cluster2(reinterpret_cast<const int*>(p), rank);
+  return make_float2(__int_as_float(v.x), __int_as_float(v.y));
+}
 #endif
 
 // Wait-site ids / index-check sites of these kernels in the status words.
@@ -126,6 +153,7 @@ struct DecodeArgs {
   int B, Hq, window;
   float scale_log2;
   int unit_heads;            // query heads of a kv group that share a unit: 8 or 16
+  int cluster;               // CTAs of a cluster that takes one unit, 0: equal parts of all tiles
   // Workspace
   DecodePart* parts;         // [kDecodeMaxParts]
   float* part;               // [kDecodeMaxParts][2][16][d] unnormalised O of units cut over CTAs

@@ -374,7 +374,7 @@ fa_status fa_paged_append(const fa_paged_kv* kv, const fa_page_table* table, con
  * d = 128; with scores 4 more for every query head and key that the block table
  * has room for), contents don't matter; calls that may run at the same time
  * need one each.  O, LSE and (but for shared pages) scores are bitwise
- * reproducible.  Two or three launches.
+ * reproducible.  One to three launches.
  */
 fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_paged_kv* kv, const fa_page_table* table,
                           const int* seq_lens, void* o, float* lse, float* scores, int B, int Hq, int window,

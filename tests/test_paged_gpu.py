@@ -388,6 +388,67 @@ def test_decode_is_reproducible_and_independent_of_the_rest_of_the_batch(cuda_li
     assert torch.equal(o1, o2) and torch.equal(l1, l2)
 
 
+def widened(table, keys, page):
+    """The table with columns, far out of range, for this many keys a sequence."""
+    wide = torch.full((table.shape[0], -(-keys // page)), 2 ** 30, dtype=torch.int32, device=table.device)
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
+SHORT = [
+    # lens, Hq, Hkv, d, page, window, dtype: units a cluster takes, shared by 8, 4, 2 or 1 CTAs
+    ([0], 2, 1, 64, 16, 0, BF),
+    ([1], 3, 1, 128, 16, 0, HF),
+    ([640], 8, 2, 128, 16, 0, BF),                            # more tiles than CTAs
+    ([511, 3, 0, 129, 64], 8, 2, 128, 16, 0, HF),             # CTAs without a tile, and whole clusters
+    ([900, 0, 257, 128], 16, 1, 64, 48, 0, BF),               # sixteen heads a group
+    ([700, 65], 40, 2, 128, 16, 0, HF),                       # two chunks, the second not full
+    ([1500, 1000, 100], 13, 1, 64, 64, 300, BF),              # a window, so other tiles than the first
+    ([2000, 10], 4, 4, 128, 256, 1, HF),
+    (list(range(0, 800, 37)), 8, 2, 64, 16, 0, HF),           # 44 units: four CTAs
+    (list(range(0, 600, 15)), 8, 2, 128, 16, 0, BF),          # 80 units: two
+    (list(range(0, 400, 4)), 6, 2, 64, 32, 0, BF),            # 200 units: one
+    (list(range(0, 170)), 4, 2, 128, 16, 0, HF),              # 340 units: more than run at a time
+]
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,page,window,dt", SHORT)
+def test_decode_by_clusters_and_by_equal_parts(cuda_lib, lens, Hq, Hkv, d, page, window, dt):
+    k, v, table, ln = filled(lens, Hkv, page, d, dt, seed=len(lens) + Hq, layout="nhd" if page > 32 else "hnd")
+    q = torch.randn((len(lens), Hq, d), generator=torch.Generator().manual_seed(4)).to(dt).to(DEV)
+    gb = GuardedBuffers(DEV)
+    o, lse = gb.empty((len(lens), Hq, d), dt), gb.empty((len(lens), Hq), torch.float32)
+    for t in (table, widened(table, 1 << 15, page)):
+        o.fill_(float("nan"))
+        lse.fill_(float("nan"))
+        fa.paged_decode(q, k, v, t, ln, window=window, out=o, lse=lse)
+        ok()
+        gb.check()
+        assert_decoded(o, lse, q, k, v, t, ln, d ** -0.5, window, what=f"{t.shape[1]} columns")
+        o2, l2 = fa.paged_decode(q, k, v, t, ln, window=window)
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("bad", ["page", "negative page", "length", "negative length"])
+def test_decode_by_clusters_records_bad_indices(cuda_lib, bad):
+    lens = [400, 300, 50]
+    k, v, table, ln = filled(lens, 2, 16, 128, HF, seed=15)
+    q = torch.randn((3, 4, 128), generator=torch.Generator().manual_seed(3)).to(HF).to(DEV)
+    good_o, good_l = fa.paged_decode(q, k, v, table, ln)
+    ok()
+    t2, n2 = table.clone(), ln.clone()
+    if bad.endswith("page"):
+        t2[1, 3] = -1 if bad.startswith("neg") else k.shape[0]
+    else:
+        n2[1] = -5 if bad.startswith("neg") else table.shape[1] * 16 + 1
+    o, l = fa.paged_decode(q, k, v, t2, n2)
+    s, _ = fa.fa_last_device_status()
+    assert s == fa.FA_ERR_BAD_INDEX
+    for b in (0, 2):                                      # a cluster does not see the other sequences
+        assert torch.equal(o[b], good_o[b]) and torch.equal(l[b], good_l[b])
+    ok()
+
+
 @pytest.mark.parametrize("bad", ["page", "negative page", "length", "negative length"])
 def test_decode_bad_indices_are_recorded(cuda_lib, bad):
     lens = [100, 200, 50]
