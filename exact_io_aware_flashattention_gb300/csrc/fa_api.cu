@@ -915,18 +915,20 @@ DecodeWs decode_ws(int B, int Hq, int d, int page_size, int max_pages, bool with
 // take a second kernel to join them and a scan of the lengths at the start,
 // 3-5 us together, the time of about 4 tiles of a CTA.  So clusters, as large as
 // the `slots` CTAs that run at a time allow, where the busiest CTA gets no more
-// than 4 tiles above an equal part, and no more than 16: lengths that differ
-// leave CTAs idle, equal parts don't.  (Calls on a stream, 32 q and 8 kv heads,
+// than 4 tiles above an equal part, and no more than 12: lengths that differ
+// leave CTAs idle, equal parts don't.  (With scores the weights of a kv head
+// must be summed in one place, so its heads must be one unit's.  Calls on a stream, 32 q and 8 kv heads,
 // d = 128, tiles of 64 keys, us by clusters | equal parts: 1 sequence of 2000
 // keys 7.5 | 8.9, of 4000 10.9 | 9.9; 8 of 1000 9.0 | 12.7, of 2000 14.8 | 19.0;
 // 64 of 250 18.5 | 19.5; 128 of 250 34.3 | 30.5; 8 of 0-2000 12.4 | 15.9; 32 of
-// 0-1000 18.4 | 21.3, of 0-2000 32.4 | 29.9.)
+// 0-1000, 16 tiles a CTA, 18.4 | 21.3, with scores 26.8 | 28.1; of 0-2000 32.4 |
+// 29.9; 8 of 0-8000, d = 64, 16 tiles, with scores, 30.9 | 26.7.)
 int decode_cluster(long long units, long long tiles, int slots) {
   int c = 1;
   while (c < fa::kMaxCluster && units * c * 2 <= slots && c < tiles) c *= 2;
   if (units * c > 2 * slots) return 0;
   const long long waves = (units * c + slots - 1) / slots, busiest = (tiles + c - 1) / c;
-  return busiest <= 16 && waves * busiest <= (units * tiles + slots - 1) / slots + 4 ? c : 0;
+  return busiest <= 12 && waves * busiest <= (units * tiles + slots - 1) / slots + 4 ? c : 0;
 }
 
 // device_state, with the kernels of this section set up (on their first use,
@@ -1135,7 +1137,7 @@ fa_status fa_paged_decode(const void* q, const long long* q_strides, const fa_pa
   if (window > 0) unit_tiles = std::min(unit_tiles, (window - 1LL) / keys + 2);
   // Two CTAs per SM, but no more than there can be tiles.
   int parts = (int)std::min<long long>(units * unit_tiles, std::min(2 * ds->num_sms, fa::kDecodeMaxParts));
-  if (!scores) {
+  if (!scores || G <= a.unit_heads) {
     const int c = decode_cluster(units, unit_tiles, 2 * ds->num_sms);
     a.cluster = c;
     if (c) parts = (int)units * c;

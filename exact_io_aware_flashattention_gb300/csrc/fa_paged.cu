@@ -255,6 +255,46 @@ __device__ __forceinline__ void join_cluster(const DecodeArgs& a, const uint8_t*
   }
 }
 
+// The accumulated weights of the keys of this CTA's tiles [tile, tile + n) of
+// the unit, whose group's heads it has all, from the scores that the CTA
+// stashed.
+template <typename T, int D>
+__device__ __forceinline__ void add_cluster_weights(const DecodeArgs& a, const uint8_t* smem,
+                                                    const Walk<Cfg<D>::kKeys>& w, int rank, int g, int G, int tile, int n) {
+  constexpr int kKeys = Cfg<D>::kKeys;
+  const int lane = threadIdx.x & 31;
+  float2 y[kMaxCluster];               // lane h: head h of the group
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    y[r] = ld_cluster2(reinterpret_cast<const float2*>(smem + kClusterMl<D>) + min(lane, G - 1), r < a.cluster ? r : rank);
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) m = fmaxf(m, y[r].x);
+  const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) l = r < a.cluster ? fmaf(ex2(y[r].x - mu), y[r].y, l) : l;
+  const float lse2 = m + (log2f(l) - Mma<T>::kShift);
+  const int from = max((w.s.tile0 + tile) * kKeys, w.s.first), to = min((w.s.tile0 + tile + n) * kKeys, w.s.len);
+  for (int key0 = from + (threadIdx.x & ~31); key0 < to; key0 += kConsumers * 32) {
+    const int key = key0 + lane, c = key / a.kv.page_size;
+    const bool in = key < to;
+    const int page = in ? a.table.pages[w.b * a.table.stride + c] : -1;
+    const float* x = a.stash + (((long long)w.b * a.kv.Hkv + g) * a.stash_keys + (in ? key : from)) * G;
+    float sum = 0.f;
+    if (G % 4 == 0) {
+      for (int h = 0; h < G; h += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(x + h);
+        sum += (ex2(v.x - __shfl_sync(0xffffffffu, lse2, h)) + ex2(v.y - __shfl_sync(0xffffffffu, lse2, h + 1))) +
+               (ex2(v.z - __shfl_sync(0xffffffffu, lse2, h + 2)) + ex2(v.w - __shfl_sync(0xffffffffu, lse2, h + 3)));
+      }
+    } else {
+      for (int h = 0; h < G; ++h) sum += ex2(x[h] - __shfl_sync(0xffffffffu, lse2, h));
+    }
+    if (page >= 0 && page < a.kv.num_pages)
+      atomicAdd(&a.scores[((long long)page * a.kv.Hkv + g) * a.kv.page_size + (key - c * a.kv.page_size)], sum);
+  }
+}
+
 template <typename T, int D, int NT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 2)
     fa_paged_decode_kernel(const __grid_constant__ TmaMap4 tmK, const __grid_constant__ TmaMap4 tmV, const DecodeArgs a,
@@ -462,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t q[NT][D / 16][2], q_next[NT][D / 16][2];
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
   bool dead = false, fresh = true;
+  const int my_tile = w.tile, my_n = (int)w.left;
   int unit_pos = w.tile;                          // tile of the unit at which this CTA entered it
   // (Where the registers for a second set of query rows are lacking they are
   // loaded when their unit comes up.)
@@ -737,6 +778,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (a.cluster > 1) cluster_sync();
     else consumer_sync();
     join_cluster<T, D>(a, smem, w, rank, h0, min(h1, h0 + 8 * NT));
+    if (a.stash) {
+      __syncwarp();
+      add_cluster_weights<T, D>(a, smem, w, rank, g, G, my_tile, my_n);
+    }
     __syncwarp();
     if (a.cluster > 1) cluster_sync();             // nobody exits while its share is read
   }

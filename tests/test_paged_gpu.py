@@ -429,6 +429,26 @@ def test_decode_by_clusters_and_by_equal_parts(cuda_lib, lens, Hq, Hkv, d, page,
         assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,d,page,window,dt", SHORT)
+def test_scores_by_clusters_and_by_equal_parts(cuda_lib, lens, Hq, Hkv, d, page, window, dt):
+    k, v, table, ln = filled(lens, Hkv, page, d, dt, seed=len(lens) + Hq + 1, layout="nhd" if page > 32 else "hnd")
+    g = torch.Generator().manual_seed(5)
+    q = torch.randn((len(lens), Hq, d), generator=g).to(dt).to(DEV)
+    before = torch.rand(k.shape[:3], generator=g).to(DEV)
+    gb = GuardedBuffers(DEV)
+    scores = gb.empty(tuple(k.shape[:3]), torch.float32)
+    for t in (table, widened(table, 1 << 15, page)):
+        ws = gb.empty((fa.paged_decode_workspace(len(lens), Hq, k, t, True).numel(),), torch.uint8)
+        scores.copy_(before)
+        o, lse = fa.paged_decode(q, k, v, t, ln, window=window, scores=scores, workspace=ws)
+        ok()
+        gb.check()
+        assert_decoded(o, lse, q, k, v, t, ln, d ** -0.5, window, scores, before, f"{t.shape[1]} columns")
+        again = before.clone()
+        o2, l2 = fa.paged_decode(q, k, v, t, ln, window=window, scores=again, workspace=ws)
+        assert torch.equal(o, o2) and torch.equal(lse, l2) and torch.equal(scores, again)
+
+
 @pytest.mark.parametrize("bad", ["page", "negative page", "length", "negative length"])
 def test_decode_by_clusters_records_bad_indices(cuda_lib, bad):
     lens = [400, 300, 50]
