@@ -396,12 +396,10 @@ __global__ void __launch_bounds__(kCopyThreads, 8)
   const int unit = blockIdx.x / blocks_per_unit, b = unit / a.kv.Hkv, g = unit - b * a.kv.Hkv, ps = a.kv.page_size;
   const int r0 = (blockIdx.x - unit * blocks_per_unit) * kBlockRows + warp * kRows;
   wait_for_previous();
-  const int m = a.new_lens[b];
-  if (r0 >= m) return;
-  const int n = min(kRows, m - r0);
+  const int i = r0 + lane, j = lane < kRows && i < a.budget ? a.kept[(long long)unit * a.budget + i] : -1;
+  if (__all_sync(0xffffffffu, j < 0)) return;
   long long from = -1, to = -1;
-  if (lane < n) {
-    const int i = r0 + lane, j = a.kept[(long long)unit * a.budget + i];
+  if (j >= 0) {
     const int cj = page_of(j, a), ci = page_of(i, a);
     const int p = a.table.pages[b * a.table.stride + cj], q = a.dst.pages[b * a.dst.stride + ci];
     if (p >= 0 && p < a.kv.num_pages && q >= 0 && q < a.kv.num_pages) {
