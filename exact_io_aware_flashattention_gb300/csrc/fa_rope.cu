@@ -153,24 +153,34 @@ __device__ __forceinline__ Chunk chunk_of(int c, int rot) {
   return k;
 }
 
-// Heads [h0, h1) of one token: in + h * in_sh -> out + h * out_sh.
+// The next heads of [h, h1) of one token, in + h * in_sh.
+struct Batch {
+  uint4 a[kUnroll], b[kUnroll];
+};
+template <typename T>
+__device__ __forceinline__ void load_heads(const T* in, long long in_sh, int h, int h1, const Chunk& ck, Batch& x) {
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u)
+    if (h + u < h1) {
+      x.a[u] = __ldcs(reinterpret_cast<const uint4*>(in + (h + u) * in_sh + ck.e0));
+      x.b[u] = __ldcs(reinterpret_cast<const uint4*>(in + (h + u) * in_sh + ck.e1));
+    }
+}
+// Heads [h0, h1) of one token: in + h * in_sh -> out + h * out_sh; the first
+// of them are in x already if `loaded`.
 template <typename T, bool kInter>
 __device__ __forceinline__ void do_heads(const T* in, long long in_sh, T* out, long long out_sh, int h0, int h1,
-                                         const Chunk& ck, bool turned, const float (&cs)[8], const float (&sn)[8]) {
+                                         const Chunk& ck, bool turned, const float (&cs)[8], const float (&sn)[8], Batch& x,
+                                         bool loaded) {
   for (int h = h0; h < h1; h += kUnroll) {
-    uint4 a[kUnroll], b[kUnroll];
+    if (!loaded) load_heads(in, in_sh, h, h1, ck, x);
+    loaded = false;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
       if (h + u < h1) {
-        a[u] = __ldcs(reinterpret_cast<const uint4*>(in + (h + u) * in_sh + ck.e0));
-        b[u] = __ldcs(reinterpret_cast<const uint4*>(in + (h + u) * in_sh + ck.e1));
-      }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (h + u < h1) {
-        if (turned) turn8<T, kInter>(a[u], b[u], cs, sn);
-        __stcs(reinterpret_cast<uint4*>(out + (h + u) * out_sh + ck.e0), a[u]);
-        __stcs(reinterpret_cast<uint4*>(out + (h + u) * out_sh + ck.e1), b[u]);
+        if (turned) turn8<T, kInter>(x.a[u], x.b[u], cs, sn);
+        __stcs(reinterpret_cast<uint4*>(out + (h + u) * out_sh + ck.e0), x.a[u]);
+        __stcs(reinterpret_cast<uint4*>(out + (h + u) * out_sh + ck.e1), x.b[u]);
       }
   }
 }
@@ -182,24 +192,32 @@ __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeArgs a, int
   __shared__ Pairs pairs;
   launch_dependents();
   wait_for_previous();
-  load_pairs(a.r, pairs, st);
-  __syncthreads();
   const int nch = a.d / 16, tpb = kThreads / nch;
   const int lt = threadIdx.x / nch, c = threadIdx.x - lt * nch;
   const long long t = (long long)blockIdx.x * tpb + lt;
-  if (lt >= tpb || t >= (long long)a.B * a.N) return;
-  const int b = (int)(t / a.N), n = (int)(t - (long long)b * a.N);
+  const bool live = lt < tpb && t < (long long)a.B * a.N;
+  const int b = live ? (int)(t / a.N) : 0, n = live ? (int)(t - (long long)b * a.N) : 0;
   const Chunk ck = chunk_of<kInter>(c, a.r.rot);
+  const int h0 = blockIdx.y * hpb, h1 = min(h0 + hpb, a.Hq + a.Hk);
+  const T* q = static_cast<const T*>(a.q.p) + b * a.q.sb + n * a.q.sn;
+  const T* k = static_cast<const T*>(a.k.p) + b * a.k.sb + n * a.k.sn;
+  // The first rows are on their way while the angles are formed.
+  Batch x;
+  if (live) {
+    if (h0 < a.Hq) load_heads(q, a.q.sh, h0, min(h1, a.Hq), ck, x);
+    else load_heads(k, a.k.sh, h0 - a.Hq, h1 - a.Hq, ck, x);
+  }
+  load_pairs(a.r, pairs, st);
+  __syncthreads();
+  if (!live) return;
   float cs[8] = {}, sn[8] = {};
   if (ck.turned) load_angles(a.r, pairs, a.r.pos + b * a.r.pos_batch + n, c, cs, sn);
-  const int h0 = blockIdx.y * hpb, h1 = min(h0 + hpb, a.Hq + a.Hk);
-  auto rows = [&](const RowView& in, const RowView& out, int lo, int hi) {
-    if (lo < hi)
-      do_heads<T, kInter>(static_cast<const T*>(in.p) + b * in.sb + n * in.sn, in.sh,
-                          static_cast<T*>(out.p) + b * out.sb + n * out.sn, out.sh, lo, hi, ck, ck.turned, cs, sn);
-  };
-  rows(a.q, a.q_out, h0, min(h1, a.Hq));
-  rows(a.k, a.k_out, max(h0 - a.Hq, 0), h1 - a.Hq);
+  if (h0 < a.Hq)
+    do_heads<T, kInter>(q, a.q.sh, static_cast<T*>(a.q_out.p) + b * a.q_out.sb + n * a.q_out.sn, a.q_out.sh, h0, min(h1, a.Hq),
+                        ck, ck.turned, cs, sn, x, true);
+  if (h1 > a.Hq)
+    do_heads<T, kInter>(k, a.k.sh, static_cast<T*>(a.k_out.p) + b * a.k_out.sb + n * a.k_out.sn, a.k_out.sh,
+                        max(h0 - a.Hq, 0), h1 - a.Hq, ck, ck.turned, cs, sn, x, h0 >= a.Hq);
 }
 
 // Where token t goes: sequence, index in it, page and slot.  Returns false for
@@ -242,35 +260,43 @@ __global__ void __launch_bounds__(kThreads) fa_append_kernel(const AppendArgs a,
   __shared__ Pairs pairs;
   launch_dependents();
   wait_for_previous();
-  load_pairs(a.r, pairs, st);
-  __syncthreads();
   const int nch = a.kv.d / 16, tpb = kThreads / nch;
   const int lt = threadIdx.x / nch, c = threadIdx.x - lt * nch;
   const long long t = (long long)blockIdx.x * tpb + lt;
-  if (lt >= tpb || t >= a.T) return;
-  int page, slot;
-  if (!place_token(a, (int)t, st, page, slot)) return;
+  const bool live = lt < tpb && t < a.T;
   const int Hkv = a.kv.Hkv;
   const int h0 = blockIdx.y * hpb, h1 = min(h0 + hpb, a.Hq + 2 * Hkv);
+  const int k0 = max(h0 - a.Hq, 0), k1 = min(h1 - a.Hq, Hkv), v0 = max(h0 - a.Hq - Hkv, 0), v1 = h1 - a.Hq - Hkv;
   const Chunk ck = chunk_of<kInter>(c, a.r.rot);
+  const T* q = static_cast<const T*>(a.q.p) + t * a.q.sn;
+  const T* k = static_cast<const T*>(a.k.p) + t * a.k.sn;
+  const T* v = static_cast<const T*>(a.v.p) + t * a.v.sn;
+  // The first rows are on their way while the slot is looked up and the angles
+  // are formed.
+  Batch x;
+  const int first = h0 < a.Hq ? 0 : k0 < k1 ? 1 : 2;
+  if (live) {
+    if (first == 0) load_heads(q, a.q.sh, h0, min(h1, a.Hq), ck, x);
+    else if (first == 1) load_heads(k, a.k.sh, k0, k1, ck, x);
+    else load_heads(v, a.v.sh, v0, v1, ck, x);
+  }
+  load_pairs(a.r, pairs, st);
+  __syncthreads();
+  int page, slot;
+  if (!live || !place_token(a, (int)t, st, page, slot)) return;
   float cs[8] = {}, sn[8] = {};
   if (ck.turned && h0 < a.Hq + Hkv) load_angles(a.r, pairs, a.r.pos + t, c, cs, sn);
   const long long at = page * a.kv.s_page + slot * a.kv.s_slot;
-  if (h0 < a.Hq)
-    do_heads<T, kInter>(static_cast<const T*>(a.q.p) + t * a.q.sn, a.q.sh, static_cast<T*>(a.q_out.p) + t * a.q_out.sn,
-                        a.q_out.sh, h0, min(h1, a.Hq), ck, ck.turned, cs, sn);
-  int lo = max(h0 - a.Hq, 0), hi = min(h1 - a.Hq, Hkv);
-  if (lo < hi) {
-    do_heads<T, kInter>(static_cast<const T*>(a.k.p) + t * a.k.sn, a.k.sh, static_cast<T*>(a.kv.k) + at, a.kv.s_head, lo,
-                        hi, ck, ck.turned, cs, sn);
+  if (first == 0)
+    do_heads<T, kInter>(q, a.q.sh, static_cast<T*>(a.q_out.p) + t * a.q_out.sn, a.q_out.sh, h0, min(h1, a.Hq), ck, ck.turned,
+                        cs, sn, x, true);
+  if (k0 < k1) {
+    do_heads<T, kInter>(k, a.k.sh, static_cast<T*>(a.kv.k) + at, a.kv.s_head, k0, k1, ck, ck.turned, cs, sn, x, first == 1);
     if (a.scores)
-      for (int h = lo + c; h < hi; h += nch) a.scores[((long long)page * Hkv + h) * a.kv.page_size + slot] = 0.f;
+      for (int h = k0 + c; h < k1; h += nch) a.scores[((long long)page * Hkv + h) * a.kv.page_size + slot] = 0.f;
   }
-  lo = max(h0 - a.Hq - Hkv, 0);
-  hi = h1 - a.Hq - Hkv;
-  if (lo < hi)
-    do_heads<T, kInter>(static_cast<const T*>(a.v.p) + t * a.v.sn, a.v.sh, static_cast<T*>(a.kv.v) + at, a.kv.s_head, lo,
-                        hi, ck, false, cs, sn);
+  if (v0 < v1)
+    do_heads<T, kInter>(v, a.v.sh, static_cast<T*>(a.kv.v) + at, a.kv.s_head, v0, v1, ck, false, cs, sn, x, first == 2);
 }
 
 // Heads per block: as many as still leave 16 blocks of 128 threads an SM, so
