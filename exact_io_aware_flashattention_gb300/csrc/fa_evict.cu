@@ -14,25 +14,28 @@
 //
 // fa_evict_select_kernel.  One cluster of 1, 2, 4 or 8 CTAs per (b, g), each
 // with an equal run of the keys, held in shared memory as order-preserving
-// integers (protected ones as the largest).  The m-th largest is found 11, 11
-// and 10 bits at a time: every CTA counts its keys that match the digits found
-// so far into a histogram, reads the others' through distributed shared memory
-// (64 sums of 32 bins first, then 32 bins), and all reach the same digit; three
-// passes over shared memory replace a sort.  It stops early when the digit's
-// bin is wanted whole.  The kept indices then go out in order: each warp counts
-// its run of keys, sums the counts of the warps and CTAs before, and writes.
+// integers (protected ones as the largest).  The range of the others that
+// holds the last key to stay is narrowed to one of 2048 equal parts, at most
+// three times: every CTA counts its keys of the range into a histogram, reads
+// the others' through distributed shared memory (64 sums of 32 bins first, then
+// 32 bins), and all reach the same part; three passes over shared memory
+// replace a sort.  (The first digits of all keys instead of their range: scores
+// within a few powers of two meet in a few bins; from 1.0 to 1.01, 106.3 us
+// instead of 102.9 in the first example below.)  It stops early when the part is wanted whole.  The kept indices then go
+// out in order: each warp counts its run of keys, sums the counts of the warps
+// and CTAs before, and writes.
 //
 // fa_evict_copy_kernel.  A warp takes 8 consecutive kept keys: eight lanes look
 // one up each (index, source page, target page) and move its score, then the
 // rows go 16 bytes a lane, all loads in flight before the first store.  (16 or
 // 32 keys a warp, in rounds of 8 or 4, fill the last wave worse: 2-5 % slower.)
 //
-// Measured: 2 sequences of 131072 keys, 8 heads, d = 128, to 32768: 103.5 us, of
-// which the selection 19 and the copy of 541 MB 82 (97 % of the 6.79 TB/s copy
-// rate); 16 sequences of 0 to 8192 keys to 2048: 43 us, the copy of 202 MB 32;
-// one of 1000 keys, 2 heads: 7.4 us.  The selection is bound by instructions
-// and latencies: of its 33 thousand cycles at 16384 keys a CTA the loads take
-// 7, the histograms 7, the exchanges over the cluster 10, the list 9.
+// Measured: 2 sequences of 131072 keys, 8 heads, d = 128, to 32768: 102.5 us, of
+// which the selection 18 and the copy of 541 MB 82 (97 % of the 6.79 TB/s copy
+// rate); 16 sequences of 0 to 8192 keys to 2048: 42.5 us, the copy of 202 MB 32;
+// one of 1000 keys, 2 heads: 7.7 us.  The selection is bound by instructions
+// and latencies: loads, histograms, exchanges over the cluster and the list
+// take about a quarter each.
 #include "fa_paged.h"
 #include "sm103a.cuh"
 
@@ -71,6 +74,8 @@ struct Select {
   int coarse[3][kBins / 32];          // sums of 32 bins
   int above[kWarps], equal[kWarps];   // each warp's keys above the threshold, and equal to it
   int2 counts;                        // the CTA's
+  uint32_t least[kWarps], most[kWarps];   // each warp's smallest and largest key that is not protected
+  uint2 range;                        // the CTA's
   int bin, left, whole;
 };
 
@@ -117,11 +122,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int* pages = a.table.pages + b * a.table.stride;
   const float* pool = a.scores + (long long)g * ps;
   const long long page_scores = (long long)a.kv.Hkv * ps;
-  // Keys [from, from + n) into shared memory, in fours, and the first digits
-  // into `hist` if given.  Past the sequence's end 0, the smallest: equal keys
-  // go by index, so those never come before a key of the sequence.  n rounded
-  // up to 128 is filled.
-  auto load = [&](int from, int n, int* hist) {
+  // Keys [from, from + n) into shared memory, in fours, with the smallest and
+  // largest of those that are not protected.  Past the sequence's end 0, the
+  // smallest: equal keys go by index, so those never come before a key of the
+  // sequence.  n rounded up to 128 is filled.
+  uint32_t least = 0xffffffffu, most = 0;
+  auto load = [&](int from, int n) {
     constexpr int kBatch = 8;          // page numbers, then copies, in flight per thread
     const int quads = (n + 127) / 128 * 32;
     uint4* quad = reinterpret_cast<uint4*>(keys);
@@ -144,7 +150,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     wait_copies();
-    if (hist) __syncthreads();         // the histogram is empty by now
     // Each thread turns the scores it copied into keys.
     for (int i = tid; i < quads; i += kThreads) {
       const int j = from + 4 * i;
@@ -152,17 +157,19 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (j < from + n) {
         const float4 x = reinterpret_cast<const float4*>(quad)[i];
         k = make_uint4(score_key(x.x), score_key(x.y), score_key(x.z), score_key(x.w));
-        if (j < lo || j + 4 > hi) {
+        if (j >= lo && j + 4 <= hi) {
+          least = min(least, min(min(k.x, k.y), min(k.z, k.w)));
+          most = max(most, max(max(k.x, k.y), max(k.z, k.w)));
+        } else {
           uint32_t* y = &k.x;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (j + e < lo || j + e >= hi) y[e] = j + e < len ? kProtected : 0u;
-        }
-        if (hist) {
-          atomicAdd(&hist[k.x >> 21], 1);
-          atomicAdd(&hist[k.y >> 21], 1);
-          atomicAdd(&hist[k.z >> 21], 1);
-          atomicAdd(&hist[k.w >> 21], 1);
+            if (j + e < lo || j + e >= hi) {
+              y[e] = j + e < len ? kProtected : 0u;
+            } else {
+              least = min(least, y[e]);
+              most = max(most, y[e]);
+            }
         }
       }
       quad[i] = k;
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int n = min(cap, j0 + n_run - from);
       if (!cached) {
         __syncthreads();
-        load(from, n, nullptr);
+        load(from, n);
         __syncthreads();
       }
       body(from, n);
@@ -182,32 +189,45 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
 
-  // The m-th largest key, digit by digit.
-  uint32_t prefix = 0, mask = 0;
-  int need = m;
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+  // The range of the keys to choose from.
+  for (int from = j0; from < j0 + n_run; from += cap) load(from, min(cap, j0 + n_run - from));
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) {
+    sh.least[warp] = least;
+    sh.most[warp] = most;
+  }
+  __syncthreads();
+  least = __reduce_min_sync(0xffffffffu, sh.least[lane % kWarps]);
+  most = __reduce_max_sync(0xffffffffu, sh.most[lane % kWarps]);
+  if (cluster > 1) {
+    if (tid == 0) sh.range = make_uint2(least, most);
+    cluster_sync();
+    const int2 r = ld_cluster2(reinterpret_cast<const int*>(&sh.range), lane < cluster ? lane : rank);
+    least = __reduce_min_sync(0xffffffffu, (uint32_t)r.x);
+    most = __reduce_max_sync(0xffffffffu, (uint32_t)r.y);
+  }
+
+  // The m-th largest key lies in [base, base + span], which each pass narrows
+  // to one of at most 2048 equal parts.
+  uint32_t base = least, span = most - least;
+  int need = m - a.sinks - a.recent;
+  bool whole = need == 0;              // only the protected ones stay
+  for (int pass = 0; !whole; ++pass) {
+    const int shift = max(21 - __clz(span), 0);    // clz(0) = 32
     int* hist = sh.hist[pass];
-    if (pass == 0) {
-      for (int from = j0; from < j0 + n_run; from += cap) load(from, min(cap, j0 + n_run - from), hist);
-    } else {
-      pieces([&](int, int n) {
-        const int quads = (n + 3) / 4;
+    pieces([&](int, int n) {
+      const int quads = (n + 3) / 4;
 #pragma unroll 2
-        for (int i = tid; i < quads; i += kThreads) {
-          const uint4 k = reinterpret_cast<const uint4*>(keys)[i];
-          const bool x = (k.x & mask) == prefix, y = (k.y & mask) == prefix;
-          const bool z = (k.z & mask) == prefix, w = (k.w & mask) == prefix;
-          if (x || y || z || w) {
-            const uint32_t digit = (1u << bits) - 1;
-            if (x) atomicAdd(&hist[(k.x >> shift) & digit], 1);
-            if (y) atomicAdd(&hist[(k.y >> shift) & digit], 1);
-            if (z) atomicAdd(&hist[(k.z >> shift) & digit], 1);
-            if (w) atomicAdd(&hist[(k.w >> shift) & digit], 1);
-          }
-        }
-      });
-    }
+      for (int i = tid; i < quads; i += kThreads) {
+        const uint4 k = reinterpret_cast<const uint4*>(keys)[i];
+        const uint32_t x = k.x - base, y = k.y - base, z = k.z - base, w = k.w - base;
+        if (x <= span) atomicAdd(&hist[x >> shift], 1);
+        if (y <= span) atomicAdd(&hist[y >> shift], 1);
+        if (z <= span) atomicAdd(&hist[z >> shift], 1);
+        if (w <= span) atomicAdd(&hist[w >> shift], 1);
+      }
+    });
     __syncthreads();
     // Sums of 32 bins, so that the others need to read 64 of them and then 32
     // bins, not all 2048.
@@ -257,18 +277,19 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     __syncthreads();
-    prefix |= (uint32_t)sh.bin << shift;
-    mask |= ((1u << bits) - 1) << shift;
+    base += (uint32_t)sh.bin << shift;
+    span = min(most - base, (1u << shift) - 1);    // (never past the largest: protected keys are no candidates)
     need = sh.left;
-    if (sh.whole) break;               // every key with these digits stays
+    whole = sh.whole;                  // every key of the part stays
+    if (shift == 0) break;
   }
-  // A key stays if its digits are above `bound`, or, where only some of the
-  // keys with the last digits found are wanted (ties), equal to it and among
-  // the first `need` such keys.  Each warp takes a run of a piece, 128 keys at a
-  // time, four consecutive ones a lane.  (Without ties the last digits are at
-  // least 1: all digits 0 would mean that every key stays.)
-  const bool ties = !sh.whole;
-  const uint32_t bound = ties ? prefix : prefix - 1, below = (1u << lane) - 1;
+  // A key stays if it is above `bound`, or, where only some of the equal keys
+  // in the last part are wanted (ties), equal to it and among the first `need`
+  // such keys.  Each warp takes a run of a piece, 128 keys at a time, four
+  // consecutive ones a lane.  (Without ties base is at least 1: a base of 0
+  // would mean that every key stays.)
+  const bool ties = !whole;
+  const uint32_t bound = ties ? base : need == 0 ? most : base - 1, below = (1u << lane) - 1;
   int above_before = 0, equal_before = 0;          // of the CTAs before, then of the pieces before
   // Keys above and equal to the bound in the warp's run of a piece, then per
   // warp in shared memory.
@@ -282,9 +303,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     warp_run(n, i0, i1);
     for (int i = i0 + 4 * lane; i < i1; i += 128) {
       const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
-      above += ((k.x & mask) > bound) + ((k.y & mask) > bound) + ((k.z & mask) > bound) + ((k.w & mask) > bound);
+      above += (k.x > bound) + (k.y > bound) + (k.z > bound) + (k.w > bound);
       if (ties)
-        equal += ((k.x & mask) == bound) + ((k.y & mask) == bound) + ((k.z & mask) == bound) + ((k.w & mask) == bound);
+        equal += (k.x == bound) + (k.y == bound) + (k.z == bound) + (k.w == bound);
     }
   };
   auto publish = [&](int above, int equal) {
@@ -352,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = i0; i < i1; i += 128) {
         const int at = i + 4 * lane;
         const uint4 q = *reinterpret_cast<const uint4*>(keys + at);
-        const bool keep[4] = {(q.x & mask) > bound, (q.y & mask) > bound, (q.z & mask) > bound, (q.w & mask) > bound};
+        const bool keep[4] = {q.x > bound, q.y > bound, q.z > bound, q.w > bound};
         out += put(out, at, keep);
       }
       return;
@@ -361,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = i0; i < i1; i += 128) {
       const int at = i + 4 * lane;
       const uint4 q = *reinterpret_cast<const uint4*>(keys + at);
-      const uint32_t k[4] = {q.x & mask, q.y & mask, q.z & mask, q.w & mask};
+      const uint32_t k[4] = {q.x, q.y, q.z, q.w};
       bool keep[4], eq[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
