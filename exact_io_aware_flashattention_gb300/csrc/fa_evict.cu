@@ -21,9 +21,9 @@
 // 32 bins), and all reach the same part; three passes over shared memory
 // replace a sort.  (The first digits of all keys instead of their range: scores
 // within a few powers of two meet in a few bins; from 1.0 to 1.01, 106.3 us
-// instead of 102.9 in the first example below.)  It stops early when the part is wanted whole.  The kept indices then go
-// out in order: each warp counts its run of keys, sums the counts of the warps
-// and CTAs before, and writes.
+// instead of 102.9 in the first example below.)  It stops early when the part
+// is wanted whole.  The kept indices then go out in order: each warp counts its
+// run of keys, sums the counts of the warps and CTAs before, and writes.
 //
 // fa_evict_copy_kernel.  A warp takes 8 consecutive kept keys: eight lanes look
 // one up each (index, source page, target page) and move its score, then the

@@ -21,15 +21,16 @@
 // Bound by HBM: every element is read once and written once.  A thread owns
 // one token and eight pairs (two 16-byte vectors of a row): its eight
 // cosines and sines are formed once and used for all the heads of its block.
-// Loads and stores are marked as streaming: nothing is read twice.
+// Loads and stores are marked as streaming: nothing is read twice.  The first
+// heads' rows are requested before the angles are formed and, in the append,
+// the slot is looked up (gradient 52.6 -> 51.9 us, prompt 31.4 -> 30.9).
 //
 // Measured (calls in a row on three sets of tensors), of the 6.79 TB/s copy
 // rate: q and k of 4 x (16 + 16) heads x 2048 tokens, d = 128, 134 MB: 23.5 us,
-// 84 %; the gradient for 2 x (32 + 8) x 8192, 336 MB: 52.7 us, 94 %; appending
+// 84 %; the gradient for 2 x (32 + 8) x 8192, 336 MB: 51.9 us, 95 %; appending
 // 7357 prompt tokens (32 q heads turned, 8 k and 8 v heads stored), 181 MB:
-// 31.4 us, 85 % (95 registers leave 20 warps an SM, and each token first looks
-// its slot up); one token for each of 64 sequences: 3.8 us, of which the launch
-// is most.
+// 30.9 us, 86 % (90 registers leave 20 warps an SM); one token for each of 64
+// sequences: 3.7 us, of which the launch is most.
 #include "fa_paged.h"
 #include "sm103a.cuh"
 
