@@ -12,7 +12,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/cuda/EmptyTensor.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -78,8 +79,10 @@ bool dense(const at::Tensor& t, const Where& w, at::ScalarType type, Shape shape
 bool fits(int64_t n) { return n >= 0 && n <= INT32_MAX; }
 
 const long long* strides(const at::Tensor& t) { return reinterpret_cast<const long long*>(t.strides().data()); }
-at::Tensor empty(Shape shape, at::ScalarType type, const Where& w) {
-  return at::detail::empty_cuda(shape, type, w.device, std::nullopt);
+// On the current device, which is the call's.
+at::Tensor empty(Shape shape, at::ScalarType type) {
+  return at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                   type, std::nullopt);
 }
 int dtype_code(at::ScalarType t) { return t == at::kBFloat16 ? FA_BF16 : t == at::kHalf ? FA_FP16 : -1; }
 
@@ -169,7 +172,7 @@ bool output(PyObject* o, const Where& w, at::ScalarType type, Shape shape, bool 
   const at::Tensor* x;
   if (!maybe(o, x)) return false;
   if (!x) {
-    t = empty(shape, type, w);
+    t = empty(shape, type);
     return true;
   }
   if (!(whole ? dense(*x, w, type, shape) : rows_of(*x, w, type, shape))) return false;
@@ -267,20 +270,19 @@ PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (a[5] == Py_None) scale = (float)(1.0 / std::sqrt((double)d));
   else if (PyFloat_CheckExact(a[5])) scale = (float)PyFloat_AS_DOUBLE(a[5]);
   else Py_RETURN_NONE;
-  at::Tensor o, lse, own;
+  at::Tensor o, lse;
+  c10::DataPtr own;
   if (ws && (ws->dim() != 1 || !dense(*ws, c.w, at::kByte, ws->sizes()))) Py_RETURN_NONE;
+  size_t bytes = ws ? (size_t)ws->numel() : 0;
   if (!ws) {
-    const size_t bytes =
-        p_decode_ws((int)B, (int)Hq, c.kv.Hkv, c.kv.d, c.kv.page_size, c.table.max_pages, scores != nullptr);
+    bytes = p_decode_ws((int)B, (int)Hq, c.kv.Hkv, c.kv.d, c.kv.page_size, c.table.max_pages, scores != nullptr);
     if (bytes == 0) Py_RETURN_NONE;
-    own = empty((int64_t)bytes, at::kByte, c.w);
-    ws = &own;
+    own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
   }
   if (!output(a[8], c.w, c.type, {B, Hq, d}, true, o) || !output(a[9], c.w, at::kFloat, {B, Hq}, true, lse)) Py_RETURN_NONE;
   fa_status s;
   const void* qp = q->const_data_ptr();
-  void *op = o.mutable_data_ptr(), *lp = lse.mutable_data_ptr(), *wp = ws->mutable_data_ptr();
-  const size_t bytes = (size_t)ws->numel();
+  void *op = o.mutable_data_ptr(), *lp = lse.mutable_data_ptr(), *wp = ws ? ws->mutable_data_ptr() : own.mutable_get();
   Py_BEGIN_ALLOW_THREADS;
   s = p_decode(qp, strides(*q), &c.kv, &c.table, c.lens, op, static_cast<float*>(lp), scores, (int)B, (int)Hq, window, scale,
                wp, bytes, c.w.stream);
