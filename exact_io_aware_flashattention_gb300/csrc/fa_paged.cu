@@ -717,8 +717,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           mine[d1] = o[n][k][2] * f[0];
           mine[D + d1] = o[n][k][3] * f[1];
         }
-        consumer_sync();
-        // 16 threads a head, D / 16 elements each.
+        // 16 threads a head, D / 16 elements each.  The last read of ml before
+        // the barrier: behind it a warp may be past its tiles of the next unit
+        // and store that unit's (max, sum) while others still sum here.
         const int hh = threadIdx.x >> 4, e0 = (threadIdx.x & 15) * (D / 16), h = h0 + n * 8 + hh;
         float M = -INFINITY, L = 0.f;
 #pragma unroll
@@ -728,6 +729,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float2 y = ml[x * 16 + n * 8 + hh];
           L += M == -INFINITY ? 0.f : y.y * ex2(y.x - M);
         }
+        consumer_sync();
         float r[D / 16];
 #pragma unroll
         for (int e = 0; e < D / 16; e += 4) {

@@ -367,6 +367,28 @@ def test_decode_many_small_weights(cuda_lib, dt, gap):
     assert abs(lse[0, 0].item() - math.log(math.exp(gap) + n - 1)) <= n * 2.0 ** -24 + 2.0 ** -20
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,d,longest,dt", [
+    (3000, 8, 8, 128, 16, BF),
+    (1500, 16, 4, 128, 40, HF),
+    (1200, 32, 2, 128, 16, BF),             # sixteen heads a group
+    (2000, 8, 4, 64, 16, HF),
+    (1000, 20, 2, 64, 30, BF),
+])
+def test_decode_many_units_of_one_tile(cuda_lib, B, Hq, Hkv, d, longest, dt):
+    # Dozens of units in a row for each CTA, most of them of one 16-key slice,
+    # so that three of its four warps have nothing to do between one unit's sums
+    # and the next's: each unit's statistics stay apart, in every run alike.
+    lens = torch.randint(0, longest + 1, (B,), generator=torch.Generator().manual_seed(B)).tolist()
+    k, v, table, ln = filled(lens, Hkv, 16, d, dt, seed=B + 1, sigma=3.0)
+    q = torch.randn((B, Hq, d), generator=torch.Generator().manual_seed(B + 2)).to(dt).to(DEV)
+    o, lse = fa.paged_decode(q, k, v, table, ln, scale=0.2)
+    again = [fa.paged_decode(q, k, v, table, ln, scale=0.2) for _ in range(30)]
+    ok()
+    assert_decoded(o, lse, q, k, v, table, ln, 0.2, 0, what=f"{B} short sequences")
+    for o2, l2 in again:
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
 def test_decode_pages_shared_by_sequences(cuda_lib):
     # Two sequences with a common prefix: the weights of both add up.
     k, v, table, ln = filled([200, 200], 2, 16, 64, BF, seed=12)
