@@ -367,6 +367,9 @@ fa_status fa_paged_append(const fa_paged_kv* kv, const fa_page_table* table, con
  * Writes o [B,Hq,d] and lse fp32 [B,Hq] (natural log), both contiguous.  A
  * sequence of length 0 gets o = 0, lse = -inf.  Cache slots that are not
  * visible may hold anything, NaN included.
+ * Scores, softmax and sums are fp32; a weight enters the product with v as the
+ * sum of two values of dtype, off by 2^-15 (FA_BF16) or 2^-21 (FA_FP16) of itself
+ * at most, or by 2^-37 of the row's largest; o is rounded once.
  * scores (may be NULL), fp32 [num_pages, Hkv, page_size] contiguous: the entry
  * of each visible key grows by the sum over the group's heads of its softmax
  * weight.  Sequences may share pages: their weights add up (in no fixed order).

@@ -389,6 +389,69 @@ def test_decode_many_units_of_one_tile(cuda_lib, B, Hq, Hkv, d, longest, dt):
         assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
+# Weights at more than the tensors' precision.  q and k are small integers, so
+# the scores are exact in fp32 whatever the order of the sums, and with n keys
+# of scores |x| <= X (log2 units) what is left of the error of o, relative to A =
+# sum p |v|, is:
+#   the weights as two values of the tensors' type, the first rounded down (off
+#     by up to 2 u), the second to nearest: 2 u^2 (fp16: and half a subnormal
+#     step, 2^-25, next to a largest weight of 2^12, so 2^-37 of max |v| for
+#     each key);
+#   x: two roundings of at most X 2^-24 in its scaling and one of 2 X 2^-24 in
+#     its difference to the maximum; 2^x to 2^-22, again for each of R
+#     rescalings of a key's weight on its way to the sum; each twice (numerator
+#     and denominator);
+#   sums of n terms in fp32 that truncate, of O and l: n 2^-23 each; the last
+#     product and quotient 2^-22.
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("lens,Hq,Hkv,d,wide", [
+    ([50, 64, 37], 8, 2, 128, False),                     # in clusters
+    ([50, 64, 37], 8, 2, 128, True),                      # in equal parts
+    ([60, 33], 4, 4, 64, True),
+    ([64, 3, 41], 16, 1, 128, True),                      # sixteen heads a group
+    ([64, 17], 12, 1, 64, False),
+])
+def test_decode_weights_are_finer_than_the_tensors_type(cuda_lib, lens, Hq, Hkv, d, wide, dt):
+    n, scale = max(lens), 2.0 ** -5
+    k, v, table, ln = filled(lens, Hkv, 16, d, dt, seed=41)
+    g = torch.Generator().manual_seed(42)
+    k.copy_(torch.where(k.isnan().cpu(), torch.nan, torch.randint(-2, 3, k.shape, generator=g).float()))
+    q = torch.randint(-2, 3, (len(lens), Hq, d), generator=g).to(dt).to(DEV)
+    o, _ = fa.paged_decode(q, k, v, widened(table, 1 << 15, 16) if wide else table, ln, scale=scale)
+    ok()
+    kn, vn = f64(k), f64(v)
+    ro, _, _, a = paged.decode(f64(q), kn, vn, table.cpu().numpy(), ln.cpu().numpy(), scale, 0)
+    X = 1.4427 * scale * d * 4
+    R = 8                                                 # tiles of a warp, its warps, CTAs: few keys, so few
+    e = math.log(2) * X * 2.0 ** -22 + (1 + R) * 2.0 ** -22
+    rel = 2 * U[dt] ** 2 + 2 * e + 2 * n * 2.0 ** -23 + 2.0 ** -22
+    floor = 2.0 ** -37 * n * np.nanmax(np.abs(vn)) + 2.0 ** -25 if dt == HF else 0.0
+    bound = U[dt] * np.abs(ro) + 1.01 * rel * a + floor
+    worst = (np.abs(f64(o) - ro) / bound).max()
+    assert worst <= 1, f"off by {worst} of the bound"
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_infinite_values(cuda_lib, wide, dt):
+    # An infinite v under a positive weight, be it a power of two (the largest)
+    # or any other, gives an infinite o; two of opposite sign, or a NaN, NaN.
+    k, v, table, ln = filled([70, 33], 2, 16, 64, dt, seed=43)
+    flat = lambda b, j: (table[b, j // 16].item(), slice(None), j % 16)  # noqa: E731
+    q = torch.randn((2, 4, 64), generator=torch.Generator().manual_seed(44)).to(dt).to(DEV)
+    for j in range(70):
+        v[flat(0, j)][:, j % 64] = (math.inf, -math.inf)[j // 32 % 2]      # 64 .. 69 meet 0 .. 5, of the same sign
+    v[flat(1, 5)][:, 7] = math.inf
+    v[flat(1, 6)][:, 7] = -math.inf
+    v[flat(1, 7)][:, 9] = math.nan
+    o, lse = fa.paged_decode(q, k, v, widened(table, 1 << 15, 16) if wide else table, ln)
+    ok()
+    assert bool((o[0, :, :32] == math.inf).all()) and bool((o[0, :, 32:] == -math.inf).all())
+    assert bool(o[1, :, [7, 9]].isnan().all())
+    rest = [i for i in range(64) if i not in (7, 9)]
+    assert bool(o[1, :, rest].isfinite().all()) and bool(lse.isfinite().all())
+
+
 def test_decode_pages_shared_by_sequences(cuda_lib):
     # Two sequences with a common prefix: the weights of both add up.
     k, v, table, ln = filled([200, 200], 2, 16, 64, BF, seed=12)
