@@ -221,10 +221,22 @@ __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeArgs a, int
                         max(h0 - a.Hq, 0), h1 - a.Hq, ck, ck.turned, cs, sn, x, h0 >= a.Hq);
 }
 
+// Offsets of new tokens run from 0 and upwards, to T at most.  The first blocks
+// look at all of them: a pair out of order may leave every token with a
+// sequence, but not with its own.
+__device__ __forceinline__ void check_offsets(const AppendArgs& a, const DevStatus& st) {
+  for (long long b = (long long)blockIdx.x * kThreads + threadIdx.x; b < a.B; b += (long long)gridDim.x * kThreads) {
+    const int from = a.cu[b], to = a.cu[b + 1];
+    if (from < 0 || to < from || to > a.T || (b == 0 && from != 0)) record_error(st, kErrBadIndex, kSiteAppend);
+  }
+}
+
 // Where token t goes: sequence, index in it, page and slot.  Returns false for
 // a token that is not stored: padding (past the last sequence, or a sequence
 // of length 0 in the one-token form), or an index out of range, which is
-// recorded.
+// recorded here or by check_offsets.  A token that is stored lies in its
+// sequence's range, and that in [0, T), so it is one of the sequence's last and
+// falls on no older key.
 __device__ __forceinline__ bool place_token(const AppendArgs& a, int t, const DevStatus& st, int& page, int& slot) {
   int b = t, back = 1;
   if (a.cu) {
@@ -235,7 +247,9 @@ __device__ __forceinline__ bool place_token(const AppendArgs& a, int t, const De
       if (a.cu[mid] <= t) lo = mid; else hi = mid;
     }
     b = lo;
-    back = a.cu[b + 1] - t;
+    const int from = a.cu[b], to = a.cu[b + 1];
+    if (from < 0 || from > t || to > a.T) return false;
+    back = to - t;
   } else if (a.seq_lens[b] == 0) {
     return false;
   }
@@ -282,6 +296,7 @@ __global__ void __launch_bounds__(kThreads) fa_append_kernel(const AppendArgs a,
     else load_heads(v, a.v.sh, v0, v1, ck, x);
   }
   load_pairs(a.r, pairs, st);
+  if (a.cu && blockIdx.y == 0) check_offsets(a, st);
   __syncthreads();
   int page, slot;
   if (!live || !place_token(a, (int)t, st, page, slot)) return;

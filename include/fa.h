@@ -346,7 +346,9 @@ typedef struct fa_page_table {
  *     a sequence of length 0 is padding, its token is skipped.
  *   - cu_seqlens [B + 1], from 0, non-decreasing: tokens cu[b] .. cu[b+1]-1
  *     are the last cu[b+1] - cu[b] of sequence b, in order; tokens from cu[B]
- *     on are padding and are skipped.
+ *     on are padding and are skipped.  Offsets that do not start at 0, fall, or
+ *     pass T are recorded like other bad indices; no call stores a token
+ *     outside the last cu[b+1] - cu[b] slots of a sequence.
  * rotary (may be NULL): k is stored turned, at positions [n_axes, T]
  * (batch_stride unused), and, if q [T,Hq,d] is given, q_out [T,Hq,d] is q
  * turned (may be q itself); rows of skipped tokens are left as they were.  q

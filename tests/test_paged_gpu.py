@@ -752,6 +752,61 @@ def test_append_bad_indices_are_recorded(cuda_lib, bad):
     ok()
 
 
+@pytest.mark.parametrize("cu,stored", [
+    # offsets for lengths 20, 40, 33 and 9 tokens; (sequence, index) of each token that may be stored
+    ([3, 4, 6, 9], [None, None, None, (0, 19), (1, 38), (1, 39), (2, 30), (2, 31), (2, 32)]),    # not from 0
+    ([0, -2, 6, 9], [None] * 6 + [(2, 30), (2, 31), (2, 32)]),
+    ([-5, 2, 6, 9], [None, None, (1, 36), (1, 37), (1, 38), (1, 39), (2, 30), (2, 31), (2, 32)]),
+    ([0, 2, 6, 10], [(0, 18), (0, 19), (1, 36), (1, 37), (1, 38), (1, 39), None, None, None]),   # past the tokens
+    ([0, 6, 4, 9], [(0, 14 + t) for t in range(6)] + [(2, 30), (2, 31), (2, 32)]),               # not in order
+    ([0, 2, 6, -1], [None] * 9),
+    ([1, 1, 1, 1], [None] * 9),
+])
+def test_append_bad_offsets_are_recorded_and_touch_no_other_slot(cuda_lib, cu, stored):
+    lens, T = [20, 40, 33], 9
+    kc, vc, table, ln = filled(lens, 2, 16, 64, BF, seed=25, layout="pair")
+    sc = torch.rand(kc.shape[:3], device=DEV)
+    want_k, want_v, want_s = kc.clone(), vc.clone(), sc.clone()
+    g = torch.Generator().manual_seed(26)
+    x = torch.randn((T, 8, 64), generator=g).to(BF).to(DEV)
+    q, k, v = x.split([4, 2, 2], dim=1)
+    w, axes = fa.rope_frequencies((32,), device=DEV)
+    pos = torch.zeros((1, T), dtype=torch.int32, device=DEV)          # a turn by 0 keeps every bit
+    qo = torch.full_like(q, 7.0)
+    want_q = qo.clone()
+    fa.paged_append(kc, vc, table, ln, k, v, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV), q=q, positions=pos,
+                    inv_freq=w, axes=axes, scores=sc, q_out=qo)
+    s, _ = fa.fa_last_device_status()
+    assert s == fa.FA_ERR_BAD_INDEX
+    for t, at in enumerate(stored):
+        if at is None:
+            continue
+        p, slot = table[at[0], at[1] // 16].item(), at[1] % 16
+        want_k[p, :, slot], want_v[p, :, slot], want_s[p, :, slot], want_q[t] = k[t], v[t], 0, q[t]
+    bits = lambda x: x.contiguous().view(torch.int16)  # noqa: E731
+    assert torch.equal(bits(kc), bits(want_k)) and torch.equal(bits(vc), bits(want_v))
+    assert torch.equal(sc, want_s) and torch.equal(qo, want_q)
+    ok()
+
+
+def test_append_bad_offsets_of_many_sequences_are_recorded(cuda_lib):
+    # One pair out of order among many more sequences than a block has threads,
+    # and every token finds a place in some sequence.
+    B = 3000
+    lens = [5] * B
+    kc, vc, table, ln = filled(lens, 1, 16, 64, HF, seed=27)
+    x = torch.randn((B, 1, 64), device=DEV).to(HF)
+    cu = torch.arange(B + 1, dtype=torch.int32, device=DEV)
+    fa.paged_append(kc, vc, table, ln, x, x, cu_seqlens=cu)
+    ok()
+    for at in (1, 129, 2600, B - 1):
+        bad = cu.clone()
+        bad[at] = at - 2
+        fa.paged_append(kc, vc, table, ln, x, x, cu_seqlens=bad)
+        assert fa.fa_last_device_status()[0] == fa.FA_ERR_BAD_INDEX
+    ok()
+
+
 # ---------------------------------------------------------------------------
 # Eviction
 # ---------------------------------------------------------------------------
