@@ -408,14 +408,16 @@ def _load_native():
     if os.path.exists(path):
         import importlib.util
         import torch  # noqa: F401  (its libraries, which the module needs, are then loaded)
+        from . import _build
         try:
             spec = importlib.util.spec_from_file_location("fa_torch", path)
             m = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(m)
-            m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-                lib.fa_rope, lib.fa_paged_append, lib.fa_paged_decode, lib.fa_paged_decode_workspace_bytes,
-                lib.fa_paged_evict)))
-            _native = m
+            if getattr(m, "key", None) == _build.native_key():
+                m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                    lib.fa_rope, lib.fa_paged_append, lib.fa_paged_decode, lib.fa_paged_decode_workspace_bytes,
+                    lib.fa_paged_evict)))
+                _native = m
         except ImportError:          # built against another torch
             pass
     return _native

@@ -7,16 +7,20 @@ spills) is kept next to the library as ``ptxas.txt``.
 
 ``_lib/fa_torch.so``, the native marshalling of torch tensors, is host code
 compiled beside it against the installed torch; the library does not need it,
-and where it does not compile the binding marshals in Python.  What the
-compiler said is kept as ``fa_torch.txt``.
+and where it does not compile the binding marshals in Python.  The module
+carries what it was compiled against (``native_key``): with another torch,
+Python or ``fa.h`` it is compiled again, and until then not loaded.  What the
+compiler said is kept, under the key, as ``fa_torch.txt``.
 """
 from __future__ import annotations
 
+import hashlib
 import os
 import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -53,10 +57,31 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(TORCH_LOG):
+    if not os.path.exists(LIB_PATH):
         return False
     t = os.path.getmtime(LIB_PATH)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def native_key() -> str:
+    """What fa_torch.so depends on besides its source: the installed torch and Python, and fa.h."""
+    try:
+        import torch
+        version = torch.__version__
+    except Exception:
+        version = "none"
+    with open(os.path.join(INCLUDE, "fa.h"), "rb") as f:
+        header = hashlib.sha256(f.read()).hexdigest()[:16]
+    return f"torch {version}, {sysconfig.get_config_var('SOABI')}, fa.h {header}"
+
+
+def native_up_to_date() -> bool:
+    """Whether fa_torch.txt tells of a module, or of a failure, with today's torch, Python and fa.h."""
+    try:
+        with open(TORCH_LOG) as f:
+            return f.readline().rstrip("\n") == native_key()
+    except OSError:
+        return False
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -71,13 +96,13 @@ def _compile(src: str) -> tuple[str, str]:
 def _compile_torch() -> None:
     """fa_torch.so, or the reason why not in fa_torch.txt."""
     tmp = TORCH_PATH + ".tmp"
+    key, done = native_key(), False
     try:
-        import sysconfig
-
         import torch
         where = os.path.dirname(torch.__file__)
         cuda = os.path.dirname(os.path.dirname(nvcc()))
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               f'-DFA_TORCH_KEY="{key}"',
                "-isystem", os.path.join(where, "include"), "-isystem", sysconfig.get_paths()["include"],
                "-isystem", os.path.join(cuda, "include"), "-I", INCLUDE, os.path.join(CSRC, TORCH_SOURCE), "-o", tmp,
                "-L", os.path.join(where, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
@@ -85,13 +110,14 @@ def _compile_torch() -> None:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode == 0:
             os.replace(tmp, TORCH_PATH)
-        elif os.path.exists(TORCH_PATH):
-            os.remove(TORCH_PATH)
+            done = True
         said = f"{' '.join(cmd)}\nexit {r.returncode}\n{r.stdout}{r.stderr}"
     except Exception as e:       # no torch, no compiler: Python marshals
         said = f"{type(e).__name__}: {e}\n"
+    if not done and os.path.exists(TORCH_PATH):
+        os.remove(TORCH_PATH)    # of an earlier build: not this library's
     with open(TORCH_LOG, "w") as f:
-        f.write(said)
+        f.write(f"{key}\n{said}")
 
 
 # The forward kernel splits its launch allocation between warpgroups with
@@ -125,10 +151,13 @@ def check_registers(ptxas_log: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if any source is newer than it; return its path."""
-    if not force and up_to_date():
-        return LIB_PATH
+    """Compile the library if any source is newer than it, and its marshalling
+    also for another torch; return the library's path."""
     os.makedirs(OUT_DIR, exist_ok=True)
+    if not force and up_to_date():
+        if not native_up_to_date():
+            _compile_torch()
+        return LIB_PATH
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         native = ex.submit(_compile_torch)
         results = list(ex.map(_compile, SOURCES))

@@ -347,4 +347,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "fa_torch", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_fa_torch() { return PyModule_Create(&module); }
+// FA_TORCH_KEY names the torch, Python and fa.h that this was compiled against;
+// nothing here may be called with others (see native_key in _build.py).
+PyMODINIT_FUNC PyInit_fa_torch() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "key", FA_TORCH_KEY) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -3,6 +3,7 @@
 of the C entry points, which come before any CUDA call."""
 import ctypes
 import math
+import os
 
 import numpy as np
 import pytest
@@ -347,3 +348,60 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         fa.rope(torch.zeros((1, 2, 4, 64)), None, torch.zeros((1, 1, 4), dtype=torch.int32), w, ax)
     with pytest.raises(ValueError):
         fa.rope(kc[0], None, torch.zeros((1, 1, 4), dtype=torch.int32), w, ax)
+
+
+# ---------------------------------------------------------------------------
+# The native marshalling's build
+# ---------------------------------------------------------------------------
+@pytest.fixture
+def fresh_native(lib, monkeypatch):
+    """The native marshalling as a new process finds it."""
+    pytest.importorskip("torch")
+    monkeypatch.setattr(fa, "_native", None)
+    if not fa.native_marshalling():
+        pytest.skip("not built here (see _lib/fa_torch.txt)")
+    monkeypatch.setattr(fa, "_native", None)
+
+
+@pytest.mark.parametrize("what", ["torch", "fa.h"])
+def test_native_marshalling_of_another_torch_or_header_is_not_loaded(fresh_native, monkeypatch, tmp_path, what):
+    if what == "torch":
+        import torch
+        monkeypatch.setattr(torch, "__version__", torch.__version__ + "1")
+    else:
+        text = open(os.path.join(_build.INCLUDE, "fa.h")).read()
+        (tmp_path / "fa.h").write_text(text.replace("int n_axes;", "int n_axes, more;"))
+        monkeypatch.setattr(_build, "INCLUDE", str(tmp_path))
+    assert not fa.native_marshalling()
+    assert not _build.native_up_to_date()
+
+
+def test_native_marshalling_is_compiled_again_for_another_torch(fresh_native, monkeypatch):
+    # The library's sources are as they were: only the module is built.
+    import torch
+    made = []
+    monkeypatch.setattr(_build, "_compile_torch", lambda: made.append(1))
+    monkeypatch.setattr(_build, "_compile", lambda src: pytest.fail("the library was compiled"))
+    _build.build()
+    assert not made
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + "1")
+    _build.build()
+    assert made
+
+
+@pytest.mark.parametrize("failure", ["compiler", "no compiler"])
+def test_a_failed_build_leaves_no_native_marshalling(monkeypatch, tmp_path, failure):
+    so, log = tmp_path / "fa_torch.so", tmp_path / "fa_torch.txt"
+    so.write_bytes(b"of an earlier build")
+    monkeypatch.setattr(_build, "TORCH_PATH", str(so))
+    monkeypatch.setattr(_build, "TORCH_LOG", str(log))
+
+    def run(cmd, **kw):
+        if failure == "no compiler":
+            raise FileNotFoundError("g++")
+        return _build.subprocess.CompletedProcess(cmd, 1, "", "an error")
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    _build._compile_torch()
+    assert not so.exists()
+    assert ("an error" if failure == "compiler" else "FileNotFoundError") in log.read_text()
+    assert _build.native_up_to_date()              # not tried again with the same torch, Python and header
