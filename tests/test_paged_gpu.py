@@ -473,6 +473,31 @@ def test_decode_is_reproducible_and_independent_of_the_rest_of_the_batch(cuda_li
     assert torch.equal(o1, o2) and torch.equal(l1, l2)
 
 
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_decode_alone_and_within_a_batch(cuda_lib, dt):
+    # Another batch cuts a sequence's keys elsewhere, so the sums have another
+    # order: equal within twice the bound of one of them, not bit by bit.
+    lens = [3000, 70, 1200, 0, 16, 900]
+    k, v, table, ln = filled(lens, 2, 16, 128, dt, seed=46)
+    q = torch.randn((len(lens), 8, 128), generator=torch.Generator().manual_seed(47)).to(dt).to(DEV)
+    o, lse = fa.paged_decode(q, k, v, table, ln)
+    ok()
+    assert_decoded(o, lse, q, k, v, table, ln, 128 ** -0.5, 0, what="together")
+    for b in range(len(lens)):
+        i = slice(b, b + 1)
+        o1, l1 = fa.paged_decode(q[i], k, v, table[i], ln[i])
+        ok()
+        assert_decoded(o1, l1, q[i], k, v, table[i], ln[i], 128 ** -0.5, 0, what=f"sequence {b} alone")
+        # The scores are the same ones. On either side o is rounded once, the
+        # weights are off by 2 u^2, and the sums of n terms of O and l by n 2^-23
+        # of sum p |v| <= max |v| each; rescalings, one for 16 keys or more, by
+        # 2^-22 each: less than the sums.
+        n, top = lens[b], float(torch.nan_to_num(v.float()).abs().max())
+        far = (o1.float() - o[i].float()).abs()
+        assert bool((far <= 2 * U[dt] * o[i].float().abs() + 4 * (n * 2.0 ** -23 + 2 * U[dt] ** 2) * top).all())
+        assert torch.equal(torch.isneginf(l1), torch.isneginf(lse[i]))
+
+
 def widened(table, keys, page):
     """The table with columns, far out of range, for this many keys a sequence."""
     wide = torch.full((table.shape[0], -(-keys // page)), 2 ** 30, dtype=torch.int32, device=table.device)
