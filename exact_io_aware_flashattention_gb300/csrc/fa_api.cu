@@ -918,12 +918,13 @@ DecodeWs decode_ws(int B, int Hq, int d, int page_size, int max_pages, bool with
 // than 4 tiles above an equal part, and no more than 12: lengths that differ
 // leave CTAs idle, equal parts don't.  (With scores the weights of a kv head
 // must be summed in one place, so its heads must be one unit's.  Calls on a
-// stream, 32 q and 8 kv heads, d = 128, tiles of 64 keys, us by clusters | equal
-// parts: 1 sequence of 2000 keys 7.5 | 8.9, of 4000 10.9 | 9.9; 8 of 1000 9.0 |
-// 12.7, of 2000 14.8 | 19.0; 64 of 250 18.5 | 19.5; 128 of 250 34.3 | 30.5; 8 of
-// 0-2000 12.4 | 15.9; 32 of 0-1000, 16 tiles a CTA, 18.4 | 21.3, with scores
-// 26.8 | 28.1; of 0-2000 32.4 | 29.9; 8 of 0-8000, d = 64, 16 tiles, with
-// scores, 30.9 | 26.7.)
+// stream, pages of 16, 32 q and 8 kv heads, d = 128, tiles of 64 keys, us by
+// clusters | equal parts: 1 sequence of 2000 keys 7.7 | 9.0, of 4000 11.1 | 10.1;
+// 8 of 1000 9.0 | 12.5, of 2000 15.0 | 18.9; 64 of 250 18.7 | 19.4; 128 of 250 35.8 |
+// 30.1; lengths from 0 to 2000 in equal steps, 8 sequences 11.6 | 12.7, 32 33.1 |
+// 30.3; 32 from 0 to 1000, 16 tiles a CTA, 19.1 | 21.6, with scores 23.6 | 24.2; 8
+// from 0 to 8000, d = 64, 16 tiles, with scores, 28.7 | 22.8.  128 q heads, 8 of
+// 1000 12.0 | 19.2.)
 int decode_cluster(long long units, long long tiles, int slots) {
   int c = 1;
   while (c < fa::kMaxCluster && units * c * 2 <= slots && c < tiles) c *= 2;

@@ -46,7 +46,7 @@ namespace {
 constexpr int kThreads = 512;                 // of the selection
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCached = 49 * 1024;         // keys in shared memory: 196 KB with the histograms
+constexpr int kMaxCached = 49 * 1024;         // keys in shared memory: 196 KB, 222 KB with the histograms
 constexpr uint32_t kProtected = 0xffffffffu;  // above every score's key, so taken first
 
 // Order-preserving map of scores to unsigned: larger score, larger key;

@@ -7,7 +7,8 @@
 // p_h(j).
 //
 // Bound by HBM: each K and V row is read once for all query heads of its kv
-// head, 4 d bytes per key against 4 G d operations (G = Hq / Hkv heads).
+// head where these are at most 16, 4 d bytes per key against 4 G d operations (G
+// = Hq / Hkv heads); above that once for every 16 of them.
 //
 // fa_paged_decode_kernel.  The keys of all (sequence, kv head, chunk of up to
 // 16 query heads) units, in tiles of 64 (d = 128) or 128 (d = 64), form one
@@ -29,8 +30,8 @@
 // head's maximum, sum and rescale factor sit in the lanes that hold its
 // column of S^T and O^T alike.  P^T goes from accumulator to operand layout
 // by one 8x8 transpose in registers.  At one query row per head the tensor
-// work is 1-2 % of what the copies take, so the tcgen05 path, whose 128-row
-// tiles would be filled 1/16 by a group of 8, has nothing to win here.
+// pipe is busy 13 % of the time that the copies take, so the tcgen05 path, whose
+// 128-row tiles would be filled 1/16 by a group of 8, has nothing to win here.
 //
 //   Few short units.  A cluster of up to 8 CTAs takes each unit, its CTAs equal
 // runs of the unit's tiles; what they leave stays in their shared memory, where
@@ -41,12 +42,18 @@
 //
 // Measured (calls in a row on three sets of tensors; of the 6.79 TB/s copy
 // rate), decode and finish kernels together: 8 sequences of 32768 keys, 32 q
-// and 8 kv heads, d = 128, 1074 MB: 164 us, 96 %; 64 sequences of 0 to 8192 keys,
-// 16 heads, d = 64, 1000 MB: 155 us, 95 %; 16 sequences of 0 to 8192, 236 MB: 45
+// and 8 kv heads, d = 128, 1074 MB: 164 us, 97 %; 64 sequences of 0 to 8192 keys,
+// 16 heads, d = 64, 1000 MB: 152 us, 97 %; 16 sequences of 0 to 8192, 236 MB: 45
 // us, and 51 us with scores.  About 5 us of these are the start (lengths, page
 // numbers, first tiles) and the finish kernel.  One sequence of 1000 keys, by
-// clusters: 4.8 us, 6.9 by equal parts.  From L2 alone the tiles run at 10-11 TB/s, so the SMs keep ahead of
-// HBM.
+// clusters: 5.0 us, 7.0 by equal parts.  A window of 1024 keys on the first of
+// these: 8.6 us for 34 MB.
+//   Larger groups, 8 sequences of 32768 keys, d = 128.  8 kv heads, 1074 MB: 8
+// heads each 165 us, 96 %; 16 heads each 171 us, 92 %.  One kv head, 134 MB: 16
+// heads 35.4 us; 32 heads, which read it twice, 49.7.  (9 and more heads at d =
+// 128 want more than the 168 registers that two CTAs leave a thread: the query
+// rows are loaded when their unit comes up, and the equal-parts kernel spills 64
+// bytes.)
 #include "fa_paged.h"
 #include "sm103a.cuh"
 
@@ -1075,8 +1082,13 @@ cudaError_t launch_decode(const TmaMap4& tk, const TmaMap4& tv, const DecodeArgs
                    kThreads, Cfg<D>::kBytes, 1, stream, tk, tv, a, st);
   if (e != cudaSuccess) return e;
   const int joins = (parts - 1) * (a.unit_heads / 4), adds = parts * kSplit;
-  // In one launch unless units are cut into more than about eight (2 sequences
-  // of 93735 keys, 152 parts each: 29.2 us in one, 27.2 us in two).
+  // In one launch unless units are cut into more than eight or so: it saves 1-2
+  // us, but every warp forms the LSE from all of a unit's parts, the slower the
+  // more heads a group has.  Us in one launch | in two, d = 128, by parts a unit
+  // and heads a group: 10 parts, 1 head 38.5 | 39.8, 8 heads 42.2 | 43.2, 16 heads
+  // 59.6 | 60.7; 19 parts 37.9 | 39.9, 42.4 | 43.1, 58.6 | 58.9; 38 parts 30.8 | 32.9,
+  // 35.3 | 35.3, 50.7 | 48.7; 152 parts 24.0 | 23.6, 31.1 | 24.9, 50.0 | 34.5.  (So few
+  // heads a group would take one launch up to about 100 parts.)
   if (a.scores && a.Hq / a.kv.Hkv <= a.unit_heads && parts <= 8LL * a.B * a.kv.Hkv)
     return launch_after(fa_paged_finish_kernel<T, D, true>, joins + adds, 128, 0, 1, stream, a, joins);
   if (joins > 0) e = launch_after(fa_paged_finish_kernel<T, D, false>, joins, 128, 0, 1, stream, a, joins);

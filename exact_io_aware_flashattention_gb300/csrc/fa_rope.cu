@@ -133,9 +133,9 @@ __device__ __forceinline__ void turn8(uint4& va, uint4& vb, const float (&cs)[8]
   }
 }
 
-// What one thread does to a row: the two 16-byte vectors it owns, turned, or
-// (kind kCopy) moved unchanged.  A row has rot/16 turned chunks and then
-// (d - rot)/16 chunks that pass through.
+// What one thread does to a row: the two 16-byte vectors it owns, turned or
+// moved unchanged.  A row has rot/16 turned chunks and then (d - rot)/16 chunks
+// that pass through.
 struct Chunk {
   int e0, e1;      // first elements of the two vectors
   bool turned;
@@ -186,7 +186,7 @@ __device__ __forceinline__ void do_heads(const T* in, long long in_sh, T* out, l
   }
 }
 
-// grid: x over groups of 256 / (d/16) tokens, y over groups of hpb heads of q
+// grid: x over groups of kThreads / (d/16) tokens, y over groups of hpb heads of q
 // and then k.
 template <typename T, bool kInter>
 __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeArgs a, int hpb, const DevStatus st) {
