@@ -6,8 +6,10 @@ The names ``fa_fwd``, ``fa_fwd_ex``, ``fa_fwd_ex_workspace_bytes``,
 ``fa_last_device_status``, ``fa_selftest_wait_timeout``,
 ``fa_selftest_drain_timeout``, ``fa_bwd_noalloc``, ``fa_rope``,
 ``fa_paged_append``, ``fa_paged_decode``, ``fa_paged_decode_workspace_bytes``,
-``fa_paged_evict``, ``fa_last_cuda_error`` and ``fa_version`` are
-the C entry points of ``include/fa.h`` with the same arguments (pointers as
+``fa_paged_evict``, ``fa_qk_norm_rope``, ``fa_qk_norm_rope_bwd``,
+``fa_qk_norm_rope_bwd_workspace_bytes``, ``fa_paged4_append``, ``fa_paged4_read``,
+``fa_paged4_decode``, ``fa_paged4_decode_workspace_bytes``,
+``fa_last_cuda_error`` and ``fa_version`` are the C entry points of ``include/fa.h`` with the same arguments (pointers as
 Python ints, stream as an int handle); they return the integer status.
 
 ``forward``/``backward`` marshal torch CUDA tensors into those calls: they
@@ -15,7 +17,9 @@ check dtype, shape, contiguity and device, allocate outputs with torch, pass
 ``data_ptr()`` and the current stream, and raise ``FAError`` on a non-zero
 status.  ``rope``, ``rope_backward``, ``paged_append``, ``paged_decode`` and
 ``paged_evict`` do the same for rotary positions and the paged key / value
-cache.  Every step of the computation runs in the library's kernels; there
+cache; ``qk_norm_rope``, ``qk_norm_rope_backward``, ``paged4_append``,
+``paged4_read`` and ``paged4_decode`` for the norms of queries and keys and the
+cache held in 4 bits.  Every step of the computation runs in the library's kernels; there
 is no fallback of any kind.  If the library has not been built the first call
 raises ``FAError``.
 """
@@ -83,6 +87,15 @@ class fa_page_table(ctypes.Structure):
     _fields_ = [("pages", _p), ("stride", _ll), ("max_pages", _i)]
 
 
+class fa_qk_norm(ctypes.Structure):
+    _fields_ = [("q_weight", _p), ("k_weight", _p), ("weights_fp32", _i), ("eps", _f)]
+
+
+class fa_paged4_kv(ctypes.Structure):
+    _fields_ = [("data", _p), ("page_stride", _ll), ("head_stride", _ll), ("num_pages", _i), ("page_size", _i),
+                ("Hkv", _i), ("d", _i), ("dtype", _i)]
+
+
 _SIGNATURES = {
     "fa_fwd": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f, _p], _i),
     "fa_fwd_ex": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _sz, _p], _i),
@@ -106,6 +119,13 @@ _SIGNATURES = {
     "fa_paged_decode": ([_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _f, _p, _sz, _p], _i),
     "fa_paged_decode_workspace_bytes": ([_i, _i, _i, _i, _i, _i, _i], _sz),
     "fa_paged_evict": ([_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _p], _i),
+    "fa_qk_norm_rope": ([_p] * 8 + [_i] * 6 + [_p, _p, _p], _i),
+    "fa_qk_norm_rope_bwd": ([_p] * 14 + [_i] * 6 + [_p, _p, _p, _sz, _p], _i),
+    "fa_qk_norm_rope_bwd_workspace_bytes": ([_i], _sz),
+    "fa_paged4_append": ([_p, _p, _p, _p, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p, _i, _p, _p, _p], _i),
+    "fa_paged4_read": ([_p, _p, _p, _p, _p, _p, _p, _i, _i, _p], _i),
+    "fa_paged4_decode": ([_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _f, _p, _sz, _p], _i),
+    "fa_paged4_decode_workspace_bytes": ([_i, _i, _i, _i], _sz),
 }
 
 
@@ -253,6 +273,44 @@ def fa_paged_decode_workspace_bytes(B, Hq, Hkv, d, page_size, max_pages, with_sc
 def fa_paged_evict(kv, scores, table, seq_lens, dst, new_lens, kept, B, budget, recent, sinks, stream):
     return load_library().fa_paged_evict(_ref(kv), scores, _ref(table), seq_lens, _ref(dst), new_lens, kept, B,
                                          int(budget), int(recent), int(sinks), stream)
+
+
+def fa_qk_norm_rope(q, q_strides, q_out, q_out_strides, k, k_strides, k_out, k_out_strides, B, Hq, Hk, N, d, dtype, norm,
+                    rotary, stream):
+    return load_library().fa_qk_norm_rope(q, q_strides, q_out, q_out_strides, k, k_strides, k_out, k_out_strides, B, Hq,
+                                          Hk, N, d, dtype, _ref(norm), _ref(rotary), stream)
+
+
+def fa_qk_norm_rope_bwd(dq_out, dq_out_strides, q, q_strides, dq, dq_strides, dk_out, dk_out_strides, k, k_strides, dk,
+                        dk_strides, dq_weight, dk_weight, B, Hq, Hk, N, d, dtype, norm, rotary, workspace,
+                        workspace_bytes, stream):
+    return load_library().fa_qk_norm_rope_bwd(dq_out, dq_out_strides, q, q_strides, dq, dq_strides, dk_out,
+                                              dk_out_strides, k, k_strides, dk, dk_strides, dq_weight, dk_weight, B, Hq,
+                                              Hk, N, d, dtype, _ref(norm), _ref(rotary), workspace, workspace_bytes,
+                                              stream)
+
+
+def fa_qk_norm_rope_bwd_workspace_bytes(d):
+    return load_library().fa_qk_norm_rope_bwd_workspace_bytes(d)
+
+
+def fa_paged4_append(kv, table, seq_lens, cu_seqlens, B, T, k, k_strides, v, v_strides, q, q_strides, q_out,
+                     q_out_strides, Hq, norm, rotary, stream):
+    return load_library().fa_paged4_append(_ref(kv), _ref(table), seq_lens, cu_seqlens, B, T, k, k_strides, v, v_strides,
+                                           q, q_strides, q_out, q_out_strides, Hq, _ref(norm), _ref(rotary), stream)
+
+
+def fa_paged4_read(kv, table, seq_lens, k, k_strides, v, v_strides, B, N, stream):
+    return load_library().fa_paged4_read(_ref(kv), _ref(table), seq_lens, k, k_strides, v, v_strides, B, N, stream)
+
+
+def fa_paged4_decode(q, q_strides, kv, table, seq_lens, o, lse, B, Hq, window, scale, workspace, workspace_bytes, stream):
+    return load_library().fa_paged4_decode(q, q_strides, _ref(kv), _ref(table), seq_lens, o, lse, B, Hq, int(window),
+                                           float(scale), workspace, workspace_bytes, stream)
+
+
+def fa_paged4_decode_workspace_bytes(B, Hq, Hkv, d):
+    return load_library().fa_paged4_decode_workspace_bytes(B, Hq, Hkv, d)
 
 
 # ---------------------------------------------------------------------------
@@ -804,3 +862,314 @@ def _paged_evict(k_cache, v_cache, scores, block_table, seq_lens, dst_table, bud
     if status:
         _raise(status, "fa_paged_evict")
     return new_lens, kept
+
+
+# ---------------------------------------------------------------------------
+# Norms of queries and keys, and the cache held in 4 bits
+# ---------------------------------------------------------------------------
+_pack_norm = struct.Struct("@PPif").pack                  # fa_qk_norm
+_pack_kv4 = struct.Struct("@Pqqiiiii4x").pack             # fa_paged4_kv
+
+
+def _norm(q_weight, k_weight, eps, d, dt, dev):
+    """fa_qk_norm of weights [d] (fp32 or the tensors' type, both alike; None: ones)."""
+    fp32, ptrs = 0, []
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            ptrs.append(None)
+            continue
+        if isinstance(w, _torch.Tensor) and w.dtype is _torch.float32:
+            fp32 = 1
+        ptrs.append((w, name))
+    ptrs = [0 if p is None else _check_dense(p[0], p[1], (d,), _torch.float32 if fp32 else dt, dev) for p in ptrs]
+    return _pack_norm(ptrs[0], ptrs[1], fp32, float(eps))
+
+
+def _maybe_rotary(positions, inv_freq, axes, interleaved, d, lead, dev):
+    if positions is None and inv_freq is None and axes is None:
+        return None
+    return _rotary(positions, inv_freq, axes, interleaved, d, lead, dev)
+
+
+def _rows_like(t, name, shape, dt, dev):
+    """(tensor, address, packed strides) of a given output, or of a new one."""
+    if t is None:
+        t = _torch.empty(shape, dtype=dt, device=_torch.device("cuda", dev))
+        p = t.data_ptr()
+    else:
+        p = _check_view(t, name, shape, dt, dev)
+    return t, p, struct.pack("@%dq" % (len(shape) - 1), *t.stride()[:-1])
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, positions=None, inv_freq=None, axes=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """``rope`` with the norm of each head's rows in front of it, in one pass: q
+    [B,Hq,N,d] and k [B,Hk,N,d] (k may be None) times (mean of squares + eps)^-1/2
+    times their weights [d] (fp32 or the tensors' type; None: ones), then turned
+    as by ``rope``; without ``positions``, ``inv_freq`` and ``axes`` they are normed
+    only.  Outputs may be the inputs themselves.  Returns (q_out, k_out), or q_out
+    without k.  See fa_qk_norm_rope."""
+    return _qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, axes, eps, interleaved, q_out, k_out, stream)
+
+
+def _qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, axes, eps, interleaved, q_out, k_out, stream):
+    (B, Hq, N, d), dev, code, dt = _first(q, "q", 4, "[B, Hq, N, d]")
+    qp = _check_view(q, "q", q.shape, dt, dev)
+    Hk, kp, ks = 0, None, None
+    if k is not None:
+        Hk = k.shape[1] if isinstance(k, _torch.Tensor) and k.dim() == 4 else 0
+        kp = _check_view(k, "k", (B, Hk, N, d), dt, dev)
+        ks = _pack3(*k.stride()[:3])
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out or k_weight without k")
+    norm = _norm(q_weight, k_weight, eps, d, dt, dev)
+    rot = _maybe_rotary(positions, inv_freq, axes, interleaved, d, (B, N), dev)
+    handle = _raw_stream(dev, stream)
+    if handle is None:
+        with _on(dev, stream):
+            return _qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, axes, eps, interleaved, q_out, k_out, None)
+    q_out, op, os_ = _rows_like(q_out, "q_out", (B, Hq, N, d), dt, dev)
+    okp, oks = None, None
+    if k is not None:
+        k_out, okp, oks = _rows_like(k_out, "k_out", (B, Hk, N, d), dt, dev)
+    status = fa_qk_norm_rope(qp, _pack3(*q.stride()[:3]), op, os_, kp, ks, okp, oks, B, Hq, Hk, N, d, code, norm, rot, handle)
+    if status:
+        _raise(status, "fa_qk_norm_rope")
+    return q_out if k is None else (q_out, k_out)
+
+
+def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions=None, inv_freq=None, axes=None, eps: float = 1e-6,
+                          interleaved: bool = False, dq_out=None, dk_out=None, dq_weight=None, dk_weight=None,
+                          workspace=None, stream=None):
+    """Gradients of ``qk_norm_rope``'s inputs q and k and of its weights from those
+    of its outputs, dq and dk.  Returns (dq, dk, dq_weight, dk_weight), or (dq,
+    dq_weight) without k (dk None too); the weights' gradients are fp32 [d], None
+    for weights that are None.  ``dq_out`` and ``dk_out`` may be dq and dk
+    themselves.  See fa_qk_norm_rope_bwd."""
+    return _qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, axes, eps, interleaved, dq_out,
+                                  dk_out, dq_weight, dk_weight, workspace, stream)
+
+
+def qk_norm_rope_backward_workspace(d, device="cuda"):
+    """Workspace of qk_norm_rope_backward, for callers that keep one (one for each call that may run at the same time)."""
+    import torch
+    n = fa_qk_norm_rope_bwd_workspace_bytes(d)
+    if n == 0:
+        raise FAError(FA_ERR_UNSUPPORTED_HEADDIM, "fa_qk_norm_rope_bwd_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, axes, eps, interleaved, dq_out, dk_out,
+                           dq_weight, dk_weight, workspace, stream):
+    (B, Hq, N, d), dev, code, dt = _first(q, "q", 4, "[B, Hq, N, d]")
+    qp = _check_view(q, "q", q.shape, dt, dev)
+    dqp = _check_view(dq, "dq", (B, Hq, N, d), dt, dev)
+    Hk, kp, ks, dkp, dks = 0, None, None, None, None
+    if k is not None:
+        Hk = k.shape[1] if isinstance(k, _torch.Tensor) and k.dim() == 4 else 0
+        kp = _check_view(k, "k", (B, Hk, N, d), dt, dev)
+        dkp = _check_view(dk, "dk", (B, Hk, N, d), dt, dev)
+        ks, dks = _pack3(*k.stride()[:3]), _pack3(*dk.stride()[:3])
+    elif not (dk is None and k_weight is None and dk_out is None and dk_weight is None):
+        raise ValueError("dk, k_weight, dk_out or dk_weight without k")
+    for w, dw, name in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
+        if w is None and dw is not None:
+            raise ValueError(f"{name} without its weights")
+    norm = _norm(q_weight, k_weight, eps, d, dt, dev)
+    rot = _maybe_rotary(positions, inv_freq, axes, interleaved, d, (B, N), dev)
+    handle = _raw_stream(dev, stream)
+    if handle is None:
+        with _on(dev, stream):
+            return _qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, axes, eps, interleaved,
+                                          dq_out, dk_out, dq_weight, dk_weight, workspace, None)
+    dq_out, op, os_ = _rows_like(dq_out, "dq_out", (B, Hq, N, d), dt, dev)
+    okp, oks = None, None
+    if k is not None:
+        dk_out, okp, oks = _rows_like(dk_out, "dk_out", (B, Hk, N, d), dt, dev)
+    grads = []
+    for w, dw, name in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
+        if w is None:
+            grads += [None, None]
+        elif dw is None:
+            dw = _torch.empty((d,), dtype=_torch.float32, device=q.device)
+            grads += [dw, dw.data_ptr()]
+        else:
+            grads += [dw, _check_dense(dw, name, (d,), _torch.float32, dev)]
+    wp, n = None, 0
+    if grads[1] or grads[3]:
+        if workspace is None:
+            workspace = qk_norm_rope_backward_workspace(d, q.device)
+        n = workspace.numel()
+        wp = _check_dense(workspace, "workspace", (n,), _torch.uint8, dev)
+    status = fa_qk_norm_rope_bwd(dqp, _pack3(*dq.stride()[:3]), qp, _pack3(*q.stride()[:3]), op, os_, dkp, dks, kp, ks, okp,
+                                 oks, grads[1], grads[3], B, Hq, Hk, N, d, code, norm, rot, wp, n, handle)
+    if status:
+        _raise(status, "fa_qk_norm_rope_bwd")
+    return (dq_out, grads[0]) if k is None else (dq_out, dk_out, grads[0], grads[2])
+
+
+def paged4_cache(pages, Hkv, page_size, d, device="cuda"):
+    """A pool for ``paged4_append``: uint8 [pages, Hkv, page_size, d + d/8], K and V in 4 bits.
+    Its contents are the library's; whole pages may be copied."""
+    import torch
+    if d not in (64, 128):
+        raise FAError(FA_ERR_UNSUPPORTED_HEADDIM, "paged4_cache")
+    if page_size < 16 or page_size > 65536 or page_size % 16:
+        raise FAError(FA_ERR_BAD_SHAPE, "paged4_cache")
+    return torch.empty((pages, Hkv, page_size, d + d // 8), dtype=torch.uint8, device=device)
+
+
+def _paged4(cache, block_table, seq_lens, dtype):
+    """Checked cache tensors: (Hkv, d, device index, fa_paged4_kv, fa_page_table, B, seq_lens address)."""
+    if _torch is None:
+        _load_torch()
+    if not isinstance(cache, _torch.Tensor):
+        raise TypeError("cache must be a torch.Tensor")
+    if cache.dim() != 4 or cache.shape[3] not in (72, 144):
+        raise ValueError(f"cache must be a [pages, Hkv, page_size, d + d/8] tensor with d 64 or 128, got shape "
+                         f"{tuple(cache.shape)}")
+    code = {_torch.bfloat16: FA_BF16, _torch.float16: FA_FP16}.get(dtype)
+    if code is None:
+        raise TypeError(f"the cache's values must be torch.bfloat16 or torch.float16, got {dtype}")
+    dev = cache.get_device()
+    if not cache.is_cuda:
+        raise ValueError(f"cache must be a CUDA tensor, got {cache.device}")
+    p = _check_view(cache, "cache", cache.shape, _torch.uint8, dev)
+    (P, Hkv, ps, row), st = cache.shape, cache.stride()
+    if ps > 1 and st[2] != row:
+        raise ValueError("cache must be contiguous in its last two dimensions")
+    d = row // 9 * 8
+    table, B = _table(block_table, "block_table", dev)
+    return (Hkv, d, dev, _pack_kv4(p, st[0], st[1], P, ps, Hkv, d, code), table, B,
+            _check_dense(seq_lens, "seq_lens", (B,), _torch.int32, dev))
+
+
+def paged4_append(cache, block_table, seq_lens, k, v, cu_seqlens=None, q=None, q_weight=None, k_weight=None,
+                  eps: float | None = None, positions=None, inv_freq=None, axes=None, interleaved: bool = False, q_out=None,
+                  stream=None):
+    """``paged_append`` into a cache of ``paged4_cache``: k, v [T,Hkv,d] are stored in 4
+    bits.  With ``eps`` k, and q [T,Hq,d] if given, are normed first (weights as in
+    ``qk_norm_rope``); with ``positions`` [n_axes,T], ``inv_freq`` and ``axes`` they are
+    then turned.  Returns q so (into ``q_out``, which may be q), or None without q.
+    A cache's calls must all have the same type.  See fa_paged4_append."""
+    return _paged4_append(cache, block_table, seq_lens, k, v, cu_seqlens, q, q_weight, k_weight, eps, positions, inv_freq,
+                          axes, interleaved, q_out, stream)
+
+
+def _paged4_append(cache, block_table, seq_lens, k, v, cu_seqlens, q, q_weight, k_weight, eps, positions, inv_freq, axes,
+                   interleaved, q_out, stream):
+    if _torch is None:
+        _load_torch()
+    if not isinstance(k, _torch.Tensor):
+        raise TypeError("k must be a torch.Tensor")
+    dt = k.dtype
+    Hkv, d, dev, kv, table, B, lens = _paged4(cache, block_table, seq_lens, dt)
+    T = k.shape[0] if k.dim() == 3 else 0
+    kp = _check_view(k, "k", (T, Hkv, d), dt, dev)
+    vp = _check_view(v, "v", (T, Hkv, d), dt, dev)
+    if cu_seqlens is None:
+        cu = None
+        if T != B:
+            raise ValueError(f"{T} tokens for {B} sequences without cu_seqlens")
+    else:
+        cu = _check_dense(cu_seqlens, "cu_seqlens", (B + 1,), _torch.int32, dev)
+    norm = None
+    if eps is not None:
+        norm = _norm(q_weight, k_weight, eps, d, dt, dev)
+    elif q_weight is not None or k_weight is not None:
+        raise ValueError("weights of a norm without eps")
+    rot = _maybe_rotary(positions, inv_freq, axes, interleaved, d, (T,), dev)
+    qp, qs, Hq = None, None, 0
+    if q is not None:
+        if norm is None and rot is None:
+            raise ValueError("q without a norm or a rotation")
+        Hq = q.shape[1] if isinstance(q, _torch.Tensor) and q.dim() == 3 else 0
+        qp = _check_view(q, "q", (T, Hq, d), dt, dev)
+        qs = _pack2(*q.stride()[:2])
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    handle = _raw_stream(dev, stream)
+    if handle is None:
+        with _on(dev, stream):
+            return _paged4_append(cache, block_table, seq_lens, k, v, cu_seqlens, q, q_weight, k_weight, eps, positions,
+                                  inv_freq, axes, interleaved, q_out, None)
+    op, os_ = None, None
+    if q is not None:
+        q_out, op, os_ = _rows_like(q_out, "q_out", (T, Hq, d), dt, dev)
+    if T:
+        status = fa_paged4_append(kv, table, lens, cu, B, T, kp, _pack2(*k.stride()[:2]), vp, _pack2(*v.stride()[:2]), qp,
+                                  qs, op, os_, Hq, norm, rot, handle)
+        if status:
+            _raise(status, "fa_paged4_append")
+    return q_out
+
+
+def paged4_read(cache, block_table, seq_lens, n: int, dtype, k_out=None, v_out=None, stream=None):
+    """The last n keys of each sequence of a 4-bit cache as k, v [B,Hkv,n,d] of
+    ``dtype``, the type it was appended in; row i is key seq_lens[b] - n + i, zero
+    where that is negative.  With one sequence's whole length they are what
+    ``forward_ex`` takes for its next queries.  See fa_paged4_read."""
+    return _paged4_read(cache, block_table, seq_lens, n, dtype, k_out, v_out, stream)
+
+
+def _paged4_read(cache, block_table, seq_lens, n, dtype, k_out, v_out, stream):
+    Hkv, d, dev, kv, table, B, lens = _paged4(cache, block_table, seq_lens, dtype)
+    if n < 1:
+        raise ValueError("n must be at least 1")
+    handle = _raw_stream(dev, stream)
+    if handle is None:
+        with _on(dev, stream):
+            return _paged4_read(cache, block_table, seq_lens, n, dtype, k_out, v_out, None)
+    k_out, kp, ks = _rows_like(k_out, "k_out", (B, Hkv, n, d), dtype, dev)
+    v_out, vp, vs = _rows_like(v_out, "v_out", (B, Hkv, n, d), dtype, dev)
+    status = fa_paged4_read(kv, table, lens, kp, ks, vp, vs, B, n, handle)
+    if status:
+        _raise(status, "fa_paged4_read")
+    return k_out, v_out
+
+
+_decode4_ws_bytes = functools.lru_cache(maxsize=256)(
+    lambda *shape: fa_paged4_decode_workspace_bytes(*shape))
+
+
+def paged4_decode_workspace(B, Hq, cache):
+    """Workspace of paged4_decode, for callers that keep one (one for each call that may run at the same time)."""
+    import torch
+    n = _decode4_ws_bytes(B, Hq, cache.shape[1], cache.shape[3] // 9 * 8)
+    if n == 0:
+        raise FAError(FA_ERR_BAD_SHAPE, "fa_paged4_decode_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def paged4_decode(q, cache, block_table, seq_lens, scale: float | None = None, window: int = 0, out=None, lse=None,
+                  workspace=None, stream=None):
+    """O [B,Hq,d], LSE [B,Hq] of one query row per sequence, q [B,Hq,d], against the
+    seq_lens[b] keys of a 4-bit cache (the last ``window`` of them if window > 0),
+    as the values that it holds.  See fa_paged4_decode."""
+    return _paged4_decode(q, cache, block_table, seq_lens, scale, window, out, lse, workspace, stream)
+
+
+def _paged4_decode(q, cache, block_table, seq_lens, scale, window, out, lse, workspace, stream):
+    (B, Hq, _), _, _, dt = _first(q, "q", 3, "[B, Hq, d]")
+    Hkv, d, dev, kv, table, rows, lens = _paged4(cache, block_table, seq_lens, dt)
+    qp = _check_view(q, "q", (rows, Hq, d), dt, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    handle = _raw_stream(dev, stream)
+    if handle is None:
+        with _on(dev, stream):
+            return _paged4_decode(q, cache, block_table, seq_lens, scale, window, out, lse, workspace, None)
+    if out is None:
+        out = _torch.empty((B, Hq, d), dtype=dt, device=cache.device)
+    op = _check_dense(out, "out", (B, Hq, d), dt, dev)
+    if lse is None:
+        lse = _torch.empty((B, Hq), dtype=_torch.float32, device=cache.device)
+    lp = _check_dense(lse, "lse", (B, Hq), _torch.float32, dev)
+    if workspace is None:
+        workspace = paged4_decode_workspace(B, Hq, cache)
+    n = workspace.numel()
+    wp = _check_dense(workspace, "workspace", (n,), _torch.uint8, dev)
+    status = fa_paged4_decode(qp, _pack2(*q.stride()[:2]), kv, table, lens, op, lp, B, Hq, window, scale, wp, n, handle)
+    if status:
+        _raise(status, "fa_paged4_decode")
+    return out, lse

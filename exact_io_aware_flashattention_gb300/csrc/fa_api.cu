@@ -17,6 +17,7 @@
 
 #include "fa_internal.h"
 #include "fa_paged.h"
+#include "fa_paged4.h"
 
 namespace {
 
@@ -95,6 +96,7 @@ constexpr int kMaxDevices = 64;
 struct DeviceState {
   bool ready = false;
   std::atomic<bool> paged_ready{false};   // the paged-cache and rotary kernels too
+  std::atomic<bool> paged4_ready{false};  // and those of the norms and the 4-bit cache
   bool unusable = false;   // a kernel's drain gave up: no further launches on this device
   int num_sms = 0;
   int* status = nullptr;
@@ -1186,6 +1188,332 @@ fa_status fa_paged_evict(const fa_paged_kv* kv, float* scores, const fa_page_tab
   a.recent = recent;
   a.sinks = sinks;
   return launch_status(fa::launch_paged_evict(a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Norms with rotary positions, and the 4-bit cache
+// ---------------------------------------------------------------------------
+namespace {
+
+fa_status check_norm(const fa_qk_norm* n) {
+  if ((n->weights_fp32 != 0 && n->weights_fp32 != 1) || !(n->eps >= 0.f) || std::isinf(n->eps)) return FA_ERR_BAD_ARGUMENT;
+  const size_t by = n->weights_fp32 ? 4 : 16;
+  if (!aligned(n->q_weight, by) || !aligned(n->k_weight, by)) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+fa::NormArgs norm_args(const fa_qk_norm* n) {
+  return n ? fa::NormArgs{n->q_weight, n->k_weight, n->weights_fp32, 1, n->eps} : fa::NormArgs{};
+}
+
+// What a call reads by element: the rotation's arrays and the norm's weights.
+struct Tables {
+  View v[8];
+  int n = 0;
+  void add(const View& x) { v[n++] = x; }
+  void rotary(const fa_rotary* r, int B, int N) {
+    if (!r) return;
+    add(view(r->positions, N, 4, {{r->n_axes, r->axis_stride}, {B, r->batch_stride}}));
+    add(bytes_view(r->inv_freq, (size_t)r->rot / 2 * 8));
+    add(bytes_view(r->axes, (size_t)r->rot / 2 * 4));
+  }
+  void norm(const fa_qk_norm* n_, int d) {
+    if (!n_) return;
+    const size_t bytes = (size_t)d * (n_->weights_fp32 ? 4 : 2);
+    if (n_->q_weight) add(bytes_view(n_->q_weight, bytes));
+    if (n_->k_weight) add(bytes_view(n_->k_weight, bytes));
+  }
+  bool apart_from(const View& out) const {
+    for (int i = 0; i < n; ++i)
+      if (!apart(out, v[i])) return false;
+    return true;
+  }
+};
+
+fa_status check_rows(int B, int Hq, int Hk, int N, int d, int dtype) {
+  if (B < 1 || Hq < 1 || Hk < 0 || N < 1 || (long long)B * N >= (1LL << 31) || (long long)Hq + Hk > 65535)
+    return FA_ERR_BAD_SHAPE;
+  if (d < 16 || d > 256 || d % 16) return FA_ERR_UNSUPPORTED_HEADDIM;
+  return check_dtype(dtype);
+}
+
+// [B,H,N,d] rows of a call.
+fa_status rows_of(const void* p, const long long* s, int B, int H, int N, int d, fa::RowView& r, View& v) {
+  FA_TRY(check_strides({{B, s[0]}, {H, s[1]}, {N, s[2]}}));
+  if (!aligned16(p)) return FA_ERR_MISALIGNED;
+  r = fa::RowView{const_cast<void*>(p), stride_of(B, s[0]), stride_of(H, s[1]), stride_of(N, s[2])};
+  v = view(p, d, 2, {{B, s[0]}, {H, s[1]}, {N, s[2]}});
+  return FA_OK;
+}
+
+View kv4_view(const fa_paged4_kv* kv) {
+  return view(kv->data, (long long)kv->page_size * (kv->d + kv->d / 8), 1,
+              {{kv->num_pages, kv->page_stride}, {kv->Hkv, kv->head_stride}});
+}
+
+fa_status check_kv4(const fa_paged4_kv* kv) {
+  if (!kv || !kv->data) return FA_ERR_NULL_PTR;
+  FA_TRY(check_dtype(kv->dtype));
+  if (kv->num_pages < 1 || kv->Hkv < 1 || kv->page_size < 16 || kv->page_size > 65536 || kv->page_size % 16)
+    return FA_ERR_BAD_SHAPE;
+  if (kv->d != 64 && kv->d != 128) return FA_ERR_UNSUPPORTED_HEADDIM;
+  for (const auto& d : {std::pair<long long, long long>{kv->num_pages, kv->page_stride}, {kv->Hkv, kv->head_stride}})
+    if (d.first > 1) {
+      if (d.second < 0 || d.second > kMaxSpan / d.first) return FA_ERR_BAD_ARGUMENT;
+      if (d.second % 16) return FA_ERR_MISALIGNED;
+    }
+  if (!aligned16(kv->data)) return FA_ERR_MISALIGNED;
+  return kv4_view(kv).distinct() ? FA_OK : FA_ERR_BAD_ARGUMENT;
+}
+
+fa::PagedKv kv4_args(const fa_paged4_kv* kv) {
+  return fa::PagedKv{kv->data,
+                     kv->data,
+                     stride_of(kv->num_pages, kv->page_stride),
+                     stride_of(kv->Hkv, kv->head_stride),
+                     0,
+                     kv->num_pages,
+                     kv->page_size,
+                     kv->Hkv,
+                     kv->d};
+}
+
+// As paged_device_state, for the kernels of this section.
+fa_status paged4_device_state(DeviceState** out) {
+  FA_TRY(device_state(out));
+  if ((*out)->paged4_ready) return FA_OK;
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!(*out)->paged4_ready) {
+    const cudaError_t e = fa::configure_paged4_kernels();
+    if (e != cudaSuccess) return launch_status(e);
+    (*out)->paged4_ready = true;
+  }
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_qk_norm_rope(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+                          const void* k, const long long* k_strides, void* k_out, const long long* k_out_strides, int B,
+                          int Hq, int Hk, int N, int d, int dtype, const fa_qk_norm* norm, const fa_rotary* rotary,
+                          void* stream) {
+  NvtxRange nv("fa_qk_norm_rope");
+  if (!q || !q_strides || !q_out || !q_out_strides || !norm) return FA_ERR_NULL_PTR;
+  if (Hk != 0 && (!k || !k_strides || !k_out || !k_out_strides)) return FA_ERR_NULL_PTR;
+  if (Hk == 0 && (k || k_out)) return FA_ERR_BAD_SHAPE;
+  FA_TRY(check_rows(B, Hq, Hk, N, d, dtype));
+  FA_TRY(check_norm(norm));
+  if (rotary) FA_TRY(check_rotary(rotary, d));
+  fa::RowView rows[4] = {};
+  View views[4];
+  FA_TRY(rows_of(q, q_strides, B, Hq, N, d, rows[0], views[0]));
+  FA_TRY(rows_of(q_out, q_out_strides, B, Hq, N, d, rows[1], views[1]));
+  if (Hk) {
+    FA_TRY(rows_of(k, k_strides, B, Hk, N, d, rows[2], views[2]));
+    FA_TRY(rows_of(k_out, k_out_strides, B, Hk, N, d, rows[3], views[3]));
+  }
+  Tables tables;
+  tables.rotary(rotary, B, N);
+  tables.norm(norm, d);
+  const int n = Hk ? 4 : 2;
+  for (int i = 1; i < n; i += 2) {
+    if (!views[i].distinct() || !tables.apart_from(views[i])) return FA_ERR_ALIASING;
+    for (int j = 0; j < n; ++j)
+      if (j != i && !(j == i - 1 && in_place(rows[i], rows[j])) && !apart(views[i], views[j])) return FA_ERR_ALIASING;
+  }
+  DeviceState* ds = nullptr;
+  FA_TRY(paged4_device_state(&ds));
+  const fa::NormRopeArgs a{rows[0], rows[1], rows[2], rows[3], B, Hq, Hk, N, d,
+                           rotary ? rotary_args(rotary, 0) : fa::RotaryArgs{}, norm_args(norm)};
+  return launch_status(fa::launch_norm_rope(dtype, a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int d) {
+  return d < 16 || d > 256 || d % 16 ? 0 : (size_t)fa::kNormBwdMaxBlocks * d * 4;
+}
+
+fa_status fa_qk_norm_rope_bwd(const void* dq_out, const long long* dq_out_strides, const void* q, const long long* q_strides,
+                              void* dq, const long long* dq_strides, const void* dk_out, const long long* dk_out_strides,
+                              const void* k, const long long* k_strides, void* dk, const long long* dk_strides,
+                              float* dq_weight, float* dk_weight, int B, int Hq, int Hk, int N, int d, int dtype,
+                              const fa_qk_norm* norm, const fa_rotary* rotary, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  NvtxRange nv("fa_qk_norm_rope_bwd");
+  if (!dq_out || !dq_out_strides || !q || !q_strides || !dq || !dq_strides || !norm) return FA_ERR_NULL_PTR;
+  if (Hk != 0 && (!dk_out || !dk_out_strides || !k || !k_strides || !dk || !dk_strides)) return FA_ERR_NULL_PTR;
+  if (Hk == 0 && (dk_out || k || dk || dk_weight)) return FA_ERR_BAD_SHAPE;
+  FA_TRY(check_rows(B, Hq, Hk, N, d, dtype));
+  FA_TRY(check_norm(norm));
+  if (rotary) FA_TRY(check_rotary(rotary, d));
+  const bool weights = dq_weight || dk_weight;
+  if (weights && !workspace) return FA_ERR_NULL_PTR;
+  if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4) || !aligned16(workspace)) return FA_ERR_MISALIGNED;
+  const size_t need = fa_qk_norm_rope_bwd_workspace_bytes(d);
+  if (weights && workspace_bytes < need) return FA_ERR_WORKSPACE_TOO_SMALL;
+  fa::NormRopeBwdArgs a{};
+  View in[4], out[5];
+  FA_TRY(rows_of(dq_out, dq_out_strides, B, Hq, N, d, a.dy[0], in[0]));
+  FA_TRY(rows_of(q, q_strides, B, Hq, N, d, a.x[0], in[1]));
+  FA_TRY(rows_of(dq, dq_strides, B, Hq, N, d, a.dx[0], out[0]));
+  if (Hk) {
+    FA_TRY(rows_of(dk_out, dk_out_strides, B, Hk, N, d, a.dy[1], in[2]));
+    FA_TRY(rows_of(k, k_strides, B, Hk, N, d, a.x[1], in[3]));
+    FA_TRY(rows_of(dk, dk_strides, B, Hk, N, d, a.dx[1], out[1]));
+  }
+  Tables tables;
+  tables.rotary(rotary, B, N);
+  tables.norm(norm, d);
+  const int ni = Hk ? 4 : 2;
+  int no = Hk ? 2 : 1;
+  const int rows = no;
+  if (dq_weight) out[no++] = bytes_view(dq_weight, (size_t)d * 4);
+  if (dk_weight) out[no++] = bytes_view(dk_weight, (size_t)d * 4);
+  if (weights) out[no++] = bytes_view(workspace, need);
+  for (int i = 0; i < no; ++i) {
+    if (!out[i].distinct() || !tables.apart_from(out[i])) return FA_ERR_ALIASING;
+    for (int j = 0; j < ni; ++j)
+      if (!(i < rows && j == 2 * i && in_place(a.dx[i], a.dy[i])) && !apart(out[i], in[j])) return FA_ERR_ALIASING;
+    for (int j = 0; j < i; ++j)
+      if (!apart(out[i], out[j])) return FA_ERR_ALIASING;
+  }
+  DeviceState* ds = nullptr;
+  FA_TRY(paged4_device_state(&ds));
+  a.H[0] = Hq;
+  a.H[1] = Hk;
+  a.B = B;
+  a.N = N;
+  a.d = d;
+  if (rotary) a.r = rotary_args(rotary, 1);
+  a.n = norm_args(norm);
+  a.dw[0] = dq_weight;
+  a.dw[1] = dk_weight;
+  a.part = static_cast<float*>(workspace);
+  return launch_status(fa::launch_norm_rope_bwd(dtype, a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_paged4_append(const fa_paged4_kv* kv, const fa_page_table* table, const int* seq_lens, const int* cu_seqlens,
+                           int B, int T, const void* k, const long long* k_strides, const void* v,
+                           const long long* v_strides, const void* q, const long long* q_strides, void* q_out,
+                           const long long* q_out_strides, int Hq, const fa_qk_norm* norm, const fa_rotary* rotary,
+                           void* stream) {
+  NvtxRange nv("fa_paged4_append");
+  FA_TRY(check_kv4(kv));
+  if (!seq_lens || !k_strides || !v_strides || (T != 0 && (!k || !v))) return FA_ERR_NULL_PTR;
+  if (B < 1 || T < 0 || (!cu_seqlens && T != B)) return FA_ERR_BAD_SHAPE;
+  FA_TRY(check_table(table, B, kv->page_size));
+  if (!aligned(seq_lens, 4) || !aligned(cu_seqlens, 4)) return FA_ERR_MISALIGNED;
+  if (q && !rotary && !norm) return FA_ERR_BAD_ARGUMENT;
+  if (q ? (!q_out || !q_strides || !q_out_strides) : q_out != nullptr) return FA_ERR_NULL_PTR;
+  if (q ? Hq < 1 : Hq != 0) return FA_ERR_BAD_SHAPE;
+  if ((long long)Hq + 2LL * kv->Hkv > 65535) return FA_ERR_BAD_SHAPE;
+  if (rotary) FA_TRY(check_rotary(rotary, kv->d));
+  if (norm) FA_TRY(check_norm(norm));
+  if (T == 0) return FA_OK;
+  fa::Append4Args a{};
+  View in[3], out[2] = {kv4_view(kv)};
+  const long long ks[3] = {0, k_strides[1], k_strides[0]}, vs[3] = {0, v_strides[1], v_strides[0]};
+  FA_TRY(rows_of(k, ks, 1, kv->Hkv, T, kv->d, a.k, in[0]));
+  FA_TRY(rows_of(v, vs, 1, kv->Hkv, T, kv->d, a.v, in[1]));
+  if (q) {
+    const long long qs[3] = {0, q_strides[1], q_strides[0]}, os[3] = {0, q_out_strides[1], q_out_strides[0]};
+    FA_TRY(rows_of(q, qs, 1, Hq, T, kv->d, a.q, in[2]));
+    FA_TRY(rows_of(q_out, os, 1, Hq, T, kv->d, a.q_out, out[1]));
+  }
+  Tables tables;
+  tables.add(table_view(table, B));
+  tables.add(bytes_view(seq_lens, (size_t)B * 4));
+  if (cu_seqlens) tables.add(bytes_view(cu_seqlens, (size_t)(B + 1) * 4));
+  tables.rotary(rotary, 1, T);
+  tables.norm(norm, kv->d);
+  for (int i = 0; i < (q ? 2 : 1); ++i) {
+    if (!out[i].distinct() || !tables.apart_from(out[i])) return FA_ERR_ALIASING;
+    for (int j = 0; j < (q ? 3 : 2); ++j)
+      if (!(i == 1 && j == 2 && in_place(a.q_out, a.q)) && !apart(out[i], in[j])) return FA_ERR_ALIASING;
+  }
+  if (q && !apart(out[0], out[1])) return FA_ERR_ALIASING;
+  DeviceState* ds = nullptr;
+  FA_TRY(paged4_device_state(&ds));
+  a.kv = kv4_args(kv);
+  a.table = table_args(table);
+  a.seq_lens = seq_lens;
+  a.cu = cu_seqlens;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  if (rotary) a.r = rotary_args(rotary, 0);
+  a.n = norm_args(norm);
+  return launch_status(fa::launch_append4(kv->dtype, a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_paged4_read(const fa_paged4_kv* kv, const fa_page_table* table, const int* seq_lens, void* k,
+                         const long long* k_strides, void* v, const long long* v_strides, int B, int N, void* stream) {
+  NvtxRange nv("fa_paged4_read");
+  FA_TRY(check_kv4(kv));
+  if (!seq_lens || !k || !k_strides || !v || !v_strides) return FA_ERR_NULL_PTR;
+  if (B < 1 || N < 1 || N > (1 << 30)) return FA_ERR_BAD_SHAPE;
+  FA_TRY(check_table(table, B, kv->page_size));
+  if (!aligned(seq_lens, 4)) return FA_ERR_MISALIGNED;
+  fa::Read4Args a{};
+  View out[2];
+  FA_TRY(rows_of(k, k_strides, B, kv->Hkv, N, kv->d, a.k, out[0]));
+  FA_TRY(rows_of(v, v_strides, B, kv->Hkv, N, kv->d, a.v, out[1]));
+  const View in[] = {kv4_view(kv), table_view(table, B), bytes_view(seq_lens, (size_t)B * 4)};
+  if (!out[0].distinct() || !out[1].distinct() || !outputs_apart(out, in)) return FA_ERR_ALIASING;
+  DeviceState* ds = nullptr;
+  FA_TRY(paged4_device_state(&ds));
+  a.kv = kv4_args(kv);
+  a.table = table_args(table);
+  a.seq_lens = seq_lens;
+  a.B = B;
+  a.N = N;
+  return launch_status(fa::launch_read4(kv->dtype, a, dev_status(ds), ds->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_paged4_decode_workspace_bytes(int B, int Hq, int Hkv, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (d != 64 && d != 128) || (long long)B * Hq >= (1LL << 31)) return 0;
+  return decode_ws(B, Hq, d, 16, 1, false).total;
+}
+
+fa_status fa_paged4_decode(const void* q, const long long* q_strides, const fa_paged4_kv* kv, const fa_page_table* table,
+                           const int* seq_lens, void* o, float* lse, int B, int Hq, int window, float scale,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nv("fa_paged4_decode");
+  FA_TRY(check_kv4(kv));
+  if (!q || !q_strides || !seq_lens || !o || !lse || !workspace) return FA_ERR_NULL_PTR;
+  if (B < 1 || Hq < 1 || Hq % kv->Hkv || (long long)B * Hq >= (1LL << 31)) return FA_ERR_BAD_SHAPE;
+  FA_TRY(check_table(table, B, kv->page_size));
+  FA_TRY(check_scale(0, scale));
+  if (window < 0) return FA_ERR_BAD_ARGUMENT;
+  FA_TRY(check_strides({{B, q_strides[0]}, {Hq, q_strides[1]}}));
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(workspace) || !aligned(seq_lens, 4))
+    return FA_ERR_MISALIGNED;
+  const size_t need = fa_paged4_decode_workspace_bytes(B, Hq, kv->Hkv, kv->d);
+  if (workspace_bytes < need) return FA_ERR_WORKSPACE_TOO_SMALL;
+  const View ins[] = {view(q, kv->d, 2, {{B, q_strides[0]}, {Hq, q_strides[1]}}), kv4_view(kv), table_view(table, B),
+                      bytes_view(seq_lens, (size_t)B * 4)};
+  const View outs[] = {bytes_view(o, (size_t)B * Hq * kv->d * 2), bytes_view(lse, (size_t)B * Hq * 4),
+                       bytes_view(workspace, need)};
+  if (!outputs_apart(outs, ins)) return FA_ERR_ALIASING;
+  DeviceState* ds = nullptr;
+  FA_TRY(paged4_device_state(&ds));
+  fa::DecodeArgs a{};
+  a.q = q;
+  a.q_sb = stride_of(B, q_strides[0]);
+  a.q_sh = stride_of(Hq, q_strides[1]);
+  a.kv = kv4_args(kv);
+  a.table = table_args(table);
+  a.seq_lens = seq_lens;
+  a.o = o;
+  a.lse = lse;
+  a.B = B;
+  a.Hq = Hq;
+  a.window = window;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return launch_status(fa::launch_decode4(kv->dtype, a, dev_status(ds), 0, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,100 @@
+// Internal launcher interface of the normed rotary positions (fa_qknorm.cu) and
+// of the cache held in 4 bits (fa_append4.cu, fa_decode4.cu), between the C-ABI
+// layer (fa_api.cu) and the kernels.  Nothing here is exported.
+#pragma once
+
+#include "fa_paged.h"
+
+namespace fa {
+
+enum : int { kSiteReadLen = 50, kSiteReadPage = 51, kSiteDecode4Len = 52, kSiteDecode4Page = 53 };
+
+// Norm of each head's rows: x (mean x^2 + eps)^-1/2 w.
+struct NormArgs {
+  const void* wq;            // [d] each, fp32 or the call's type; NULL: ones
+  const void* wk;
+  int fp32;
+  int on;                    // 0: no norm
+  float eps;
+};
+
+struct NormRopeArgs {
+  RowView q, q_out, k, k_out;
+  int B, Hq, Hk, N, d;
+  RotaryArgs r;              // rot = 0: nothing is turned
+  NormArgs n;
+};
+
+struct NormRopeBwdArgs {
+  RowView dy[2], x[2], dx[2];   // q, k
+  int H[2];
+  int B, N, d;
+  RotaryArgs r;              // inverse
+  NormArgs n;
+  float* dw[2];              // [d], NULL: not wanted
+  float* part;               // [blocks][d], the blocks of q and then those of k
+  int blocks[2];
+};
+
+// Blocks of the backward kernel at most (its workspace has a row for each).
+constexpr int kNormBwdMaxBlocks = 2048;
+
+cudaError_t launch_norm_rope(int dtype, const NormRopeArgs& a, const DevStatus& st, int num_sms, cudaStream_t stream);
+cudaError_t launch_norm_rope_bwd(int dtype, NormRopeBwdArgs a, const DevStatus& st, int num_sms, cudaStream_t stream);
+
+// The 4-bit cache.  16 slots of a page and kv head form a record of 18 d bytes:
+// K codes [16][d/2], V codes [16][d/2], then (s, z) of K and of V, [16][d/64]
+// pairs of the call's type each.  A page's records follow one another.
+//   A row's codes are d/8 words of eight elements each, element e of a word in
+// bits 16 (e % 2) + 4 (e / 2) on: two neighbours lie in the same place of the
+// word's halves, where one mask makes a pair of matrix operands of them.  At d
+// = 128 word i of both groups stand side by side, at 8-byte chunk i ^ 4 ((slot /
+// 2) % 2): the lanes of a warp that read 8 bytes of four rows each, or 16 bytes
+// of eight rows, then meet all banks of shared memory alike.
+template <int D>
+struct Record {
+  static constexpr int kRow = D / 2;                 // bytes of a row's codes
+  static constexpr int kV = 16 * kRow, kKp = 32 * kRow, kPar = D / 64 * 4, kVp = kKp + 16 * kPar;
+  static constexpr int kBytes = kVp + 16 * kPar;
+  static_assert(kBytes == 18 * D, "record");
+  // Byte of word i of a slot's row.
+  static __host__ __device__ constexpr int word(int slot, int i) {
+    return slot * kRow + (D == 128 ? (((i & 7) ^ ((slot & 2) << 1)) << 3) + ((i >> 3) << 2) : i << 2);
+  }
+};
+
+struct Append4Args {
+  RowView q, q_out, k, v;    // tokens as N (sb unused); q.p NULL: no q
+  PagedKv kv;                // k: the records; strides in bytes
+  PageTable table;
+  const int* seq_lens;
+  const int* cu;             // [B + 1] or NULL
+  int B, T, Hq;
+  RotaryArgs r;              // rot = 0: nothing is turned
+  NormArgs n;
+};
+
+struct Read4Args {
+  PagedKv kv;
+  PageTable table;
+  const int* seq_lens;
+  RowView k, v;
+  int B, N;
+};
+
+cudaError_t launch_append4(int dtype, const Append4Args& a, const DevStatus& st, int num_sms, cudaStream_t stream);
+cudaError_t launch_read4(int dtype, const Read4Args& a, const DevStatus& st, int num_sms, cudaStream_t stream);
+cudaError_t launch_decode4(int dtype, const DecodeArgs& a, const DevStatus& st, int parts, cudaStream_t stream);
+
+cudaError_t configure_norm_kernels();
+cudaError_t configure_append4_kernels();
+cudaError_t configure_decode4_kernels();
+
+inline cudaError_t configure_paged4_kernels() {
+  cudaError_t e = configure_norm_kernels();
+  if (e == cudaSuccess) e = configure_append4_kernels();
+  if (e == cudaSuccess) e = configure_decode4_kernels();
+  return e;
+}
+
+}  // namespace fa

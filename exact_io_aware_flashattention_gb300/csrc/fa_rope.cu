@@ -32,9 +32,8 @@
 // 30.9 us, 86 % (90 registers leave 20 warps an SM); one token for each of 64
 // sequences: 3.7 us, of which the launch is most.
 #include "fa_paged.h"
+#include "fa_rotary.cuh"
 #include "sm103a.cuh"
-
-#include <cuda_fp16.h>
 
 namespace fa {
 
@@ -42,117 +41,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kUnroll = 4;   // heads whose loads are in flight per thread
-
-template <typename T>
-struct Pair2;
-template <>
-struct Pair2<__nv_bfloat16> {
-  static __device__ __forceinline__ float2 up(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  }
-  static __device__ __forceinline__ uint32_t down(float lo, float hi) { return cvt_bf16x2(lo, hi); }
-};
-template <>
-struct Pair2<__half> {
-  static __device__ __forceinline__ float2 up(uint32_t w) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-  }
-  static __device__ __forceinline__ uint32_t down(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-};
-
-// inv_freq / (2 pi) modulo 1, in units of 2^-64 turns.  inv_freq = M 2^(e-63)
-// with M its mantissa in the top bits of a word, 1 / (2 pi) = C 2^-66, so the
-// result is the 128-bit product M C shifted by e - 65.
-__device__ __forceinline__ uint64_t turns64(double w) {
-  const uint64_t bits = (uint64_t)__double_as_longlong(w);
-  const int ex = (int)((bits >> 52) & 0x7ff);
-  if (ex == 0 || ex == 0x7ff) return 0;                     // zero (or not a finite frequency)
-  const uint64_t M = (1ull << 63) | ((bits & 0xfffffffffffffull) << 11);
-  const uint64_t C = 0xA2F9836E4E44152Aull;                 // 2^66 / (2 pi)
-  const uint64_t hi = __umul64hi(M, C), lo = M * C;
-  const int s = ex - 1023 - 1;                              // hi:lo shifted left by s, the upper word
-  uint64_t F;
-  if (s >= 64) F = 0;
-  else if (s > 0) F = (hi << s) | (lo >> (64 - s));
-  else F = s > -64 ? hi >> -s : 0;
-  return (bits >> 63) ? 0 - F : F;
-}
-
-// What a block keeps of the rotation: each pair's F and axis.
-struct Pairs {
-  uint64_t turns[128];
-  int axis[128];
-};
-__device__ __forceinline__ void load_pairs(const RotaryArgs& r, Pairs& p, const DevStatus& st) {
-  for (int i = threadIdx.x; i < r.rot / 2; i += kThreads) {
-    int ax = r.axes[i];
-    if (ax < 0 || ax >= r.n_axes) {
-      record_error(st, kErrBadIndex, kSiteAxis);
-      ax = 0;
-    }
-    p.axis[i] = ax;
-    p.turns[i] = turns64(r.inv_freq[i]);
-  }
-}
-
-// Cosines and sines of the pairs 8c .. 8c+7 of the token whose positions
-// start at pos.
-__device__ __forceinline__ void load_angles(const RotaryArgs& r, const Pairs& p, const int* pos, int c, float (&cs)[8],
-                                            float (&sn)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint64_t phase = (uint64_t)(int64_t)pos[p.axis[c * 8 + i] * r.pos_axis] * p.turns[c * 8 + i];
-    const float angle = (float)(int32_t)(uint32_t)(phase >> 32) * 1.4629180792671596e-9f;   // 2 pi / 2^32
-    cs[i] = __cosf(angle);
-    sn[i] = __sinf(r.inverse ? -angle : angle);
-  }
-}
-
-// Eight pairs: elements of a at i, of b at i (halves) or adjacent (interleaved).
-template <typename T, bool kInter>
-__device__ __forceinline__ void turn8(uint4& va, uint4& vb, const float (&cs)[8], const float (&sn)[8]) {
-  uint32_t* a = reinterpret_cast<uint32_t*>(&va);
-  uint32_t* b = reinterpret_cast<uint32_t*>(&vb);
-  if constexpr (kInter) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t& w = i < 4 ? a[i] : b[i - 4];
-      const float2 x = Pair2<T>::up(w);
-      w = Pair2<T>::down(x.x * cs[i] - x.y * sn[i], x.y * cs[i] + x.x * sn[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = Pair2<T>::up(a[i]), y = Pair2<T>::up(b[i]);
-      a[i] = Pair2<T>::down(x.x * cs[2 * i] - y.x * sn[2 * i], x.y * cs[2 * i + 1] - y.y * sn[2 * i + 1]);
-      b[i] = Pair2<T>::down(y.x * cs[2 * i] + x.x * sn[2 * i], y.y * cs[2 * i + 1] + x.y * sn[2 * i + 1]);
-    }
-  }
-}
-
-// What one thread does to a row: the two 16-byte vectors it owns, turned or
-// moved unchanged.  A row has rot/16 turned chunks and then (d - rot)/16 chunks
-// that pass through.
-struct Chunk {
-  int e0, e1;      // first elements of the two vectors
-  bool turned;
-};
-template <bool kInter>
-__device__ __forceinline__ Chunk chunk_of(int c, int rot) {
-  Chunk k;
-  k.turned = c < rot / 16;
-  if (k.turned && !kInter) {
-    k.e0 = 8 * c;
-    k.e1 = rot / 2 + 8 * c;
-  } else {
-    k.e0 = 16 * c;
-    k.e1 = 16 * c + 8;
-  }
-  return k;
-}
 
 // The next heads of [h, h1) of one token, in + h * in_sh.
 struct Batch {
@@ -208,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeArgs a, int
     if (h0 < a.Hq) load_heads(q, a.q.sh, h0, min(h1, a.Hq), ck, x);
     else load_heads(k, a.k.sh, h0 - a.Hq, h1 - a.Hq, ck, x);
   }
-  load_pairs(a.r, pairs, st);
+  load_pairs<kThreads>(a.r, pairs, st);
   __syncthreads();
   if (!live) return;
   float cs[8] = {}, sn[8] = {};
@@ -219,53 +107,6 @@ __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeArgs a, int
   if (h1 > a.Hq)
     do_heads<T, kInter>(k, a.k.sh, static_cast<T*>(a.k_out.p) + b * a.k_out.sb + n * a.k_out.sn, a.k_out.sh,
                         max(h0 - a.Hq, 0), h1 - a.Hq, ck, ck.turned, cs, sn, x, h0 >= a.Hq);
-}
-
-// Offsets of new tokens run from 0 and upwards, to T at most.  The first blocks
-// look at all of them: a pair out of order may leave every token with a
-// sequence, but not with its own.
-__device__ __forceinline__ void check_offsets(const AppendArgs& a, const DevStatus& st) {
-  for (long long b = (long long)blockIdx.x * kThreads + threadIdx.x; b < a.B; b += (long long)gridDim.x * kThreads) {
-    const int from = a.cu[b], to = a.cu[b + 1];
-    if (from < 0 || to < from || to > a.T || (b == 0 && from != 0)) record_error(st, kErrBadIndex, kSiteAppend);
-  }
-}
-
-// Where token t goes: sequence, index in it, page and slot.  Returns false for
-// a token that is not stored: padding (past the last sequence, or a sequence
-// of length 0 in the one-token form), or an index out of range, which is
-// recorded here or by check_offsets.  A token that is stored lies in its
-// sequence's range, and that in [0, T), so it is one of the sequence's last and
-// falls on no older key.
-__device__ __forceinline__ bool place_token(const AppendArgs& a, int t, const DevStatus& st, int& page, int& slot) {
-  int b = t, back = 1;
-  if (a.cu) {
-    if (t >= a.cu[a.B]) return false;
-    int lo = 0, hi = a.B;                  // last b with cu[b] <= t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu[mid] <= t) lo = mid; else hi = mid;
-    }
-    b = lo;
-    const int from = a.cu[b], to = a.cu[b + 1];
-    if (from < 0 || from > t || to > a.T) return false;
-    back = to - t;
-  } else if (a.seq_lens[b] == 0) {
-    return false;
-  }
-  const long long i = (long long)a.seq_lens[b] - back;
-  if (back < 1 || i < 0 || i >= (long long)a.table.cols * a.kv.page_size) {
-    record_error(st, kErrBadIndex, kSiteAppend);
-    return false;
-  }
-  const int col = (int)i / a.kv.page_size;
-  page = a.table.pages[b * a.table.stride + col];
-  slot = (int)i - col * a.kv.page_size;
-  if (page < 0 || page >= a.kv.num_pages) {
-    record_error(st, kErrBadIndex, kSiteAppend);
-    return false;
-  }
-  return true;
 }
 
 // As fa_rope_kernel over tokens, with the heads of q, then k, then v; k and v
@@ -295,8 +136,8 @@ __global__ void __launch_bounds__(kThreads) fa_append_kernel(const AppendArgs a,
     else if (first == 1) load_heads(k, a.k.sh, k0, k1, ck, x);
     else load_heads(v, a.v.sh, v0, v1, ck, x);
   }
-  load_pairs(a.r, pairs, st);
-  if (a.cu && blockIdx.y == 0) check_offsets(a, st);
+  load_pairs<kThreads>(a.r, pairs, st);
+  if (a.cu && blockIdx.y == 0) check_offsets<kThreads>(a, st);
   __syncthreads();
   int page, slot;
   if (!live || !place_token(a, (int)t, st, page, slot)) return;

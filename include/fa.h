@@ -407,6 +407,117 @@ fa_status fa_paged_evict(const fa_paged_kv* kv, float* scores, const fa_page_tab
                          const fa_page_table* dst, int* new_lens, int* kept, int B, int budget, int recent, int sinks,
                          void* stream);
 
+/* ------------------------------------------------------------------------
+ * Norms of queries and keys, with the rotary positions in the same pass.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * The norm of a row x of d elements: x (mean x^2 + eps)^-1/2 w.  Weights [d]
+ * of q's heads and of k's: fp32 (weights_fp32 = 1, element-aligned) or the
+ * call's dtype (weights_fp32 = 0, 16-byte aligned); NULL: all ones.  eps is
+ * finite and not negative.
+ */
+typedef struct fa_qk_norm {
+  const void* q_weight;
+  const void* k_weight;
+  int weights_fp32;
+  float eps;
+} fa_qk_norm;
+
+/*
+ * fa_rope with the norm in front of it: q_out = turned(norm(q)), k_out likewise,
+ * in one pass; statistics and products are fp32, an output is rounded once.
+ * rotary = NULL: the norm alone.  Layouts, limits and in-place use as fa_rope.
+ * One launch.
+ */
+fa_status fa_qk_norm_rope(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+                          const void* k, const long long* k_strides, void* k_out, const long long* k_out_strides, int B,
+                          int Hq, int Hk, int N, int d, int dtype, const fa_qk_norm* norm, const fa_rotary* rotary,
+                          void* stream);
+
+/*
+ * Its gradient.  dq_out and dk_out are the gradients of fa_qk_norm_rope's
+ * outputs, q and k its inputs; writes dq and dk, those of the inputs, and
+ * dq_weight and dk_weight fp32 [d], those of the weights, summed over batches,
+ * heads and tokens (either may be NULL: not wanted).  dq may be dq_out, and dk
+ * dk_out, itself (same pointer and strides).  k, dk_out, dk and dk_weight are
+ * NULL with Hk = 0.  rotary as in the forward: the kernel turns back.
+ * workspace: at least fa_qk_norm_rope_bwd_workspace_bytes(d), contents don't
+ * matter; calls that may run at the same time need one each; NULL if neither
+ * weight's gradient is wanted.  All outputs are bitwise reproducible.  One
+ * launch, and one more for the weights.
+ */
+fa_status fa_qk_norm_rope_bwd(const void* dq_out, const long long* dq_out_strides, const void* q, const long long* q_strides,
+                              void* dq, const long long* dq_strides, const void* dk_out, const long long* dk_out_strides,
+                              const void* k, const long long* k_strides, void* dk, const long long* dk_strides,
+                              float* dq_weight, float* dk_weight, int B, int Hq, int Hk, int N, int d, int dtype,
+                              const fa_qk_norm* norm, const fa_rotary* rotary, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Workspace of fa_qk_norm_rope_bwd; 0 for an invalid d. */
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int d);
+
+/* ------------------------------------------------------------------------
+ * The paged cache held in 4 bits.
+ *
+ * A cached row of d elements (d is 64 or 128) is held in groups of 64: with x
+ * the 16-bit value of dtype T that a 16-bit cache would hold,
+ *   z = the group's smallest,  s = T((largest - z) / 15),
+ *   c = (x - z) / s rounded to nearest (ties to even) in 0 .. 15, 0 where s = 0,
+ * and it stands for z + s c.  x is off by s / 2 at most, and by 15 roundings of
+ * s.  A group with a value that is not finite reads as NaN throughout; one whose
+ * largest value is within 1/16 of T's may read as infinite there.
+ *
+ * The pool holds num_pages pages of page_size slots (a multiple of 16, at most
+ * 65536) for each kv head; page p of head g starts p * page_stride + g *
+ * head_stride BYTES from data, both multiples of 16, and takes page_size * (d +
+ * d / 8) contiguous bytes.  What these hold is the library's own: whole pages
+ * may be copied or moved to other pools of the same page_size, d and dtype.
+ * Everything said of the 16-bit cache above about tables, lengths, offsets,
+ * bad indices and graphs holds here too.
+ * ---------------------------------------------------------------------- */
+typedef struct fa_paged4_kv {
+  void* data;
+  long long page_stride, head_stride;
+  int num_pages, page_size, Hkv, d, dtype;
+} fa_paged4_kv;
+
+/*
+ * fa_paged_append into the 4-bit cache.  With norm (may be NULL) q and k are
+ * normed, with rotary (may be NULL) turned after that, and rounded to dtype; k
+ * and v are then stored.  q needs norm or rotary (FA_ERR_BAD_ARGUMENT without).
+ * One launch.
+ */
+fa_status fa_paged4_append(const fa_paged4_kv* kv, const fa_page_table* table, const int* seq_lens, const int* cu_seqlens,
+                           int B, int T, const void* k, const long long* k_strides, const void* v,
+                           const long long* v_strides, const void* q, const long long* q_strides, void* q_out,
+                           const long long* q_out_strides, int Hq, const fa_qk_norm* norm, const fa_rotary* rotary,
+                           void* stream);
+
+/*
+ * The last N keys of each sequence as 16-bit rows: k and v [B,Hkv,N,d]
+ * (strides: batch, head, token) of dtype get the values that the cache holds,
+ * rounded to it; row n is key seq_lens[b] - N + n, and zero where that is
+ * negative.  So one sequence's keys are what fa_fwd_ex takes for the queries of
+ * its next tokens.  One launch.
+ */
+fa_status fa_paged4_read(const fa_paged4_kv* kv, const fa_page_table* table, const int* seq_lens, void* k,
+                         const long long* k_strides, void* v, const long long* v_strides, int B, int N, void* stream);
+
+/*
+ * fa_paged_decode over the 4-bit cache (without scores): q, o and lse as there;
+ * scores, softmax and sums are fp32.  workspace: at least
+ * fa_paged4_decode_workspace_bytes(...), contents don't matter; calls that may
+ * run at the same time need one each.  O and LSE are bitwise reproducible.  One
+ * or two launches.
+ */
+fa_status fa_paged4_decode(const void* q, const long long* q_strides, const fa_paged4_kv* kv, const fa_page_table* table,
+                           const int* seq_lens, void* o, float* lse, int B, int Hq, int window, float scale,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of fa_paged4_decode; 0 for invalid shapes. */
+size_t fa_paged4_decode_workspace_bytes(int B, int Hq, int Hkv, int d);
+
 /*
  * Text of the most recent CUDA runtime error behind an FA_ERR_LAUNCH or
  * FA_ERR_CUDA status returned on the calling thread ("no error" if none).
