@@ -2,96 +2,680 @@
 //   o_h = sum_j p_h(j) v_j,  p_h(j) = exp(scale q_h . k_j - lse_h),
 // where k_j and v_j are the values z + s c that the cached codes stand for.
 //
-// One block per (sequence, query head), a warp every fourth key, each with its
-// own running maximum and sum; lane l owns D/32 elements.
+// Every code enters the matrix products as it is: the four bits become the
+// mantissa of 1 + c / 16, exact in bf16 and fp16, by a shift and one logic
+// instruction for a pair, and s and z are applied in fp32 outside,
+//   q . k_j = sum over groups g of 16 s_jg (sum_i q_i (1 + c_ji / 16) - Q_g) + z_jg Q_g,
+// Q_g the sum of q over the group (-Q_g is what the accumulators start from), and
+//   o = sum_j (16 s_j p_j) (1 + c_j / 16) + sum_j p_j (z_j - 16 s_j),
+// the second sum one number a head and group.  So nothing is rounded to 16 bits
+// but the weights 16 s p, which enter as the sum of two bf16 values (off by 2^-16
+// of themselves).
+//
+// The line of tiles, its cut into equal parts, one a CTA, and their joins are
+// those of the 16-bit kernel (fa_decode.cuh, fa_paged.cu); a warp's slice of a tile
+// is one record of 16 keys, which one untiled copy fetches.  Warp 8 is the
+// producer, warps 0-7 own a slice of each tile each.  Products by mma.sync
+// (m16n8k16) with keys, then elements of d as rows and 8 heads as columns: see
+// fa_paged.cu.  Row i of a slice's S^T is the key (i % 8) / 2 + 4 (i % 2) + 8 (i / 8),
+// so that the lanes that read the pairs of keys of V from shared memory, four
+// keys a lane, meet all banks; O^T's rows are the elements 8 r + 2 n + h of a group
+// (lane row r, tile n, row half h).
+//   A running maximum that is behind by less than 2^8 is as good as the exact
+// one (weights up to 2^8, sums in fp32): the warp then neither exchanges maxima
+// nor rescales.
+#include "fa_decode.cuh"
 #include "fa_paged4.h"
-#include "fa_rotary.cuh"
 #include "sm103a.cuh"
+
+#include <cuda_fp16.h>
 
 namespace fa {
 
 namespace {
 
+constexpr int kWarps = 8;                          // consumers, one 16-key slice of a tile each
+constexpr int kConsumerThreads = kWarps * 32;
+constexpr int kThreads = kConsumerThreads + 32;
+constexpr int kKeys = 16 * kWarps;
+
+enum : int { kSiteFull = 54, kSiteEmpty = 55, kDrainFull = 56 };
+
+template <int D>
+struct Cfg {
+  static constexpr uint32_t kSlice = Record<D>::kBytes, kStage = kWarps * kSlice;
+  static constexpr int kStages = D == 128 ? 4 : 8;             // 74 KB in flight
+  static constexpr uint32_t kBuf = kStages * kStage;           // [8 warps][8 heads][D] fp32, one head group
+  static constexpr uint32_t kMl = kBuf + kWarps * 8u * D * 4u; // [8 warps][16 heads] (max, sum)
+  static constexpr uint32_t kBar = kMl + kWarps * 16u * 8u;
+  static constexpr uint32_t kBytes = kBar + 256u;
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];
+  int mask[8];               // slices of the stage's tile that were loaded
+  int abort;
+  int scan[kThreads / 32];
+  int b0;                    // first sequence of this CTA's part
+  long long before;          // tiles (per unit column) of the sequences before it
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+template <typename T>
+struct Type;
+template <>
+struct Type<__nv_bfloat16> {
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return cvt_bf16x2(lo, hi); }
+  static __device__ __forceinline__ float2 up(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  // 1 + c / 16 for code n of both halves of w.
+  template <int n>
+  static __device__ __forceinline__ uint32_t code(uint32_t w) {
+    return ((n == 0 ? w << 3 : w >> (n == 0 ? 0 : 4 * n - 3)) & 0x00780078u) | 0x3f803f80u;
+  }
+};
+template <>
+struct Type<__half> {
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 up(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+  template <int n>
+  static __device__ __forceinline__ uint32_t code(uint32_t w) {
+    return ((n < 2 ? w << (n < 2 ? 6 - 4 * n : 0) : w >> (n < 2 ? 0 : 4 * n - 6)) & 0x03c003c0u) | 0x3c003c00u;
+  }
+};
+using Bf = Type<__nv_bfloat16>;
+
+template <typename T_, int D_>
+struct Traits {
+  using T = T_;
+  static constexpr int D = D_, kKeys = 16 * kWarps, kJoinThreads = kConsumerThreads;
+  static constexpr float kShift = 0.f;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return Type<T>::pack(lo, hi); }
+};
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumerThreads) : "memory"); }
+
+// Two weights as the sum of two bf16 values each: hi their upper halves.
+__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  hi = __byte_perm(a, b, 0x7632);
+  lo = cvt_bf16x2(x - __uint_as_float(a & 0xffff0000u), y - __uint_as_float(b & 0xffff0000u));
+}
+
+// The (s, z) pairs of one row, D / 64 of them.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) fa_decode4_kernel(const DecodeArgs a, const DevStatus st) {
-  constexpr int kE = D / 32;
-  __shared__ float so[4][D], sm[4], sl[4];
+__device__ __forceinline__ void load_pars(const uint8_t* p, float2 (&x)[D / 64]) {
+  if constexpr (D == 128) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    x[0] = Type<T>::up(w.x);
+    x[1] = Type<T>::up(w.y);
+  } else {
+    x[0] = Type<T>::up(*reinterpret_cast<const uint32_t*>(p));
+  }
+}
+
+// Query rows of unit (b, col) as B operands, column = head lane / 4: q[n][g][w] the
+// eight elements 64 g + 16 (lane % 4) + 8 w on; and nq, the negative sums over the
+// groups for the heads 2 (lane % 4) and the next, this lane's columns of S^T.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int col, int chunks, uint4 (&q)[NT][D / 64][2],
+                                       float (&nq)[NT][D / 64][2]) {
+  const int lane = threadIdx.x & 31, G = a.Hq / a.kv.Hkv;
+  const int g = col / chunks, h0 = g * G + (col - g * chunks) * 8 * NT + (lane >> 2), h1 = (g + 1) * G;
+  const T* p = static_cast<const T*>(a.q) + b * a.q_sb + (lane & 3) * 16;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const bool in = h0 + n * 8 < h1;
+    const T* x = p + (in ? h0 + n * 8 : h1 - 1) * a.q_sh;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        q[n][k][w] = in ? *reinterpret_cast<const uint4*>(x + k * 64 + w * 8) : make_uint4(0, 0, 0, 0);
+        const uint32_t e[4] = {q[n][k][w].x, q[n][k][w].y, q[n][k][w].z, q[n][k][w].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = Type<T>::up(e[i]);
+          s += y.x + y.y;
+        }
+      }
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      nq[n][k][0] = -__shfl_sync(0xffffffffu, s, (lane & 3) * 8);
+      nq[n][k][1] = -__shfl_sync(0xffffffffu, s, (lane & 3) * 8 + 4);
+    }
+  }
+}
+
+template <typename T, int n>
+__device__ __forceinline__ void score_step(float (&c)[4], uint32_t wa, uint32_t wb, uint32_t b0, uint32_t b1) {
+  const uint32_t x[4] = {Type<T>::template code<n>(wa), Type<T>::template code<n>(wb), Type<T>::template code<n + 1>(wa),
+                         Type<T>::template code<n + 1>(wb)};
+  Type<T>::mma(c, x, b0, b1);
+}
+
+constexpr float kNone = -1e30f;      // below every score: the maximum before the first key
+
+template <typename T, int D, int NT, bool kCluster>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(const DecodeArgs a, const DevStatus st) {
+  using C = Cfg<D>;
+  using Tr = Traits<T, D>;
+  constexpr int kG = D / 64;
+  extern __shared__ __align__(128) uint8_t smem[];
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kBar);
+  volatile int* abort_flag = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], kWarps);
+    }
+    bars->abort = 0;
+    mbar_fence_init();
+  }
+  wait_for_previous();
+  const int G = a.Hq / a.kv.Hkv, chunks = (G + 8 * NT - 1) / (8 * NT), cols = a.kv.Hkv * chunks;
+  Walk<kKeys> w;
+  long long total = 0, t0 = 0, t1 = 0;            // the line's tiles, and this CTA's part of them
+  int parts = 0, rank = 0;
+  if constexpr (kCluster) {
+    // The cluster's unit, and this CTA's share of its tiles (perhaps none).
+    const int unit = blockIdx.x / a.cluster;
+    rank = blockIdx.x - unit * a.cluster;
+    w.b = unit / cols;
+    w.col = unit - w.b * cols;
+    w.s = span_of<kKeys>(a, w.b);
+    w.tile = w.s.n * rank / a.cluster;
+    w.left = w.s.n * (rank + 1) / a.cluster - w.tile;
+    if (w.s.len < 0 && w.col == 0 && rank == 0 && threadIdx.x == 0) record_error(st, kErrBadIndex, kSiteDecode4Len);
+    __syncthreads();
+  } else {
+    // The line: its length, and this CTA's first sequence.  Round 0 finds the
+    // total; round 1, for batches of more than one block's worth, walks again
+    // to find the start (one block's worth is still there).
+    const int first_len = (int)threadIdx.x < a.B ? a.seq_lens[threadIdx.x] : 0;
+    for (int round = 0; round < 2; ++round) {
+      long long before = 0, start = 0;
+      for (int base = 0; base < a.B; base += kThreads) {
+        const int b = base + threadIdx.x;
+        Span s{};
+        if (b < a.B) {
+          s = span_of_len<kKeys>(a, base == 0 ? first_len : a.seq_lens[b]);
+          if (s.len < 0 && round == 0 && blockIdx.x == 0) record_error(st, kErrBadIndex, kSiteDecode4Len);
+        }
+        int x = s.n;
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, d);
+          if (lane >= d) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) bars->scan[warp] = x;
+        __syncthreads();
+        long long pre = before + x - s.n;
+        for (int i = 0; i < kThreads / 32; ++i) {
+          if (i < warp) pre += bars->scan[i];
+          before += bars->scan[i];
+        }
+        const bool last = base + kThreads >= a.B;
+        if (round == 0 && last) total = before * cols;
+        const int all = (int)min(total, (long long)gridDim.x);
+        if ((last || round == 1) && blockIdx.x < all) start = part_start(total, blockIdx.x, all);
+        if ((round == 1 || a.B <= kThreads) && s.n > 0 && pre * cols <= start && start < (pre + s.n) * cols) {
+          bars->b0 = b;
+          bars->before = pre * cols;
+        }
+      }
+      if (a.B <= kThreads) break;
+    }
+    __syncthreads();
+    parts = (int)min(total, (long long)gridDim.x);
+    if ((int)blockIdx.x >= parts) {
+      if (threadIdx.x == 0) a.parts[blockIdx.x].left = 0;
+      if (warp == kWarps) fill_empty<Tr>(a);
+      return;
+    }
+    t0 = part_start(total, blockIdx.x, parts);
+    t1 = part_start(total, blockIdx.x + 1, parts);
+    w.left = t1 - t0;
+    w.b = bars->b0;
+    w.s = span_of<kKeys>(a, w.b);
+    const long long in = t0 - bars->before;
+    w.col = (int)(in / w.s.n);
+    w.tile = (int)(in - (long long)w.col * w.s.n);
+  }
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    // Lane l looks up slice l % 8 of tile l / 8 of the unit's next four tiles, one
+    // run ahead of the copies; lanes 0-7 issue a slice's copy each.
+    constexpr int kAhead = 32 / kWarps;
+    const int my_slice = lane % kWarps, my_tile = lane / kWarps;
+    auto look_up = [&](const Walk<kKeys>& x, int& page, int& slot) {
+      const int have = (int)min((long long)min(x.s.n - x.tile, kAhead), x.left);
+      const int key0 = (x.s.tile0 + x.tile + my_tile) * kKeys + my_slice * 16;
+      page = 0;
+      slot = -1;                       // not visible: not copied
+      if (my_tile < have && key0 < x.s.len && key0 + 16 > x.s.first) {
+        const int c = key0 / a.kv.page_size;
+        slot = key0 - c * a.kv.page_size;
+        page = a.table.pages[x.b * a.table.stride + c];
+      }
+      return have;
+    };
+    DecodePart part{};
+    part.b = w.b;
+    part.col = w.col;
+    part.tile = w.tile;
+    part.left = (int)w.left;
+    const int first_n = w.s.n;
+    int it = 0, page, slot, have = look_up(w, page, slot);
+    bool good = true;
+    while (good && w.left > 0) {
+      Walk<kKeys> x = w;
+      x.left -= have;
+      x.tile += have;
+      if (x.tile == x.s.n && x.left > 0) x.next_unit(a, cols);
+      int page_next = page, slot_next = slot, have_next = have;
+      if (x.left > 0 && !(x.b == w.b && x.tile == w.tile && x.left >= have)) have_next = look_up(x, page_next, slot_next);
+      if (slot >= 0 && (page < 0 || page >= a.kv.num_pages)) {
+        record_error(st, kErrBadIndex, kSiteDecode4Page);
+        slot = -1;
+      }
+      const uint8_t* base = static_cast<const uint8_t*>(a.kv.k) + (w.col / chunks) * a.kv.s_head;
+      for (int i = 0; i < have; ++i, ++it) {
+        const int s = it % C::kStages, r = it / C::kStages;
+        if (r > 0 && !mbar_wait_warp(&bars->empty[s], (r - 1) & 1, st, abort_flag, kSiteEmpty)) {
+          good = false;
+          break;
+        }
+        const int p = __shfl_sync(0xffffffffu, page, i * kWarps + my_slice);
+        const int sl = __shfl_sync(0xffffffffu, slot, i * kWarps + my_slice);
+        const uint32_t mask = __ballot_sync(0xffffffffu, sl >= 0) & ((1u << kWarps) - 1);
+        if (lane == 0) {
+          bars->mask[s] = mask;
+          mbar_arrive_expect_tx(&bars->full[s], __popc(mask) * C::kSlice);
+        }
+        __syncwarp();
+        if (lane < kWarps && sl >= 0)
+          bulk_load(smem_u32(smem) + s * C::kStage + lane * C::kSlice,
+                    base + p * a.kv.s_page + (long long)(sl >> 4) * C::kSlice, C::kSlice, &bars->full[s]);
+      }
+      w = x;
+      page = page_next;
+      slot = slot_next;
+      have = have_next;
+    }
+    if (!kCluster && lane == 0) {
+      DecodePart d = part;
+      const long long u0 = t0 - d.tile;
+      d.i0 = part_of(u0, total, parts);
+      d.i1 = part_of(u0 + first_n - 1, total, parts);
+      d.last_i1 = good && w.tile < w.s.n ? part_of(t1 - 1 + (w.s.n - w.tile), total, parts) : blockIdx.x;
+      a.parts[blockIdx.x] = d;
+    }
+    if (!kCluster) fill_empty<Tr>(a);
+    // Every copy issued must have landed before the CTA may exit.
+    if (lane == 0)
+      for (int s = 0; s < C::kStages && s < it; ++s) {
+        const int last = it - 1 - ((it - 1 - s) % C::kStages);
+        mbar_wait_drain(&bars->full[s], (last / C::kStages) & 1, st, kDrainFull);
+      }
+    if (kCluster && a.cluster > 1) {
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int qr = lane >> 2, qc = lane & 3;        // fragment row and column pair
+  const int ka = (qr >> 1) + 4 * (qr & 1);        // the keys of rows qr and qr + 8: ka and ka + 8
+  const uint8_t* mine = smem + warp * C::kSlice;
+  const uint32_t k_at = Record<D>::word(ka, 2 * qc);
+  const uint32_t v_at = Record<D>::kV + Record<D>::word(qc, qr);
+  const uint32_t kp_at = Record<D>::kKp + ka * Record<D>::kPar, vp_at = Record<D>::kVp + ka * Record<D>::kPar;
+  float* buf = reinterpret_cast<float*>(smem + C::kBuf);
+  float2* ml = reinterpret_cast<float2*>(smem + C::kMl);
+  const float sl2 = a.scale_log2;
+
+  uint4 q[NT][kG][2];
+  float nq[NT][kG][2], o[NT][D / 16][4], zs[NT][kG][2], m[NT][2], l[NT][2];
+  bool dead = false, fresh = true;
+  int unit_pos = w.tile;                          // tile of the unit at which this CTA entered it
+  int g = 0, h0 = 0, h1 = 0;                      // kv head, query heads [h0, h1) of the unit
+  for (int it = 0; w.left > 0 || (kCluster && it == 0); ++it) {
+    const bool some = !kCluster || w.left > 0;    // a CTA of a cluster may have no tile, and joins in all the same
+    if (fresh) {
+      fresh = false;
+      unit_pos = w.tile;
+      g = w.col / chunks;
+      h0 = g * G + (w.col - g * chunks) * 8 * NT;
+      h1 = (g + 1) * G;
+      load_q<T, D, NT>(a, w.b, w.col, chunks, q, nq);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kG; ++k) zs[n][k][0] = zs[n][k][1] = 0.f;
+        m[n][0] = m[n][1] = kNone;
+        l[n][0] = l[n][1] = 0.f;
+      }
+    }
+    const int s = it % C::kStages;
+    // After a wait that gave up the warp goes on through its part without
+    // touching the tiles, so that the warps still meet at each unit's end.
+    if (some && !dead && !mbar_wait_warp(&bars->full[s], (it / C::kStages) & 1, st, abort_flag, kSiteFull)) dead = true;
+    if (!dead && some && (bars->mask[s] >> warp & 1)) {
+      const uint8_t* rec = mine + s * C::kStage;
+      const int key0 = (w.s.tile0 + w.tile) * kKeys + warp * 16;
+      const int lo = w.s.first - key0, hi = w.s.len - key0;        // keys [lo, hi) of the slice are visible
+      const bool edge = lo > 0 || hi < 16, in0 = ka >= lo && ka < hi, in1 = ka + 8 >= lo && ka + 8 < hi;
+      float2 pa[kG], pb[kG];
+      // Scores: S^T rows ka, ka + 8, columns 2 qc, 2 qc + 1.
+      float x[NT][4];
+      load_pars<T, D>(rec + kp_at, pa);
+      load_pars<T, D>(rec + kp_at + 8 * Record<D>::kPar, pb);
+      uint32_t wa[kG][2], wb[kG][2];
+      if constexpr (D == 128) {
+        const uint4 ya = *reinterpret_cast<const uint4*>(rec + k_at), yb = *reinterpret_cast<const uint4*>(rec + k_at + 8 * Record<D>::kRow);
+        wa[0][0] = ya.x, wa[1][0] = ya.y, wa[0][1] = ya.z, wa[1][1] = ya.w;
+        wb[0][0] = yb.x, wb[1][0] = yb.y, wb[0][1] = yb.z, wb[1][1] = yb.w;
+      } else {
+        const uint2 ya = *reinterpret_cast<const uint2*>(rec + k_at), yb = *reinterpret_cast<const uint2*>(rec + k_at + 8 * Record<D>::kRow);
+        wa[0][0] = ya.x, wa[0][1] = ya.y, wb[0][0] = yb.x, wb[0][1] = yb.y;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float c[kG][4];
+#pragma unroll
+        for (int k = 0; k < kG; ++k) {
+          c[k][0] = c[k][2] = nq[n][k][0];
+          c[k][1] = c[k][3] = nq[n][k][1];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int k = 0; k < kG; ++k) {
+            score_step<T, 0>(c[k], wa[k][u], wb[k][u], q[n][k][u].x, q[n][k][u].y);
+            score_step<T, 2>(c[k], wa[k][u], wb[k][u], q[n][k][u].z, q[n][k][u].w);
+          }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kG; ++k) {
+          const float sa = pa[k].x * (16.f * sl2), za = pa[k].y * -sl2, sb = pb[k].x * (16.f * sl2), zb = pb[k].y * -sl2;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[n][e] = fmaf(c[k][e], e < 2 ? sa : sb, fmaf(nq[n][k][e & 1], e < 2 ? za : zb, x[n][e]));
+        }
+        if (edge) {
+          if (!in0) x[n][0] = x[n][1] = -INFINITY;
+          if (!in1) x[n][2] = x[n][3] = -INFINITY;
+        }
+        // Weights.
+        float mx0 = fmaxf(x[n][0], x[n][2]), mx1 = fmaxf(x[n][1], x[n][3]);
+        if (__any_sync(0xffffffffu, mx0 > m[n][0] + 8.f || mx1 > m[n][1] + 8.f)) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
+          }
+          const float n0 = fmaxf(m[n][0], mx0), n1 = fmaxf(m[n][1], mx1);
+          const float f0 = ex2(m[n][0] - n0), f1 = ex2(m[n][1] - n1);
+          m[n][0] = n0;
+          m[n][1] = n1;
+          l[n][0] *= f0;
+          l[n][1] *= f1;
+#pragma unroll
+          for (int k = 0; k < kG; ++k) {
+            zs[n][k][0] *= f0;
+            zs[n][k][1] *= f1;
+          }
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            o[n][k][0] *= f0;
+            o[n][k][1] *= f1;
+            o[n][k][2] *= f0;
+            o[n][k][3] *= f1;
+          }
+        }
+        x[n][0] = ex2(x[n][0] - m[n][0]);
+        x[n][1] = ex2(x[n][1] - m[n][1]);
+        x[n][2] = ex2(x[n][2] - m[n][0]);
+        x[n][3] = ex2(x[n][3] - m[n][1]);
+        l[n][0] += x[n][0] + x[n][2];
+        l[n][1] += x[n][1] + x[n][3];
+      }
+      // Values.  The (s, z) of slots that are not visible may be anything.
+      load_pars<T, D>(rec + vp_at, pa);
+      load_pars<T, D>(rec + vp_at + 8 * Record<D>::kPar, pb);
+      uint32_t v[4][kG];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (D == 128) {
+          const uint2 y = *reinterpret_cast<const uint2*>(rec + v_at + i * 4 * Record<D>::kRow);
+          v[i][0] = y.x;
+          v[i][1] = y.y;
+        } else {
+          v[i][0] = *reinterpret_cast<const uint32_t*>(rec + v_at + i * 4 * Record<D>::kRow);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kG; ++k) {
+        if (edge) {
+          if (!in0) pa[k] = make_float2(0.f, 0.f);
+          if (!in1) pb[k] = make_float2(0.f, 0.f);
+        }
+        const float sa = 16.f * pa[k].x, sb = 16.f * pb[k].x, za = pa[k].y - sa, zb = pb[k].y - sb;
+        uint32_t p[NT][2][2];          // P^T: [high, low][keys 0-7, 8-15 of the fragment]
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          zs[n][k][0] = fmaf(x[n][0], za, fmaf(x[n][2], zb, zs[n][k][0]));
+          zs[n][k][1] = fmaf(x[n][1], za, fmaf(x[n][3], zb, zs[n][k][1]));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t high, low;
+            split(x[n][2 * e] * (e ? sb : sa), x[n][2 * e + 1] * (e ? sb : sa), high, low);
+            p[n][0][e] = transpose8(high);
+            p[n][1][e] = transpose8(low);
+          }
+        }
+        // Pairs of keys: elements 8 r + 2 t in the low halves, 8 r + 2 t + 1 in the high ones.
+        const uint32_t e01 = __byte_perm(v[0][k], v[1][k], 0x5410), f01 = __byte_perm(v[0][k], v[1][k], 0x7632);
+        const uint32_t e23 = __byte_perm(v[2][k], v[3][k], 0x5410), f23 = __byte_perm(v[2][k], v[3][k], 0x7632);
+        auto tile = [&](float (&c)[4], const uint32_t (&y)[4], int n) {
+          Bf::mma(c, y, p[n][0][0], p[n][0][1]);
+          Bf::mma(c, y, p[n][1][0], p[n][1][1]);
+        };
+        const uint32_t y0[4] = {Bf::code<0>(e01), Bf::code<0>(f01), Bf::code<0>(e23), Bf::code<0>(f23)};
+        const uint32_t y1[4] = {Bf::code<1>(e01), Bf::code<1>(f01), Bf::code<1>(e23), Bf::code<1>(f23)};
+        const uint32_t y2[4] = {Bf::code<2>(e01), Bf::code<2>(f01), Bf::code<2>(e23), Bf::code<2>(f23)};
+        const uint32_t y3[4] = {Bf::code<3>(e01), Bf::code<3>(f01), Bf::code<3>(e23), Bf::code<3>(f23)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          tile(o[n][4 * k], y0, n);
+          tile(o[n][4 * k + 1], y1, n);
+          tile(o[n][4 * k + 2], y2, n);
+          tile(o[n][4 * k + 3], y3, n);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && some) mbar_arrive(&bars->empty[s]);
+
+    const bool unit_ends = w.tile + 1 == w.s.n;
+    if (unit_ends || w.left <= 1) {
+      // ------------------------------------------------ the unit's end here
+      const bool whole = unit_ends && unit_pos == 0;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          l[n][0] += __shfl_xor_sync(0xffffffffu, l[n][0], d);
+          l[n][1] += __shfl_xor_sync(0xffffffffu, l[n][1], d);
+#pragma unroll
+          for (int k = 0; k < kG; ++k) {
+            zs[n][k][0] += __shfl_xor_sync(0xffffffffu, zs[n][k][0], d);
+            zs[n][k][1] += __shfl_xor_sync(0xffffffffu, zs[n][k][1], d);
+          }
+        }
+        if (qr == 0) {
+          ml[warp * 16 + n * 8 + qc * 2] = make_float2(m[n][0], l[n][0]);
+          ml[warp * 16 + n * 8 + qc * 2 + 1] = make_float2(m[n][1], l[n][1]);
+        }
+      }
+      consumer_sync();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n > 0) consumer_sync();                // the buffer's last readers
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float M = kNone;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) M = fmaxf(M, ml[i * 16 + n * 8 + qc * 2 + e].x);
+          f[e] = ex2(m[n][e] - M);
+        }
+        // [warp][head][d], d xor 2 (head / 2): the four rows and four column pairs
+        // that half a warp stores at once fall on 32 banks.
+        float* to = buf + (warp * 8 + qc * 2) * D;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const int z = k / 4, d = (z * 64 + qr * 8 + (k & 3) * 2) ^ (qc * 2);
+          *reinterpret_cast<float2*>(to + d) = make_float2((o[n][k][0] + zs[n][z][0]) * f[0], (o[n][k][2] + zs[n][z][0]) * f[0]);
+          *reinterpret_cast<float2*>(to + D + d) = make_float2((o[n][k][1] + zs[n][z][1]) * f[1], (o[n][k][3] + zs[n][z][1]) * f[1]);
+        }
+        // A warp a head, two elements a lane.  The last read of ml before the
+        // barrier: behind it a warp may be past its tiles of the next unit and
+        // store that unit's (max, sum) while others still sum here.
+        const int hh = warp, h = h0 + n * 8 + hh;
+        float M = kNone, L = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, ml[i * 16 + n * 8 + hh].x);
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          const float2 y = ml[i * 16 + n * 8 + hh];
+          L += y.y * ex2(y.x - M);
+        }
+        consumer_sync();
+#pragma unroll
+        for (int k = 0; k < kG; ++k) {
+          const int d = k * 64 + lane * 2;
+          const float* from = buf + hh * D + (d ^ ((hh >> 1) * 2));
+          float2 y = *reinterpret_cast<const float2*>(from);
+#pragma unroll
+          for (int i = 1; i < kWarps; ++i) {
+            const float2 z = *reinterpret_cast<const float2*>(from + i * 8 * D);
+            y.x += z.x;
+            y.y += z.y;
+          }
+          if constexpr (kCluster) {
+            // For the join; the tiles have been read.
+            *reinterpret_cast<float2*>(smem + ((n * 8 + hh) * D + d) * 4) = y;
+            if (d == 0) reinterpret_cast<float2*>(smem + kClusterMl<D>)[n * 8 + hh] = make_float2(M, L);
+          } else if (h < h1) {
+            const long long row = (long long)w.b * a.Hq + h;
+            if (whole) {
+              const float inv = 1.f / L;
+              *reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + row * D + d) = Tr::pack(y.x * inv, y.y * inv);
+              if (d == 0) a.lse[row] = (M + log2f(L)) * 0.69314718055994530942f;
+            } else {
+              // Slot 1: the unit starts in this CTA and goes on; slot 0: it
+              // started earlier.
+              const long long at = ((long long)blockIdx.x * 2 + (unit_pos == 0 ? 1 : 0)) * 16 + n * 8 + hh;
+              *reinterpret_cast<float2*>(a.part + at * D + d) = y;
+              if (d == 0) a.part_ml[at] = make_float2(M, L);
+            }
+          }
+        }
+      }
+      fresh = true;
+    }
+    w.next(a, cols);
+  }
+  if constexpr (kCluster) {
+    if (a.cluster > 1) cluster_sync();
+    else consumer_sync();
+    join_cluster<Tr>(a, smem, w, rank, h0, min(h1, h0 + 8 * NT));
+    __syncwarp();
+    if (a.cluster > 1) cluster_sync();             // nobody exits while its share is read
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(128) fa_decode4_join_kernel(const DecodeArgs a) {
   launch_dependents();
   wait_for_previous();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / a.Hq, h = blockIdx.x - b * a.Hq, g = h / (a.Hq / a.kv.Hkv);
-  int len = a.seq_lens[b];
-  if (len < 0 || len > (long long)a.table.cols * a.kv.page_size) {
-    if (threadIdx.x == 0) record_error(st, kErrBadIndex, kSiteDecode4Len);
-    len = 0;
-  }
-  const int first = a.window > 0 && len > a.window ? len - a.window : 0;
-  float q[kE], o[kE] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < kE; ++e)
-    q[e] = (float)(static_cast<const T*>(a.q) + b * a.q_sb + h * a.q_sh)[lane * kE + e];
-  const int word = lane * kE / 8, group = lane * kE / 64, e0 = lane * kE % 8;
-  for (int j = first + warp; j < len; j += 4) {
-    const int col = j / a.kv.page_size, slot = j - col * a.kv.page_size, page = a.table.pages[b * a.table.stride + col];
-    if (page < 0 || page >= a.kv.num_pages) {
-      if (lane == 0) record_error(st, kErrBadIndex, kSiteDecode4Page);
-      continue;
-    }
-    const uint8_t* rec = static_cast<const uint8_t*>(a.kv.k) + page * a.kv.s_page + g * a.kv.s_head +
-                         (slot >> 4) * (long long)Record<D>::kBytes;
-    float x[2][kE];
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + (kv ? Record<D>::kV : 0) + Record<D>::word(slot & 15, word));
-      const float2 p = Pair2<T>::up(reinterpret_cast<const uint32_t*>(rec + (kv ? Record<D>::kVp : Record<D>::kKp) +
-                                                                      (slot & 15) * Record<D>::kPar)[group]);
-      for (int e = 0; e < kE; ++e) x[kv][e] = p.y + p.x * (float)((w >> (16 * (e & 1) + 4 * ((e0 + e) >> 1))) & 15u);
-    }
-    float s = 0.f;
-    for (int e = 0; e < kE; ++e) s = fmaf(q[e], x[0][e], s);
-    s = sum_over(s, 32) * a.scale_log2;
-    const float n = fmaxf(m, s), f = m == -INFINITY ? 0.f : ex2(m - n), p = ex2(s - n);
-    m = n;
-    l = l * f + p;
-    for (int e = 0; e < kE; ++e) o[e] = o[e] * f + p * x[1][e];
-  }
-  for (int e = 0; e < kE; ++e) so[warp][lane * kE + e] = o[e];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  __syncthreads();
-  const float M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float L = 0.f, f[4];
-  for (int i = 0; i < 4; ++i) {
-    f[i] = sm[i] == -INFINITY ? 0.f : ex2(sm[i] - M);
-    L += f[i] * sl[i];
-  }
-  const long long row = (long long)b * a.Hq + h;
-  for (int d = threadIdx.x * 2; d < D; d += 256) {
-    float y[2];
-    for (int e = 0; e < 2; ++e) {
-      y[e] = 0.f;
-      for (int i = 0; i < 4; ++i) y[e] += f[i] * so[i][d + e];
-      y[e] = len > 0 ? y[e] / L : 0.f;
-    }
-    *reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + row * D + d) = Pair2<T>::down(y[0], y[1]);
-  }
-  if (threadIdx.x == 0) a.lse[row] = len > 0 ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+  join<Traits<T, D>>(a);
+}
+
+template <typename T, int D>
+cudaError_t launch(const DecodeArgs& a, const DevStatus& st, int parts, cudaStream_t stream) {
+  if (a.cluster)
+    return launch_after(a.unit_heads == 8 ? fa_decode4_kernel<T, D, 1, true> : fa_decode4_kernel<T, D, 2, true>, parts,
+                        kThreads, Cfg<D>::kBytes, a.cluster, stream, a, st);
+  cudaError_t e = launch_after(a.unit_heads == 8 ? fa_decode4_kernel<T, D, 1, false> : fa_decode4_kernel<T, D, 2, false>,
+                               parts, kThreads, Cfg<D>::kBytes, 1, stream, a, st);
+  const int joins = (parts - 1) * (a.unit_heads / 4);
+  if (e == cudaSuccess && joins > 0) e = launch_after(fa_decode4_join_kernel<T, D>, joins, 128, 0, 1, stream, a);
+  return e;
+}
+
+template <typename T, int D>
+cudaError_t configure() {
+  static_assert(Cfg<D>::kBytes <= 115712, "two CTAs per SM");
+  static_assert(kKeys == kDecode4TileKeys, "tile");
+  cudaError_t e = cudaSuccess;
+  for (auto k : {fa_decode4_kernel<T, D, 1, false>, fa_decode4_kernel<T, D, 2, false>, fa_decode4_kernel<T, D, 1, true>,
+                 fa_decode4_kernel<T, D, 2, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kBytes);
+  if (e == cudaSuccess) e = preload_kernel(fa_decode4_join_kernel<T, D>);
+  return e;
 }
 
 }  // namespace
 
 cudaError_t configure_decode4_kernels() {
-  cudaError_t e = preload_kernel(fa_decode4_kernel<__nv_bfloat16, 64>);
-  if (e == cudaSuccess) e = preload_kernel(fa_decode4_kernel<__nv_bfloat16, 128>);
-  if (e == cudaSuccess) e = preload_kernel(fa_decode4_kernel<__half, 64>);
-  if (e == cudaSuccess) e = preload_kernel(fa_decode4_kernel<__half, 128>);
+  cudaError_t e = configure<__nv_bfloat16, 64>();
+  if (e == cudaSuccess) e = configure<__nv_bfloat16, 128>();
+  if (e == cudaSuccess) e = configure<__half, 64>();
+  if (e == cudaSuccess) e = configure<__half, 128>();
   return e;
 }
 
 cudaError_t launch_decode4(int dtype, const DecodeArgs& a, const DevStatus& st, int parts, cudaStream_t stream) {
-  auto k = dtype == 0 ? (a.kv.d == 64 ? fa_decode4_kernel<__nv_bfloat16, 64> : fa_decode4_kernel<__nv_bfloat16, 128>)
-                      : (a.kv.d == 64 ? fa_decode4_kernel<__half, 64> : fa_decode4_kernel<__half, 128>);
-  return launch_after(k, a.B * a.Hq, 128, 0, 1, stream, a, st);
+  if (dtype == 0)
+    return a.kv.d == 64 ? launch<__nv_bfloat16, 64>(a, st, parts, stream) : launch<__nv_bfloat16, 128>(a, st, parts, stream);
+  return a.kv.d == 64 ? launch<__half, 64>(a, st, parts, stream) : launch<__half, 128>(a, st, parts, stream);
 }
 
 }  // namespace fa

@@ -82,6 +82,10 @@ struct Read4Args {
   int B, N;
 };
 
+constexpr int kDecode4TileKeys = 128;
+// CTAs of the decode kernel that an SM holds, by the heads of a unit.
+constexpr int decode4_ctas_per_sm(int unit_heads) { return unit_heads == 8 ? 2 : 1; }
+
 cudaError_t launch_append4(int dtype, const Append4Args& a, const DevStatus& st, int num_sms, cudaStream_t stream);
 cudaError_t launch_read4(int dtype, const Read4Args& a, const DevStatus& st, int num_sms, cudaStream_t stream);
 cudaError_t launch_decode4(int dtype, const DecodeArgs& a, const DevStatus& st, int parts, cudaStream_t stream);

@@ -193,6 +193,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const TmaMap3* m, uint64_
       : "memory");
 }
 
+// Untiled load of `bytes` contiguous bytes; both addresses 16-byte aligned, bytes
+// a multiple of 16.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // Tiled 3-D reduce-add of a shared-memory box into global memory (the tensor
 // map's element type and reduction), tracked by this thread's bulk group.
 __device__ __forceinline__ void tma_reduce_add_3d(const TmaMap3* m, uint32_t ssrc, int c0, int c1, int c2) {
