@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t encode8(const float (&x)[8], float s, float 
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int c = __float2int_rn(__fdiv_rn(__fsub_rn(x[e], z), s));
-    w |= (uint32_t)min(max(c, 0), 15) << (16 * (e & 1) + 4 * (e >> 1));
+    w |= place_code((uint32_t)min(max(c, 0), 15), e);
   }
   return s == 0.f ? 0u : w;
 }
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) fa_read4_kernel(const Read4Args a, c
               reinterpret_cast<const uint32_t*>(rec + (kv ? Record<D>::kVp : Record<D>::kKp) + s * Record<D>::kPar)[g]);
           float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = p.y + p.x * (float)((w >> (16 * (e & 1) + 4 * (e >> 1))) & 15u);
+          for (int e = 0; e < 8; ++e) x[e] = p.y + p.x * (float)code_at(w, e);
           (kv ? v : k) = down8<T>(x);
         }
       }

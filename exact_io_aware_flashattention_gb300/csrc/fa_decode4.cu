@@ -2,20 +2,28 @@
 //   o_h = sum_j p_h(j) v_j,  p_h(j) = exp(scale q_h . k_j - lse_h),
 // where k_j and v_j are the values z + s c that the cached codes stand for.
 //
-// Every code enters the matrix products as it is: the four bits become the
-// mantissa of 1 + c / 16, exact in bf16 and fp16, by a shift and one logic
-// instruction for a pair, and s and z are applied in fp32 outside,
-//   q . k_j = sum over groups g of 16 s_jg (sum_i q_i (1 + c_ji / 16) - Q_g) + z_jg Q_g,
-// Q_g the sum of q over the group (-Q_g is what the accumulators start from), and
-//   o = sum_j (16 s_j p_j) (1 + c_j / 16) + sum_j p_j (z_j - 16 s_j),
-// the second sum one number a head and group.  So nothing is rounded to 16 bits
-// but the weights 16 s p, which enter as the sum of two bf16 values (off by 2^-16
-// of themselves).
+// Every code enters the matrix products as it is, s and z are applied in fp32
+// outside: with Q_g the sum of q over group g,
+//   q . k_j = sum over g of s_jg sum_i q_i c_ji + z_jg Q_g,
+//   o = sum_j (s_j p_j) (c_j - 8) + sum_j p_j (z_j + 8 s_j),
+// the last sum one number a head and group.  Four bits in the upper or the next
+// mantissa bits of an fp16 number with exponent 0 are the subnormal c 2^-18 or c
+// 2^-22: one AND for a pair of codes (and two bytes swapped give the other half of
+// a word).  So they enter for K; for V one multiply-add makes both (c - 8) 2^-7:
+// the tensor pipe cuts its sums instead of rounding them, which adds up over
+// many keys where all terms have one sign (with c, o was 1.2 times, with 1 + c /
+// 16 2.8 times as far off at 32768 keys).
+//   q, whatever its type, enters in fp16 times a power of two that brings a
+// unit's largest element to 2^10 (16 times that for the codes held as c 2^-22):
+// exact but for elements 2^-24 times smaller than the largest.  The weights s p
+// enter times a power of two that brings the largest s so far to 2^6 (p is 2^8 at
+// most), as the sum of two fp16 values, off by 2^-22 of themselves or 2^-32 of the
+// largest.
 //
 // The line of tiles, its cut into equal parts, one a CTA, and their joins are
 // those of the 16-bit kernel (fa_decode.cuh, fa_paged.cu); a warp's slice of a tile
-// is one record of 16 keys, which one untiled copy fetches.  Warp 8 is the
-// producer, warps 0-7 own a slice of each tile each.  Products by mma.sync
+// is one record of 16 keys, which one untiled copy fetches.  Warp 7 is the
+// producer, warps 0-6 own a slice of each tile each.  Products by mma.sync
 // (m16n8k16) with keys, then elements of d as rows and 8 heads as columns: see
 // fa_paged.cu.  Row i of a slice's S^T is the key (i % 8) / 2 + 4 (i % 2) + 8 (i / 8),
 // so that the lanes that read the pairs of keys of V from shared memory, four
@@ -34,7 +42,7 @@ namespace fa {
 
 namespace {
 
-constexpr int kWarps = 8;                          // consumers, one 16-key slice of a tile each
+constexpr int kWarps = 7;                          // consumers, one 16-key slice of a tile each
 constexpr int kConsumerThreads = kWarps * 32;
 constexpr int kThreads = kConsumerThreads + 32;
 constexpr int kKeys = 16 * kWarps;
@@ -53,7 +61,6 @@ struct Cfg {
 
 struct Bars {
   uint64_t full[8], empty[8];
-  int mask[8];               // slices of the stage's tile that were loaded
   int abort;
   int scan[kThreads / 32];
   int b0;                    // first sequence of this CTA's part
@@ -65,43 +72,50 @@ template <typename T>
 struct Type;
 template <>
 struct Type<__nv_bfloat16> {
-  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
+  static constexpr int kWeights = 1;              // fp16 values a weight is the sum of
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return cvt_bf16x2(lo, hi); }
   static __device__ __forceinline__ float2 up(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  // 1 + c / 16 for code n of both halves of w.
-  template <int n>
-  static __device__ __forceinline__ uint32_t code(uint32_t w) {
-    return ((n == 0 ? w << 3 : w >> (n == 0 ? 0 : 4 * n - 3)) & 0x00780078u) | 0x3f803f80u;
-  }
 };
 template <>
 struct Type<__half> {
-  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
+  static constexpr int kWeights = 2;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
   static __device__ __forceinline__ float2 up(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
-  template <int n>
-  static __device__ __forceinline__ uint32_t code(uint32_t w) {
-    return ((n < 2 ? w << (n < 2 ? 6 - 4 * n : 0) : w >> (n < 2 ? 0 : 4 * n - 6)) & 0x03c003c0u) | 0x3c003c00u;
-  }
 };
-using Bf = Type<__nv_bfloat16>;
+using Half = Type<__half>;
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Codes of two halves as c 2^-18 (of places 0 and 2) and c 2^-22 (1 and 3); places 2
+// and 3 after the halves' bytes are swapped.
+__device__ __forceinline__ uint32_t upper(uint32_t w) { return w & 0x03c003c0u; }
+__device__ __forceinline__ uint32_t lower(uint32_t w) { return w & 0x003c003cu; }
+// Either as (c - 8) 2^-7.
+template <bool kLower>
+__device__ __forceinline__ uint32_t centred(uint32_t x) {
+  uint32_t y;                                     // x 2^11 - 2^-4, or x 2^15 - 2^-4
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(kLower ? 0x78007800u : 0x68006800u), "r"(0xac00ac00u));
+  return y;
+}
+__device__ __forceinline__ uint32_t swapped(uint32_t w) { return __byte_perm(w, w, 0x2301); }
 
 template <typename T_, int D_>
 struct Traits {
@@ -118,11 +132,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumerThreads) : "memory"); }
 
-// Two weights as the sum of two bf16 values each: hi their upper halves.
-__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
-  hi = __byte_perm(a, b, 0x7632);
-  lo = cvt_bf16x2(x - __uint_as_float(a & 0xffff0000u), y - __uint_as_float(b & 0xffff0000u));
+// The power of two above a positive finite x.
+__device__ __forceinline__ float power_above(float x) {
+  return __uint_as_float((__float_as_uint(x) & 0x7f800000u) + 0x00800000u);
 }
 
 // The (s, z) pairs of one row, D / 64 of them.
@@ -138,14 +150,16 @@ __device__ __forceinline__ void load_pars(const uint8_t* p, float2 (&x)[D / 64])
 }
 
 // Query rows of unit (b, col) as B operands, column = head lane / 4: q[n][g][w] the
-// eight elements 64 g + 16 (lane % 4) + 8 w on; and nq, the negative sums over the
-// groups for the heads 2 (lane % 4) and the next, this lane's columns of S^T.
+// eight elements 64 g + 16 (lane % 4) + 8 w on, times `times` and, the odd pairs,
+// 16; and sums[n][g], those over the groups for the heads 2 (lane % 4) and the
+// next, this lane's columns of S^T.
 template <typename T, int D, int NT>
 __device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int col, int chunks, uint4 (&q)[NT][D / 64][2],
-                                       float (&nq)[NT][D / 64][2]) {
+                                       float (&sums)[NT][D / 64][2], float& times) {
   const int lane = threadIdx.x & 31, G = a.Hq / a.kv.Hkv;
   const int g = col / chunks, h0 = g * G + (col - g * chunks) * 8 * NT + (lane >> 2), h1 = (g + 1) * G;
   const T* p = static_cast<const T*>(a.q) + b * a.q_sb + (lane & 3) * 16;
+  float top = 0.f;                                // the largest finite |q|
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const bool in = h0 + n * 8 < h1;
@@ -161,24 +175,225 @@ __device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int col, int 
         for (int i = 0; i < 4; ++i) {
           const float2 y = Type<T>::up(e[i]);
           s += y.x + y.y;
+          top = fmaxf(top, fabsf(y.x) < INFINITY ? fabsf(y.x) : 0.f);
+          top = fmaxf(top, fabsf(y.y) < INFINITY ? fabsf(y.y) : 0.f);
         }
       }
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
-      nq[n][k][0] = -__shfl_sync(0xffffffffu, s, (lane & 3) * 8);
-      nq[n][k][1] = -__shfl_sync(0xffffffffu, s, (lane & 3) * 8 + 4);
+      sums[n][k][0] = __shfl_sync(0xffffffffu, s, (lane & 3) * 8);
+      sums[n][k][1] = __shfl_sync(0xffffffffu, s, (lane & 3) * 8 + 4);
     }
   }
-}
-
-template <typename T, int n>
-__device__ __forceinline__ void score_step(float (&c)[4], uint32_t wa, uint32_t wb, uint32_t b0, uint32_t b1) {
-  const uint32_t x[4] = {Type<T>::template code<n>(wa), Type<T>::template code<n>(wb), Type<T>::template code<n + 1>(wa),
-                         Type<T>::template code<n + 1>(wb)};
-  Type<T>::mma(c, x, b0, b1);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  times = 2048.f / power_above(fmaxf(top, 0x1p-100f));
+  const float more = 16.f * times;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint4& v = q[n][k][w];
+        const float2 y0 = Type<T>::up(v.x), y1 = Type<T>::up(v.y), y2 = Type<T>::up(v.z), y3 = Type<T>::up(v.w);
+        v = make_uint4(Half::pack(y0.x * times, y0.y * times), Half::pack(y1.x * more, y1.y * more),
+                       Half::pack(y2.x * times, y2.y * times), Half::pack(y3.x * more, y3.y * more));
+      }
 }
 
 constexpr float kNone = -1e30f;      // below every score: the maximum before the first key
+
+// mbar_wait_warp with the phase usually complete: one poll and one vote.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const DevStatus& st, volatile int* abort, int site) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
+  return mbar_wait_warp(bar, parity, st, abort, site);
+}
+
+// A warp's work on one slice, the record rec of the 16 keys from key0 on: S^T, its
+// weights against the running maximum m and, in l, zs and o, their sums.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void slice(const uint8_t* rec, int key0, const Span& s, uint32_t k_at, uint32_t v_at, uint32_t kp_at,
+                                      uint32_t vp_at, int ka, float sl2, float by, const uint4 (&q)[NT][D / 64][2],
+                                      const float (&qs)[NT][D / 64][2], float (&o)[NT][D / 16][4], float (&zs)[NT][D / 64][2],
+                                      float (&m)[NT][2], float (&l)[NT][2], float (&grow)[D / 64]) {
+  constexpr int kG = D / 64;
+  constexpr int kW = Type<T>::kWeights;
+  const bool edge = key0 < s.first || key0 + 16 > s.len;
+  // Scores: S^T rows ka, ka + 8, columns 2 qc, 2 qc + 1.
+  float x[NT][4];
+  float2 pa[kG], pb[kG];
+  load_pars<T, D>(rec + kp_at, pa);
+  load_pars<T, D>(rec + kp_at + 8 * Record<D>::kPar, pb);
+  uint32_t wa[kG][2], wb[kG][2];
+  if constexpr (D == 128) {
+    const uint4 ya = *reinterpret_cast<const uint4*>(rec + k_at);
+    const uint4 yb = *reinterpret_cast<const uint4*>(rec + k_at + 8 * Record<D>::kRow);
+    wa[0][0] = ya.x, wa[1][0] = ya.y, wa[0][1] = ya.z, wa[1][1] = ya.w;
+    wb[0][0] = yb.x, wb[1][0] = yb.y, wb[0][1] = yb.z, wb[1][1] = yb.w;
+  } else {
+    const uint2 ya = *reinterpret_cast<const uint2*>(rec + k_at);
+    const uint2 yb = *reinterpret_cast<const uint2*>(rec + k_at + 8 * Record<D>::kRow);
+    wa[0][0] = ya.x, wa[0][1] = ya.y, wb[0][0] = yb.x, wb[0][1] = yb.y;
+  }
+  {
+    float c[NT][kG][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int k = 0; k < kG; ++k) {
+        const uint32_t y = wa[k][u], z = wb[k][u], ys = swapped(y), zs_ = swapped(z);
+        const uint32_t f[8] = {upper(y), upper(z), lower(y), lower(z), upper(ys), upper(zs_), lower(ys), lower(zs_)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (u == 0) mma_first(c[n][k], f[0], f[1], f[2], f[3], q[n][k][u].x, q[n][k][u].y);
+          else mma(c[n][k], f[0], f[1], f[2], f[3], q[n][k][u].x, q[n][k][u].y);
+          mma(c[n][k], f[4], f[5], f[6], f[7], q[n][k][u].z, q[n][k][u].w);
+        }
+      }
+#pragma unroll
+    for (int k = 0; k < kG; ++k) {
+      const float sa = pa[k].x * by, za = pa[k].y * sl2, sb = pb[k].x * by, zb = pb[k].y * sl2;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[n][e] = fmaf(c[n][k][e], e < 2 ? sa : sb,
+                         k == 0 ? qs[n][k][e & 1] * (e < 2 ? za : zb) : fmaf(qs[n][k][e & 1], e < 2 ? za : zb, x[n][e]));
+    }
+  }
+  load_pars<T, D>(rec + vp_at, pa);
+  load_pars<T, D>(rec + vp_at + 8 * Record<D>::kPar, pb);
+  if (edge) {
+    // The (s, z) of slots that are not visible may be anything.
+    if (key0 + ka < s.first || key0 + ka >= s.len) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kG; ++k) pa[k] = make_float2(0.f, 0.f);
+    }
+    if (key0 + ka + 8 < s.first || key0 + ka + 8 >= s.len) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) x[n][2] = x[n][3] = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kG; ++k) pb[k] = make_float2(0.f, 0.f);
+    }
+  }
+  bool more = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    more |= fmaxf(x[n][0], x[n][2]) > m[n][0] + 8.f || fmaxf(x[n][1], x[n][3]) > m[n][1] + 8.f;
+#pragma unroll
+  for (int k = 0; k < kG; ++k) more |= fmaxf(pa[k].x, pb[k].x) * grow[k] >= 128.f;
+  if (__any_sync(0xffffffffu, more)) {
+    // Maxima to the exact ones, and what was summed so far to them.
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float mx0 = fmaxf(x[n][0], x[n][2]), mx1 = fmaxf(x[n][1], x[n][3]);
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
+      }
+      const float n0 = fmaxf(m[n][0], mx0), n1 = fmaxf(m[n][1], mx1);
+      const float f0 = ex2(m[n][0] - n0), f1 = ex2(m[n][1] - n1);
+      m[n][0] = n0;
+      m[n][1] = n1;
+      l[n][0] *= f0;
+      l[n][1] *= f1;
+#pragma unroll
+      for (int k = 0; k < kG; ++k) {
+        zs[n][k][0] *= f0;
+        zs[n][k][1] *= f1;
+      }
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        o[n][k][0] *= f0;
+        o[n][k][1] *= f1;
+        o[n][k][2] *= f0;
+        o[n][k][3] *= f1;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kG; ++k) {
+      // (An infinite s, of a group that reads as NaN, does not count.)
+      float top = fmaxf(pa[k].x < INFINITY ? pa[k].x : 0.f, pb[k].x < INFINITY ? pb[k].x : 0.f);
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      if (top * grow[k] >= 128.f) {
+        const float to = 128.f / power_above(top), f = to / grow[k];
+        grow[k] = to;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][k * 4 + t][e] *= f;
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    x[n][0] = ex2(x[n][0] - m[n][0]);
+    x[n][1] = ex2(x[n][1] - m[n][1]);
+    x[n][2] = ex2(x[n][2] - m[n][0]);
+    x[n][3] = ex2(x[n][3] - m[n][1]);
+    l[n][0] += x[n][0] + x[n][2];
+    l[n][1] += x[n][1] + x[n][3];
+  }
+  // Values.
+  uint32_t v[4][kG];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (D == 128) {
+      const uint2 y = *reinterpret_cast<const uint2*>(rec + v_at + i * 4 * Record<D>::kRow);
+      v[i][0] = y.x;
+      v[i][1] = y.y;
+    } else {
+      v[i][0] = *reinterpret_cast<const uint32_t*>(rec + v_at + i * 4 * Record<D>::kRow);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kG; ++k) {
+    const float sa = pa[k].x * grow[k], sb = pb[k].x * grow[k];
+    const float za = fmaf(pa[k].x, 8.f, pa[k].y), zb = fmaf(pb[k].x, 8.f, pb[k].y);
+    uint32_t p[NT][kW][2];         // P^T: [high, low][keys 0-7, 8-15 of the fragment]
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      zs[n][k][0] = fmaf(x[n][0], za, fmaf(x[n][2], zb, zs[n][k][0]));
+      zs[n][k][1] = fmaf(x[n][1], za, fmaf(x[n][3], zb, zs[n][k][1]));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float w0 = x[n][2 * e] * (e ? sb : sa), w1 = x[n][2 * e + 1] * (e ? sb : sa);
+        const uint32_t high = Half::pack(w0, w1);
+        p[n][0][e] = transpose8(high);
+        if constexpr (kW == 2) {
+          const float2 h = Half::up(high);
+          p[n][1][e] = transpose8(Half::pack(w0 - h.x, w1 - h.y));
+        }
+      }
+    }
+    // Pairs of keys: elements 8 r + 2 t from the low halves, 8 r + 2 t + 1 from the
+    // high ones, for tiles t = 0 and 1, then with their bytes swapped for 2 and 3.
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t e01 = __byte_perm(v[0][k], v[1][k], u ? 0x4501 : 0x5410);
+      const uint32_t f01 = __byte_perm(v[0][k], v[1][k], u ? 0x6723 : 0x7632);
+      const uint32_t e23 = __byte_perm(v[2][k], v[3][k], u ? 0x4501 : 0x5410);
+      const uint32_t f23 = __byte_perm(v[2][k], v[3][k], u ? 0x6723 : 0x7632);
+      const uint32_t y[8] = {centred<false>(upper(e01)), centred<false>(upper(f01)), centred<false>(upper(e23)),
+                             centred<false>(upper(f23)), centred<true>(lower(e01)),  centred<true>(lower(f01)),
+                             centred<true>(lower(e23)),  centred<true>(lower(f23))};
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+          mma(o[n][4 * k + 2 * u], y[0], y[1], y[2], y[3], p[n][i][0], p[n][i][1]);
+          mma(o[n][4 * k + 2 * u + 1], y[4], y[5], y[6], y[7], p[n][i][0], p[n][i][1]);
+        }
+    }
+  }
+}
 
 template <typename T, int D, int NT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(const DecodeArgs a, const DevStatus st) {
@@ -271,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
-    // Lane l looks up slice l % 8 of tile l / 8 of the unit's next four tiles, one
-    // run ahead of the copies; lanes 0-7 issue a slice's copy each.
+    // Lane l looks up slice l % kWarps of tile l / kWarps of the unit's next tiles,
+    // one run ahead of the copies; lanes below kWarps issue a slice's copy each.
     constexpr int kAhead = 32 / kWarps;
     const int my_slice = lane % kWarps, my_tile = lane / kWarps;
     auto look_up = [&](const Walk<kKeys>& x, int& page, int& slot) {
@@ -317,7 +532,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
         const int sl = __shfl_sync(0xffffffffu, slot, i * kWarps + my_slice);
         const uint32_t mask = __ballot_sync(0xffffffffu, sl >= 0) & ((1u << kWarps) - 1);
         if (lane == 0) {
-          bars->mask[s] = mask;
           mbar_arrive_expect_tx(&bars->full[s], __popc(mask) * C::kSlice);
         }
         __syncwarp();
@@ -365,177 +579,52 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
   const float sl2 = a.scale_log2;
 
   uint4 q[NT][kG][2];
-  float nq[NT][kG][2], o[NT][D / 16][4], zs[NT][kG][2], m[NT][2], l[NT][2];
-  bool dead = false, fresh = true;
-  int unit_pos = w.tile;                          // tile of the unit at which this CTA entered it
+  float qs[NT][kG][2], o[NT][D / 16][4], zs[NT][kG][2], m[NT][2], l[NT][2];
+  float by = 0.f, grow[kG];                       // of S^T; brings the s of V so far to 2^7 at most
+  bool dead = false;
   int g = 0, h0 = 0, h1 = 0;                      // kv head, query heads [h0, h1) of the unit
-  for (int it = 0; w.left > 0 || (kCluster && it == 0); ++it) {
-    const bool some = !kCluster || w.left > 0;    // a CTA of a cluster may have no tile, and joins in all the same
-    if (fresh) {
-      fresh = false;
-      unit_pos = w.tile;
-      g = w.col / chunks;
-      h0 = g * G + (w.col - g * chunks) * 8 * NT;
-      h1 = (g + 1) * G;
-      load_q<T, D, NT>(a, w.b, w.col, chunks, q, nq);
+  uint32_t stage = 0, phase = 0;
+  do {
+    // ------------------------------------------------ one unit's tiles here
+    // (A CTA of a cluster may have none, and joins in all the same.)
+    const int nt = (int)min((long long)(w.s.n - w.tile), w.left);
+    g = w.col / chunks;
+    h0 = g * G + (w.col - g * chunks) * 8 * NT;
+    h1 = (g + 1) * G;
+    load_q<T, D, NT>(a, w.b, w.col, chunks, q, qs, by);
+    by = sl2 * 0x1p18f / by;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+    for (int k = 0; k < kG; ++k) grow[k] = 0x1p107f;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
+      for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-        for (int k = 0; k < kG; ++k) zs[n][k][0] = zs[n][k][1] = 0.f;
-        m[n][0] = m[n][1] = kNone;
-        l[n][0] = l[n][1] = 0.f;
+        for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kG; ++k) zs[n][k][0] = zs[n][k][1] = 0.f;
+      m[n][0] = m[n][1] = kNone;
+      l[n][0] = l[n][1] = 0.f;
+    }
+    int key0 = (w.s.tile0 + w.tile) * kKeys + warp * 16;
+    for (int i = 0; i < nt; ++i, key0 += kKeys) {
+      // After a wait that gave up the warp goes on through its part without
+      // touching the tiles, so that the warps still meet at each unit's end.
+      if (!dead && !wait_warp(&bars->full[stage], phase, st, abort_flag, kSiteFull)) dead = true;
+      // (A slice whose page number is out of range was not loaded: what lies
+      // there is worked on, and its sequence's outputs are unspecified.)
+      if (!dead && key0 < w.s.len && key0 + 16 > w.s.first)
+        slice<T, D, NT>(mine + stage * C::kStage, key0, w.s, k_at, v_at, kp_at, vp_at, ka, sl2, by, q, qs, o, zs, m, l, grow);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->empty[stage]);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
       }
     }
-    const int s = it % C::kStages;
-    // After a wait that gave up the warp goes on through its part without
-    // touching the tiles, so that the warps still meet at each unit's end.
-    if (some && !dead && !mbar_wait_warp(&bars->full[s], (it / C::kStages) & 1, st, abort_flag, kSiteFull)) dead = true;
-    if (!dead && some && (bars->mask[s] >> warp & 1)) {
-      const uint8_t* rec = mine + s * C::kStage;
-      const int key0 = (w.s.tile0 + w.tile) * kKeys + warp * 16;
-      const int lo = w.s.first - key0, hi = w.s.len - key0;        // keys [lo, hi) of the slice are visible
-      const bool edge = lo > 0 || hi < 16, in0 = ka >= lo && ka < hi, in1 = ka + 8 >= lo && ka + 8 < hi;
-      float2 pa[kG], pb[kG];
-      // Scores: S^T rows ka, ka + 8, columns 2 qc, 2 qc + 1.
-      float x[NT][4];
-      load_pars<T, D>(rec + kp_at, pa);
-      load_pars<T, D>(rec + kp_at + 8 * Record<D>::kPar, pb);
-      uint32_t wa[kG][2], wb[kG][2];
-      if constexpr (D == 128) {
-        const uint4 ya = *reinterpret_cast<const uint4*>(rec + k_at), yb = *reinterpret_cast<const uint4*>(rec + k_at + 8 * Record<D>::kRow);
-        wa[0][0] = ya.x, wa[1][0] = ya.y, wa[0][1] = ya.z, wa[1][1] = ya.w;
-        wb[0][0] = yb.x, wb[1][0] = yb.y, wb[0][1] = yb.z, wb[1][1] = yb.w;
-      } else {
-        const uint2 ya = *reinterpret_cast<const uint2*>(rec + k_at), yb = *reinterpret_cast<const uint2*>(rec + k_at + 8 * Record<D>::kRow);
-        wa[0][0] = ya.x, wa[0][1] = ya.y, wb[0][0] = yb.x, wb[0][1] = yb.y;
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float c[kG][4];
-#pragma unroll
-        for (int k = 0; k < kG; ++k) {
-          c[k][0] = c[k][2] = nq[n][k][0];
-          c[k][1] = c[k][3] = nq[n][k][1];
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int k = 0; k < kG; ++k) {
-            score_step<T, 0>(c[k], wa[k][u], wb[k][u], q[n][k][u].x, q[n][k][u].y);
-            score_step<T, 2>(c[k], wa[k][u], wb[k][u], q[n][k][u].z, q[n][k][u].w);
-          }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < kG; ++k) {
-          const float sa = pa[k].x * (16.f * sl2), za = pa[k].y * -sl2, sb = pb[k].x * (16.f * sl2), zb = pb[k].y * -sl2;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[n][e] = fmaf(c[k][e], e < 2 ? sa : sb, fmaf(nq[n][k][e & 1], e < 2 ? za : zb, x[n][e]));
-        }
-        if (edge) {
-          if (!in0) x[n][0] = x[n][1] = -INFINITY;
-          if (!in1) x[n][2] = x[n][3] = -INFINITY;
-        }
-        // Weights.
-        float mx0 = fmaxf(x[n][0], x[n][2]), mx1 = fmaxf(x[n][1], x[n][3]);
-        if (__any_sync(0xffffffffu, mx0 > m[n][0] + 8.f || mx1 > m[n][1] + 8.f)) {
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
-          }
-          const float n0 = fmaxf(m[n][0], mx0), n1 = fmaxf(m[n][1], mx1);
-          const float f0 = ex2(m[n][0] - n0), f1 = ex2(m[n][1] - n1);
-          m[n][0] = n0;
-          m[n][1] = n1;
-          l[n][0] *= f0;
-          l[n][1] *= f1;
-#pragma unroll
-          for (int k = 0; k < kG; ++k) {
-            zs[n][k][0] *= f0;
-            zs[n][k][1] *= f1;
-          }
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            o[n][k][0] *= f0;
-            o[n][k][1] *= f1;
-            o[n][k][2] *= f0;
-            o[n][k][3] *= f1;
-          }
-        }
-        x[n][0] = ex2(x[n][0] - m[n][0]);
-        x[n][1] = ex2(x[n][1] - m[n][1]);
-        x[n][2] = ex2(x[n][2] - m[n][0]);
-        x[n][3] = ex2(x[n][3] - m[n][1]);
-        l[n][0] += x[n][0] + x[n][2];
-        l[n][1] += x[n][1] + x[n][3];
-      }
-      // Values.  The (s, z) of slots that are not visible may be anything.
-      load_pars<T, D>(rec + vp_at, pa);
-      load_pars<T, D>(rec + vp_at + 8 * Record<D>::kPar, pb);
-      uint32_t v[4][kG];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (D == 128) {
-          const uint2 y = *reinterpret_cast<const uint2*>(rec + v_at + i * 4 * Record<D>::kRow);
-          v[i][0] = y.x;
-          v[i][1] = y.y;
-        } else {
-          v[i][0] = *reinterpret_cast<const uint32_t*>(rec + v_at + i * 4 * Record<D>::kRow);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kG; ++k) {
-        if (edge) {
-          if (!in0) pa[k] = make_float2(0.f, 0.f);
-          if (!in1) pb[k] = make_float2(0.f, 0.f);
-        }
-        const float sa = 16.f * pa[k].x, sb = 16.f * pb[k].x, za = pa[k].y - sa, zb = pb[k].y - sb;
-        uint32_t p[NT][2][2];          // P^T: [high, low][keys 0-7, 8-15 of the fragment]
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          zs[n][k][0] = fmaf(x[n][0], za, fmaf(x[n][2], zb, zs[n][k][0]));
-          zs[n][k][1] = fmaf(x[n][1], za, fmaf(x[n][3], zb, zs[n][k][1]));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t high, low;
-            split(x[n][2 * e] * (e ? sb : sa), x[n][2 * e + 1] * (e ? sb : sa), high, low);
-            p[n][0][e] = transpose8(high);
-            p[n][1][e] = transpose8(low);
-          }
-        }
-        // Pairs of keys: elements 8 r + 2 t in the low halves, 8 r + 2 t + 1 in the high ones.
-        const uint32_t e01 = __byte_perm(v[0][k], v[1][k], 0x5410), f01 = __byte_perm(v[0][k], v[1][k], 0x7632);
-        const uint32_t e23 = __byte_perm(v[2][k], v[3][k], 0x5410), f23 = __byte_perm(v[2][k], v[3][k], 0x7632);
-        auto tile = [&](float (&c)[4], const uint32_t (&y)[4], int n) {
-          Bf::mma(c, y, p[n][0][0], p[n][0][1]);
-          Bf::mma(c, y, p[n][1][0], p[n][1][1]);
-        };
-        const uint32_t y0[4] = {Bf::code<0>(e01), Bf::code<0>(f01), Bf::code<0>(e23), Bf::code<0>(f23)};
-        const uint32_t y1[4] = {Bf::code<1>(e01), Bf::code<1>(f01), Bf::code<1>(e23), Bf::code<1>(f23)};
-        const uint32_t y2[4] = {Bf::code<2>(e01), Bf::code<2>(f01), Bf::code<2>(e23), Bf::code<2>(f23)};
-        const uint32_t y3[4] = {Bf::code<3>(e01), Bf::code<3>(f01), Bf::code<3>(e23), Bf::code<3>(f23)};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          tile(o[n][4 * k], y0, n);
-          tile(o[n][4 * k + 1], y1, n);
-          tile(o[n][4 * k + 2], y2, n);
-          tile(o[n][4 * k + 3], y3, n);
-        }
-      }
-    }
-    __syncwarp();
-    if (lane == 0 && some) mbar_arrive(&bars->empty[s]);
-
-    const bool unit_ends = w.tile + 1 == w.s.n;
-    if (unit_ends || w.left <= 1) {
+    {
       // ------------------------------------------------ the unit's end here
-      const bool whole = unit_ends && unit_pos == 0;
+      const bool whole = w.tile == 0 && nt == w.s.n;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -570,58 +659,63 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
         float* to = buf + (warp * 8 + qc * 2) * D;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
+          // What O^T stands for: codes are (c - 8) 2^-7, weights s p grow.
           const int z = k / 4, d = (z * 64 + qr * 8 + (k & 3) * 2) ^ (qc * 2);
-          *reinterpret_cast<float2*>(to + d) = make_float2((o[n][k][0] + zs[n][z][0]) * f[0], (o[n][k][2] + zs[n][z][0]) * f[0]);
-          *reinterpret_cast<float2*>(to + D + d) = make_float2((o[n][k][1] + zs[n][z][1]) * f[1], (o[n][k][3] + zs[n][z][1]) * f[1]);
+          const float u = 128.f / grow[z];
+          *reinterpret_cast<float2*>(to + d) =
+              make_float2(fmaf(o[n][k][0], u, zs[n][z][0]) * f[0], fmaf(o[n][k][2], u, zs[n][z][0]) * f[0]);
+          *reinterpret_cast<float2*>(to + D + d) =
+              make_float2(fmaf(o[n][k][1], u, zs[n][z][1]) * f[1], fmaf(o[n][k][3], u, zs[n][z][1]) * f[1]);
         }
-        // A warp a head, two elements a lane.  The last read of ml before the
+        // Lane h < 8 of each warp sums head h.  The last read of ml before the
         // barrier: behind it a warp may be past its tiles of the next unit and
         // store that unit's (max, sum) while others still sum here.
-        const int hh = warp, h = h0 + n * 8 + hh;
         float M = kNone, L = 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, ml[i * 16 + n * 8 + hh].x);
+        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, ml[i * 16 + n * 8 + (lane & 7)].x);
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-          const float2 y = ml[i * 16 + n * 8 + hh];
+          const float2 y = ml[i * 16 + n * 8 + (lane & 7)];
           L += y.y * ex2(y.x - M);
         }
         consumer_sync();
-#pragma unroll
-        for (int k = 0; k < kG; ++k) {
-          const int d = k * 64 + lane * 2;
+        // A group of a head a warp at a time.
+        for (int i = warp; i < 8 * kG; i += kWarps) {
+          const int hh = i / kG, d = (i - hh * kG) * 64 + lane * 2, h = h0 + n * 8 + hh;
+          const float Mh = __shfl_sync(0xffffffffu, M, hh), Lh = __shfl_sync(0xffffffffu, L, hh);
           const float* from = buf + hh * D + (d ^ ((hh >> 1) * 2));
           float2 y = *reinterpret_cast<const float2*>(from);
 #pragma unroll
-          for (int i = 1; i < kWarps; ++i) {
-            const float2 z = *reinterpret_cast<const float2*>(from + i * 8 * D);
+          for (int u = 1; u < kWarps; ++u) {
+            const float2 z = *reinterpret_cast<const float2*>(from + u * 8 * D);
             y.x += z.x;
             y.y += z.y;
           }
           if constexpr (kCluster) {
             // For the join; the tiles have been read.
             *reinterpret_cast<float2*>(smem + ((n * 8 + hh) * D + d) * 4) = y;
-            if (d == 0) reinterpret_cast<float2*>(smem + kClusterMl<D>)[n * 8 + hh] = make_float2(M, L);
+            if (d == 0) reinterpret_cast<float2*>(smem + kClusterMl<D>)[n * 8 + hh] = make_float2(Mh, Lh);
           } else if (h < h1) {
             const long long row = (long long)w.b * a.Hq + h;
             if (whole) {
-              const float inv = 1.f / L;
+              const float inv = 1.f / Lh;
               *reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + row * D + d) = Tr::pack(y.x * inv, y.y * inv);
-              if (d == 0) a.lse[row] = (M + log2f(L)) * 0.69314718055994530942f;
+              if (d == 0) a.lse[row] = (Mh + log2f(Lh)) * 0.69314718055994530942f;
             } else {
               // Slot 1: the unit starts in this CTA and goes on; slot 0: it
               // started earlier.
-              const long long at = ((long long)blockIdx.x * 2 + (unit_pos == 0 ? 1 : 0)) * 16 + n * 8 + hh;
+              const long long at = ((long long)blockIdx.x * 2 + (w.tile == 0 ? 1 : 0)) * 16 + n * 8 + hh;
               *reinterpret_cast<float2*>(a.part + at * D + d) = y;
-              if (d == 0) a.part_ml[at] = make_float2(M, L);
+              if (d == 0) a.part_ml[at] = make_float2(Mh, Lh);
             }
           }
         }
       }
-      fresh = true;
     }
-    w.next(a, cols);
-  }
+    w.left -= nt;
+    w.tile += nt;
+    if (!kCluster && w.left > 0) w.next_unit(a, cols);
+  } while (!kCluster && w.left > 0);
   if constexpr (kCluster) {
     if (a.cluster > 1) cluster_sync();
     else consumer_sync();

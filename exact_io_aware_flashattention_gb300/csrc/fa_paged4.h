@@ -46,11 +46,24 @@ cudaError_t launch_norm_rope_bwd(int dtype, NormRopeBwdArgs a, const DevStatus& 
 // K codes [16][d/2], V codes [16][d/2], then (s, z) of K and of V, [16][d/64]
 // pairs of the call's type each.  A page's records follow one another.
 //   A row's codes are d/8 words of eight elements each, element e of a word in
-// bits 16 (e % 2) + 4 (e / 2) on: two neighbours lie in the same place of the
-// word's halves, where one mask makes a pair of matrix operands of them.  At d
+// place e / 2 of half e % 2: bits 9-6, bits 5-2, and these two with the half's
+// bytes swapped (so bits 1, 0, 15, 14 and 13-10).  Two neighbours lie in the same
+// place of the halves, where one mask makes a pair of fp16 numbers of them.  At d
 // = 128 word i of both groups stand side by side, at 8-byte chunk i ^ 4 ((slot /
 // 2) % 2): the lanes of a warp that read 8 bytes of four rows each, or 16 bytes
 // of eight rows, then meet all banks of shared memory alike.
+#ifdef __CUDACC__
+__device__ __forceinline__ uint32_t place_code(uint32_t c, int e) {
+  const int n = e >> 1;
+  const uint32_t h = n == 0 ? c << 6 : n == 1 ? c << 2 : n == 2 ? c >> 2 | (c & 3) << 14 : c << 10;
+  return h << (16 * (e & 1));
+}
+__device__ __forceinline__ uint32_t code_at(uint32_t w, int e) {
+  const int n = e >> 1;
+  const uint32_t h = w >> (16 * (e & 1));
+  return (n == 0 ? h >> 6 : n == 1 ? h >> 2 : n == 2 ? h << 2 | (h >> 14 & 3) : h >> 10) & 15u;
+}
+#endif
 template <int D>
 struct Record {
   static constexpr int kRow = D / 2;                 // bytes of a row's codes
@@ -82,7 +95,7 @@ struct Read4Args {
   int B, N;
 };
 
-constexpr int kDecode4TileKeys = 128;
+constexpr int kDecode4TileKeys = 112;
 // CTAs of the decode kernel that an SM holds, by the heads of a unit.
 constexpr int decode4_ctas_per_sm(int unit_heads) { return unit_heads == 8 ? 2 : 1; }
 
