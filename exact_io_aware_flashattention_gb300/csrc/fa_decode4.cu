@@ -45,22 +45,23 @@ namespace {
 constexpr int kWarps = 7;                          // consumers, one 16-key slice of a tile each
 constexpr int kConsumerThreads = kWarps * 32;
 constexpr int kThreads = kConsumerThreads + 32;
-constexpr int kKeys = 16 * kWarps;
 
 enum : int { kSiteFull = 54, kSiteEmpty = 55, kDrainFull = 56 };
 
-template <int D>
+// kSl slices of a tile a warp.
+template <int D, int kSl>
 struct Cfg {
-  static constexpr uint32_t kSlice = Record<D>::kBytes, kStage = kWarps * kSlice;
-  static constexpr int kStages = D == 128 ? 4 : 8;             // 74 KB in flight
-  static constexpr uint32_t kBuf = kStages * kStage;           // [8 warps][8 heads][D] fp32, one head group
-  static constexpr uint32_t kMl = kBuf + kWarps * 8u * D * 4u; // [8 warps][16 heads] (max, sum)
+  static constexpr int kSlices = kSl * kWarps, kKeys = 16 * kSlices;
+  static constexpr uint32_t kSlice = Record<D>::kBytes, kStage = kSlices * kSlice;
+  static constexpr int kStages = 6 * 128 / D / kSl;            // 97 KB in flight
+  static constexpr uint32_t kBuf = kStages * kStage;           // [kWarps][8 heads][64] fp32, a head group of a group
+  static constexpr uint32_t kMl = kBuf + kWarps * 8u * 64u * 4u;     // [kWarps][16 heads] (max, sum)
   static constexpr uint32_t kBar = kMl + kWarps * 16u * 8u;
   static constexpr uint32_t kBytes = kBar + 256u;
 };
 
 struct Bars {
-  uint64_t full[8], empty[8];
+  uint64_t full[12], empty[12];
   int abort;
   int scan[kThreads / 32];
   int b0;                    // first sequence of this CTA's part
@@ -117,10 +118,10 @@ __device__ __forceinline__ uint32_t centred(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t swapped(uint32_t w) { return __byte_perm(w, w, 0x2301); }
 
-template <typename T_, int D_>
+template <typename T_, int D_, int kSl>
 struct Traits {
   using T = T_;
-  static constexpr int D = D_, kKeys = 16 * kWarps, kJoinThreads = kConsumerThreads;
+  static constexpr int D = D_, kKeys = Cfg<D_, kSl>::kKeys, kJoinThreads = kConsumerThreads;
   static constexpr float kShift = 0.f;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return Type<T>::pack(lo, hi); }
 };
@@ -214,7 +215,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
 // weights against the running maximum m and, in l, zs and o, their sums.
 template <typename T, int D, int NT>
 __device__ __forceinline__ void slice(const uint8_t* rec, int key0, const Span& s, uint32_t k_at, uint32_t v_at, uint32_t kp_at,
-                                      uint32_t vp_at, int ka, float sl2, float by, const uint4 (&q)[NT][D / 64][2],
+                                      uint32_t vp_at, int ka, float by, const uint4 (&q)[NT][D / 64][2],
                                       const float (&qs)[NT][D / 64][2], float (&o)[NT][D / 16][4], float (&zs)[NT][D / 64][2],
                                       float (&m)[NT][2], float (&l)[NT][2], float (&grow)[D / 64]) {
   constexpr int kG = D / 64;
@@ -253,13 +254,13 @@ __device__ __forceinline__ void slice(const uint8_t* rec, int key0, const Span& 
       }
 #pragma unroll
     for (int k = 0; k < kG; ++k) {
-      const float sa = pa[k].x * by, za = pa[k].y * sl2, sb = pb[k].x * by, zb = pb[k].y * sl2;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[n][e] = fmaf(c[n][k][e], e < 2 ? sa : sb,
-                         k == 0 ? qs[n][k][e & 1] * (e < 2 ? za : zb) : fmaf(qs[n][k][e & 1], e < 2 ? za : zb, x[n][e]));
+        for (int e = 0; e < 4; ++e) {
+          const float2& y = e < 2 ? pa[k] : pb[k];
+          x[n][e] = fmaf(c[n][k][e], y.x, k == 0 ? qs[n][k][e & 1] * y.y : fmaf(qs[n][k][e & 1], y.y, x[n][e]));
+        }
     }
   }
   load_pars<T, D>(rec + vp_at, pa);
@@ -282,7 +283,7 @@ __device__ __forceinline__ void slice(const uint8_t* rec, int key0, const Span& 
   bool more = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
-    more |= fmaxf(x[n][0], x[n][2]) > m[n][0] + 8.f || fmaxf(x[n][1], x[n][3]) > m[n][1] + 8.f;
+    more |= fmaxf(x[n][0], x[n][2]) * by > m[n][0] + 8.f || fmaxf(x[n][1], x[n][3]) * by > m[n][1] + 8.f;
 #pragma unroll
   for (int k = 0; k < kG; ++k) more |= fmaxf(pa[k].x, pb[k].x) * grow[k] >= 128.f;
   if (__any_sync(0xffffffffu, more)) {
@@ -295,7 +296,7 @@ __device__ __forceinline__ void slice(const uint8_t* rec, int key0, const Span& 
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
       }
-      const float n0 = fmaxf(m[n][0], mx0), n1 = fmaxf(m[n][1], mx1);
+      const float n0 = fmaxf(m[n][0], mx0 * by), n1 = fmaxf(m[n][1], mx1 * by);
       const float f0 = ex2(m[n][0] - n0), f1 = ex2(m[n][1] - n1);
       m[n][0] = n0;
       m[n][1] = n1;
@@ -334,10 +335,10 @@ __device__ __forceinline__ void slice(const uint8_t* rec, int key0, const Span& 
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    x[n][0] = ex2(x[n][0] - m[n][0]);
-    x[n][1] = ex2(x[n][1] - m[n][1]);
-    x[n][2] = ex2(x[n][2] - m[n][0]);
-    x[n][3] = ex2(x[n][3] - m[n][1]);
+    x[n][0] = ex2(fmaf(x[n][0], by, -m[n][0]));
+    x[n][1] = ex2(fmaf(x[n][1], by, -m[n][1]));
+    x[n][2] = ex2(fmaf(x[n][2], by, -m[n][0]));
+    x[n][3] = ex2(fmaf(x[n][3], by, -m[n][1]));
     l[n][0] += x[n][0] + x[n][2];
     l[n][1] += x[n][1] + x[n][3];
   }
@@ -395,10 +396,11 @@ __device__ __forceinline__ void slice(const uint8_t* rec, int key0, const Span& 
   }
 }
 
-template <typename T, int D, int NT, bool kCluster>
+template <typename T, int D, int NT, int kSl, bool kCluster>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(const DecodeArgs a, const DevStatus st) {
-  using C = Cfg<D>;
-  using Tr = Traits<T, D>;
+  using C = Cfg<D, kSl>;
+  using Tr = Traits<T, D, kSl>;
+  constexpr int kKeys = C::kKeys;
   constexpr int kG = D / 64;
   extern __shared__ __align__(128) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kBar);
@@ -486,10 +488,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
-    // Lane l looks up slice l % kWarps of tile l / kWarps of the unit's next tiles,
-    // one run ahead of the copies; lanes below kWarps issue a slice's copy each.
-    constexpr int kAhead = 32 / kWarps;
-    const int my_slice = lane % kWarps, my_tile = lane / kWarps;
+    // Lane l looks up slice l % kSlices of tile l / kSlices of the unit's next tiles,
+    // one run ahead of the copies; lanes below kSlices issue a slice's copy each.
+    constexpr int kAhead = 32 / C::kSlices;
+    const int my_slice = lane % C::kSlices, my_tile = lane / C::kSlices;
     auto look_up = [&](const Walk<kKeys>& x, int& page, int& slot) {
       const int have = (int)min((long long)min(x.s.n - x.tile, kAhead), x.left);
       const int key0 = (x.s.tile0 + x.tile + my_tile) * kKeys + my_slice * 16;
@@ -528,14 +530,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
           good = false;
           break;
         }
-        const int p = __shfl_sync(0xffffffffu, page, i * kWarps + my_slice);
-        const int sl = __shfl_sync(0xffffffffu, slot, i * kWarps + my_slice);
-        const uint32_t mask = __ballot_sync(0xffffffffu, sl >= 0) & ((1u << kWarps) - 1);
+        const int p = __shfl_sync(0xffffffffu, page, i * C::kSlices + my_slice);
+        const int sl = __shfl_sync(0xffffffffu, slot, i * C::kSlices + my_slice);
+        const uint32_t mask = __ballot_sync(0xffffffffu, sl >= 0) & ((1u << C::kSlices) - 1);
         if (lane == 0) {
           mbar_arrive_expect_tx(&bars->full[s], __popc(mask) * C::kSlice);
         }
         __syncwarp();
-        if (lane < kWarps && sl >= 0)
+        if (lane < C::kSlices && sl >= 0)
           bulk_load(smem_u32(smem) + s * C::kStage + lane * C::kSlice,
                     base + p * a.kv.s_page + (long long)(sl >> 4) * C::kSlice, C::kSlice, &bars->full[s]);
       }
@@ -592,7 +594,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
     h0 = g * G + (w.col - g * chunks) * 8 * NT;
     h1 = (g + 1) * G;
     load_q<T, D, NT>(a, w.b, w.col, chunks, q, qs, by);
-    by = sl2 * 0x1p18f / by;
+    by = sl2 * 0x1p18f / by;                      // x in slice() is in units of log2 / by
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < kG; ++k) {
+        qs[n][k][0] *= sl2 / by;
+        qs[n][k][1] *= sl2 / by;
+      }
 #pragma unroll
     for (int k = 0; k < kG; ++k) grow[k] = 0x1p107f;
 #pragma unroll
@@ -613,8 +622,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
       if (!dead && !wait_warp(&bars->full[stage], phase, st, abort_flag, kSiteFull)) dead = true;
       // (A slice whose page number is out of range was not loaded: what lies
       // there is worked on, and its sequence's outputs are unspecified.)
-      if (!dead && key0 < w.s.len && key0 + 16 > w.s.first)
-        slice<T, D, NT>(mine + stage * C::kStage, key0, w.s, k_at, v_at, kp_at, vp_at, ka, sl2, by, q, qs, o, zs, m, l, grow);
+#pragma unroll 1
+      for (int u = 0; u < kSl; ++u) {
+        const int key = key0 + u * kWarps * 16;
+        if (!dead && key < w.s.len && key + 16 > w.s.first)
+          slice<T, D, NT>(mine + stage * C::kStage + u * kWarps * C::kSlice, key, w.s, k_at, v_at, kp_at, vp_at, ka, by, q, qs, o,
+                          zs, m, l, grow);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->empty[stage]);
       if (++stage == C::kStages) {
@@ -645,7 +659,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
       consumer_sync();
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (n > 0) consumer_sync();                // the buffer's last readers
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -654,21 +667,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
           for (int i = 0; i < kWarps; ++i) M = fmaxf(M, ml[i * 16 + n * 8 + qc * 2 + e].x);
           f[e] = ex2(m[n][e] - M);
         }
-        // [warp][head][d], d xor 2 (head / 2): the four rows and four column pairs
-        // that half a warp stores at once fall on 32 banks.
-        float* to = buf + (warp * 8 + qc * 2) * D;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          // What O^T stands for: codes are (c - 8) 2^-7, weights s p grow.
-          const int z = k / 4, d = (z * 64 + qr * 8 + (k & 3) * 2) ^ (qc * 2);
-          const float u = 128.f / grow[z];
-          *reinterpret_cast<float2*>(to + d) =
-              make_float2(fmaf(o[n][k][0], u, zs[n][z][0]) * f[0], fmaf(o[n][k][2], u, zs[n][z][0]) * f[0]);
-          *reinterpret_cast<float2*>(to + D + d) =
-              make_float2(fmaf(o[n][k][1], u, zs[n][z][1]) * f[1], fmaf(o[n][k][3], u, zs[n][z][1]) * f[1]);
-        }
-        // Lane h < 8 of each warp sums head h.  The last read of ml before the
-        // barrier: behind it a warp may be past its tiles of the next unit and
+        // Lane h < 8 of each warp sums head h.  The last reads of ml are before the
+        // last barrier: behind it a warp may be past its tiles of the next unit and
         // store that unit's (max, sum) while others still sum here.
         float M = kNone, L = 0.f;
 #pragma unroll
@@ -678,35 +678,51 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
           const float2 y = ml[i * 16 + n * 8 + (lane & 7)];
           L += y.y * ex2(y.x - M);
         }
-        consumer_sync();
-        // A group of a head a warp at a time.
-        for (int i = warp; i < 8 * kG; i += kWarps) {
-          const int hh = i / kG, d = (i - hh * kG) * 64 + lane * 2, h = h0 + n * 8 + hh;
-          const float Mh = __shfl_sync(0xffffffffu, M, hh), Lh = __shfl_sync(0xffffffffu, L, hh);
-          const float* from = buf + hh * D + (d ^ ((hh >> 1) * 2));
-          float2 y = *reinterpret_cast<const float2*>(from);
 #pragma unroll
-          for (int u = 1; u < kWarps; ++u) {
-            const float2 z = *reinterpret_cast<const float2*>(from + u * 8 * D);
-            y.x += z.x;
-            y.y += z.y;
+        for (int k = 0; k < kG; ++k) {
+          if (n + k > 0) consumer_sync();          // the buffer's last readers
+          // [warp][head][element of the group], this xor 2 (head / 2): the four rows and
+          // four column pairs that half a warp stores at once fall on 32 banks.
+          float* to = buf + (warp * 8 + qc * 2) * 64;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // What O^T stands for: codes are (c - 8) 2^-7, weights s p grow.
+            const int d = (qr * 8 + i * 2) ^ (qc * 2);
+            const float u = 128.f / grow[k];
+            const float (&c)[4] = o[n][4 * k + i];
+            *reinterpret_cast<float2*>(to + d) = make_float2(fmaf(c[0], u, zs[n][k][0]) * f[0], fmaf(c[2], u, zs[n][k][0]) * f[0]);
+            *reinterpret_cast<float2*>(to + 64 + d) =
+                make_float2(fmaf(c[1], u, zs[n][k][1]) * f[1], fmaf(c[3], u, zs[n][k][1]) * f[1]);
           }
-          if constexpr (kCluster) {
-            // For the join; the tiles have been read.
-            *reinterpret_cast<float2*>(smem + ((n * 8 + hh) * D + d) * 4) = y;
-            if (d == 0) reinterpret_cast<float2*>(smem + kClusterMl<D>)[n * 8 + hh] = make_float2(Mh, Lh);
-          } else if (h < h1) {
-            const long long row = (long long)w.b * a.Hq + h;
-            if (whole) {
-              const float inv = 1.f / Lh;
-              *reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + row * D + d) = Tr::pack(y.x * inv, y.y * inv);
-              if (d == 0) a.lse[row] = (Mh + log2f(Lh)) * 0.69314718055994530942f;
-            } else {
-              // Slot 1: the unit starts in this CTA and goes on; slot 0: it
-              // started earlier.
-              const long long at = ((long long)blockIdx.x * 2 + (w.tile == 0 ? 1 : 0)) * 16 + n * 8 + hh;
-              *reinterpret_cast<float2*>(a.part + at * D + d) = y;
-              if (d == 0) a.part_ml[at] = make_float2(Mh, Lh);
+          consumer_sync();
+          for (int hh = warp; hh < 8; hh += kWarps) {            // a head a warp at a time
+            const int e = lane * 2, d = k * 64 + e, h = h0 + n * 8 + hh;
+            const float Mh = __shfl_sync(0xffffffffu, M, hh), Lh = __shfl_sync(0xffffffffu, L, hh);
+            const float* from = buf + hh * 64 + (e ^ ((hh >> 1) * 2));
+            float2 y = *reinterpret_cast<const float2*>(from);
+#pragma unroll
+            for (int u = 1; u < kWarps; ++u) {
+              const float2 z = *reinterpret_cast<const float2*>(from + u * 8 * 64);
+              y.x += z.x;
+              y.y += z.y;
+            }
+            if constexpr (kCluster) {
+              // For the join; the tiles have been read.
+              *reinterpret_cast<float2*>(smem + ((n * 8 + hh) * D + d) * 4) = y;
+              if (d == 0) reinterpret_cast<float2*>(smem + kClusterMl<D>)[n * 8 + hh] = make_float2(Mh, Lh);
+            } else if (h < h1) {
+              const long long row = (long long)w.b * a.Hq + h;
+              if (whole) {
+                const float inv = 1.f / Lh;
+                *reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + row * D + d) = Tr::pack(y.x * inv, y.y * inv);
+                if (d == 0) a.lse[row] = (Mh + log2f(Lh)) * 0.69314718055994530942f;
+              } else {
+                // Slot 1: the unit starts in this CTA and goes on; slot 0: it
+                // started earlier.
+                const long long at = ((long long)blockIdx.x * 2 + (w.tile == 0 ? 1 : 0)) * 16 + n * 8 + hh;
+                *reinterpret_cast<float2*>(a.part + at * D + d) = y;
+                if (d == 0) a.part_ml[at] = make_float2(Mh, Lh);
+              }
             }
           }
         }
@@ -729,16 +745,20 @@ template <typename T, int D>
 __global__ void __launch_bounds__(128) fa_decode4_join_kernel(const DecodeArgs a) {
   launch_dependents();
   wait_for_previous();
-  join<Traits<T, D>>(a);
+  join<Traits<T, D, 1>>(a);
 }
+
+// Slices of a tile a warp: one where a cluster shares few tiles.
+constexpr int kShort = kDecode4ClusterKeys / 16 / kWarps, kLong = kDecode4TileKeys / 16 / kWarps;
 
 template <typename T, int D>
 cudaError_t launch(const DecodeArgs& a, const DevStatus& st, int parts, cudaStream_t stream) {
   if (a.cluster)
-    return launch_after(a.unit_heads == 8 ? fa_decode4_kernel<T, D, 1, true> : fa_decode4_kernel<T, D, 2, true>, parts,
-                        kThreads, Cfg<D>::kBytes, a.cluster, stream, a, st);
-  cudaError_t e = launch_after(a.unit_heads == 8 ? fa_decode4_kernel<T, D, 1, false> : fa_decode4_kernel<T, D, 2, false>,
-                               parts, kThreads, Cfg<D>::kBytes, 1, stream, a, st);
+    return launch_after(a.unit_heads == 8 ? fa_decode4_kernel<T, D, 1, kShort, true> : fa_decode4_kernel<T, D, 2, kShort, true>,
+                        parts, kThreads, Cfg<D, kShort>::kBytes, a.cluster, stream, a, st);
+  cudaError_t e =
+      launch_after(a.unit_heads == 8 ? fa_decode4_kernel<T, D, 1, kLong, false> : fa_decode4_kernel<T, D, 2, kLong, false>, parts,
+                   kThreads, Cfg<D, kLong>::kBytes, 1, stream, a, st);
   const int joins = (parts - 1) * (a.unit_heads / 4);
   if (e == cudaSuccess && joins > 0) e = launch_after(fa_decode4_join_kernel<T, D>, joins, 128, 0, 1, stream, a);
   return e;
@@ -746,12 +766,13 @@ cudaError_t launch(const DecodeArgs& a, const DevStatus& st, int parts, cudaStre
 
 template <typename T, int D>
 cudaError_t configure() {
-  static_assert(Cfg<D>::kBytes <= 115712, "two CTAs per SM");
-  static_assert(kKeys == kDecode4TileKeys, "tile");
+  static_assert(Cfg<D, kShort>::kBytes <= 115712 && Cfg<D, kLong>::kBytes <= 115712, "two CTAs per SM");
+  static_assert(Cfg<D, kShort>::kKeys == kDecode4ClusterKeys && Cfg<D, kLong>::kKeys == kDecode4TileKeys, "tile");
   cudaError_t e = cudaSuccess;
-  for (auto k : {fa_decode4_kernel<T, D, 1, false>, fa_decode4_kernel<T, D, 2, false>, fa_decode4_kernel<T, D, 1, true>,
-                 fa_decode4_kernel<T, D, 2, true>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kBytes);
+  for (auto k : {fa_decode4_kernel<T, D, 1, kShort, true>, fa_decode4_kernel<T, D, 2, kShort, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, kShort>::kBytes);
+  for (auto k : {fa_decode4_kernel<T, D, 1, kLong, false>, fa_decode4_kernel<T, D, 2, kLong, false>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, kLong>::kBytes);
   if (e == cudaSuccess) e = preload_kernel(fa_decode4_join_kernel<T, D>);
   return e;
 }

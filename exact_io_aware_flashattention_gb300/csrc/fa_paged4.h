@@ -95,7 +95,8 @@ struct Read4Args {
   int B, N;
 };
 
-constexpr int kDecode4TileKeys = 112;
+// Keys of a tile: where equal parts of the line are taken, and by clusters.
+constexpr int kDecode4TileKeys = 224, kDecode4ClusterKeys = 112;
 // CTAs of the decode kernel that an SM holds, by the heads of a unit.
 constexpr int decode4_ctas_per_sm(int unit_heads) { return unit_heads == 8 ? 2 : 1; }
 
