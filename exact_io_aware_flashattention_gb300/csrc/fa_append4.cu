@@ -37,22 +37,32 @@ __device__ __forceinline__ float round_to(float x) {
   return Pair2<T>::up(Pair2<T>::down(x, 0.f)).x;
 }
 
-// Codes of eight elements in a word (see Record).
+// Codes of eight elements, in the two halves of K's word or in V's two halves.
+template <bool kKeys>
 __device__ __forceinline__ uint32_t encode8(const float (&x)[8], float s, float z) {
   uint32_t w = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int c = __float2int_rn(__fdiv_rn(__fsub_rn(x[e], z), s));
-    w |= place_code((uint32_t)min(max(c, 0), 15), e);
+    w |= place_code((uint32_t)min(max(c, 0), 15), kKeys ? e / 2 : e % 4) << 16 * (kKeys ? e % 2 : e / 4);
   }
   return s == 0.f ? 0u : w;
 }
+template <int D, bool kKeys>
+__device__ __forceinline__ void store_codes(uint8_t* rec, int slot, int i, uint32_t w) {
+  if constexpr (kKeys) {
+    *reinterpret_cast<uint32_t*>(rec + Record<D>::k_word(slot, i)) = w;
+  } else {
+    *reinterpret_cast<uint16_t*>(rec + Record<D>::v_half(slot, i, 0)) = (uint16_t)w;
+    *reinterpret_cast<uint16_t*>(rec + Record<D>::v_half(slot, i, 1)) = (uint16_t)(w >> 16);
+  }
+}
 
-// One row of K or V, 16 elements a thread, into its record: codes at `codes`, (s,
-// z) at `par`.  All lanes of a row take part.
-template <typename T, int D>
-__device__ __forceinline__ void store_row(const float (&xa)[8], const float (&xb)[8], const Chunk& ck, uint8_t* codes,
-                                          uint8_t* par, int slot, int c, bool live) {
+// One row of K or V, 16 elements a thread, into its record.  All lanes of a row
+// take part.
+template <typename T, int D, bool kKeys>
+__device__ __forceinline__ void store_row(const float (&xa)[8], const float (&xb)[8], const Chunk& ck, uint8_t* rec, int slot, int c,
+                                          bool live) {
   constexpr int kGroups = D / 64;
   const int ga = ck.e0 / 64, gb = ck.e1 / 64;
   float lo[kGroups], hi[kGroups];
@@ -84,9 +94,10 @@ __device__ __forceinline__ void store_row(const float (&xa)[8], const float (&xb
   if (!live) return;
   const float sa = kGroups == 1 || ga == 0 ? s[0] : s[kGroups - 1], za = kGroups == 1 || ga == 0 ? lo[0] : lo[kGroups - 1];
   const float sb = kGroups == 1 || gb == 0 ? s[0] : s[kGroups - 1], zb = kGroups == 1 || gb == 0 ? lo[0] : lo[kGroups - 1];
-  *reinterpret_cast<uint32_t*>(codes + Record<D>::word(slot, ck.e0 / 8)) = encode8(xa, sa, za);
-  *reinterpret_cast<uint32_t*>(codes + Record<D>::word(slot, ck.e1 / 8)) = encode8(xb, sb, zb);
+  store_codes<D, kKeys>(rec, slot, ck.e0 / 8, encode8<kKeys>(xa, sa, za));
+  store_codes<D, kKeys>(rec, slot, ck.e1 / 8, encode8<kKeys>(xb, sb, zb));
   if (c == 0) {
+    uint8_t* par = rec + (kKeys ? Record<D>::kKp : Record<D>::kVp);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) reinterpret_cast<uint32_t*>(par + slot * Record<D>::kPar)[g] = p[g];
   }
@@ -157,8 +168,8 @@ __global__ void __launch_bounds__(kThreads) fa_append4_kernel(const Append4Args 
         up8<T>(va, xa);
         up8<T>(vb, xb);
         uint8_t* rec = at + h * a.kv.s_head;
-        store_row<T, D>(xa, xb, my, rec + (part == 2 ? Record<D>::kV : 0), rec + (part == 2 ? Record<D>::kVp : Record<D>::kKp),
-                        slot & 15, c, live);
+        if (part == 1) store_row<T, D, true>(xa, xb, my, rec, slot & 15, c, live);
+        else store_row<T, D, false>(xa, xb, my, rec, slot & 15, c, live);
       }
     }
   }
@@ -188,12 +199,14 @@ __global__ void __launch_bounds__(kThreads) fa_read4_kernel(const Read4Args a, c
         const int s = slot & 15, g = i / 8;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + (kv ? Record<D>::kV : 0) + Record<D>::word(s, i));
+          const uint32_t h0 = kv ? *reinterpret_cast<const uint16_t*>(rec + Record<D>::v_half(s, i, 0))
+                                 : *reinterpret_cast<const uint32_t*>(rec + Record<D>::k_word(s, i));
+          const uint32_t h1 = kv ? *reinterpret_cast<const uint16_t*>(rec + Record<D>::v_half(s, i, 1)) : h0 >> 16;
           const float2 p = Pair2<T>::up(
               reinterpret_cast<const uint32_t*>(rec + (kv ? Record<D>::kVp : Record<D>::kKp) + s * Record<D>::kPar)[g]);
           float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = p.y + p.x * (float)code_at(w, e);
+          for (int e = 0; e < 8; ++e) x[e] = p.y + p.x * (float)(kv ? code_at(e < 4 ? h0 : h1, e % 4) : code_at(e % 2 ? h1 : h0, e / 2));
           (kv ? v : k) = down8<T>(x);
         }
       }

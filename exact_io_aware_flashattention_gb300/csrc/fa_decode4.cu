@@ -5,14 +5,16 @@
 // Every code enters the matrix products as it is, s and z are applied in fp32
 // outside: with Q_g the sum of q over group g,
 //   q . k_j = sum over g of s_jg sum_i q_i c_ji + z_jg Q_g,
-//   o = sum_j (s_j p_j) (c_j - 8) + sum_j p_j (z_j + 8 s_j),
+//   o = sum_j (s_j p_j) (c_j - 7.5) + sum_j p_j (z_j + 7.5 s_j),
 // the last sum one number a head and group.  Four bits in the upper or the next
 // mantissa bits of an fp16 number with exponent 0 are the subnormal c 2^-18 or c
 // 2^-22: one AND for a pair of codes (and two bytes swapped give the other half of
-// a word).  So they enter for K; for V one multiply-add makes both (c - 8) 2^-7:
-// the tensor pipe cuts its sums instead of rounding them, which adds up over
-// many keys where all terms have one sign (with c, o was 1.2 times, with 1 + c /
-// 16 2.8 times as far off at 32768 keys).
+// a word).  -7.5 times the sum of the weights, the same for all elements of a
+// group, is formed by one product more and is what the others start from.  The
+// tensor pipe cuts its sums instead of rounding them, which adds up over many
+// keys; so products with V are summed over a tile's two slices only, and those
+// sums added in fp32 (as running sums of the pipe, and of c, o was 1.2 times as far
+// off at 32768 keys).
 //   q, whatever its type, enters in fp16 times a power of two that brings a
 // unit's largest element to 2^10 (16 times that for the codes held as c 2^-22):
 // exact but for elements 2^-24 times smaller than the largest.  The weights s p
@@ -26,9 +28,8 @@
 // producer, warps 0-6 own a slice of each tile each.  Products by mma.sync
 // (m16n8k16) with keys, then elements of d as rows and 8 heads as columns: see
 // fa_paged.cu.  Row i of a slice's S^T is the key (i % 8) / 2 + 4 (i % 2) + 8 (i / 8),
-// so that the lanes that read the pairs of keys of V from shared memory, four
-// keys a lane, meet all banks; O^T's rows are the elements 8 r + 2 n + h of a group
-// (lane row r, tile n, row half h).
+// the pairs of keys that a word of V holds (fa_paged4.h); O^T's rows are the
+// elements 8 r + t and 8 r + 4 + t of a group (lane row r, tile t).
 //   A running maximum that is behind by less than 2^8 is as good as the exact
 // one (weights up to 2^8, sums in fp32): the warp then neither exchanges maxima
 // nor rescales.
@@ -57,7 +58,8 @@ struct Cfg {
   static constexpr uint32_t kBuf = kStages * kStage;           // [kWarps][8 heads][64] fp32, a head group of a group
   static constexpr uint32_t kMl = kBuf + kWarps * 8u * 64u * 4u;     // [kWarps][16 heads] (max, sum)
   static constexpr uint32_t kBar = kMl + kWarps * 16u * 8u;
-  static constexpr uint32_t kBytes = kBar + 256u;
+  static constexpr uint32_t kQ = kBar + 256u;                  // the unit's query rows as operands
+  static constexpr uint32_t bytes(int NT) { return kQ + NT * D * 16u; }
 };
 
 struct Bars {
@@ -97,25 +99,19 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
+// The same starting from c0 in the columns' first, c1 in their second.
+__device__ __forceinline__ void mma_from(float (&c)[4], float c0, float c1, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
+      "{%10, %11, %10, %11};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 // Codes of two halves as c 2^-18 (of places 0 and 2) and c 2^-22 (1 and 3); places 2
 // and 3 after the halves' bytes are swapped.
 __device__ __forceinline__ uint32_t upper(uint32_t w) { return w & 0x03c003c0u; }
 __device__ __forceinline__ uint32_t lower(uint32_t w) { return w & 0x003c003cu; }
-// Either as (c - 8) 2^-7.
-template <bool kLower>
-__device__ __forceinline__ uint32_t centred(uint32_t x) {
-  uint32_t y;                                     // x 2^11 - 2^-4, or x 2^15 - 2^-4
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(kLower ? 0x78007800u : 0x68006800u), "r"(0xac00ac00u));
-  return y;
-}
 __device__ __forceinline__ uint32_t swapped(uint32_t w) { return __byte_perm(w, w, 0x2301); }
 
 template <typename T_, int D_, int kSl>
@@ -150,16 +146,16 @@ __device__ __forceinline__ void load_pars(const uint8_t* p, float2 (&x)[D / 64])
   }
 }
 
-// Query rows of unit (b, col) as B operands, column = head lane / 4: q[n][g][w] the
-// eight elements 64 g + 16 (lane % 4) + 8 w on, times `times` and, the odd pairs,
-// 16; and sums[n][g], those over the groups for the heads 2 (lane % 4) and the
+// Query rows of unit (b, col) as B operands, column = head lane / 4: at to[n][g][w] of
+// each lane (if `to`) the eight elements 64 g + 16 (lane % 4) + 8 w on, times `times`
+// and, the odd pairs, 16; and sums[n][g], those over the groups for the heads 2 (lane % 4) and the
 // next, this lane's columns of S^T.
 template <typename T, int D, int NT>
-__device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int col, int chunks, uint4 (&q)[NT][D / 64][2],
-                                       float (&sums)[NT][D / 64][2], float& times) {
+__device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int col, int chunks, uint4* to, float (&sums)[NT][D / 64][2], float& times) {
   const int lane = threadIdx.x & 31, G = a.Hq / a.kv.Hkv;
   const int g = col / chunks, h0 = g * G + (col - g * chunks) * 8 * NT + (lane >> 2), h1 = (g + 1) * G;
   const T* p = static_cast<const T*>(a.q) + b * a.q_sb + (lane & 3) * 16;
+  uint4 q[NT][D / 64][2];
   float top = 0.f;                                // the largest finite |q|
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -196,9 +192,9 @@ __device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int col, int 
     for (int k = 0; k < D / 64; ++k)
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        uint4& v = q[n][k][w];
+        const uint4 v = q[n][k][w];
         const float2 y0 = Type<T>::up(v.x), y1 = Type<T>::up(v.y), y2 = Type<T>::up(v.z), y3 = Type<T>::up(v.w);
-        v = make_uint4(Half::pack(y0.x * times, y0.y * times), Half::pack(y1.x * more, y1.y * more),
+        if (to) to[((n * (D / 64) + k) * 2 + w) * 32 + lane] = make_uint4(Half::pack(y0.x * times, y0.y * times), Half::pack(y1.x * more, y1.y * more),
                        Half::pack(y2.x * times, y2.y * times), Half::pack(y3.x * more, y3.y * more));
       }
 }
@@ -211,186 +207,236 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
   return mbar_wait_warp(bar, parity, st, abort, site);
 }
 
-// A warp's work on one slice, the record rec of the 16 keys from key0 on: S^T, its
-// weights against the running maximum m and, in l, zs and o, their sums.
-template <typename T, int D, int NT>
-__device__ __forceinline__ void slice(const uint8_t* rec, int key0, const Span& s, uint32_t k_at, uint32_t v_at, uint32_t kp_at,
-                                      uint32_t vp_at, int ka, float by, const uint4 (&q)[NT][D / 64][2],
-                                      const float (&qs)[NT][D / 64][2], float (&o)[NT][D / 16][4], float (&zs)[NT][D / 64][2],
-                                      float (&m)[NT][2], float (&l)[NT][2], float (&grow)[D / 64]) {
-  constexpr int kG = D / 64;
-  constexpr int kW = Type<T>::kWeights;
-  const bool edge = key0 < s.first || key0 + 16 > s.len;
-  // Scores: S^T rows ka, ka + 8, columns 2 qc, 2 qc + 1.
-  float x[NT][4];
-  float2 pa[kG], pb[kG];
-  load_pars<T, D>(rec + kp_at, pa);
-  load_pars<T, D>(rec + kp_at + 8 * Record<D>::kPar, pb);
-  uint32_t wa[kG][2], wb[kG][2];
-  if constexpr (D == 128) {
-    const uint4 ya = *reinterpret_cast<const uint4*>(rec + k_at);
-    const uint4 yb = *reinterpret_cast<const uint4*>(rec + k_at + 8 * Record<D>::kRow);
-    wa[0][0] = ya.x, wa[1][0] = ya.y, wa[0][1] = ya.z, wa[1][1] = ya.w;
-    wb[0][0] = yb.x, wb[1][0] = yb.y, wb[0][1] = yb.z, wb[1][1] = yb.w;
-  } else {
-    const uint2 ya = *reinterpret_cast<const uint2*>(rec + k_at);
-    const uint2 yb = *reinterpret_cast<const uint2*>(rec + k_at + 8 * Record<D>::kRow);
-    wa[0][0] = ya.x, wa[0][1] = ya.y, wb[0][0] = yb.x, wb[0][1] = yb.y;
-  }
+// A warp's work on its kSl slices of a tile, records kStep bytes and kGap keys apart,
+// rec the first, of the 16 keys from key0 on: S^T, its weights against the running
+// maximum m and, in l, zs and o, their sums.
+template <typename T, int D, int NT, int kSl, int kStep, int kGap>
+__device__ __forceinline__ void work(const uint8_t* rec, int key0, const Span& s, uint32_t k_at, uint32_t v_at, uint32_t kp_at,
+                                     uint32_t vp_at, int ka, float by, const uint4* q,
+                                     const float (&qs)[NT][D / 64][2], float (&o)[NT][D / 16][4], float (&zs)[NT][D / 64][2],
+                                     float (&m)[NT][2], float (&l)[NT][2], float (&grow)[D / 64]) {
+  constexpr int kG = D / 64, kW = Type<T>::kWeights;
+  // Scores, in units of log2 / by: S^T rows ka, ka + 8, columns 2 qc, 2 qc + 1.
+  float x[kSl][NT][4];
   {
-    float c[NT][kG][4];
+    uint32_t wa[kSl][kG][2], wb[kSl][kG][2];
+    float c[kSl][NT][kG][4];
+#pragma unroll
+    for (int j = 0; j < kSl; ++j) {
+      const uint8_t* r = rec + j * kStep;
+      if constexpr (D == 128) {
+        const uint4 ya = *reinterpret_cast<const uint4*>(r + k_at);
+        const uint4 yb = *reinterpret_cast<const uint4*>(r + k_at + 8 * Record<D>::kRow);
+        wa[j][0][0] = ya.x, wa[j][1][0] = ya.y, wa[j][0][1] = ya.z, wa[j][1][1] = ya.w;
+        wb[j][0][0] = yb.x, wb[j][1][0] = yb.y, wb[j][0][1] = yb.z, wb[j][1][1] = yb.w;
+      } else {
+        const uint2 ya = *reinterpret_cast<const uint2*>(r + k_at);
+        const uint2 yb = *reinterpret_cast<const uint2*>(r + k_at + 8 * Record<D>::kRow);
+        wa[j][0][0] = ya.x, wa[j][0][1] = ya.y, wb[j][0][0] = yb.x, wb[j][0][1] = yb.y;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int k = 0; k < kG; ++k) {
-        const uint32_t y = wa[k][u], z = wb[k][u], ys = swapped(y), zs_ = swapped(z);
-        const uint32_t f[8] = {upper(y), upper(z), lower(y), lower(z), upper(ys), upper(zs_), lower(ys), lower(zs_)};
+      for (int k = 0; k < kG; ++k)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          if (u == 0) mma_first(c[n][k], f[0], f[1], f[2], f[3], q[n][k][u].x, q[n][k][u].y);
-          else mma(c[n][k], f[0], f[1], f[2], f[3], q[n][k][u].x, q[n][k][u].y);
-          mma(c[n][k], f[4], f[5], f[6], f[7], q[n][k][u].z, q[n][k][u].w);
+          const uint4 b = q[((n * kG + k) * 2 + u) * 32];
+#pragma unroll
+          for (int j = 0; j < kSl; ++j) {
+            const uint32_t y = wa[j][k][u], z = wb[j][k][u], ys = swapped(y), zt = swapped(z);
+            if (u == 0) mma_from(c[j][n][k], 0.f, 0.f, upper(y), upper(z), lower(y), lower(z), b.x, b.y);
+            else mma(c[j][n][k], upper(y), upper(z), lower(y), lower(z), b.x, b.y);
+            mma(c[j][n][k], upper(ys), upper(zt), lower(ys), lower(zt), b.z, b.w);
+          }
         }
+#pragma unroll
+    for (int j = 0; j < kSl; ++j) {
+      float2 pa[kG], pb[kG];
+      load_pars<T, D>(rec + j * kStep + kp_at, pa);
+      load_pars<T, D>(rec + j * kStep + kp_at + 8 * Record<D>::kPar, pb);
+#pragma unroll
+      for (int k = 0; k < kG; ++k)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2& y = e < 2 ? pa[k] : pb[k];
+            x[j][n][e] = fmaf(c[j][n][k][e], y.x, k == 0 ? qs[n][k][e & 1] * y.y : fmaf(qs[n][k][e & 1], y.y, x[j][n][e]));
+          }
+    }
+  }
+  float2 pa[kSl][kG], pb[kSl][kG];               // (s, z) of V
+#pragma unroll
+  for (int j = 0; j < kSl; ++j) {
+    load_pars<T, D>(rec + j * kStep + vp_at, pa[j]);
+    load_pars<T, D>(rec + j * kStep + vp_at + 8 * Record<D>::kPar, pb[j]);
+  }
+  if (key0 < s.first || key0 + (kSl - 1) * kGap + 16 > s.len) {
+    // Keys that are not visible: their (s, z), perhaps never loaded, may be anything.
+#pragma unroll
+    for (int j = 0; j < kSl; ++j) {
+      const int key = key0 + j * kGap + ka;
+      if (key < s.first || key >= s.len) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[j][n][0] = x[j][n][1] = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kG; ++k) pa[j][k] = make_float2(0.f, 0.f);
       }
+      if (key + 8 < s.first || key + 8 >= s.len) {
 #pragma unroll
-    for (int k = 0; k < kG; ++k) {
+        for (int n = 0; n < NT; ++n) x[j][n][2] = x[j][n][3] = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2& y = e < 2 ? pa[k] : pb[k];
-          x[n][e] = fmaf(c[n][k][e], y.x, k == 0 ? qs[n][k][e & 1] * y.y : fmaf(qs[n][k][e & 1], y.y, x[n][e]));
-        }
+        for (int k = 0; k < kG; ++k) pb[j][k] = make_float2(0.f, 0.f);
+      }
     }
   }
-  load_pars<T, D>(rec + vp_at, pa);
-  load_pars<T, D>(rec + vp_at + 8 * Record<D>::kPar, pb);
-  if (edge) {
-    // The (s, z) of slots that are not visible may be anything.
-    if (key0 + ka < s.first || key0 + ka >= s.len) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kG; ++k) pa[k] = make_float2(0.f, 0.f);
-    }
-    if (key0 + ka + 8 < s.first || key0 + ka + 8 >= s.len) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) x[n][2] = x[n][3] = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kG; ++k) pb[k] = make_float2(0.f, 0.f);
-    }
-  }
+  float top[NT][2], most[kG];
   bool more = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
-    more |= fmaxf(x[n][0], x[n][2]) * by > m[n][0] + 8.f || fmaxf(x[n][1], x[n][3]) * by > m[n][1] + 8.f;
 #pragma unroll
-  for (int k = 0; k < kG; ++k) more |= fmaxf(pa[k].x, pb[k].x) * grow[k] >= 128.f;
+    for (int e = 0; e < 2; ++e) {
+      top[n][e] = fmaxf(x[0][n][e], x[0][n][2 + e]);
+#pragma unroll
+      for (int j = 1; j < kSl; ++j) top[n][e] = fmax3(top[n][e], x[j][n][e], x[j][n][2 + e]);
+      more |= fmaf(top[n][e], by, -8.f) > m[n][e];
+    }
+#pragma unroll
+  for (int k = 0; k < kG; ++k) {
+    most[k] = fmaxf(pa[0][k].x, pb[0][k].x);
+#pragma unroll
+    for (int j = 1; j < kSl; ++j) most[k] = fmax3(most[k], pa[j][k].x, pb[j][k].x);
+    more |= most[k] * grow[k] >= 128.f;
+  }
   if (__any_sync(0xffffffffu, more)) {
     // Maxima to the exact ones, and what was summed so far to them.
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float mx0 = fmaxf(x[n][0], x[n][2]), mx1 = fmaxf(x[n][1], x[n][3]);
+      float f[2];
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
-      }
-      const float n0 = fmaxf(m[n][0], mx0 * by), n1 = fmaxf(m[n][1], mx1 * by);
-      const float f0 = ex2(m[n][0] - n0), f1 = ex2(m[n][1] - n1);
-      m[n][0] = n0;
-      m[n][1] = n1;
-      l[n][0] *= f0;
-      l[n][1] *= f1;
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int k = 0; k < kG; ++k) {
-        zs[n][k][0] *= f0;
-        zs[n][k][1] *= f1;
+        for (int d = 4; d < 32; d <<= 1) top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(0xffffffffu, top[n][e], d));
+        const float to = fmaxf(m[n][e], top[n][e] * by);
+        f[e] = ex2(m[n][e] - to);
+        m[n][e] = to;
+        l[n][e] *= f[e];
+#pragma unroll
+        for (int k = 0; k < kG; ++k) zs[n][k][e] *= f[e];
       }
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        o[n][k][0] *= f0;
-        o[n][k][1] *= f1;
-        o[n][k][2] *= f0;
-        o[n][k][3] *= f1;
+        o[n][k][0] *= f[0];
+        o[n][k][1] *= f[1];
+        o[n][k][2] *= f[0];
+        o[n][k][3] *= f[1];
       }
     }
 #pragma unroll
     for (int k = 0; k < kG; ++k) {
       // (An infinite s, of a group that reads as NaN, does not count.)
-      float top = fmaxf(pa[k].x < INFINITY ? pa[k].x : 0.f, pb[k].x < INFINITY ? pb[k].x : 0.f);
+      float y = 0.f;
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      if (top * grow[k] >= 128.f) {
-        const float to = 128.f / power_above(top), f = to / grow[k];
+      for (int j = 0; j < kSl; ++j) {
+        y = fmaxf(y, pa[j][k].x < INFINITY ? pa[j][k].x : 0.f);
+        y = fmaxf(y, pb[j][k].x < INFINITY ? pb[j][k].x : 0.f);
+      }
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+      if (y * grow[k] >= 128.f) {
+        const float to = 128.f / power_above(y), f = to / grow[k];
         grow[k] = to;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][k * 4 + t][e] *= f;
+            for (int e = 0; e < 4; ++e) o[n][k * 4 + i][e] *= f;
       }
     }
   }
+  // Weights.
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    x[n][0] = ex2(fmaf(x[n][0], by, -m[n][0]));
-    x[n][1] = ex2(fmaf(x[n][1], by, -m[n][1]));
-    x[n][2] = ex2(fmaf(x[n][2], by, -m[n][0]));
-    x[n][3] = ex2(fmaf(x[n][3], by, -m[n][1]));
-    l[n][0] += x[n][0] + x[n][2];
-    l[n][1] += x[n][1] + x[n][3];
-  }
-  // Values.
-  uint32_t v[4][kG];
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (D == 128) {
-      const uint2 y = *reinterpret_cast<const uint2*>(rec + v_at + i * 4 * Record<D>::kRow);
-      v[i][0] = y.x;
-      v[i][1] = y.y;
-    } else {
-      v[i][0] = *reinterpret_cast<const uint32_t*>(rec + v_at + i * 4 * Record<D>::kRow);
+    for (int j = 0; j < kSl; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[j][n][e] = ex2(fmaf(x[j][n][e], by, -m[n][e & 1]));
+      l[n][0] += x[j][n][0] + x[j][n][2];
+      l[n][1] += x[j][n][1] + x[j][n][3];
     }
-  }
+  // Values, group by group.
 #pragma unroll
   for (int k = 0; k < kG; ++k) {
-    const float sa = pa[k].x * grow[k], sb = pb[k].x * grow[k];
-    const float za = fmaf(pa[k].x, 8.f, pa[k].y), zb = fmaf(pb[k].x, 8.f, pb[k].y);
-    uint32_t p[NT][kW][2];         // P^T: [high, low][keys 0-7, 8-15 of the fragment]
+    uint32_t p[kSl][NT][kW][2];          // P^T: [high, low][keys 0-7, 8-15 of the fragment]
+    uint32_t v[kSl][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      zs[n][k][0] = fmaf(x[n][0], za, fmaf(x[n][2], zb, zs[n][k][0]));
-      zs[n][k][1] = fmaf(x[n][1], za, fmaf(x[n][3], zb, zs[n][k][1]));
+    for (int j = 0; j < kSl; ++j) {
+      const float sa = pa[j][k].x * grow[k], sb = pb[j][k].x * grow[k];
+      const float za = fmaf(pa[j][k].x, 7.5f, pa[j][k].y), zb = fmaf(pb[j][k].x, 7.5f, pb[j][k].y);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float w0 = x[n][2 * e] * (e ? sb : sa), w1 = x[n][2 * e + 1] * (e ? sb : sa);
-        const uint32_t high = Half::pack(w0, w1);
-        p[n][0][e] = transpose8(high);
-        if constexpr (kW == 2) {
-          const float2 h = Half::up(high);
-          p[n][1][e] = transpose8(Half::pack(w0 - h.x, w1 - h.y));
+      for (int n = 0; n < NT; ++n) {
+        zs[n][k][0] = fmaf(x[j][n][0], za, fmaf(x[j][n][2], zb, zs[n][k][0]));
+        zs[n][k][1] = fmaf(x[j][n][1], za, fmaf(x[j][n][3], zb, zs[n][k][1]));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float w0 = x[j][n][2 * e] * (e ? sb : sa), w1 = x[j][n][2 * e + 1] * (e ? sb : sa);
+          const uint32_t high = Half::pack(w0, w1);
+          p[j][n][0][e] = transpose8(high);
+          if constexpr (kW == 2) {
+            const float2 h = Half::up(high);
+            p[j][n][1][e] = transpose8(Half::pack(w0 - h.x, w1 - h.y));
+          }
         }
       }
+      const uint4 y = *reinterpret_cast<const uint4*>(rec + j * kStep + v_at + k * 512);
+      v[j][0] = y.x, v[j][1] = y.y, v[j][2] = y.z, v[j][3] = y.w;
     }
-    // Pairs of keys: elements 8 r + 2 t from the low halves, 8 r + 2 t + 1 from the
-    // high ones, for tiles t = 0 and 1, then with their bytes swapped for 2 and 3.
+    // What the codes are counted from: -7.5 times the sums of the weights.
+    float minus[NT][2];                  // for codes c 2^-18; columns 2 qc, 2 qc + 1, all rows alike
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      constexpr uint32_t kMinus = 0x81e081e0u;                           // -7.5 2^-18
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < kSl; ++j)
+#pragma unroll
+        for (int h = 0; h < kW; ++h) {
+          if (j + h == 0) mma_from(y, 0.f, 0.f, kMinus, kMinus, kMinus, kMinus, p[j][n][h][0], p[j][n][h][1]);
+          else mma(y, kMinus, kMinus, kMinus, kMinus, p[j][n][h][0], p[j][n][h][1]);
+        }
+      minus[n][0] = y[0];
+      minus[n][1] = y[1];
+    }
+    // Words: keys c, c + 4 of elements 8 r + t and 8 r + 4 + t, then keys c + 8, c + 12;
+    // tiles t = 0 and 1, then with the bytes swapped 2 and 3.
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint32_t e01 = __byte_perm(v[0][k], v[1][k], u ? 0x4501 : 0x5410);
-      const uint32_t f01 = __byte_perm(v[0][k], v[1][k], u ? 0x6723 : 0x7632);
-      const uint32_t e23 = __byte_perm(v[2][k], v[3][k], u ? 0x4501 : 0x5410);
-      const uint32_t f23 = __byte_perm(v[2][k], v[3][k], u ? 0x6723 : 0x7632);
-      const uint32_t y[8] = {centred<false>(upper(e01)), centred<false>(upper(f01)), centred<false>(upper(e23)),
-                             centred<false>(upper(f23)), centred<true>(lower(e01)),  centred<true>(lower(f01)),
-                             centred<true>(lower(e23)),  centred<true>(lower(f23))};
+      if (u == 1) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int j = 0; j < kSl; ++j)
 #pragma unroll
-        for (int i = 0; i < kW; ++i) {
-          mma(o[n][4 * k + 2 * u], y[0], y[1], y[2], y[3], p[n][i][0], p[n][i][1]);
-          mma(o[n][4 * k + 2 * u + 1], y[4], y[5], y[6], y[7], p[n][i][0], p[n][i][1]);
+          for (int i = 0; i < 4; ++i) v[j][i] = swapped(v[j][i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float c[4];
+#pragma unroll
+          for (int j = 0; j < kSl; ++j)
+#pragma unroll
+            for (int h = 0; h < kW; ++h) {
+              const uint32_t (&y)[4] = v[j];
+              const uint32_t (&b)[2] = p[j][n][h];
+              if (j + h == 0) mma_from(c, minus[n][0] * (i ? 0x1p-4f : 1.f), minus[n][1] * (i ? 0x1p-4f : 1.f), i ? lower(y[0]) : upper(y[0]), i ? lower(y[1]) : upper(y[1]),
+                                       i ? lower(y[2]) : upper(y[2]), i ? lower(y[3]) : upper(y[3]), b[0], b[1]);
+              else mma(c, i ? lower(y[0]) : upper(y[0]), i ? lower(y[1]) : upper(y[1]), i ? lower(y[2]) : upper(y[2]),
+                       i ? lower(y[3]) : upper(y[3]), b[0], b[1]);
+            }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][4 * k + 2 * u + i][e] += c[e];
         }
     }
   }
@@ -573,14 +619,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
   const int qr = lane >> 2, qc = lane & 3;        // fragment row and column pair
   const int ka = (qr >> 1) + 4 * (qr & 1);        // the keys of rows qr and qr + 8: ka and ka + 8
   const uint8_t* mine = smem + warp * C::kSlice;
-  const uint32_t k_at = Record<D>::word(ka, 2 * qc);
-  const uint32_t v_at = Record<D>::kV + Record<D>::word(qc, qr);
+  const uint32_t k_at = Record<D>::k_word(ka, 2 * qc);
+  const uint32_t v_at = Record<D>::kV + lane * 16;
   const uint32_t kp_at = Record<D>::kKp + ka * Record<D>::kPar, vp_at = Record<D>::kVp + ka * Record<D>::kPar;
   float* buf = reinterpret_cast<float*>(smem + C::kBuf);
   float2* ml = reinterpret_cast<float2*>(smem + C::kMl);
   const float sl2 = a.scale_log2;
 
-  uint4 q[NT][kG][2];
+  uint4* q = reinterpret_cast<uint4*>(smem + C::kQ);
   float qs[NT][kG][2], o[NT][D / 16][4], zs[NT][kG][2], m[NT][2], l[NT][2];
   float by = 0.f, grow[kG];                       // of S^T; brings the s of V so far to 2^7 at most
   bool dead = false;
@@ -593,7 +639,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
     g = w.col / chunks;
     h0 = g * G + (w.col - g * chunks) * 8 * NT;
     h1 = (g + 1) * G;
-    load_q<T, D, NT>(a, w.b, w.col, chunks, q, qs, by);
+    load_q<T, D, NT>(a, w.b, w.col, chunks, warp == 0 ? q : nullptr, qs, by);
+    consumer_sync();
     by = sl2 * 0x1p18f / by;                      // x in slice() is in units of log2 / by
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -622,13 +669,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
       if (!dead && !wait_warp(&bars->full[stage], phase, st, abort_flag, kSiteFull)) dead = true;
       // (A slice whose page number is out of range was not loaded: what lies
       // there is worked on, and its sequence's outputs are unspecified.)
-#pragma unroll 1
-      for (int u = 0; u < kSl; ++u) {
-        const int key = key0 + u * kWarps * 16;
-        if (!dead && key < w.s.len && key + 16 > w.s.first)
-          slice<T, D, NT>(mine + stage * C::kStage + u * kWarps * C::kSlice, key, w.s, k_at, v_at, kp_at, vp_at, ka, by, q, qs, o,
-                          zs, m, l, grow);
-      }
+      if (!dead && key0 < w.s.len && key0 + (kSl - 1) * kWarps * 16 + 16 > w.s.first)
+        work<T, D, NT, kSl, kWarps * C::kSlice, kWarps * 16>(mine + stage * C::kStage, key0, w.s, k_at, v_at, kp_at, vp_at, ka, by,
+                                                            q + lane, qs, o, zs, m, l, grow);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->empty[stage]);
       if (++stage == C::kStages) {
@@ -681,24 +724,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
 #pragma unroll
         for (int k = 0; k < kG; ++k) {
           if (n + k > 0) consumer_sync();          // the buffer's last readers
-          // [warp][head][element of the group], this xor 2 (head / 2): the four rows and
-          // four column pairs that half a warp stores at once fall on 32 banks.
+          // [warp][head][element of the group], this xor 4 (head / 2): the rows and column
+          // pairs that a quarter of a warp stores at once fall on 32 banks.
           float* to = buf + (warp * 8 + qc * 2) * 64;
+          const float u0 = 0x1p18f / grow[k], u1 = 0x1p22f / grow[k];        // codes are c 2^-18 or c 2^-22, weights s p grow
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // What O^T stands for: codes are (c - 8) 2^-7, weights s p grow.
-            const int d = (qr * 8 + i * 2) ^ (qc * 2);
-            const float u = 128.f / grow[k];
-            const float (&c)[4] = o[n][4 * k + i];
-            *reinterpret_cast<float2*>(to + d) = make_float2(fmaf(c[0], u, zs[n][k][0]) * f[0], fmaf(c[2], u, zs[n][k][0]) * f[0]);
-            *reinterpret_cast<float2*>(to + 64 + d) =
-                make_float2(fmaf(c[1], u, zs[n][k][1]) * f[1], fmaf(c[3], u, zs[n][k][1]) * f[1]);
+          for (int e = 0; e < 4; ++e) {
+            const float z = zs[n][k][e & 1], s = f[e & 1];
+            *reinterpret_cast<float4*>(to + (e & 1) * 64 + ((qr * 8 + (e >> 1) * 4) ^ (qc * 4))) =
+                make_float4(fmaf(o[n][4 * k][e], u0, z) * s, fmaf(o[n][4 * k + 1][e], u1, z) * s,
+                            fmaf(o[n][4 * k + 2][e], u0, z) * s, fmaf(o[n][4 * k + 3][e], u1, z) * s);
           }
           consumer_sync();
           for (int hh = warp; hh < 8; hh += kWarps) {            // a head a warp at a time
             const int e = lane * 2, d = k * 64 + e, h = h0 + n * 8 + hh;
             const float Mh = __shfl_sync(0xffffffffu, M, hh), Lh = __shfl_sync(0xffffffffu, L, hh);
-            const float* from = buf + hh * 64 + (e ^ ((hh >> 1) * 2));
+            const float* from = buf + hh * 64 + (e ^ ((hh >> 1) * 4));
             float2 y = *reinterpret_cast<const float2*>(from);
 #pragma unroll
             for (int u = 1; u < kWarps; ++u) {
@@ -755,10 +796,10 @@ template <typename T, int D>
 cudaError_t launch(const DecodeArgs& a, const DevStatus& st, int parts, cudaStream_t stream) {
   if (a.cluster)
     return launch_after(a.unit_heads == 8 ? fa_decode4_kernel<T, D, 1, kShort, true> : fa_decode4_kernel<T, D, 2, kShort, true>,
-                        parts, kThreads, Cfg<D, kShort>::kBytes, a.cluster, stream, a, st);
+                        parts, kThreads, Cfg<D, kShort>::bytes(a.unit_heads / 8), a.cluster, stream, a, st);
   cudaError_t e =
       launch_after(a.unit_heads == 8 ? fa_decode4_kernel<T, D, 1, kLong, false> : fa_decode4_kernel<T, D, 2, kLong, false>, parts,
-                   kThreads, Cfg<D, kLong>::kBytes, 1, stream, a, st);
+                   kThreads, Cfg<D, kLong>::bytes(a.unit_heads / 8), 1, stream, a, st);
   const int joins = (parts - 1) * (a.unit_heads / 4);
   if (e == cudaSuccess && joins > 0) e = launch_after(fa_decode4_join_kernel<T, D>, joins, 128, 0, 1, stream, a);
   return e;
@@ -766,13 +807,13 @@ cudaError_t launch(const DecodeArgs& a, const DevStatus& st, int parts, cudaStre
 
 template <typename T, int D>
 cudaError_t configure() {
-  static_assert(Cfg<D, kShort>::kBytes <= 115712 && Cfg<D, kLong>::kBytes <= 115712, "two CTAs per SM");
+  static_assert(Cfg<D, kShort>::bytes(1) <= 115712 && Cfg<D, kLong>::bytes(1) <= 115712, "two CTAs per SM");
   static_assert(Cfg<D, kShort>::kKeys == kDecode4ClusterKeys && Cfg<D, kLong>::kKeys == kDecode4TileKeys, "tile");
   cudaError_t e = cudaSuccess;
   for (auto k : {fa_decode4_kernel<T, D, 1, kShort, true>, fa_decode4_kernel<T, D, 2, kShort, true>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, kShort>::kBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, kShort>::bytes(2));
   for (auto k : {fa_decode4_kernel<T, D, 1, kLong, false>, fa_decode4_kernel<T, D, 2, kLong, false>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, kLong>::kBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, kLong>::bytes(2));
   if (e == cudaSuccess) e = preload_kernel(fa_decode4_join_kernel<T, D>);
   return e;
 }

@@ -43,24 +43,26 @@ cudaError_t launch_norm_rope(int dtype, const NormRopeArgs& a, const DevStatus& 
 cudaError_t launch_norm_rope_bwd(int dtype, NormRopeBwdArgs a, const DevStatus& st, int num_sms, cudaStream_t stream);
 
 // The 4-bit cache.  16 slots of a page and kv head form a record of 18 d bytes:
-// K codes [16][d/2], V codes [16][d/2], then (s, z) of K and of V, [16][d/64]
-// pairs of the call's type each.  A page's records follow one another.
-//   A row's codes are d/8 words of eight elements each, element e of a word in
-// place e / 2 of half e % 2: bits 9-6, bits 5-2, and these two with the half's
-// bytes swapped (so bits 1, 0, 15, 14 and 13-10).  Two neighbours lie in the same
-// place of the halves, where one mask makes a pair of fp16 numbers of them.  At d
-// = 128 word i of both groups stand side by side, at 8-byte chunk i ^ 4 ((slot /
-// 2) % 2): the lanes of a warp that read 8 bytes of four rows each, or 16 bytes
-// of eight rows, then meet all banks of shared memory alike.
+// K codes [16][d/2], V codes, as many bytes, (s, z) of K and of V, [16][d/64] pairs
+// of the call's type each.  A page's records follow one another.
+//   Codes lie in 16-bit halves of four, place n at bits 9-6, 5-2, and these two with
+// the half's bytes swapped (so bits 1, 0, 15, 14 and 13-10), and two halves in a
+// word are a pair of operands of a matrix product, which one mask makes fp16
+// numbers of: of K neighbouring elements of d, of V two keys.
+//   K: a row's word i holds elements 8 i .. 8 i + 7, element e in place e / 2 of
+// half e % 2.  At d = 128 word i of both groups stand side by side, at 8-byte chunk i
+// ^ 4 ((slot / 2) % 2): lanes that read 16 bytes of eight rows each then meet all
+// banks of shared memory alike.
+//   V: group by group, 16 bytes for each lane of a warp.  Lane 4 r + c has the
+// elements 8 r .. 8 r + 7 of the slots c, c + 4, c + 8 and c + 12: four words, of
+// the slots (c, c + 4) and then (c + 8, c + 12) the elements 8 r .. 8 r + 3 and then
+// the other four, the first slot in the lower half.
 #ifdef __CUDACC__
-__device__ __forceinline__ uint32_t place_code(uint32_t c, int e) {
-  const int n = e >> 1;
-  const uint32_t h = n == 0 ? c << 6 : n == 1 ? c << 2 : n == 2 ? c >> 2 | (c & 3) << 14 : c << 10;
-  return h << (16 * (e & 1));
+// A code in place n of its half, and back.
+__device__ __forceinline__ uint32_t place_code(uint32_t c, int n) {
+  return n == 0 ? c << 6 : n == 1 ? c << 2 : n == 2 ? c >> 2 | (c & 3) << 14 : c << 10;
 }
-__device__ __forceinline__ uint32_t code_at(uint32_t w, int e) {
-  const int n = e >> 1;
-  const uint32_t h = w >> (16 * (e & 1));
+__device__ __forceinline__ uint32_t code_at(uint32_t h, int n) {
   return (n == 0 ? h >> 6 : n == 1 ? h >> 2 : n == 2 ? h << 2 | (h >> 14 & 3) : h >> 10) & 15u;
 }
 #endif
@@ -70,9 +72,13 @@ struct Record {
   static constexpr int kV = 16 * kRow, kKp = 32 * kRow, kPar = D / 64 * 4, kVp = kKp + 16 * kPar;
   static constexpr int kBytes = kVp + 16 * kPar;
   static_assert(kBytes == 18 * D, "record");
-  // Byte of word i of a slot's row.
-  static __host__ __device__ constexpr int word(int slot, int i) {
+  // Byte of word i of a slot's row of K.
+  static __host__ __device__ constexpr int k_word(int slot, int i) {
     return slot * kRow + (D == 128 ? (((i & 7) ^ ((slot & 2) << 1)) << 3) + ((i >> 3) << 2) : i << 2);
+  }
+  // Byte of the half that holds elements 8 i + 4 h .. 8 i + 4 h + 3 of a slot's row of V.
+  static __host__ __device__ constexpr int v_half(int slot, int i, int h) {
+    return kV + (i >> 3) * 512 + ((i & 7) * 4 + (slot & 3)) * 16 + (slot >> 3) * 8 + h * 4 + ((slot >> 2) & 1) * 2;
   }
 };
 
