@@ -146,12 +146,17 @@ __device__ __forceinline__ void load_pars(const uint8_t* p, float2 (&x)[D / 64])
   }
 }
 
-// Query rows of unit (b, col) as B operands, column = head lane / 4: at to[n][g][w] of
-// each lane (if `to`) the eight elements 64 g + 16 (lane % 4) + 8 w on, times `times`
+template <typename T>
+__device__ __forceinline__ float2 load_par(const uint8_t* p) {
+  return Type<T>::up(*reinterpret_cast<const uint32_t*>(p));
+}
+
+// Query rows of unit (b, col) as B operands, column = head lane / 4: at to[n][g][w][h][lane]
+// (if `to`) the four elements 64 g + 16 (lane % 4) + 8 w + 4 h on, times `times`
 // and, the odd pairs, 16; and sums[n][g], those over the groups for the heads 2 (lane % 4) and the
 // next, this lane's columns of S^T.
 template <typename T, int D, int NT>
-__device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int col, int chunks, uint4* to, float (&sums)[NT][D / 64][2], float& times) {
+__device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int col, int chunks, uint2* to, float (&sums)[NT][D / 64][2], float& times) {
   const int lane = threadIdx.x & 31, G = a.Hq / a.kv.Hkv;
   const int g = col / chunks, h0 = g * G + (col - g * chunks) * 8 * NT + (lane >> 2), h1 = (g + 1) * G;
   const T* p = static_cast<const T*>(a.q) + b * a.q_sb + (lane & 3) * 16;
@@ -194,8 +199,11 @@ __device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int col, int 
       for (int w = 0; w < 2; ++w) {
         const uint4 v = q[n][k][w];
         const float2 y0 = Type<T>::up(v.x), y1 = Type<T>::up(v.y), y2 = Type<T>::up(v.z), y3 = Type<T>::up(v.w);
-        if (to) to[((n * (D / 64) + k) * 2 + w) * 32 + lane] = make_uint4(Half::pack(y0.x * times, y0.y * times), Half::pack(y1.x * more, y1.y * more),
-                       Half::pack(y2.x * times, y2.y * times), Half::pack(y3.x * more, y3.y * more));
+        if (to) {
+          uint2* x = to + ((n * (D / 64) + k) * 2 + w) * 64 + lane;
+          x[0] = make_uint2(Half::pack(y0.x * times, y0.y * times), Half::pack(y1.x * more, y1.y * more));
+          x[32] = make_uint2(Half::pack(y2.x * times, y2.y * times), Half::pack(y3.x * more, y3.y * more));
+        }
       }
 }
 
@@ -211,8 +219,8 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
 // rec the first, of the 16 keys from key0 on: S^T, its weights against the running
 // maximum m and, in l, zs and o, their sums.
 template <typename T, int D, int NT, int kSl, int kStep, int kGap>
-__device__ __forceinline__ void work(const uint8_t* rec, int key0, const Span& s, uint32_t k_at, uint32_t v_at, uint32_t kp_at,
-                                     uint32_t vp_at, int ka, float by, const uint4* q,
+__device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint32_t k_at, uint32_t v_at, uint32_t kp_at,
+                                     uint32_t vp_at, int ka, float by, const uint2* q,
                                      const float (&qs)[NT][D / 64][2], float (&o)[NT][D / 16][4], float (&zs)[NT][D / 64][2],
                                      float (&m)[NT][2], float (&l)[NT][2], float (&grow)[D / 64]) {
   constexpr int kG = D / 64, kW = Type<T>::kWeights;
@@ -235,21 +243,24 @@ __device__ __forceinline__ void work(const uint8_t* rec, int key0, const Span& s
         wa[j][0][0] = ya.x, wa[j][0][1] = ya.y, wb[j][0][0] = yb.x, wb[j][0][1] = yb.y;
       }
     }
+    // Products that follow one another are of different sums, since a product has
+    // to wait for the last one of its own.
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int k = 0; k < kG; ++k)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 b = q[((n * kG + k) * 2 + u) * 32];
+        for (int k = 0; k < kG; ++k)
 #pragma unroll
-          for (int j = 0; j < kSl; ++j) {
-            const uint32_t y = wa[j][k][u], z = wb[j][k][u], ys = swapped(y), zt = swapped(z);
-            if (u == 0) mma_from(c[j][n][k], 0.f, 0.f, upper(y), upper(z), lower(y), lower(z), b.x, b.y);
-            else mma(c[j][n][k], upper(y), upper(z), lower(y), lower(z), b.x, b.y);
-            mma(c[j][n][k], upper(ys), upper(zt), lower(ys), lower(zt), b.z, b.w);
+          for (int n = 0; n < NT; ++n) {
+            const uint2 b = q[(((n * kG + k) * 2 + u) * 2 + h) * 32];
+#pragma unroll
+            for (int j = 0; j < kSl; ++j) {
+              const uint32_t y = h ? swapped(wa[j][k][u]) : wa[j][k][u], z = h ? swapped(wb[j][k][u]) : wb[j][k][u];
+              if (u + h == 0) mma_from(c[j][n][k], 0.f, 0.f, upper(y), upper(z), lower(y), lower(z), b.x, b.y);
+              else mma(c[j][n][k], upper(y), upper(z), lower(y), lower(z), b.x, b.y);
+            }
           }
-        }
 #pragma unroll
     for (int j = 0; j < kSl; ++j) {
       float2 pa[kG], pb[kG];
@@ -266,30 +277,24 @@ __device__ __forceinline__ void work(const uint8_t* rec, int key0, const Span& s
           }
     }
   }
-  float2 pa[kSl][kG], pb[kSl][kG];               // (s, z) of V
-#pragma unroll
-  for (int j = 0; j < kSl; ++j) {
-    load_pars<T, D>(rec + j * kStep + vp_at, pa[j]);
-    load_pars<T, D>(rec + j * kStep + vp_at + 8 * Record<D>::kPar, pb[j]);
-  }
   if (key0 < s.first || key0 + (kSl - 1) * kGap + 16 > s.len) {
-    // Keys that are not visible: their (s, z), perhaps never loaded, may be anything.
+    // Keys that are not visible: their (s, z) of V, perhaps never loaded, may be
+    // anything, and become 0.
 #pragma unroll
     for (int j = 0; j < kSl; ++j) {
       const int key = key0 + j * kGap + ka;
-      if (key < s.first || key >= s.len) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[j][n][0] = x[j][n][1] = -INFINITY;
+      for (int h = 0; h < 2; ++h)
+        if (key + 8 * h < s.first || key + 8 * h >= s.len) {
 #pragma unroll
-        for (int k = 0; k < kG; ++k) pa[j][k] = make_float2(0.f, 0.f);
-      }
-      if (key + 8 < s.first || key + 8 >= s.len) {
+          for (int n = 0; n < NT; ++n) x[j][n][2 * h] = x[j][n][2 * h + 1] = -INFINITY;
+          uint32_t* par = reinterpret_cast<uint32_t*>(rec + j * kStep + vp_at + 8 * h * Record<D>::kPar);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[j][n][2] = x[j][n][3] = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kG; ++k) pb[j][k] = make_float2(0.f, 0.f);
-      }
+          for (int k = 0; k < kG; ++k) par[k] = 0u;
+        }
     }
+    __syncwarp();
+    fence_proxy_async_smem();          // before the slots' next copy
   }
   float top[NT][2], most[kG];
   bool more = false;
@@ -303,12 +308,17 @@ __device__ __forceinline__ void work(const uint8_t* rec, int key0, const Span& s
       more |= fmaf(top[n][e], by, -8.f) > m[n][e];
     }
 #pragma unroll
-  for (int k = 0; k < kG; ++k) {
-    most[k] = fmaxf(pa[0][k].x, pb[0][k].x);
+  for (int k = 0; k < kG; ++k) most[k] = 0.f;
 #pragma unroll
-    for (int j = 1; j < kSl; ++j) most[k] = fmax3(most[k], pa[j][k].x, pb[j][k].x);
-    more |= most[k] * grow[k] >= 128.f;
+  for (int j = 0; j < kSl; ++j) {
+    float2 y[kG], z[kG];
+    load_pars<T, D>(rec + j * kStep + vp_at, y);
+    load_pars<T, D>(rec + j * kStep + vp_at + 8 * Record<D>::kPar, z);
+#pragma unroll
+    for (int k = 0; k < kG; ++k) most[k] = fmax3(most[k], y[k].x, z[k].x);
   }
+#pragma unroll
+  for (int k = 0; k < kG; ++k) more |= most[k] * grow[k] >= 128.f;
   if (__any_sync(0xffffffffu, more)) {
     // Maxima to the exact ones, and what was summed so far to them.
 #pragma unroll
@@ -338,10 +348,12 @@ __device__ __forceinline__ void work(const uint8_t* rec, int key0, const Span& s
       // (An infinite s, of a group that reads as NaN, does not count.)
       float y = 0.f;
 #pragma unroll
-      for (int j = 0; j < kSl; ++j) {
-        y = fmaxf(y, pa[j][k].x < INFINITY ? pa[j][k].x : 0.f);
-        y = fmaxf(y, pb[j][k].x < INFINITY ? pb[j][k].x : 0.f);
-      }
+      for (int j = 0; j < kSl; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float z = load_par<T>(rec + j * kStep + vp_at + 8 * h * Record<D>::kPar + k * 4).x;
+          y = fmaxf(y, z < INFINITY ? z : 0.f);
+        }
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
       if (y * grow[k] >= 128.f) {
@@ -373,8 +385,9 @@ __device__ __forceinline__ void work(const uint8_t* rec, int key0, const Span& s
     uint32_t v[kSl][4];
 #pragma unroll
     for (int j = 0; j < kSl; ++j) {
-      const float sa = pa[j][k].x * grow[k], sb = pb[j][k].x * grow[k];
-      const float za = fmaf(pa[j][k].x, 7.5f, pa[j][k].y), zb = fmaf(pb[j][k].x, 7.5f, pb[j][k].y);
+      const float2 pa = load_par<T>(rec + j * kStep + vp_at + k * 4);
+      const float2 pb = load_par<T>(rec + j * kStep + vp_at + 8 * Record<D>::kPar + k * 4);
+      const float sa = pa.x * grow[k], sb = pb.x * grow[k], za = fmaf(pa.x, 7.5f, pa.y), zb = fmaf(pb.x, 7.5f, pb.y);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         zs[n][k][0] = fmaf(x[j][n][0], za, fmaf(x[j][n][2], zb, zs[n][k][0]));
@@ -413,31 +426,33 @@ __device__ __forceinline__ void work(const uint8_t* rec, int key0, const Span& s
     // tiles t = 0 and 1, then with the bytes swapped 2 and 3.
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      if (u == 1) {
+      float c[NT][2][4];
 #pragma unroll
-        for (int j = 0; j < kSl; ++j)
+      for (int j = 0; j < kSl; ++j) {
+        uint32_t y[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[j][i] = swapped(v[j][i]);
+        for (int i = 0; i < 4; ++i) y[i] = u ? swapped(v[j][i]) : v[j][i];
+#pragma unroll
+        for (int h = 0; h < kW; ++h)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t (&b)[2] = p[j][n][h];
+            if (j + h == 0) {
+              mma_from(c[n][0], minus[n][0], minus[n][1], upper(y[0]), upper(y[1]), upper(y[2]), upper(y[3]), b[0], b[1]);
+              mma_from(c[n][1], minus[n][0] * 0x1p-4f, minus[n][1] * 0x1p-4f, lower(y[0]), lower(y[1]), lower(y[2]), lower(y[3]),
+                       b[0], b[1]);
+            } else {
+              mma(c[n][0], upper(y[0]), upper(y[1]), upper(y[2]), upper(y[3]), b[0], b[1]);
+              mma(c[n][1], lower(y[0]), lower(y[1]), lower(y[2]), lower(y[3]), b[0], b[1]);
+            }
+          }
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float c[4];
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < kSl; ++j)
-#pragma unroll
-            for (int h = 0; h < kW; ++h) {
-              const uint32_t (&y)[4] = v[j];
-              const uint32_t (&b)[2] = p[j][n][h];
-              if (j + h == 0) mma_from(c, minus[n][0] * (i ? 0x1p-4f : 1.f), minus[n][1] * (i ? 0x1p-4f : 1.f), i ? lower(y[0]) : upper(y[0]), i ? lower(y[1]) : upper(y[1]),
-                                       i ? lower(y[2]) : upper(y[2]), i ? lower(y[3]) : upper(y[3]), b[0], b[1]);
-              else mma(c, i ? lower(y[0]) : upper(y[0]), i ? lower(y[1]) : upper(y[1]), i ? lower(y[2]) : upper(y[2]),
-                       i ? lower(y[3]) : upper(y[3]), b[0], b[1]);
-            }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][4 * k + 2 * u + i][e] += c[e];
-        }
+          for (int e = 0; e < 4; ++e) o[n][4 * k + 2 * u + i][e] += c[n][i][e];
     }
   }
 }
@@ -618,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
   // -------------------------------------------------------------- consumers
   const int qr = lane >> 2, qc = lane & 3;        // fragment row and column pair
   const int ka = (qr >> 1) + 4 * (qr & 1);        // the keys of rows qr and qr + 8: ka and ka + 8
-  const uint8_t* mine = smem + warp * C::kSlice;
+  uint8_t* mine = smem + warp * C::kSlice;
   const uint32_t k_at = Record<D>::k_word(ka, 2 * qc);
   const uint32_t v_at = Record<D>::kV + lane * 16;
   const uint32_t kp_at = Record<D>::kKp + ka * Record<D>::kPar, vp_at = Record<D>::kVp + ka * Record<D>::kPar;
@@ -626,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
   float2* ml = reinterpret_cast<float2*>(smem + C::kMl);
   const float sl2 = a.scale_log2;
 
-  uint4* q = reinterpret_cast<uint4*>(smem + C::kQ);
+  uint2* q = reinterpret_cast<uint2*>(smem + C::kQ);
   float qs[NT][kG][2], o[NT][D / 16][4], zs[NT][kG][2], m[NT][2], l[NT][2];
   float by = 0.f, grow[kG];                       // of S^T; brings the s of V so far to 2^7 at most
   bool dead = false;
