@@ -38,41 +38,76 @@ __host__ __device__ inline int tokens_per_block(int d) {
   return kThreads / p;
 }
 
+// Asynchronous copies of a thread's own vectors into its own places of a ring in
+// shared memory, kSlots rows deep: what a row needs is on its way while others are
+// worked on, without registers, and nobody else waits for it.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+constexpr int kSlots = 4, kSlotsBwd = 4;
+constexpr int kBwdBlocks = 3;                      // of the backward kernel an SM
+
+// grid: x over groups of tpb tokens, y over groups of hpb heads of q and then k.
+// The first rows are on their way while the angles are formed.
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(kThreads) fa_qk_norm_kernel(const NormRopeArgs a, int hpb, const DevStatus st) {
+__global__ void __launch_bounds__(kThreads, 5) fa_qk_norm_kernel(const NormRopeArgs a, int hpb, const DevStatus st) {
   __shared__ Pairs pairs;
+  __shared__ uint4 ring[kSlots][2][kThreads];
   launch_dependents();
   wait_for_previous();
-  load_pairs<kThreads>(a.r, pairs, st);
-  __syncthreads();
   const Lanes ln(a.d);
   const long long t = (long long)blockIdx.x * ln.tpb + ln.lt;
   const bool live = ln.c < a.d / 16 && t < (long long)a.B * a.N;
   const int b = live ? (int)(t / a.N) : 0, n = live ? (int)(t - (long long)b * a.N) : 0;
   const Chunk ck = chunk_of<kInter>(live ? ln.c : 0, a.r.rot);
-  float cs[8] = {}, sn[8] = {};
-  if (ck.turned) load_fine_angles(a.r, pairs, a.r.pos + b * a.r.pos_batch + n, live ? ln.c : 0, cs, sn);
   const int h0 = blockIdx.y * hpb, h1 = min(h0 + hpb, a.Hq + a.Hk);
+  const T* q = static_cast<const T*>(a.q.p) + b * a.q.sb + n * a.q.sn;
+  const T* k = static_cast<const T*>(a.k.p) + b * a.k.sb + n * a.k.sn;
+  auto copy = [&](int h, int slot) {
+    if (live && h < h1) {
+      const T* x = h < a.Hq ? q + h * a.q.sh : k + (h - a.Hq) * a.k.sh;
+      copy16(&ring[slot][0][threadIdx.x], x + ck.e0);
+      copy16(&ring[slot][1][threadIdx.x], x + ck.e1);
+    }
+    copies_end();
+  };
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) copy(h0 + s, s);
+  load_pairs<kThreads>(a.r, pairs, st);
+  __syncthreads();
+  float cs[8] = {}, sn[8] = {};
+  if (ck.turned) load_angles(a.r, pairs, a.r.pos + b * a.r.pos_batch + n, live ? ln.c : 0, cs, sn);
   const float inv_d = 1.f / a.d;
+  int slot = 0, h = h0;
+#pragma unroll 1
   for (int part = 0; part < 2; ++part) {
-    const RowView &in = part ? a.k : a.q, &out = part ? a.k_out : a.q_out;
-    const int from = part ? max(h0 - a.Hq, 0) : h0, to = part ? h1 - a.Hq : min(h1, a.Hq);
-    if (from >= to) continue;
-    const T* x = static_cast<const T*>(in.p) + b * in.sb + n * in.sn;
-    T* y = static_cast<T*>(out.p) + b * out.sb + n * out.sn;
+    const int end = part ? h1 : min(h1, a.Hq);
+    if (h >= end) continue;
+    const RowView& out = part ? a.k_out : a.q_out;
+    T* y = static_cast<T*>(out.p) + b * out.sb + n * out.sn + (h - (part ? a.Hq : 0)) * out.sh;
     float wa[8], wb[8];
     load_weights<T>(part ? a.n.wk : a.n.wq, a.n.fp32, ck.e0, wa);
     load_weights<T>(part ? a.n.wk : a.n.wq, a.n.fp32, ck.e1, wb);
-    for (int h = from; h < to; ++h) {
+#pragma unroll 1
+    for (; h < end; ++h, y += out.sh) {
+      copies_wait<kSlots - 1>();
       uint4 va = make_uint4(0, 0, 0, 0), vb = va;
       if (live) {
-        va = *reinterpret_cast<const uint4*>(x + h * in.sh + ck.e0);
-        vb = *reinterpret_cast<const uint4*>(x + h * in.sh + ck.e1);
+        va = ring[slot][0][threadIdx.x];
+        vb = ring[slot][1][threadIdx.x];
       }
       float xa[8], xb[8];
       up8<T>(va, xa);
       up8<T>(vb, xb);
       const float r = rsqrtf(sum_over(sum_of_squares(xa, xb), ln.per_row) * inv_d + a.n.eps);
+      copy(h + kSlots, slot);
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         xa[i] = xa[i] * r * wa[i];
@@ -80,19 +115,20 @@ __global__ void __launch_bounds__(kThreads) fa_qk_norm_kernel(const NormRopeArgs
       }
       if (ck.turned) turn8<kInter>(xa, xb, cs, sn);
       if (live) {
-        *reinterpret_cast<uint4*>(y + h * out.sh + ck.e0) = down8<T>(xa);
-        *reinterpret_cast<uint4*>(y + h * out.sh + ck.e1) = down8<T>(xb);
+        __stcs(reinterpret_cast<uint4*>(y + ck.e0), down8<T>(xa));
+        __stcs(reinterpret_cast<uint4*>(y + ck.e1), down8<T>(xb));
       }
     }
   }
 }
 
-// The blocks of q and then those of k, each block its share of the (tokens, heads)
-// items of its part; what it adds up of dw goes to its row of a.part.
+// The blocks of q and then those of k.  A block has a run of at most hpb heads of its
+// part and every so many groups of tpb tokens; what it adds up of dw goes to its
+// row of a.part.
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(kThreads) fa_qk_norm_bwd_kernel(const NormRopeBwdArgs a, int hpb, const DevStatus st) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) fa_qk_norm_bwd_kernel(const NormRopeBwdArgs a, int hpb, const DevStatus st) {
   __shared__ Pairs pairs;
-  __shared__ float sums[kThreads][17];
+  __shared__ uint4 ring[kSlotsBwd][4][kThreads];
   launch_dependents();
   wait_for_previous();
   load_pairs<kThreads>(a.r, pairs, st);
@@ -100,8 +136,10 @@ __global__ void __launch_bounds__(kThreads) fa_qk_norm_bwd_kernel(const NormRope
   const Lanes ln(a.d);
   const int part = blockIdx.x >= a.blocks[0], block = blockIdx.x - (part ? a.blocks[0] : 0), H = a.H[part];
   const RowView &dy = a.dy[part], &xv = a.x[part], &dx = a.dx[part];
-  const int splits = (H + hpb - 1) / hpb;
-  const long long tokens = (long long)a.B * a.N, items = (tokens + ln.tpb - 1) / ln.tpb * splits;
+  const int splits = (H + hpb - 1) / hpb, h0 = block % splits * hpb, heads = min(hpb, H - h0);
+  // (The launcher gives each part a multiple of its splits in blocks.)
+  const int step = a.blocks[part] / splits * ln.tpb;
+  const long long tokens = (long long)a.B * a.N;
   const bool in_row = ln.c < a.d / 16;
   const Chunk ck = chunk_of<kInter>(in_row ? ln.c : 0, a.r.rot);
   const void* w = part ? a.n.wk : a.n.wq;
@@ -109,23 +147,57 @@ __global__ void __launch_bounds__(kThreads) fa_qk_norm_bwd_kernel(const NormRope
   load_weights<T>(w, a.n.fp32, ck.e0, wa);
   load_weights<T>(w, a.n.fp32, ck.e1, wb);
   const float inv_d = 1.f / a.d;
-  for (long long it = block; it < items; it += a.blocks[part]) {
-    const long long tb = it / splits, t = tb * ln.tpb + ln.lt;
-    const int h0 = (int)(it - tb * splits) * hpb, h1 = min(h0 + hpb, H);
+
+  // t0: the block's first token of a group.  A thread's rows are copied kSlotsBwd
+  // heads ahead of the work, into the next group where the heads end.
+  const long long first = (long long)(block / splits) * ln.tpb;
+  long long to_t0 = first;
+  int to_h = 0;
+  const T *px = nullptr, *pg = nullptr;
+  auto aim = [&]() {
+    const long long t = to_t0 + ln.lt;
+    px = nullptr;
+    if (in_row && t < tokens) {
+      const int b = (int)(t / a.N), n = (int)(t - (long long)b * a.N);
+      px = static_cast<const T*>(xv.p) + b * xv.sb + n * xv.sn + h0 * xv.sh;
+      pg = static_cast<const T*>(dy.p) + b * dy.sb + n * dy.sn + h0 * dy.sh;
+    }
+  };
+  auto copy = [&](int slot) {
+    if (px) {
+      copy16(&ring[slot][0][threadIdx.x], px + ck.e0);
+      copy16(&ring[slot][1][threadIdx.x], px + ck.e1);
+      copy16(&ring[slot][2][threadIdx.x], pg + ck.e0);
+      copy16(&ring[slot][3][threadIdx.x], pg + ck.e1);
+      px += xv.sh;
+      pg += dy.sh;
+    }
+    copies_end();
+    if (++to_h == heads) {
+      to_h = 0;
+      to_t0 += step;
+      aim();
+    }
+  };
+  aim();
+#pragma unroll
+  for (int s = 0; s < kSlotsBwd; ++s) copy(s);
+  int slot = 0;
+#pragma unroll 1
+  for (long long t0 = first; t0 < tokens; t0 += step) {
+    const long long t = t0 + ln.lt;
     const bool live = in_row && t < tokens;
     const int b = live ? (int)(t / a.N) : 0, n = live ? (int)(t - (long long)b * a.N) : 0;
     float cs[8] = {}, sn[8] = {};
-    if (ck.turned) load_fine_angles(a.r, pairs, a.r.pos + b * a.r.pos_batch + n, in_row ? ln.c : 0, cs, sn);
-    const T* x = static_cast<const T*>(xv.p) + b * xv.sb + n * xv.sn;
-    const T* g = static_cast<const T*>(dy.p) + b * dy.sb + n * dy.sn;
-    T* y = static_cast<T*>(dx.p) + b * dx.sb + n * dx.sn;
-    for (int h = h0; h < h1; ++h) {
+    if (ck.turned) load_angles(a.r, pairs, a.r.pos + b * a.r.pos_batch + n, in_row ? ln.c : 0, cs, sn);
+    T* y = static_cast<T*>(dx.p) + b * dx.sb + n * dx.sn + h0 * dx.sh;
+#pragma unroll 1
+    for (int h = 0; h < heads; ++h, y += dx.sh) {
+      copies_wait<kSlotsBwd - 1>();
       uint4 v[4] = {};
       if (live) {
-        v[0] = *reinterpret_cast<const uint4*>(x + h * xv.sh + ck.e0);
-        v[1] = *reinterpret_cast<const uint4*>(x + h * xv.sh + ck.e1);
-        v[2] = *reinterpret_cast<const uint4*>(g + h * dy.sh + ck.e0);
-        v[3] = *reinterpret_cast<const uint4*>(g + h * dy.sh + ck.e1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = ring[slot][i][threadIdx.x];
       }
       float xa[8], xb[8], ga[8], gb[8];
       up8<T>(v[0], xa);
@@ -138,21 +210,27 @@ __global__ void __launch_bounds__(kThreads) fa_qk_norm_bwd_kernel(const NormRope
       for (int i = 0; i < 8; ++i) dot = fmaf(ga[i] * wa[i], xa[i], fmaf(gb[i] * wb[i], xb[i], dot));
       const float r = rsqrtf(sum_over(sum_of_squares(xa, xb), ln.per_row) * inv_d + a.n.eps);
       const float m = sum_over(dot, ln.per_row) * r * inv_d;        // mean of g w x r
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float ya = xa[i] * r, yb = xb[i] * r;
-        da[i] = fmaf(ga[i], ya, da[i]);
-        db[i] = fmaf(gb[i], yb, db[i]);
-        xa[i] = r * (ga[i] * wa[i] - ya * m);
-        xb[i] = r * (gb[i] * wb[i] - yb * m);
-      }
+      copy(slot);
+      slot = slot + 1 == kSlotsBwd ? 0 : slot + 1;
       if (live) {
-        *reinterpret_cast<uint4*>(y + h * dx.sh + ck.e0) = down8<T>(xa);
-        *reinterpret_cast<uint4*>(y + h * dx.sh + ck.e1) = down8<T>(xb);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float ya = xa[i] * r, yb = xb[i] * r;
+          da[i] = fmaf(ga[i], ya, da[i]);
+          db[i] = fmaf(gb[i], yb, db[i]);
+          xa[i] = r * (ga[i] * wa[i] - ya * m);
+          xb[i] = r * (gb[i] * wb[i] - yb * m);
+        }
+        __stcs(reinterpret_cast<uint4*>(y + ck.e0), down8<T>(xa));
+        __stcs(reinterpret_cast<uint4*>(y + ck.e1), down8<T>(xb));
       }
     }
   }
   if (!a.dw[part]) return;
+  copies_wait<0>();
+  __syncthreads();
+  float(*sums)[17] = reinterpret_cast<float(*)[17]>(ring);
+  static_assert(sizeof(ring) >= sizeof(float[kThreads][17]), "room for the sums");
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     sums[threadIdx.x][i] = da[i];
@@ -183,16 +261,18 @@ __global__ void __launch_bounds__(kThreads) fa_qk_norm_dw_kernel(const NormRopeB
   const int i = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, part = blockIdx.y, lane = threadIdx.x % 32;
   if (i >= a.d || !a.dw[part]) return;
   const float* p = a.part + (long long)(part ? a.blocks[0] : 0) * a.d + i;
-  float s = 0.f;
-  for (int b = lane; b < a.blocks[part]; b += 32) s += p[(long long)b * a.d];
-  s = sum_over(s, 32);
-  if (lane == 0) a.dw[part][i] = s;
+  double s = 0.0;
+  for (int b = lane; b < a.blocks[part]; b += 32) s += (double)p[(long long)b * a.d];
+  for (int d = 1; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (lane == 0) a.dw[part][i] = (float)s;
 }
 
+// Heads per block of the forward: see fa_rope.cu.
 int heads_per_block(long long token_blocks, int heads, int num_sms) {
   const long long want = 16LL * num_sms;
   long long splits = (want + token_blocks - 1) / token_blocks;
-  if (splits > heads) splits = heads;
+  const long long most = (heads + kSlots - 1) / kSlots;
+  if (splits > most) splits = most;
   if (splits < 1) splits = 1;
   return (int)((heads + splits - 1) / splits);
 }
@@ -221,16 +301,25 @@ cudaError_t launch_norm_rope(int dtype, const NormRopeArgs& a, const DevStatus& 
 }
 
 cudaError_t launch_norm_rope_bwd(int dtype, NormRopeBwdArgs a, const DevStatus& st, int num_sms, cudaStream_t stream) {
-  const int tpb = tokens_per_block(a.d), hpb = 4;
+  const int tpb = tokens_per_block(a.d);
   const long long token_blocks = ((long long)a.B * a.N + tpb - 1) / tpb;
-  const int most = min(4 * num_sms, kNormBwdMaxBlocks), heads = a.H[0] + a.H[1];
-  long long items[2];
-  for (int i = 0; i < 2; ++i) items[i] = token_blocks * ((a.H[i] + hpb - 1) / hpb);
-  if (items[0] + items[1] <= most) {
-    for (int i = 0; i < 2; ++i) a.blocks[i] = (int)items[i];
-  } else {
-    a.blocks[1] = a.H[1] ? max(1, (int)((long long)most * a.H[1] / heads)) : 0;
-    a.blocks[0] = max(1, most - a.blocks[1]);
+  const int most = min(kBwdBlocks * num_sms, kNormBwdMaxBlocks), heads = a.H[0] + a.H[1];
+  // Heads of a block, which share their angles: eight, or fewer where there would
+  // be less than eight groups of tokens a block.
+  int hpb = 8;
+  while (hpb > 1 && token_blocks * heads < 8LL * most * hpb) hpb /= 2;
+  for (int i = 0; i < 2; ++i) {
+    // The part's share of the blocks, a multiple of its splits, no more than it has
+    // groups for and at least one a split.
+    const int splits = (a.H[i] + hpb - 1) / hpb;
+    if (splits == 0) continue;
+    const long long share = (long long)most * a.H[i] / heads / splits;
+    a.blocks[i] = (int)(splits * max(1LL, min(share, token_blocks)));
+  }
+  if (a.blocks[0] + a.blocks[1] > kNormBwdMaxBlocks) {
+    // Thousands of heads: a block for all heads of a part.
+    hpb = max(a.H[0], a.H[1]);
+    for (int i = 0; i < 2; ++i) a.blocks[i] = a.H[i] ? (int)min(token_blocks, (long long)max(1, most / 2)) : 0;
   }
   auto k = dtype == 0
                ? (a.r.interleaved ? fa_qk_norm_bwd_kernel<__nv_bfloat16, true> : fa_qk_norm_bwd_kernel<__nv_bfloat16, false>)
