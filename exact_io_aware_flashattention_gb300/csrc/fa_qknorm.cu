@@ -50,7 +50,7 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-constexpr int kSlots = 4, kSlotsBwd = 4;
+constexpr int kSlots = 3, kSlotsBwd = 4;
 constexpr int kBwdBlocks = 3;                      // of the backward kernel an SM
 
 // grid: x over groups of tpb tokens, y over groups of hpb heads of q and then k.
@@ -267,12 +267,12 @@ __global__ void __launch_bounds__(kThreads) fa_qk_norm_dw_kernel(const NormRopeB
   if (lane == 0) a.dw[part][i] = (float)s;
 }
 
-// Heads per block of the forward: see fa_rope.cu.
+// Heads per block of the forward: as many as still leave 16 blocks an SM, so that
+// angles are formed for several heads at once.
 int heads_per_block(long long token_blocks, int heads, int num_sms) {
   const long long want = 16LL * num_sms;
   long long splits = (want + token_blocks - 1) / token_blocks;
-  const long long most = (heads + kSlots - 1) / kSlots;
-  if (splits > most) splits = most;
+  if (splits > heads) splits = heads;
   if (splits < 1) splits = 1;
   return (int)((heads + splits - 1) / splits);
 }
