@@ -37,35 +37,50 @@ __device__ __forceinline__ float round_to(float x) {
   return Pair2<T>::up(Pair2<T>::down(x, 0.f)).x;
 }
 
-// Codes of eight elements, in the two halves of K's word or in V's two halves.
-template <bool kKeys>
-__device__ __forceinline__ uint32_t encode8(const float (&x)[8], float s, float z) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int c = __float2int_rn(__fdiv_rn(__fsub_rn(x[e], z), s));
-    w |= place_code((uint32_t)min(max(c, 0), 15), kKeys ? e / 2 : e % 4) << 16 * (kKeys ? e % 2 : e / 4);
-  }
-  return s == 0.f ? 0u : w;
+// The group's s and what divides by it.
+struct Step {
+  float s, z, inv;
+  bool slow;         // so small or so large that the residual below may not be exact
+};
+template <typename T>
+__device__ __forceinline__ Step step_of(float lo, float hi) {
+  Step g;
+  g.s = round_to<T>(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+  if (!(g.s < INFINITY)) g.s = __int_as_float(0x7fffffff);
+  g.z = lo;
+  g.inv = __frcp_rn(g.s);
+  g.slow = g.s < 0x1p-90f || g.s > 0x1p90f;
+  return g;
 }
-template <int D, bool kKeys>
-__device__ __forceinline__ void store_codes(uint8_t* rec, int slot, int i, uint32_t w) {
-  if constexpr (kKeys) {
-    *reinterpret_cast<uint32_t*>(rec + Record<D>::k_word(slot, i)) = w;
-  } else {
-    *reinterpret_cast<uint16_t*>(rec + Record<D>::v_half(slot, i, 0)) = (uint16_t)w;
-    *reinterpret_cast<uint16_t*>(rec + Record<D>::v_half(slot, i, 1)) = (uint16_t)(w >> 16);
-  }
+// (x - z) / s, rounded as an IEEE division rounds it: with the reciprocal correctly
+// rounded, a quotient within a unit of the last place and its exact residual, one
+// more step gives the correctly rounded quotient (Markstein's theorem).  At most 15.
+__device__ __forceinline__ float quotient(float x, const Step& g) {
+  const float d = __fsub_rn(x, g.z);
+  if (g.slow) return g.s == 0.f ? 0.f : fminf(__fdiv_rn(d, g.s), 15.f);
+  const float q = __fmul_rn(d, g.inv);
+  return fminf(__fmaf_rn(__fmaf_rn(-q, g.s, d), g.inv, q), 15.f);
+}
+// Four codes in a half: the nearest whole numbers (ties to even) by adding 1.5 2^23,
+// their places by exact products; what passes bit 15 of place 2 goes to bits 0 and 1.
+__device__ __forceinline__ uint32_t half_of(float c0, float c1, float c2, float c3) {
+  constexpr float kRound = 12582912.f;
+  c0 = __fsub_rn(__fadd_rn(c0, kRound), kRound);
+  c1 = __fsub_rn(__fadd_rn(c1, kRound), kRound);
+  c2 = __fsub_rn(__fadd_rn(c2, kRound), kRound);
+  c3 = __fsub_rn(__fadd_rn(c3, kRound), kRound);
+  const float h = __fmaf_rn(c2, 16384.f, __fmaf_rn(c3, 1024.f, __fmaf_rn(c0, 64.f, __fmaf_rn(c1, 4.f, 8388608.f))));
+  const uint32_t w = __float_as_uint(h);           // the mantissa is the whole number
+  return (w & 0xffffu) | (w >> 16 & 3u);
 }
 
-// One row of K or V, 16 elements a thread, into its record.  All lanes of a row
-// take part.
+// One row of K or V, 16 elements a thread, into its record: codes to the addresses
+// of the thread's vectors, (s, z) by lane 0 to par.  All lanes of a row take part.
 template <typename T, int D, bool kKeys>
-__device__ __forceinline__ void store_row(const float (&xa)[8], const float (&xb)[8], const Chunk& ck, uint8_t* rec, int slot, int c,
-                                          bool live) {
+__device__ __forceinline__ void store_row(const float (&xa)[8], const float (&xb)[8], const Chunk& ck, uint8_t* ca, uint8_t* cb,
+                                          uint8_t* par, int c, bool live) {
   constexpr int kGroups = D / 64;
   const int ga = ck.e0 / 64, gb = ck.e1 / 64;
-  float lo[kGroups], hi[kGroups];
   float la = xa[0], ha = xa[0], lb = xb[0], hb = xb[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) {
@@ -74,102 +89,137 @@ __device__ __forceinline__ void store_row(const float (&xa)[8], const float (&xb
     lb = min_nan(lb, xb[i]);
     hb = max_nan(hb, xb[i]);
   }
+  Step g[kGroups];
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    lo[g] = min_nan(g == ga ? la : INFINITY, g == gb ? lb : INFINITY);
-    hi[g] = max_nan(g == ga ? ha : -INFINITY, g == gb ? hb : -INFINITY);
+  for (int k = 0; k < kGroups; ++k) {
+    float lo = min_nan(k == ga ? la : INFINITY, k == gb ? lb : INFINITY);
+    float hi = max_nan(k == ga ? ha : -INFINITY, k == gb ? hb : -INFINITY);
 #pragma unroll
     for (int d = 1; d < D / 16; d <<= 1) {
-      lo[g] = min_nan(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], d));
-      hi[g] = max_nan(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], d));
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, d));
     }
-  }
-  float s[kGroups];
-  uint32_t p[kGroups];
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    s[g] = round_to<T>(__fdiv_rn(__fsub_rn(hi[g], lo[g]), 15.f));
-    p[g] = Pair2<T>::down(s[g], lo[g]);
+    g[k] = step_of<T>(lo, hi);
   }
   if (!live) return;
-  const float sa = kGroups == 1 || ga == 0 ? s[0] : s[kGroups - 1], za = kGroups == 1 || ga == 0 ? lo[0] : lo[kGroups - 1];
-  const float sb = kGroups == 1 || gb == 0 ? s[0] : s[kGroups - 1], zb = kGroups == 1 || gb == 0 ? lo[0] : lo[kGroups - 1];
-  store_codes<D, kKeys>(rec, slot, ck.e0 / 8, encode8<kKeys>(xa, sa, za));
-  store_codes<D, kKeys>(rec, slot, ck.e1 / 8, encode8<kKeys>(xb, sb, zb));
-  if (c == 0) {
-    uint8_t* par = rec + (kKeys ? Record<D>::kKp : Record<D>::kVp);
+  auto encode = [&](const float (&x)[8], const Step& s, uint8_t* to) {
+    float q[8];
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) reinterpret_cast<uint32_t*>(par + slot * Record<D>::kPar)[g] = p[g];
+    for (int e = 0; e < 8; ++e) q[e] = quotient(x[e], s);
+    if constexpr (kKeys) {
+      *reinterpret_cast<uint32_t*>(to) = half_of(q[0], q[2], q[4], q[6]) | half_of(q[1], q[3], q[5], q[7]) << 16;
+    } else {
+      *reinterpret_cast<uint16_t*>(to) = (uint16_t)half_of(q[0], q[1], q[2], q[3]);
+      *reinterpret_cast<uint16_t*>(to + 4) = (uint16_t)half_of(q[4], q[5], q[6], q[7]);
+    }
+  };
+  encode(xa, g[kGroups > 1 && ga ? kGroups - 1 : 0], ca);
+  encode(xb, g[kGroups > 1 && gb ? kGroups - 1 : 0], cb);
+  if (c == 0) {
+    if constexpr (kGroups == 2)
+      *reinterpret_cast<uint2*>(par) = make_uint2(Pair2<T>::down(g[0].s, g[0].z), Pair2<T>::down(g[1].s, g[1].z));
+    else
+      *reinterpret_cast<uint32_t*>(par) = Pair2<T>::down(g[0].s, g[0].z);
   }
 }
 
 // grid: x over groups of kThreads / (D/16) tokens, y over groups of hpb heads of q,
-// then k, then v.
+// then k, then v.  The first rows are on their way while the slot is looked up and
+// the angles are formed.
+constexpr int kSlots = 3;
 template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(kThreads) fa_append4_kernel(const Append4Args a, int hpb, const DevStatus st) {
+__global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Args a, int hpb, const DevStatus st) {
+  using R = Record<D>;
   __shared__ Pairs pairs;
+  __shared__ uint4 ring[kSlots][2][kThreads];
   constexpr int kLanes = D / 16, kTokens = kThreads / kLanes;
   launch_dependents();
   wait_for_previous();
-  load_pairs<kThreads>(a.r, pairs, st);
-  if (a.cu && blockIdx.y == 0) check_offsets<kThreads>(a, st);
-  __syncthreads();
   const int lt = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
   const long long t = (long long)blockIdx.x * kTokens + lt;
-  int page = 0, slot = 0;
-  const bool live = t < a.T && place_token(a, (int)t, st, page, slot);
-  const long long tt = live ? t : 0;
   const Chunk ck = chunk_of<kInter>(c, a.r.rot);
   const Chunk plain{16 * c, 16 * c + 8, false};
   const int Hkv = a.kv.Hkv, h0 = blockIdx.y * hpb, h1 = min(h0 + hpb, a.Hq + 2 * Hkv);
+  auto copy = [&](int h, int slot) {
+    if (t < a.T && h < h1) {
+      const bool v = h >= a.Hq + Hkv;
+      const T* x = h < a.Hq ? static_cast<const T*>(a.q.p) + t * a.q.sn + h * a.q.sh
+                   : !v     ? static_cast<const T*>(a.k.p) + t * a.k.sn + (h - a.Hq) * a.k.sh
+                            : static_cast<const T*>(a.v.p) + t * a.v.sn + (h - a.Hq - Hkv) * a.v.sh;
+      copy16(&ring[slot][0][threadIdx.x], x + (v ? plain.e0 : ck.e0));
+      copy16(&ring[slot][1][threadIdx.x], x + (v ? plain.e1 : ck.e1));
+    }
+    copies_end();
+  };
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) copy(h0 + s, s);
+  load_pairs<kThreads>(a.r, pairs, st);
+  if (a.cu && blockIdx.y == 0) check_offsets<kThreads>(a, st);
+  __syncthreads();
+  int page = 0, place = 0;
+  const bool live = t < a.T && place_token(a, (int)t, st, page, place);
   float cs[8] = {}, sn[8] = {};
   if (live && ck.turned && h0 < a.Hq + Hkv) load_fine_angles(a.r, pairs, a.r.pos + t, c, cs, sn);
-  uint8_t* at = static_cast<uint8_t*>(a.kv.k) + page * a.kv.s_page + (slot >> 4) * (long long)Record<D>::kBytes;
-  const int first[4] = {0, a.Hq, a.Hq + Hkv, a.Hq + 2 * Hkv};
+  uint8_t* at = static_cast<uint8_t*>(a.kv.k) + page * a.kv.s_page + (place >> 4) * (long long)R::kBytes;
+  place &= 15;
+  int slot = 0, h = h0;
+#pragma unroll 1
   for (int part = 0; part < 3; ++part) {                  // q, k, v
-    const int from = max(h0 - first[part], 0), to = min(h1, first[part + 1]) - first[part];
-    if (from >= to) continue;
-    const RowView& in = part == 0 ? a.q : part == 1 ? a.k : a.v;
-    const Chunk& my = part == 2 ? plain : ck;
-    const T* x = static_cast<const T*>(in.p) + tt * in.sn;
+    const int first = part == 0 ? 0 : part == 1 ? a.Hq : a.Hq + Hkv, end = min(h1, part == 0 ? a.Hq : first + Hkv);
+    if (h >= end) continue;
+    const Chunk my = part == 2 ? plain : ck;
     const bool normed = a.n.on && part < 2;
     float wa[8] = {}, wb[8] = {};
     if (normed) {
       load_weights<T>(part ? a.n.wk : a.n.wq, a.n.fp32, my.e0, wa);
       load_weights<T>(part ? a.n.wk : a.n.wq, a.n.fp32, my.e1, wb);
     }
-    for (int h = from; h < to; ++h) {
+    // Where the next head's row goes.
+    T* y = part == 0 ? static_cast<T*>(a.q_out.p) + t * a.q_out.sn + h * a.q_out.sh : nullptr;
+    uint8_t* rec = at + (h - first) * a.kv.s_head;
+    const int ca = part == 1 ? R::k_word(place, my.e0 / 8) : R::v_half(place, my.e0 / 8, 0);
+    const int cb = part == 1 ? R::k_word(place, my.e1 / 8) : R::v_half(place, my.e1 / 8, 0);
+#pragma unroll 1
+    for (; h < end; ++h) {
+      copies_wait<kSlots - 1>();
       uint4 va = make_uint4(0, 0, 0, 0), vb = va;
       if (live) {
-        va = *reinterpret_cast<const uint4*>(x + h * in.sh + my.e0);
-        vb = *reinterpret_cast<const uint4*>(x + h * in.sh + my.e1);
+        va = ring[slot][0][threadIdx.x];
+        vb = ring[slot][1][threadIdx.x];
       }
       float xa[8], xb[8];
       up8<T>(va, xa);
       up8<T>(vb, xb);
-      if (normed) {
-        const float r = rsqrtf(sum_over(sum_of_squares(xa, xb), kLanes) * (1.f / D) + a.n.eps);
+      if (part < 2) {
+        if (normed) {
+          const float r = rsqrtf(sum_over(sum_of_squares(xa, xb), kLanes) * (1.f / D) + a.n.eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          xa[i] = xa[i] * r * wa[i];
-          xb[i] = xb[i] * r * wb[i];
+          for (int i = 0; i < 8; ++i) {
+            xa[i] = xa[i] * r * wa[i];
+            xb[i] = xb[i] * r * wb[i];
+          }
         }
+        if (my.turned) turn8<kInter>(xa, xb, cs, sn);
+        va = down8<T>(xa);
+        vb = down8<T>(xb);
       }
-      if (my.turned) turn8<kInter>(xa, xb, cs, sn);
-      va = down8<T>(xa);
-      vb = down8<T>(xb);
+      copy(h + kSlots, slot);
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
       if (part == 0) {
-        T* y = static_cast<T*>(a.q_out.p) + tt * a.q_out.sn + h * a.q_out.sh;
         if (live) {
-          *reinterpret_cast<uint4*>(y + my.e0) = va;
-          *reinterpret_cast<uint4*>(y + my.e1) = vb;
+          __stcs(reinterpret_cast<uint4*>(y + my.e0), va);
+          __stcs(reinterpret_cast<uint4*>(y + my.e1), vb);
         }
+        y += a.q_out.sh;
       } else {
-        up8<T>(va, xa);
-        up8<T>(vb, xb);
-        uint8_t* rec = at + h * a.kv.s_head;
-        if (part == 1) store_row<T, D, true>(xa, xb, my, rec, slot & 15, c, live);
-        else store_row<T, D, false>(xa, xb, my, rec, slot & 15, c, live);
+        if (part == 1) {
+          up8<T>(va, xa);
+          up8<T>(vb, xb);
+          store_row<T, D, true>(xa, xb, my, rec + ca, rec + cb, rec + R::kKp + place * R::kPar, c, live);
+        } else {
+          store_row<T, D, false>(xa, xb, my, rec + ca, rec + cb, rec + R::kVp + place * R::kPar, c, live);
+        }
+        rec += a.kv.s_head;
       }
     }
   }

@@ -58,10 +58,7 @@ cudaError_t launch_norm_rope_bwd(int dtype, NormRopeBwdArgs a, const DevStatus& 
 // the slots (c, c + 4) and then (c + 8, c + 12) the elements 8 r .. 8 r + 3 and then
 // the other four, the first slot in the lower half.
 #ifdef __CUDACC__
-// A code in place n of its half, and back.
-__device__ __forceinline__ uint32_t place_code(uint32_t c, int n) {
-  return n == 0 ? c << 6 : n == 1 ? c << 2 : n == 2 ? c >> 2 | (c & 3) << 14 : c << 10;
-}
+// The code in place n of a half.
 __device__ __forceinline__ uint32_t code_at(uint32_t h, int n) {
   return (n == 0 ? h >> 6 : n == 1 ? h >> 2 : n == 2 ? h << 2 | (h >> 14 & 3) : h >> 10) & 15u;
 }

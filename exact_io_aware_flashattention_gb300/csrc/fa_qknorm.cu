@@ -38,18 +38,6 @@ __host__ __device__ inline int tokens_per_block(int d) {
   return kThreads / p;
 }
 
-// Asynchronous copies of a thread's own vectors into its own places of a ring in
-// shared memory, kSlots rows deep: what a row needs is on its way while others are
-// worked on, without registers, and nobody else waits for it.
-__device__ __forceinline__ void copy16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
-}
-
 constexpr int kSlots = 3, kSlotsBwd = 4;
 constexpr int kBwdBlocks = 3;                      // of the backward kernel an SM
 

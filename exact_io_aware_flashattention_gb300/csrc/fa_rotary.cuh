@@ -189,6 +189,18 @@ __device__ __forceinline__ void load_fine_angles(const RotaryArgs& r, const Pair
   }
 }
 
+// Asynchronous copies of a thread's own vectors into its own places of a ring in
+// shared memory, some rows deep: what a row needs is on its way while others are
+// worked on, without registers, and nobody else waits for it.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
 // Offsets of new tokens run from 0 and upwards, to T at most.  The first blocks
 // look at all of them: a pair out of order may leave every token with a
 // sequence, but not with its own.
