@@ -20,16 +20,21 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// NaN if either is.
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// The smaller of each half, NaN if either is.
+template <typename T>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (sizeof(T) == 2 && Pair2<T>::kBf16) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+// (smallest, -largest) of a vector, as a pair whose halves grow smaller alike.
+template <typename T>
+__device__ __forceinline__ uint32_t ends_of(const uint4& v) {
+  constexpr uint32_t kSign = 0x80008000u;
+  const uint32_t lo = min2<T>(min2<T>(v.x, v.y), min2<T>(v.z, v.w));
+  const uint32_t hi = min2<T>(min2<T>(v.x ^ kSign, v.y ^ kSign), min2<T>(v.z ^ kSign, v.w ^ kSign));
+  return min2<T>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
 }
 
 template <typename T>
@@ -37,89 +42,99 @@ __device__ __forceinline__ float round_to(float x) {
   return Pair2<T>::up(Pair2<T>::down(x, 0.f)).x;
 }
 
-// The group's s and what divides by it.
+// x / y for a correctly rounded reciprocal inv of y, as an IEEE division rounds it:
+// with a quotient within a unit of the last place and its exact residual, one more
+// step gives the correctly rounded quotient (Markstein's theorem).
+__device__ __forceinline__ float quotient(float x, float y, float inv) {
+  const float q = __fmul_rn(x, inv);
+  return __fmaf_rn(__fmaf_rn(-q, y, x), inv, q);
+}
+// A group's s and z, from (smallest, -largest).
 struct Step {
   float s, z, inv;
-  bool slow;         // so small or so large that the residual below may not be exact
+  bool plain;        // the residuals above are exact: s is not extremely small or large
 };
 template <typename T>
-__device__ __forceinline__ Step step_of(float lo, float hi) {
+__device__ __forceinline__ Step step_of(uint32_t ends) {
+  const float2 e = Pair2<T>::up(ends);
+  const float range = __fsub_rn(-e.y, e.x);
   Step g;
-  g.s = round_to<T>(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-  if (!(g.s < INFINITY)) g.s = __int_as_float(0x7fffffff);
-  g.z = lo;
+  g.plain = range > 0x1p-90f && range < 0x1p90f;
+  g.s = round_to<T>(g.plain ? quotient(range, 15.f, 1.f / 15.f) : __fdiv_rn(range, 15.f));
+  if (!(range < INFINITY)) g.s = __int_as_float(0x7fffffff);
+  g.z = e.x;
   g.inv = __frcp_rn(g.s);
-  g.slow = g.s < 0x1p-90f || g.s > 0x1p90f;
+  // (An s of fp16's subnormal steps may be so far from range / 15 that a quotient
+  // passes 15.5; so it is not plain either.)
+  g.plain = g.plain && g.s >= (Pair2<T>::kBf16 ? 0x1p-90f : 0x1p-14f);
   return g;
 }
-// (x - z) / s, rounded as an IEEE division rounds it: with the reciprocal correctly
-// rounded, a quotient within a unit of the last place and its exact residual, one
-// more step gives the correctly rounded quotient (Markstein's theorem).  At most 15.
-__device__ __forceinline__ float quotient(float x, const Step& g) {
-  const float d = __fsub_rn(x, g.z);
-  if (g.slow) return g.s == 0.f ? 0.f : fminf(__fdiv_rn(d, g.s), 15.f);
-  const float q = __fmul_rn(d, g.inv);
-  return fminf(__fmaf_rn(__fmaf_rn(-q, g.s, d), g.inv, q), 15.f);
-}
-// Four codes in a half: the nearest whole numbers (ties to even) by adding 1.5 2^23,
-// their places by exact products; what passes bit 15 of place 2 goes to bits 0 and 1.
+// Four codes, quotients of 0 .. 15.1, in a half: the nearest whole numbers (ties to
+// even) in the last bits of their sums with 1.5 2^23, their places by products; what
+// passes bit 15 of place 2 goes to bits 0 and 1.
 __device__ __forceinline__ uint32_t half_of(float c0, float c1, float c2, float c3) {
   constexpr float kRound = 12582912.f;
-  c0 = __fsub_rn(__fadd_rn(c0, kRound), kRound);
-  c1 = __fsub_rn(__fadd_rn(c1, kRound), kRound);
-  c2 = __fsub_rn(__fadd_rn(c2, kRound), kRound);
-  c3 = __fsub_rn(__fadd_rn(c3, kRound), kRound);
-  const float h = __fmaf_rn(c2, 16384.f, __fmaf_rn(c3, 1024.f, __fmaf_rn(c0, 64.f, __fmaf_rn(c1, 4.f, 8388608.f))));
-  const uint32_t w = __float_as_uint(h);           // the mantissa is the whole number
-  return (w & 0xffffu) | (w >> 16 & 3u);
+  constexpr uint32_t kBits = 0x4b400000u;
+  const uint32_t w = __float_as_uint(__fadd_rn(c0, kRound)) * 64u + __float_as_uint(__fadd_rn(c1, kRound)) * 4u +
+                     __float_as_uint(__fadd_rn(c2, kRound)) * 16384u + __float_as_uint(__fadd_rn(c3, kRound)) * 1024u -
+                     kBits * (64u + 4u + 16384u + 1024u);
+  return (w & 0xffffu) | (w >> 16);
+}
+// Eight codes: in the two halves of K's word or in V's two halves.
+template <typename T, bool kKeys>
+__device__ __forceinline__ void encode8(const uint4& v, const Step& g, uint8_t* to) {
+  float x[8];
+  up8<T>(v, x);
+  if (g.plain) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = quotient(__fsub_rn(x[e], g.z), g.s, g.inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = g.s > 0.f ? fminf(__fdiv_rn(__fsub_rn(x[e], g.z), g.s), 15.f) : 0.f;
+  }
+  if constexpr (kKeys) {
+    *reinterpret_cast<uint32_t*>(to) = half_of(x[0], x[2], x[4], x[6]) | half_of(x[1], x[3], x[5], x[7]) << 16;
+  } else {
+    *reinterpret_cast<uint16_t*>(to) = (uint16_t)half_of(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint16_t*>(to + 4) = (uint16_t)half_of(x[4], x[5], x[6], x[7]);
+  }
 }
 
-// One row of K or V, 16 elements a thread, into its record: codes to the addresses
-// of the thread's vectors, (s, z) by lane 0 to par.  All lanes of a row take part.
+// One row of K or V, two vectors a thread, into its record: codes to the addresses of
+// the vectors, (s, z) to par.  All lanes of a row take part.  own: a thread's vectors
+// are of the group of its four lanes.
 template <typename T, int D, bool kKeys>
-__device__ __forceinline__ void store_row(const float (&xa)[8], const float (&xb)[8], const Chunk& ck, uint8_t* ca, uint8_t* cb,
+__device__ __forceinline__ void store_row(const uint4& va, const uint4& vb, const Chunk& ck, bool own, uint8_t* ca, uint8_t* cb,
                                           uint8_t* par, int c, bool live) {
-  constexpr int kGroups = D / 64;
-  const int ga = ck.e0 / 64, gb = ck.e1 / 64;
-  float la = xa[0], ha = xa[0], lb = xb[0], hb = xb[0];
+  constexpr uint32_t kNone = Pair2<T>::kBf16 ? 0x7f807f80u : 0x7c007c00u;         // infinities
+  const uint32_t pa = ends_of<T>(va), pb = ends_of<T>(vb);
+  if (own) {
+    uint32_t p = min2<T>(pa, pb);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    la = min_nan(la, xa[i]);
-    ha = max_nan(ha, xa[i]);
-    lb = min_nan(lb, xb[i]);
-    hb = max_nan(hb, xb[i]);
+    for (int d = 1; d < 4; d <<= 1) p = min2<T>(p, __shfl_xor_sync(0xffffffffu, p, d));
+    if (!live) return;
+    const Step g = step_of<T>(p);
+    encode8<T, kKeys>(va, g, ca);
+    encode8<T, kKeys>(vb, g, cb);
+    if ((c & 3) == 0) *reinterpret_cast<uint32_t*>(par + c) = Pair2<T>::down(g.s, g.z);
+    return;
   }
-  Step g[kGroups];
+  if constexpr (D == 128) {
+    const int ga = ck.e0 / 64, gb = ck.e1 / 64;
+    uint32_t p[2];
 #pragma unroll
-  for (int k = 0; k < kGroups; ++k) {
-    float lo = min_nan(k == ga ? la : INFINITY, k == gb ? lb : INFINITY);
-    float hi = max_nan(k == ga ? ha : -INFINITY, k == gb ? hb : -INFINITY);
+    for (int k = 0; k < 2; ++k) {
+      p[k] = min2<T>(k == ga ? pa : kNone, k == gb ? pb : kNone);
 #pragma unroll
-    for (int d = 1; d < D / 16; d <<= 1) {
-      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+      for (int d = 1; d < 8; d <<= 1) p[k] = min2<T>(p[k], __shfl_xor_sync(0xffffffffu, p[k], d));
     }
-    g[k] = step_of<T>(lo, hi);
-  }
-  if (!live) return;
-  auto encode = [&](const float (&x)[8], const Step& s, uint8_t* to) {
-    float q[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = quotient(x[e], s);
-    if constexpr (kKeys) {
-      *reinterpret_cast<uint32_t*>(to) = half_of(q[0], q[2], q[4], q[6]) | half_of(q[1], q[3], q[5], q[7]) << 16;
-    } else {
-      *reinterpret_cast<uint16_t*>(to) = (uint16_t)half_of(q[0], q[1], q[2], q[3]);
-      *reinterpret_cast<uint16_t*>(to + 4) = (uint16_t)half_of(q[4], q[5], q[6], q[7]);
-    }
-  };
-  encode(xa, g[kGroups > 1 && ga ? kGroups - 1 : 0], ca);
-  encode(xb, g[kGroups > 1 && gb ? kGroups - 1 : 0], cb);
-  if (c == 0) {
-    if constexpr (kGroups == 2)
-      *reinterpret_cast<uint2*>(par) = make_uint2(Pair2<T>::down(g[0].s, g[0].z), Pair2<T>::down(g[1].s, g[1].z));
-    else
-      *reinterpret_cast<uint32_t*>(par) = Pair2<T>::down(g[0].s, g[0].z);
+    if (!live) return;
+    const Step a = step_of<T>(p[ga]), b = step_of<T>(p[gb]);
+    encode8<T, kKeys>(va, a, ca);
+    encode8<T, kKeys>(vb, b, cb);
+    // Some lane has a vector of each group; lane 0's first is of group 0.
+    if (c == 0) *reinterpret_cast<uint32_t*>(par) = Pair2<T>::down(a.s, a.z);
+    if (c == 7) *reinterpret_cast<uint32_t*>(par + 4) = Pair2<T>::down(b.s, b.z);
   }
 }
 
@@ -160,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
   const bool live = t < a.T && place_token(a, (int)t, st, page, place);
   float cs[8] = {}, sn[8] = {};
   if (live && ck.turned && h0 < a.Hq + Hkv) load_fine_angles(a.r, pairs, a.r.pos + t, c, cs, sn);
+  // K's vectors: halves of the turned elements, or neighbours.
+  const bool own = D == 64 || kInter || a.r.rot == 0 || a.r.rot == 64;
   uint8_t* at = static_cast<uint8_t*>(a.kv.k) + page * a.kv.s_page + (place >> 4) * (long long)R::kBytes;
   place &= 15;
   int slot = 0, h = h0;
@@ -187,10 +204,10 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
         va = ring[slot][0][threadIdx.x];
         vb = ring[slot][1][threadIdx.x];
       }
-      float xa[8], xb[8];
-      up8<T>(va, xa);
-      up8<T>(vb, xb);
-      if (part < 2) {
+      if (part < 2 && (normed || a.r.rot)) {
+        float xa[8], xb[8];
+        up8<T>(va, xa);
+        up8<T>(vb, xb);
         if (normed) {
           const float r = rsqrtf(sum_over(sum_of_squares(xa, xb), kLanes) * (1.f / D) + a.n.eps);
 #pragma unroll
@@ -213,11 +230,9 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
         y += a.q_out.sh;
       } else {
         if (part == 1) {
-          up8<T>(va, xa);
-          up8<T>(vb, xb);
-          store_row<T, D, true>(xa, xb, my, rec + ca, rec + cb, rec + R::kKp + place * R::kPar, c, live);
+          store_row<T, D, true>(va, vb, my, own, rec + ca, rec + cb, rec + R::kKp + place * R::kPar, c, live);
         } else {
-          store_row<T, D, false>(xa, xb, my, rec + ca, rec + cb, rec + R::kVp + place * R::kPar, c, live);
+          store_row<T, D, false>(va, vb, my, true, rec + ca, rec + cb, rec + R::kVp + place * R::kPar, c, live);
         }
         rec += a.kv.s_head;
       }

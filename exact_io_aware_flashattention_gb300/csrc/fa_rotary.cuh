@@ -16,6 +16,7 @@ template <typename T>
 struct Pair2;
 template <>
 struct Pair2<__nv_bfloat16> {
+  static constexpr bool kBf16 = true;
   static __device__ __forceinline__ float2 up(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
@@ -23,6 +24,7 @@ struct Pair2<__nv_bfloat16> {
 };
 template <>
 struct Pair2<__half> {
+  static constexpr bool kBf16 = false;
   static __device__ __forceinline__ float2 up(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
   }
