@@ -240,44 +240,100 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
   }
 }
 
-// The last N keys of each sequence: a thread a word of eight elements of K and V;
-// grid: x over (key, word), y over (sequence, kv head).
+// c / 8 of the codes in place 0 of a word's halves, as fp16 by one product of the
+// subnormal c 2^-18; place 1 after a shift by 4, places 2 and 3 with bytes swapped.
+__device__ __forceinline__ float2 codes8(uint32_t w) {
+  uint32_t h;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(w & 0x03c003c0u), "r"(0x78007800u));       // 2^15
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ float2 codes8(uint32_t w, int place) {
+  if (place & 2) w = __byte_perm(w, w, 0x2301);
+  return codes8(place & 1 ? w << 4 : w);
+}
+
+// The last N keys of each sequence.  A warp a record of 16 keys, all its loads first:
+// K by words, a lane eight elements of a row; V by the 16 bytes that a lane has of a
+// group, eight elements of four rows.  grid: x over records, y over (sequence, kv head).
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) fa_read4_kernel(const Read4Args a, const DevStatus st) {
+  using R = Record<D>;
+  constexpr int kG = D / 64, kWords = D / 8, kRows = 32 / kWords;      // rows of K a warp reads at once
   launch_dependents();
   wait_for_previous();
-  constexpr int kWords = D / 8;
-  const int i = threadIdx.x % kWords, n = blockIdx.x * (kThreads / kWords) + threadIdx.x / kWords;
-  if (n >= a.N) return;
+  const int lane = threadIdx.x % 32, w = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   for (long long bh = blockIdx.y; bh < (long long)a.B * a.kv.Hkv; bh += gridDim.y) {
-    const int b = (int)(bh / a.kv.Hkv), h = (int)(bh - (long long)b * a.kv.Hkv), len = a.seq_lens[b];
-    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    const int b = (int)(bh / a.kv.Hkv), h = (int)(bh - (long long)b * a.kv.Hkv);
+    int len = a.seq_lens[b];
     if (len < 0 || len > (long long)a.table.cols * a.kv.page_size) {
-      record_error(st, kErrBadIndex, kSiteReadLen);
-    } else if (const int j = len - a.N + n; j >= 0) {
-      const int col = j / a.kv.page_size, slot = j - col * a.kv.page_size, page = a.table.pages[b * a.table.stride + col];
-      if (page < 0 || page >= a.kv.num_pages) {
-        record_error(st, kErrBadIndex, kSiteReadPage);
-      } else {
-        const uint8_t* rec = static_cast<const uint8_t*>(a.kv.k) + page * a.kv.s_page + h * a.kv.s_head +
-                             (slot >> 4) * (long long)Record<D>::kBytes;
-        const int s = slot & 15, g = i / 8;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t h0 = kv ? *reinterpret_cast<const uint16_t*>(rec + Record<D>::v_half(s, i, 0))
-                                 : *reinterpret_cast<const uint32_t*>(rec + Record<D>::k_word(s, i));
-          const uint32_t h1 = kv ? *reinterpret_cast<const uint16_t*>(rec + Record<D>::v_half(s, i, 1)) : h0 >> 16;
-          const float2 p = Pair2<T>::up(
-              reinterpret_cast<const uint32_t*>(rec + (kv ? Record<D>::kVp : Record<D>::kKp) + s * Record<D>::kPar)[g]);
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = p.y + p.x * (float)(kv ? code_at(e < 4 ? h0 : h1, e % 4) : code_at(e % 2 ? h1 : h0, e / 2));
-          (kv ? v : k) = down8<T>(x);
-        }
-      }
+      if (lane == 0) record_error(st, kErrBadIndex, kSiteReadLen);
+      len = 0;
     }
-    *reinterpret_cast<uint4*>(static_cast<T*>(a.k.p) + b * a.k.sb + h * a.k.sh + n * a.k.sn + 8 * i) = k;
-    *reinterpret_cast<uint4*>(static_cast<T*>(a.v.p) + b * a.v.sb + h * a.v.sh + n * a.v.sn + 8 * i) = v;
+    const int from = max(len - a.N, 0);            // first key that is read
+    T* ko = static_cast<T*>(a.k.p) + b * a.k.sb + h * a.k.sh;
+    T* vo = static_cast<T*>(a.v.p) + b * a.v.sb + h * a.v.sh;
+    // Rows in front of the sequence.
+    const int zeros = min(a.N - len, 16 * w + 16);
+    for (int n = 16 * w + lane / kWords; n < zeros; n += 32 / kWords) {
+      const int e = lane % kWords * 8;
+      *reinterpret_cast<uint4*>(ko + n * a.k.sn + e) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(vo + n * a.v.sn + e) = make_uint4(0, 0, 0, 0);
+    }
+    const int key0 = (from & ~15) + 16 * w;
+    if (key0 >= len) continue;
+    const int col = key0 / a.kv.page_size, slot0 = key0 - col * a.kv.page_size, page = a.table.pages[b * a.table.stride + col];
+    if (page < 0 || page >= a.kv.num_pages) {
+      if (lane == 0) record_error(st, kErrBadIndex, kSiteReadPage);
+      continue;
+    }
+    const uint8_t* rec = static_cast<const uint8_t*>(a.kv.k) + page * a.kv.s_page + h * a.kv.s_head +
+                         (slot0 >> 4) * (long long)R::kBytes;
+    const int row = lane / kWords, i = lane % kWords, r = lane >> 2, c = lane & 3;
+    uint32_t kw[16 / kRows], kp[16 / kRows], vp[4][kG];
+    uint4 vw[kG];
+#pragma unroll
+    for (int u = 0; u < 16 / kRows; ++u) {
+      const int s = u * kRows + row;
+      kw[u] = *reinterpret_cast<const uint32_t*>(rec + R::k_word(s, i));
+      kp[u] = *reinterpret_cast<const uint32_t*>(rec + R::kKp + s * R::kPar + i / 8 * 4);
+    }
+#pragma unroll
+    for (int k = 0; k < kG; ++k) {
+      vw[k] = *reinterpret_cast<const uint4*>(rec + R::kV + k * 512 + lane * 16);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) vp[u][k] = *reinterpret_cast<const uint32_t*>(rec + R::kVp + (c + 4 * u) * R::kPar + k * 4);
+    }
+    ko += (long long)(a.N - len) * a.k.sn;         // row of key 0
+    vo += (long long)(a.N - len) * a.v.sn;
+#pragma unroll
+    for (int u = 0; u < 16 / kRows; ++u) {
+      const int key = key0 + u * kRows + row;
+      const float2 p = Pair2<T>::up(kp[u]);
+      uint32_t y[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float2 x = codes8(kw[u], n);
+        y[n] = Pair2<T>::down(fmaf(x.x, 8.f * p.x, p.y), fmaf(x.y, 8.f * p.x, p.y));
+      }
+      if (key >= from && key < len) __stcs(reinterpret_cast<uint4*>(ko + key * a.k.sn + 8 * i), make_uint4(y[0], y[1], y[2], y[3]));
+    }
+#pragma unroll
+    for (int k = 0; k < kG; ++k)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {                // slots c and c + 4, then c + 8 and c + 12
+        const uint32_t words[2] = {g ? vw[k].z : vw[k].x, g ? vw[k].w : vw[k].y};
+        const float2 p0 = Pair2<T>::up(vp[2 * g][k]), p1 = Pair2<T>::up(vp[2 * g + 1][k]);
+        float x0[8], x1[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const float2 x = codes8(words[n / 4], n % 4);
+          x0[n] = fmaf(x.x, 8.f * p0.x, p0.y);
+          x1[n] = fmaf(x.y, 8.f * p1.x, p1.y);
+        }
+        const int key = key0 + c + 8 * g, e = 64 * k + 8 * r;
+        if (key >= from && key < len) __stcs(reinterpret_cast<uint4*>(vo + key * a.v.sn + e), down8<T>(x0));
+        if (key + 4 >= from && key + 4 < len) __stcs(reinterpret_cast<uint4*>(vo + (key + 4) * a.v.sn + e), down8<T>(x1));
+      }
   }
 }
 
@@ -301,8 +357,8 @@ cudaError_t launch_append(const Append4Args& a, const DevStatus& st, int num_sms
 
 template <typename T, int D>
 cudaError_t launch_read(const Read4Args& a, const DevStatus& st, cudaStream_t stream) {
-  constexpr int kKeys = kThreads / (D / 8);
-  const dim3 grid((unsigned)((a.N + kKeys - 1) / kKeys), (unsigned)min((long long)a.B * a.kv.Hkv, 65535LL));
+  const long long records = (a.N + 15LL) / 16 + 1;       // that N keys may lie in
+  const dim3 grid((unsigned)((records + kThreads / 32 - 1) / (kThreads / 32)), (unsigned)min((long long)a.B * a.kv.Hkv, 65535LL));
   return launch_after(fa_read4_kernel<T, D>, grid, kThreads, 0, 1, stream, a, st);
 }
 

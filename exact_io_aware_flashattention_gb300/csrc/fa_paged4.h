@@ -57,12 +57,6 @@ cudaError_t launch_norm_rope_bwd(int dtype, NormRopeBwdArgs a, const DevStatus& 
 // elements 8 r .. 8 r + 7 of the slots c, c + 4, c + 8 and c + 12: four words, of
 // the slots (c, c + 4) and then (c + 8, c + 12) the elements 8 r .. 8 r + 3 and then
 // the other four, the first slot in the lower half.
-#ifdef __CUDACC__
-// The code in place n of a half.
-__device__ __forceinline__ uint32_t code_at(uint32_t h, int n) {
-  return (n == 0 ? h >> 6 : n == 1 ? h >> 2 : n == 2 ? h << 2 | (h >> 14 & 3) : h >> 10) & 15u;
-}
-#endif
 template <int D>
 struct Record {
   static constexpr int kRow = D / 2;                 // bytes of a row's codes
