@@ -452,6 +452,7 @@ class _NotBuilt:
     def _none(*args):
         return None
     rope = paged_append = paged_decode = paged_evict = _none
+    qk_norm_rope = qk_norm_rope_backward = paged4_append = paged4_read = paged4_decode = _none
 
 
 _native = None
@@ -474,7 +475,9 @@ def _load_native():
             if getattr(m, "key", None) == _build.native_key():
                 m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                     lib.fa_rope, lib.fa_paged_append, lib.fa_paged_decode, lib.fa_paged_decode_workspace_bytes,
-                    lib.fa_paged_evict)))
+                    lib.fa_paged_evict, lib.fa_qk_norm_rope, lib.fa_qk_norm_rope_bwd,
+                    lib.fa_qk_norm_rope_bwd_workspace_bytes, lib.fa_paged4_append, lib.fa_paged4_read,
+                    lib.fa_paged4_decode, lib.fa_paged4_decode_workspace_bytes)))
                 _native = m
         except ImportError:          # built against another torch
             pass
@@ -909,6 +912,10 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions=None, inv_freq=None, axes=N
     as by ``rope``; without ``positions``, ``inv_freq`` and ``axes`` they are normed
     only.  Outputs may be the inputs themselves.  Returns (q_out, k_out), or q_out
     without k.  See fa_qk_norm_rope."""
+    if stream is None:
+        r = (_native or _load_native()).qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, axes, eps, interleaved, q_out, k_out)
+        if r is not None:
+            return _answer(r, "fa_qk_norm_rope")
     return _qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, axes, eps, interleaved, q_out, k_out, stream)
 
 
@@ -946,6 +953,11 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions=None, inv_
     dq_weight) without k (dk None too); the weights' gradients are fp32 [d], None
     for weights that are None.  ``dq_out`` and ``dk_out`` may be dq and dk
     themselves.  See fa_qk_norm_rope_bwd."""
+    if stream is None:
+        r = (_native or _load_native()).qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, axes, eps, interleaved,
+                                                              dq_out, dk_out, dq_weight, dk_weight, workspace)
+        if r is not None:
+            return _answer(r, "fa_qk_norm_rope_bwd")
     return _qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, axes, eps, interleaved, dq_out,
                                   dk_out, dq_weight, dk_weight, workspace, stream)
 
@@ -1052,6 +1064,11 @@ def paged4_append(cache, block_table, seq_lens, k, v, cu_seqlens=None, q=None, q
     ``qk_norm_rope``); with ``positions`` [n_axes,T], ``inv_freq`` and ``axes`` they are
     then turned.  Returns q so (into ``q_out``, which may be q), or None without q.
     A cache's calls must all have the same type.  See fa_paged4_append."""
+    if stream is None:
+        r = (_native or _load_native()).paged4_append(cache, block_table, seq_lens, k, v, cu_seqlens, q, q_weight, k_weight, eps,
+                                                      positions, inv_freq, axes, interleaved, q_out)
+        if r is not None:
+            return None if r is False else _answer(r, "fa_paged4_append")
     return _paged4_append(cache, block_table, seq_lens, k, v, cu_seqlens, q, q_weight, k_weight, eps, positions, inv_freq,
                           axes, interleaved, q_out, stream)
 
@@ -1109,6 +1126,10 @@ def paged4_read(cache, block_table, seq_lens, n: int, dtype, k_out=None, v_out=N
     ``dtype``, the type it was appended in; row i is key seq_lens[b] - n + i, zero
     where that is negative.  With one sequence's whole length they are what
     ``forward_ex`` takes for its next queries.  See fa_paged4_read."""
+    if stream is None:
+        r = (_native or _load_native()).paged4_read(cache, block_table, seq_lens, n, dtype, k_out, v_out)
+        if r is not None:
+            return _answer(r, "fa_paged4_read")
     return _paged4_read(cache, block_table, seq_lens, n, dtype, k_out, v_out, stream)
 
 
@@ -1146,6 +1167,10 @@ def paged4_decode(q, cache, block_table, seq_lens, scale: float | None = None, w
     """O [B,Hq,d], LSE [B,Hq] of one query row per sequence, q [B,Hq,d], against the
     seq_lens[b] keys of a 4-bit cache (the last ``window`` of them if window > 0),
     as the values that it holds.  See fa_paged4_decode."""
+    if stream is None:
+        r = (_native or _load_native()).paged4_decode(q, cache, block_table, seq_lens, scale, window, out, lse, workspace)
+        if r is not None:
+            return _answer(r, "fa_paged4_decode")
     return _paged4_decode(q, cache, block_table, seq_lens, scale, window, out, lse, workspace, stream)
 
 
