@@ -1521,12 +1521,12 @@ fa_status fa_paged4_decode(const void* q, const long long* q_strides, const fa_p
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   const long long units = (long long)B * kv->Hkv * ((G + a.unit_heads - 1) / a.unit_heads);
-  const int slots = std::min(fa::decode4_ctas_per_sm(a.unit_heads) * ds->num_sms, fa::kDecodeMaxParts);
   auto tiles_of = [&](int keys) {                  // of a unit, at most
     const long long n = ((long long)kv->page_size * table->max_pages + keys - 1) / keys;
     return window > 0 ? std::min(n, (window - 1LL) / keys + 2) : n;
   };
   // As many CTAs as run at a time, but no more than there can be tiles.
+  const int slots = std::min(fa::decode4_ctas_per_sm(a.unit_heads) * ds->num_sms, fa::kDecodeMaxParts);
   int parts = (int)std::min<long long>(units * tiles_of(fa::kDecode4TileKeys), slots);
   a.cluster = decode_cluster(units, tiles_of(fa::kDecode4ClusterKeys), slots);
   if (a.cluster) parts = (int)units * a.cluster;

@@ -20,7 +20,10 @@
 // exact but for elements 2^-24 times smaller than the largest.  The weights s p
 // enter times a power of two that brings the largest s so far to 2^6 (p is 2^8 at
 // most), as the sum of two fp16 values, off by 2^-22 of themselves or 2^-32 of the
-// largest.
+// largest.  Up to four heads a group (kDup) the eight columns hold the heads twice,
+// and the second four the weights' low parts, which costs no product; above that
+// fp16 has two products, and bf16, whose own rounding is 2^4 times coarser, the high
+// parts alone (o is 1.01 times as far off).
 //
 // The line of tiles, its cut into equal parts, one a CTA, and their joins are
 // those of the 16-bit kernel (fa_decode.cuh, fa_paged.cu); a warp's slice of a tile
@@ -43,33 +46,30 @@ namespace fa {
 
 namespace {
 
-constexpr int kWarps = 7;                          // consumers, one 16-key slice of a tile each
-constexpr int kConsumerThreads = kWarps * 32;
-constexpr int kThreads = kConsumerThreads + 32;
-
 enum : int { kSiteFull = 54, kSiteEmpty = 55, kDrainFull = 56 };
 
-// kSl slices of a tile a warp.
-template <int D, int kSl>
+// A CTA's shape: kWarps consumers, kSl slices of a tile each, and the producer.
+template <int D, int W, int kSl>
 struct Cfg {
-  static constexpr int kSlices = kSl * kWarps, kKeys = 16 * kSlices;
+  static constexpr int kWarps = W, kSlices = kSl * W, kKeys = 16 * kSlices, kThreads = 32 * W + 32;
   static constexpr uint32_t kSlice = Record<D>::kBytes, kStage = kSlices * kSlice;
-  static constexpr int kStages = 6 * 128 / D / kSl;            // 97 KB in flight
+  static constexpr int kStages = 6 * 128 / D / kSl;            // 97 KB in flight with 7 warps
   static constexpr uint32_t kBuf = kStages * kStage;           // [kWarps][8 heads][64] fp32, a head group of a group
-  static constexpr uint32_t kMl = kBuf + kWarps * 8u * 64u * 4u;     // [kWarps][16 heads] (max, sum)
-  static constexpr uint32_t kBar = kMl + kWarps * 16u * 8u;
-  static constexpr uint32_t kQ = kBar + 256u;                  // the unit's query rows as operands
-  static constexpr uint32_t bytes(int NT) { return kQ + NT * D * 16u; }
+  static constexpr uint32_t kMl = kBuf + W * 8u * 64u * 4u;    // [kWarps][16 heads] (max, sum)
+  static constexpr uint32_t kBar = kMl + W * 16u * 8u;
+  static constexpr uint32_t kQ = kBar + 320u;                  // the unit's query rows as operands
+  static constexpr uint32_t kQs(int NT) { return kQ + NT * D * 16u; }   // [NT][D / 64][8 heads] their sums, and a factor
+  static constexpr uint32_t bytes(int NT) { return kQs(NT) + NT * (D / 64) * 32u + 16u; }
 };
 
 struct Bars {
-  uint64_t full[12], empty[12];
+  uint64_t full[12], empty[12], q;
   int abort;
-  int scan[kThreads / 32];
+  int scan[16];
   int b0;                    // first sequence of this CTA's part
   long long before;          // tiles (per unit column) of the sequences before it
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
+static_assert(sizeof(Bars) <= 320, "barrier block");
 
 template <typename T>
 struct Type;
@@ -114,10 +114,10 @@ __device__ __forceinline__ uint32_t upper(uint32_t w) { return w & 0x03c003c0u; 
 __device__ __forceinline__ uint32_t lower(uint32_t w) { return w & 0x003c003cu; }
 __device__ __forceinline__ uint32_t swapped(uint32_t w) { return __byte_perm(w, w, 0x2301); }
 
-template <typename T_, int D_, int kSl>
+template <typename T_, int D_, int W, int kSl>
 struct Traits {
   using T = T_;
-  static constexpr int D = D_, kKeys = Cfg<D_, kSl>::kKeys, kJoinThreads = kConsumerThreads;
+  static constexpr int D = D_, kKeys = Cfg<D_, W, kSl>::kKeys, kJoinThreads = 32 * W;
   static constexpr float kShift = 0.f;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return Type<T>::pack(lo, hi); }
 };
@@ -127,12 +127,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumerThreads) : "memory"); }
-
-// The power of two above a positive finite x.
-__device__ __forceinline__ float power_above(float x) {
-  return __uint_as_float((__float_as_uint(x) & 0x7f800000u) + 0x00800000u);
+template <int kThreads>
+__device__ __forceinline__ void barrier_of() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
+
+// The largest power of two up to a positive normal x.
+__device__ __forceinline__ float power_of(float x) { return __uint_as_float(__float_as_uint(x) & 0x7f800000u); }
 
 // The (s, z) pairs of one row, D / 64 of them.
 template <typename T, int D>
@@ -151,60 +152,73 @@ __device__ __forceinline__ float2 load_par(const uint8_t* p) {
   return Type<T>::up(*reinterpret_cast<const uint32_t*>(p));
 }
 
-// Query rows of unit (b, col) as B operands, column = head lane / 4: at to[n][g][w][h][lane]
-// (if `to`) the four elements 64 g + 16 (lane % 4) + 8 w + 4 h on, times `times`
-// and, the odd pairs, 16; and sums[n][g], those over the groups for the heads 2 (lane % 4) and the
-// next, this lane's columns of S^T.
-template <typename T, int D, int NT>
-__device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int col, int chunks, uint2* to, float (&sums)[NT][D / 64][2], float& times) {
+// A lane's share of the query rows of unit (b, col): of head lane / 4 (of each eight),
+// and of each group, the 16 elements 16 (lane % 4) on.
+template <int D, int NT>
+struct QRows {
+  uint4 x[NT][D / 64][2];
+};
+template <typename T, int D, int NT, bool kDup>
+__device__ __forceinline__ void fetch_q(const DecodeArgs& a, int b, int col, int chunks, QRows<D, NT>& q) {
   const int lane = threadIdx.x & 31, G = a.Hq / a.kv.Hkv;
-  const int g = col / chunks, h0 = g * G + (col - g * chunks) * 8 * NT + (lane >> 2), h1 = (g + 1) * G;
+  const int g = col / chunks, h0 = g * G + (col - g * chunks) * 8 * NT + (lane >> 2 & (kDup ? 3 : 7)), h1 = (g + 1) * G;
   const T* p = static_cast<const T*>(a.q) + b * a.q_sb + (lane & 3) * 16;
-  uint4 q[NT][D / 64][2];
-  float top = 0.f;                                // the largest finite |q|
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const bool in = h0 + n * 8 < h1;
     const T* x = p + (in ? h0 + n * 8 : h1 - 1) * a.q_sh;
 #pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        q.x[n][k][w] = in ? *reinterpret_cast<const uint4*>(x + k * 64 + w * 8) : make_uint4(0, 0, 0, 0);
+  }
+}
+// The same as B operands, column = head lane / 4: at to[n][g][w][h][lane] the four
+// elements 64 g + 16 (lane % 4) + 8 w + 4 h on, times a power of two and, the odd
+// pairs, 16; at sums[n][g] the heads' sums over the groups, and behind them the
+// factor, both in the units of the scores (see work).
+template <typename T, int D, int NT>
+__device__ __forceinline__ void store_q(const QRows<D, NT>& q, float scale_log2, uint2* to, float* sums) {
+  const int lane = threadIdx.x & 31;
+  float top = 0x1p-100f, s[NT][D / 64];           // the largest finite |q|
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
     for (int k = 0; k < D / 64; ++k) {
-      float s = 0.f;
+      s[n][k] = 0.f;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        q[n][k][w] = in ? *reinterpret_cast<const uint4*>(x + k * 64 + w * 8) : make_uint4(0, 0, 0, 0);
-        const uint32_t e[4] = {q[n][k][w].x, q[n][k][w].y, q[n][k][w].z, q[n][k][w].w};
+        const uint32_t e[4] = {q.x[n][k][w].x, q.x[n][k][w].y, q.x[n][k][w].z, q.x[n][k][w].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 y = Type<T>::up(e[i]);
-          s += y.x + y.y;
+          s[n][k] += y.x + y.y;
           top = fmaxf(top, fabsf(y.x) < INFINITY ? fabsf(y.x) : 0.f);
           top = fmaxf(top, fabsf(y.y) < INFINITY ? fabsf(y.y) : 0.f);
         }
       }
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      sums[n][k][0] = __shfl_sync(0xffffffffu, s, (lane & 3) * 8);
-      sums[n][k][1] = __shfl_sync(0xffffffffu, s, (lane & 3) * 8 + 4);
+      s[n][k] += __shfl_xor_sync(0xffffffffu, s[n][k], 1);
+      s[n][k] += __shfl_xor_sync(0xffffffffu, s[n][k], 2);
     }
-  }
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  times = 2048.f / power_above(fmaxf(top, 0x1p-100f));
-  const float more = 16.f * times;
+  const float times = 1024.f / power_of(top), more = 16.f * times;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k)
+    for (int k = 0; k < D / 64; ++k) {
+      if ((lane & 3) == 0) sums[(n * (D / 64) + k) * 8 + (lane >> 2)] = s[n][k] * (times * 0x1p-18f);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const uint4 v = q[n][k][w];
+        const uint4 v = q.x[n][k][w];
         const float2 y0 = Type<T>::up(v.x), y1 = Type<T>::up(v.y), y2 = Type<T>::up(v.z), y3 = Type<T>::up(v.w);
-        if (to) {
-          uint2* x = to + ((n * (D / 64) + k) * 2 + w) * 64 + lane;
-          x[0] = make_uint2(Half::pack(y0.x * times, y0.y * times), Half::pack(y1.x * more, y1.y * more));
-          x[32] = make_uint2(Half::pack(y2.x * times, y2.y * times), Half::pack(y3.x * more, y3.y * more));
-        }
+        uint2* x = to + ((n * (D / 64) + k) * 2 + w) * 64 + lane;
+        x[0] = make_uint2(Half::pack(y0.x * times, y0.y * times), Half::pack(y1.x * more, y1.y * more));
+        x[32] = make_uint2(Half::pack(y2.x * times, y2.y * times), Half::pack(y3.x * more, y3.y * more));
       }
+    }
+  if (lane == 0) sums[NT * (D / 64) * 8] = scale_log2 * 0x1p18f / times;
 }
 
 constexpr float kNone = -1e30f;      // below every score: the maximum before the first key
@@ -215,15 +229,15 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
   return mbar_wait_warp(bar, parity, st, abort, site);
 }
 
-// A warp's work on its kSl slices of a tile, records kStep bytes and kGap keys apart,
-// rec the first, of the 16 keys from key0 on: S^T, its weights against the running
+// A warp's work on its kSl slices of a tile, rec the first one's record, of the 16 keys
+// from key0 on: S^T, its weights against the running
 // maximum m and, in l, zs and o, their sums.
-template <typename T, int D, int NT, int kSl, int kStep, int kGap>
+template <typename T, int D, int NT, bool kDup, int kSl>
 __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint32_t k_at, uint32_t v_at, uint32_t kp_at,
                                      uint32_t vp_at, int ka, float by, const uint2* q,
                                      const float (&qs)[NT][D / 64][2], float (&o)[NT][D / 16][4], float (&zs)[NT][D / 64][2],
                                      float (&m)[NT][2], float (&l)[NT][2], float (&grow)[D / 64]) {
-  constexpr int kG = D / 64, kW = Type<T>::kWeights;
+  constexpr int kG = D / 64, kW = kDup ? 1 : Type<T>::kWeights, kStep = Record<D>::kBytes, kGap = 16;
   // Scores, in units of log2 / by: S^T rows ka, ka + 8, columns 2 qc, 2 qc + 1.
   float x[kSl][NT][4];
   {
@@ -357,7 +371,7 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
       if (y * grow[k] >= 128.f) {
-        const float to = 128.f / power_above(y), f = to / grow[k];
+        const float to = 64.f / power_of(y), f = to / grow[k];
         grow[k] = to;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -396,10 +410,13 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
         for (int e = 0; e < 2; ++e) {
           const float w0 = x[j][n][2 * e] * (e ? sb : sa), w1 = x[j][n][2 * e + 1] * (e ? sb : sa);
           const uint32_t high = Half::pack(w0, w1);
-          p[j][n][0][e] = transpose8(high);
-          if constexpr (kW == 2) {
+          if constexpr (kDup || kW == 2) {
             const float2 h = Half::up(high);
-            p[j][n][1][e] = transpose8(Half::pack(w0 - h.x, w1 - h.y));
+            const uint32_t low = Half::pack(w0 - h.x, w1 - h.y);
+            p[j][n][0][e] = transpose8(kDup && (threadIdx.x & 2) ? low : high);
+            if constexpr (kW == 2) p[j][n][1][e] = transpose8(low);
+          } else {
+            p[j][n][0][e] = transpose8(high);
           }
         }
       }
@@ -457,11 +474,12 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
   }
 }
 
-template <typename T, int D, int NT, int kSl, bool kCluster>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(const DecodeArgs a, const DevStatus st) {
-  using C = Cfg<D, kSl>;
-  using Tr = Traits<T, D, kSl>;
-  constexpr int kKeys = C::kKeys;
+template <typename T, int D, int NT, bool kDup, int W, int kSl, bool kCluster>
+__global__ void __launch_bounds__(32 * W + 32, NT == 1 && W <= 7 ? 2 : 1) fa_decode4_kernel(const DecodeArgs a, const DevStatus st) {
+  using C = Cfg<D, W, kSl>;
+  using Tr = Traits<T, D, W, kSl>;
+  constexpr int kKeys = C::kKeys, kWarps = W, kThreads = C::kThreads;
+  auto consumer_sync = [] { barrier_of<32 * W>(); };
   constexpr int kG = D / 64;
   extern __shared__ __align__(128) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kBar);
@@ -473,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], kWarps);
     }
+    mbar_init(&bars->q, 1);
     bars->abort = 0;
     mbar_fence_init();
   }
@@ -571,6 +590,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
     part.tile = w.tile;
     part.left = (int)w.left;
     const int first_n = w.s.n;
+    // The query rows of the unit that starts: stored once the consumers are through
+    // tile it_q, the unit's before.
+    QRows<D, NT> rows;
+    int it_q = -1;
+    bool pending = w.left > 0;
+    if (pending) fetch_q<T, D, NT, kDup>(a, w.b, w.col, chunks, rows);
+    auto put_q = [&] {
+      store_q<T, D, NT>(rows, a.scale_log2, reinterpret_cast<uint2*>(smem + C::kQ), reinterpret_cast<float*>(smem + C::kQs(NT)));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q);
+      pending = false;
+    };
+    auto wait_and_put_q = [&] {
+      if (it_q >= 0 && !mbar_wait_warp(&bars->empty[it_q % C::kStages], it_q / C::kStages & 1, st, abort_flag, kSiteEmpty)) return false;
+      put_q();
+      return true;
+    };
     int it = 0, page, slot, have = look_up(w, page, slot);
     bool good = true;
     while (good && w.left > 0) {
@@ -587,6 +623,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
       const uint8_t* base = static_cast<const uint8_t*>(a.kv.k) + (w.col / chunks) * a.kv.s_head;
       for (int i = 0; i < have; ++i, ++it) {
         const int s = it % C::kStages, r = it / C::kStages;
+        if (pending && it >= it_q + C::kStages && it_q >= 0 && !wait_and_put_q()) {
+          good = false;
+          break;
+        }
         if (r > 0 && !mbar_wait_warp(&bars->empty[s], (r - 1) & 1, st, abort_flag, kSiteEmpty)) {
           good = false;
           break;
@@ -598,15 +638,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
           mbar_arrive_expect_tx(&bars->full[s], __popc(mask) * C::kSlice);
         }
         __syncwarp();
-        if (lane < C::kSlices && sl >= 0)
+        // Records of one page follow one another there as here: one copy a run.
+        const int p0 = __shfl_up_sync(0xffffffffu, p, 1), sl0 = __shfl_up_sync(0xffffffffu, sl, 1);
+        const uint32_t starts = __ballot_sync(0xffffffffu, lane == 0 || sl0 < 0 || sl < 0 || p != p0 || sl != sl0 + 16) | ~((1u << (C::kSlices - 1)) * 2u - 1u);
+        if (lane < C::kSlices && sl >= 0 && (starts >> lane & 1)) {
+          const uint32_t after = lane == 31 ? 0u : starts >> (lane + 1);
+          const int run = after ? __ffs(after) : 32 - lane;
           bulk_load(smem_u32(smem) + s * C::kStage + lane * C::kSlice,
-                    base + p * a.kv.s_page + (long long)(sl >> 4) * C::kSlice, C::kSlice, &bars->full[s]);
+                    base + p * a.kv.s_page + (long long)(sl >> 4) * C::kSlice, run * C::kSlice, &bars->full[s]);
+        }
+        if (pending && (it_q < 0 || __all_sync(0xffffffffu, mbar_test(smem_u32(&bars->empty[it_q % C::kStages]), it_q / C::kStages & 1))))
+          put_q();
+      }
+      if (good && x.left > 0 && !(x.b == w.b && x.col == w.col)) {
+        if (pending && !wait_and_put_q()) good = false;
+        pending = good;
+        it_q = it - 1;
+        if (pending) fetch_q<T, D, NT, kDup>(a, x.b, x.col, chunks, rows);
       }
       w = x;
       page = page_next;
       slot = slot_next;
       have = have_next;
     }
+    if (good && pending) good = wait_and_put_q();
     if (!kCluster && lane == 0) {
       DecodePart d = part;
       const long long u0 = t0 - d.tile;
@@ -633,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
   // -------------------------------------------------------------- consumers
   const int qr = lane >> 2, qc = lane & 3;        // fragment row and column pair
   const int ka = (qr >> 1) + 4 * (qr & 1);        // the keys of rows qr and qr + 8: ka and ka + 8
-  uint8_t* mine = smem + warp * C::kSlice;
+  uint8_t* mine = smem + warp * kSl * C::kSlice;
   const uint32_t k_at = Record<D>::k_word(ka, 2 * qc);
   const uint32_t v_at = Record<D>::kV + lane * 16;
   const uint32_t kp_at = Record<D>::kKp + ka * Record<D>::kPar, vp_at = Record<D>::kVp + ka * Record<D>::kPar;
@@ -641,12 +696,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
   float2* ml = reinterpret_cast<float2*>(smem + C::kMl);
   const float sl2 = a.scale_log2;
 
-  uint2* q = reinterpret_cast<uint2*>(smem + C::kQ);
+  const uint2* q = reinterpret_cast<const uint2*>(smem + C::kQ);
+  const float* q_sums = reinterpret_cast<const float*>(smem + C::kQs(NT));
   float qs[NT][kG][2], o[NT][D / 16][4], zs[NT][kG][2], m[NT][2], l[NT][2];
   float by = 0.f, grow[kG];                       // of S^T; brings the s of V so far to 2^7 at most
   bool dead = false;
   int g = 0, h0 = 0, h1 = 0;                      // kv head, query heads [h0, h1) of the unit
-  uint32_t stage = 0, phase = 0;
+  uint32_t stage = 0, phase = 0, q_phase = 0;
   do {
     // ------------------------------------------------ one unit's tiles here
     // (A CTA of a cluster may have none, and joins in all the same.)
@@ -654,16 +710,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
     g = w.col / chunks;
     h0 = g * G + (w.col - g * chunks) * 8 * NT;
     h1 = (g + 1) * G;
-    load_q<T, D, NT>(a, w.b, w.col, chunks, warp == 0 ? q : nullptr, qs, by);
-    consumer_sync();
-    by = sl2 * 0x1p18f / by;                      // x in slice() is in units of log2 / by
+    if (!kCluster || nt > 0) {
+      if (!dead && !wait_warp(&bars->q, q_phase, st, abort_flag, kSiteFull)) dead = true;
+      q_phase ^= 1;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < kG; ++k) {
-        qs[n][k][0] *= sl2 / by;
-        qs[n][k][1] *= sl2 / by;
-      }
+        for (int k = 0; k < kG; ++k) {
+          const float2 y = *reinterpret_cast<const float2*>(q_sums + (n * kG + k) * 8 + qc * 2);
+          qs[n][k][0] = y.x;
+          qs[n][k][1] = y.y;
+        }
+      by = q_sums[NT * kG * 8];
+    }
 #pragma unroll
     for (int k = 0; k < kG; ++k) grow[k] = 0x1p107f;
 #pragma unroll
@@ -677,15 +736,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
       m[n][0] = m[n][1] = kNone;
       l[n][0] = l[n][1] = 0.f;
     }
-    int key0 = (w.s.tile0 + w.tile) * kKeys + warp * 16;
+    int key0 = (w.s.tile0 + w.tile) * kKeys + warp * kSl * 16;
     for (int i = 0; i < nt; ++i, key0 += kKeys) {
       // After a wait that gave up the warp goes on through its part without
       // touching the tiles, so that the warps still meet at each unit's end.
       if (!dead && !wait_warp(&bars->full[stage], phase, st, abort_flag, kSiteFull)) dead = true;
       // (A slice whose page number is out of range was not loaded: what lies
       // there is worked on, and its sequence's outputs are unspecified.)
-      if (!dead && key0 < w.s.len && key0 + (kSl - 1) * kWarps * 16 + 16 > w.s.first)
-        work<T, D, NT, kSl, kWarps * C::kSlice, kWarps * 16>(mine + stage * C::kStage, key0, w.s, k_at, v_at, kp_at, vp_at, ka, by,
+      if (!dead && key0 < w.s.len && key0 + kSl * 16 > w.s.first)
+        work<T, D, NT, kDup, kSl>(mine + stage * C::kStage, key0, w.s, k_at, v_at, kp_at, vp_at, ka, by,
                                                             q + lane, qs, o, zs, m, l, grow);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->empty[stage]);
@@ -745,38 +804,39 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_decode4_kernel(c
           const float u0 = 0x1p18f / grow[k], u1 = 0x1p22f / grow[k];        // codes are c 2^-18 or c 2^-22, weights s p grow
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float z = zs[n][k][e & 1], s = f[e & 1];
+            const float z = kDup && qc >= 2 ? 0.f : zs[n][k][e & 1], s = f[e & 1];
             *reinterpret_cast<float4*>(to + (e & 1) * 64 + ((qr * 8 + (e >> 1) * 4) ^ (qc * 4))) =
                 make_float4(fmaf(o[n][4 * k][e], u0, z) * s, fmaf(o[n][4 * k + 1][e], u1, z) * s,
                             fmaf(o[n][4 * k + 2][e], u0, z) * s, fmaf(o[n][4 * k + 3][e], u1, z) * s);
           }
           consumer_sync();
-          for (int hh = warp; hh < 8; hh += kWarps) {            // a head a warp at a time
-            const int e = lane * 2, d = k * 64 + e, h = h0 + n * 8 + hh;
+          static_assert(kWarps >= 4, "heads of a unit");
+          if (warp < (kDup ? 2 : 4)) {             // two heads a warp
+            const int hh = warp * 2 + (lane >> 4), e = (lane & 15) * 4, d = k * 64 + e, h = h0 + n * 8 + hh;
             const float Mh = __shfl_sync(0xffffffffu, M, hh), Lh = __shfl_sync(0xffffffffu, L, hh);
-            const float* from = buf + hh * 64 + (e ^ ((hh >> 1) * 4));
-            float2 y = *reinterpret_cast<const float2*>(from);
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int u = 1; u < kWarps; ++u) {
-              const float2 z = *reinterpret_cast<const float2*>(from + u * 8 * 64);
-              y.x += z.x;
-              y.y += z.y;
+            for (int c = 0; c < (kDup ? 2 : 1); ++c) {             // the low parts' sums with them
+              const int from = (hh + 4 * c) * 64 + (e ^ ((hh + 4 * c >> 1) * 4));
+#pragma unroll
+              for (int u = 0; u < kWarps; ++u) add_scaled(y, 1.f, *reinterpret_cast<const float4*>(buf + from + u * 8 * 64));
             }
             if constexpr (kCluster) {
               // For the join; the tiles have been read.
-              *reinterpret_cast<float2*>(smem + ((n * 8 + hh) * D + d) * 4) = y;
+              *reinterpret_cast<float4*>(smem + ((n * 8 + hh) * D + d) * 4) = y;
               if (d == 0) reinterpret_cast<float2*>(smem + kClusterMl<D>)[n * 8 + hh] = make_float2(Mh, Lh);
             } else if (h < h1) {
               const long long row = (long long)w.b * a.Hq + h;
               if (whole) {
                 const float inv = 1.f / Lh;
-                *reinterpret_cast<uint32_t*>(static_cast<T*>(a.o) + row * D + d) = Tr::pack(y.x * inv, y.y * inv);
+                *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + row * D + d) =
+                    make_uint2(Tr::pack(y.x * inv, y.y * inv), Tr::pack(y.z * inv, y.w * inv));
                 if (d == 0) a.lse[row] = (Mh + log2f(Lh)) * 0.69314718055994530942f;
               } else {
                 // Slot 1: the unit starts in this CTA and goes on; slot 0: it
                 // started earlier.
                 const long long at = ((long long)blockIdx.x * 2 + (w.tile == 0 ? 1 : 0)) * 16 + n * 8 + hh;
-                *reinterpret_cast<float2*>(a.part + at * D + d) = y;
+                *reinterpret_cast<float4*>(a.part + at * D + d) = y;
                 if (d == 0) a.part_ml[at] = make_float2(Mh, Lh);
               }
             }
@@ -801,34 +861,56 @@ template <typename T, int D>
 __global__ void __launch_bounds__(128) fa_decode4_join_kernel(const DecodeArgs a) {
   launch_dependents();
   wait_for_previous();
-  join<Traits<T, D, 1>>(a);
+  join<Traits<T, D, 7, 1>>(a);
 }
 
-// Slices of a tile a warp: one where a cluster shares few tiles.
-constexpr int kShort = kDecode4ClusterKeys / 16 / kWarps, kLong = kDecode4TileKeys / 16 / kWarps;
+// A kernel and its CTA's shape.
+template <typename T, int D, int NT, bool kDup, int W, int kSl, bool kCluster>
+struct Shape {
+  using C = Cfg<D, W, kSl>;
+  static constexpr auto kernel = fa_decode4_kernel<T, D, NT, kDup, W, kSl, kCluster>;
+  static cudaError_t launch(const DecodeArgs& a, const DevStatus& st, int ctas, cudaStream_t stream) {
+    return launch_after(kernel, ctas, C::kThreads, C::bytes(NT), kCluster ? a.cluster : 1, stream, a, st);
+  }
+  static cudaError_t configure() {
+    static_assert(C::bytes(NT) <= (NT == 1 && W <= 7 ? 115712 : 232448), "shared memory");
+    static_assert(C::kKeys == (kCluster ? kDecode4ClusterKeys : kDecode4TileKeys), "tile");
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes(NT));
+  }
+};
+// For clusters, which share few tiles, one slice of a tile a warp.
+template <typename T, int D, int NT, bool kDup>
+using Short = Shape<T, D, NT, kDup, 7, 1, true>;
+template <typename T, int D, int NT, bool kDup>
+using Long = Shape<T, D, NT, kDup, 7, 2, false>;
 
+template <typename T, int D, int NT, bool kDup>
+cudaError_t launch_shape(const DecodeArgs& a, const DevStatus& st, int parts, cudaStream_t stream) {
+  if (a.cluster) return Short<T, D, NT, kDup>::launch(a, st, parts, stream);
+  const cudaError_t e = Long<T, D, NT, kDup>::launch(a, st, parts, stream);
+  const int joins = (parts - 1) * (a.unit_heads / 4);
+  if (e != cudaSuccess || joins == 0) return e;
+  return launch_after(fa_decode4_join_kernel<T, D>, joins, 128, 0, 1, stream, a);
+}
 template <typename T, int D>
 cudaError_t launch(const DecodeArgs& a, const DevStatus& st, int parts, cudaStream_t stream) {
-  if (a.cluster)
-    return launch_after(a.unit_heads == 8 ? fa_decode4_kernel<T, D, 1, kShort, true> : fa_decode4_kernel<T, D, 2, kShort, true>,
-                        parts, kThreads, Cfg<D, kShort>::bytes(a.unit_heads / 8), a.cluster, stream, a, st);
-  cudaError_t e =
-      launch_after(a.unit_heads == 8 ? fa_decode4_kernel<T, D, 1, kLong, false> : fa_decode4_kernel<T, D, 2, kLong, false>, parts,
-                   kThreads, Cfg<D, kLong>::bytes(a.unit_heads / 8), 1, stream, a, st);
-  const int joins = (parts - 1) * (a.unit_heads / 4);
-  if (e == cudaSuccess && joins > 0) e = launch_after(fa_decode4_join_kernel<T, D>, joins, 128, 0, 1, stream, a);
-  return e;
+  if (a.unit_heads == 16) return launch_shape<T, D, 2, false>(a, st, parts, stream);
+  if constexpr (Type<T>::kWeights == 2)
+    if (a.Hq / a.kv.Hkv <= 4) return launch_shape<T, D, 1, true>(a, st, parts, stream);
+  return launch_shape<T, D, 1, false>(a, st, parts, stream);
 }
 
+template <typename T, int D, int NT, bool kDup>
+cudaError_t configure_shape() {
+  const cudaError_t e = Short<T, D, NT, kDup>::configure();
+  return e == cudaSuccess ? Long<T, D, NT, kDup>::configure() : e;
+}
 template <typename T, int D>
 cudaError_t configure() {
-  static_assert(Cfg<D, kShort>::bytes(1) <= 115712 && Cfg<D, kLong>::bytes(1) <= 115712, "two CTAs per SM");
-  static_assert(Cfg<D, kShort>::kKeys == kDecode4ClusterKeys && Cfg<D, kLong>::kKeys == kDecode4TileKeys, "tile");
-  cudaError_t e = cudaSuccess;
-  for (auto k : {fa_decode4_kernel<T, D, 1, kShort, true>, fa_decode4_kernel<T, D, 2, kShort, true>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, kShort>::bytes(2));
-  for (auto k : {fa_decode4_kernel<T, D, 1, kLong, false>, fa_decode4_kernel<T, D, 2, kLong, false>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, kLong>::bytes(2));
+  cudaError_t e = configure_shape<T, D, 1, false>();
+  if constexpr (Type<T>::kWeights == 2)
+    if (e == cudaSuccess) e = configure_shape<T, D, 1, true>();
+  if (e == cudaSuccess) e = configure_shape<T, D, 2, false>();
   if (e == cudaSuccess) e = preload_kernel(fa_decode4_join_kernel<T, D>);
   return e;
 }
