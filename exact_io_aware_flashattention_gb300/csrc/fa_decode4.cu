@@ -38,6 +38,7 @@
 // nor rescales.
 #include "fa_decode.cuh"
 #include "fa_paged4.h"
+#include "fa_rotary.cuh"
 #include "sm103a.cuh"
 
 #include <cuda_fp16.h>
@@ -46,30 +47,56 @@ namespace fa {
 
 namespace {
 
-enum : int { kSiteFull = 54, kSiteEmpty = 55, kDrainFull = 56 };
+enum : int { kSiteFull = 54, kSiteRead = 55, kDrainFull = 56 };
 
-// A CTA's shape: kWarps consumers, kSl slices of a tile each, and the producer.
-template <int D, int W, int kSl>
+// A CTA's shape: kWarps warps, kSl slices of a tile each, and each a ring of its own
+// for the records on their way.
+template <int D, int NT, int W, int kSl>
 struct Cfg {
-  static constexpr int kWarps = W, kSlices = kSl * W, kKeys = 16 * kSlices, kThreads = 32 * W + 32;
-  static constexpr uint32_t kSlice = Record<D>::kBytes, kStage = kSlices * kSlice;
-  static constexpr int kStages = 6 * 128 / D / kSl;            // 97 KB in flight with 7 warps
-  static constexpr uint32_t kBuf = kStages * kStage;           // [kWarps][8 heads][64] fp32, a head group of a group
-  static constexpr uint32_t kMl = kBuf + W * 8u * 64u * 4u;    // [kWarps][16 heads] (max, sum)
-  static constexpr uint32_t kBar = kMl + W * 16u * 8u;
-  static constexpr uint32_t kQ = kBar + 320u;                  // the unit's query rows as operands
-  static constexpr uint32_t kQs(int NT) { return kQ + NT * D * 16u; }   // [NT][D / 64][8 heads] their sums, and a factor
-  static constexpr uint32_t bytes(int NT) { return kQs(NT) + NT * (D / 64) * 32u + 16u; }
+  static constexpr int kWarps = W, kKeys = 16 * kSl * W, kThreads = 32 * W;
+  static constexpr uint32_t kSlice = Record<D>::kBytes, kStage = kSl * kSlice;
+  static constexpr int kStages = (NT == 1 ? 6 : 10) * 128 / D / kSl;
+  static constexpr uint32_t kRing = kStages * kStage;          // 13.5 or 22.5 KB a warp
+  // At a unit's end a warp's O [8 heads][D] and (max, sum) [8 NT] take the place of the
+  // last tile (in a cluster, of the ring's first records).
+  static constexpr uint32_t kMl = 8u * D * 4u, kStash = kMl + NT * 64u;
+  static_assert(kStash <= (kSl == 2 ? kStage : 2 * kStage) && kStash % 8 == 0, "stash");
+  static constexpr uint32_t kJoin = kStash;                    // the cluster's join, in warp 0's ring
+  static_assert(kJoin + 16u * D * 4u + 128u <= kRing && kJoin % 16 == 0, "join");
+  // Two of: a unit's query rows, first as they are and then as operands; [NT][D / 64][8
+  // heads] their sums over the groups, and a factor.
+  static constexpr uint32_t kQ = W * kRing, kQBytes = NT * D * 16u;
+  static constexpr uint32_t kQs = kQ + 2 * kQBytes, kQsBytes = NT * (D / 64) * 32u + 16u;
+  static constexpr uint32_t kBars = kQs + 2 * kQsBytes;
 };
 
+// A unit's end takes about as long as two tiles do, and counts as so many in the line that is
+// cut into equal parts.
+constexpr int kEnd = 2;
+__device__ __forceinline__ int cost_of(const Span& s) { return s.n > 0 ? s.n + kEnd : 0; }
+// On behind the tiles up to `tile` of a unit, and its end.
+template <int kKeys>
+__device__ __forceinline__ void advance(Walk<kKeys>& x, int tiles, const DecodeArgs& a, int cols) {
+  x.left -= tiles;
+  x.tile += tiles;
+  if (x.tile < x.s.n) return;
+  x.left -= x.s.n + kEnd - x.tile;
+  if (x.left > 0) x.next_unit(a, cols);
+}
+
+template <typename C>
 struct Bars {
-  uint64_t full[12], empty[12], q;
+  uint64_t full[C::kWarps][C::kStages];
+  uint64_t read;                       // a unit's stashes: every warp has read them
+  Walk<C::kKeys> ahead[C::kWarps];     // of what each warp looks up next
+  Walk<C::kKeys> next[2];              // the unit after this one
   int abort;
-  int scan[16];
+  int scan[C::kWarps];
   int b0;                    // first sequence of this CTA's part
   long long before;          // tiles (per unit column) of the sequences before it
 };
-static_assert(sizeof(Bars) <= 320, "barrier block");
+template <typename C>
+constexpr uint32_t kSmem = C::kBars + sizeof(Bars<C>);
 
 template <typename T>
 struct Type;
@@ -114,10 +141,10 @@ __device__ __forceinline__ uint32_t upper(uint32_t w) { return w & 0x03c003c0u; 
 __device__ __forceinline__ uint32_t lower(uint32_t w) { return w & 0x003c003cu; }
 __device__ __forceinline__ uint32_t swapped(uint32_t w) { return __byte_perm(w, w, 0x2301); }
 
-template <typename T_, int D_, int W, int kSl>
+template <typename T_, int D_, int kKeys_, int kThreads>
 struct Traits {
   using T = T_;
-  static constexpr int D = D_, kKeys = Cfg<D_, W, kSl>::kKeys, kJoinThreads = 32 * W;
+  static constexpr int D = D_, kKeys = kKeys_, kJoinThreads = kThreads;
   static constexpr float kShift = 0.f;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return Type<T>::pack(lo, hi); }
 };
@@ -127,11 +154,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-template <int kThreads>
-__device__ __forceinline__ void barrier_of() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-}
-
 // The largest power of two up to a positive normal x.
 __device__ __forceinline__ float power_of(float x) { return __uint_as_float(__float_as_uint(x) & 0x7f800000u); }
 
@@ -152,26 +174,37 @@ __device__ __forceinline__ float2 load_par(const uint8_t* p) {
   return Type<T>::up(*reinterpret_cast<const uint32_t*>(p));
 }
 
-// A lane's share of the query rows of unit (b, col): of head lane / 4 (of each eight),
-// and of each group, the 16 elements 16 (lane % 4) on.
+// The query rows of unit (b, col) on their way to raw [8 NT heads][D]; a warp's work.
+template <typename T, int D, int NT, bool kDup>
+__device__ __forceinline__ void fetch_q(const DecodeArgs& a, int b, int col, int chunks, uint8_t* raw) {
+  const int G = a.Hq / a.kv.Hkv, g = col / chunks, h0 = g * G + (col - g * chunks) * 8 * NT, h1 = (g + 1) * G;
+#pragma unroll
+  for (int i = threadIdx.x & 31; i < (kDup ? 4 : 8 * NT) * (D / 8); i += 32) {
+    const int h = h0 + i / (D / 8);
+    if (h < h1) copy16(raw + i * 16, static_cast<const T*>(a.q) + b * a.q_sb + h * a.q_sh + i % (D / 8) * 8);
+  }
+  copies_end();
+}
+// A lane's share of them: of head lane / 4 (of each eight), and of each group, the 16
+// elements 16 (lane % 4) on; `heads` is the unit's number of heads.
 template <int D, int NT>
 struct QRows {
   uint4 x[NT][D / 64][2];
 };
-template <typename T, int D, int NT, bool kDup>
-__device__ __forceinline__ void fetch_q(const DecodeArgs& a, int b, int col, int chunks, QRows<D, NT>& q) {
-  const int lane = threadIdx.x & 31, G = a.Hq / a.kv.Hkv;
-  const int g = col / chunks, h0 = g * G + (col - g * chunks) * 8 * NT + (lane >> 2 & (kDup ? 3 : 7)), h1 = (g + 1) * G;
-  const T* p = static_cast<const T*>(a.q) + b * a.q_sb + (lane & 3) * 16;
+template <int D, int NT, bool kDup>
+__device__ __forceinline__ void wait_q(const uint8_t* raw, int heads, QRows<D, NT>& q) {
+  copies_wait<0>();
+  __syncwarp();
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const bool in = h0 + n * 8 < h1;
-    const T* x = p + (in ? h0 + n * 8 : h1 - 1) * a.q_sh;
+    const int h = n * 8 + (lane >> 2 & (kDup ? 3 : 7));
 #pragma unroll
     for (int k = 0; k < D / 64; ++k)
 #pragma unroll
       for (int w = 0; w < 2; ++w)
-        q.x[n][k][w] = in ? *reinterpret_cast<const uint4*>(x + k * 64 + w * 8) : make_uint4(0, 0, 0, 0);
+        q.x[n][k][w] = h < heads ? *reinterpret_cast<const uint4*>(raw + h * D * 2 + k * 128 + (lane & 3) * 32 + w * 16)
+                                 : make_uint4(0, 0, 0, 0);
   }
 }
 // The same as B operands, column = head lane / 4: at to[n][g][w][h][lane] the four
@@ -475,31 +508,27 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
 }
 
 template <typename T, int D, int NT, bool kDup, int W, int kSl, bool kCluster>
-__global__ void __launch_bounds__(32 * W + 32, NT == 1 && W <= 7 ? 2 : 1) fa_decode4_kernel(const DecodeArgs a, const DevStatus st) {
-  using C = Cfg<D, W, kSl>;
-  using Tr = Traits<T, D, W, kSl>;
-  constexpr int kKeys = C::kKeys, kWarps = W, kThreads = C::kThreads;
-  auto consumer_sync = [] { barrier_of<32 * W>(); };
-  constexpr int kG = D / 64;
+__global__ void __launch_bounds__(32 * W, NT == 1 && W <= 8 ? 2 : 1) fa_decode4_kernel(const DecodeArgs a, const DevStatus st) {
+  using C = Cfg<D, NT, W, kSl>;
+  constexpr int kKeys = C::kKeys, kWarps = W, kThreads = C::kThreads, kG = D / 64;
+  using Tr = Traits<T, D, kKeys, kThreads>;
   extern __shared__ __align__(128) uint8_t smem[];
-  Bars* bars = reinterpret_cast<Bars*>(smem + C::kBar);
+  Bars<C>* bars = reinterpret_cast<Bars<C>*>(smem + C::kBars);
   volatile int* abort_flag = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&bars->full[s], 1);
-      mbar_init(&bars->empty[s], kWarps);
+  if (lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(&bars->full[warp][s], kSl);
+    if (warp == 0) {
+      mbar_init(&bars->read, kWarps);
+      bars->abort = 0;
     }
-    mbar_init(&bars->q, 1);
-    bars->abort = 0;
     mbar_fence_init();
   }
   wait_for_previous();
   const int G = a.Hq / a.kv.Hkv, chunks = (G + 8 * NT - 1) / (8 * NT), cols = a.kv.Hkv * chunks;
   Walk<kKeys> w;
-  long long total = 0, t0 = 0, t1 = 0;            // the line's tiles, and this CTA's part of them
-  int parts = 0, rank = 0;
+  int rank = 0;
   if constexpr (kCluster) {
     // The cluster's unit, and this CTA's share of its tiles (perhaps none).
     const int unit = blockIdx.x / a.cluster;
@@ -510,11 +539,11 @@ __global__ void __launch_bounds__(32 * W + 32, NT == 1 && W <= 7 ? 2 : 1) fa_dec
     w.tile = w.s.n * rank / a.cluster;
     w.left = w.s.n * (rank + 1) / a.cluster - w.tile;
     if (w.s.len < 0 && w.col == 0 && rank == 0 && threadIdx.x == 0) record_error(st, kErrBadIndex, kSiteDecode4Len);
-    __syncthreads();
   } else {
     // The line: its length, and this CTA's first sequence.  Round 0 finds the
     // total; round 1, for batches of more than one block's worth, walks again
     // to find the start (one block's worth is still there).
+    long long total = 0;
     const int first_len = (int)threadIdx.x < a.B ? a.seq_lens[threadIdx.x] : 0;
     for (int round = 0; round < 2; ++round) {
       long long before = 0, start = 0;
@@ -525,7 +554,7 @@ __global__ void __launch_bounds__(32 * W + 32, NT == 1 && W <= 7 ? 2 : 1) fa_dec
           s = span_of_len<kKeys>(a, base == 0 ? first_len : a.seq_lens[b]);
           if (s.len < 0 && round == 0 && blockIdx.x == 0) record_error(st, kErrBadIndex, kSiteDecode4Len);
         }
-        int x = s.n;
+        int x = cost_of(s);
         for (int d = 1; d < 32; d <<= 1) {
           const int y = __shfl_up_sync(0xffffffffu, x, d);
           if (lane >= d) x += y;
@@ -533,8 +562,8 @@ __global__ void __launch_bounds__(32 * W + 32, NT == 1 && W <= 7 ? 2 : 1) fa_dec
         __syncthreads();
         if (lane == 31) bars->scan[warp] = x;
         __syncthreads();
-        long long pre = before + x - s.n;
-        for (int i = 0; i < kThreads / 32; ++i) {
+        long long pre = before + x - cost_of(s);
+        for (int i = 0; i < kWarps; ++i) {
           if (i < warp) pre += bars->scan[i];
           before += bars->scan[i];
         }
@@ -542,7 +571,7 @@ __global__ void __launch_bounds__(32 * W + 32, NT == 1 && W <= 7 ? 2 : 1) fa_dec
         if (round == 0 && last) total = before * cols;
         const int all = (int)min(total, (long long)gridDim.x);
         if ((last || round == 1) && blockIdx.x < all) start = part_start(total, blockIdx.x, all);
-        if ((round == 1 || a.B <= kThreads) && s.n > 0 && pre * cols <= start && start < (pre + s.n) * cols) {
+        if ((round == 1 || a.B <= kThreads) && s.n > 0 && pre * cols <= start && start < (pre + cost_of(s)) * cols) {
           bars->b0 = b;
           bars->before = pre * cols;
         }
@@ -550,159 +579,135 @@ __global__ void __launch_bounds__(32 * W + 32, NT == 1 && W <= 7 ? 2 : 1) fa_dec
       if (a.B <= kThreads) break;
     }
     __syncthreads();
-    parts = (int)min(total, (long long)gridDim.x);
+    const int parts = (int)min(total, (long long)gridDim.x);
     if ((int)blockIdx.x >= parts) {
       if (threadIdx.x == 0) a.parts[blockIdx.x].left = 0;
-      if (warp == kWarps) fill_empty<Tr>(a);
+      if (warp == 0) fill_empty<Tr>(a);
       return;
     }
-    t0 = part_start(total, blockIdx.x, parts);
-    t1 = part_start(total, blockIdx.x + 1, parts);
-    w.left = t1 - t0;
+    const long long t0 = part_start(total, blockIdx.x, parts);
+    w.left = part_start(total, blockIdx.x + 1, parts) - t0;
     w.b = bars->b0;
     w.s = span_of<kKeys>(a, w.b);
     const long long in = t0 - bars->before;
-    w.col = (int)(in / w.s.n);
-    w.tile = (int)(in - (long long)w.col * w.s.n);
-  }
-
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ producer
-    // Lane l looks up slice l % kSlices of tile l / kSlices of the unit's next tiles,
-    // one run ahead of the copies; lanes below kSlices issue a slice's copy each.
-    constexpr int kAhead = 32 / C::kSlices;
-    const int my_slice = lane % C::kSlices, my_tile = lane / C::kSlices;
-    auto look_up = [&](const Walk<kKeys>& x, int& page, int& slot) {
-      const int have = (int)min((long long)min(x.s.n - x.tile, kAhead), x.left);
-      const int key0 = (x.s.tile0 + x.tile + my_tile) * kKeys + my_slice * 16;
-      page = 0;
-      slot = -1;                       // not visible: not copied
-      if (my_tile < have && key0 < x.s.len && key0 + 16 > x.s.first) {
-        const int c = key0 / a.kv.page_size;
-        slot = key0 - c * a.kv.page_size;
-        page = a.table.pages[x.b * a.table.stride + c];
-      }
-      return have;
-    };
-    DecodePart part{};
-    part.b = w.b;
-    part.col = w.col;
-    part.tile = w.tile;
-    part.left = (int)w.left;
-    const int first_n = w.s.n;
-    // The query rows of the unit that starts: stored once the consumers are through
-    // tile it_q, the unit's before.
-    QRows<D, NT> rows;
-    int it_q = -1;
-    bool pending = w.left > 0;
-    if (pending) fetch_q<T, D, NT, kDup>(a, w.b, w.col, chunks, rows);
-    auto put_q = [&] {
-      store_q<T, D, NT>(rows, a.scale_log2, reinterpret_cast<uint2*>(smem + C::kQ), reinterpret_cast<float*>(smem + C::kQs(NT)));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->q);
-      pending = false;
-    };
-    auto wait_and_put_q = [&] {
-      if (it_q >= 0 && !mbar_wait_warp(&bars->empty[it_q % C::kStages], it_q / C::kStages & 1, st, abort_flag, kSiteEmpty)) return false;
-      put_q();
-      return true;
-    };
-    int it = 0, page, slot, have = look_up(w, page, slot);
-    bool good = true;
-    while (good && w.left > 0) {
-      Walk<kKeys> x = w;
-      x.left -= have;
-      x.tile += have;
-      if (x.tile == x.s.n && x.left > 0) x.next_unit(a, cols);
-      int page_next = page, slot_next = slot, have_next = have;
-      if (x.left > 0 && !(x.b == w.b && x.tile == w.tile && x.left >= have)) have_next = look_up(x, page_next, slot_next);
-      if (slot >= 0 && (page < 0 || page >= a.kv.num_pages)) {
-        record_error(st, kErrBadIndex, kSiteDecode4Page);
-        slot = -1;
-      }
-      const uint8_t* base = static_cast<const uint8_t*>(a.kv.k) + (w.col / chunks) * a.kv.s_head;
-      for (int i = 0; i < have; ++i, ++it) {
-        const int s = it % C::kStages, r = it / C::kStages;
-        if (pending && it >= it_q + C::kStages && it_q >= 0 && !wait_and_put_q()) {
-          good = false;
-          break;
-        }
-        if (r > 0 && !mbar_wait_warp(&bars->empty[s], (r - 1) & 1, st, abort_flag, kSiteEmpty)) {
-          good = false;
-          break;
-        }
-        const int p = __shfl_sync(0xffffffffu, page, i * C::kSlices + my_slice);
-        const int sl = __shfl_sync(0xffffffffu, slot, i * C::kSlices + my_slice);
-        const uint32_t mask = __ballot_sync(0xffffffffu, sl >= 0) & ((1u << C::kSlices) - 1);
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars->full[s], __popc(mask) * C::kSlice);
-        }
-        __syncwarp();
-        // Records of one page follow one another there as here: one copy a run.
-        const int p0 = __shfl_up_sync(0xffffffffu, p, 1), sl0 = __shfl_up_sync(0xffffffffu, sl, 1);
-        const uint32_t starts = __ballot_sync(0xffffffffu, lane == 0 || sl0 < 0 || sl < 0 || p != p0 || sl != sl0 + 16) | ~((1u << (C::kSlices - 1)) * 2u - 1u);
-        if (lane < C::kSlices && sl >= 0 && (starts >> lane & 1)) {
-          const uint32_t after = lane == 31 ? 0u : starts >> (lane + 1);
-          const int run = after ? __ffs(after) : 32 - lane;
-          bulk_load(smem_u32(smem) + s * C::kStage + lane * C::kSlice,
-                    base + p * a.kv.s_page + (long long)(sl >> 4) * C::kSlice, run * C::kSlice, &bars->full[s]);
-        }
-        if (pending && (it_q < 0 || __all_sync(0xffffffffu, mbar_test(smem_u32(&bars->empty[it_q % C::kStages]), it_q / C::kStages & 1))))
-          put_q();
-      }
-      if (good && x.left > 0 && !(x.b == w.b && x.col == w.col)) {
-        if (pending && !wait_and_put_q()) good = false;
-        pending = good;
-        it_q = it - 1;
-        if (pending) fetch_q<T, D, NT, kDup>(a, x.b, x.col, chunks, rows);
-      }
-      w = x;
-      page = page_next;
-      slot = slot_next;
-      have = have_next;
+    w.col = (int)(in / cost_of(w.s));
+    w.tile = (int)(in - (long long)w.col * cost_of(w.s));
+    const int tile = w.tile;
+    if (tile >= w.s.n) advance(w, 0, a, cols);     // a unit's end: the part starts with the next unit, if it has one
+    if (w.left <= 0) {
+      if (threadIdx.x == 0) a.parts[blockIdx.x].left = 0;
+      if (warp == 0) fill_empty<Tr>(a);
+      return;
     }
-    if (good && pending) good = wait_and_put_q();
-    if (!kCluster && lane == 0) {
-      DecodePart d = part;
-      const long long u0 = t0 - d.tile;
-      d.i0 = part_of(u0, total, parts);
-      d.i1 = part_of(u0 + first_n - 1, total, parts);
-      d.last_i1 = good && w.tile < w.s.n ? part_of(t1 - 1 + (w.s.n - w.tile), total, parts) : blockIdx.x;
+    if (threadIdx.x == 0) {
+      DecodePart d{};
+      d.b = w.b;
+      d.col = w.col;
+      d.tile = w.tile;
+      d.left = (int)w.left;
+      d.i0 = part_of(t0 - tile, total, parts);    // (of use where the part does not start with a unit)
+      d.i1 = part_of(t0 - tile + w.s.n - 1, total, parts);
       a.parts[blockIdx.x] = d;
     }
-    if (!kCluster) fill_empty<Tr>(a);
-    // Every copy issued must have landed before the CTA may exit.
-    if (lane == 0)
-      for (int s = 0; s < C::kStages && s < it; ++s) {
-        const int last = it - 1 - ((it - 1 - s) % C::kStages);
-        mbar_wait_drain(&bars->full[s], (last / C::kStages) & 1, st, kDrainFull);
-      }
-    if (kCluster && a.cluster > 1) {
-      __syncwarp();
-      cluster_sync();
-      cluster_sync();
-    }
-    return;
   }
 
-  // -------------------------------------------------------------- consumers
+  // -------------------------------------------------------------- a warp's copies
+  // Lane l holds the place and the bytes of slice l % kSl of tile l / kSl of the next ones
+  // in the line (of one unit), `run` of them, `run_at` already on their way; and the page
+  // and slot (-1: nothing visible) of the same slice of the run after it.
+  uint8_t* ring = smem + warp * C::kRing;
+  const uint8_t* from = nullptr;
+  uint32_t bytes = 0;
+  int run = 0, run_at = 0, flying = 0, page = 0, slot = -1;
+  bool dead = false, more = true;                 // more: the run after it is not empty
+  auto run_of = [](const Walk<kKeys>& x) { return (int)max(min((long long)min(x.s.n - x.tile, 32 / kSl), x.left), 0ll); };
+  auto look_ahead = [&](const Walk<kKeys>& x) {
+    const int key0 = (x.s.tile0 + x.tile + lane / kSl) * kKeys + (warp * kSl + lane % kSl) * 16;
+    slot = -1;
+    if (lane / kSl < run_of(x) && key0 < x.s.len && key0 + 16 > x.s.first) {
+      const int c = key0 / a.kv.page_size;
+      slot = key0 - c * a.kv.page_size;
+      page = a.table.pages[x.b * a.table.stride + c];
+    }
+    more = x.left > 0;
+    if (lane == 0) bars->ahead[warp] = x;
+    __syncwarp();
+  };
+  auto look_up = [&] {
+    Walk<kKeys> x = bars->ahead[warp];
+    run = run_of(x);
+    run_at = 0;
+    from = nullptr;
+    if (slot >= 0) {
+      if (page < 0 || page >= a.kv.num_pages) record_error(st, kErrBadIndex, kSiteDecode4Page);
+      else
+        from = static_cast<const uint8_t*>(a.kv.k) + (x.col / chunks) * a.kv.s_head + page * a.kv.s_page +
+               (long long)(slot >> 4) * C::kSlice;
+    }
+    bytes = from ? C::kSlice : 0u;
+    if constexpr (kSl == 2) {
+      // Records of one page follow one another there as here: one copy for both.
+      const uint8_t* other = reinterpret_cast<const uint8_t*>(
+          __shfl_xor_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), 1));
+      if (from && other && (lane & 1 ? other + C::kSlice == from : from + C::kSlice == other)) bytes = lane & 1 ? 0u : 2 * C::kSlice;
+    }
+    advance(x, run, a, cols);
+    __syncwarp();
+    look_ahead(x);
+  };
+  // The next tile's records to stage s, whose last tile this warp has read.
+  auto issue = [&](uint32_t s) {
+    if (dead) return;
+    if (run_at == run) {
+      if (!more) return;
+      look_up();
+    }
+    if (lane / kSl == run_at) {
+      uint64_t* bar = &bars->full[warp][s];
+      if (bytes) {
+        mbar_arrive_expect_tx(bar, bytes);
+        bulk_load(smem_u32(ring) + s * C::kStage + lane % kSl * C::kSlice, from, bytes, bar);
+      } else {
+        mbar_arrive(bar);
+      }
+    }
+    ++run_at;
+    ++flying;
+  };
+  constexpr int kQWarp = W - 1;        // prepares the units' query rows
+  auto get_q = [&](const Walk<kKeys>& x, int side) { fetch_q<T, D, NT, kDup>(a, x.b, x.col, chunks, smem + C::kQ + side * C::kQBytes); };
+  auto put_q = [&](const Walk<kKeys>& x, int side) {
+    QRows<D, NT> rows;
+    uint8_t* q = smem + C::kQ + side * C::kQBytes;
+    wait_q<D, NT, kDup>(q, min(8 * NT, G - x.col % chunks * 8 * NT), rows);
+    __syncwarp();
+    store_q<T, D, NT>(rows, a.scale_log2, reinterpret_cast<uint2*>(q), reinterpret_cast<float*>(smem + C::kQs + side * C::kQsBytes));
+  };
+  look_ahead(w);
+  if (warp == kQWarp) get_q(w, 0);
+  for (int s = 0; s < C::kStages; ++s) issue(s);
+  if (warp == kQWarp) put_q(w, 0);
+  __syncthreads();
+
+  // -------------------------------------------------------------- the units
   const int qr = lane >> 2, qc = lane & 3;        // fragment row and column pair
   const int ka = (qr >> 1) + 4 * (qr & 1);        // the keys of rows qr and qr + 8: ka and ka + 8
-  uint8_t* mine = smem + warp * kSl * C::kSlice;
   const uint32_t k_at = Record<D>::k_word(ka, 2 * qc);
   const uint32_t v_at = Record<D>::kV + lane * 16;
   const uint32_t kp_at = Record<D>::kKp + ka * Record<D>::kPar, vp_at = Record<D>::kVp + ka * Record<D>::kPar;
-  float* buf = reinterpret_cast<float*>(smem + C::kBuf);
-  float2* ml = reinterpret_cast<float2*>(smem + C::kMl);
-  const float sl2 = a.scale_log2;
-
-  const uint2* q = reinterpret_cast<const uint2*>(smem + C::kQ);
-  const float* q_sums = reinterpret_cast<const float*>(smem + C::kQs(NT));
   float qs[NT][kG][2], o[NT][D / 16][4], zs[NT][kG][2], m[NT][2], l[NT][2];
   float by = 0.f, grow[kG];                       // of S^T; brings the s of V so far to 2^7 at most
-  bool dead = false;
   int g = 0, h0 = 0, h1 = 0;                      // kv head, query heads [h0, h1) of the unit
-  uint32_t stage = 0, phase = 0, q_phase = 0;
+  uint32_t stage = 0, phase = 0;
+  int side = 0, owed = -1;              // owed: the stage of the last unit's stash, to be filled
+  auto give_up = [&] {
+    dead = true;
+    // Every copy on its way has to land before the CTA may exit.
+    if (lane == 0)
+      for (uint32_t x = stage; x < stage + flying; ++x)
+        mbar_wait_drain(&bars->full[warp][x % C::kStages], phase ^ (x >= C::kStages), st, kDrainFull);
+    __syncwarp();
+  };
   do {
     // ------------------------------------------------ one unit's tiles here
     // (A CTA of a cluster may have none, and joins in all the same.)
@@ -710,19 +715,31 @@ __global__ void __launch_bounds__(32 * W + 32, NT == 1 && W <= 7 ? 2 : 1) fa_dec
     g = w.col / chunks;
     h0 = g * G + (w.col - g * chunks) * 8 * NT;
     h1 = (g + 1) * G;
-    if (!kCluster || nt > 0) {
-      if (!dead && !wait_warp(&bars->q, q_phase, st, abort_flag, kSiteFull)) dead = true;
-      q_phase ^= 1;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < kG; ++k) {
-          const float2 y = *reinterpret_cast<const float2*>(q_sums + (n * kG + k) * 8 + qc * 2);
-          qs[n][k][0] = y.x;
-          qs[n][k][1] = y.y;
-        }
-      by = q_sums[NT * kG * 8];
+    if (!kCluster && warp == kQWarp) {
+      Walk<kKeys> x = w;
+      advance(x, nt, a, cols);
+      if (x.left > 0) {
+        get_q(x, side ^ 1);
+      }
+      if (lane == 0) bars->next[side] = x;
     }
+    if (!kCluster && owed >= 0) {
+      // Once the others have read the last unit's stash here.
+      if (!dead && !wait_warp(&bars->read, side ^ 1, st, abort_flag, kSiteRead)) give_up();
+      fence_proxy_async_smem();
+      issue(owed);
+    }
+    const uint2* q = reinterpret_cast<const uint2*>(smem + C::kQ + side * C::kQBytes);
+    const float* q_sums = reinterpret_cast<const float*>(smem + C::kQs + side * C::kQsBytes);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < kG; ++k) {
+        const float2 y = *reinterpret_cast<const float2*>(q_sums + (n * kG + k) * 8 + qc * 2);
+        qs[n][k][0] = y.x;
+        qs[n][k][1] = y.y;
+      }
+    by = q_sums[NT * kG * 8];
 #pragma unroll
     for (int k = 0; k < kG; ++k) grow[k] = 0x1p107f;
 #pragma unroll
@@ -736,18 +753,21 @@ __global__ void __launch_bounds__(32 * W + 32, NT == 1 && W <= 7 ? 2 : 1) fa_dec
       m[n][0] = m[n][1] = kNone;
       l[n][0] = l[n][1] = 0.f;
     }
+    uint32_t last = 0;                 // the stage of the unit's last tile
     int key0 = (w.s.tile0 + w.tile) * kKeys + warp * kSl * 16;
     for (int i = 0; i < nt; ++i, key0 += kKeys) {
       // After a wait that gave up the warp goes on through its part without
       // touching the tiles, so that the warps still meet at each unit's end.
-      if (!dead && !wait_warp(&bars->full[stage], phase, st, abort_flag, kSiteFull)) dead = true;
+      if (!dead && !wait_warp(&bars->full[warp][stage], phase, st, abort_flag, kSiteFull)) give_up();
+      --flying;
       // (A slice whose page number is out of range was not loaded: what lies
       // there is worked on, and its sequence's outputs are unspecified.)
       if (!dead && key0 < w.s.len && key0 + kSl * 16 > w.s.first)
-        work<T, D, NT, kDup, kSl>(mine + stage * C::kStage, key0, w.s, k_at, v_at, kp_at, vp_at, ka, by,
-                                                            q + lane, qs, o, zs, m, l, grow);
+        work<T, D, NT, kDup, kSl>(ring + stage * C::kStage, key0, w.s, k_at, v_at, kp_at, vp_at, ka, by, q + lane, qs, o, zs, m, l,
+                                  grow);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->empty[stage]);
+      last = stage;
+      if (kCluster || i + 1 < nt) issue(stage);
       if (++stage == C::kStages) {
         stage = 0;
         phase ^= 1;
@@ -756,6 +776,9 @@ __global__ void __launch_bounds__(32 * W + 32, NT == 1 && W <= 7 ? 2 : 1) fa_dec
     {
       // ------------------------------------------------ the unit's end here
       const bool whole = w.tile == 0 && nt == w.s.n;
+      if (!kCluster && warp == kQWarp && bars->next[side].left > 0) put_q(bars->next[side], side ^ 1);
+      uint8_t* stash = smem + (kCluster ? 0 : last * C::kStage);                   // warp 0's
+      float2* ml = reinterpret_cast<float2*>(stash + warp * C::kRing + C::kMl);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -769,91 +792,91 @@ __global__ void __launch_bounds__(32 * W + 32, NT == 1 && W <= 7 ? 2 : 1) fa_dec
           }
         }
         if (qr == 0) {
-          ml[warp * 16 + n * 8 + qc * 2] = make_float2(m[n][0], l[n][0]);
-          ml[warp * 16 + n * 8 + qc * 2 + 1] = make_float2(m[n][1], l[n][1]);
+          ml[n * 8 + qc * 2] = make_float2(m[n][0], l[n][0]);
+          ml[n * 8 + qc * 2 + 1] = make_float2(m[n][1], l[n][1]);
         }
       }
-      consumer_sync();
+      __syncthreads();
+      auto ml_of = [&](int u, int h) { return *reinterpret_cast<const float2*>(stash + u * C::kRing + C::kMl + h * 8); };
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
+        if (n > 0) __syncthreads();                // the stash's last readers
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float M = kNone;
 #pragma unroll
-          for (int i = 0; i < kWarps; ++i) M = fmaxf(M, ml[i * 16 + n * 8 + qc * 2 + e].x);
+          for (int u = 0; u < kWarps; ++u) M = fmaxf(M, ml_of(u, n * 8 + qc * 2 + e).x);
           f[e] = ex2(m[n][e] - M);
         }
-        // Lane h < 8 of each warp sums head h.  The last reads of ml are before the
-        // last barrier: behind it a warp may be past its tiles of the next unit and
-        // store that unit's (max, sum) while others still sum here.
-        float M = kNone, L = 0.f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, ml[i * 16 + n * 8 + (lane & 7)].x);
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-          const float2 y = ml[i * 16 + n * 8 + (lane & 7)];
-          L += y.y * ex2(y.x - M);
-        }
+        // [head][element], the element xor 4 (head / 2): the rows and column pairs that
+        // a quarter of a warp stores at once fall on 32 banks.
+        float* to = reinterpret_cast<float*>(stash + warp * C::kRing) + qc * 2 * D;
 #pragma unroll
         for (int k = 0; k < kG; ++k) {
-          if (n + k > 0) consumer_sync();          // the buffer's last readers
-          // [warp][head][element of the group], this xor 4 (head / 2): the rows and column
-          // pairs that a quarter of a warp stores at once fall on 32 banks.
-          float* to = buf + (warp * 8 + qc * 2) * 64;
           const float u0 = 0x1p18f / grow[k], u1 = 0x1p22f / grow[k];        // codes are c 2^-18 or c 2^-22, weights s p grow
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float z = kDup && qc >= 2 ? 0.f : zs[n][k][e & 1], s = f[e & 1];
-            *reinterpret_cast<float4*>(to + (e & 1) * 64 + ((qr * 8 + (e >> 1) * 4) ^ (qc * 4))) =
+            *reinterpret_cast<float4*>(to + (e & 1) * D + k * 64 + ((qr * 8 + (e >> 1) * 4) ^ (qc * 4))) =
                 make_float4(fmaf(o[n][4 * k][e], u0, z) * s, fmaf(o[n][4 * k + 1][e], u1, z) * s,
                             fmaf(o[n][4 * k + 2][e], u0, z) * s, fmaf(o[n][4 * k + 3][e], u1, z) * s);
           }
-          consumer_sync();
-          static_assert(kWarps >= 4, "heads of a unit");
-          if (warp < (kDup ? 2 : 4)) {             // two heads a warp
-            const int hh = warp * 2 + (lane >> 4), e = (lane & 15) * 4, d = k * 64 + e, h = h0 + n * 8 + hh;
-            const float Mh = __shfl_sync(0xffffffffu, M, hh), Lh = __shfl_sync(0xffffffffu, L, hh);
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        __syncthreads();
+        const int hh = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4, h = h0 + n * 8 + hh;
+        static_assert(kThreads >= 8 * (D / 4), "a thread for four elements of each head");
+        if (hh < (kDup ? 4 : 8) && h < h1) {
+          float M = kNone, L = 0.f;
 #pragma unroll
-            for (int c = 0; c < (kDup ? 2 : 1); ++c) {             // the low parts' sums with them
-              const int from = (hh + 4 * c) * 64 + (e ^ ((hh + 4 * c >> 1) * 4));
+          for (int u = 0; u < kWarps; ++u) M = fmaxf(M, ml_of(u, n * 8 + hh).x);
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-              for (int u = 0; u < kWarps; ++u) add_scaled(y, 1.f, *reinterpret_cast<const float4*>(buf + from + u * 8 * 64));
-            }
-            if constexpr (kCluster) {
-              // For the join; the tiles have been read.
-              *reinterpret_cast<float4*>(smem + ((n * 8 + hh) * D + d) * 4) = y;
-              if (d == 0) reinterpret_cast<float2*>(smem + kClusterMl<D>)[n * 8 + hh] = make_float2(Mh, Lh);
-            } else if (h < h1) {
-              const long long row = (long long)w.b * a.Hq + h;
-              if (whole) {
-                const float inv = 1.f / Lh;
-                *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + row * D + d) =
-                    make_uint2(Tr::pack(y.x * inv, y.y * inv), Tr::pack(y.z * inv, y.w * inv));
-                if (d == 0) a.lse[row] = (Mh + log2f(Lh)) * 0.69314718055994530942f;
-              } else {
-                // Slot 1: the unit starts in this CTA and goes on; slot 0: it
-                // started earlier.
-                const long long at = ((long long)blockIdx.x * 2 + (w.tile == 0 ? 1 : 0)) * 16 + n * 8 + hh;
-                *reinterpret_cast<float4*>(a.part + at * D + d) = y;
-                if (d == 0) a.part_ml[at] = make_float2(Mh, Lh);
-              }
+          for (int u = 0; u < kWarps; ++u) {
+            const float2 x = ml_of(u, n * 8 + hh);
+            L = fmaf(x.y, ex2(x.x - M), L);
+#pragma unroll
+            for (int c = 0; c < (kDup ? 8 : 4); c += 4)            // and the low parts' sums
+              add_scaled(y, 1.f, *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(stash + u * C::kRing) +
+                                                                  (hh + c) * D + (d ^ (hh + c >> 1) * 4)));
+          }
+          if constexpr (kCluster) {
+            *reinterpret_cast<float4*>(smem + C::kJoin + ((n * 8 + hh) * D + d) * 4) = y;
+            if (d == 0) reinterpret_cast<float2*>(smem + C::kJoin + kClusterMl<D>)[n * 8 + hh] = make_float2(M, L);
+          } else {
+            const long long row = (long long)w.b * a.Hq + h;
+            if (whole) {
+              const float inv = 1.f / L;
+              *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + row * D + d) =
+                  make_uint2(Tr::pack(y.x * inv, y.y * inv), Tr::pack(y.z * inv, y.w * inv));
+              if (d == 0) a.lse[row] = (M + log2f(L)) * 0.69314718055994530942f;
+            } else {
+              // Slot 1: the unit starts in this CTA and goes on; slot 0: it
+              // started earlier.
+              const long long at = ((long long)blockIdx.x * 2 + (w.tile == 0 ? 1 : 0)) * 16 + n * 8 + hh;
+              *reinterpret_cast<float4*>(a.part + at * D + d) = y;
+              if (d == 0) a.part_ml[at] = make_float2(M, L);
             }
           }
         }
       }
     }
-    w.left -= nt;
-    w.tile += nt;
-    if (!kCluster && w.left > 0) w.next_unit(a, cols);
+    if constexpr (!kCluster) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->read);
+      w = bars->next[side];
+      owed = last;
+      side ^= 1;
+    }
   } while (!kCluster && w.left > 0);
   if constexpr (kCluster) {
     if (a.cluster > 1) cluster_sync();
-    else consumer_sync();
-    join_cluster<Tr>(a, smem, w, rank, h0, min(h1, h0 + 8 * NT));
+    else __syncthreads();
+    join_cluster<Tr>(a, smem + C::kJoin, w, rank, h0, min(h1, h0 + 8 * NT));
     __syncwarp();
     if (a.cluster > 1) cluster_sync();             // nobody exits while its share is read
+  } else if (warp == kQWarp) {
+    fill_empty<Tr>(a);
   }
 }
 
@@ -861,28 +884,28 @@ template <typename T, int D>
 __global__ void __launch_bounds__(128) fa_decode4_join_kernel(const DecodeArgs a) {
   launch_dependents();
   wait_for_previous();
-  join<Traits<T, D, 7, 1>>(a);
+  join<Traits<T, D, kDecode4TileKeys, 128>>(a);
 }
 
 // A kernel and its CTA's shape.
 template <typename T, int D, int NT, bool kDup, int W, int kSl, bool kCluster>
 struct Shape {
-  using C = Cfg<D, W, kSl>;
+  using C = Cfg<D, NT, W, kSl>;
   static constexpr auto kernel = fa_decode4_kernel<T, D, NT, kDup, W, kSl, kCluster>;
   static cudaError_t launch(const DecodeArgs& a, const DevStatus& st, int ctas, cudaStream_t stream) {
-    return launch_after(kernel, ctas, C::kThreads, C::bytes(NT), kCluster ? a.cluster : 1, stream, a, st);
+    return launch_after(kernel, ctas, C::kThreads, kSmem<C>, kCluster ? a.cluster : 1, stream, a, st);
   }
   static cudaError_t configure() {
-    static_assert(C::bytes(NT) <= (NT == 1 && W <= 7 ? 115712 : 232448), "shared memory");
+    static_assert(kSmem<C> <= (NT == 1 && W <= 8 ? 115712 : 232448), "shared memory");
     static_assert(C::kKeys == (kCluster ? kDecode4ClusterKeys : kDecode4TileKeys), "tile");
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes(NT));
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<C>);
   }
 };
 // For clusters, which share few tiles, one slice of a tile a warp.
 template <typename T, int D, int NT, bool kDup>
-using Short = Shape<T, D, NT, kDup, 7, 1, true>;
+using Short = Shape<T, D, NT, kDup, 8, 1, true>;
 template <typename T, int D, int NT, bool kDup>
-using Long = Shape<T, D, NT, kDup, 7, 2, false>;
+using Long = Shape<T, D, NT, kDup, 8, 2, false>;
 
 template <typename T, int D, int NT, bool kDup>
 cudaError_t launch_shape(const DecodeArgs& a, const DevStatus& st, int parts, cudaStream_t stream) {

@@ -94,7 +94,7 @@ struct Read4Args {
 
 // Keys of a tile of the decode kernel, by equal parts of the line of tiles and by
 // clusters; and the CTAs that an SM holds, by the heads of a unit.
-constexpr int kDecode4TileKeys = 224, kDecode4ClusterKeys = 112;
+constexpr int kDecode4TileKeys = 256, kDecode4ClusterKeys = 128;
 constexpr int decode4_ctas_per_sm(int unit_heads) { return unit_heads == 8 ? 2 : 1; }
 
 cudaError_t launch_append4(int dtype, const Append4Args& a, const DevStatus& st, int num_sms, cudaStream_t stream);
