@@ -15,27 +15,41 @@
 // keys; so products with V are summed over a tile's two slices only, and those
 // sums added in fp32 (as running sums of the pipe, and of c, o was 1.2 times as far
 // off at 32768 keys).
-//   q, whatever its type, enters in fp16 times a power of two that brings a
-// unit's largest element to 2^10 (16 times that for the codes held as c 2^-22):
-// exact but for elements 2^-24 times smaller than the largest.  The weights s p
-// enter times a power of two that brings the largest s so far to 2^6 (p is 2^8 at
-// most), as the sum of two fp16 values, off by 2^-22 of themselves or 2^-32 of the
-// largest.  Up to four heads a group (kDup) the eight columns hold the heads twice,
-// and the second four the weights' low parts, which costs no product; above that
-// fp16 has two products, and bf16, whose own rounding is 2^4 times coarser, the high
-// parts alone (o is 1.01 times as far off).
+//   q, whatever its type, enters in fp16 times a power of two that brings its
+// head's largest element to 2^10 (16 times that for the codes held as c 2^-22): exact
+// but for elements 2^-24 times smaller than that one.  The weights s p enter times a
+// power of two that brings the largest s so far to 2^6 (p is 2^8 at most), as the sum
+// of two fp16 values, off by 2^-22 of themselves or 2^-31 of that s.  Up to four heads a
+// group (kDup) the eight columns hold the heads twice, and the second four the weights'
+// low parts, which costs no product; above that fp16 has two products.  bf16, whose own
+// rounding is 2^4 times coarser than a high part's, has the high parts alone, off by
+// 2^-11 at most: o is 1.01 times as far off (1.667e-3 against 1.649e-3, relative l2 at
+// 32768 keys), and the low parts cost 6 % in columns and 19 % in products.
 //
-// The line of tiles, its cut into equal parts, one a CTA, and their joins are
-// those of the 16-bit kernel (fa_decode.cuh, fa_paged.cu); a warp's slice of a tile
-// is one record of 16 keys, which one untiled copy fetches.  Warp 7 is the
-// producer, warps 0-6 own a slice of each tile each.  Products by mma.sync
-// (m16n8k16) with keys, then elements of d as rows and 8 heads as columns: see
-// fa_paged.cu.  Row i of a slice's S^T is the key (i % 8) / 2 + 4 (i % 2) + 8 (i / 8),
-// the pairs of keys that a word of V holds (fa_paged4.h); O^T's rows are the
+// The line of tiles, its cut into equal parts, one a CTA, and their joins are those of
+// the 16-bit kernel (fa_decode.cuh, fa_paged.cu).  A unit's end counts as two tiles
+// there (kEnd: 64 sequences of 0 .. 8192 keys, d = 64, 96 us with none, 84, 76 and 77 us
+// with one, two and three).  A warp's slice of a tile is one record of 16 keys, and each
+// of a CTA's eight warps works on two neighbouring records of a tile, fetched by untiled
+// copies (one, where they lie in a page) into a ring of its own: it waits for no other
+// warp before the unit's end.  (Seven warps and a producer that fetched for all left two
+// of an SM's four schedulers with fewer warps: pages of 16, 126 us against 116, d = 64 142
+// against 128.)  One warp also brings the next unit's query rows.  At a unit's end each
+// warp leaves its sums in the place of its last tile, and fills that again once all have
+// read them, while its other tiles are on their way.
+//   Products by mma.sync (m16n8k16) with keys, then elements of d as rows and 8 heads as
+// columns: see fa_paged.cu.  Row i of a slice's S^T is the key (i % 8) / 2 + 4 (i % 2) +
+// 8 (i / 8), the pairs of keys that a word of V holds (fa_paged4.h); O^T's rows are the
 // elements 8 r + t and 8 r + 4 + t of a group (lane row r, tile t).
 //   A running maximum that is behind by less than 2^8 is as good as the exact
 // one (weights up to 2^8, sums in fp32): the warp then neither exchanges maxima
 // nor rescales.
+//
+// Bound by issue: 332 instructions a slice of d = 128, of them 138 on the integer pipe
+// (64 masks, 16 byte swaps) and 18 products.  16 sequences of 32768 keys, 8 kv heads of 4
+// heads (604 MB): 113 us, 5.3 TB/s; the copies alone take 98 us, the work alone as long as
+// both.  16 heads a group (two column tiles, one CTA an SM with 255 registers a thread)
+// take 177 us; as two units of eight heads they would take twice 114.
 #include "fa_decode.cuh"
 #include "fa_paged4.h"
 #include "fa_rotary.cuh"
@@ -51,7 +65,7 @@ enum : int { kSiteFull = 54, kSiteRead = 55, kDrainFull = 56 };
 
 // A CTA's shape: kWarps warps, kSl slices of a tile each, and each a ring of its own
 // for the records on their way.
-template <int D, int NT, int W, int kSl>
+template <int D, int NT, int W, int kSl, bool kCluster>
 struct Cfg {
   static constexpr int kWarps = W, kKeys = 16 * kSl * W, kThreads = 32 * W;
   static constexpr uint32_t kSlice = Record<D>::kBytes, kStage = kSl * kSlice;
@@ -60,18 +74,17 @@ struct Cfg {
   // At a unit's end a warp's O [8 heads][D] and (max, sum) [8 NT] take the place of the
   // last tile (in a cluster, of the ring's first records).
   static constexpr uint32_t kMl = 8u * D * 4u, kStash = kMl + NT * 64u;
-  static_assert(kStash <= (kSl == 2 ? kStage : 2 * kStage) && kStash % 8 == 0, "stash");
+  static_assert(kStash <= (kCluster ? kRing : kStage) && kStash % 8 == 0, "stash");
   static constexpr uint32_t kJoin = kStash;                    // the cluster's join, in warp 0's ring
   static_assert(kJoin + 16u * D * 4u + 128u <= kRing && kJoin % 16 == 0, "join");
-  // Two of: a unit's query rows, first as they are and then as operands; [NT][D / 64][8
-  // heads] their sums over the groups, and a factor.
+  // Two of (in a cluster one): a unit's query rows, first as they are and then as operands; their sums
+  // over the groups, [NT][D / 64][8 heads], and factors, [NT][8].
   static constexpr uint32_t kQ = W * kRing, kQBytes = NT * D * 16u;
-  static constexpr uint32_t kQs = kQ + 2 * kQBytes, kQsBytes = NT * (D / 64) * 32u + 16u;
-  static constexpr uint32_t kBars = kQs + 2 * kQsBytes;
+  static constexpr uint32_t kQs = kQ + (kCluster ? 1 : 2) * kQBytes, kQsBytes = NT * (D / 64 + 1) * 32u;
+  static constexpr uint32_t kBars = kQs + (kCluster ? 1 : 2) * kQsBytes;
 };
 
-// A unit's end takes about as long as two tiles do, and counts as so many in the line that is
-// cut into equal parts.
+// Tiles that a unit's end counts as in the line that is cut into equal parts.
 constexpr int kEnd = 2;
 __device__ __forceinline__ int cost_of(const Span& s) { return s.n > 0 ? s.n + kEnd : 0; }
 // On behind the tiles up to `tile` of a unit, and its end.
@@ -208,40 +221,38 @@ __device__ __forceinline__ void wait_q(const uint8_t* raw, int heads, QRows<D, N
   }
 }
 // The same as B operands, column = head lane / 4: at to[n][g][w][h][lane] the four
-// elements 64 g + 16 (lane % 4) + 8 w + 4 h on, times a power of two and, the odd
-// pairs, 16; at sums[n][g] the heads' sums over the groups, and behind them the
-// factor, both in the units of the scores (see work).
+// elements 64 g + 16 (lane % 4) + 8 w + 4 h on, times the head's power of two and, the
+// odd pairs, 16; sums[n][g][head] over the groups, and factors [n][head] behind them,
+// both in the units of the scores (see work).
 template <typename T, int D, int NT>
 __device__ __forceinline__ void store_q(const QRows<D, NT>& q, float scale_log2, uint2* to, float* sums) {
   const int lane = threadIdx.x & 31;
-  float top = 0x1p-100f, s[NT][D / 64];           // the largest finite |q|
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int n = 0; n < NT; ++n) {
+    float top = 0x1p-100f, s[D / 64];             // the largest finite |q|
 #pragma unroll
     for (int k = 0; k < D / 64; ++k) {
-      s[n][k] = 0.f;
+      s[k] = 0.f;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const uint32_t e[4] = {q.x[n][k][w].x, q.x[n][k][w].y, q.x[n][k][w].z, q.x[n][k][w].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 y = Type<T>::up(e[i]);
-          s[n][k] += y.x + y.y;
+          s[k] += y.x + y.y;
           top = fmaxf(top, fabsf(y.x) < INFINITY ? fabsf(y.x) : 0.f);
           top = fmaxf(top, fabsf(y.y) < INFINITY ? fabsf(y.y) : 0.f);
         }
       }
-      s[n][k] += __shfl_xor_sync(0xffffffffu, s[n][k], 1);
-      s[n][k] += __shfl_xor_sync(0xffffffffu, s[n][k], 2);
+      s[k] += __shfl_xor_sync(0xffffffffu, s[k], 1);
+      s[k] += __shfl_xor_sync(0xffffffffu, s[k], 2);
     }
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float times = 1024.f / power_of(top), more = 16.f * times;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const float times = 1024.f / power_of(top), more = 16.f * times;
 #pragma unroll
     for (int k = 0; k < D / 64; ++k) {
-      if ((lane & 3) == 0) sums[(n * (D / 64) + k) * 8 + (lane >> 2)] = s[n][k] * (times * 0x1p-18f);
+      if ((lane & 3) == 0) sums[(n * (D / 64) + k) * 8 + (lane >> 2)] = s[k] * (times * 0x1p-18f);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const uint4 v = q.x[n][k][w];
@@ -251,7 +262,8 @@ __device__ __forceinline__ void store_q(const QRows<D, NT>& q, float scale_log2,
         x[32] = make_uint2(Half::pack(y2.x * times, y2.y * times), Half::pack(y3.x * more, y3.y * more));
       }
     }
-  if (lane == 0) sums[NT * (D / 64) * 8] = scale_log2 * 0x1p18f / times;
+    if ((lane & 3) == 0) sums[NT * (D / 64) * 8 + n * 8 + (lane >> 2)] = scale_log2 * 0x1p18f / times;
+  }
 }
 
 constexpr float kNone = -1e30f;      // below every score: the maximum before the first key
@@ -267,7 +279,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
 // maximum m and, in l, zs and o, their sums.
 template <typename T, int D, int NT, bool kDup, int kSl>
 __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint32_t k_at, uint32_t v_at, uint32_t kp_at,
-                                     uint32_t vp_at, int ka, float by, const uint2* q,
+                                     uint32_t vp_at, int ka, const float (&by)[NT][2], const uint2* q,
                                      const float (&qs)[NT][D / 64][2], float (&o)[NT][D / 16][4], float (&zs)[NT][D / 64][2],
                                      float (&m)[NT][2], float (&l)[NT][2], float (&grow)[D / 64]) {
   constexpr int kG = D / 64, kW = kDup ? 1 : Type<T>::kWeights, kStep = Record<D>::kBytes, kGap = 16;
@@ -352,7 +364,7 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
       top[n][e] = fmaxf(x[0][n][e], x[0][n][2 + e]);
 #pragma unroll
       for (int j = 1; j < kSl; ++j) top[n][e] = fmax3(top[n][e], x[j][n][e], x[j][n][2 + e]);
-      more |= fmaf(top[n][e], by, -8.f) > m[n][e];
+      more |= fmaf(top[n][e], by[n][e], -8.f) > m[n][e];
     }
 #pragma unroll
   for (int k = 0; k < kG; ++k) most[k] = 0.f;
@@ -375,7 +387,7 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(0xffffffffu, top[n][e], d));
-        const float to = fmaxf(m[n][e], top[n][e] * by);
+        const float to = fmaxf(m[n][e], top[n][e] * by[n][e]);
         f[e] = ex2(m[n][e] - to);
         m[n][e] = to;
         l[n][e] *= f[e];
@@ -421,7 +433,7 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
 #pragma unroll
     for (int j = 0; j < kSl; ++j) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[j][n][e] = ex2(fmaf(x[j][n][e], by, -m[n][e & 1]));
+      for (int e = 0; e < 4; ++e) x[j][n][e] = ex2(fmaf(x[j][n][e], by[n][e & 1], -m[n][e & 1]));
       l[n][0] += x[j][n][0] + x[j][n][2];
       l[n][1] += x[j][n][1] + x[j][n][3];
     }
@@ -509,7 +521,7 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
 
 template <typename T, int D, int NT, bool kDup, int W, int kSl, bool kCluster>
 __global__ void __launch_bounds__(32 * W, NT == 1 && W <= 8 ? 2 : 1) fa_decode4_kernel(const DecodeArgs a, const DevStatus st) {
-  using C = Cfg<D, NT, W, kSl>;
+  using C = Cfg<D, NT, W, kSl, kCluster>;
   constexpr int kKeys = C::kKeys, kWarps = W, kThreads = C::kThreads, kG = D / 64;
   using Tr = Traits<T, D, kKeys, kThreads>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -696,7 +708,7 @@ __global__ void __launch_bounds__(32 * W, NT == 1 && W <= 8 ? 2 : 1) fa_decode4_
   const uint32_t v_at = Record<D>::kV + lane * 16;
   const uint32_t kp_at = Record<D>::kKp + ka * Record<D>::kPar, vp_at = Record<D>::kVp + ka * Record<D>::kPar;
   float qs[NT][kG][2], o[NT][D / 16][4], zs[NT][kG][2], m[NT][2], l[NT][2];
-  float by = 0.f, grow[kG];                       // of S^T; brings the s of V so far to 2^7 at most
+  float by[NT][2], grow[kG];                      // of S^T; brings the s of V so far to 2^7 at most
   int g = 0, h0 = 0, h1 = 0;                      // kv head, query heads [h0, h1) of the unit
   uint32_t stage = 0, phase = 0;
   int side = 0, owed = -1;              // owed: the stage of the last unit's stash, to be filled
@@ -732,14 +744,17 @@ __global__ void __launch_bounds__(32 * W, NT == 1 && W <= 8 ? 2 : 1) fa_decode4_
     const uint2* q = reinterpret_cast<const uint2*>(smem + C::kQ + side * C::kQBytes);
     const float* q_sums = reinterpret_cast<const float*>(smem + C::kQs + side * C::kQsBytes);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int k = 0; k < kG; ++k) {
         const float2 y = *reinterpret_cast<const float2*>(q_sums + (n * kG + k) * 8 + qc * 2);
         qs[n][k][0] = y.x;
         qs[n][k][1] = y.y;
       }
-    by = q_sums[NT * kG * 8];
+      const float2 y = *reinterpret_cast<const float2*>(q_sums + NT * kG * 8 + n * 8 + qc * 2);
+      by[n][0] = y.x;
+      by[n][1] = y.y;
+    }
 #pragma unroll
     for (int k = 0; k < kG; ++k) grow[k] = 0x1p107f;
 #pragma unroll
@@ -890,7 +905,7 @@ __global__ void __launch_bounds__(128) fa_decode4_join_kernel(const DecodeArgs a
 // A kernel and its CTA's shape.
 template <typename T, int D, int NT, bool kDup, int W, int kSl, bool kCluster>
 struct Shape {
-  using C = Cfg<D, NT, W, kSl>;
+  using C = Cfg<D, NT, W, kSl, kCluster>;
   static constexpr auto kernel = fa_decode4_kernel<T, D, NT, kDup, W, kSl, kCluster>;
   static cudaError_t launch(const DecodeArgs& a, const DevStatus& st, int ctas, cudaStream_t stream) {
     return launch_after(kernel, ctas, C::kThreads, kSmem<C>, kCluster ? a.cluster : 1, stream, a, st);

@@ -92,8 +92,9 @@ struct Read4Args {
   int B, N;
 };
 
-// Keys of a tile of the decode kernel, by equal parts of the line of tiles and by
-// clusters; and the CTAs that an SM holds, by the heads of a unit.
+// Keys of a tile of the decode kernel, by equal parts of the line of tiles (two records
+// a warp, whose products take turns) and by clusters (one, as their units are short); and
+// the CTAs that an SM holds, by the heads of a unit.
 constexpr int kDecode4TileKeys = 256, kDecode4ClusterKeys = 128;
 constexpr int decode4_ctas_per_sm(int unit_heads) { return unit_heads == 8 ? 2 : 1; }
 
