@@ -23,13 +23,19 @@ fp32 and to the type, is off by u + 2^-23 of itself.  With them the 16-bit row i
 off by e (above), its group's ends too, and so the value is within s / 2 + 15 u s
 (s rounded, codes cut at 15) of the row's, s <= ((range + 2 e) / 15)(1 + u).
 
-Attention: products of q with z + s c are formed as s times sums of q (1 + c /
-16), less q, and z times sums of q, each in fp32: the parts are bounded by |q| (|z|
-+ 32 s), and X = scale sum |q| (|z| + 32 s); a score is off by X (d + 8) 2^-23 (adders
-may truncate: a factor 2), its exponential by 2^-22, sums over n keys by n 2^-24
-together e; lse is off by e.  The weights s p enter as the sum of two bf16
-values, off by 2^-16, times (1 + c / 16): with A = sum p (|z| + 32 s), o is off by (2.1
-e + 2^-16 + (d + n) 2^-23) A and its rounding.
+Attention: products of q with z + s c are formed as s times sums of q c, and z
+times sums of q, each in fp32: the parts are bounded by |q| (|z| + 32 s), and X =
+scale sum |q| (|z| + 32 s); a score is off by X (d + 8) 2^-23 (adders may truncate: a
+factor 2), its exponential by 2^-22, sums over n keys by n 2^-24 together e; lse is
+off by e.  (q enters in fp16 times a power of two of its head, which brings the
+largest element Q to 2^10: one of fp16's subnormal steps is 2^-34 Q, so a score is off
+by scale 15 s d 2^-35 Q at most, 2^-36 d X, which the 8 above holds.)  The weights s p
+enter as fp16 values W off by 2^-11 of themselves (bf16; half a step of ten bits) or,
+two values, by 2^-22 (fp16), or by half a subnormal step, 2^-25, where the group's
+largest s so far counts 2^6 at least: 2^-31 S; each times |c - 7.5| <= 7.5.  The sum of the p that
+these are relative to is 1 at least, so with A = sum p (|z| + 32 s) >= 32 sum p s and S
+the group's largest visible s, o is off by (2.1 e + W 7.5 / 32 + (d + n) 2^-23) A + n
+2^-28 S and its rounding.
 """
 import math
 import threading
@@ -46,6 +52,7 @@ pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+WEIGHT = {torch.bfloat16: 2.0 ** -11, torch.float16: 2.0 ** -22}          # the decode kernel's weights
 TINY = {torch.bfloat16: 0.0, torch.float16: 2.0 ** -24}       # fp16's subnormal step
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
 
@@ -378,7 +385,12 @@ def assert_decoded(o, lse, q, k, v, lens, scale, window, what=""):
         ro, rl, x, a = paged4.decode(qn[b], kn[at:at + n].swapaxes(0, 1), vn[at:at + n].swapaxes(0, 1), scale, window, r)
         at += n
         e = (x * (d + 8) * 2.0 ** -23 + 2.0 ** -21 + n * 2.0 ** -24)
-        bound = U[dt] * np.abs(ro) + (2.1 * e[:, None] + 2.0 ** -16 + (d + n) * 2.0 ** -23) * a + TINY[dt]
+        most = np.zeros_like(a)
+        if n:
+            s = paged4.quantise(vn[at - min(n, window or n):at], r)[1].max(0)            # [Hkv, d / 64]
+            most = np.repeat(np.repeat(s, 64, 1), qn.shape[1] // s.shape[0], 0)
+        bound = (U[dt] * np.abs(ro) + (2.1 * e[:, None] + WEIGHT[dt] * 7.5 / 32 + (d + n) * 2.0 ** -23) * a
+                 + n * 2.0 ** -28 * most + TINY[dt])
         err = np.abs(on[b] - ro)
         assert (err <= bound).all(), f"{what} sequence {b}: o off by {(err / np.maximum(bound, 1e-30)).max()} of the bound"
         if n == 0:
@@ -416,6 +428,11 @@ APPEND = [
     ([130], [129], 0, 9, 1, 128, 32, None, F32, BF, "layers"),
     ([64, 70], [20, 70], 0, 0, 5, 128, 16, (64,), None, HF, "hpd"),
     ([1000, 600], [1000, 600], 0, 16, 8, 128, 128, (64,), HF, HF, "hnd"),
+    ([40, 9], [40, 9], 0, 3, 2, 128, 16, (8,), F32, BF, "hnd"),           # vectors of both groups in a thread
+    ([40, 9], [40, 9], 0, 3, 2, 128, 16, (8, 16), None, HF, "hnd"),
+    ([40, 9], [40, 9], 0, 3, 2, 128, 16, (16, 32), F32, BF, "hnd"),
+    ([40, 9], None, 0, 3, 2, 128, 16, (56,), False, HF, "hnd"),
+    ([40, 9], [40, 9], 0, 2, 2, 64, 16, (8,), F32, BF, "hnd"),
 ]
 
 
@@ -607,6 +624,11 @@ def spread(B, longest, seed):
     (300, 60, 2, 1, 64, 16, 0, BF),          # more sequences than a block has threads
     (700, 140, 2, 2, 64, 16, 0, HF),
     (400, 50, 16, 8, 128, 16, 0, HF),        # many units of one tile
+    (90, 700, 8, 8, 128, 32, 0, HF),         # units of one to three tiles: parts that begin at a unit's end
+    (90, 700, 16, 4, 64, 16, 0, HF),
+    (120, 600, 16, 2, 64, 48, 300, HF),
+    (280, 600, 32, 2, 64, 32, 0, BF),        # and more sequences than threads
+    (90, 1100, 5, 5, 128, 16, 0, BF),
 ])
 def test_decode_batches(cuda_lib, B, longest, Hq, Hkv, d, page, window, dt):
     lens = spread(B, longest, seed=B)
@@ -626,6 +648,65 @@ def test_decode_peaked_and_flat(cuda_lib, sigma, scale, dt):
     o, lse = fa.paged4_decode(q, cache, table, ln, scale=scale)
     ok()
     assert_decoded(o, lse, q, k, v, [1900, 64, 300], scale, 0, f"sigma {sigma}")
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("lens,Hq,Hkv,d", [([900], 8, 1, 128), ([1300] * 40, 16, 2, 64), ([1300] * 20, 32, 2, 128)])
+def test_decode_heads_of_very_different_size(cuda_lib, lens, Hq, Hkv, d, dt):
+    # Each head's q in its own range, and elements of one head far apart.
+    cache, table, ln, k, v = filled(lens, Hkv, 16, d, dt, seed=61)
+    g = torch.Generator().manual_seed(62)
+    q = torch.randn((len(lens), Hq, d), generator=g)
+    lo = -10 if dt is HF else -60
+    q *= 2.0 ** torch.randint(lo, 4, (len(lens), Hq, 1), generator=g)
+    q[:, ::3, ::2] *= 2.0 ** -9
+    q = q.to(dt).to(DEV)
+    o, lse = fa.paged4_decode(q, cache, table, ln, scale=0.3)
+    ok()
+    assert_decoded(o, lse, q, k, v, lens, 0.3, 0, "heads")
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("lens,Hq,Hkv,d", [([900], 8, 1, 128), ([900] * 48, 4, 2, 64), ([900] * 40, 16, 1, 128)])
+def test_decode_steps_of_very_different_size(cuda_lib, lens, Hq, Hkv, d, down, dt):
+    # The steps of V grow (or shrink) by 2^20 along a sequence, one group's much faster than the other's, some are 0; and
+    # the keys with the largest steps may weigh nothing.
+    g = torch.Generator().manual_seed(63)
+    T, n = sum(lens), lens[0]
+    up = torch.arange(T) % n / n
+    size = 2.0 ** torch.stack([20 * up - 12, 3 * up], 1)[:, :d // 64]
+    v = torch.randn((T, Hkv, d // 64, 64), generator=g) * (size.flip(0) if down else size)[:, None, :, None]
+    v[::7] = 0.25
+    k = torch.randn((T, Hkv, d), generator=g)
+    k[:, :, 0] = 8 * up[:, None] - 4
+    k, v = k.to(dt).to(DEV), v.reshape(T, Hkv, d).to(dt).to(DEV)
+    cache, table, ln, _, _ = filled(lens, Hkv, 32, d, dt, seed=64, rows=[k, v])
+    q = torch.randn((len(lens), Hq, d), generator=g)
+    q[:, ::2, 0] = -6
+    q = q.to(dt).to(DEV)
+    o, lse = fa.paged4_decode(q, cache, table, ln, scale=0.5)
+    ok()
+    assert_decoded(o, lse, q, k, v, lens, 0.5, 0, "steps")
+
+
+@pytest.mark.parametrize("backwards", [False, True])
+def test_decode_of_pages_side_by_side(cuda_lib, backwards):
+    # One kv head and pages in order: the records of a tile follow one another in memory, across pages too.
+    lens, d = [2000, 1999, 15, 300], 128
+    _, _, _, k, v = filled(lens, 1, 16, d, BF, seed=65)
+    n = [-(-x // 16) for x in lens]
+    first = np.concatenate([[0], np.cumsum(n)])
+    table = torch.stack([torch.arange(max(n)) + int(first[b]) for b in range(4)]).to(torch.int32)
+    if backwards:
+        table = int(first[-1]) - 1 - table
+    table, ln = table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    cache = new_cache(int(first[-1]), 1, 16, d)
+    fa.paged4_append(cache, table, ln, k, v, cu_seqlens=offsets(lens))
+    q = torch.randn((4, 6, d), generator=torch.Generator().manual_seed(66)).to(BF).to(DEV)
+    o, lse = fa.paged4_decode(q, cache, table, ln)
+    ok()
+    assert_decoded(o, lse, q, k, v, lens, d ** -0.5, 0, "side by side")
 
 
 @pytest.mark.parametrize("down", [False, True])
