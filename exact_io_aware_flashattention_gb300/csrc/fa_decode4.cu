@@ -282,7 +282,7 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
                                      uint32_t vp_at, int ka, const float (&by)[NT][2], const uint2* q,
                                      const float (&qs)[NT][D / 64][2], float (&o)[NT][D / 16][4], float (&zs)[NT][D / 64][2],
                                      float (&m)[NT][2], float (&l)[NT][2], float (&grow)[D / 64]) {
-  constexpr int kG = D / 64, kW = kDup ? 1 : Type<T>::kWeights, kStep = Record<D>::kBytes, kGap = 16;
+  constexpr int kG = D / 64, kW = kDup ? 1 : Type<T>::kWeights, kStep = Record<D>::kBytes;
   // Scores, in units of log2 / by: S^T rows ka, ka + 8, columns 2 qc, 2 qc + 1.
   float x[kSl][NT][4];
   {
@@ -336,12 +336,12 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
           }
     }
   }
-  if (key0 < s.first || key0 + (kSl - 1) * kGap + 16 > s.len) {
+  if (key0 < s.first || key0 + kSl * 16 > s.len) {
     // Keys that are not visible: their (s, z) of V, perhaps never loaded, may be
     // anything, and become 0.
 #pragma unroll
     for (int j = 0; j < kSl; ++j) {
-      const int key = key0 + j * kGap + ka;
+      const int key = key0 + 16 * j + ka;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (key + 8 * h < s.first || key + 8 * h >= s.len) {

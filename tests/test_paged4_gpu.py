@@ -690,6 +690,30 @@ def test_decode_steps_of_very_different_size(cuda_lib, lens, Hq, Hkv, d, down, d
     assert_decoded(o, lse, q, k, v, lens, 0.5, 0, "steps")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_last_keys_of_the_longest_sequences(cuda_lib, d):
+    # Lengths up to 2^30, the most a table may hold, over one page that it names again and again: the last keys.
+    ps, n = 65536, 500
+    lens = [2 ** 30, 2 ** 30 - 15, 2 ** 30 - 300]
+    g = torch.Generator().manual_seed(67)
+    k, v = (torch.randn((ps, 1, d), generator=g).to(BF).to(DEV) for _ in range(2))
+    cache = new_cache(1, 1, ps, d)
+    one = torch.zeros((1, 1), dtype=torch.int32, device=DEV)
+    fa.paged4_append(cache, one, torch.tensor([ps], dtype=torch.int32, device=DEV), k, v, cu_seqlens=offsets([ps]))
+    table = torch.zeros((3, 16384), dtype=torch.int32, device=DEV)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    at = torch.tensor([[(m - n + i) % ps for i in range(n)] for m in lens]).reshape(-1).to(DEV)
+    q = torch.randn((3, 4, d), generator=g).to(BF).to(DEV)
+    for window in (1, 15, n):
+        o, lse = fa.paged4_decode(q, cache, table, ln, window=window)
+        ok()
+        assert_decoded(o, lse, q, k[at], v[at], [n] * 3, d ** -0.5, window, f"window {window}")
+    kr, vr = fa.paged4_read(cache, table, ln, n, BF)
+    ok()
+    assert_read(kr, last_rows(k[at], [n] * 3, n, BF), BF, "k")
+    assert_read(vr, last_rows(v[at], [n] * 3, n, BF), BF, "v")
+
+
 @pytest.mark.parametrize("backwards", [False, True])
 def test_decode_of_pages_side_by_side(cuda_lib, backwards):
     # One kv head and pages in order: the records of a tile follow one another in memory, across pages too.
