@@ -341,14 +341,14 @@ __global__ void __launch_bounds__(kThreads) fa_read4_kernel(const Read4Args a, c
 }
 
 // Two waves of blocks, five an SM, and no more, since each forms its tokens' angles
-// anew; a head a block where even half as many blocks would not fill one wave.
+// anew; a head a block only where that is no more than a wave.
 // Append alone, 7357 tokens of 48 heads: 10 blocks an SM 40.2 us, 12 40.2, 16 41.2, 24
 // 43.9; 512 tokens: one head a block 10.3 us, two 8.1.
 int heads_per_block(long long token_blocks, int heads, int num_sms) {
   const long long want = 10LL * num_sms;
   const long long splits = std::min<long long>((want + token_blocks - 1) / token_blocks, heads);
   const int hpb = (int)((heads + splits - 1) / splits);
-  return hpb == 1 && token_blocks * heads >= want ? 2 : hpb;
+  return hpb == 1 && token_blocks * heads > 5LL * num_sms ? 2 : hpb;
 }
 
 template <typename T, int D>

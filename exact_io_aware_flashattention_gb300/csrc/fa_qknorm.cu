@@ -10,10 +10,19 @@
 // Bound by HBM: the forward reads and writes each element once, the gradient
 // reads dy and x and writes dx.  A thread owns one token and eight pairs (two
 // 16-byte vectors of a row), as in fa_rope.cu; the row's sums go over its
-// lanes, d / 16 rounded up to a power of two.
+// lanes, d / 16 rounded up to a power of two.  Vectors are copied to shared memory
+// three rows ahead (four in the gradient, 32 KB a block, three blocks an SM at 157
+// registers), since loads into registers kept too few bytes on their way: the
+// forward 31.2 -> 24.9 us, the gradient 210 -> 87.  4 x 2048 tokens of 32 heads, d = 128, bf16,
+// 134 MB: 23.6 us, 5.7 TB/s; the gradient of 2 x 8192 tokens of 40 heads, 503 MB, 85.7 us,
+// 5.9 TB/s.  Small calls are the latency of a load, the angles and a store, 3.3 us (8 + 2
+// heads of 513 tokens, d = 64), and of the gradient's second kernel, 6.2.
 #include "fa_paged4.h"
 #include "fa_rotary.cuh"
 #include "sm103a.cuh"
+
+#include <algorithm>
+#include <climits>
 
 namespace fa {
 
@@ -249,20 +258,27 @@ __global__ void __launch_bounds__(kThreads) fa_qk_norm_dw_kernel(const NormRopeB
   const int i = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, part = blockIdx.y, lane = threadIdx.x % 32;
   if (i >= a.d || !a.dw[part]) return;
   const float* p = a.part + (long long)(part ? a.blocks[0] : 0) * a.d + i;
-  double s = 0.0;
-  for (int b = lane; b < a.blocks[part]; b += 32) s += (double)p[(long long)b * a.d];
+  float s = 0.f, lost = 0.f;                       // (Kahan's sum: fp64 adds took 3-6 us more)
+#pragma unroll 4
+  for (int b = lane; b < a.blocks[part]; b += 32) {
+    const float x = __fsub_rn(p[(long long)b * a.d], lost), y = __fadd_rn(s, x);
+    lost = __fsub_rn(__fsub_rn(y, s), x);
+    s = y;
+  }
   for (int d = 1; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  if (lane == 0) a.dw[part][i] = (float)s;
+  if (lane == 0) a.dw[part][i] = s;
 }
 
-// Heads per block of the forward: as many as still leave 16 blocks an SM, so that
-// angles are formed for several heads at once.
+// Heads per block of the forward, which share their angles: two waves of blocks, five
+// an SM, but 11 heads at most, so that large calls end evenly; and a head a block only
+// where that is no more than a wave.  us by 10 | 16 blocks an SM: 4 x 2048
+// tokens of 32 heads 23.6 | 24.2, 2048 of 40 heads 11.3 | 12.9; 16384 of 32 heads with 16 |
+// 11 heads a block 48.0 | 45.3; 512 of 40 heads with one | two 7.9 | 5.5.
 int heads_per_block(long long token_blocks, int heads, int num_sms) {
-  const long long want = 16LL * num_sms;
-  long long splits = (want + token_blocks - 1) / token_blocks;
-  if (splits > heads) splits = heads;
-  if (splits < 1) splits = 1;
-  return (int)((heads + splits - 1) / splits);
+  const long long want = 10LL * num_sms;
+  const long long splits = std::min<long long>(std::max<long long>((want + token_blocks - 1) / token_blocks, (heads + 10) / 11), heads);
+  const int hpb = (int)((heads + splits - 1) / splits);
+  return hpb == 1 && token_blocks * heads > 5LL * num_sms ? 2 : hpb;
 }
 
 }  // namespace
@@ -291,21 +307,38 @@ cudaError_t launch_norm_rope(int dtype, const NormRopeArgs& a, const DevStatus& 
 cudaError_t launch_norm_rope_bwd(int dtype, NormRopeBwdArgs a, const DevStatus& st, int num_sms, cudaStream_t stream) {
   const int tpb = tokens_per_block(a.d);
   const long long token_blocks = ((long long)a.B * a.N + tpb - 1) / tpb;
-  const int most = min(kBwdBlocks * num_sms, kNormBwdMaxBlocks), heads = a.H[0] + a.H[1];
-  // Heads of a block, which share their angles: eight, or fewer where there would
-  // be less than eight groups of tokens a block.
-  int hpb = 8;
-  while (hpb > 1 && token_blocks * heads < 8LL * most * hpb) hpb /= 2;
-  for (int i = 0; i < 2; ++i) {
-    // The part's share of the blocks, a multiple of its splits, no more than it has
-    // groups for and at least one a split.
-    const int splits = (a.H[i] + hpb - 1) / hpb;
-    if (splits == 0) continue;
-    const long long share = (long long)most * a.H[i] / heads / splits;
-    a.blocks[i] = (int)(splits * max(1LL, min(share, token_blocks)));
+  const int most = min(kBwdBlocks * num_sms, kNormBwdMaxBlocks);
+  // Heads of a block, which share their angles: what takes the busiest block least, a
+  // group of tokens counted as its heads and two more for the angles (2048 tokens of 32 +
+  // 8 heads: one head a block 32 us, four 20).
+  int hpb = 1;
+  long long least = LLONG_MAX;
+  for (int n = 1; n <= 8; ++n) {
+    int splits[2], blocks[2] = {};
+    long long cost[2], all = 0, time = 0;
+    for (int i = 0; i < 2; ++i) {
+      splits[i] = (a.H[i] + n - 1) / n;
+      cost[i] = min(n, a.H[i]) + 2;
+      all += splits[i] * cost[i];
+    }
+    for (int i = 0; i < 2; ++i) {
+      // The part's share of the blocks by its cost, a multiple of its splits, no more
+      // than it has groups for and at least one a split.
+      if (splits[i] == 0) continue;
+      const long long share = max(1LL, min(most * cost[i] / all, token_blocks));
+      blocks[i] = (int)(splits[i] * share);
+      time = max(time, (token_blocks + share - 1) / share * cost[i]);
+    }
+    if (n < 8 && blocks[0] + blocks[1] > most) continue;               // more than run at a time
+    if (time < least) {
+      least = time;
+      hpb = n;
+      a.blocks[0] = blocks[0];
+      a.blocks[1] = blocks[1];
+    }
   }
   if (a.blocks[0] + a.blocks[1] > kNormBwdMaxBlocks) {
-    // Thousands of heads: a block for all heads of a part.
+    // More heads than eight for each of these: a block for all heads of a part.
     hpb = max(a.H[0], a.H[1]);
     for (int i = 0; i < 2; ++i) a.blocks[i] = a.H[i] ? (int)min(token_blocks, (long long)max(1, most / 2)) : 0;
   }
