@@ -138,6 +138,10 @@ NORM = [
     (1, 6, 6, 50, 96, (16,), True, 77, BF, F32),
     (2, 3, 1, 21, 48, None, False, 0, HF, HF),                # the norm alone
     (1, 8, 8, 130, 128, None, False, 0, BF, None),
+    (1, 20000, 3, 5, 16, (8,), False, 0, BF, F32),            # more heads than blocks for eight each
+    (1, 3000, 1000, 9, 32, (16,), True, 4, HF, F32),
+    (2, 1, 700, 3, 64, (32,), False, 0, BF, BF),
+    (1, 40, 1, 1000, 128, (64,), False, 0, BF, F32),          # k's few rows and many angles
     (1, 1, 1, 1, 112, (56,), False, 9, BF, BF),
     (4, 32, 32, 1, 128, (64,), False, 4000, BF, BF),          # one token a sequence
     (1, 40, 8, 5000, 64, (32,), False, 0, HF, F32),           # several items a block
