@@ -8,8 +8,11 @@
 // Every step is one IEEE operation, so that the same 16-bit row gives the same
 // codes everywhere.
 //
-// Bound by HBM: 16-bit rows in, 0.5625 bytes an element out (in and out
-// exchanged when reading back).
+// Bound by HBM: 16-bit rows in, 0.5625 bytes an element out (in and out exchanged when
+// reading back).  The append issues in 62 % of the cycles, on finding the groups' ends,
+// quotients that round as a division does and the angles: 7357 tokens of 32 + 8 + 8
+// heads, d = 128, bf16, 159 MB: 42.3 us, 3.8 TB/s.  Reading 32768 keys of 8 heads, 172 MB: 29 us,
+// 5.9 TB/s (a warp a record with all its loads first; element by element 44).
 #include "fa_paged4.h"
 #include "fa_rotary.cuh"
 #include "sm103a.cuh"
@@ -102,6 +105,43 @@ __device__ __forceinline__ void encode8(const uint4& v, const Step& g, uint8_t* 
   }
 }
 
+// A difference in a 16-bit value's last place may move a code by a whole step.  So K's
+// rows are formed as a program of plain fp32 operations would: the squares of the
+// elements that are 32 columns apart summed first, then neighbours, and the turn
+// without fused products, by angles within 2^-30 (7.5 million values of K of 7357
+// prompt tokens, against the plain form in fp32: formed as in the norm's kernel 2.5
+// codes a call differed, so none in twelve calls; 40.5 -> 42.3 us).
+// Of a row whose lane c has the elements 8 c .. 8 c + 7 and D / 2 more:
+template <int D>
+__device__ __forceinline__ float plain_sum_of_squares(const float (&a)[8], const float (&b)[8], int c) {
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float p = __fmul_rn(a[i], a[i]), q = __fmul_rn(b[i], b[i]);
+    if constexpr (D == 128) {
+      // (b's are 64 columns further, the lane's four off 32.)
+      const float po = __shfl_xor_sync(0xffffffffu, p, 4), qo = __shfl_xor_sync(0xffffffffu, q, 4);
+      s[i] = __fadd_rn(__fadd_rn(__fadd_rn(c < 4 ? p : po, c < 4 ? po : p), c < 4 ? q : qo), c < 4 ? qo : q);
+    } else {
+      s[i] = __fadd_rn(p, q);
+    }
+  }
+  const float r = __fadd_rn(__fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])),
+                            __fadd_rn(__fadd_rn(s[4], s[5]), __fadd_rn(s[6], s[7])));
+  return sum_over(r, 4);
+}
+template <bool kInter>
+__device__ __forceinline__ void plain_turn8(float (&a)[8], float (&b)[8], const float (&cs)[8], const float (&sn)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float& x = kInter ? (i < 4 ? a[2 * i] : b[2 * i - 8]) : a[i];
+    float& y = kInter ? (i < 4 ? a[2 * i + 1] : b[2 * i - 7]) : b[i];
+    const float t = __fsub_rn(__fmul_rn(x, cs[i]), __fmul_rn(y, sn[i]));
+    y = __fadd_rn(__fmul_rn(y, cs[i]), __fmul_rn(x, sn[i]));
+    x = t;
+  }
+}
+
 // One row of K or V, two vectors a thread, into its record: codes to the addresses of
 // the vectors, (s, z) to par.  All lanes of a row take part.  own: a thread's vectors
 // are of the group of its four lanes.
@@ -155,8 +195,12 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
   wait_for_previous();
   const int lt = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
   const long long t = (long long)blockIdx.x * kTokens + lt;
-  const Chunk ck = chunk_of<kInter>(c, a.r.rot);
-  const Chunk plain{16 * c, 16 * c + 8, false};
+  // What is not turned: both vectors of one group, and neighbouring lanes' next to one
+  // another (with a lane's own two so, 7357 tokens took 1.5 us more); but halves of a row
+  // in a lane for plain_sum_of_squares.
+  const Chunk plain{64 * (c >> 2) + 8 * (c & 3), 64 * (c >> 2) + 8 * (c & 3) + 32, false};
+  const bool halves = !kInter && (a.r.rot == D || (a.r.rot == 0 && a.n.on));
+  const Chunk ck = a.r.rot ? chunk_of<kInter>(c, a.r.rot) : halves ? Chunk{8 * c, D / 2 + 8 * c, false} : plain;
   const int Hkv = a.kv.Hkv, h0 = (gridDim.y - 1 - blockIdx.y) * hpb, h1 = min(h0 + hpb, a.Hq + 2 * Hkv);
   auto copy = [&](int h, int slot) {
     if (t < a.T && h < h1) {
@@ -177,9 +221,12 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
   int page = 0, place = 0;
   const bool live = t < a.T && place_token(a, (int)t, st, page, place);
   float cs[8] = {}, sn[8] = {};
-  if (live && ck.turned && h0 < a.Hq + Hkv) load_fine_angles(a.r, pairs, a.r.pos + t, c, cs, sn);
+  if (live && ck.turned && h0 < a.Hq + Hkv) {
+    if (h1 > a.Hq) load_fine_angles(a.r, pairs, a.r.pos + t, c, cs, sn);          // K's rows
+    else load_angles(a.r, pairs, a.r.pos + t, c, cs, sn);
+  }
   // K's vectors: halves of the turned elements, or neighbours.
-  const bool own = D == 64 || kInter || a.r.rot == 0 || a.r.rot == 64;
+  const bool own = D == 64 || kInter || (a.r.rot == 0 && !halves) || a.r.rot == 64;
   uint8_t* at = static_cast<uint8_t*>(a.kv.k) + page * a.kv.s_page + (place >> 4) * (long long)R::kBytes;
   place &= 15;
   int slot = 0, h = h0;
@@ -212,14 +259,16 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
         up8<T>(va, xa);
         up8<T>(vb, xb);
         if (normed) {
-          const float r = rsqrtf(sum_over(sum_of_squares(xa, xb), kLanes) * (1.f / D) + a.n.eps);
+          const float s = part == 1 && halves ? plain_sum_of_squares<D>(xa, xb, c) : sum_over(sum_of_squares(xa, xb), kLanes);
+          const float r = rsqrtf(s * (1.f / D) + a.n.eps);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             xa[i] = xa[i] * r * wa[i];
             xb[i] = xb[i] * r * wb[i];
           }
         }
-        if (my.turned) turn8<kInter>(xa, xb, cs, sn);
+        if (my.turned && part == 1) plain_turn8<kInter>(xa, xb, cs, sn);
+        else if (my.turned) turn8<kInter>(xa, xb, cs, sn);
         va = down8<T>(xa);
         vb = down8<T>(xb);
       }
