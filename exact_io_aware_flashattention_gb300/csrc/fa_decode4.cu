@@ -46,10 +46,11 @@
 // nor rescales.
 //
 // Bound by issue: 308 instructions a slice of d = 128, 64 of them masks, 16 byte swaps
-// and 18 products, in 64 % of the cycles; the integer pipe is busy 54 %, tensor 28 %.  16 sequences of 32768 keys, 8 kv heads of 4
-// heads (604 MB): 113 us, 5.3 TB/s; the copies alone take 98 us, the work alone as long as
-// both.  16 heads a group (two column tiles, one CTA an SM with 255 registers a thread)
-// take 177 us; as two units of eight heads they would take twice 114.
+// and 18 products, in 64 % of the cycles; the integer pipe is busy 54 %, the tensor pipe
+// 28 %.  16 sequences of 32768 keys, 8 kv heads of 4 heads (604 MB): 113 us, 5.3 TB/s; the
+// copies alone take 98 us, the work alone as long as both.  16 heads a group (two column
+// tiles, one CTA an SM with 255 registers a thread) take 177 us; as two units of eight
+// heads they would take twice 114.
 #include "fa_decode.cuh"
 #include "fa_paged4.h"
 #include "fa_rotary.cuh"
