@@ -11,7 +11,7 @@
 // Bound by HBM: 16-bit rows in, 0.5625 bytes an element out (in and out exchanged when
 // reading back).  The append issues in 64 % of the cycles, on finding the groups' ends,
 // quotients that round as a division does and the angles: 7357 tokens of 32 + 8 + 8
-// heads, d = 128, bf16, 159 MB: 42.3 us, 3.8 TB/s.  Reading 32768 keys of 8 heads, 172 MB: 29 us,
+// heads, d = 128, bf16, 159 MB: 42.0 us, 3.8 TB/s.  Reading 32768 keys of 8 heads, 172 MB: 29 us,
 // 5.9 TB/s (a warp a record with all its loads first; element by element 44).
 #include "fa_paged4.h"
 #include "fa_rotary.cuh"
@@ -92,7 +92,12 @@ __device__ __forceinline__ void encode8(const uint4& v, const Step& g, uint8_t* 
   up8<T>(v, x);
   if (g.plain) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = quotient(__fsub_rn(x[e], g.z), g.s, g.inv);
+    for (int e = 0; e < 8; e += 2) {               // as quotient, two at a time
+      const float2 y = add2(make_float2(x[e], x[e + 1]), two(-g.z)), q = mul2(y, two(g.inv));
+      const float2 c = fma2(fma2(q, two(-g.s), y), two(g.inv), q);
+      x[e] = c.x;
+      x[e + 1] = c.y;
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = g.s > 0.f ? fminf(__fdiv_rn(__fsub_rn(x[e], g.z), g.s), 15.f) : 0.f;
@@ -261,11 +266,8 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
         if (normed) {
           const float s = part == 1 && halves ? plain_sum_of_squares<D>(xa, xb, c) : sum_over(sum_of_squares(xa, xb), kLanes);
           const float r = rsqrtf(s * (1.f / D) + a.n.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            xa[i] = xa[i] * r * wa[i];
-            xb[i] = xb[i] * r * wb[i];
-          }
+          scale8(xa, r, wa);
+          scale8(xb, r, wb);
         }
         if (my.turned && part == 1) plain_turn8<kInter>(xa, xb, cs, sn);
         else if (my.turned) turn8<kInter>(xa, xb, cs, sn);

@@ -11,12 +11,12 @@
 // reads dy and x and writes dx.  A thread owns one token and eight pairs (two
 // 16-byte vectors of a row), as in fa_rope.cu; the row's sums go over its
 // lanes, d / 16 rounded up to a power of two.  Vectors are copied to shared memory
-// three rows ahead (four in the gradient, 32 KB a block, three blocks an SM at 157
+// three rows ahead (four in the gradient, 32 KB a block, three blocks an SM at 152
 // registers), since loads into registers kept too few bytes on their way: the
-// forward 31.2 -> 24.9 us, the gradient 210 -> 87.  4 x 2048 tokens of 32 heads, d = 128, bf16,
-// 134 MB: 23.6 us, 5.7 TB/s; the gradient of 2 x 8192 tokens of 40 heads, 503 MB, 85.7 us,
-// 5.9 TB/s.  Small calls are the latency of a load, the angles and a store, 3.3 us (8 + 2
-// heads of 513 tokens, d = 64), and of the gradient's second kernel, 6.2.
+// forward 31.2 -> 24.9 us, the gradient 210 -> 87.  4 x 2048 tokens of 32 heads, d = 128,
+// bf16, 134 MB: 23.6 us, 5.7 TB/s; the gradient of 2 x 8192 tokens of 40 heads, 503 MB,
+// 84.7 us, 5.9 TB/s.  Small calls are the latency of a load, the angles and a store, 3.3 us
+// (8 + 2 heads of 513 tokens, d = 64), and of the gradient's second kernel, 6.2.
 #include "fa_paged4.h"
 #include "fa_rotary.cuh"
 #include "sm103a.cuh"
@@ -53,7 +53,7 @@ constexpr int kBwdBlocks = 3;                      // of the backward kernel an 
 // grid: x over groups of tpb tokens, y over groups of hpb heads of q and then k.
 // The first rows are on their way while the angles are formed.
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(kThreads, 5) fa_qk_norm_kernel(const NormRopeArgs a, int hpb, const DevStatus st) {
+__global__ void __launch_bounds__(kThreads, 7) fa_qk_norm_kernel(const NormRopeArgs a, int hpb, const DevStatus st) {
   __shared__ Pairs pairs;
   __shared__ uint4 ring[kSlots][2][kThreads];
   launch_dependents();
@@ -105,11 +105,8 @@ __global__ void __launch_bounds__(kThreads, 5) fa_qk_norm_kernel(const NormRopeA
       const float r = rsqrtf(sum_over(sum_of_squares(xa, xb), ln.per_row) * inv_d + a.n.eps);
       copy(h + kSlots, slot);
       slot = slot + 1 == kSlots ? 0 : slot + 1;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        xa[i] = xa[i] * r * wa[i];
-        xb[i] = xb[i] * r * wb[i];
-      }
+      scale8(xa, r, wa);
+      scale8(xb, r, wb);
       if (ck.turned) turn8<kInter>(xa, xb, cs, sn);
       if (live) {
         __stcs(reinterpret_cast<uint4*>(y + ck.e0), down8<T>(xa));
@@ -269,11 +266,11 @@ __global__ void __launch_bounds__(kThreads) fa_qk_norm_dw_kernel(const NormRopeB
   if (lane == 0) a.dw[part][i] = s;
 }
 
-// Heads per block of the forward, which share their angles: two waves of blocks, five
-// an SM, but 11 heads at most, so that large calls end evenly; and a head a block only
-// where that is no more than a wave.  us by 10 | 16 blocks an SM: 4 x 2048
-// tokens of 32 heads 23.6 | 24.2, 2048 of 40 heads 11.3 | 12.9; 16384 of 32 heads with 16 |
-// 11 heads a block 48.0 | 45.3; 512 of 40 heads with one | two 7.9 | 5.5.
+// Heads per block of the forward, which share their angles: ten blocks an SM, of which
+// seven run at a time, but 11 heads at most, so that large calls end evenly; and a head
+// a block only where that is no more than five an SM.  us by 10 | 16 blocks an SM: 4 x
+// 2048 tokens of 32 heads 23.6 | 24.2, 2048 of 40 heads 11.3 | 12.9; 16384 of 32 heads with
+// 16 | 11 heads a block 48.0 | 45.3; 512 of 40 heads with one | two 7.9 | 5.5.
 int heads_per_block(long long token_blocks, int heads, int num_sms) {
   const long long want = 10LL * num_sms;
   const long long splits = std::min<long long>(std::max<long long>((want + token_blocks - 1) / token_blocks, (heads + 10) / 11), heads);

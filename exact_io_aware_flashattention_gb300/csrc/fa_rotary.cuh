@@ -142,15 +142,51 @@ __device__ __forceinline__ uint4 down8(const float (&x)[8]) {
   return make_uint4(Pair2<T>::down(x[0], x[1]), Pair2<T>::down(x[2], x[3]), Pair2<T>::down(x[4], x[5]),
                     Pair2<T>::down(x[6], x[7]));
 }
+// Two fp32 operations in one instruction, each rounded as its own.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 y;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(y))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(y))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(y))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return y;
+}
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+
 template <bool kInter>
 __device__ __forceinline__ void turn8(float (&a)[8], float (&b)[8], const float (&cs)[8], const float (&sn)[8]) {
+  if constexpr (kInter) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float& x = kInter ? (i < 4 ? a[2 * i] : b[2 * i - 8]) : a[i];
-    float& y = kInter ? (i < 4 ? a[2 * i + 1] : b[2 * i - 7]) : b[i];
-    const float t = x * cs[i] - y * sn[i];
-    y = y * cs[i] + x * sn[i];
-    x = t;
+    for (int i = 0; i < 8; ++i) {
+      float& x = i < 4 ? a[2 * i] : b[2 * i - 8];
+      float& y = i < 4 ? a[2 * i + 1] : b[2 * i - 7];
+      const float t = x * cs[i] - y * sn[i];
+      y = y * cs[i] + x * sn[i];
+      x = t;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float2 x = make_float2(a[i], a[i + 1]), y = make_float2(b[i], b[i + 1]);
+      const float2 c = make_float2(cs[i], cs[i + 1]), s = make_float2(sn[i], sn[i + 1]), z = mul2(y, s);
+      const float2 u = fma2(x, c, make_float2(-z.x, -z.y)), v = fma2(x, s, mul2(y, c));
+      a[i] = u.x, a[i + 1] = u.y;
+      b[i] = v.x, b[i + 1] = v.y;
+    }
   }
 }
 
@@ -172,10 +208,23 @@ __device__ __forceinline__ float sum_over(float x, int lanes) {
   return x;
 }
 __device__ __forceinline__ float sum_of_squares(const float (&a)[8], const float (&b)[8]) {
-  float s = 0.f;
+  float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s = fmaf(a[i], a[i], fmaf(b[i], b[i], s));
-  return s;
+  for (int i = 0; i < 8; i += 2) {
+    const float2 x = make_float2(a[i], a[i + 1]), y = make_float2(b[i], b[i + 1]);
+    s = fma2(x, x, fma2(y, y, s));
+  }
+  return s.x + s.y;
+}
+
+// x r w.
+__device__ __forceinline__ void scale8(float (&x)[8], float r, const float (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 y = mul2(mul2(make_float2(x[i], x[i + 1]), two(r)), make_float2(w[i], w[i + 1]));
+    x[i] = y.x;
+    x[i + 1] = y.y;
+  }
 }
 
 // Cosine and sine of phase 2^-64 turns, off by 2^-30 and rounded to fp32 (so all but a
