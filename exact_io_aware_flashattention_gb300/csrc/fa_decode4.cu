@@ -19,12 +19,10 @@
 // head's largest element to 2^10 (16 times that for the codes held as c 2^-22): exact
 // but for elements 2^-24 times smaller than that one.  The weights s p enter times a
 // power of two that brings the largest s so far to 2^6 (p is 2^8 at most), as the sum
-// of two fp16 values, off by 2^-22 of themselves or 2^-31 of that s.  Up to four heads a
-// group (kDup) the eight columns hold the heads twice, and the second four the weights'
-// low parts, which costs no product; above that fp16 has two products.  bf16, whose own
-// rounding is 2^4 times coarser than a high part's, has the high parts alone, off by
-// 2^-11 at most: o is 1.01 times as far off (1.667e-3 against 1.649e-3, relative l2 at
-// 32768 keys), and the low parts cost 6 % in columns and 19 % in products.
+// of two fp16 values, off by 2^-22 of themselves or 2^-31 of that s.  (The high parts
+// alone, off by 2^-11, would show in o where values of opposite signs cancel.)  Up to
+// four heads a group (kDup) the eight columns hold the heads twice, and the second four
+// the weights' low parts, which costs no product; above that there are two products.
 //
 // The line of tiles, its cut into equal parts, one a CTA, and their joins are those of
 // the 16-bit kernel (fa_decode.cuh, fa_paged.cu).  A unit's end counts as two tiles
@@ -116,7 +114,6 @@ template <typename T>
 struct Type;
 template <>
 struct Type<__nv_bfloat16> {
-  static constexpr int kWeights = 1;              // fp16 values a weight is the sum of
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return cvt_bf16x2(lo, hi); }
   static __device__ __forceinline__ float2 up(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -124,7 +121,6 @@ struct Type<__nv_bfloat16> {
 };
 template <>
 struct Type<__half> {
-  static constexpr int kWeights = 2;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -283,7 +279,7 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
                                      uint32_t vp_at, int ka, const float (&by)[NT][2], const uint2* q,
                                      const float (&qs)[NT][D / 64][2], float (&o)[NT][D / 16][4], float (&zs)[NT][D / 64][2],
                                      float (&m)[NT][2], float (&l)[NT][2], float (&grow)[D / 64]) {
-  constexpr int kG = D / 64, kW = kDup ? 1 : Type<T>::kWeights, kStep = Record<D>::kBytes;
+  constexpr int kG = D / 64, kW = kDup ? 1 : 2, kStep = Record<D>::kBytes;
   // Scores, in units of log2 / by: S^T rows ka, ka + 8, columns 2 qc, 2 qc + 1.
   float x[kSl][NT][4];
   {
@@ -441,7 +437,7 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
   // Values, group by group.
 #pragma unroll
   for (int k = 0; k < kG; ++k) {
-    uint32_t p[kSl][NT][kW][2];          // P^T: [high, low][keys 0-7, 8-15 of the fragment]
+    uint32_t p[kSl][NT][kW][2];          // P^T: [high, low (kDup: in other columns)][keys 0-7, 8-15 of the fragment]
     uint32_t v[kSl][4];
 #pragma unroll
     for (int j = 0; j < kSl; ++j) {
@@ -456,14 +452,10 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
         for (int e = 0; e < 2; ++e) {
           const float w0 = x[j][n][2 * e] * (e ? sb : sa), w1 = x[j][n][2 * e + 1] * (e ? sb : sa);
           const uint32_t high = Half::pack(w0, w1);
-          if constexpr (kDup || kW == 2) {
-            const float2 h = Half::up(high);
-            const uint32_t low = Half::pack(w0 - h.x, w1 - h.y);
-            p[j][n][0][e] = transpose8(kDup && (threadIdx.x & 2) ? low : high);
-            if constexpr (kW == 2) p[j][n][1][e] = transpose8(low);
-          } else {
-            p[j][n][0][e] = transpose8(high);
-          }
+          const float2 h = Half::up(high);
+          const uint32_t low = Half::pack(w0 - h.x, w1 - h.y);
+          p[j][n][0][e] = transpose8(kDup && (threadIdx.x & 2) ? low : high);
+          if constexpr (!kDup) p[j][n][1][e] = transpose8(low);
         }
       }
       const uint4 y = *reinterpret_cast<const uint4*>(rec + j * kStep + v_at + k * 512);
@@ -934,8 +926,7 @@ cudaError_t launch_shape(const DecodeArgs& a, const DevStatus& st, int parts, cu
 template <typename T, int D>
 cudaError_t launch(const DecodeArgs& a, const DevStatus& st, int parts, cudaStream_t stream) {
   if (a.unit_heads == 16) return launch_shape<T, D, 2, false>(a, st, parts, stream);
-  if constexpr (Type<T>::kWeights == 2)
-    if (a.Hq / a.kv.Hkv <= 4) return launch_shape<T, D, 1, true>(a, st, parts, stream);
+  if (a.Hq / a.kv.Hkv <= 4) return launch_shape<T, D, 1, true>(a, st, parts, stream);
   return launch_shape<T, D, 1, false>(a, st, parts, stream);
 }
 
@@ -947,8 +938,7 @@ cudaError_t configure_shape() {
 template <typename T, int D>
 cudaError_t configure() {
   cudaError_t e = configure_shape<T, D, 1, false>();
-  if constexpr (Type<T>::kWeights == 2)
-    if (e == cudaSuccess) e = configure_shape<T, D, 1, true>();
+  if (e == cudaSuccess) e = configure_shape<T, D, 1, true>();
   if (e == cudaSuccess) e = configure_shape<T, D, 2, false>();
   if (e == cudaSuccess) e = preload_kernel(fa_decode4_join_kernel<T, D>);
   return e;

@@ -1,0 +1,53 @@
+"""Where the 4-bit cache's calls and the normed rows could lose a last place or
+a range (GPU).  Tolerances as in test_paged4_gpu (u = half a step of the
+tensors' type), but for what a test states itself.
+"""
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_flashattention_gb300 as fa
+from oracle import paged4
+from tests.test_paged4_gpu import BF, DEV, HF, TINY, U, f64, filled, ok, rounder
+
+pytestmark = pytest.mark.gpu
+
+
+def widened(table, wide):
+    """The same table, or with as many columns more as make the parts equal instead of clusters."""
+    if not wide:
+        return table
+    t = torch.full((table.shape[0], 4000), 2 ** 30, dtype=torch.int32, device=DEV)
+    t[:, :table.shape[1]] = table
+    return t
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 1), (8, 2), (6, 1), (16, 2), (32, 2), (20, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_weights_whose_products_cancel(cuda_lib, dt, d, Hq, Hkv, wide):
+    # Two keys of opposite values and nearly equal weights, 1 and exp(-delta): o is their difference, and a weight rounded
+    # to 11 bits would show in it.  Rows of one value are held exactly (s = 0), odd numbers -15 .. 15 too (s = 2).
+    # K is 0 and -kappa, q one value t a head, so a score is off by its own roundings, X (d + 8) 2^-23 with X = delta; its
+    # exponential by 2^-21 (a factor 2); a weight by 2^-22; the sums of two keys' products, of codes from 0 and their start,
+    # by 16 2^-23: all relative to A = sum p (|z| + 32 s).
+    B, kappa = 8, 2.0 ** -12
+    k = torch.zeros((2 * B, Hkv, d))
+    k[1::2] = -kappa
+    g = torch.Generator().manual_seed(Hq * d)
+    v = torch.randint(0, 16, (B, Hkv, d), generator=g).float() * 2 - 15
+    v[..., 0::64], v[..., 1::64] = -15.0, 15.0
+    v = torch.stack([v, -v], dim=1).reshape(2 * B, Hkv, d)
+    q = (1 + torch.randint(0, 64, (B, Hq, 1), generator=g) / 64).expand(B, Hq, d)
+    k, v, q = (t.to(dt).to(DEV).contiguous() for t in (k, v, q))
+    cache, table, ln, _, _ = filled([2] * B, Hkv, 16, d, dt, seed=7, rows=[k, v])
+    o, _ = fa.paged4_decode(q, cache, widened(table, wide), ln)
+    ok()
+    for b in range(B):
+        kb, vb = (f64(t)[2 * b:2 * b + 2].swapaxes(0, 1) for t in (k, v))
+        want, _, x, a = paged4.decode(f64(q)[b], kb, vb, d ** -0.5, 0, rounder(dt))
+        e = (x * (d + 8) * 2.0 ** -23 + 2.0 ** -21)[:, None]
+        bound = U[dt] * np.abs(want) + (2.1 * e + 2.0 ** -22 + 16 * 2.0 ** -23) * a + TINY[dt]
+        err = np.abs(f64(o)[b] - want)
+        assert (err <= bound).all(), f"sequence {b}: {(err > bound).sum()} values, {(err / bound).max()} of the bound"
