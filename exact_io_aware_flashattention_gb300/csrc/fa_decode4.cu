@@ -822,13 +822,14 @@ __global__ void __launch_bounds__(32 * W, NT == 1 && W <= 8 ? 2 : 1) fa_decode4_
         float* to = reinterpret_cast<float*>(stash + warp * C::kRing) + qc * 2 * D;
 #pragma unroll
         for (int k = 0; k < kG; ++k) {
-          const float u0 = 0x1p18f / grow[k], u1 = 0x1p22f / grow[k];        // codes are c 2^-18 or c 2^-22, weights s p grow
+          // Codes are c 2^-18 or c 2^-22, weights s p grow; 2^22 / grow may be past fp32's range, s up to 2^124.
+          const float back = 1.f / grow[k];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float z = kDup && qc >= 2 ? 0.f : zs[n][k][e & 1], s = f[e & 1];
             *reinterpret_cast<float4*>(to + (e & 1) * D + k * 64 + ((qr * 8 + (e >> 1) * 4) ^ (qc * 4))) =
-                make_float4(fmaf(o[n][4 * k][e], u0, z) * s, fmaf(o[n][4 * k + 1][e], u1, z) * s,
-                            fmaf(o[n][4 * k + 2][e], u0, z) * s, fmaf(o[n][4 * k + 3][e], u1, z) * s);
+                make_float4(fmaf(o[n][4 * k][e] * 0x1p18f, back, z) * s, fmaf(o[n][4 * k + 1][e] * 0x1p22f, back, z) * s,
+                            fmaf(o[n][4 * k + 2][e] * 0x1p18f, back, z) * s, fmaf(o[n][4 * k + 3][e] * 0x1p22f, back, z) * s);
           }
         }
         __syncthreads();

@@ -507,7 +507,9 @@ fa_status fa_paged4_read(const fa_paged4_kv* kv, const fa_page_table* table, con
 /*
  * fa_paged_decode over the 4-bit cache (without scores): q, o and lse as there;
  * scores, softmax and sums are fp32.  The products with V take the weights
- * times a key's step s to 22 bits.  workspace: at least
+ * times a key's step s to 22 bits.  What is summed is divided by the weights'
+ * sum at the end, so over n visible keys o may be infinite or NaN where |v| is
+ * 2^120 / n or more, and where |q| or |q| scale is 2^118 or more.  workspace: at least
  * fa_paged4_decode_workspace_bytes(...), contents don't matter; calls that may
  * run at the same time need one each.  O and LSE are bitwise reproducible.  One
  * or two launches.

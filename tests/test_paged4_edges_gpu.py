@@ -8,7 +8,7 @@ import torch
 
 import exact_io_aware_flashattention_gb300 as fa
 from oracle import paged4
-from tests.test_paged4_gpu import BF, DEV, HF, TINY, U, f64, filled, ok, rounder
+from tests.test_paged4_gpu import BF, DEV, HF, TINY, U, assert_decoded, f64, filled, ok, rounder
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,20 @@ def test_weights_whose_products_cancel(cuda_lib, dt, d, Hq, Hkv, wide):
         bound = U[dt] * np.abs(want) + (2.1 * e + 2.0 ** -22 + 16 * 2.0 ** -23) * a + TINY[dt]
         err = np.abs(f64(o)[b] - want)
         assert (err <= bound).all(), f"sequence {b}: {(err > bound).sum()} values, {(err / bound).max()} of the bound"
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("Hq,d", [(4, 64), (4, 128), (8, 128), (16, 64), (32, 128)])
+@pytest.mark.parametrize("top", [100, 111, 114, 118])
+def test_values_near_the_top_of_the_range(cuda_lib, top, Hq, d, wide):
+    # Steps of V up to 2^117: at a unit's end the sums of codes go back to units of V by way of factors past fp32's range.
+    lens = [12, 1, 30]
+    g = torch.Generator().manual_seed(top)
+    k = torch.randn((sum(lens), 2, d), generator=g).to(BF).to(DEV)
+    v = (torch.randn((sum(lens), 2, d), generator=g) * 2.0 ** top).to(BF).to(DEV)
+    cache, table, ln, _, _ = filled(lens, 2, 16, d, BF, seed=8, rows=[k, v])
+    q = torch.randn((3, Hq, d), generator=g).to(BF).to(DEV)
+    o, lse = fa.paged4_decode(q, cache, widened(table, wide), ln)
+    ok()
+    assert o.isfinite().all()
+    assert_decoded(o, lse, q, k, v, lens, d ** -0.5, 0, f"values of 2^{top}")
