@@ -259,7 +259,8 @@ __device__ __forceinline__ void store_q(const QRows<D, NT>& q, float scale_log2,
         x[32] = make_uint2(Half::pack(y2.x * times, y2.y * times), Half::pack(y3.x * more, y3.y * more));
       }
     }
-    if ((lane & 3) == 0) sums[NT * (D / 64) * 8 + n * 8 + (lane >> 2)] = scale_log2 * 0x1p18f / times;
+    // (Not 0, which times a masked score's -inf is NaN; scores of so small factors are 0 all the same.)
+    if ((lane & 3) == 0) sums[NT * (D / 64) * 8 + n * 8 + (lane >> 2)] = fmaxf(scale_log2 * 0x1p18f / times, 0x1p-126f);
   }
 }
 

@@ -68,3 +68,17 @@ def test_values_near_the_top_of_the_range(cuda_lib, top, Hq, d, wide):
     ok()
     assert o.isfinite().all()
     assert_decoded(o, lse, q, k, v, lens, d ** -0.5, 0, f"values of 2^{top}")
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("Hq", [4, 16, 32])
+@pytest.mark.parametrize("scale", [1e-20, 1e-30, 0.125])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_queries_of_zero_and_tiny_scales(cuda_lib, dt, scale, Hq, wide):
+    # Weights all alike, beside keys that are masked: o is the mean of the values.
+    lens = [70, 1, 33]
+    cache, table, ln, k, v = filled(lens, 2, 16, 64, dt, seed=10)
+    q = torch.zeros((3, Hq, 64), dtype=dt, device=DEV)
+    o, lse = fa.paged4_decode(q, cache, widened(table, wide), ln, scale=scale)
+    ok()
+    assert_decoded(o, lse, q, k, v, lens, scale, 0)
