@@ -507,7 +507,10 @@ fa_status fa_paged4_read(const fa_paged4_kv* kv, const fa_page_table* table, con
 /*
  * fa_paged_decode over the 4-bit cache (without scores): q, o and lse as there;
  * scores, softmax and sums are fp32.  The products with V take the weights
- * times a key's step s to 22 bits.  What is summed is divided by the weights'
+ * times a key's step s as the sum of two fp16 values: off by 2^-22 of
+ * themselves, or by 2^-31 of the largest step that this group of 64 elements has
+ * in a visible key, whatever that key's weight (products below 2^-9 of that step have
+ * fewer than 22 bits).  What is summed is divided by the weights'
  * sum at the end, so over n visible keys o may be infinite or NaN where |v| is
  * 2^120 / n or more, and where |q| or |q| scale is 2^118 or more.  workspace: at least
  * fa_paged4_decode_workspace_bytes(...), contents don't matter; calls that may

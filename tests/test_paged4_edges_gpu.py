@@ -2,6 +2,8 @@
 a range (GPU).  Tolerances as in test_paged4_gpu (u = half a step of the
 tensors' type), but for what a test states itself.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -82,3 +84,47 @@ def test_queries_of_zero_and_tiny_scales(cuda_lib, dt, scale, Hq, wide):
     o, lse = fa.paged4_decode(q, cache, widened(table, wide), ln, scale=scale)
     ok()
     assert_decoded(o, lse, q, k, v, lens, scale, 0)
+
+
+def outlier(dt, d, Hq, Hkv, n, at, times, seed):
+    """A sequence whose key `at` nobody attends to (its score is 200 below the others') and whose value is `times` larger."""
+    g = torch.Generator().manual_seed(seed)
+    u = torch.randint(0, 2, (d,), generator=g).float() * 2 - 1
+    k = 0.01 * torch.randn((n, Hkv, d), generator=g)
+    v = torch.randn((n, Hkv, d), generator=g)
+    k[at] = -200.0 / math.sqrt(d) * u
+    v[at] *= times
+    q = u + 0.1 * torch.randn((1, Hq, d), generator=g)
+    return [t.to(dt).to(DEV) for t in (q, k, v)]
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("Hq", [4, 16, 32])
+@pytest.mark.parametrize("dt,times", [(BF, 2.0 ** 8), (BF, 2.0 ** 14), (BF, 2.0 ** 22), (BF, 2.0 ** 115), (HF, 2.0 ** 8), (HF, 2.0 ** 13)])
+@pytest.mark.parametrize("at", [0, 70])
+def test_a_key_of_large_steps_that_nobody_attends_to(cuda_lib, at, dt, times, Hq, wide):
+    # Weights times steps are held to 2^-22 of themselves or 2^-31 S, S the largest visible step: those of the other keys
+    # lose that much and no more, min(p s, 2^-31 S) each, times 7.5 at most.
+    d, n, Hkv = 128, 100, 2
+    q, k, v = outlier(dt, d, Hq, Hkv, n, at, times, seed=int(math.log2(times)) + at)
+    cache, table, ln, _, _ = filled([n], Hkv, 16, d, dt, seed=9, rows=[k, v])
+    o, lse = fa.paged4_decode(q, cache, widened(table, wide), ln)
+    ok()
+    r = rounder(dt)
+    kn, vn = (f64(t).swapaxes(0, 1) for t in (k, v))
+    want, _, _, a = paged4.decode(f64(q)[0], kn, vn, d ** -0.5, 0, r)
+    others = np.delete(kn, at, axis=1)
+    x = paged4.decode(f64(q)[0], others, others, d ** -0.5, 0, r)[2]    # the bound of their scores
+    s = np.repeat(paged4.quantise(vn, r)[1], 64, -1)                   # [Hkv, n, d]
+    kv, G = paged4.values(kn, r), Hq // Hkv
+    e = (x * (d + 8) * 2.0 ** -23 + 2.0 ** -21 + n * 2.0 ** -24)[:, None]
+    lost = np.zeros_like(want)
+    for h in range(Hq):
+        y = d ** -0.5 * (kv[h // G] @ f64(q)[0, h])
+        p = np.exp(y - y.max())
+        p /= p.sum()
+        lost[h] = 7.5 * np.minimum(p[:, None] * s[h // G], 2.0 ** -31 * s[h // G].max(0)).sum(0)
+    bound = U[dt] * np.abs(want) + (2.1 * e + 2.0 ** -22 * 7.5 / 32 + (d + n) * 2.0 ** -23) * a + lost + TINY[dt]
+    err = np.abs(f64(o)[0] - want)
+    assert (err <= bound).all(), f"{(err > bound).sum()} values, {(err / np.maximum(bound, 1e-30)).max()} of the bound"
+    assert lse.isfinite().all()
