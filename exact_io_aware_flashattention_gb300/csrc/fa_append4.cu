@@ -226,10 +226,6 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
   int page = 0, place = 0;
   const bool live = t < a.T && place_token(a, (int)t, st, page, place);
   float cs[8] = {}, sn[8] = {};
-  if (live && ck.turned && h0 < a.Hq + Hkv) {
-    if (h1 > a.Hq) load_fine_angles(a.r, pairs, a.r.pos + t, c, cs, sn);          // K's rows
-    else load_angles(a.r, pairs, a.r.pos + t, c, cs, sn);
-  }
   // K's vectors: halves of the turned elements, or neighbours.
   const bool own = D == 64 || kInter || (a.r.rot == 0 && !halves) || a.r.rot == 64;
   uint8_t* at = static_cast<uint8_t*>(a.kv.k) + page * a.kv.s_page + (place >> 4) * (long long)R::kBytes;
@@ -241,6 +237,11 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
     if (h >= end) continue;
     const Chunk my = part == 2 ? plain : ck;
     const bool normed = a.n.on && part < 2;
+    // Each part's own, so that rows don't depend on the heads and tokens of their block.
+    if (part < 2 && live && ck.turned) {
+      if (part) load_fine_angles(a.r, pairs, a.r.pos + t, c, cs, sn);
+      else load_angles(a.r, pairs, a.r.pos + t, c, cs, sn);
+    }
     float wa[8] = {}, wb[8] = {};
     if (normed) {
       load_weights<T>(part ? a.n.wk : a.n.wq, a.n.fp32, my.e0, wa);

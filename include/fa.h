@@ -486,7 +486,7 @@ typedef struct fa_paged4_kv {
  * fa_paged_append into the 4-bit cache.  With norm (may be NULL) q and k are
  * normed, with rotary (may be NULL) turned after that, and rounded to dtype; k
  * and v are then stored.  q needs norm or rotary (FA_ERR_BAD_ARGUMENT without).
- * One launch.
+ * A token's bits are the same whatever else the call appends.  One launch.
  */
 fa_status fa_paged4_append(const fa_paged4_kv* kv, const fa_page_table* table, const int* seq_lens, const int* cu_seqlens,
                            int B, int T, const void* k, const long long* k_strides, const void* v,

@@ -10,7 +10,8 @@ import torch
 
 import exact_io_aware_flashattention_gb300 as fa
 from oracle import paged4
-from tests.test_paged4_gpu import BF, DEV, HF, TINY, U, assert_decoded, f64, filled, ok, rounder
+from tests.test_paged4_gpu import (BF, DEV, F32, HF, TINY, U, assert_decoded, f64, filled, new_cache, offsets, ok, rounder,
+                                   tables, turned, weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +129,33 @@ def test_a_key_of_large_steps_that_nobody_attends_to(cuda_lib, at, dt, times, Hq
     err = np.abs(f64(o)[0] - want)
     assert (err <= bound).all(), f"{(err > bound).sum()} values, {(err / np.maximum(bound, 1e-30)).max()} of the bound"
     assert lse.isfinite().all()
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("Hq,Hkv,d,sections,interleaved", [(8, 2, 128, (64,), False), (12, 4, 64, (32,), False), (8, 1, 128, (16, 16), False),
+                                                           (16, 8, 128, (64,), True), (5, 5, 64, None, False)])
+def test_rows_do_not_depend_on_how_many_are_appended_with_them(cuda_lib, Hq, Hkv, d, sections, interleaved, dt):
+    # One token a call, a few, and all in one: q and the pool's bytes are the same.
+    n = 6000
+    g = torch.Generator().manual_seed(d + Hq)
+    q, k, v = torch.randn((n, Hq + 2 * Hkv, d), generator=g).to(dt).to(DEV).split([Hq, Hkv, Hkv], dim=1)
+    rot, kw = turned(g, sections, interleaved, 100, 1, n)
+    pos = None if rot is None else rot[0][:, 0]
+    norm = dict(q_weight=weights(g, d, F32), k_weight=weights(g, d, F32), eps=1e-6)
+    total, table, ln = tables([n], 16, seed=12)
+    whole, parts = new_cache(total, Hkv, 16, d, fill=0), new_cache(total, Hkv, 16, d, fill=0)
+
+    def append(cache, at, end):
+        ln.fill_(end)
+        turn = {} if rot is None else dict(kw, positions=pos[:, at:end])
+        return fa.paged4_append(cache, table, ln, k[at:end], v[at:end], cu_seqlens=offsets([end - at]), q=q[at:end], **norm, **turn)
+    want = append(whole, 0, n)
+    got, at = [], 0
+    for c in [1] * 40 + [3, 17, 64, 100, 400, 1500, n]:
+        end = min(at + c, n)
+        got.append(append(parts, at, end))
+        at = end
+    ok()
+    got = torch.cat(got)
+    assert torch.equal(got, want), f"{(got != want).sum().item()} values of q"
+    assert torch.equal(parts, whole)
