@@ -11,7 +11,7 @@
 // Bound by HBM: 16-bit rows in, 0.5625 bytes an element out (in and out exchanged when
 // reading back).  The append issues in 64 % of the cycles, on finding the groups' ends,
 // quotients that round as a division does and the angles: 7357 tokens of 32 + 8 + 8
-// heads, d = 128, bf16, 159 MB: 42.0 us, 3.8 TB/s.  Reading 32768 keys of 8 heads, 172 MB: 29 us,
+// heads, d = 128, bf16, 159 MB: 39.9 us, 4.0 TB/s.  Reading 32768 keys of 8 heads, 172 MB: 29 us,
 // 5.9 TB/s (a warp a record with all its loads first; element by element 44).
 #include "fa_paged4.h"
 #include "fa_rotary.cuh"
@@ -110,12 +110,15 @@ __device__ __forceinline__ void encode8(const uint4& v, const Step& g, uint8_t* 
   }
 }
 
-// A difference in a 16-bit value's last place may move a code by a whole step.  So K's
-// rows are formed as a program of plain fp32 operations would: the squares of the
-// elements that are 32 columns apart summed first, then neighbours, and the turn
-// without fused products, by angles within 2^-30 (7.5 million values of K of 7357
-// prompt tokens, against the plain form in fp32: formed as in the norm's kernel 2.5
-// codes a call differed, so none in twelve calls; 40.5 -> 42.3 us).
+// A difference in a 16-bit value's last place may move a code by a whole step, so a
+// program that forms its rows elsewhere (the prompts of a cache filled before, a check
+// against elementary operations) and this kernel should agree to that place.  K's rows
+// are therefore formed by fp32 operations that are rounded one by one, in an order that
+// is the same for every layout of the pairs: the squares of the elements that are 32
+// columns apart summed first, then neighbours; the turn without fused products, by
+// angles within 2^-30.  (7.5 million values of K of 7357 prompt tokens against such a
+// program: as in the norm's kernel 2.5 codes a call differed, so none in twelve calls;
+// 40.5 -> 42.3 us.)
 // Of a row whose lane c has the elements 8 c .. 8 c + 7 and D / 2 more:
 template <int D>
 __device__ __forceinline__ float plain_sum_of_squares(const float (&a)[8], const float (&b)[8], int c) {
@@ -145,6 +148,13 @@ __device__ __forceinline__ void plain_turn8(float (&a)[8], float (&b)[8], const 
     y = __fadd_rn(__fmul_rn(y, cs[i]), __fmul_rn(x, sn[i]));
     x = t;
   }
+}
+
+// Which lane of a row has vector v of it (8 elements), as its first or second one, where
+// the lanes have the chunks of chunk_of.
+__device__ __forceinline__ int2 place_of(int v, const RotaryArgs& r) {
+  if (r.interleaved || v >= r.rot / 8) return make_int2(v / 2, v % 2);
+  return v < r.rot / 16 ? make_int2(v, 0) : make_int2(v - r.rot / 16, 1);
 }
 
 // One row of K or V, two vectors a thread, into its record: codes to the addresses of
@@ -190,7 +200,10 @@ __device__ __forceinline__ void store_row(const uint4& va, const uint4& vb, cons
 // one token each 4.8 -> 4.3).  The first rows are on their way while the slot is looked up and
 // the angles are formed.
 constexpr int kSlots = 3;
-template <typename T, int D, bool kInter>
+// kHalves: a lane has eight neighbours of each half of a row of q and K, as
+// plain_sum_of_squares takes them (rows turned whole by halves, or normed only); an
+// instance of its own, as the other layouts' look-ups in its loop cost it 2 us of 42.
+template <typename T, int D, bool kInter, bool kHalves>
 __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Args a, int hpb, const DevStatus st) {
   using R = Record<D>;
   __shared__ Pairs pairs;
@@ -201,11 +214,9 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
   const int lt = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
   const long long t = (long long)blockIdx.x * kTokens + lt;
   // What is not turned: both vectors of one group, and neighbouring lanes' next to one
-  // another (with a lane's own two so, 7357 tokens took 1.5 us more); but halves of a row
-  // in a lane for plain_sum_of_squares.
+  // another (with a lane's own two so, 7357 tokens took 1.5 us more).
   const Chunk plain{64 * (c >> 2) + 8 * (c & 3), 64 * (c >> 2) + 8 * (c & 3) + 32, false};
-  const bool halves = !kInter && (a.r.rot == D || (a.r.rot == 0 && a.n.on));
-  const Chunk ck = a.r.rot ? chunk_of<kInter>(c, a.r.rot) : halves ? Chunk{8 * c, D / 2 + 8 * c, false} : plain;
+  const Chunk ck = kHalves ? Chunk{8 * c, D / 2 + 8 * c, a.r.rot != 0} : a.r.rot ? chunk_of<kInter>(c, a.r.rot) : plain;
   const int Hkv = a.kv.Hkv, h0 = (gridDim.y - 1 - blockIdx.y) * hpb, h1 = min(h0 + hpb, a.Hq + 2 * Hkv);
   auto copy = [&](int h, int slot) {
     if (t < a.T && h < h1) {
@@ -227,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
   const bool live = t < a.T && place_token(a, (int)t, st, page, place);
   float cs[8] = {}, sn[8] = {};
   // K's vectors: halves of the turned elements, or neighbours.
-  const bool own = D == 64 || kInter || (a.r.rot == 0 && !halves) || a.r.rot == 64;
+  const bool own = D == 64 || kInter || (!kHalves && (a.r.rot == 0 || a.r.rot == 64));
   uint8_t* at = static_cast<uint8_t*>(a.kv.k) + page * a.kv.s_page + (place >> 4) * (long long)R::kBytes;
   place &= 15;
   int slot = 0, h = h0;
@@ -252,6 +263,9 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
     uint8_t* rec = at + (h - first) * a.kv.s_head;
     const int ca = part == 1 ? R::k_word(place, my.e0 / 8) : R::v_half(place, my.e0 / 8, 0);
     const int cb = part == 1 ? R::k_word(place, my.e1 / 8) : R::v_half(place, my.e1 / 8, 0);
+    // Who has the vectors of plain_sum_of_squares.
+    const int2 pa = place_of(c, a.r), pb = place_of(kLanes + c, a.r);
+    const int row = threadIdx.x - c;
 #pragma unroll 1
     for (; h < end; ++h) {
       copies_wait<kSlots - 1>();
@@ -265,7 +279,19 @@ __global__ void __launch_bounds__(kThreads, 5) fa_append4_kernel(const Append4Ar
         up8<T>(va, xa);
         up8<T>(vb, xb);
         if (normed) {
-          const float s = part == 1 && halves ? plain_sum_of_squares<D>(xa, xb, c) : sum_over(sum_of_squares(xa, xb), kLanes);
+          float s;
+          if (part == 0) {
+            s = sum_over(sum_of_squares(xa, xb), kLanes);
+          } else if constexpr (kHalves) {
+            s = plain_sum_of_squares<D>(xa, xb, c);
+          } else {
+            float ya[8], yb[8];
+            __syncwarp();                          // every lane's copies have landed
+            up8<T>(ring[slot][pa.y][row + pa.x], ya);
+            up8<T>(ring[slot][pb.y][row + pb.x], yb);
+            s = plain_sum_of_squares<D>(ya, yb, c);
+            __syncwarp();                          // before the next copies
+          }
           const float r = rsqrtf(s * (1.f / D) + a.n.eps);
           scale8(xa, r, wa);
           scale8(xb, r, wb);
@@ -409,8 +435,11 @@ cudaError_t launch_append(const Append4Args& a, const DevStatus& st, int num_sms
   const long long blocks = ((long long)a.T + kTokens - 1) / kTokens;
   const int heads = a.Hq + 2 * a.kv.Hkv, hpb = heads_per_block(blocks, heads, num_sms);
   const dim3 grid((unsigned)blocks, (unsigned)((heads + hpb - 1) / hpb));
-  return launch_after(a.r.interleaved ? fa_append4_kernel<T, D, true> : fa_append4_kernel<T, D, false>, grid, kThreads, 0, 1,
-                      stream, a, hpb, st);
+  const bool halves = a.r.rot == D || (a.r.rot == 0 && a.n.on);
+  auto k = a.r.interleaved ? fa_append4_kernel<T, D, true, false>
+           : halves        ? fa_append4_kernel<T, D, false, true>
+                           : fa_append4_kernel<T, D, false, false>;
+  return launch_after(k, grid, kThreads, 0, 1, stream, a, hpb, st);
 }
 
 template <typename T, int D>
@@ -422,8 +451,9 @@ cudaError_t launch_read(const Read4Args& a, const DevStatus& st, cudaStream_t st
 
 template <typename T, int D>
 cudaError_t configure() {
-  cudaError_t e = preload_kernel(fa_append4_kernel<T, D, false>);
-  if (e == cudaSuccess) e = preload_kernel(fa_append4_kernel<T, D, true>);
+  cudaError_t e = preload_kernel(fa_append4_kernel<T, D, false, true>);
+  if (e == cudaSuccess) e = preload_kernel(fa_append4_kernel<T, D, false, false>);
+  if (e == cudaSuccess) e = preload_kernel(fa_append4_kernel<T, D, true, false>);
   if (e == cudaSuccess) e = preload_kernel(fa_read4_kernel<T, D>);
   return e;
 }

@@ -159,3 +159,66 @@ def test_rows_do_not_depend_on_how_many_are_appended_with_them(cuda_lib, Hq, Hkv
     got = torch.cat(got)
     assert torch.equal(got, want), f"{(got != want).sum().item()} values of q"
     assert torch.equal(parts, whole)
+
+
+def elementary_rows(x, w, eps, pos, freq, axes, interleaved):
+    """Rows x [T, H, d] normed and turned by elementary fp32 operations, each rounded as it is: squares of elements 32
+    columns apart are added first, then neighbours; angles are formed in 64 bits and their sines and cosines rounded."""
+    dt, d = x.dtype, x.shape[-1]
+    y = x.float()
+    if eps is not None:
+        p = y * y
+        s = p[..., :32] + p[..., 32:64]
+        for i in range(64, d, 32):
+            s = s + p[..., i:i + 32]
+        while s.shape[-1] > 1:
+            s = s[..., 0::2] + s[..., 1::2]
+        y = y * torch.rsqrt(s / d + eps)
+        if w is not None:
+            y = y * w.float()
+    if pos is not None:
+        rot = 2 * freq.numel()
+        angle = (pos[axes.long()].double().movedim(0, -1) * freq)[:, None]
+        c, s = angle.cos().float(), angle.sin().float()
+        a, b = (y[..., 0:rot:2], y[..., 1:rot:2]) if interleaved else (y[..., :rot // 2], y[..., rot // 2:rot])
+        u, v = a * c - b * s, b * c + a * s
+        head = torch.stack([u, v], -1).flatten(-2) if interleaved else torch.cat([u, v], -1)
+        y = torch.cat([head, y[..., rot:]], -1)
+    return y.to(dt)
+
+
+def held(x):
+    """What the cache holds for 16-bit rows x [T, H, d], in x's type."""
+    y = x.float().unflatten(-1, (-1, 64))
+    lo, hi = y.amin(-1, keepdim=True), y.amax(-1, keepdim=True)
+    s = ((hi - lo) / 15.0).to(x.dtype).float()
+    c = torch.where(s == 0, 0.0, ((y - lo) / s).round().clamp(0, 15))
+    return (lo.double() + s.double() * c.double()).float().to(x.dtype).flatten(-2)
+
+
+@pytest.mark.parametrize("d,sections,interleaved", [(128, None, False), (128, (64,), False), (128, (64,), True), (128, (32,), False),
+                                                    (128, (16, 24), False), (128, (16,), True), (64, (32,), False), (64, (32,), True),
+                                                    (64, (8, 8), False)])
+def test_rows_of_k_are_those_of_elementary_operations(cuda_lib, d, sections, interleaved):
+    # A last place of a 16-bit value can move a code by a whole step, and a row's sum that is off by a last place shows as
+    # often.  What remains is the angles, within 2^-30: a value of fp16 moves by a last place, 2^-11 of itself at least, in
+    # 2^-18 of the cases (their error is 2^-29 (|a| + |b|) wide), and shows where it is its group's smallest or largest or a
+    # code's border is in that place (3e-3 of the others): 2.2 values of 64.  2^20 groups, so 9 are expected at most; 24 are
+    # five deviations more.  A sum off by 2^-24 in half of the rows would show in some 90.
+    T, H = 2 ** 22 // d, 16
+    g = torch.Generator().manual_seed(d + len(sections or ()))
+    k = torch.randn((T, H, d), generator=g).to(HF).to(DEV)
+    w = weights(g, d, F32)
+    rot, kw = turned(g, sections, interleaved, 0, 1, T)
+    pos = None
+    if rot is not None:
+        pos = kw["positions"] = rot[0][:, 0].contiguous()
+    total, table, ln = tables([T], 64, seed=13)
+    cache = new_cache(total, H, 64, d)
+    fa.paged4_append(cache, table, ln, k, k, cu_seqlens=offsets([T]), k_weight=w, eps=1e-6, **kw)
+    got, raw = fa.paged4_read(cache, table, ln, T, HF)
+    want = held(elementary_rows(k, w, 1e-6, pos, kw.get("inv_freq"), kw.get("axes"), interleaved)).transpose(0, 1)[None]
+    ok()
+    assert torch.equal(raw, held(k).transpose(0, 1)[None])
+    off = (got != want).unflatten(-1, (-1, 64)).any(-1)
+    assert off.sum().item() <= 24, f"{off.sum().item()} of {off.numel()} groups"
