@@ -10,8 +10,8 @@ import torch
 
 import exact_io_aware_flashattention_gb300 as fa
 from oracle import paged4
-from tests.test_paged4_gpu import (BF, DEV, F32, HF, TINY, U, assert_decoded, f64, filled, new_cache, offsets, ok, rounder,
-                                   tables, turned, weights)
+from tests.test_paged4_gpu import (BF, DEV, F32, HF, TINY, U, assert_decoded, assert_normed, assert_read, f64, filled, last_rows,
+                                   new_cache, offsets, ok, rounder, tables, turned, weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -222,3 +222,46 @@ def test_rows_of_k_are_those_of_elementary_operations(cuda_lib, d, sections, int
     assert torch.equal(raw, held(k).transpose(0, 1)[None])
     off = (got != want).unflatten(-1, (-1, 64)).any(-1)
     assert off.sum().item() <= 24, f"{off.sum().item()} of {off.numel()} groups"
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("Hq,Hkv,d,sections,interleaved", [(8, 2, 128, (64,), False), (8, 2, 128, (16, 16), True), (6, 2, 64, (32,), False),
+                                                           (32, 2, 128, (64,), False)])
+def test_serving_run_step_by_step(cuda_lib, Hq, Hkv, d, sections, interleaved, dt):
+    # Prompts, then steps of one token: what the cache holds and the attention over it, compared at every step.  (Of some
+    # 30000 values of K, those that the angles' last places move, 1e-6 of them: none.)
+    lens = [70, 0, 33]
+    g = torch.Generator().manual_seed(71)
+    total, table, _ = tables([n + 8 for n in lens], 16, seed=72)
+    cache = new_cache(total, Hkv, 16, d)
+    wq, wk = weights(g, d, dt), weights(g, d, dt)
+    freq, axes = fa.rope_frequencies(sections, device=DEV)
+    turn = dict(inv_freq=freq, axes=axes, interleaved=interleaved)
+    rows = [[[], []] for _ in lens]
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    for step in range(8):
+        counts = [1, 1, 1] if step else list(lens)
+        if step:
+            lens = [n + 1 for n in lens]
+        ln.copy_(torch.tensor(lens, dtype=torch.int32))
+        q, k, v = torch.randn((sum(counts), Hq + 2 * Hkv, d), generator=g).to(dt).to(DEV).split([Hq, Hkv, Hkv], dim=1)
+        one = torch.tensor([n - c + i for n, c in zip(lens, counts) for i in range(c)], dtype=torch.int32, device=DEV)
+        pos = torch.stack([one + 5 * i for i in range(len(sections))])
+        qn = fa.paged4_append(cache, table, ln, k, v, cu_seqlens=None if step else offsets(counts), q=q, q_weight=wq, k_weight=wk,
+                              eps=1e-6, positions=pos, **turn)
+        kn, at = elementary_rows(k, wk, 1e-6, pos, freq, axes, interleaved), 0
+        for b, c in enumerate(counts):
+            rows[b][0].append(kn[at:at + c])
+            rows[b][1].append(v[at:at + c])
+            at += c
+        ok()
+        assert_normed(qn.transpose(0, 1)[None], q.transpose(0, 1)[None], wq, 1e-6, (pos[:, None], freq, axes, interleaved), "q")
+        kall, vall = (torch.cat([t for r in rows for t in r[i]]) for i in range(2))
+        got = fa.paged4_read(cache, table, ln, max(lens), dt)
+        assert_read(got[0], last_rows(kall, lens, max(lens), dt), dt, "k")
+        assert_read(got[1], last_rows(vall, lens, max(lens), dt), dt, "v")
+        if step:
+            window = 0 if step % 2 else 50
+            o, lse = fa.paged4_decode(qn, cache, table, ln, window=window)
+            ok()
+            assert_decoded(o, lse, qn, kall, vall, lens, d ** -0.5, window, f"step {step}")
