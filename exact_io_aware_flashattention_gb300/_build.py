@@ -37,7 +37,7 @@ TORCH_LOG = os.path.join(OUT_DIR, "fa_torch.txt")
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_rope.cu", "fa_paged.cu", "fa_evict.cu", "fa_qknorm.cu",
            "fa_append4.cu", "fa_decode4.cu"]
-HEADERS = ["sm103a.cuh", "fa_internal.h", "fa_paged.h", "fa_paged4.h", "fa_rotary.cuh", "fa_decode.cuh"]
+HEADERS = ["sm103a.cuh", "fa_internal.h", "fa_paged.h", "fa_paged4.h", "fa_angle.h", "fa_rotary.cuh", "fa_decode.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

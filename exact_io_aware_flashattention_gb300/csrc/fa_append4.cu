@@ -116,7 +116,7 @@ __device__ __forceinline__ void encode8(const uint4& v, const Step& g, uint8_t* 
 // are therefore formed by fp32 operations that are rounded one by one, in an order that
 // is the same for every layout of the pairs: the squares of the elements that are 32
 // columns apart summed first, then neighbours; the turn without fused products, by
-// angles within 2^-30.  (7.5 million values of K of 7357 prompt tokens against such a
+// angles within 2^-29.5.  (7.5 million values of K of 7357 prompt tokens against such a
 // program: as in the norm's kernel 2.5 codes a call differed, so none in twelve calls;
 // 40.5 -> 42.3 us.)
 // Of a row whose lane c has the elements 8 c .. 8 c + 7 and D / 2 more:

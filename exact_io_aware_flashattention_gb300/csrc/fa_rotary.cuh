@@ -5,6 +5,7 @@
 
 #include <cuda_fp16.h>
 
+#include "fa_angle.h"
 #include "fa_paged.h"
 #include "sm103a.cuh"
 
@@ -227,33 +228,14 @@ __device__ __forceinline__ void scale8(float (&x)[8], float r, const float (&w)[
   }
 }
 
-// Cosine and sine of phase 2^-64 turns, off by 2^-30 and rounded to fp32 (so all but a
-// few of a hundred as one rounding of the exact ones): the nearest quarter turn off,
-// Taylor's polynomials of what is left, theta <= pi / 4, in 32-bit fixed point.
+// Cosine and sine of phase 2^-64 turns, off by 2^-29.5 at most before they are rounded to fp32.
 __device__ __forceinline__ void fine_angle(uint64_t phase, float& cs, float& sn) {
-  const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
-  const int64_t rest = (int64_t)(phase - ((uint64_t)quarter << 62));
-  const uint32_t x = (uint32_t)((uint64_t)(rest < 0 ? -rest : rest) >> 30);            // 2^31 an eighth of a turn
-  const uint32_t theta = __umulhi(x, 3373259426u) << 1;            // pi 2^30; theta and its square in units of 2^-32
-  const uint32_t t = __umulhi(theta, theta);
-  // 2^32 / n! for n = 11, 9, 7, 5, 3 and 10, 8, 6, 4, 2.
-  uint32_t p = __umulhi(t, 108u);
-  p = __umulhi(t, 11836u - p);
-  p = __umulhi(t, 852176u - p);
-  p = __umulhi(t, 35791394u - p);
-  p = __umulhi(t, 715827883u - p);
-  float s = (float)(theta - __umulhi(theta, p)) * 0x1p-32f;
-  p = __umulhi(t, 1184u);
-  p = __umulhi(t, 106522u - p);
-  p = __umulhi(t, 5965232u - p);
-  p = __umulhi(t, 178956971u - p);
-  p = __umulhi(t, 2147483648u - p);
-  const float c = (float)(2147483648u - (p >> 1)) * 0x1p-31f;
-  if (rest < 0) s = -s;
-  cs = quarter & 1 ? s : c;
-  sn = quarter & 1 ? c : s;
-  if (quarter == 1 || quarter == 2) cs = -cs;
-  if (quarter & 2) sn = -sn;
+  const FixedAngle a = fixed_angle(phase);
+  const float c = (float)a.cos31 * 0x1p-31f, s = (float)a.sin32 * (a.negative ? -0x1p-32f : 0x1p-32f);
+  cs = a.quarter & 1 ? s : c;
+  sn = a.quarter & 1 ? c : s;
+  if (a.quarter == 1 || a.quarter == 2) cs = -cs;
+  if (a.quarter & 2) sn = -sn;
 }
 // Those of the pairs 8c .. 8c+7.
 __device__ __forceinline__ void load_fine_angles(const RotaryArgs& r, const Pairs& p, const int* pos, int c, float (&cs)[8],

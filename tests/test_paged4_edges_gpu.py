@@ -201,10 +201,10 @@ def held(x):
                                                     (64, (8, 8), False)])
 def test_rows_of_k_are_those_of_elementary_operations(cuda_lib, d, sections, interleaved):
     # A last place of a 16-bit value can move a code by a whole step, and a row's sum that is off by a last place shows as
-    # often.  What remains is the angles, within 2^-30: a value of fp16 moves by a last place, 2^-11 of itself at least, in
-    # 2^-18 of the cases (their error is 2^-29 (|a| + |b|) wide), and shows where it is its group's smallest or largest or a
-    # code's border is in that place (3e-3 of the others): 2.2 values of 64.  2^20 groups, so 9 are expected at most; 24 are
-    # five deviations more.  A sum off by 2^-24 in half of the rows would show in some 90.
+    # often.  What remains is the angles, within 2^-29.5: a value of fp16 moves by a last place, 2^-11 of itself at least, in
+    # 2^-17.5 of the cases (their error is 2^-28.5 (|a| + |b|) wide), and shows where it is its group's smallest or largest or
+    # a code's border is in that place (3e-3 of the others): 2.2 values of 64.  2^20 groups, so 13 are expected at most; 24
+    # are three deviations more.  A sum off by 2^-24 in half of the rows would show in some 90.
     T, H = 2 ** 22 // d, 16
     g = torch.Generator().manual_seed(d + len(sections or ()))
     k = torch.randn((T, H, d), generator=g).to(HF).to(DEV)
