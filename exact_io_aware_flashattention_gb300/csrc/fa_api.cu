@@ -1211,9 +1211,10 @@ fa::NormArgs norm_args(const fa_qk_norm* n) {
   return n ? fa::NormArgs{n->q_weight, n->k_weight, n->weights_fp32, 1, n->eps} : fa::NormArgs{};
 }
 
-// What a call reads by element: the rotation's arrays and the norm's weights.
+// What a call reads by element: the rotation's arrays (three), the norm's weights (two),
+// and an append's table, lengths and offsets.
 struct Tables {
-  View v[8];
+  View v[3 + 2 + 3];
   int n = 0;
   void add(const View& x) { v[n++] = x; }
   void rotary(const fa_rotary* r, int B, int N) {

@@ -15,6 +15,13 @@ namespace fa {
 
 namespace {
 
+// Fragments of eight rows of a matrix of 16-bit values as those of its columns.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // Visible keys [first, len) of a sequence, as tiles [tile0, tile0 + n) of kKeys.
 struct Span {
   int len, first, tile0, n;

@@ -110,24 +110,7 @@ struct Bars {
 template <typename C>
 constexpr uint32_t kSmem = C::kBars + sizeof(Bars<C>);
 
-template <typename T>
-struct Type;
-template <>
-struct Type<__nv_bfloat16> {
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return cvt_bf16x2(lo, hi); }
-  static __device__ __forceinline__ float2 up(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  }
-};
-template <>
-struct Type<__half> {
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  static __device__ __forceinline__ float2 up(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
-};
-using Half = Type<__half>;
+using Half = Pair2<__half>;
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -156,14 +139,9 @@ struct Traits {
   using T = T_;
   static constexpr int D = D_, kKeys = kKeys_, kJoinThreads = kThreads;
   static constexpr float kShift = 0.f;
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return Type<T>::pack(lo, hi); }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return Pair2<T>::down(lo, hi); }
 };
 
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
 // The largest power of two up to a positive normal x.
 __device__ __forceinline__ float power_of(float x) { return __uint_as_float(__float_as_uint(x) & 0x7f800000u); }
 
@@ -172,16 +150,16 @@ template <typename T, int D>
 __device__ __forceinline__ void load_pars(const uint8_t* p, float2 (&x)[D / 64]) {
   if constexpr (D == 128) {
     const uint2 w = *reinterpret_cast<const uint2*>(p);
-    x[0] = Type<T>::up(w.x);
-    x[1] = Type<T>::up(w.y);
+    x[0] = Pair2<T>::up(w.x);
+    x[1] = Pair2<T>::up(w.y);
   } else {
-    x[0] = Type<T>::up(*reinterpret_cast<const uint32_t*>(p));
+    x[0] = Pair2<T>::up(*reinterpret_cast<const uint32_t*>(p));
   }
 }
 
 template <typename T>
 __device__ __forceinline__ float2 load_par(const uint8_t* p) {
-  return Type<T>::up(*reinterpret_cast<const uint32_t*>(p));
+  return Pair2<T>::up(*reinterpret_cast<const uint32_t*>(p));
 }
 
 // The query rows of unit (b, col) on their way to raw [8 NT heads][D]; a warp's work.
@@ -235,7 +213,7 @@ __device__ __forceinline__ void store_q(const QRows<D, NT>& q, float scale_log2,
         const uint32_t e[4] = {q.x[n][k][w].x, q.x[n][k][w].y, q.x[n][k][w].z, q.x[n][k][w].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 y = Type<T>::up(e[i]);
+          const float2 y = Pair2<T>::up(e[i]);
           s[k] += y.x + y.y;
           top = fmaxf(top, fabsf(y.x) < INFINITY ? fabsf(y.x) : 0.f);
           top = fmaxf(top, fabsf(y.y) < INFINITY ? fabsf(y.y) : 0.f);
@@ -253,10 +231,10 @@ __device__ __forceinline__ void store_q(const QRows<D, NT>& q, float scale_log2,
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const uint4 v = q.x[n][k][w];
-        const float2 y0 = Type<T>::up(v.x), y1 = Type<T>::up(v.y), y2 = Type<T>::up(v.z), y3 = Type<T>::up(v.w);
+        const float2 y0 = Pair2<T>::up(v.x), y1 = Pair2<T>::up(v.y), y2 = Pair2<T>::up(v.z), y3 = Pair2<T>::up(v.w);
         uint2* x = to + ((n * (D / 64) + k) * 2 + w) * 64 + lane;
-        x[0] = make_uint2(Half::pack(y0.x * times, y0.y * times), Half::pack(y1.x * more, y1.y * more));
-        x[32] = make_uint2(Half::pack(y2.x * times, y2.y * times), Half::pack(y3.x * more, y3.y * more));
+        x[0] = make_uint2(Half::down(y0.x * times, y0.y * times), Half::down(y1.x * more, y1.y * more));
+        x[32] = make_uint2(Half::down(y2.x * times, y2.y * times), Half::down(y3.x * more, y3.y * more));
       }
     }
     // (Not 0, which times a masked score's -inf is NaN; scores of so small factors are 0 all the same.)
@@ -452,9 +430,9 @@ __device__ __forceinline__ void work(uint8_t* rec, int key0, const Span& s, uint
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float w0 = x[j][n][2 * e] * (e ? sb : sa), w1 = x[j][n][2 * e + 1] * (e ? sb : sa);
-          const uint32_t high = Half::pack(w0, w1);
+          const uint32_t high = Half::down(w0, w1);
           const float2 h = Half::up(high);
-          const uint32_t low = Half::pack(w0 - h.x, w1 - h.y);
+          const uint32_t low = Half::down(w0 - h.x, w1 - h.y);
           p[j][n][0][e] = transpose8(kDup && (threadIdx.x & 2) ? low : high);
           if constexpr (!kDup) p[j][n][1][e] = transpose8(low);
         }
