@@ -14,9 +14,10 @@
 // three rows ahead (four in the gradient, 32 KB a block, three blocks an SM at 152
 // registers), since loads into registers kept too few bytes on their way: the
 // forward 31.2 -> 24.9 us, the gradient 210 -> 87.  4 x 2048 tokens of 32 heads, d = 128,
-// bf16, 134 MB: 23.6 us, 5.7 TB/s; the gradient of 2 x 8192 tokens of 40 heads, 503 MB,
-// 84.7 us, 5.9 TB/s.  Small calls are the latency of a load, the angles and a store, 3.3 us
-// (8 + 2 heads of 513 tokens, d = 64), and of the gradient's second kernel, 6.2.
+// bf16, 134 MB: 25.0 us, 5.4 TB/s; the gradient of 2 x 8192 tokens of 40 heads, 503 MB,
+// 84.6 us, 5.9 TB/s (outputs of twelve calls in turn, so that all of it is written back).
+// Small calls are the latency of a load, the angles and a store, 3.3 us (8 + 2 heads of
+// 513 tokens, d = 64), and of the gradient's second kernel, 6.1.
 #include "fa_paged4.h"
 #include "fa_rotary.cuh"
 #include "sm103a.cuh"
@@ -266,14 +267,17 @@ __global__ void __launch_bounds__(kThreads) fa_qk_norm_dw_kernel(const NormRopeB
   if (lane == 0) a.dw[part][i] = s;
 }
 
-// Heads per block of the forward, which share their angles: ten blocks an SM, of which
-// seven run at a time, but 11 heads at most, so that large calls end evenly; and a head
-// a block only where that is no more than five an SM.  us by 10 | 16 blocks an SM: 4 x
-// 2048 tokens of 32 heads 23.6 | 24.2, 2048 of 40 heads 11.3 | 12.9; 16384 of 32 heads with
-// 16 | 11 heads a block 48.0 | 45.3; 512 of 40 heads with one | two 7.9 | 5.5.
+// Heads per block of the forward, which share their angles: as few blocks as run at a
+// time, seven an SM, so that small calls have no second wave; but eight heads at most, as
+// at the end SMs wait for one block's time at most, and a block of fewer heads is shorter
+// (of six, it forms its angles too often); and a head a block only where that is no more than five an SM.  us a call, outputs
+// of twelve calls in turn, d = 128: by 7 | 10 blocks an SM 1024 tokens of 40 heads 6.9 | 8.4,
+// 2048 of 40 10.7 | 12.1, 4096 of 40 18.9 | 18.1 (the worst), 8192 of 40 29.7 | 29.8; with
+// 6 | 8 | 11 | all heads a block 4 x 2048 of 32 heads 25.1 | 25.0 | 26.0 | 26.0, 32768 of 40
+// heads 103.5 | 100.8 | 101.6 | 111.1; 512 of 40 heads with one | two 7.9 | 5.5.
 int heads_per_block(long long token_blocks, int heads, int num_sms) {
-  const long long want = 10LL * num_sms;
-  const long long splits = std::min<long long>(std::max<long long>((want + token_blocks - 1) / token_blocks, (heads + 10) / 11), heads);
+  const long long want = 7LL * num_sms;
+  const long long splits = std::min<long long>(std::max<long long>((want + token_blocks - 1) / token_blocks, (heads + 7) / 8), heads);
   const int hpb = (int)((heads + splits - 1) / splits);
   return hpb == 1 && token_blocks * heads > 5LL * num_sms ? 2 : hpb;
 }
