@@ -11,7 +11,7 @@
 // Bound by HBM: 16-bit rows in, 0.5625 bytes an element out (in and out exchanged when
 // reading back).  The append issues in 64 % of the cycles, on finding the groups' ends,
 // quotients that round as a division does and the angles: 7357 tokens of 32 + 8 + 8
-// heads, d = 128, bf16, 159 MB: 39.9 us, 4.0 TB/s.  Reading 32768 keys of 8 heads, 172 MB: 29 us,
+// heads, d = 128, bf16, 159 MB: 36.9 us, 4.3 TB/s.  Reading 32768 keys of 8 heads, 172 MB: 29 us,
 // 5.9 TB/s (a warp a record with all its loads first; element by element 44).
 #include "fa_paged4.h"
 #include "fa_rotary.cuh"
@@ -418,12 +418,13 @@ __global__ void __launch_bounds__(kThreads) fa_read4_kernel(const Read4Args a, c
   }
 }
 
-// Two waves of blocks, five an SM, and no more, since each forms its tokens' angles
-// anew; a head a block only where that is no more than a wave.
-// Append alone, 7357 tokens of 48 heads: 10 blocks an SM 40.2 us, 12 40.2, 16 41.2, 24
-// 43.9; 512 tokens: one head a block 10.3 us, two 8.1.
+// Somewhat more blocks than run at a time, five an SM, but not many, since each forms its
+// tokens' angles anew; a head a block only where they all run at once.  us alone, outputs
+// of twelve calls in turn, by 5 | 7 | 10 | 15 blocks an SM: 7357 tokens of 48
+// heads 40.2 | 36.9 | 40.1 | 39.0, 8192 43.5 | 41.1 | 41.0 | 43.5, 2048 17.7 | 16.8 | 17.8
+// | 19.6; 512 tokens: one head a block 10.3, two 8.1.
 int heads_per_block(long long token_blocks, int heads, int num_sms) {
-  const long long want = 10LL * num_sms;
+  const long long want = 7LL * num_sms;
   const long long splits = std::min<long long>((want + token_blocks - 1) / token_blocks, heads);
   const int hpb = (int)((heads + splits - 1) / splits);
   return hpb == 1 && token_blocks * heads > 5LL * num_sms ? 2 : hpb;
