@@ -1124,8 +1124,9 @@ def _paged4_append(cache, block_table, seq_lens, k, v, cu_seqlens, q, q_weight, 
 def paged4_read(cache, block_table, seq_lens, n: int, dtype, k_out=None, v_out=None, stream=None):
     """The last n keys of each sequence of a 4-bit cache as k, v [B,Hkv,n,d] of
     ``dtype``, the type it was appended in; row i is key seq_lens[b] - n + i, zero
-    where that is negative.  With one sequence's whole length they are what
-    ``forward_ex`` takes for its next queries.  See fa_paged4_read."""
+    where that is negative.  With one sequence's whole length they are, in bf16,
+    what ``forward_ex`` (bf16 only) takes for its next queries.  See
+    fa_paged4_read."""
     if stream is None:
         r = (_native or _load_native()).paged4_read(cache, block_table, seq_lens, n, dtype, k_out, v_out)
         if r is not None:

@@ -927,9 +927,9 @@ DecodeWs decode_ws(int B, int Hq, int d, int page_size, int max_pages, bool with
 // 30.3; 32 from 0 to 1000, 16 tiles a CTA, 19.1 | 21.6, with scores 23.6 | 24.2; 8
 // from 0 to 8000, d = 64, 16 tiles, with scores, 28.7 | 22.8.  128 q heads, 8 of
 // 1000 12.0 | 19.2.  The 4-bit cache, tiles of 128 keys, in a graph: 1 sequence of 2000
-// keys 7.3 | 10.4, of 8000, 8 tiles a CTA, 13.3 | 13.4; 4 of 2000 8.7 | 13.4; 16 of 1000
-// 10.9 | 15.1; 64 of 600 22.5 | 23.8; 32 of up to 4096, 16 heads a group, 16 tiles a CTA,
-// 23.8 | 22.1.)
+// keys 7.4 | 10.8, of 8000, 8 tiles a CTA, 12.6 | 13.5; 4 of 2000 9.0 | 13.7; 16 of 1000
+// 11.2 | 15.4; 64 of 600 23.2 | 24.6; 32 of up to 4096, 16 heads a group, 16 tiles a CTA,
+// 26.8 | 25.2.)
 int decode_cluster(long long units, long long tiles, int slots) {
   int c = 1;
   while (c < fa::kMaxCluster && units * c * 2 <= slots && c < tiles) c *= 2;

@@ -9,7 +9,7 @@
 // codes everywhere.
 //
 // Bound by HBM: 16-bit rows in, 0.5625 bytes an element out (in and out exchanged when
-// reading back).  The append issues in 64 % of the cycles, on finding the groups' ends,
+// reading back).  The append issues in 62 % of the cycles, on finding the groups' ends,
 // quotients that round as a division does and the angles: 7357 tokens of 32 + 8 + 8
 // heads, d = 128, bf16, 159 MB: 36.9 us, 4.3 TB/s.  Reading 32768 keys of 8 heads, 172 MB: 29 us,
 // 5.9 TB/s (a warp a record with all its loads first; element by element 44).

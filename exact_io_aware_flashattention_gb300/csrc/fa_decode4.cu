@@ -43,12 +43,15 @@
 // one (weights up to 2^8, sums in fp32): the warp then neither exchanges maxima
 // nor rescales.
 //
-// Bound by issue: 308 instructions a slice of d = 128, 64 of them masks, 16 byte swaps
-// and 18 products, in 64 % of the cycles; the integer pipe is busy 54 %, the tensor pipe
-// 28 %.  16 sequences of 32768 keys, 8 kv heads of 4 heads (604 MB): 113 us, 5.3 TB/s; the
-// copies alone take 98 us, the work alone as long as both.  16 heads a group (two column
-// tiles, one CTA an SM with 255 registers a thread) take 177 us; as two units of eight
-// heads they would take twice 114.
+// Bound by what is done to a slice: 333 instructions at d = 128, 64 of them masks, 16 byte
+// swaps and 18 products.  Four warps a scheduler issue in 65 % of the cycles, the rest is
+// waiting for results; the integer pipe is busy 52 %, the tensor pipe 27 %.  16 sequences
+// of 32768 keys, 8 kv heads of 4 heads (604 MB): 119 us, 5.1 TB/s; the copies alone take 98
+// us.  Eight heads a group, whose low parts are products of their own, take 140 us.  16
+// heads a group (two column tiles, one CTA an SM with 255 registers a thread) take 224 us;
+// as two units of eight heads they would take twice 140.  At 128 registers the shapes of
+// equal parts, one column tile and d = 128 spill 56-80 bytes, outside the loop over tiles
+// (one local load for 3800 instructions).
 #include "fa_decode.cuh"
 #include "fa_paged4.h"
 #include "fa_rotary.cuh"

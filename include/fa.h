@@ -498,8 +498,8 @@ fa_status fa_paged4_append(const fa_paged4_kv* kv, const fa_page_table* table, c
  * The last N keys of each sequence as 16-bit rows: k and v [B,Hkv,N,d]
  * (strides: batch, head, token) of dtype get the values that the cache holds,
  * rounded to it; row n is key seq_lens[b] - N + n, and zero where that is
- * negative.  So one sequence's keys are what fa_fwd_ex takes for the queries of
- * its next tokens.  One launch.
+ * negative.  So one sequence's keys in bf16 are what fa_fwd_ex, which has bf16
+ * alone, takes for the queries of its next tokens.  One launch.
  */
 fa_status fa_paged4_read(const fa_paged4_kv* kv, const fa_page_table* table, const int* seq_lens, void* k,
                          const long long* k_strides, void* v, const long long* v_strides, int B, int N, void* stream);
