@@ -265,3 +265,94 @@ def test_serving_run_step_by_step(cuda_lib, Hq, Hkv, d, sections, interleaved, d
             o, lse = fa.paged4_decode(qn, cache, table, ln, window=window)
             ok()
             assert_decoded(o, lse, qn, kall, vall, lens, d ** -0.5, window, f"step {step}")
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (8, 1), (32, 2), (20, 1)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_query_that_is_not_finite_spoils_its_head_alone(cuda_lib, bad, Hq, Hkv, wide):
+    lens = [300, 0, 41]
+    cache, table, ln, k, v = filled(lens, Hkv, 16, 128, BF, seed=14)
+    table = widened(table, wide)
+    q = torch.randn((3, Hq, 128), generator=torch.Generator().manual_seed(15)).to(BF).to(DEV)
+    want, wl = fa.paged4_decode(q, cache, table, ln)
+    spoilt = q.clone()
+    spoilt[0, Hq - 1, 77] = bad
+    spoilt[1, 0] = bad                                              # of a sequence without keys
+    got, gl = fa.paged4_decode(spoilt, cache, table, ln)
+    ok()
+    assert not got[0, Hq - 1].isfinite().any()
+    assert torch.equal(got[0, :Hq - 1], want[0, :Hq - 1]) and torch.equal(got[1:], want[1:])
+    assert torch.equal(gl[0, :Hq - 1], wl[0, :Hq - 1]) and torch.equal(gl[1:], wl[1:])
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_inputs_that_are_broadcast(cuda_lib, dt):
+    # One row for many heads, tokens or sequences (stride 0) gives what its copies give, gradients too.
+    d, g = 128, torch.Generator().manual_seed(16)
+    x = torch.randn((1, 1, 37, d), generator=g).to(dt).to(DEV)
+    dy = torch.randn((3, 1, 1, d), generator=g).to(dt).to(DEV)
+    w = weights(g, d, F32)
+    freq, axes = fa.rope_frequencies((64,), device=DEV)
+    pos = torch.arange(37, dtype=torch.int32, device=DEV).expand(1, 3, 37)
+    q, k, dq, dk = x.expand(3, 8, 37, d), x.expand(3, 2, 37, d), dy.expand(3, 8, 37, d), dy.expand(3, 2, 37, d)
+    for a, b in ((q, q.contiguous()), (k, k.contiguous())):
+        assert torch.equal(fa.qk_norm_rope(a, None, w, None, pos, freq, axes), fa.qk_norm_rope(b, None, w, None, pos, freq, axes))
+    got = fa.qk_norm_rope_backward(dq, dk, q, k, w, w, pos, freq, axes)
+    want = fa.qk_norm_rope_backward(dq.contiguous(), dk.contiguous(), q.contiguous(), k.contiguous(), w, w, pos.contiguous(), freq, axes)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    total, table, ln = tables([40, 37], 16, seed=17)
+    one, all_ = (new_cache(total, 2, 16, d, fill=0) for _ in range(2))
+    rows = x[0, 0, :1].expand(40, 2, d)
+    cu = offsets([3, 37])
+    qs = x[0, :, :1].expand(40, 8, d)
+    turn = dict(positions=torch.arange(40, dtype=torch.int32, device=DEV)[None], inv_freq=freq, axes=axes)
+    a = fa.paged4_append(one, table, ln, rows, rows, cu_seqlens=cu, q=qs, k_weight=w, eps=1e-6, **turn)
+    b = fa.paged4_append(all_, table, ln, rows.contiguous(), rows.contiguous(), cu_seqlens=cu, q=qs.contiguous(), k_weight=w, eps=1e-6, **turn)
+    assert torch.equal(a, b) and torch.equal(one, all_)
+    query = x[0, :, :1].expand(2, 8, d)
+    ln.copy_(torch.tensor([3, 37], dtype=torch.int32))
+    assert all(torch.equal(s, t) for s, t in zip(fa.paged4_decode(query, one, table, ln), fa.paged4_decode(query.contiguous(), one, table, ln)))
+    with pytest.raises(fa.FAError):
+        fa.qk_norm_rope_backward(dq, None, q, None, w, None, pos, freq, axes, dq_out=dq)       # rows that many would write
+    ok()
+
+
+def test_norm_without_eps_and_with_a_whole_number(cuda_lib):
+    # eps = 0 (a row of zeros is then 0 times infinity) and numbers that are no floats, by the Python marshalling.
+    x = torch.randn((1, 2, 9, 64), generator=torch.Generator().manual_seed(18)).to(HF).to(DEV)
+    x[0, 0, 3] = 0
+    y = fa.qk_norm_rope(x, None, None, None, eps=0)
+    z = fa.qk_norm_rope(x, None, None, None, eps=0.0)
+    ok()
+    assert torch.equal(y.nan_to_num(7.0), z.nan_to_num(7.0))
+    assert y[0, 0, 3].isnan().all() and y[0, 1].isfinite().all()
+    rest = [i for i in range(9) if i != 3]
+    assert_normed(y[:, :, rest], x[:, :, rest], None, 0.0, None, "eps 0")
+
+
+def test_two_calls_on_two_streams_share_a_pool(cuda_lib):
+    # Two streams append to different sequences of one pool and read them, again and again; then the pool is as if one had.
+    lens, d, n = [500, 500], 128, 500
+    g = torch.Generator().manual_seed(19)
+    total, table, _ = tables(lens, 16, seed=20)
+    rows = [torch.randn((n, 2, d), generator=g).to(BF).to(DEV) for _ in range(2)]
+    alone, both = (new_cache(total, 2, 16, d, fill=0) for _ in range(2))
+    lengths = torch.arange(n + 1, dtype=torch.int32, device=DEV)
+    for b in range(2):
+        fa.paged4_append(alone, table[b:b + 1], lengths[n:], rows[b], rows[b], cu_seqlens=offsets([n]))
+    q = torch.randn((1, 8, d), generator=g).to(BF).to(DEV)
+    want = [fa.paged4_decode(q, alone, table[b:b + 1], lengths[n:]) for b in range(2)]
+    ok()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    cu = offsets([1])
+    for at in range(n):
+        for b in range(2):
+            fa.paged4_append(both, table[b:b + 1], lengths[at + 1:at + 2], rows[b][at:at + 1], rows[b][at:at + 1], cu_seqlens=cu,
+                             stream=streams[b])
+            got[b] = fa.paged4_decode(q, both, table[b:b + 1], lengths[at + 1:at + 2], stream=streams[b])
+    ok()
+    assert torch.equal(both, alone)
+    for b in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(got[b], want[b]))
