@@ -465,8 +465,9 @@ size_t fa_qk_norm_rope_bwd_workspace_bytes(int d);
  *   z = the group's smallest,  s = T((largest - z) / 15),
  *   c = (x - z) / s rounded to nearest (ties to even) in 0 .. 15, 0 where s = 0,
  * and it stands for z + s c.  x is off by s / 2 at most, and by 15 roundings of
- * s.  A group with a value that is not finite reads as NaN throughout; one whose
- * largest value is within 1/16 of T's may read as infinite there.
+ * s.  A group with a value that is not finite, or whose largest and smallest are
+ * further apart than fp32's largest number (bf16 alone), reads as NaN throughout;
+ * one whose largest value is within 1/16 of T's may read as infinite there.
  *
  * The pool holds num_pages pages of page_size slots (a multiple of 16, at most
  * 65536) for each kv head; page p of head g starts p * page_stride + g *

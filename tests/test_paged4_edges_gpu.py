@@ -356,3 +356,18 @@ def test_two_calls_on_two_streams_share_a_pool(cuda_lib):
     assert torch.equal(both, alone)
     for b in range(2):
         assert all(torch.equal(x, y) for x, y in zip(got[b], want[b]))
+
+
+def test_groups_wider_than_fp32_read_as_nan(cuda_lib):
+    # 3e38 and -3e38 are bf16 numbers, their difference is no fp32 one; half as far apart they are held.
+    x = torch.randn((3, 1, 64), generator=torch.Generator().manual_seed(21))
+    x[1, 0, 5], x[1, 0, 60] = 3e38, -3e38
+    x[2, 0, 5], x[2, 0, 60] = 1.5e38, -1.5e38
+    x = x.to(BF).to(DEV)
+    total, table, ln = tables([3], 16, seed=22)
+    cache = new_cache(total, 1, 16, 64)
+    fa.paged4_append(cache, table, ln, x, x, cu_seqlens=offsets([3]))
+    for got in fa.paged4_read(cache, table, ln, 3, BF):
+        assert got[0, 0, 1].isnan().all()
+        assert_read(got[:, :, [0, 2]], last_rows(x[[0, 2]], [2], 2, BF), BF)
+    ok()
